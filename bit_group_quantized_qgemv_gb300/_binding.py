@@ -18,6 +18,7 @@ from . import build as _build
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 
 _SIGS = {
     "qgemv_w4g64": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
@@ -49,6 +50,13 @@ _SIGS = {
     "qgemv_lut4": (_I, [_P, _P, _I, _I, _P, _P, _I, _I, _P, _P]),
     "qgemv_lm_head_sample": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _P, _P, _P, _P]),
     "qgemv_plan_gemv": (_I, [_I, _I, _I, _I, _I, _I, _P]),
+    "qgemv_qk_norm_rope_append": (_I, [_P, _P, _L, _I, _I, _P, _P, _P, _I, _I, _P, _P, _F, _P, _L,
+                                       _P, _P, _P, _P]),
+    "qgemv_paged_attention": (_I, [_P, _P, _L, _I, _I, _P, _I, _F, _P, _L, _P, _P, ctypes.c_size_t,
+                                   _P, _P]),
+    "qgemv_paged_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
+    "qgemv_attention_mass": (_I, [_P, _P, _L, _I, _I, _P, _I, _F, _P, _P, _P, _P, _P]),
+    "qgemv_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -121,6 +129,8 @@ def _cuda(t, dtypes, name):
 
 _CODES = (torch.int32, getattr(torch, "uint32", torch.int32))
 _F16 = (torch.float16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
 
 
 def _weight(w, name):
@@ -487,6 +497,238 @@ def decode_stack(layers, shape: StackShape, x, y=None, workspace=None, stream=No
                                 workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "qgemv_decode_stack")
     return y
+
+
+class KVCacheStruct(ctypes.Structure):
+    """qgemv_kv_cache (include/qgemv.h)."""
+    _fields_ = ([(n, _P) for n in ("k", "v", "page_table", "kv_len")] +
+                [(n, _I) for n in ("n_pages", "page_size", "n_kv", "head_dim", "n_seqs",
+                                   "max_pages")])
+
+
+class KVCache:
+    """Handle of a paged key/value cache (kv_cache()); it keeps its tensors alive."""
+
+    def __init__(self, k, v, page_table, kv_len):
+        self.k, self.v = _cuda(k, _F16, "k"), _cuda(v, _F16, "v")
+        self.page_table = _cuda(page_table, _I32, "page_table")
+        self.kv_len = _cuda(kv_len, _I32, "kv_len")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [n_pages][n_kv][page_size][head_dim]")
+        if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1]:
+            raise ValueError("page_table must be [n_seqs][max_pages] and kv_len [n_seqs]")
+        self.device = k.device
+        for name, t in (("v", v), ("page_table", page_table), ("kv_len", kv_len)):
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, k on {self.device}")
+        n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
+        self.n_seqs, self.max_pages = page_table.shape
+        self.capacity = self.max_pages * self.page_size
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(),
+                                    kv_len.data_ptr(), n_pages, self.page_size, self.n_kv,
+                                    self.head_dim, self.n_seqs, self.max_pages)
+        self.ref = ctypes.byref(self.struct)
+
+
+def kv_cache(k, v, page_table, kv_len) -> KVCache:
+    """Handle of a paged cache: k, v fp16 [n_pages][n_kv][page_size][head_dim],
+    page_table int32 [n_seqs][max_pages], kv_len int32 [n_seqs] (entries of
+    each sequence, the new tokens of a call included; read when the kernels
+    run), all on one GPU."""
+    return KVCache(k, v, page_table, kv_len)
+
+
+class _On:
+    """The device and stream of a cache call: launches go to the cache's
+    device, and what the call allocates belongs to the stream it runs on."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, []
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"stream is on {self.stream.device}, the cache on {self.device}")
+            self.guards.append(torch.cuda.stream(self.stream))
+        elif torch.cuda.current_device() != self.device.index:
+            self.guards.append(torch.cuda.device(self.device))
+        for g in self.guards:
+            g.__enter__()
+        return ctypes.c_void_p((self.stream or torch.cuda.current_stream()).cuda_stream)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _at(cache, t, dtypes, name, shape=None):
+    """A contiguous tensor on the cache's device, of the given shape; None passes."""
+    if t is None:
+        return None
+    _cuda(t, dtypes, name)
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _token_rows(cache, t, name, width=None):
+    """fp16 rows of tokens, [tokens][width] or [tokens][heads][head_dim], whose
+    row stride is free: (width, row stride)."""
+    if not t.is_cuda or t.device != cache.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {cache.device}")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
+    if t.dim() not in (2, 3) or t.stride(-1) != 1 or (t.dim() == 3 and
+                                                      t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be rows of tokens, contiguous within a row")
+    w = t.shape[1] * (t.shape[2] if t.dim() == 3 else 1)
+    if width is not None and w != width:
+        raise ValueError(f"{name} has rows of {w}, expected {width}")
+    return w, (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), w))
+
+
+def _heads(cache, width, extra, name):
+    n = width // cache.head_dim - extra
+    if width % cache.head_dim or n < 1:
+        raise ValueError(f"{name} has rows of {width}, not whole heads of {cache.head_dim}")
+    return n
+
+
+def qk_norm_rope_append(cache, qkv, q_start, positions, inv_freq=None, interleaved=False,
+                        q_norm=None, k_norm=None, eps=1e-6, q_out=None, entry_pos=None,
+                        entry_mass=None, err_flag=None, stream=None):
+    """qgemv_qk_norm_rope_append: per-head norms and rotation of the queries and
+    keys in qkv [tokens][(n_q + 2 n_kv) head_dim], keys and values into the
+    cache.  inv_freq: fp32 [rotary_dim / 2], None for no rotation.  Returns
+    q_out [tokens][n_q head_dim]."""
+    width, stride = _token_rows(cache, qkv, "qkv")
+    n_q, T = _heads(cache, width, 2 * cache.n_kv, "qkv"), qkv.shape[0]
+    with _On(cache.device, stream) as st:
+        if q_out is None:
+            q_out = torch.empty(T, n_q * cache.head_dim, dtype=torch.float16, device=cache.device)
+        _, q_stride = _token_rows(cache, q_out, "q_out", n_q * cache.head_dim)
+        if q_out.shape[0] != T:
+            raise ValueError(f"q_out has {q_out.shape[0]} rows, qkv {T}")
+        entries = (cache.n_seqs, cache.n_kv, cache.capacity)
+        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
+        _at(cache, positions, _I32, "positions", (T,))
+        _at(cache, inv_freq, _F32, "inv_freq")
+        _at(cache, q_norm, _F16, "q_norm", (cache.head_dim,))
+        _at(cache, k_norm, _F16, "k_norm", (cache.head_dim,))
+        _at(cache, entry_pos, _I32, "entry_pos", entries)
+        _at(cache, entry_mass, _F32, "entry_mass", entries)
+        _at(cache, err_flag, _I32, "err_flag")
+        rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
+        rc = lib.qgemv_qk_norm_rope_append(
+            cache.ref, _ptr(qkv), stride, T, n_q, _ptr(q_start), _ptr(positions), _ptr(inv_freq),
+            rotary, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps), _ptr(q_out),
+            q_stride, _ptr(entry_pos), _ptr(entry_mass), _ptr(err_flag), st)
+    _check(rc, "qgemv_qk_norm_rope_append")
+    return q_out
+
+
+def paged_attention_workspace_bytes(cache, n_tokens, n_q, max_q) -> int:
+    with _On(cache.device, None):
+        return int(lib.qgemv_paged_attention_workspace_bytes(cache.ref, int(n_tokens), int(n_q),
+                                                             int(max_q)))
+
+
+def paged_attention(cache, q, q_start, max_q=None, scale=None, out=None, want_lse=False, lse=None,
+                    workspace=None, err_flag=None, stream=None):
+    """qgemv_paged_attention: causal attention of each sequence's new tokens over
+    its cache; q [tokens][n_q head_dim].  max_q: the largest number of new
+    tokens in a sequence (default: all).  scale: default head_dim ** -0.5.
+    Returns (out, lse fp32 [tokens][n_q] or None)."""
+    width, stride = _token_rows(cache, q, "q")
+    n_q, T = _heads(cache, width, 0, "q"), q.shape[0]
+    max_q = max(T, 1) if max_q is None else int(max_q)
+    with _On(cache.device, stream) as st:
+        if out is None:
+            out = torch.empty(T, width, dtype=torch.float16, device=cache.device)
+        _, out_stride = _token_rows(cache, out, "out", width)
+        if out.shape[0] != T:
+            raise ValueError(f"out has {out.shape[0]} rows, q {T}")
+        if lse is None and want_lse:
+            lse = torch.empty(T, n_q, dtype=torch.float32, device=cache.device)
+        _at(cache, lse, _F32, "lse", (T, n_q))
+        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
+        _at(cache, err_flag, _I32, "err_flag")
+        if workspace is None:
+            n = int(lib.qgemv_paged_attention_workspace_bytes(cache.ref, T, n_q, max_q))
+            if n:
+                workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        elif workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the cache's device")
+        rc = lib.qgemv_paged_attention(
+            cache.ref, _ptr(q), stride, T, n_q, _ptr(q_start), max_q,
+            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(out), out_stride,
+            _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(err_flag), st)
+    _check(rc, "qgemv_paged_attention")
+    return out, lse
+
+
+def attention_mass(cache, q, q_start, lse, max_q=None, scale=None, mass=None, mass_out=None,
+                   err_flag=None, stream=None):
+    """qgemv_attention_mass: mass (fp32 [n_seqs][n_kv][capacity], None: zeros) plus
+    the attention weight every cached entry receives from the new tokens; q
+    and lse as paged_attention took and gave them.  Returns mass_out (a new
+    array is zero behind each sequence's length; it may be mass itself)."""
+    width, stride = _token_rows(cache, q, "q")
+    n_q, T = _heads(cache, width, 0, "q"), q.shape[0]
+    max_q = max(T, 1) if max_q is None else int(max_q)
+    entries = (cache.n_seqs, cache.n_kv, cache.capacity)
+    with _On(cache.device, stream) as st:
+        if mass_out is None:
+            mass_out = torch.zeros(entries, dtype=torch.float32, device=cache.device)
+        _at(cache, mass, _F32, "mass", entries)
+        _at(cache, mass_out, _F32, "mass_out", entries)
+        _at(cache, lse, _F32, "lse", (T, n_q))
+        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
+        _at(cache, err_flag, _I32, "err_flag")
+        rc = lib.qgemv_attention_mass(
+            cache.ref, _ptr(q), stride, T, n_q, _ptr(q_start), max_q,
+            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(lse), _ptr(mass),
+            _ptr(mass_out), _ptr(err_flag), st)
+    _check(rc, "qgemv_attention_mass")
+    return mass_out
+
+
+def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, kept=None,
+                mass_out=None, pos_out=None, kv_len_out=None, err_flag=None, stream=None):
+    """qgemv_cache_evict: cut every sequence to its `keep` entries of largest mass
+    (positions below n_sink and the last n_recent before next_pos first), each
+    head for itself; rows of the cache move in place.  Returns (kept int32
+    [n_seqs][n_kv][keep], mass_out, pos_out, kv_len_out); kv_len_out is the new
+    length, to be written into the cache's kv_len before the next call."""
+    entries = (cache.n_seqs, cache.n_kv, cache.capacity)
+    keep = int(keep)
+    with _On(cache.device, stream) as st:
+        if kept is None:
+            kept = torch.empty(cache.n_seqs, cache.n_kv, max(keep, 0), dtype=torch.int32,
+                               device=cache.device)
+        if mass_out is None:
+            mass_out = torch.zeros(entries, dtype=torch.float32, device=cache.device)
+        if pos_out is None:
+            pos_out = torch.zeros(entries, dtype=torch.int32, device=cache.device)
+        if kv_len_out is None:
+            kv_len_out = torch.empty(cache.n_seqs, dtype=torch.int32, device=cache.device)
+        _at(cache, mass, _F32, "mass", entries)
+        _at(cache, entry_pos, _I32, "entry_pos", entries)
+        _at(cache, next_pos, _I32, "next_pos", (cache.n_seqs,))
+        _at(cache, kept, _I32, "kept", (cache.n_seqs, cache.n_kv, keep))
+        _at(cache, mass_out, _F32, "mass_out", entries)
+        _at(cache, pos_out, _I32, "pos_out", entries)
+        _at(cache, kv_len_out, _I32, "kv_len_out", (cache.n_seqs,))
+        _at(cache, err_flag, _I32, "err_flag")
+        rc = lib.qgemv_cache_evict(cache.ref, _ptr(mass), _ptr(entry_pos), _ptr(next_pos), keep,
+                                   int(n_sink), int(n_recent), _ptr(kept), _ptr(mass_out),
+                                   _ptr(pos_out), _ptr(kv_len_out), _ptr(err_flag), st)
+    _check(rc, "qgemv_cache_evict")
+    return kept, mass_out, pos_out, kv_len_out
 
 
 def device_status() -> int:

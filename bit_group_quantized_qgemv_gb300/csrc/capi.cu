@@ -214,6 +214,12 @@ int plain_impl(int bits, const uint32_t* codes, const uint16_t* scales, const ui
 
 }  // namespace
 
+namespace qgemv {
+// For the paged-cache entry points (capi_cache.cu).
+int report_launch(cudaError_t e) { return finish(e); }
+int device_and_sms(int* dev, int* sms) { return current_device(dev, sms); }
+}  // namespace qgemv
+
 extern "C" {
 
 int qgemv_w4g64(const uint32_t* codes, const uint16_t* scales, const uint16_t* biases,

@@ -1,0 +1,66 @@
+// kv_cache.cuh -- device-side helpers shared by the paged-cache kernels.
+#pragma once
+
+#include "kv_cache.h"
+#include "qgemv_device.cuh"
+
+namespace qgemv {
+
+__device__ __forceinline__ void flag_error(int* err) {
+  if (err != nullptr) *err = 1;
+}
+
+// Entries of sequence s, clamped to what its page-table row can hold.
+__device__ __forceinline__ int seq_len(const KvView& c, int s, int* err) {
+  const int n = c.kv_len[s], cap = c.max_pages << c.page_shift;
+  if (n < 0 || n > cap) flag_error(err);
+  return min(max(n, 0), cap);
+}
+
+// First row and number of new tokens of sequence s.
+__device__ __forceinline__ void seq_rows(const int* q_start, int s, int n_tokens, int* err,
+                                         int* first, int* count) {
+  const int a = q_start[s], b = q_start[s + 1];
+  if (a < 0 || b < a || b > n_tokens) flag_error(err);
+  const int a0 = min(max(a, 0), n_tokens), b0 = min(max(b, a0), n_tokens);
+  *first = a0;
+  *count = b0 - a0;
+}
+
+// Page that holds entry i of sequence s; -1 for a bad page number.
+__device__ __forceinline__ int page_of(const KvView& c, int s, int i, int* err) {
+  const int p = c.page_table[static_cast<long long>(s) * c.max_pages + (i >> c.page_shift)];
+  if (p < 0 || p >= c.n_pages) {
+    flag_error(err);
+    return -1;
+  }
+  return p;
+}
+
+// Row of entry i on page p for head h, as a row index into k or v.
+__device__ __forceinline__ long long cache_row(const KvView& c, int p, int h, int i) {
+  return ((static_cast<long long>(p) * c.n_kv + h) << c.page_shift) +
+         (i & ((1 << c.page_shift) - 1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D += A B, 16 x 8 x 16, fp16 operands, fp32 accumulator.
+__device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace qgemv

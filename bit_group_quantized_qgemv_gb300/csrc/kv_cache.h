@@ -1,0 +1,91 @@
+// kv_cache.h -- argument blocks and launch entry points of the paged-cache
+// operators (host and device).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace qgemv {
+
+// The cache as the kernels see it (page_size = 1 << page_shift).
+struct KvView {
+  __half *k, *v;           // [n_pages][n_kv][page_size][head_dim]
+  const int* page_table;   // [n_seqs][max_pages]
+  const int* kv_len;       // [n_seqs]
+  int n_pages, page_shift, n_kv, head_dim, n_seqs, max_pages;
+};
+
+struct RopeArgs {
+  KvView c;
+  const __half* qkv;
+  long long qkv_stride;
+  int n_tokens, n_q;
+  const int* q_start;
+  const int* positions;
+  const float* inv_freq;
+  int rotary_dim, interleaved;
+  const __half *q_norm, *k_norm;
+  float eps;
+  __half* q_out;
+  long long q_stride;
+  int* entry_pos;
+  float* entry_mass;
+  int* err;
+};
+
+struct AttnArgs {
+  KvView c;
+  const __half* q;
+  long long q_stride;
+  int n_tokens, n_q, group;  // group: query heads per key/value head
+  const int* q_start;
+  int max_q;
+  float scale_log2;          // scale * log2(e)
+  __half* out;
+  long long out_stride;
+  float* lse;
+  // Parts of a split cache: part_o [split][token][n_q][head_dim] (not yet
+  // divided by the sum), part_ml [split][token][n_q] {max, sum} in log2 units.
+  float* part_o;
+  float2* part_ml;
+  int n_splits, row_tiles;
+  int* err;
+};
+
+struct MassArgs {
+  KvView c;
+  const __half* q;
+  long long q_stride;
+  int n_tokens, n_q, group;
+  const int* q_start;
+  int max_q;
+  float scale_log2;
+  const float *lse, *mass;
+  float* mass_out;
+  int* err;
+};
+
+struct EvictArgs {
+  KvView c;
+  const float* mass;
+  const int *entry_pos, *next_pos;
+  int keep, n_sink, n_recent;
+  int* kept;
+  float* mass_out;
+  int* pos_out;
+  int* len_out;
+  int* err;
+};
+
+cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
+cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st);
+cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st);
+
+// Parts the cache is split into for a call of these sizes.
+int attention_splits(int n_seqs, int n_kv, int group, int max_q, long long capacity, int sms);
+// Bytes of workspace for that many parts.
+size_t attention_part_bytes(int splits, int n_tokens, int n_q, int head_dim);
+cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device);
+
+}  // namespace qgemv

@@ -476,6 +476,145 @@ int qgemv_lut4(const uint32_t *codes, const uint16_t *lut, int n_luts, int rows_
                void *stream);
 
 /*
+ * Paged key/value cache.  What stands between the QKV matvec and o_proj when
+ * a sequence has more than one cached position: the per-head norms, the
+ * rotation and the append (qgemv_qk_norm_rope_append), causal attention over
+ * the cache (qgemv_paged_attention), the weight each cached position has
+ * received (qgemv_attention_mass) and the eviction by it (qgemv_cache_evict).
+ *   k, v        fp16 [n_pages][n_kv][page_size][head_dim], 16-byte aligned
+ *   page_table  int32 [n_seqs][max_pages]: entry i of sequence s lies in page
+ *               page_table[s][i / page_size], at row i % page_size
+ *   kv_len      int32 [n_seqs]: entries of each sequence, the new tokens of
+ *               the call included
+ * New tokens of all sequences lie one behind the other: sequence s has rows
+ * q_start[s] .. q_start[s+1]-1 (q_start: int32 [n_seqs+1], device), 0 or more.
+ * Its j-th new token is entry kv_len[s] - q_len + j and sees the entries up
+ * to its own.  Rows before q_start[0] and from q_start[n_seqs] on belong to no
+ * sequence: they are neither read nor written.
+ * Checks of the four calls: head_dim 64 or 128; page_size 16, 32, 64, 128 or
+ * 256; n_pages, n_kv, n_seqs, max_pages >= 1; n_seqs <= 65535; n_kv <= 1024;
+ * max_pages * page_size and n_pages * n_kv * page_size < 2^31 (EINVAL).
+ * What lies on the device is checked by the kernels, which set *err_flag = 1
+ * (device int or NULL; never cleared by the library) and go on: a page number
+ * outside [0, n_pages) is an entry that nothing sees, reads or writes; a
+ * kv_len outside [0, max_pages * page_size] and a q_start that falls or leaves
+ * [0, n_tokens] are clamped.  Pages may be shared between sequences where no
+ * call writes them.  With n_tokens = 0 the arrays of token rows may be NULL.
+ */
+typedef struct {
+  uint16_t *k, *v;
+  const int32_t *page_table;
+  const int32_t *kv_len;
+  int n_pages, page_size, n_kv, head_dim, n_seqs, max_pages;
+} qgemv_kv_cache;
+
+/*
+ * qgemv_qk_norm_rope_append -- from the fused QKV vectors of new tokens to
+ * queries ready for attention and keys and values in the cache, in one pass.
+ * For each token t (row qkv + t * qkv_stride: n_q query, n_kv key, n_kv value
+ * heads) and query or key head x:
+ *   n = x * gamma / sqrt(mean(x^2) + eps)      (gamma = q_norm or k_norm
+ *       [head_dim] fp16; both NULL: n = x)
+ *   pairs (n[i], n[i + rotary_dim/2]) -- interleaved: (n[2i], n[2i+1]) --
+ *   of the first rotary_dim components turn by the angle
+ *   positions[t] * inv_freq[i]; the rest stay,
+ * rounded once to fp16.  Queries go to q_out + t * q_stride, keys and values
+ * (values unchanged) to the token's cache entry.  entry_pos (int32) and
+ * entry_mass (fp32), [n_seqs][n_kv][max_pages * page_size], are optional:
+ * the entry's are set to positions[t] and 0 for every head.  A token whose
+ * entry would be negative (q_len > kv_len) sets *err_flag; its query is
+ * written, its key and value are not.
+ *   positions int32 [n_tokens] (any value; the angle is reduced from the exact
+ *   product), inv_freq fp32 [rotary_dim/2], both device; strides in elements,
+ *   multiples of 4; qkv, q_out, norms 8-byte aligned, the rest 4-byte.
+ *   Checks: n_tokens >= 0 (0: nothing is enqueued), n_q a multiple of n_kv,
+ *   0 <= rotary_dim <= head_dim, a multiple of 8, qkv_stride >= (n_q + 2
+ *   n_kv) * head_dim, q_stride >= n_q * head_dim, eps > 0 when normed, the
+ *   norms both given or both NULL.  One launch.
+ */
+int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
+                              long long qkv_stride, int n_tokens, int n_q,
+                              const int32_t *q_start, const int32_t *positions,
+                              const float *inv_freq, int rotary_dim, int interleaved,
+                              const uint16_t *q_norm, const uint16_t *k_norm, float eps,
+                              uint16_t *q_out, long long q_stride, int32_t *entry_pos,
+                              float *entry_mass, int *err_flag, void *stream);
+
+/*
+ * qgemv_paged_attention -- causal attention of every sequence's new tokens,
+ * one or many, over its cache.  For token t at entry e and query head h, which
+ * reads key/value head h / (n_q / n_kv):
+ *   p_j = exp(scale * q . k_j),  out = sum_{j <= e} p_j v_j / sum_{j <= e} p_j,
+ *   lse = log(sum_{j <= e} p_j)
+ * with fp32 scores, maxima and sums (the weights p_j enter the product with v
+ * as fp16).  A token that sees nothing (e < 0, or only bad pages) gets out = 0
+ * and lse = -inf.  What a token does not see does not reach it, not even as an
+ * infinity or a NaN.
+ *   q, out: fp16 rows of n_q * head_dim, strides in elements; 16-byte aligned,
+ *   strides multiples of 8.  lse: fp32 [n_tokens][n_q] or NULL.
+ *   max_q: the largest q_len (tokens beyond it are left out and set
+ *   *err_flag).  scale > 0.
+ *   workspace: device, 16-byte aligned, workspace_bytes long, contents on entry
+ *   ignored; with fewer than qgemv_paged_attention_workspace_bytes bytes (NULL
+ *   and 0 too) the cache is split over fewer thread blocks, which is slower.
+ *   Calls sharing a workspace must not overlap on the GPU.
+ * Up to two launches (the second joins the parts of a split cache).
+ */
+int qgemv_paged_attention(const qgemv_kv_cache *cache, const uint16_t *q, long long q_stride,
+                          int n_tokens, int n_q, const int32_t *q_start, int max_q, float scale,
+                          uint16_t *out, long long out_stride, float *lse, void *workspace,
+                          size_t workspace_bytes, int *err_flag, void *stream);
+
+/* Workspace with which qgemv_paged_attention is fastest on the current device
+ * (0: it needs none, or an argument is out of range). */
+size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache *cache, int n_tokens, int n_q,
+                                             int max_q);
+
+/*
+ * qgemv_attention_mass -- the attention weight that each cached entry receives
+ * from the call's new tokens, added up over them and over the query heads that
+ * share its key/value head:
+ *   mass_out[s][h][j] = mass[s][h][j] + sum_{t, head : sees j}
+ *                       exp(scale * q . k_j - lse[t][head])
+ * for j < kv_len[s]; what lies behind is left as it was.  q, scale and lse as
+ * qgemv_paged_attention took and gave them (a row with lse = -inf adds
+ * nothing).  mass (NULL: zeros) and mass_out: fp32
+ * [n_seqs][n_kv][max_pages * page_size] device, which may be the same array.
+ * An entry on a bad page receives nothing.  max_q as there; the sums run in a
+ * fixed order.  One launch.
+ */
+int qgemv_attention_mass(const qgemv_kv_cache *cache, const uint16_t *q, long long q_stride,
+                         int n_tokens, int n_q, const int32_t *q_start, int max_q, float scale,
+                         const float *lse, const float *mass, float *mass_out, int *err_flag,
+                         void *stream);
+
+/*
+ * qgemv_cache_evict -- cut every sequence down to `keep` entries, each
+ * key/value head for itself.  Of the entries i < kv_len[s] of head h, keep
+ * stay: first those with entry_pos < n_sink or entry_pos >= next_pos[s] -
+ * n_recent, then those of largest mass, the lower index first among equals (a
+ * NaN ranks below every number).  With len' = min(kv_len[s], keep), survivors
+ * below len' stay where they are; the k-th of those from len' on, in rising
+ * order, moves into the k-th freed place below it.  Attention over a cache
+ * does not depend on the order of the entries that every new token sees, so
+ * only the moved rows of k and v are touched.
+ *   mass fp32, entry_pos int32 [n_seqs][n_kv][max_pages * page_size],
+ *   next_pos int32 [n_seqs]: device, not changed.
+ *   kept     int32 [n_seqs][n_kv][keep]: the former index of each entry now
+ *            below len', -1 from there on
+ *   mass_out, pos_out: as mass and entry_pos, permuted alike below len', left
+ *            as they were from there on
+ *   kv_len_out int32 [n_seqs]: len'
+ * The outputs may not overlap the inputs.  An entry of kept whose page, old or
+ * new, is bad is listed but not copied.  Checks: keep >= 1, n_sink, n_recent
+ * >= 0, n_sink + n_recent <= keep.  Two launches.
+ */
+int qgemv_cache_evict(const qgemv_kv_cache *cache, const float *mass, const int32_t *entry_pos,
+                      const int32_t *next_pos, int keep, int n_sink, int n_recent, int32_t *kept,
+                      float *mass_out, int32_t *pos_out, int32_t *kv_len_out, int *err_flag,
+                      void *stream);
+
+/*
  * qgemv_selftest_wait_timeout -- health check of the bounded device waits
  * every kernel uses: enqueues one tiny kernel on `stream` whose thread waits
  * on a shared-memory mbarrier that nothing ever arrives on, with a limit of
