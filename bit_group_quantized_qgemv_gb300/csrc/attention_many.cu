@@ -1,0 +1,519 @@
+// attention_many.cu -- qgemv_paged_attention for many query rows per
+// key/value head (prompts, chunks of prompts): tcgen05 products, TMA loads.
+//
+// A thread block takes 256 rows (two tiles of 128, A and B) of one (sequence,
+// key/value head) and walks the cache in tiles of 128 entries:
+//   warp 9      producer: K and V tiles by TMA, page by page, into a ring of
+//               128-byte-swizzled slots (keys and values alternate);
+//   warp 8      issues the products: S = Q K^T (operands in shared memory) and
+//               O += P V (P in tensor memory, V as the transposed operand);
+//   warps 0-3   softmax of tile A, warps 4-7 of tile B: one row per thread,
+//               read from tensor memory, weights written back as fp16 over the
+//               scores they came from.
+// While one tile's weights are computed the tensor core works on the other's
+// products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
+// (HD each).
+//
+// The running maximum is lazy: the weights are taken relative to an older
+// maximum until the new one exceeds it by 2^kSlack, so O is rescaled (a round
+// trip through tensor memory) a few times per row instead of at every tile.
+// Weights are then at most 2^kSlack, far inside fp16; their relative rounding is
+// the same as below 1.
+//
+// Entries behind the sequence or on bad pages are loaded as zeros (a TMA box
+// outside the tensor); the rows of the last page behind the sequence's end,
+// which may hold anything, are zeroed in the V tile before the product.
+#include <atomic>
+
+#include "attention_common.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+namespace qgemv {
+namespace {
+
+__device__ unsigned g_status = 0;
+
+constexpr int kTile = 128;           // rows of a tile, entries of a step
+// Three warpgroups; the launch gives 168 registers a thread (64,512 of 65,536), of
+// which the third group passes on what the two of the softmax need: 2 x 128 x
+// 208 + 128 x 80 = 63,488.
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.0f;       // log2 of the growth that makes O be rescaled
+
+template <int HD>
+struct Shape {
+  static constexpr int kHalves = HD / 64;                 // 128-byte columns of a row
+  static constexpr int kSlotBytes = kTile * HD * 2;
+  static constexpr int kSlots = HD == 128 ? 5 : 10;
+  static constexpr int kSmem = 1024 + (2 + kSlots) * kSlotBytes;
+  static constexpr uint32_t kDescS = tc::idesc_f16(kTile, kTile, false);
+  static constexpr uint32_t kDescO = tc::idesc_f16(kTile, HD, true);
+};
+
+struct Bars {
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
+};
+
+// (sequence, row tile) of block unit u: sequences in order, each with
+// ceil(rows / 256) units, the last (longest) first.  s = -1 behind the end.
+__device__ __forceinline__ void find_unit(const AttnArgs& a, int u, int lane, int* s_out, int* rt) {
+  *s_out = -1;
+  *rt = 0;
+  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int first = 0, count = 0;
+    if (s < a.c.n_seqs) seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
+    if (count > a.max_q) flag_error(a.err);
+    const int mine = (min(count, a.max_q) * a.group + 2 * kTile - 1) / (2 * kTile);
+    int incl = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, k);
+      if (lane >= k) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, u < incl);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      const int end = __shfl_sync(0xFFFFFFFFu, incl, l);
+      *s_out = s0 + l;
+      *rt = end - 1 - u;
+      return;
+    }
+    u -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_many_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                          const __grid_constant__ CUtensorMap v_map) {
+  using Sh = Shape<HD>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_unit[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* ring = base + 2 * Sh::kSlotBytes;
+
+  pdl_launch_dependents();
+  if (warp == 8) {
+    if (lane == 0) {
+      for (int i = 0; i < Sh::kSlots; ++i) {
+        mbar_init(smem_u32(&bars.full[i]), 1);
+        mbar_init(smem_u32(&bars.empty[i]), 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(smem_u32(&bars.s_full[x]), 1);
+        mbar_init(smem_u32(&bars.p_full[x]), kTile);
+        mbar_init(smem_u32(&bars.o_full[x]), 1);
+      }
+      mbar_init(smem_u32(&bars.drain), 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+  }
+  pdl_wait();
+  if (warp == 9) {
+    int s, rt;
+    find_unit(a, static_cast<int>(blockIdx.x / (a.n_splits * a.c.n_kv)), lane, &s, &rt);
+    if (lane == 0) {
+      s_unit[0] = s;
+      s_unit[1] = rt;
+    }
+  }
+  __syncthreads();
+  const int s = s_unit[0];
+  if (s < 0) return;
+  const int sp = blockIdx.x % a.n_splits, h = blockIdx.x / a.n_splits % a.c.n_kv;
+  int first, count;
+  seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
+  const int rows = min(count, a.max_q) * a.group;
+  const int r0 = s_unit[1] * 2 * kTile;
+  const int len = seq_len(a.c, s, a.err);
+  const int off = len - count;
+  const int per = part_len(len, a.n_splits, a.part_unit);
+  const int k0 = sp * per;
+  if (sp > 0 && k0 >= len) return;
+  // tiles of entries that tile x sees (its last row sees the most)
+  int nt[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int last = min(rows, r0 + (x + 1) * kTile) - 1;
+    const int see = last >= r0 + x * kTile ? min(min(len, off + last / a.group + 1), k0 + per) : 0;
+    nt[x] = see > k0 ? (see - k0 + kTile - 1) / kTile : 0;
+  }
+  const int tiles = max(nt[0], nt[1]);
+  const bool has_b = r0 + kTile < rows;
+
+  if (warp == 8) {
+    tc::alloc(smem_u32(&s_tmem), 512);
+  } else if (warp < 8 && tiles > 0) {
+    // Queries into the swizzled operand layout: [column of 128 bytes][row][128 B].
+    const int x = warp >> 2;
+    uint8_t* qs = base + x * Sh::kSlotBytes;
+    if (x == 0 || has_b)
+      for (int c = threadIdx.x & 127; c < kTile * (HD / 8); c += 128) {
+        const int r = c / (HD / 8), ch = c % (HD / 8), rr = r0 + x * kTile + r;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < rows)
+          v = *reinterpret_cast<const uint4*>(
+              a.q + static_cast<long long>(first + rr / a.group) * a.q_stride +
+              (h * a.group + rr % a.group) * HD + ch * 8);
+        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + r * 128 +
+                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
+      }
+    tc::fence_async_shared();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == 9) {
+    // ---------------------------------------------------------- producer
+    const int page_rows = min(1 << a.c.page_shift, kTile);
+    const int boxes = kTile / page_rows;  // per tile, at most 8
+    const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;  // a row outside the tensor
+    auto row_of = [&](int j) {
+      const int e = k0 + j * kTile + lane * page_rows;
+      if (lane >= boxes || e >= len) return beyond;
+      const int p = page_of(a.c, s, e, a.err);
+      return p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
+    };
+    int row = tiles > 0 ? row_of(0) : 0, issued = 0;
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int next = j + 1 < tiles ? row_of(j + 1) : 0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int n = 2 * j + w, slot = n % Sh::kSlots, use = n / Sh::kSlots;
+        if (use > 0 && !mbar_wait(smem_u32(&bars.empty[slot]), (use - 1) & 1, &g_status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = smem_u32(&bars.full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(full, Sh::kSlotBytes);
+        __syncwarp();
+        issued = n + 1;
+        if (lane < boxes) {
+          const uint32_t dst = smem_u32(ring + slot * Sh::kSlotBytes) + lane * page_rows * 128;
+#pragma unroll
+          for (int c = 0; c < Sh::kHalves; ++c)
+            tc::tma_2d(dst + c * (kTile * 128), w == 0 ? &k_map : &v_map, c * 64, row, full);
+        }
+        __syncwarp();
+      }
+      row = next;
+    }
+    // no copy may be in flight when the block ends
+    for (int n = max(0, issued - Sh::kSlots); n < issued; ++n)
+      mbar_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
+  } else if (warp == 8) {
+    // ---------------------------------------------------------- products
+    auto slot_of = [&](int n) { return smem_u32(ring + (n % Sh::kSlots) * Sh::kSlotBytes); };
+    auto wait_full = [&](int n) {
+      return mbar_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
+    };
+    auto release = [&](int n) { tc::commit(smem_u32(&bars.empty[n % Sh::kSlots])); };
+    auto scores = [&](int x, int j) {
+      if (lane == 0) {
+        const uint64_t q = tc::desc_k_major(smem_u32(base + x * Sh::kSlotBytes));
+        const uint64_t k = tc::desc_k_major(slot_of(2 * j));
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+          const int step = (i / 4) * (kTile * 128) + (i % 4) * 32;
+          tc::mma_ss(tmem + x * kTile, q + (step >> 4), k + (step >> 4), Sh::kDescS, i > 0);
+        }
+        tc::commit(smem_u32(&bars.s_full[x]));
+      }
+    };
+    if (tiles > 0) ok = wait_full(0);
+    if (ok && tiles > 0) {
+      if (nt[0] > 0) scores(0, 0);
+      if (nt[1] > 0) scores(1, 0);
+      if (lane == 0) release(0);
+    }
+    for (int j = 0; j < tiles && ok; ++j) {
+      if (!wait_full(2 * j + 1)) {
+        ok = false;
+        break;
+      }
+      const int e0 = k0 + j * kTile;
+      if (len < e0 + kTile) {
+        // the rest of the last page may hold anything
+        const int ps = 1 << a.c.page_shift;
+        const int from = len - e0, to = min(kTile, (from + ps - 1) / ps * ps);
+        uint8_t* v = ring + ((2 * j + 1) % Sh::kSlots) * Sh::kSlotBytes;
+        for (int c = lane; c < (to - from) * 8 * Sh::kHalves; c += 32) {
+          const int r = from + c / (8 * Sh::kHalves), ch = c % (8 * Sh::kHalves);
+          *reinterpret_cast<uint4*>(v + (ch >> 3) * (kTile * 128) + r * 128 + (ch & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        tc::fence_async_shared();
+        __syncwarp();
+      }
+      const bool more = j + 1 < tiles;
+      bool have_k = false;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (j < nt[x] && ok) {
+          if (!mbar_wait(smem_u32(&bars.p_full[x]), j & 1, &g_status)) {
+            ok = false;
+          } else {
+            tc::fence_after();
+            if (lane == 0) {
+              const uint64_t v = tc::desc_mn_major(slot_of(2 * j + 1), kTile * 128);
+#pragma unroll
+              for (int i = 0; i < kTile / 16; ++i)
+                tc::mma_ts(tmem + 2 * kTile + x * HD, tmem + x * kTile + i * 8, v + (i * 2048 >> 4),
+                           Sh::kDescO, j > 0 || i > 0);
+              if (j == nt[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
+            }
+          }
+        }
+        if (x == 1 && lane == 0 && ok) release(2 * j + 1);
+        if (more && ok && j + 1 < nt[x]) {
+          if (!have_k) {
+            ok = wait_full(2 * j + 2);
+            have_k = true;
+          }
+          if (ok) scores(x, j + 1);
+        }
+      }
+      if (more && ok && lane == 0) release(2 * j + 2);
+    }
+    // every product is done before tensor memory goes back
+    if (lane == 0) tc::commit(smem_u32(&bars.drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&bars.drain), 0, &g_status);
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ----------------------------------------------------------- softmax
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane, rr = r0 + x * kTile + r;
+    const bool live = rr < rows;
+    const int i = live ? rr / a.group : 0;
+    const int lim = live ? off + i : -1;
+    const uint32_t lanes = tmem + ((warp & 3) << 21);  // 32 lanes per warp, lane in bits 16..
+    const uint32_t st = lanes + x * kTile, ot = lanes + 2 * kTile + x * HD;
+    auto bad_pages = [&](int j) {  // lane b: entries 16b.. of tile j lie on a bad page
+      const int e = k0 + j * kTile + lane * 16;
+      return lane < kTile / 16 && e < len && page_of(a.c, s, e, nullptr) < 0;
+    };
+    float m = -INFINITY, l = 0.f;
+    bool bad_next = nt[x] > 0 && bad_pages(0);
+    for (int j = 0; j < nt[x]; ++j) {
+      const unsigned bad = __ballot_sync(0xFFFFFFFFu, bad_next);
+      if (j + 1 < nt[x]) bad_next = bad_pages(j + 1);
+      if (!mbar_wait(smem_u32(&bars.s_full[x]), j & 1, &g_status)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after();
+      uint32_t v[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::ld32(v + 32 * c, st + 32 * c);
+      tc::wait_ld128(v);
+      const int hide = lim - (k0 + j * kTile);  // entries above this one are hidden
+      if (__any_sync(0xFFFFFFFFu, hide < kTile - 1)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k > hide) v[k] = 0xFF800000u;
+      }
+      if (bad != 0) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if ((bad >> (k / 16)) & 1) v[k] = 0xFF800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      // a row grows from nothing, or past the slack: rescale
+      const bool grow = mt > m + kSlack || (m == -INFINITY && mt > m);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float mn = fmaxf(m, mt);
+        const float f = mn == m ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tc::ld32(o, ot + c);
+            tc::wait_ld32(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tc::st32(ot + c, o);
+          }
+        }
+      }
+      const float b = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float x0 = ex2(fmaf(__uint_as_float(v[64 * c + 2 * k]), a.scale_log2, -b));
+          const float x1 = ex2(fmaf(__uint_as_float(v[64 * c + 2 * k + 1]), a.scale_log2, -b));
+          sum[(2 * k) & 3] += x0;
+          sum[(2 * k + 1) & 3] += x1;
+          p[k] = pack_f16(x0, x1);
+        }
+        tc::st32(st + 32 * c, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc::wait_st();
+      tc::fence_before();
+      mbar_arrive(smem_u32(&bars.p_full[x]));
+    }
+    if (ok && nt[x] > 0 && !mbar_wait(smem_u32(&bars.o_full[x]), 0, &g_status)) ok = false;
+    tc::fence_after();
+    const int t = first + i, head = h * a.group + (live ? rr % a.group : 0);
+    const long long at = static_cast<long long>(t) * a.n_q + head;
+    if (ok && a.n_splits > 1) {
+      float* po = a.part_o + (static_cast<long long>(sp) * a.n_tokens * a.n_q + at) * HD;
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t o[32];
+        if (nt[x] > 0) {
+          tc::ld32(o, ot + c);
+          tc::wait_ld32(o);
+        }
+        if (live)
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4*>(po + c + k) =
+                nt[x] > 0 ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
+      }
+      if (live) a.part_ml[static_cast<long long>(sp) * a.n_tokens * a.n_q + at] = make_float2(m, l);
+    } else if (ok) {
+      const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
+      bool odd = false;
+      __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD;
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t o[32];
+        if (nt[x] > 0) {
+          tc::ld32(o, ot + c);
+          tc::wait_ld32(o);
+        }
+        float w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          w[k] = nt[x] > 0 ? __uint_as_float(o[k]) * inv : 0.f;
+          odd |= !(fabsf(w[k]) <= 3.0e38f);
+        }
+        if (live)
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(y + c + k) =
+                make_uint4(pack_f16(w[k], w[k + 1]), pack_f16(w[k + 2], w[k + 3]),
+                           pack_f16(w[k + 4], w[k + 5]), pack_f16(w[k + 6], w[k + 7]));
+      }
+      if (live && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * kLn2;
+      // rows that hide entries and came out infinite or NaN: again, without them
+      unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && lim < len - 1);
+      while (again != 0) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int tt = __shfl_sync(0xFFFFFFFFu, t, src), hh = __shfl_sync(0xFFFFFFFFu, head, src);
+        const int ll = __shfl_sync(0xFFFFFFFFu, lim, src);
+        __syncwarp();
+        slow_row<HD>(a, s, h, tt, hh, ll, lane);
+      }
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+// Map of a pool as rows of HD values, boxes of 64 columns and up to 128 rows.
+bool encode_pool(CUtensorMap* m, const KvView& c, const __half* pool) {
+  const EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int page = 1 << c.page_shift;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(c.head_dim),
+                             static_cast<cuuint64_t>(c.n_pages) * c.n_kv * page};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(c.head_dim) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(page < kTile ? page : kTile)};
+  const cuuint32_t estride[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(pool), dim, stride, box,
+            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD>
+cudaError_t launch_many(const AttnArgs& a, cudaStream_t st, int device) {
+  static std::atomic<unsigned long long> done{0};
+  auto* k = attention_many_kernel<HD>;
+  const unsigned long long bit = 1ull << (device & 63);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<HD>::kSmem);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  CUtensorMap km, vm;
+  if (!encode_pool(&km, a.c, a.c.k) || !encode_pool(&vm, a.c, a.c.v)) return cudaErrorInvalidValue;
+  const long long blocks =
+      attention_many_units(a.c.n_seqs, a.n_tokens, a.group, a.max_q) * a.c.n_kv * a.n_splits;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<HD>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, a, km, vm);
+}
+
+}  // namespace
+
+// Upper bound of the row tiles (256 rows) of all sequences: a sequence adds
+// at most one that is not full.
+long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q) {
+  const long long each = (static_cast<long long>(max_q) * group + 2 * kTile - 1) / (2 * kTile);
+  const long long full = static_cast<long long>(n_tokens) * group / (2 * kTile);
+  const long long part = n_seqs < n_tokens ? n_seqs : n_tokens;
+  const long long bound = full + part;
+  return each * n_seqs < bound ? each * n_seqs : bound;
+}
+
+// Parts of the cache: as many as fill the machine once (a block takes a whole
+// multiprocessor), each of 512 entries at least.
+int attention_many_splits(long long units, int n_kv, long long capacity, int sms) {
+  long long want = sms / (units * n_kv);
+  const long long most = (capacity + 511) / 512;
+  if (want > most) want = most;
+  return want < 1 ? 1 : static_cast<int>(want);
+}
+
+cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device) {
+  return a.c.head_dim == 64 ? launch_many<64>(a, st, device) : launch_many<128>(a, st, device);
+}
+
+cudaError_t status_attention(unsigned* out) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *out |= v;
+  return e;
+}
+
+}  // namespace qgemv

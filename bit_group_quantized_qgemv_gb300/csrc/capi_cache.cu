@@ -118,13 +118,15 @@ size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache* cache, int n_
   KvView c{};
   if (check_cache(cache, &c) != QGEMV_OK ||
       check_queries(c, static_cast<long long>(n_q) * c.head_dim, n_tokens, n_q, max_q, 1.0f) !=
-          QGEMV_OK)
+          QGEMV_OK ||
+      n_tokens == 0)
     return 0;
   int dev, sms;
   if (qgemv::device_and_sms(&dev, &sms) != QGEMV_OK) return 0;
   const long long cap = static_cast<long long>(c.max_pages) << c.page_shift;
   return qgemv::attention_part_bytes(
-      qgemv::attention_splits(c.n_seqs, c.n_kv, n_q / c.n_kv, max_q, cap, sms), n_tokens, n_q,
+      qgemv::attention_splits(c.n_seqs, c.n_kv, n_tokens, n_q / c.n_kv,
+                               max_q < n_tokens ? max_q : n_tokens, cap, sms), n_tokens, n_q,
       c.head_dim);
 }
 
@@ -158,7 +160,8 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
   a.lse = lse;
   a.err = err_flag;
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  int splits = qgemv::attention_splits(a.c.n_seqs, a.c.n_kv, a.group, a.max_q, cap, sms);
+  int splits = qgemv::attention_splits(a.c.n_seqs, a.c.n_kv, n_tokens, a.group, a.max_q, cap,
+                                       sms);
   while (splits > 1 &&
          qgemv::attention_part_bytes(splits, n_tokens, n_q, a.c.head_dim) > workspace_bytes)
     --splits;

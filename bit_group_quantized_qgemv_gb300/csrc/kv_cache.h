@@ -50,6 +50,7 @@ struct AttnArgs {
   float* part_o;
   float2* part_ml;
   int n_splits, row_tiles;
+  int part_unit;  // parts are multiples of this many entries
   int* err;
 };
 
@@ -83,9 +84,19 @@ cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st);
 cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st);
 
 // Parts the cache is split into for a call of these sizes.
-int attention_splits(int n_seqs, int n_kv, int group, int max_q, long long capacity, int sms);
+int attention_splits(int n_seqs, int n_kv, int n_tokens, int group, int max_q, long long capacity,
+                     int sms);
 // Bytes of workspace for that many parts.
 size_t attention_part_bytes(int splits, int n_tokens, int n_q, int head_dim);
+// Whether a call has more query rows per key/value head than the mma.sync
+// kernel takes in one pass over the cache: those go to the tcgen05 kernel.
+inline bool attention_is_many(int group, int max_q) {
+  return static_cast<long long>(group) * max_q > 32;
+}
+long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q);
+int attention_many_splits(long long units, int n_kv, long long capacity, int sms);
+cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device);
+cudaError_t status_attention(unsigned* out);
 cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device);
 
 }  // namespace qgemv

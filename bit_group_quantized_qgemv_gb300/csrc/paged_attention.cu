@@ -17,7 +17,7 @@
 // is bound by HBM.
 #include <atomic>
 
-#include "kv_cache.cuh"
+#include "attention_common.cuh"
 
 namespace qgemv {
 namespace {
@@ -25,7 +25,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTile = 16;    // entries per warp and step
 constexpr int kStages = 3;   // ring depth of each warp
-constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int HD>
 __host__ __device__ constexpr int stage_bytes() {
@@ -54,50 +53,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
                : "r"(addr));
 }
 
-// Entries of one part of a sequence's cache (the same in every kernel).
-__device__ __forceinline__ int part_len(int len, int n_splits) {
-  const int per = (len + n_splits - 1) / n_splits;
-  return (per + 63) / 64 * 64;
-}
-
 // Byte offset of 16-byte chunk ch of row r in a tile of HD-wide rows; the
 // swizzle spreads 8 rows over the banks.
 template <int HD>
 __device__ __forceinline__ int tile_off(int r, int ch) {
   return r * (HD * 2) + ((ch ^ (r & 7)) << 4);
-}
-
-// One row computed entry by entry in fp32, by a whole warp: taken where a
-// value that the row does not see is an infinity or a NaN, which the tensor
-// cores' 0 * v would carry into it.  Writes out and returns nothing else (the
-// maximum and the sum are not affected by values).
-template <int HD>
-__device__ __noinline__ void slow_row(const AttnArgs& a, int s, int h, int t, int head, int last,
-                                      int lane) {
-  constexpr int D = HD / 32;
-  const __half* q = a.q + static_cast<long long>(t) * a.q_stride + head * HD + lane * D;
-  float qv[D], o[D], m = -INFINITY, l = 0.f;
-  for (int d = 0; d < D; ++d) {
-    qv[d] = __half2float(q[d]);
-    o[d] = 0.f;
-  }
-  for (int j = 0; j <= last; ++j) {
-    const int p = page_of(a.c, s, j, nullptr);
-    if (p < 0) continue;
-    const long long at = cache_row(a.c, p, h, j) * HD + lane * D;
-    float x = 0.f;
-    for (int d = 0; d < D; ++d) x = fmaf(qv[d], __half2float(a.c.k[at + d]), x);
-    for (int k = 16; k > 0; k /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ms), w = ex2(x - ms);
-    l = l * f + w;
-    for (int d = 0; d < D; ++d) o[d] = o[d] * f + w * __half2float(a.c.v[at + d]);
-    m = mn;
-  }
-  __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD + lane * D;
-  const float r = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
-  for (int d = 0; d < D; ++d) y[d] = __float2half_rn(o[d] * r);
 }
 
 template <int HD, int MT>
@@ -130,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   const int nr = min(kRows, rows - r0);
   const int len = seq_len(a.c, s, a.err);
   const int off = len - count;  // token i sees entries up to off + i
-  const int per = part_len(len, a.n_splits);
+  const int per = part_len(len, a.n_splits, a.part_unit);
   const int k0 = sp * per;
   if (sp > 0 && k0 >= len) return;  // the join knows
   // entries that some row of this block sees
@@ -328,22 +288,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
       if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
       continue;
     }
-    const float inv = ll > 0.f || !(ll == ll) ? 1.0f / ll : 0.f;
-    bool odd = false;
-    __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD + lane * D;
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const float v = acc[d] * inv;
-      odd |= !(fabsf(v) <= 3.0e38f);
-      y[d] = __float2half_rn(v);
-    }
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[static_cast<long long>(t) * a.n_q + head] = (mm + log2f(ll)) * kLn2;
-    const int last = min(off + i, len - 1);
-    if (__any_sync(0xFFFFFFFFu, odd) && last < len - 1) {
-      __syncwarp();
-      slow_row<HD>(a, s, h, t, head, last, lane);
-    }
+    store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
   }
 }
 
@@ -365,7 +310,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
   if (i >= count) return;
   const int t = first + i;
   const int len = seq_len(a.c, s, nullptr);
-  const int per = part_len(len, a.n_splits);
+  const int per = part_len(len, a.n_splits, a.part_unit);
   const int parts = len > 0 ? (len + per - 1) / per : 1;
   const long long step = static_cast<long long>(a.n_tokens) * a.n_q;
   const long long at = static_cast<long long>(t) * a.n_q + head;
@@ -384,21 +329,7 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
 #pragma unroll
     for (int d = 0; d < D; ++d) acc[d] += o[d] * f;
   }
-  const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
-  bool odd = false;
-  __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD + lane * D;
-#pragma unroll
-  for (int d = 0; d < D; ++d) {
-    const float v = acc[d] * inv;
-    odd |= !(fabsf(v) <= 3.0e38f);
-    y[d] = __float2half_rn(v);
-  }
-  if (lane == 0 && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * kLn2;
-  const int last = min(len - count + i, len - 1);
-  if (__any_sync(0xFFFFFFFFu, odd) && last < len - 1) {
-    __syncwarp();
-    slow_row<HD>(a, s, head / a.group, t, head, last, lane);
-  }
+  store_row<HD>(a, s, head / a.group, t, head, min(len - count + i, len - 1), len, acc, m, l, lane);
 }
 
 template <typename F>
@@ -437,8 +368,12 @@ cudaError_t launch_few(AttnArgs a, cudaStream_t st, int device) {
 
 }  // namespace
 
-int attention_splits(int n_seqs, int n_kv, int group, int max_q, long long capacity, int sms) {
+int attention_splits(int n_seqs, int n_kv, int n_tokens, int group, int max_q, long long capacity,
+                     int sms) {
   const long long rows = static_cast<long long>(max_q) * group;
+  if (attention_is_many(group, max_q))
+    return attention_many_splits(attention_many_units(n_seqs, n_tokens, group, max_q), n_kv,
+                                 capacity, sms);
   const long long tiles = rows <= 16 ? 1 : (rows + 31) / 32;
   const long long units = tiles * n_kv * n_seqs;
   long long want = (2LL * sms + units - 1) / units;  // two blocks to a multiprocessor
@@ -456,7 +391,10 @@ cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int dev
   (void)sms;
   const bool one = a.max_q * a.group <= 16;
   cudaError_t e;
-  if (a.c.head_dim == 64)
+  a.part_unit = attention_is_many(a.group, a.max_q) ? 128 : 64;
+  if (attention_is_many(a.group, a.max_q))
+    e = attention_many_launch(a, st, device);
+  else if (a.c.head_dim == 64)
     e = one ? launch_few<64, 1>(a, st, device) : launch_few<64, 2>(a, st, device);
   else
     e = one ? launch_few<128, 1>(a, st, device) : launch_few<128, 2>(a, st, device);

@@ -36,6 +36,7 @@
 #include <mutex>
 
 #include "qgemv_stream.cuh"
+#include "tensor_map.h"
 
 namespace qgemv {
 namespace {
@@ -658,27 +659,6 @@ bool pick_chunk(int bits, int K, int cl, int xs_bytes, int* kc_out, int* stage_o
   *stage_out = stage_bytes_for(bits, K, kc, cl);
   *ns_out = ring(kc);
   return true;
-}
-
-// The driver's cuTensorMapEncodeTiled, reached through the runtime.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// (looked up once, thread-safely; null when the driver does not provide it)
-EncodeTiledFn encode_fn() {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<EncodeTiledFn>(f);
-    cudaGetLastError();
-    return static_cast<EncodeTiledFn>(nullptr);
-  }();
-  return fn;
 }
 
 // 2-D byte-tensor map of `rows` rows of `row_bytes` bytes, boxes of
