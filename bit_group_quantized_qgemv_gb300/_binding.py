@@ -129,7 +129,6 @@ def _cuda(t, dtypes, name):
 
 _CODES = (torch.int32, getattr(torch, "uint32", torch.int32))
 _F16 = (torch.float16,)
-_F32 = (torch.float32,)
 _I32 = (torch.int32,)
 
 
@@ -517,13 +516,17 @@ class KVCache:
             raise ValueError("k and v must both be [n_pages][n_kv][page_size][head_dim]")
         if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1]:
             raise ValueError("page_table must be [n_seqs][max_pages] and kv_len [n_seqs]")
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         for name, t in (("v", v), ("page_table", page_table), ("kv_len", kv_len)):
             if t.device != self.device:
                 raise ValueError(f"{name} is on {t.device}, k on {self.device}")
         n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
         self.n_seqs, self.max_pages = page_table.shape
         self.capacity = self.max_pages * self.page_size
+        self.starts = (self.n_seqs + 1,)                       # shape of q_start
+        self.entries = (self.n_seqs, self.n_kv, self.capacity)  # shape of mass and entry_pos
+        self.scale = self.head_dim ** -0.5
+        self.workspace_sizes = {}
         self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), page_table.data_ptr(),
                                     kv_len.data_ptr(), n_pages, self.page_size, self.n_kv,
                                     self.head_dim, self.n_seqs, self.max_pages)
@@ -538,55 +541,61 @@ def kv_cache(k, v, page_table, kv_len) -> KVCache:
     return KVCache(k, v, page_table, kv_len)
 
 
-class _On:
-    """The device and stream of a cache call: launches go to the cache's
-    device, and what the call allocates belongs to the stream it runs on."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, []
-
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"stream is on {self.stream.device}, the cache on {self.device}")
-            self.guards.append(torch.cuda.stream(self.stream))
-        elif torch.cuda.current_device() != self.device.index:
-            self.guards.append(torch.cuda.device(self.device))
-        for g in self.guards:
-            g.__enter__()
-        return ctypes.c_void_p((self.stream or torch.cuda.current_stream()).cuda_stream)
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+# The current stream's handle of a device, without making a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _at(cache, t, dtypes, name, shape=None):
-    """A contiguous tensor on the cache's device, of the given shape; None passes."""
+def _on(cache, stream, body):
+    """body(stream handle) with the cache's device current; what it allocates
+    belongs to the stream its kernels run on."""
+    index = cache.index
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if stream.device != cache.device:
+        raise ValueError(f"stream is on {stream.device}, the cache on {cache.device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _at(cache, t, dtype, name, shape=None):
+    """Address of a contiguous tensor on the cache's device, of the given
+    shape; None for None."""
     if t is None:
         return None
-    _cuda(t, dtypes, name)
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if (t.dtype is not dtype or t.get_device() != cache.index or not t.is_contiguous() or
+            (shape is not None and t.shape != shape)):
+        _cuda(t, (dtype,), name)
+        if t.get_device() != cache.index:
+            raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _token_rows(cache, t, name, width=None):
+def _token_rows(cache, t, name, rows=None, width=None):
     """fp16 rows of tokens, [tokens][width] or [tokens][heads][head_dim], whose
-    row stride is free: (width, row stride)."""
-    if not t.is_cuda or t.device != cache.device:
+    row stride is free: (address, tokens, width, row stride)."""
+    if t.get_device() != cache.index:
         raise ValueError(f"{name} must be a CUDA tensor on {cache.device}")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float16")
-    if t.dim() not in (2, 3) or t.stride(-1) != 1 or (t.dim() == 3 and
-                                                      t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        n, w = shape
+        inner = stride[1] == 1
+    elif len(shape) == 3:
+        n, w = shape[0], shape[1] * shape[2]
+        inner = stride[2] == 1 and stride[1] == shape[2]
+    else:
+        inner = False
+    if not inner:
         raise ValueError(f"{name} must be rows of tokens, contiguous within a row")
-    w = t.shape[1] * (t.shape[2] if t.dim() == 3 else 1)
-    if width is not None and w != width:
-        raise ValueError(f"{name} has rows of {w}, expected {width}")
-    return w, (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), w))
+    if (width is not None and w != width) or (rows is not None and n != rows):
+        raise ValueError(f"{name} has {n} rows of {w}, expected {rows} of {width}")
+    return t.data_ptr(), n, w, stride[0] if n > 1 else max(stride[0], w)
 
 
 def _heads(cache, width, extra, name):
@@ -603,36 +612,41 @@ def qk_norm_rope_append(cache, qkv, q_start, positions, inv_freq=None, interleav
     keys in qkv [tokens][(n_q + 2 n_kv) head_dim], keys and values into the
     cache.  inv_freq: fp32 [rotary_dim / 2], None for no rotation.  Returns
     q_out [tokens][n_q head_dim]."""
-    width, stride = _token_rows(cache, qkv, "qkv")
-    n_q, T = _heads(cache, width, 2 * cache.n_kv, "qkv"), qkv.shape[0]
-    with _On(cache.device, stream) as st:
-        if q_out is None:
-            q_out = torch.empty(T, n_q * cache.head_dim, dtype=torch.float16, device=cache.device)
-        _, q_stride = _token_rows(cache, q_out, "q_out", n_q * cache.head_dim)
-        if q_out.shape[0] != T:
-            raise ValueError(f"q_out has {q_out.shape[0]} rows, qkv {T}")
-        entries = (cache.n_seqs, cache.n_kv, cache.capacity)
-        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
-        _at(cache, positions, _I32, "positions", (T,))
-        _at(cache, inv_freq, _F32, "inv_freq")
-        _at(cache, q_norm, _F16, "q_norm", (cache.head_dim,))
-        _at(cache, k_norm, _F16, "k_norm", (cache.head_dim,))
-        _at(cache, entry_pos, _I32, "entry_pos", entries)
-        _at(cache, entry_mass, _F32, "entry_mass", entries)
-        _at(cache, err_flag, _I32, "err_flag")
-        rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
-        rc = lib.qgemv_qk_norm_rope_append(
-            cache.ref, _ptr(qkv), stride, T, n_q, _ptr(q_start), _ptr(positions), _ptr(inv_freq),
-            rotary, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm), float(eps), _ptr(q_out),
-            q_stride, _ptr(entry_pos), _ptr(entry_mass), _ptr(err_flag), st)
-    _check(rc, "qgemv_qk_norm_rope_append")
-    return q_out
+    x, T, width, stride = _token_rows(cache, qkv, "qkv")
+    hd = cache.head_dim
+    n_q = _heads(cache, width, 2 * cache.n_kv, "qkv")
+
+    def body(st):
+        y = q_out
+        if y is None:
+            y = torch.empty(T, n_q * hd, dtype=torch.float16, device=cache.device)
+        yp, _, _, y_stride = _token_rows(cache, y, "q_out", T, n_q * hd)
+        _check(lib.qgemv_qk_norm_rope_append(
+            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
+            _at(cache, positions, torch.int32, "positions", (T,)),
+            _at(cache, inv_freq, torch.float32, "inv_freq"),
+            0 if inv_freq is None else 2 * inv_freq.numel(), bool(interleaved),
+            _at(cache, q_norm, torch.float16, "q_norm", (hd,)),
+            _at(cache, k_norm, torch.float16, "k_norm", (hd,)), eps, yp, y_stride,
+            _at(cache, entry_pos, torch.int32, "entry_pos", cache.entries),
+            _at(cache, entry_mass, torch.float32, "entry_mass", cache.entries),
+            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_qk_norm_rope_append")
+        return y
+
+    return _on(cache, stream, body)
 
 
 def paged_attention_workspace_bytes(cache, n_tokens, n_q, max_q) -> int:
-    with _On(cache.device, None):
-        return int(lib.qgemv_paged_attention_workspace_bytes(cache.ref, int(n_tokens), int(n_q),
-                                                             int(max_q)))
+    """Workspace with which paged_attention is fastest for these sizes."""
+    key = (int(n_tokens), int(n_q), int(max_q))
+    n = cache.workspace_sizes.get(key)
+    if n is None:
+        n = _on(cache, None, lambda st: int(
+            lib.qgemv_paged_attention_workspace_bytes(cache.ref, *key)))
+        if len(cache.workspace_sizes) >= 1024:
+            cache.workspace_sizes.clear()
+        cache.workspace_sizes[key] = n
+    return n
 
 
 def paged_attention(cache, q, q_start, max_q=None, scale=None, out=None, want_lse=False, lse=None,
@@ -641,34 +655,33 @@ def paged_attention(cache, q, q_start, max_q=None, scale=None, out=None, want_ls
     its cache; q [tokens][n_q head_dim].  max_q: the largest number of new
     tokens in a sequence (default: all).  scale: default head_dim ** -0.5.
     Returns (out, lse fp32 [tokens][n_q] or None)."""
-    width, stride = _token_rows(cache, q, "q")
-    n_q, T = _heads(cache, width, 0, "q"), q.shape[0]
+    x, T, width, stride = _token_rows(cache, q, "q")
+    n_q = _heads(cache, width, 0, "q")
     max_q = max(T, 1) if max_q is None else int(max_q)
-    with _On(cache.device, stream) as st:
-        if out is None:
-            out = torch.empty(T, width, dtype=torch.float16, device=cache.device)
-        _, out_stride = _token_rows(cache, out, "out", width)
-        if out.shape[0] != T:
-            raise ValueError(f"out has {out.shape[0]} rows, q {T}")
-        if lse is None and want_lse:
-            lse = torch.empty(T, n_q, dtype=torch.float32, device=cache.device)
-        _at(cache, lse, _F32, "lse", (T, n_q))
-        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
-        _at(cache, err_flag, _I32, "err_flag")
-        if workspace is None:
-            n = int(lib.qgemv_paged_attention_workspace_bytes(cache.ref, T, n_q, max_q))
+
+    def body(st):
+        y, z, ws = out, lse, workspace
+        if y is None:
+            y = torch.empty(T, width, dtype=torch.float16, device=cache.device)
+        yp, _, _, y_stride = _token_rows(cache, y, "out", T, width)
+        if z is None and want_lse:
+            z = torch.empty(T, n_q, dtype=torch.float32, device=cache.device)
+        if ws is None:
+            n = paged_attention_workspace_bytes(cache, T, n_q, max_q)
             if n:
-                workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
-        elif workspace.device != cache.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous, on the cache's device")
-        rc = lib.qgemv_paged_attention(
-            cache.ref, _ptr(q), stride, T, n_q, _ptr(q_start), max_q,
-            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(out), out_stride,
-            _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(err_flag), st)
-    _check(rc, "qgemv_paged_attention")
-    return out, lse
+                ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        else:
+            if ws.get_device() != cache.index or not ws.is_contiguous():
+                raise ValueError("workspace must be contiguous, on the cache's device")
+            n = ws.numel() * ws.element_size()
+        _check(lib.qgemv_paged_attention(
+            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
+            max_q, cache.scale if scale is None else scale, yp, y_stride,
+            _at(cache, z, torch.float32, "lse", (T, n_q)), ws.data_ptr() if n else None, n,
+            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_paged_attention")
+        return y, z
+
+    return _on(cache, stream, body)
 
 
 def attention_mass(cache, q, q_start, lse, max_q=None, scale=None, mass=None, mass_out=None,
@@ -677,24 +690,24 @@ def attention_mass(cache, q, q_start, lse, max_q=None, scale=None, mass=None, ma
     the attention weight every cached entry receives from the new tokens; q
     and lse as paged_attention took and gave them.  Returns mass_out (a new
     array is zero behind each sequence's length; it may be mass itself)."""
-    width, stride = _token_rows(cache, q, "q")
-    n_q, T = _heads(cache, width, 0, "q"), q.shape[0]
+    x, T, width, stride = _token_rows(cache, q, "q")
+    n_q = _heads(cache, width, 0, "q")
     max_q = max(T, 1) if max_q is None else int(max_q)
-    entries = (cache.n_seqs, cache.n_kv, cache.capacity)
-    with _On(cache.device, stream) as st:
-        if mass_out is None:
-            mass_out = torch.zeros(entries, dtype=torch.float32, device=cache.device)
-        _at(cache, mass, _F32, "mass", entries)
-        _at(cache, mass_out, _F32, "mass_out", entries)
-        _at(cache, lse, _F32, "lse", (T, n_q))
-        _at(cache, q_start, _I32, "q_start", (cache.n_seqs + 1,))
-        _at(cache, err_flag, _I32, "err_flag")
-        rc = lib.qgemv_attention_mass(
-            cache.ref, _ptr(q), stride, T, n_q, _ptr(q_start), max_q,
-            float(cache.head_dim ** -0.5 if scale is None else scale), _ptr(lse), _ptr(mass),
-            _ptr(mass_out), _ptr(err_flag), st)
-    _check(rc, "qgemv_attention_mass")
-    return mass_out
+
+    def body(st):
+        y = mass_out
+        if y is None:
+            y = torch.zeros(cache.entries, dtype=torch.float32, device=cache.device)
+        _check(lib.qgemv_attention_mass(
+            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
+            max_q, cache.scale if scale is None else scale,
+            _at(cache, lse, torch.float32, "lse", (T, n_q)),
+            _at(cache, mass, torch.float32, "mass", cache.entries),
+            _at(cache, y, torch.float32, "mass_out", cache.entries),
+            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_attention_mass")
+        return y
+
+    return _on(cache, stream, body)
 
 
 def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, kept=None,
@@ -704,31 +717,31 @@ def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, ke
     head for itself; rows of the cache move in place.  Returns (kept int32
     [n_seqs][n_kv][keep], mass_out, pos_out, kv_len_out); kv_len_out is the new
     length, to be written into the cache's kv_len before the next call."""
-    entries = (cache.n_seqs, cache.n_kv, cache.capacity)
     keep = int(keep)
-    with _On(cache.device, stream) as st:
-        if kept is None:
-            kept = torch.empty(cache.n_seqs, cache.n_kv, max(keep, 0), dtype=torch.int32,
-                               device=cache.device)
-        if mass_out is None:
-            mass_out = torch.zeros(entries, dtype=torch.float32, device=cache.device)
-        if pos_out is None:
-            pos_out = torch.zeros(entries, dtype=torch.int32, device=cache.device)
-        if kv_len_out is None:
-            kv_len_out = torch.empty(cache.n_seqs, dtype=torch.int32, device=cache.device)
-        _at(cache, mass, _F32, "mass", entries)
-        _at(cache, entry_pos, _I32, "entry_pos", entries)
-        _at(cache, next_pos, _I32, "next_pos", (cache.n_seqs,))
-        _at(cache, kept, _I32, "kept", (cache.n_seqs, cache.n_kv, keep))
-        _at(cache, mass_out, _F32, "mass_out", entries)
-        _at(cache, pos_out, _I32, "pos_out", entries)
-        _at(cache, kv_len_out, _I32, "kv_len_out", (cache.n_seqs,))
-        _at(cache, err_flag, _I32, "err_flag")
-        rc = lib.qgemv_cache_evict(cache.ref, _ptr(mass), _ptr(entry_pos), _ptr(next_pos), keep,
-                                   int(n_sink), int(n_recent), _ptr(kept), _ptr(mass_out),
-                                   _ptr(pos_out), _ptr(kv_len_out), _ptr(err_flag), st)
-    _check(rc, "qgemv_cache_evict")
-    return kept, mass_out, pos_out, kv_len_out
+    S, dev = cache.n_seqs, cache.device
+
+    def body(st):
+        k, m, p, n = kept, mass_out, pos_out, kv_len_out
+        if k is None:
+            k = torch.empty(S, cache.n_kv, max(keep, 0), dtype=torch.int32, device=dev)
+        if m is None:
+            m = torch.zeros(cache.entries, dtype=torch.float32, device=dev)
+        if p is None:
+            p = torch.zeros(cache.entries, dtype=torch.int32, device=dev)
+        if n is None:
+            n = torch.empty(S, dtype=torch.int32, device=dev)
+        _check(lib.qgemv_cache_evict(
+            cache.ref, _at(cache, mass, torch.float32, "mass", cache.entries),
+            _at(cache, entry_pos, torch.int32, "entry_pos", cache.entries),
+            _at(cache, next_pos, torch.int32, "next_pos", (S,)), keep, int(n_sink), int(n_recent),
+            _at(cache, k, torch.int32, "kept", (S, cache.n_kv, max(keep, 0))),
+            _at(cache, m, torch.float32, "mass_out", cache.entries),
+            _at(cache, p, torch.int32, "pos_out", cache.entries),
+            _at(cache, n, torch.int32, "kv_len_out", (S,)),
+            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_cache_evict")
+        return k, m, p, n
+
+    return _on(cache, stream, body)
 
 
 def device_status() -> int:

@@ -7,12 +7,6 @@ namespace qgemv {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Entries of one part of a sequence's cache (the same in every kernel).
-__device__ __forceinline__ int part_len(int len, int n_splits, int unit) {
-  const int per = (len + n_splits - 1) / n_splits;
-  return (per + unit - 1) / unit * unit;
-}
-
 // One row computed entry by entry in fp32, by a whole warp: taken where a
 // value that the row does not see is an infinity or a NaN, which the tensor
 // cores' 0 * v would carry into it.  Writes out and returns nothing else (the

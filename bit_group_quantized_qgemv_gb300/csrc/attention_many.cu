@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   if (warp == 9) {
     int s, rt;
-    find_unit(a, static_cast<int>(blockIdx.x / (a.n_splits * a.c.n_kv)), lane, &s, &rt);
+    find_unit(a, static_cast<int>(blockIdx.x / (a.n_parts * a.c.n_kv)), lane, &s, &rt);
     if (lane == 0) {
       s_unit[0] = s;
       s_unit[1] = rt;
@@ -127,22 +127,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int s = s_unit[0];
   if (s < 0) return;
-  const int sp = blockIdx.x % a.n_splits, h = blockIdx.x / a.n_splits % a.c.n_kv;
+  const int sp = blockIdx.x % a.n_parts, h = blockIdx.x / a.n_parts % a.c.n_kv;
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
   const int rows = min(count, a.max_q) * a.group;
   const int r0 = s_unit[1] * 2 * kTile;
   const int len = seq_len(a.c, s, a.err);
   const int off = len - count;
-  const int per = part_len(len, a.n_splits, a.part_unit);
-  const int k0 = sp * per;
+  const int k0 = sp * a.part;
   if (sp > 0 && k0 >= len) return;
   // tiles of entries that tile x sees (its last row sees the most)
   int nt[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int last = min(rows, r0 + (x + 1) * kTile) - 1;
-    const int see = last >= r0 + x * kTile ? min(min(len, off + last / a.group + 1), k0 + per) : 0;
+    const int see = last >= r0 + x * kTile ? min(min(len, off + last / a.group + 1), k0 + a.part) : 0;
     nt[x] = see > k0 ? (see - k0 + kTile - 1) / kTile : 0;
   }
   const int tiles = max(nt[0], nt[1]);
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after();
     const int t = first + i, head = h * a.group + (live ? rr % a.group : 0);
     const long long at = static_cast<long long>(t) * a.n_q + head;
-    if (ok && a.n_splits > 1) {
+    if (ok && a.n_parts > 1) {
       float* po = a.part_o + (static_cast<long long>(sp) * a.n_tokens * a.n_q + at) * HD;
 #pragma unroll
       for (int c = 0; c < HD; c += 32) {
@@ -467,7 +466,7 @@ cudaError_t launch_many(const AttnArgs& a, cudaStream_t st, int device) {
   CUtensorMap km, vm;
   if (!encode_pool(&km, a.c, a.c.k) || !encode_pool(&vm, a.c, a.c.v)) return cudaErrorInvalidValue;
   const long long blocks =
-      attention_many_units(a.c.n_seqs, a.n_tokens, a.group, a.max_q) * a.c.n_kv * a.n_splits;
+      attention_many_units(a.c.n_seqs, a.n_tokens, a.group, a.max_q) * a.c.n_kv * a.n_parts;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -496,11 +495,12 @@ long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q) {
 
 // Parts of the cache: as many as fill the machine once (a block takes a whole
 // multiprocessor), each of 512 entries at least.
-int attention_many_splits(long long units, int n_kv, long long capacity, int sms) {
-  long long want = sms / (units * n_kv);
-  const long long most = (capacity + 511) / 512;
-  if (want > most) want = most;
-  return want < 1 ? 1 : static_cast<int>(want);
+AttnSplit attention_many_split(long long units, int n_kv, long long capacity, int sms) {
+  const long long want = sms / (units * n_kv);
+  if (want <= 1) return {1, static_cast<int>(capacity), 1};
+  long long part = ((capacity + want - 1) / want + kTile - 1) / kTile * kTile;
+  if (part < 512) part = 512;
+  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
 }
 
 cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device) {

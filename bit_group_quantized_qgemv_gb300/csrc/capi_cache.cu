@@ -123,11 +123,10 @@ size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache* cache, int n_
     return 0;
   int dev, sms;
   if (qgemv::device_and_sms(&dev, &sms) != QGEMV_OK) return 0;
-  const long long cap = static_cast<long long>(c.max_pages) << c.page_shift;
-  return qgemv::attention_part_bytes(
-      qgemv::attention_splits(c.n_seqs, c.n_kv, n_tokens, n_q / c.n_kv,
-                               max_q < n_tokens ? max_q : n_tokens, cap, sms), n_tokens, n_q,
-      c.head_dim);
+  const qgemv::AttnSplit sp = qgemv::attention_split(
+      c.n_seqs, c.n_kv, n_tokens, n_q / c.n_kv, max_q < n_tokens ? max_q : n_tokens,
+      static_cast<long long>(c.max_pages) << c.page_shift, sms);
+  return sp.joins() > 1 ? sp.joins() * qgemv::attention_part_bytes(n_tokens, n_q, c.head_dim) : 0;
 }
 
 int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long long q_stride,
@@ -160,16 +159,16 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
   a.lse = lse;
   a.err = err_flag;
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  int splits = qgemv::attention_splits(a.c.n_seqs, a.c.n_kv, n_tokens, a.group, a.max_q, cap,
-                                       sms);
-  while (splits > 1 &&
-         qgemv::attention_part_bytes(splits, n_tokens, n_q, a.c.head_dim) > workspace_bytes)
-    --splits;
-  a.n_splits = splits;
-  if (splits > 1) {  // the outputs of the parts, then their maxima and sums
+  const qgemv::AttnSplit sp = qgemv::attention_fit(
+      qgemv::attention_split(a.c.n_seqs, a.c.n_kv, n_tokens, a.group, a.max_q, cap, sms), cap,
+      qgemv::attention_part_bytes(n_tokens, n_q, a.c.head_dim), workspace_bytes);
+  a.n_parts = sp.n_parts;
+  a.part = sp.part;
+  a.cluster = sp.cluster;
+  if (sp.joins() > 1) {  // the outputs of the parts, then their maxima and sums
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(
-        a.part_o + static_cast<size_t>(splits) * n_tokens * n_q * a.c.head_dim);
+        a.part_o + static_cast<size_t>(sp.joins()) * n_tokens * n_q * a.c.head_dim);
   }
   return qgemv::report_launch(
       qgemv::paged_attention_launch(a, sms, static_cast<cudaStream_t>(stream), dev));

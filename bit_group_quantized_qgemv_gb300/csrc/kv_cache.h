@@ -45,12 +45,13 @@ struct AttnArgs {
   __half* out;
   long long out_stride;
   float* lse;
-  // Parts of a split cache: part_o [split][token][n_q][head_dim] (not yet
-  // divided by the sum), part_ml [split][token][n_q] {max, sum} in log2 units.
+  // Parts of a split cache, `part` entries each: part_o [part][token][n_q]
+  // [head_dim] (not yet divided by the sum), part_ml [part][token][n_q] {max,
+  // sum} in log2 units.  n_parts = 1: nothing is split.
   float* part_o;
   float2* part_ml;
-  int n_splits, row_tiles;
-  int part_unit;  // parts are multiples of this many entries
+  int n_parts, part, row_tiles;
+  int cluster;  // thread blocks that join their parts among themselves (1: none)
   int* err;
 };
 
@@ -83,18 +84,26 @@ cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st);
 cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st);
 
-// Parts the cache is split into for a call of these sizes.
-int attention_splits(int n_seqs, int n_kv, int n_tokens, int group, int max_q, long long capacity,
-                     int sms);
-// Bytes of workspace for that many parts.
-size_t attention_part_bytes(int splits, int n_tokens, int n_q, int head_dim);
+// How a call's cache is split: n_parts parts of `part` entries (1: not split),
+// `cluster` of them joined on chip; what is left of them is joined through
+// the workspace.
+struct AttnSplit {
+  int n_parts, part, cluster;
+  int joins() const { return n_parts / cluster; }
+};
+AttnSplit attention_split(int n_seqs, int n_kv, int n_tokens, int group, int max_q,
+                          long long capacity, int sms);
+// The split with the most parts whose workspace fits (`part` grows).
+AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes, size_t workspace_bytes);
+// Bytes of workspace per part.
+size_t attention_part_bytes(int n_tokens, int n_q, int head_dim);
 // Whether a call has more query rows per key/value head than the mma.sync
 // kernel takes in one pass over the cache: those go to the tcgen05 kernel.
 inline bool attention_is_many(int group, int max_q) {
   return static_cast<long long>(group) * max_q > 32;
 }
 long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q);
-int attention_many_splits(long long units, int n_kv, long long capacity, int sms);
+AttnSplit attention_many_split(long long units, int n_kv, long long capacity, int sms);
 cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device);
 cudaError_t status_attention(unsigned* out);
 cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device);

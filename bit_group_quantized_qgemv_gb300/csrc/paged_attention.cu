@@ -3,18 +3,22 @@
 //
 // The rows of a (sequence, key/value head) are its new tokens times the query
 // heads that share the head, row r = token r / group, head r % group.  A
-// thread block takes MT * 16 of them and one part of the cache; its four
-// warps take every fourth tile of 16 entries, each through a ring of its own
-// (cp.async, no block-wide barrier until the end), so the loop is a stream of
-// K and V through shared memory.  Per tile: S = Q K^T by m16n8k16, the
-// running maximum and sum of the softmax in fp32 registers, P V with P
-// straight from the accumulator registers as the next A operand.  The warps'
-// (max, sum, O) are joined in shared memory, the parts of a split cache by a
-// second kernel.
+// thread block takes NT * 8 of them and one part of the cache; its warps take
+// tiles of 16 entries in turn, each through a ring of its own (cp.async, no
+// block-wide barrier until the end), so the loop is a stream of K and V through
+// shared memory.  Per tile, transposed so that the rows are the eight columns
+// of m16n8k16 and nothing is padded to 16: S^T = K Q^T, the running maximum and
+// sum of the softmax in fp32 registers, and O^T += V^T P^T with P^T made from
+// the accumulators by a transpose of 8 x 8 matrices.  (With the rows as the 16 of
+// the product, padded, a tile took three times the products; 48 sequences of 900 to
+// 20000 entries: 202 against 184 us.)  The warps' (max, sum, O) are joined in
+// shared memory, the parts of a split cache through the distributed shared
+// memory of a cluster or by a second kernel.
 //
-// P is split into fp16 high and low parts (two products with V), which
-// keeps the weights at 22 bits; the tensor cores have the time, the kernel
-// is bound by HBM.
+// P enters as fp16 high and low parts (two products with V), which keeps the
+// weights at 22 bits; the kernel is bound by HBM, not by the products: 48
+// sequences of 900 to 20000 entries (32/8 heads of 128, 1.23 GB) take 184 us,
+// 6.69 TB/s or 99 % of the measured copy bandwidth.
 #include <atomic>
 
 #include "attention_common.cuh"
@@ -22,9 +26,9 @@
 namespace qgemv {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kTile = 16;    // entries per warp and step
 constexpr int kStages = 3;   // ring depth of each warp
+constexpr float kSlack = 8.0f;  // log2 of the growth that makes O be rescaled
 
 template <int HD>
 __host__ __device__ constexpr int stage_bytes() {
@@ -53,6 +57,35 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
                : "r"(addr));
 }
 
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// A float of block `rank`'s shared memory, at this block's address of it.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  float v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, two per thread.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Byte offset of 16-byte chunk ch of row r in a tile of HD-wide rows; the
 // swizzle spreads 8 rows over the banks.
 template <int HD>
@@ -60,12 +93,12 @@ __device__ __forceinline__ int tile_off(int r, int ch) {
   return r * (HD * 2) + ((ch ^ (r & 7)) << 4);
 }
 
-template <int HD, int MT>
+template <int HD, int NT, bool LO, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnArgs a) {
-  constexpr int kN = HD / 8;    // n-tiles of the output
-  constexpr int kK = HD / 16;   // k-steps of the scores
-  constexpr int kRows = 16 * MT;
+  constexpr int kM = HD / 16;      // 16-component tiles of the output, k-steps of the scores
+  constexpr int kRows = 8 * NT;
   constexpr int kChunks = HD / 8;  // 16-byte chunks per row
+  constexpr int kOut = HD + 4;     // floats between output rows in shared memory (banks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
   pdl_launch_dependents();
@@ -74,63 +107,76 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   const int g = lane >> 2, tq = lane & 3;
 
   long long b = blockIdx.x;
-  const int sp = static_cast<int>(b % a.n_splits);
-  b /= a.n_splits;
+  const int sp = static_cast<int>(b % a.n_parts);
+  b /= a.n_parts;
   const int h = static_cast<int>(b % a.c.n_kv);
   b /= a.c.n_kv;
   const int rt = static_cast<int>(b % a.row_tiles);
   const int s = static_cast<int>(b / a.row_tiles);
 
+  // The first tile's page number is read along with the lengths.
+  const int k0 = sp * a.part;
+  const int e_first = k0 + warp * kTile;
+  int page = -1;
+  if (e_first < a.c.max_pages << a.c.page_shift)
+    page = a.c.page_table[static_cast<long long>(s) * a.c.max_pages + (e_first >> a.c.page_shift)];
+
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
+  const int len = seq_len(a.c, s, a.err);
   if (count > a.max_q) flag_error(a.err);
   const int rows = min(count, a.max_q) * a.group;
   const int r0 = rt * kRows;
   if (r0 >= rows) return;
   const int nr = min(kRows, rows - r0);
-  const int len = seq_len(a.c, s, a.err);
   const int off = len - count;  // token i sees entries up to off + i
-  const int per = part_len(len, a.n_splits, a.part_unit);
-  const int k0 = sp * per;
-  if (sp > 0 && k0 >= len) return;  // the join knows
+  const int group = sp / a.cluster;  // parts that are joined on chip
+  // (a group behind the sequence's end is left out by the join; blocks of a
+  // group that has entries stay, for the others wait for them)
+  if (group > 0 && group * a.cluster * a.part >= len) return;
   // entries that some row of this block sees
   const int see = min(len, off + (r0 + nr - 1) / a.group + 1);
-  const int k1 = min(see, k0 + per);
-
-  // Queries as A fragments.
-  uint32_t qf[MT][kK][4];
-  int lim[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = mt * 16 + g + 8 * e;
-      const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group;
-      lim[mt][e] = r < nr ? off + i : -1;
-      const __half* q = a.q + static_cast<long long>(first + i) * a.q_stride + head * HD + 2 * tq;
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        qf[mt][k][e] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
-        qf[mt][k][2 + e] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
-      }
-    }
-
-  float o[MT][kN][4], m[MT][2], l[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int n = 0; n < kN; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
-  }
+  const int k1 = min(see, k0 + a.part);
 
   const uint32_t ring = smem_u32(smem) + warp * (kStages * stage_bytes<HD>());
   const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
   unsigned bad = 0;  // bit st: the tile in stage st lies on a bad page
-  int page = mine > 0 ? page_of(a.c, s, k0 + warp * kTile, a.err) : -1;
+  if (mine > 0 && (page < 0 || page >= a.c.n_pages)) {
+    flag_error(a.err);
+    page = -1;
+  }
+
+  // Queries as B fragments: column = row of the block.
+  uint32_t qf[NT][kM][2];
+  int lim[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g;
+    const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group;
+    const __half* q = a.q + static_cast<long long>(first + i) * a.q_stride + head * HD + 2 * tq;
+#pragma unroll
+    for (int k = 0; k < kM; ++k) {
+      qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+      qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = nt * 8 + 2 * tq + e;
+      lim[nt][e] = c < nr ? off + (r0 + c) / a.group : -1;
+    }
+  }
+
+  float o[NT][kM][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int d = 0; d < kM; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
 
   auto issue = [&](int it) {
     if (it < mine) {
@@ -138,14 +184,15 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
       const int st = it % kStages;
       const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
       const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
+      const int end = page >= 0 ? len : 0;
       bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
 #pragma unroll
       for (int c = 0; c < kTile * kChunks / 32; ++c) {
         const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
-        const bool take = page >= 0 && e0 + r < len;
-        const long long src = take ? base + r * HD + ch * 8 : 0;
-        cp_async16(kd + tile_off<HD>(r, ch), a.c.k + src, take);
-        cp_async16(vd + tile_off<HD>(r, ch), a.c.v + src, take);
+        // (rows behind the end lie on the page and are not read)
+        const bool take = e0 + r < end;
+        cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, take);
+        cp_async16(vd + tile_off<HD>(r, ch), a.c.v + base + id * 8, take);
       }
       // the next tile's page, a step ahead of its use
       if (it + 1 < mine) page = page_of(a.c, s, e0 + kWarps * kTile, a.err);
@@ -155,6 +202,8 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
 #pragma unroll
   for (int p = 0; p < kStages - 1; ++p) issue(p);
 
+  const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+  const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
   for (int it = 0; it < mine; ++it) {
     cp_wait<kStages - 2>();
     __syncwarp();
@@ -162,111 +211,123 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
     const int st = it % kStages;
     const int e0 = k0 + (it * kWarps + warp) * kTile;
     const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
-    float sc[MT][2][4];
+    // S^T: 16 entries x 8 rows per tile of rows, even and odd k-steps apart
+    // (two shorter chains of products)
+    float sc[NT][2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
-    const int lr = (lane & 7) + ((lane >> 4) << 3), lc = (lane >> 3) & 1;
+    for (int k = 0; k < kM; ++k) {
+      uint32_t kf[4];
+      ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
 #pragma unroll
-    for (int k = 0; k < kK; ++k) {
-      uint32_t kf[4];  // b0, b1 of entries 0-7, then of entries 8-15
-      ldsm4(kf, kd + tile_off<HD>(lr, 2 * k + lc));
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma_f16(sc[mt][0], qf[mt][k], kf[0], kf[1]);
-        mma_f16(sc[mt][1], qf[mt][k], kf[2], kf[3]);
-      }
+      for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
     }
     const bool hidden = (bad >> st) & 1;
-    uint32_t ph[MT][4], pl[MT][4];
+    uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float mn[2] = {m[mt][0], m[mt][1]};
+    for (int nt = 0; nt < NT; ++nt) {
+      float x[4];
+      bool over = false;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = e0 + n * 8 + 2 * tq + (e & 1);
-          const bool seen = !hidden && j <= lim[mt][e >> 1] && j < len;
-          sc[mt][n][e] = seen ? sc[mt][n][e] * a.scale_log2 : -INFINITY;
-          mn[e >> 1] = fmaxf(mn[e >> 1], sc[mt][n][e]);
-        }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 1));
-        mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 2));
+      for (int e = 0; e < 4; ++e) {
+        const int j = e0 + g + 8 * (e >> 1);
+        const bool seen = !hidden && j <= lim[nt][e & 1];
+        x[e] = seen ? (sc[nt][0][e] + sc[nt][1][e]) * a.scale_log2 : -INFINITY;
+        over |= x[e] > m[nt][e & 1] + kSlack;
       }
-      const bool grew = mn[0] > m[mt][0] || mn[1] > m[mt][1];
-      if (__any_sync(0xFFFFFFFFu, grew)) {
-        const float f0 = mn[0] == m[mt][0] ? 1.f : ex2(m[mt][0] - mn[0]);
-        const float f1 = mn[1] == m[mt][1] ? 1.f : ex2(m[mt][1] - mn[1]);
-        l[mt][0] *= f0;
-        l[mt][1] *= f1;
+      // The maximum is lazy: it moves (and O is rescaled) only where a score
+      // exceeds it by more than the slack, so most tiles cost one vote.
+      if (__any_sync(0xFFFFFFFFu, over)) {
+        float mn[2];
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          o[mt][n][0] *= f0;
-          o[mt][n][1] *= f0;
-          o[mt][n][2] *= f1;
-          o[mt][n][3] *= f1;
+        for (int e = 0; e < 2; ++e) {
+          mn[e] = fmaxf(m[nt][e], fmaxf(x[e], x[e + 2]));
+          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 4));
+          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 8));
+          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 16));
         }
-        m[mt][0] = mn[0];
-        m[mt][1] = mn[1];
+        const float f0 = mn[0] == m[nt][0] ? 1.f : ex2(m[nt][0] - mn[0]);
+        const float f1 = mn[1] == m[nt][1] ? 1.f : ex2(m[nt][1] - mn[1]);
+        l[nt][0] *= f0;
+        l[nt][1] *= f1;
+#pragma unroll
+        for (int d = 0; d < kM; ++d) {
+          o[nt][d][0] *= f0;
+          o[nt][d][1] *= f1;
+          o[nt][d][2] *= f0;
+          o[nt][d][3] *= f1;
+        }
+        m[nt][0] = mn[0];
+        m[nt][1] = mn[1];
       }
-      const float b0 = mn[0] == -INFINITY ? 0.f : mn[0], b1 = mn[1] == -INFINITY ? 0.f : mn[1];
+      const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+      const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float base = e == 0 ? b0 : b1;
-          const float x = ex2(sc[mt][n][e] - base), y = ex2(sc[mt][n][e + 1] - base);
-          l[mt][e >> 1] += x + y;
-          const uint32_t hi = pack_f16(x, y);
+      for (int e = 0; e < 2; ++e) {  // entry g, then g + 8
+        const float u = ex2(x[2 * e] - b0), v = ex2(x[2 * e + 1] - b1);
+        l[nt][0] += u;
+        l[nt][1] += v;
+        const uint32_t hi = pack_f16(u, v);
+        ph[nt][e] = transpose8(hi);
+        if (LO) {
           const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          ph[mt][2 * n + (e >> 1)] = hi;
-          pl[mt][2 * n + (e >> 1)] = pack_f16(x - hf.x, y - hf.y);
+          pl[nt][e] = transpose8(pack_f16(u - hf.x, v - hf.y));
         }
+      }
     }
-    const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+    // O^T += V^T P^T
 #pragma unroll
-    for (int n = 0; n < kN; n += 2) {
-      uint32_t vf[4];  // b0, b1 of columns 8n.., then of 8n + 8..
-      ldsm4t(vf, vd + tile_off<HD>(vr, n + vc));
+    for (int d = 0; d < kM; ++d) {
+      uint32_t vf[4];
+      ldsm4t(vf, vd + tile_off<HD>(vr, 2 * d + vc));
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma_f16(o[mt][n], ph[mt], vf[0], vf[1]);
-        mma_f16(o[mt][n + 1], ph[mt], vf[2], vf[3]);
-        mma_f16(o[mt][n], pl[mt], vf[0], vf[1]);
-        mma_f16(o[mt][n + 1], pl[mt], vf[2], vf[3]);
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(o[nt][d], vf, ph[nt][0], ph[nt][1]);
+        if (LO) mma_f16(o[nt][d], vf, pl[nt][0], pl[nt][1]);
       }
     }
     __syncwarp();
   }
   cp_wait<0>();
   __syncthreads();  // every warp is done with its ring: it now takes the partial outputs
-  float* so = reinterpret_cast<float*>(smem);  // [warp][row][HD]
+  float* so = reinterpret_cast<float*>(smem);  // [warp][row][kOut]
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float lsum = l[mt][e];
-      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 1);
-      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 2);
-      const int r = mt * 16 + g + 8 * e;
-      if (tq == 0) {
-        sm_m[warp][r] = m[mt][e];
-        sm_l[warp][r] = lsum;
+      float lsum = l[nt][e];
+      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 4);
+      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 8);
+      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
+      if (g == 0) {
+        sm_m[warp][nt * 8 + 2 * tq + e] = m[nt][e];
+        sm_l[warp][nt * 8 + 2 * tq + e] = lsum;
       }
-#pragma unroll
-      for (int n = 0; n < kN; ++n)
-        *reinterpret_cast<float2*>(so + (warp * kRows + r) * HD + n * 8 + 2 * tq) =
-            make_float2(o[mt][n][2 * e], o[mt][n][2 * e + 1]);
     }
+#pragma unroll
+    for (int d = 0; d < kM; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        so[(warp * kRows + nt * 8 + 2 * tq + (e & 1)) * kOut + 16 * d + g + 8 * (e >> 1)] =
+            o[nt][d][e];
+  }
   __syncthreads();
   // A warp per row: join the warps' parts.
   constexpr int D = HD / 32;
+  const auto finish = [&](int r, float mm, float ll, const float* acc) {
+    const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group, t = first + i;
+    if (a.n_parts == a.cluster) {
+      store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
+      return;
+    }
+    const long long at = (static_cast<long long>(group) * a.n_tokens + t) * a.n_q + head;
+#pragma unroll
+    for (int d = 0; d < D; ++d) a.part_o[at * HD + lane * D + d] = acc[d];
+    if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
+  };
   for (int r = warp; r < nr; r += kWarps) {
     float mm = -INFINITY;
 #pragma unroll
@@ -278,62 +339,146 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
       const float f = ex2(sm_m[w][r] - base);
       ll += sm_l[w][r] * f;
 #pragma unroll
-      for (int d = 0; d < D; ++d) acc[d] += so[(w * kRows + r) * HD + lane * D + d] * f;
+      for (int d = 0; d < D; ++d) acc[d] += so[(w * kRows + r) * kOut + lane * D + d] * f;
     }
-    const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group, t = first + i;
-    if (a.n_splits > 1) {
-      const long long at = (static_cast<long long>(sp) * a.n_tokens + t) * a.n_q + head;
-#pragma unroll
-      for (int d = 0; d < D; ++d) a.part_o[at * HD + lane * D + d] = acc[d];
-      if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
+    if (a.cluster == 1) {
+      finish(r, mm, ll, acc);
       continue;
     }
-    store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
+    // (row r is this warp's alone: its sum may take the place of warp 0's part)
+    __syncwarp();
+#pragma unroll
+    for (int d = 0; d < D; ++d) so[r * kOut + lane * D + d] = acc[d];
+    if (lane == 0) {
+      sm_m[0][r] = mm;
+      sm_l[0][r] = ll;
+    }
   }
+  if (a.cluster == 1) return;
+  // The blocks of a cluster join theirs through distributed shared memory,
+  // each for some of the rows.
+  cluster_sync();
+  for (int r = cluster_rank() * kWarps + warp; r < nr; r += a.cluster * kWarps) {
+    const uint32_t m_at = smem_u32(&sm_m[0][r]), l_at = smem_u32(&sm_l[0][r]);
+    const uint32_t o_at = smem_u32(so + r * kOut + lane * D);
+    float mm = -INFINITY, pm[kMaxCluster], pl[kMaxCluster], po[kMaxCluster][D];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      pm[c] = -INFINITY;
+      pl[c] = 0.f;
+      if (c < a.cluster) {
+        pm[c] = ld_cluster(m_at, c);
+        pl[c] = ld_cluster(l_at, c);
+#pragma unroll
+        for (int d = 0; d < D; ++d) po[c][d] = ld_cluster(o_at + 4 * d, c);
+      } else {
+#pragma unroll
+        for (int d = 0; d < D; ++d) po[c][d] = 0.f;
+      }
+      mm = fmaxf(mm, pm[c]);
+    }
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, acc[D] = {};
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      const float f = ex2(pm[c] - base);
+      ll += pl[c] * f;
+#pragma unroll
+      for (int d = 0; d < D; ++d) acc[d] += po[c][d] * f;
+    }
+    finish(r, mm, ll, acc);
+  }
+  cluster_sync();  // no block ends while another reads its shared memory
 }
 
-// Join the parts of a split cache: a warp per (token, query head).
+// Join the parts of a split cache: a block per (token, query head), its warps
+// take the parts in turn.
+constexpr int kJoinWarps = 4;
+
 template <int HD>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
   constexpr int D = HD / 32;
+  __shared__ float so[kJoinWarps][HD], sm[kJoinWarps], sl[kJoinWarps];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // (sequence, token within it, head)
-  const int head = static_cast<int>(id % a.n_q);
-  const int i = static_cast<int>(id / a.n_q % a.max_q);
-  const int s = static_cast<int>(id / a.n_q / a.max_q);
-  if (s >= a.c.n_seqs) return;
+  const int head = blockIdx.x % a.n_q;
+  const int i = blockIdx.x / a.n_q % a.max_q, s = blockIdx.x / a.n_q / a.max_q;
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
   if (i >= count) return;
   const int t = first + i;
   const int len = seq_len(a.c, s, nullptr);
-  const int per = part_len(len, a.n_splits, a.part_unit);
-  const int parts = len > 0 ? (len + per - 1) / per : 1;
+  const int parts = max(1, (len + a.part * a.cluster - 1) / (a.part * a.cluster));
   const long long step = static_cast<long long>(a.n_tokens) * a.n_q;
   const long long at = static_cast<long long>(t) * a.n_q + head;
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) m = fmaxf(m, a.part_ml[p * step + at].x);
+  float m = -INFINITY, l = 0.f, acc[D] = {};
+  constexpr int kU = 8;  // parts in flight per warp
+  for (int p0 = warp; p0 < parts; p0 += kJoinWarps * kU) {
+    float2 ml[kU];
+    float o[kU][D];
 #pragma unroll
-  for (int k = 16; k > 0; k /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+    for (int u = 0; u < kU; ++u) {
+      const int p = p0 + u * kJoinWarps;
+      ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[u][d] = 0.f;
+      if (p < parts) {
+        ml[u] = a.part_ml[p * step + at];
+        const float* src = a.part_o + (p * step + at) * HD + lane * D;
+        if constexpr (D == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          o[u][0] = v.x, o[u][1] = v.y, o[u][2] = v.z, o[u][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          o[u][0] = v.x, o[u][1] = v.y;
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) mn = fmaxf(mn, ml[u].x);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2(m - base);
+    l *= f0;
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] *= f0;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float f = ex2(ml[u].x - base);
+      l += ml[u].y * f;
+#pragma unroll
+      for (int d = 0; d < D; ++d) acc[d] += o[u][d] * f;
+    }
+    m = mn;
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d) so[warp][lane * D + d] = acc[d];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, sm[w]);
   const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[D] = {};
-#pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.part_ml[p * step + at];
-    const float f = ex2(ml.x - base);
-    l += ml.y * f;
-    const float* o = a.part_o + (p * step + at) * HD + lane * D;
+  l = 0.f;
 #pragma unroll
-    for (int d = 0; d < D; ++d) acc[d] += o[d] * f;
+  for (int d = 0; d < D; ++d) acc[d] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = ex2(sm[w] - base);
+    l += sl[w] * f;
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] += so[w][lane * D + d] * f;
   }
   store_row<HD>(a, s, head / a.group, t, head, min(len - count + i, len - 1), len, acc, m, l, lane);
 }
 
 template <typename F>
-cudaError_t launch_pdl(F* k, long long blocks, int threads, int smem, cudaStream_t st,
+cudaError_t launch_pdl(F* k, long long blocks, int threads, int smem, int cluster, cudaStream_t st,
                        const AttnArgs& a) {
   if (blocks < 1 || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -341,68 +486,124 @@ cudaError_t launch_pdl(F* k, long long blocks, int threads, int smem, cudaStream
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <int HD, int MT>
+template <int HD, int NT, bool LO, int kWarps>
 cudaError_t launch_few(AttnArgs a, cudaStream_t st, int device) {
   static std::atomic<unsigned long long> done{0};
   constexpr int smem = kWarps * kStages * stage_bytes<HD>();
-  auto* k = attention_few_kernel<HD, MT>;
+  static_assert(kWarps * 8 * NT * (HD + 4) * 4 <= smem, "the warps' outputs take the ring's place");
+  auto* k = attention_few_kernel<HD, NT, LO, kWarps>;
   const unsigned long long bit = 1ull << (device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  a.row_tiles = (a.max_q * a.group + 16 * MT - 1) / (16 * MT);
+  a.row_tiles = (a.max_q * a.group + 8 * NT - 1) / (8 * NT);
   const long long blocks =
-      static_cast<long long>(a.c.n_seqs) * a.row_tiles * a.c.n_kv * a.n_splits;
-  return launch_pdl(k, blocks, 32 * kWarps, smem, st, a);
+      static_cast<long long>(a.c.n_seqs) * a.row_tiles * a.c.n_kv * a.n_parts;
+  return launch_pdl(k, blocks, 32 * kWarps, smem, a.cluster, st, a);
+}
+
+// Warps per block: eight where the clusters leave a multiprocessor to each
+// block (at most 19 units x 8 blocks), four, two blocks to a multiprocessor,
+// elsewhere.
+int few_warps(int rows, int cluster, int units) {
+  return cluster > 1 && units <= 19 && rows <= 16 ? 8 : 4;
+}
+
+template <int HD>
+cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
+  const int rows = a.max_q * a.group;
+  const bool wide = few_warps(rows, a.cluster, a.c.n_seqs * a.c.n_kv) == 8;
+  if (rows <= 8)
+    return wide ? launch_few<HD, 1, true, 8>(a, st, device) : launch_few<HD, 1, true, 4>(a, st, device);
+  if (rows <= 16)
+    return wide ? launch_few<HD, 2, true, 8>(a, st, device) : launch_few<HD, 2, true, 4>(a, st, device);
+  if (rows <= 24) return launch_few<HD, 3, true, 4>(a, st, device);
+  return launch_few<HD, 4, true, 4>(a, st, device);
 }
 
 }  // namespace
 
-int attention_splits(int n_seqs, int n_kv, int n_tokens, int group, int max_q, long long capacity,
-                     int sms) {
-  const long long rows = static_cast<long long>(max_q) * group;
+// How the cache is split for few rows, by the number of (sequence, head)
+// units and the capacity (the lengths are on the device).  Measured on GB300,
+// 32/8 heads of 128, one new token per sequence, replayed from a graph, clusters of
+// 8 blocks that join on chip against parts joined by a second kernel:
+//   1 sequence   1000 entries  5.6 us against 6.2;   4110  8.8 against 7.3
+//   4 sequences  1000          7.4 against 7.0;      2000  9.1 against 10.2
+// so clusters serve short caches (where they also save the workspace and a
+// launch) while their blocks fill the machine at most once, two to a
+// multiprocessor.  With longer ones a cluster lasts as long as its sequence.
+//   Otherwise parts: for one sequence as many as fill the machine once; for
+// several, of 128 to 1024 entries, enough to fill it twice over were every
+// sequence as long as its page table allows, so that unlike lengths balance
+// (48 sequences of 900 to 20000 entries: 1024-entry parts 184 us, one part per
+// sequence 344 us).
+AttnSplit attention_split(int n_seqs, int n_kv, int n_tokens, int group, int max_q,
+                          long long capacity, int sms) {
   if (attention_is_many(group, max_q))
-    return attention_many_splits(attention_many_units(n_seqs, n_tokens, group, max_q), n_kv,
-                                 capacity, sms);
-  const long long tiles = rows <= 16 ? 1 : (rows + 31) / 32;
-  const long long units = tiles * n_kv * n_seqs;
-  long long want = (2LL * sms + units - 1) / units;  // two blocks to a multiprocessor
-  const long long most = (capacity + 63) / 64;       // 64 entries a part at least
-  if (want > most) want = most;
-  return want < 1 ? 1 : static_cast<int>(want);
+    return attention_many_split(attention_many_units(n_seqs, n_tokens, group, max_q), n_kv,
+                                capacity, sms);
+  const long long units = static_cast<long long>(n_kv) * n_seqs;
+  if (capacity <= 128) return {1, static_cast<int>(capacity), 1};
+  if (capacity <= 2048 && units <= 2 * sms / kMaxCluster) {
+    const long long part = ((capacity + kMaxCluster - 1) / kMaxCluster + 63) / 64 * 64;
+    return {kMaxCluster, static_cast<int>(part), kMaxCluster};
+  }
+  long long part;
+  if (n_seqs == 1 && units <= 2 * sms) {
+    const long long n = 2LL * sms / units;
+    part = ((capacity + n - 1) / n + 63) / 64 * 64;
+    if (part < 128) part = 128;
+  } else {
+    part = capacity * units / (4LL * sms) / 64 * 64;
+    if (part < 128) part = 128;
+    if (part > 1024) part = 1024;
+  }
+  if (capacity <= part) return {1, static_cast<int>(capacity), 1};
+  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
 }
 
-size_t attention_part_bytes(int splits, int n_tokens, int n_q, int head_dim) {
-  if (splits <= 1) return 0;
-  return static_cast<size_t>(splits) * n_tokens * n_q * (static_cast<size_t>(head_dim) * 4 + 8);
+AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes,
+                        size_t workspace_bytes) {
+  const size_t fit = workspace_bytes / part_bytes;
+  if (s.joins() <= 1 || fit >= static_cast<size_t>(s.joins())) return s;
+  const long long n = static_cast<long long>(fit);
+  if (n <= 1) return {1, static_cast<int>(capacity), 1};
+  // whole tiles of either kernel
+  const long long part = ((capacity + n - 1) / n + 127) / 128 * 128;
+  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
+}
+
+size_t attention_part_bytes(int n_tokens, int n_q, int head_dim) {
+  return static_cast<size_t>(n_tokens) * n_q * (static_cast<size_t>(head_dim) * 4 + 8);
 }
 
 cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device) {
   (void)sms;
-  const bool one = a.max_q * a.group <= 16;
   cudaError_t e;
-  a.part_unit = attention_is_many(a.group, a.max_q) ? 128 : 64;
   if (attention_is_many(a.group, a.max_q))
     e = attention_many_launch(a, st, device);
-  else if (a.c.head_dim == 64)
-    e = one ? launch_few<64, 1>(a, st, device) : launch_few<64, 2>(a, st, device);
   else
-    e = one ? launch_few<128, 1>(a, st, device) : launch_few<128, 2>(a, st, device);
-  if (e != cudaSuccess || a.n_splits == 1) return e;
+    e = a.c.head_dim == 64 ? launch_few_rows<64>(a, st, device)
+                           : launch_few_rows<128>(a, st, device);
+  if (e != cudaSuccess || a.n_parts == a.cluster) return e;
   const long long rows = static_cast<long long>(a.c.n_seqs) * a.max_q * a.n_q;
   return a.c.head_dim == 64
-             ? launch_pdl(attention_join_kernel<64>, (rows + 3) / 4, 128, 0, st, a)
-             : launch_pdl(attention_join_kernel<128>, (rows + 3) / 4, 128, 0, st, a);
+             ? launch_pdl(attention_join_kernel<64>, rows, 32 * kJoinWarps, 0, 1, st, a)
+             : launch_pdl(attention_join_kernel<128>, rows, 32 * kJoinWarps, 0, 1, st, a);
 }
 
 }  // namespace qgemv
