@@ -2,141 +2,469 @@
 // cached entry receives from the new tokens.
 //
 //   mass_out[j] = mass[j] + sum_r exp2(scale_log2 q_r . k_j - lse2_r)
-// over the rows r = (token, head of the group) that see entry j; lse is known,
-// so no softmax statistics are left to carry and every entry is summed on its
-// own: a warp keeps 16 entries' keys as A fragments (m16n8k16) and walks the
-// rows, eight columns at a time, from shared memory.  The order of the k index
-// inside a product is free: thread t of a quad takes the eight components 8t..
-// of every 32, one 16-byte load for keys and queries alike.
-#include "kv_cache.cuh"
+// over the rows r = (token, head of the group) that see entry j.  lse is known,
+// so no softmax statistics are carried, every entry is summed on its own in
+// the order of the rows, and nothing has to be joined: only K is read.
+//
+// Few rows (decode steps): the keys stream through shared memory in tiles of
+// 16 entries, a ring per warp (cp.async), S^T = K Q^T by m16n8k16 with the rows
+// as columns.  Bound by HBM.
+// Many rows (chunks): a block keeps 256 entries' keys in shared memory as the
+// A operands of tcgen05 products and walks the query rows 128 at a time, one
+// TMA box each; thread e of a softmax warpgroup owns entry e: its row of
+// scores lies in its lane of tensor memory, so the sum over the rows is a sum
+// over columns in one thread.  Scores are double-buffered (4 x 128 columns).
+// 256 entries a block halve the query traffic, which 128 would put at the
+// multiprocessor's share of the L2 bandwidth (32 KB per 512 clocks of products).
+#include <atomic>
+
+#include "kv_tensor_map.h"
+#include "mma_tile.cuh"
+#include "tcgen05.cuh"
 
 namespace qgemv {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRowTile = 64;  // query rows staged at a time
+__device__ unsigned g_status = 0;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Shared-memory stride of a query row, in bytes: 64 more than the row, so
-// that the 8 rows x 4 chunks of a load phase fall on different banks.
-template <int HD>
-__host__ __device__ constexpr int row_stride() {
-  return HD * 2 + 64;
-}
+// ------------------------------------------------------------- few rows
+constexpr int kWarps = 4;
+constexpr int kTile = 16;
+constexpr int kStages = 4;
+constexpr int kRowsMax = 32;  // rows of one walk over the entries
 
 template <int HD>
-__global__ void __launch_bounds__(32 * kWarps) attention_mass_kernel(const MassArgs a,
-                                                                     int key_tiles) {
-  constexpr int kP = HD / 32;
-  __shared__ __align__(16) uint8_t qs[kRowTile * row_stride<HD>()];
-  __shared__ float ls[kRowTile];
-  __shared__ int lim[kRowTile];
+__host__ __device__ constexpr int key_bytes() {
+  return kTile * HD * 2;
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(32 * kWarps) mass_few_kernel(const MassArgs a, int part,
+                                                               int parts) {
+  constexpr int kM = HD / 16, kChunks = HD / 8, kRows = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   long long b = blockIdx.x;
-  const int kt = static_cast<int>(b % key_tiles);
-  b /= key_tiles;
-  const int h = static_cast<int>(b % a.c.n_kv);
-  const int s = static_cast<int>(b / a.c.n_kv);
+  const int k0 = static_cast<int>(b % parts) * part;
+  b /= parts;
+  const int h = static_cast<int>(b % a.c.n_kv), s = static_cast<int>(b / a.c.n_kv);
   const int len = seq_len(a.c, s, a.err);
-  if (kt * 16 * kWarps >= len) return;
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
   if (count > a.max_q) flag_error(a.err);
+  if (k0 >= len) return;
+  const int k1 = min(len, k0 + part);
   const int rows = min(count, a.max_q) * a.group, off = len - count;
-  const int e0 = (kt * kWarps + warp) * 16;  // this warp's entries
-  const int page = e0 < len ? page_of(a.c, s, e0, a.err) : -1;
+  const int tiles = (k1 - k0 + kTile - 1) / kTile;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * key_bytes<HD>());
+  const long long entries = (static_cast<long long>(s) * a.c.n_kv + h) *
+                            (static_cast<long long>(a.c.max_pages) << a.c.page_shift);
 
-  uint4 kf[kP][2];
+  int r0 = 0;
+  do {  // one walk over the entries for every kRows rows (and one if there are none)
+    const int nr = min(kRows, rows - r0);
+    uint32_t qf[NT][kM][2];
+    float ls[NT][2];
+    int lim[NT][2];
 #pragma unroll
-  for (int p = 0; p < kP; ++p)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      const __half* q = a.q + static_cast<long long>(first + (r0 + r) / a.group) * a.q_stride +
+                        (h * a.group + (r0 + r) % a.group) * HD + 2 * tq;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int j = e0 + g + 8 * e;
-      kf[p][e] = page >= 0 && j < len
-                     ? *reinterpret_cast<const uint4*>(a.c.k + cache_row(a.c, page, h, j) * HD +
-                                                       32 * p + 8 * tq)
-                     : make_uint4(0u, 0u, 0u, 0u);
-    }
-  float sum[2] = {0.f, 0.f};
-  // rows whose last entry lies before this block's first see none of it
-  const int r_first = max(0, (kt * kWarps * 16 - off) * a.group) / kRowTile * kRowTile;
-  for (int rb = r_first; rb < rows; rb += kRowTile) {
-    __syncthreads();
-    for (int c = threadIdx.x; c < kRowTile * (HD / 8); c += 32 * kWarps) {
-      const int r = c / (HD / 8), ch = c % (HD / 8), rr = rb + r;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < rows)
-        v = *reinterpret_cast<const uint4*>(a.q + static_cast<long long>(first + rr / a.group) * a.q_stride +
-                                            (h * a.group + rr % a.group) * HD + ch * 8);
-      *reinterpret_cast<uint4*>(qs + r * row_stride<HD>() + ch * 16) = v;
-    }
-    for (int r = threadIdx.x; r < kRowTile; r += 32 * kWarps) {
-      const int rr = rb + r;
-      float v = -INFINITY;
-      if (rr < rows)
-        v = a.lse[static_cast<long long>(first + rr / a.group) * a.n_q + h * a.group + rr % a.group];
-      // a row that saw nothing takes no part
-      lim[r] = rr < rows && v != -INFINITY ? off + rr / a.group : -1;
-      ls[r] = v * kLog2e;
-    }
-    __syncthreads();
-    if (page < 0) continue;
-    for (int n = 0; n < kRowTile && rb + n < rows; n += 8) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int p = 0; p < kP; ++p) {
-        const uint4 q = *reinterpret_cast<const uint4*>(qs + (n + g) * row_stride<HD>() +
-                                                        (4 * p + tq) * 16);
-        const uint32_t a0[4] = {kf[p][0].x, kf[p][1].x, kf[p][0].y, kf[p][1].y};
-        const uint32_t a1[4] = {kf[p][0].z, kf[p][1].z, kf[p][0].w, kf[p][1].w};
-        mma_f16(d, a0, q.x, q.y);
-        mma_f16(d, a1, q.z, q.w);
+      for (int k = 0; k < kM; ++k) {
+        qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+        qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = n + 2 * tq + (e & 1), j = e0 + g + 8 * (e >> 1);
-        if (j <= lim[r] && j < len) sum[e >> 1] += ex2(d[e] * a.scale_log2 - ls[r]);
+      for (int e = 0; e < 2; ++e) {
+        const int c = nt * 8 + 2 * tq + e, rr = r0 + c;
+        float v = -INFINITY;
+        if (c < nr)
+          v = a.lse[static_cast<long long>(first + rr / a.group) * a.n_q + h * a.group + rr % a.group];
+        lim[nt][e] = c < nr && v != -INFINITY ? off + rr / a.group : -1;  // a row that saw nothing
+        ls[nt][e] = v * kLog2e;
       }
     }
+    unsigned bad = 0;
+    int page = mine > 0 ? page_of(a.c, s, k0 + warp * kTile, a.err) : -1;
+    auto issue = [&](int it) {
+      if (it < mine) {
+        const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
+        const uint32_t kd = ring + st * key_bytes<HD>();
+        const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
+        const int end = page >= 0 ? len : 0;
+        bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
+#pragma unroll
+        for (int c = 0; c < kTile * kChunks / 32; ++c) {
+          const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
+          cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, e0 + r < end);
+        }
+        if (it + 1 < mine) page = page_of(a.c, s, e0 + kWarps * kTile, a.err);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int p = 0; p < kStages - 1; ++p) issue(p);
+    const float* src = r0 == 0 ? a.mass : a.mass_out;
+    const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+    for (int it = 0; it < mine; ++it) {
+      const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
+      // the entry this thread writes: tq 0 those of g, tq 1 those of g + 8
+      const int j_out = e0 + g + 8 * tq;
+      const bool writes = tq < 2 && j_out < len;
+      float before = 0.f;
+      if (writes && src != nullptr) before = src[entries + j_out];
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      issue(it + kStages - 1);
+      const uint32_t kd = ring + st * key_bytes<HD>();
+      float sc[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kM; ++k) {
+        uint32_t kf[4];
+        ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
+      }
+      const bool hidden = (bad >> st) & 1;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w =
+              ex2(fmaf(sc[nt][0][e] + sc[nt][1][e], a.scale_log2, -ls[nt][e & 1]));
+          if (!hidden && e0 + g + 8 * (e >> 1) <= lim[nt][e & 1]) sum[e >> 1] += w;
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
+        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+      }
+      if (writes) a.mass_out[entries + j_out] = before + (tq == 0 ? sum[0] : sum[1]);
+      __syncwarp();
+    }
+    cp_wait<0>();
+    __syncwarp();
+    r0 += kRows;
+  } while (r0 < rows);
+}
+
+// ------------------------------------------------------------ many rows
+constexpr int kBlock = 128;  // entries of a tile, rows of a step
+constexpr int kManyThreads = 384;
+constexpr int kSlots = 3;    // query tiles in flight
+
+template <int HD>
+struct Shape {
+  static constexpr int kHalves = HD / 64;
+  static constexpr int kBytes = kBlock * HD * 2;
+  static constexpr int kSmem = 1024 + (2 + kSlots) * kBytes;
+  static constexpr uint32_t kDesc = tc::idesc_f16(kBlock, kBlock, false);
+};
+
+struct Bars {
+  uint64_t keys, q_full[kSlots], q_empty[kSlots], s_full[2][2], s_empty[2][2], l_full[2], l_empty[2],
+      drain;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kManyThreads, 1)
+    mass_many_kernel(const MassArgs a, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap q_map, int blocks_per_head, int step_tokens) {
+  using Sh = Shape<HD>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(16) float s_lse[2][kBlock];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  uint8_t* qring = base + 2 * Sh::kBytes;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars.keys), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&bars.q_full[i]), 1);
+      mbar_init(smem_u32(&bars.q_empty[i]), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      for (int d = 0; d < 2; ++d) {
+        mbar_init(smem_u32(&bars.s_full[x][d]), 1);
+        mbar_init(smem_u32(&bars.s_empty[x][d]), kBlock);
+      }
+      mbar_init(smem_u32(&bars.l_full[x]), 32);
+      mbar_init(smem_u32(&bars.l_empty[x]), 2 * kBlock);
+    }
+    mbar_init(smem_u32(&bars.drain), 1);
+    fence_mbar_init();
   }
+  pdl_wait();
+  long long b = blockIdx.x;
+  const int e0 = static_cast<int>(b % blocks_per_head) * 2 * kBlock;
+  b /= blocks_per_head;
+  const int h = static_cast<int>(b % a.c.n_kv), s = static_cast<int>(b / a.c.n_kv);
+  const int len = seq_len(a.c, s, a.err);
+  int first, count;
+  seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
+  if (count > a.max_q) flag_error(a.err);
+  if (e0 >= len) return;
+  const int tokens = min(count, a.max_q), off = len - count;
+  // steps of step_tokens tokens, from the one whose last token sees entry e0
+  const int from = max(0, e0 - off) / step_tokens;
+  const int steps = max(0, (tokens + step_tokens - 1) / step_tokens - from);
+  const int tiles = e0 + kBlock < len ? 2 : 1;
+  if (warp == 8) tc::alloc(smem_u32(&s_tmem), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+
+  if (warp == 9) {
+    // ---------------------------------------------------------- producer
+    int issued = 0;
+    if (steps > 0) {
+      const int page_rows = min(1 << a.c.page_shift, kBlock), boxes = kBlock / page_rows;
+      const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.keys), 2 * Sh::kBytes);
+      __syncwarp();
+      if (lane < 2 * boxes) {
+        const int x = lane / boxes, e = e0 + lane * page_rows;
+        const int p = e < len ? page_of(a.c, s, e, a.err) : -1;
+        const int row = p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
+        const uint32_t dst =
+            smem_u32(base + x * Sh::kBytes) + (lane % boxes) * page_rows * 128;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
-    sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
-    const int j = e0 + g + 8 * e;
-    if (tq == 0 && j < len) {
-      const long long at = (static_cast<long long>(s) * a.c.n_kv + h) *
-                               (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + j;
-      a.mass_out[at] = (a.mass != nullptr ? a.mass[at] : 0.f) + sum[e];
+        for (int c = 0; c < Sh::kHalves; ++c)
+          tc::tma_2d(dst + c * (kBlock * 128), &k_map, c * 64, row, smem_u32(&bars.keys));
+      }
+      __syncwarp();
+      // queries: [token][head of the group] rows of 128 bytes
+      const uint32_t bytes = static_cast<uint32_t>(step_tokens * a.group * HD * 2);
+      for (int j = 0; j < steps; ++j) {
+        const int slot = j % kSlots, use = j / kSlots;
+        if (use > 0 && !mbar_wait(smem_u32(&bars.q_empty[slot]), (use - 1) & 1, &g_status)) break;
+        if (lane == 0) {
+          const uint32_t full = smem_u32(&bars.q_full[slot]);
+          mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+          for (int c = 0; c < Sh::kHalves; ++c)
+            tc::tma_3d(smem_u32(qring + slot * Sh::kBytes) + c * (kBlock * 128), &q_map, c * 64,
+                       h * a.group, first + (from + j) * step_tokens, full);
+        }
+        __syncwarp();
+        issued = j + 1;
+      }
+      // no copy may be in flight when the block ends
+      mbar_wait(smem_u32(&bars.keys), 0, &g_status);
+      for (int j = max(0, issued - kSlots); j < issued; ++j)
+        mbar_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
     }
+  } else if (warp == 10) {
+    // ------------------------------------------------- lse of each step's rows
+    // (a row outside the sequence, or one that saw nothing: +inf, weight 0)
+    for (int j = 0; j < steps; ++j) {
+      const int d = j & 1;
+      float v[kBlock / 32];
+#pragma unroll
+      for (int k = 0; k < kBlock / 32; ++k) {
+        const int c = lane + 32 * k, t = (from + j) * step_tokens + c / a.group;
+        v[k] = INFINITY;
+        if (c < step_tokens * a.group && t < tokens) {
+          const float x =
+              a.lse[static_cast<long long>(first + t) * a.n_q + h * a.group + c % a.group];
+          if (x != -INFINITY) v[k] = x * kLog2e;
+        }
+      }
+      if (j > 1 && !mbar_wait(smem_u32(&bars.l_empty[d]), (j / 2 - 1) & 1, &g_status)) break;
+#pragma unroll
+      for (int k = 0; k < kBlock / 32; ++k) s_lse[d][lane + 32 * k] = v[k];
+      mbar_arrive(smem_u32(&bars.l_full[d]));
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------- products
+    if (steps > 0) ok = mbar_wait(smem_u32(&bars.keys), 0, &g_status);
+    for (int j = 0; j < steps && ok; ++j) {
+      const int slot = j % kSlots, d = j & 1;
+      if (!mbar_wait(smem_u32(&bars.q_full[slot]), (j / kSlots) & 1, &g_status)) break;
+      for (int x = 0; x < tiles; ++x) {
+        if (j > 1 && !mbar_wait(smem_u32(&bars.s_empty[x][d]), (j / 2 - 1) & 1, &g_status)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        if (lane == 0) {
+          const uint64_t k = tc::desc_k_major(smem_u32(base + x * Sh::kBytes));
+          const uint64_t q = tc::desc_k_major(smem_u32(qring + slot * Sh::kBytes));
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            const int step = (i / 4) * (kBlock * 128) + (i % 4) * 32;
+            tc::mma_ss(tmem + (2 * x + d) * kBlock, k + (step >> 4), q + (step >> 4), Sh::kDesc,
+                       i > 0);
+          }
+          tc::commit(smem_u32(&bars.s_full[x][d]));
+        }
+        __syncwarp();
+      }
+      if (lane == 0) tc::commit(smem_u32(&bars.q_empty[slot]));
+      __syncwarp();
+    }
+    if (lane == 0) tc::commit(smem_u32(&bars.drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&bars.drain), 0, &g_status);
+  } else if (warp < 8) {
+    // -------------------------------------------------------------- sums
+    const int x = warp >> 2, e = e0 + x * kBlock + (warp & 3) * 32 + lane;
+    const bool live = e < len;
+    const int page = live ? page_of(a.c, s, e, nullptr) : -1;
+    const long long at = (static_cast<long long>(s) * a.c.n_kv + h) *
+                             (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + e;
+    const float before = live && a.mass != nullptr ? a.mass[at] : 0.f;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
+    for (int j = 0; j < steps; ++j) {
+      const int d = j & 1;
+      if (!mbar_wait(smem_u32(&bars.l_full[d]), (j / 2) & 1, &g_status)) break;
+      if (x < tiles) {
+        if (!mbar_wait(smem_u32(&bars.s_full[x][d]), (j / 2) & 1, &g_status)) break;
+        tc::fence_after();
+        // columns before `seen` are rows that lie before this entry, those from
+        // `end` on belong to no token of the sequence (and may hold anything)
+        const int t0 = (from + j) * step_tokens;
+        const int seen = (e - off - t0) * a.group;
+        const int end = min(step_tokens, tokens - t0) * a.group;
+        const bool all = __all_sync(0xFFFFFFFFu, seen <= 0) && end == kBlock;
+#pragma unroll
+        for (int c = 0; c < kBlock; c += 32) {
+          uint32_t v[32];
+          tc::ld32(v, lanes + d * kBlock + c);
+          tc::wait_ld32(v);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(&s_lse[d][c + k]);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float w = ex2(fmaf(__uint_as_float(v[k + i]), a.scale_log2, -l[i]));
+              if (all)
+                sum[i] += w;
+              else
+                sum[i] += c + k + i >= seen && c + k + i < end ? w : 0.f;
+            }
+          }
+        }
+        tc::fence_before();
+        mbar_arrive(smem_u32(&bars.s_empty[x][d]));
+      }
+      mbar_arrive(smem_u32(&bars.l_empty[d]));
+    }
+    if (live)
+      a.mass_out[at] = before + (page >= 0 ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f);
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
   }
 }
 
-template <int HD>
-cudaError_t launch_t(const MassArgs& a, cudaStream_t st) {
-  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  const int key_tiles = static_cast<int>((cap + 16 * kWarps - 1) / (16 * kWarps));
-  const long long blocks = static_cast<long long>(key_tiles) * a.c.n_kv * a.c.n_seqs;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+template <typename F, typename... Args>
+cudaError_t launch(F* k, std::atomic<unsigned long long>* done, long long blocks, int threads,
+                   int smem, cudaStream_t st, int device, Args... args) {
+  const unsigned long long bit = 1ull << (device & 63);
+  if (!(done->load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    done->fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (blocks < 1 || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_mass_kernel<HD>, a, key_tiles);
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int HD, int NT>
+cudaError_t launch_few(const MassArgs& a, int sms, cudaStream_t st, int device) {
+  static std::atomic<unsigned long long> done{0};
+  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
+  const long long units = static_cast<long long>(a.c.n_kv) * a.c.n_seqs;
+  // Parts of 128 to 1024 entries, enough to fill the machine (three blocks to
+  // a multiprocessor) twice over.
+  long long part = cap * units / (6LL * sms) / 64 * 64;
+  if (part < 128) part = 128;
+  if (part > 1024) part = 1024;
+  const long long parts = (cap + part - 1) / part;
+  return launch(mass_few_kernel<HD, NT>, &done, parts * units, 32 * kWarps,
+                kWarps * kStages * key_bytes<HD>(), st, device, a, static_cast<int>(part),
+                static_cast<int>(parts));
+}
+
+template <int HD>
+cudaError_t launch_many(const MassArgs& a, cudaStream_t st, int device) {
+  static std::atomic<unsigned long long> done{0};
+  const EncodeTiledFn fn = encode_fn();
+  CUtensorMap km, qm;
+  const int step_tokens = kBlock / a.group;
+  const cuuint64_t dim[3] = {static_cast<cuuint64_t>(HD), static_cast<cuuint64_t>(a.n_q),
+                             static_cast<cuuint64_t>(a.n_tokens)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(HD) * 2,
+                                static_cast<cuuint64_t>(a.q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.group),
+                             static_cast<cuuint32_t>(step_tokens)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  if (fn == nullptr || !encode_pool(&km, a.c, a.c.k) ||
+      fn(&qm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(a.q), dim, stride, box,
+         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
+  const int per_head = static_cast<int>((cap + 2 * kBlock - 1) / (2 * kBlock));
+  return launch(mass_many_kernel<HD>, &done, static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs,
+                kManyThreads, Shape<HD>::kSmem, st, device, a, km, qm, per_head, step_tokens);
+}
+
+template <int HD>
+cudaError_t launch_t(const MassArgs& a, int sms, cudaStream_t st, int device) {
+  const long long rows = static_cast<long long>(a.max_q) * a.group;
+  // (a group of more than 128 heads has no box of whole tokens)
+  if (rows > kRowsMax && a.group <= kBlock && a.n_tokens > 0) return launch_many<HD>(a, st, device);
+  if (rows <= 8) return launch_few<HD, 1>(a, sms, st, device);
+  if (rows <= 16) return launch_few<HD, 2>(a, sms, st, device);
+  return launch_few<HD, 4>(a, sms, st, device);
 }
 
 }  // namespace
 
-cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
-  return a.c.head_dim == 64 ? launch_t<64>(a, st) : launch_t<128>(a, st);
+cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device) {
+  return a.c.head_dim == 64 ? launch_t<64>(a, sms, st, device) : launch_t<128>(a, sms, st, device);
+}
+
+cudaError_t status_mass(unsigned* out) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *out |= v;
+  return e;
 }
 
 }  // namespace qgemv

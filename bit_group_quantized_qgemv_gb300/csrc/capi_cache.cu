@@ -193,14 +193,14 @@ int qgemv_attention_mass(const qgemv_kv_cache* cache, const uint16_t* q, long lo
   a.n_q = n_q;
   a.group = n_q / a.c.n_kv;
   a.q_start = q_start;
-  a.max_q = max_q;
+  a.max_q = n_tokens > 0 && n_tokens < max_q ? n_tokens : max_q;
   a.scale_log2 = scale * kLog2e;
   a.lse = lse;
   a.mass = mass;
   a.mass_out = mass_out;
   a.err = err_flag;
   return qgemv::report_launch(
-      qgemv::attention_mass_launch(a, sms, static_cast<cudaStream_t>(stream)));
+      qgemv::attention_mass_launch(a, sms, static_cast<cudaStream_t>(stream), dev));
 }
 
 int qgemv_cache_evict(const qgemv_kv_cache* cache, const float* mass, const int32_t* entry_pos,

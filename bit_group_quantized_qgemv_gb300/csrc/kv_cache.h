@@ -81,7 +81,7 @@ struct EvictArgs {
 };
 
 cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
-cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st);
+cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device);
 cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st);
 
 // How a call's cache is split: n_parts parts of `part` entries (1: not split),
@@ -106,6 +106,7 @@ long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q);
 AttnSplit attention_many_split(long long units, int n_kv, long long capacity, int sms);
 cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device);
 cudaError_t status_attention(unsigned* out);
+cudaError_t status_mass(unsigned* out);
 cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device);
 
 }  // namespace qgemv

@@ -22,6 +22,7 @@
 #include <atomic>
 
 #include "attention_common.cuh"
+#include "mma_tile.cuh"
 
 namespace qgemv {
 namespace {
@@ -33,28 +34,6 @@ constexpr float kSlack = 8.0f;  // log2 of the growth that makes O be rescaled
 template <int HD>
 __host__ __device__ constexpr int stage_bytes() {
   return 2 * kTile * HD * 2;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  const int n = take ? 16 : 0;  // 0: the 16 bytes are filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
 }
 
 constexpr int kMaxCluster = 8;
@@ -84,13 +63,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-
-// Byte offset of 16-byte chunk ch of row r in a tile of HD-wide rows; the
-// swizzle spreads 8 rows over the banks.
-template <int HD>
-__device__ __forceinline__ int tile_off(int r, int ch) {
-  return r * (HD * 2) + ((ch ^ (r & 7)) << 4);
 }
 
 template <int HD, int NT, bool LO, int kWarps>
