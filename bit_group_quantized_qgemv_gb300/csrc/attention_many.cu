@@ -9,7 +9,8 @@
 //               O += P V (P in tensor memory, V as the transposed operand);
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B: one row per thread,
 //               read from tensor memory, weights written back as fp16 over the
-//               scores they came from.
+//               scores they came from, in two halves: the product with the first
+//               starts while the second is computed.
 // While one tile's weights are computed the tensor core works on the other's
 // products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
 // (HD each).
@@ -35,10 +36,11 @@ namespace {
 __device__ unsigned g_status = 0;
 
 constexpr int kTile = 128;           // rows of a tile, entries of a step
-// Three warpgroups; the launch gives 168 registers a thread (64,512 of 65,536), of
-// which the third group passes on what the two of the softmax need: 2 x 128 x
-// 208 + 128 x 80 = 63,488.
+// Three warpgroups; the launch gives 168 registers a thread (64,512), of which
+// the third group passes on what the two of the softmax need: 256 x 200 + 128 x
+// 104 = 64,512.
 constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
 constexpr float kSlack = 8.0f;       // log2 of the growth that makes O be rescaled
 
 template <int HD>
@@ -47,13 +49,14 @@ struct Shape {
   static constexpr int kSlotBytes = kTile * HD * 2;
   static constexpr int kSlots = HD == 128 ? 5 : 10;
   static constexpr int kSmem = 1024 + (2 + kSlots) * kSlotBytes;
+  static_assert(kSmem + 1024 <= 227 * 1024, "dynamic and static shared memory");
   static constexpr uint32_t kDescS = tc::idesc_f16(kTile, kTile, false);
   static constexpr uint32_t kDescO = tc::idesc_f16(kTile, HD, true);
 };
 
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t s_full[2], p_full[2][2], o_full[2], drain;
 };
 
 // (sequence, row tile) of block unit u: sequences in order, each with
@@ -85,6 +88,12 @@ __device__ __forceinline__ void find_unit(const AttnArgs& a, int u, int lane, in
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_many_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -93,13 +102,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
+  __shared__ int s_failed;  // a wait ran out
   __shared__ int s_unit[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring = base + 2 * Sh::kSlotBytes;
 
   pdl_launch_dependents();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < Sh::kSlots; ++i) {
         mbar_init(smem_u32(&bars.full[i]), 1);
@@ -107,16 +117,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int x = 0; x < 2; ++x) {
         mbar_init(smem_u32(&bars.s_full[x]), 1);
-        mbar_init(smem_u32(&bars.p_full[x]), kTile);
+        mbar_init(smem_u32(&bars.p_full[x][0]), 4);  // one arrival per warp
+        mbar_init(smem_u32(&bars.p_full[x][1]), 4);
         mbar_init(smem_u32(&bars.o_full[x]), 1);
       }
       mbar_init(smem_u32(&bars.drain), 1);
       fence_mbar_init();
+      s_failed = 0;
     }
     __syncwarp();
   }
   pdl_wait();
-  if (warp == 9) {
+  if (warp == kTmaWarp) {
     int s, rt;
     find_unit(a, static_cast<int>(blockIdx.x / (a.n_parts * a.c.n_kv)), lane, &s, &rt);
     if (lane == 0) {
@@ -147,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = max(nt[0], nt[1]);
   const bool has_b = r0 + kTile < rows;
 
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tc::alloc(smem_u32(&s_tmem), 512);
   } else if (warp < 8 && tiles > 0) {
     // Queries into the swizzled operand layout: [column of 128 bytes][row][128 B].
@@ -170,29 +182,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
-  bool ok = true;
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp == kTmaWarp) {
     // ---------------------------------------------------------- producer
     const int page_rows = min(1 << a.c.page_shift, kTile);
     const int boxes = kTile / page_rows;  // per tile, at most 8
     const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;  // a row outside the tensor
-    auto row_of = [&](int j) {
+    auto page_at = [&](int j) {  // this lane's box of tile j
       const int e = k0 + j * kTile + lane * page_rows;
-      if (lane >= boxes || e >= len) return beyond;
-      const int p = page_of(a.c, s, e, a.err);
-      return p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
+      return lane < boxes && e < len ? raw_page(a.c, s, e) : 0;
     };
-    int row = tiles > 0 ? row_of(0) : 0, issued = 0;
-    for (int j = 0; j < tiles && ok; ++j) {
-      const int next = j + 1 < tiles ? row_of(j + 1) : 0;
+    int next = tiles > 0 ? page_at(0) : 0, issued = 0;
+    for (int j = 0; j < tiles; ++j) {
+      const int e = k0 + j * kTile + lane * page_rows, p = good_page(a.c, next, a.err);
+      const int row = p < 0 || e >= len ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
+      if (j + 1 < tiles) next = page_at(j + 1);
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const int n = 2 * j + w, slot = n % Sh::kSlots, use = n / Sh::kSlots;
-        if (use > 0 && !mbar_wait(smem_u32(&bars.empty[slot]), (use - 1) & 1, &g_status)) {
-          ok = false;
+        if (use > 0 && !warp_wait(smem_u32(&bars.empty[slot]), (use - 1) & 1, &g_status)) {
+          j = tiles;  // no more copies
           break;
         }
         const uint32_t full = smem_u32(&bars.full[slot]);
@@ -207,46 +218,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      row = next;
     }
     // no copy may be in flight when the block ends
     for (int n = max(0, issued - Sh::kSlots); n < issued; ++n)
-      mbar_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
-  } else if (warp == 8) {
+      warp_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- products
+    const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
+    const int n_tiles = tc::uniform(tiles), n_of[2] = {tc::uniform(nt[0]), tc::uniform(nt[1])};
+    const int tail = tc::uniform(len - k0);
     auto slot_of = [&](int n) { return smem_u32(ring + (n % Sh::kSlots) * Sh::kSlotBytes); };
     auto wait_full = [&](int n) {
-      return mbar_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
+      step_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &s_failed, &g_status);
     };
     auto release = [&](int n) { tc::commit(smem_u32(&bars.empty[n % Sh::kSlots])); };
     auto scores = [&](int x, int j) {
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint64_t q = tc::desc_k_major(smem_u32(base + x * Sh::kSlotBytes));
         const uint64_t k = tc::desc_k_major(slot_of(2 * j));
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
           const int step = (i / 4) * (kTile * 128) + (i % 4) * 32;
-          tc::mma_ss(tmem + x * kTile, q + (step >> 4), k + (step >> 4), Sh::kDescS, i > 0);
+          tc::mma_ss(tm + x * kTile, q + (step >> 4), k + (step >> 4), Sh::kDescS, i > 0);
         }
         tc::commit(smem_u32(&bars.s_full[x]));
       }
+      __syncwarp();
     };
-    if (tiles > 0) ok = wait_full(0);
-    if (ok && tiles > 0) {
-      if (nt[0] > 0) scores(0, 0);
-      if (nt[1] > 0) scores(1, 0);
-      if (lane == 0) release(0);
+    if (n_tiles > 0) {
+      wait_full(0);
+      if (n_of[0] > 0) scores(0, 0);
+      if (n_of[1] > 0) scores(1, 0);
+      if (tc::elect_one()) release(0);
     }
-    for (int j = 0; j < tiles && ok; ++j) {
-      if (!wait_full(2 * j + 1)) {
-        ok = false;
-        break;
-      }
-      const int e0 = k0 + j * kTile;
-      if (len < e0 + kTile) {
+    for (int j = 0; j < n_tiles; ++j) {
+      wait_full(2 * j + 1);
+      if (tail < (j + 1) * kTile) {
         // the rest of the last page may hold anything
         const int ps = 1 << a.c.page_shift;
-        const int from = len - e0, to = min(kTile, (from + ps - 1) / ps * ps);
+        const int from = tail - j * kTile, to = min(kTile, (from + ps - 1) / ps * ps);
         uint8_t* v = ring + ((2 * j + 1) % Sh::kSlots) * Sh::kSlotBytes;
         for (int c = lane; c < (to - from) * 8 * Sh::kHalves; c += 32) {
           const int r = from + c / (8 * Sh::kHalves), ch = c % (8 * Sh::kHalves);
@@ -256,43 +266,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_async_shared();
         __syncwarp();
       }
-      const bool more = j + 1 < tiles;
-      bool have_k = false;
+      if (j + 1 < n_tiles) wait_full(2 * j + 2);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (j < nt[x] && ok) {
-          if (!mbar_wait(smem_u32(&bars.p_full[x]), j & 1, &g_status)) {
-            ok = false;
-          } else {
+        if (j < n_of[x]) {
+          // the first half of the weights, then the second
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            step_wait(smem_u32(&bars.p_full[x][c]), j & 1, &s_failed, &g_status);
             tc::fence_after();
-            if (lane == 0) {
+            if (tc::elect_one()) {
               const uint64_t v = tc::desc_mn_major(slot_of(2 * j + 1), kTile * 128);
 #pragma unroll
-              for (int i = 0; i < kTile / 16; ++i)
-                tc::mma_ts(tmem + 2 * kTile + x * HD, tmem + x * kTile + i * 8, v + (i * 2048 >> 4),
-                           Sh::kDescO, j > 0 || i > 0);
-              if (j == nt[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
+              for (int i = 0; i < kTile / 32; ++i) {
+                const int k = c * (kTile / 32) + i;
+                tc::mma_ts(tm + 2 * kTile + x * HD, tm + x * kTile + k * 8, v + (k * 2048 >> 4),
+                           Sh::kDescO, j > 0 || k > 0);
+              }
+              if (c == 1 && j == n_of[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
             }
+            __syncwarp();
           }
         }
-        if (x == 1 && lane == 0 && ok) release(2 * j + 1);
-        if (more && ok && j + 1 < nt[x]) {
-          if (!have_k) {
-            ok = wait_full(2 * j + 2);
-            have_k = true;
-          }
-          if (ok) scores(x, j + 1);
-        }
+        if (x == 1 && tc::elect_one()) release(2 * j + 1);
+        __syncwarp();
+        if (j + 1 < n_of[x]) scores(x, j + 1);
       }
-      if (more && ok && lane == 0) release(2 * j + 2);
+      if (j + 1 < n_tiles && tc::elect_one()) release(2 * j + 2);
+      __syncwarp();
     }
     // every product is done before tensor memory goes back
-    if (lane == 0) tc::commit(smem_u32(&bars.drain));
+    if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
     __syncwarp();
-    mbar_wait(smem_u32(&bars.drain), 0, &g_status);
+    warp_wait(smem_u32(&bars.drain), 0, &g_status);
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ----------------------------------------------------------- softmax
     const int x = warp >> 2, r = (warp & 3) * 32 + lane, rr = r0 + x * kTile + r;
     const bool live = rr < rows;
@@ -300,24 +309,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lim = live ? off + i : -1;
     const uint32_t lanes = tmem + ((warp & 3) << 21);  // 32 lanes per warp, lane in bits 16..
     const uint32_t st = lanes + x * kTile, ot = lanes + 2 * kTile + x * HD;
-    auto bad_pages = [&](int j) {  // lane b: entries 16b.. of tile j lie on a bad page
+    auto page_at = [&](int j) {  // lane b: page of entries 16b.. of tile j
       const int e = k0 + j * kTile + lane * 16;
-      return lane < kTile / 16 && e < len && page_of(a.c, s, e, nullptr) < 0;
+      return lane < kTile / 16 && e < len ? raw_page(a.c, s, e) : 0;
     };
     float m = -INFINITY, l = 0.f;
-    bool bad_next = nt[x] > 0 && bad_pages(0);
+    int page_next = nt[x] > 0 ? page_at(0) : 0;
     for (int j = 0; j < nt[x]; ++j) {
-      const unsigned bad = __ballot_sync(0xFFFFFFFFu, bad_next);
-      if (j + 1 < nt[x]) bad_next = bad_pages(j + 1);
-      if (!mbar_wait(smem_u32(&bars.s_full[x]), j & 1, &g_status)) {
-        ok = false;
-        break;
-      }
+      const unsigned bad = __ballot_sync(0xFFFFFFFFu, good_page(a.c, page_next, nullptr) < 0);
+      if (j + 1 < nt[x]) page_next = page_at(j + 1);
+      step_wait(smem_u32(&bars.s_full[x]), j & 1, &s_failed, &g_status);
       tc::fence_after();
       uint32_t v[128];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::ld32(v + 32 * c, st + 32 * c);
-      tc::wait_ld128(v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::wait_ld32(v + 32 * c);
       const int hide = lim - (k0 + j * kTile);  // entries above this one are hidden
       if (__any_sync(0xFFFFFFFFu, hide < kTile - 1)) {
 #pragma unroll
@@ -331,48 +338,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < 128; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
+      for (int k = 0; k < 128; k += 2)
+        mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      // a row grows from nothing, or past the slack: rescale
-      const bool grow = mt > m + kSlack || (m == -INFINITY && mt > m);
-      if (__any_sync(0xFFFFFFFFu, grow)) {
+      // a row that grows past the slack (or from nothing) is rescaled
+      if (__any_sync(0xFFFFFFFFu, mt > m + kSlack)) {
         const float mn = fmaxf(m, mt);
         const float f = mn == m ? 1.f : ex2(m - mn);
         m = mn;
         l *= f;
         if (j > 0) {
 #pragma unroll
-          for (int c = 0; c < HD; c += 32) {
-            uint32_t o[32];
-            tc::ld32(o, ot + c);
-            tc::wait_ld32(o);
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t o[16];
+            tc::ld16(o, ot + c);
+            tc::wait_ld16(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tc::st32(ot + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tc::st16(ot + c, o);
           }
         }
       }
       const float b = m == -INFINITY ? 0.f : m;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t p[32];
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float x0 = ex2(fmaf(__uint_as_float(v[64 * c + 2 * k]), a.scale_log2, -b));
-          const float x1 = ex2(fmaf(__uint_as_float(v[64 * c + 2 * k + 1]), a.scale_log2, -b));
-          sum[(2 * k) & 3] += x0;
-          sum[(2 * k + 1) & 3] += x1;
-          p[k] = pack_f16(x0, x1);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int n = 64 * half + 32 * c + 2 * k;
+            const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
+            const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
+            sum[n & 3] += x0;
+            sum[(n + 1) & 3] += x1;
+            p[k] = pack_f16(x0, x1);
+          }
+          tc::st16(st + 32 * half + 16 * c, p);
         }
-        tc::st32(st + 32 * c, p);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc::wait_st();
-      tc::fence_before();
-      mbar_arrive(smem_u32(&bars.p_full[x]));
     }
-    if (ok && nt[x] > 0 && !mbar_wait(smem_u32(&bars.o_full[x]), 0, &g_status)) ok = false;
+    if (nt[x] > 0) step_wait(smem_u32(&bars.o_full[x]), 0, &s_failed, &g_status);
+    const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
     tc::fence_after();
     const int t = first + i, head = h * a.group + (live ? rr % a.group : 0);
     const long long at = static_cast<long long>(t) * a.n_q + head;
@@ -403,18 +416,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::ld32(o, ot + c);
           tc::wait_ld32(o);
         }
-        float w[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          w[k] = nt[x] > 0 ? __uint_as_float(o[k]) * inv : 0.f;
-          odd |= !(fabsf(w[k]) <= 3.0e38f);
-        }
-        if (live)
+        for (int k = 0; k < 32; k += 8) {
+          float w[8];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
+          for (int e = 0; e < 8; ++e) {
+            w[e] = nt[x] > 0 ? __uint_as_float(o[k + e]) * inv : 0.f;
+            odd |= !(fabsf(w[e]) <= 3.0e38f);
+          }
+          if (live)
             *reinterpret_cast<uint4*>(y + c + k) =
-                make_uint4(pack_f16(w[k], w[k + 1]), pack_f16(w[k + 2], w[k + 3]),
-                           pack_f16(w[k + 4], w[k + 5]), pack_f16(w[k + 6], w[k + 7]));
+                make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                           pack_f16(w[6], w[7]));
+        }
       }
       if (live && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * kLn2;
       // rows that hide entries and came out infinite or NaN: again, without them
@@ -431,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
   }

@@ -92,11 +92,12 @@ __global__ void __launch_bounds__(32 * kWarps) mass_few_kernel(const MassArgs a,
       }
     }
     unsigned bad = 0;
-    int page = mine > 0 ? page_of(a.c, s, k0 + warp * kTile, a.err) : -1;
+    int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
     auto issue = [&](int it) {
       if (it < mine) {
         const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
         const uint32_t kd = ring + st * key_bytes<HD>();
+        const int page = good_page(a.c, next, a.err);
         const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
         const int end = page >= 0 ? len : 0;
         bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps) mass_few_kernel(const MassArgs a,
           const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
           cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, e0 + r < end);
         }
-        if (it + 1 < mine) page = page_of(a.c, s, e0 + kWarps * kTile, a.err);
+        if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
       }
       cp_commit();
     };
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
+  __shared__ int s_failed;  // a wait ran out
   __shared__ __align__(16) float s_lse[2][kBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -200,13 +202,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     for (int x = 0; x < 2; ++x) {
       for (int d = 0; d < 2; ++d) {
         mbar_init(smem_u32(&bars.s_full[x][d]), 1);
-        mbar_init(smem_u32(&bars.s_empty[x][d]), kBlock);
+        mbar_init(smem_u32(&bars.s_empty[x][d]), 4);  // one arrival per warp
       }
-      mbar_init(smem_u32(&bars.l_full[x]), 32);
-      mbar_init(smem_u32(&bars.l_empty[x]), 2 * kBlock);
+      mbar_init(smem_u32(&bars.l_full[x]), 1);
+      mbar_init(smem_u32(&bars.l_empty[x]), 8);
     }
     mbar_init(smem_u32(&bars.drain), 1);
     fence_mbar_init();
+    s_failed = 0;
   }
   pdl_wait();
   long long b = blockIdx.x;
@@ -228,7 +231,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
-  bool ok = true;
 
   if (warp == 9) {
     // ---------------------------------------------------------- producer
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const uint32_t bytes = static_cast<uint32_t>(step_tokens * a.group * HD * 2);
       for (int j = 0; j < steps; ++j) {
         const int slot = j % kSlots, use = j / kSlots;
-        if (use > 0 && !mbar_wait(smem_u32(&bars.q_empty[slot]), (use - 1) & 1, &g_status)) break;
+        if (use > 0 && !warp_wait(smem_u32(&bars.q_empty[slot]), (use - 1) & 1, &g_status)) break;
         if (lane == 0) {
           const uint32_t full = smem_u32(&bars.q_full[slot]);
           mbar_arrive_expect_tx(full, bytes);
@@ -266,9 +268,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         issued = j + 1;
       }
       // no copy may be in flight when the block ends
-      mbar_wait(smem_u32(&bars.keys), 0, &g_status);
+      warp_wait(smem_u32(&bars.keys), 0, &g_status);
       for (int j = max(0, issued - kSlots); j < issued; ++j)
-        mbar_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
+        warp_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
     }
   } else if (warp == 10) {
     // ------------------------------------------------- lse of each step's rows
@@ -286,42 +288,42 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (x != -INFINITY) v[k] = x * kLog2e;
         }
       }
-      if (j > 1 && !mbar_wait(smem_u32(&bars.l_empty[d]), (j / 2 - 1) & 1, &g_status)) break;
+      if (j > 1 && !warp_wait(smem_u32(&bars.l_empty[d]), (j / 2 - 1) & 1, &g_status)) break;
 #pragma unroll
       for (int k = 0; k < kBlock / 32; ++k) s_lse[d][lane + 32 * k] = v[k];
-      mbar_arrive(smem_u32(&bars.l_full[d]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.l_full[d]));
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------- products
-    if (steps > 0) ok = mbar_wait(smem_u32(&bars.keys), 0, &g_status);
-    for (int j = 0; j < steps && ok; ++j) {
+    const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
+    const int n_steps = tc::uniform(steps), n_tiles = tc::uniform(tiles);
+    if (n_steps > 0) step_wait(smem_u32(&bars.keys), 0, &s_failed, &g_status);
+    for (int j = 0; j < n_steps; ++j) {
       const int slot = j % kSlots, d = j & 1;
-      if (!mbar_wait(smem_u32(&bars.q_full[slot]), (j / kSlots) & 1, &g_status)) break;
-      for (int x = 0; x < tiles; ++x) {
-        if (j > 1 && !mbar_wait(smem_u32(&bars.s_empty[x][d]), (j / 2 - 1) & 1, &g_status)) {
-          ok = false;
-          break;
-        }
+      step_wait(smem_u32(&bars.q_full[slot]), (j / kSlots) & 1, &s_failed, &g_status);
+      for (int x = 0; x < n_tiles; ++x) {
+        if (j > 1) step_wait(smem_u32(&bars.s_empty[x][d]), (j / 2 - 1) & 1, &s_failed, &g_status);
         tc::fence_after();
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint64_t k = tc::desc_k_major(smem_u32(base + x * Sh::kBytes));
           const uint64_t q = tc::desc_k_major(smem_u32(qring + slot * Sh::kBytes));
 #pragma unroll
           for (int i = 0; i < HD / 16; ++i) {
             const int step = (i / 4) * (kBlock * 128) + (i % 4) * 32;
-            tc::mma_ss(tmem + (2 * x + d) * kBlock, k + (step >> 4), q + (step >> 4), Sh::kDesc,
+            tc::mma_ss(tm + (2 * x + d) * kBlock, k + (step >> 4), q + (step >> 4), Sh::kDesc,
                        i > 0);
           }
           tc::commit(smem_u32(&bars.s_full[x][d]));
         }
         __syncwarp();
       }
-      if (lane == 0) tc::commit(smem_u32(&bars.q_empty[slot]));
+      if (tc::elect_one()) tc::commit(smem_u32(&bars.q_empty[slot]));
       __syncwarp();
     }
-    if (lane == 0) tc::commit(smem_u32(&bars.drain));
+    if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
     __syncwarp();
-    mbar_wait(smem_u32(&bars.drain), 0, &g_status);
+    warp_wait(smem_u32(&bars.drain), 0, &g_status);
   } else if (warp < 8) {
     // -------------------------------------------------------------- sums
     const int x = warp >> 2, e = e0 + x * kBlock + (warp & 3) * 32 + lane;
@@ -334,9 +336,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
     for (int j = 0; j < steps; ++j) {
       const int d = j & 1;
-      if (!mbar_wait(smem_u32(&bars.l_full[d]), (j / 2) & 1, &g_status)) break;
+      step_wait(smem_u32(&bars.l_full[d]), (j / 2) & 1, &s_failed, &g_status);
       if (x < tiles) {
-        if (!mbar_wait(smem_u32(&bars.s_full[x][d]), (j / 2) & 1, &g_status)) break;
+        step_wait(smem_u32(&bars.s_full[x][d]), (j / 2) & 1, &s_failed, &g_status);
         tc::fence_after();
         // columns before `seen` are rows that lie before this entry, those from
         // `end` on belong to no token of the sequence (and may hold anything)
@@ -364,11 +366,12 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           }
         }
         tc::fence_before();
-        mbar_arrive(smem_u32(&bars.s_empty[x][d]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.s_empty[x][d]));
       }
-      mbar_arrive(smem_u32(&bars.l_empty[d]));
+      if (lane == 0) mbar_arrive(smem_u32(&bars.l_empty[d]));
     }
-    if (live)
+    if (live && *static_cast<volatile int*>(&s_failed) == 0)
       a.mass_out[at] = before + (page >= 0 ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f);
   }
   tc::fence_before();

@@ -27,20 +27,61 @@ __device__ __forceinline__ void seq_rows(const int* q_start, int s, int n_tokens
   *count = b0 - a0;
 }
 
-// Page that holds entry i of sequence s; -1 for a bad page number.
+// Page-table entry for entry i of sequence s, as it stands there.  Loops load it
+// a step ahead and look at it (good_page) when they need it: a look right after
+// the load would wait for it.
+__device__ __forceinline__ int raw_page(const KvView& c, int s, int i) {
+  return c.page_table[static_cast<long long>(s) * c.max_pages + (i >> c.page_shift)];
+}
+
+// A page number, -1 for a bad one.
+__device__ __forceinline__ int good_page(const KvView& c, int p, int* err) {
+  if (p >= 0 && p < c.n_pages) return p;
+  flag_error(err);
+  return -1;
+}
+
 __device__ __forceinline__ int page_of(const KvView& c, int s, int i, int* err) {
-  const int p = c.page_table[static_cast<long long>(s) * c.max_pages + (i >> c.page_shift)];
-  if (p < 0 || p >= c.n_pages) {
-    flag_error(err);
-    return -1;
-  }
-  return p;
+  return good_page(c, raw_page(c, s, i), err);
 }
 
 // Row of entry i on page p for head h, as a row index into k or v.
 __device__ __forceinline__ long long cache_row(const KvView& c, int p, int h, int i) {
   return ((static_cast<long long>(p) * c.n_kv + h) << c.page_shift) +
          (i & ((1 << c.page_shift) - 1));
+}
+
+// A bounded wait of a whole warp: every lane gets the same answer, so a wait
+// that runs out does not split the warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, status));
+}
+
+// A bounded wait that answers nothing, for loops whose steps are short: there
+// an answer to test at every wait, or to carry along, cost a seventh of the time
+// (measured on GB300: 448 against 387 us for 1216 tokens over 30000 entries).  A
+// wait of more than a second sets *failed (in shared memory), after which the
+// block's waits last for a thousand tries: its loops go on over whatever they
+// find, in bounds and for as many steps as they have, and the results are
+// dropped.
+__device__ __forceinline__ void step_wait(uint32_t bar, uint32_t parity, volatile int* failed,
+                                          unsigned* status) {
+  bool done = mbar_try_wait(bar, parity);
+  uint64_t t0 = 0;
+  for (int i = 1; !done; ++i) {
+    done = mbar_try_wait(bar, parity);
+    if ((i & 1023) == 0) {
+      if (*failed != 0) break;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 1000000000ull) {
+        *failed = 1;
+        atomicOr(status, kStatusWaitTimeout);
+        break;
+      }
+    }
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ float ex2(float x) {

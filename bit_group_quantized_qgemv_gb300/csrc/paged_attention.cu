@@ -89,9 +89,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   // The first tile's page number is read along with the lengths.
   const int k0 = sp * a.part;
   const int e_first = k0 + warp * kTile;
-  int page = -1;
-  if (e_first < a.c.max_pages << a.c.page_shift)
-    page = a.c.page_table[static_cast<long long>(s) * a.c.max_pages + (e_first >> a.c.page_shift)];
+  int next = e_first < a.c.max_pages << a.c.page_shift ? raw_page(a.c, s, e_first) : -1;
 
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
@@ -114,10 +112,6 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
   unsigned bad = 0;  // bit st: the tile in stage st lies on a bad page
-  if (mine > 0 && (page < 0 || page >= a.c.n_pages)) {
-    flag_error(a.err);
-    page = -1;
-  }
 
   // Queries as B fragments: column = row of the block.
   uint32_t qf[NT][kM][2];
@@ -155,6 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
       const int e0 = k0 + (it * kWarps + warp) * kTile;
       const int st = it % kStages;
       const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
+      const int page = good_page(a.c, next, a.err);
       const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
       const int end = page >= 0 ? len : 0;
       bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
@@ -167,7 +162,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
         cp_async16(vd + tile_off<HD>(r, ch), a.c.v + base + id * 8, take);
       }
       // the next tile's page, a step ahead of its use
-      if (it + 1 < mine) page = page_of(a.c, s, e0 + kWarps * kTile, a.err);
+      if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
     }
     cp_commit();
   };

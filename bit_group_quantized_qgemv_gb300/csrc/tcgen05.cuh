@@ -30,6 +30,20 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t column
          (static_cast<uint64_t>(column >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// One lane of a converged warp.  Products are issued under this, with
+// operands that the compiler can see to be the same for the whole warp
+// (uniform() below): they go to uniform registers, and an operand it takes for
+// divergent costs more clocks to move there than the product takes (measured on
+// GB300: about 160 clocks a product against the 64 of 128 x 128 x 16).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Tensor memory: a whole warp allocates and frees.
 __device__ __forceinline__ void alloc(uint32_t dst, uint32_t columns) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
@@ -77,7 +91,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-// 32 columns of this warp's 32 lanes, one lane per thread.  The registers of
+// 32 (16) columns of this warp's 32 lanes, one lane per thread.  The registers of
 // a load are valid after the wait that names them.
 __device__ __forceinline__ void ld32(uint32_t* r, uint32_t addr) {
   asm volatile(
@@ -89,17 +103,6 @@ __device__ __forceinline__ void ld32(uint32_t* r, uint32_t addr) {
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void wait_st() {
@@ -117,11 +120,31 @@ __device__ __forceinline__ void wait_ld32(uint32_t* r) {
                :
                : "memory");
 }
-__device__ __forceinline__ void wait_ld128(uint32_t* r) {
-  wait_ld32(r);
-  wait_ld32(r + 32);
-  wait_ld32(r + 64);
-  wait_ld32(r + 96);
+__device__ __forceinline__ void ld16(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
 // TMA: a 2-D box into shared memory, its bytes counted on `bar`.
