@@ -9,8 +9,7 @@
 //               O += P V (P in tensor memory, V as the transposed operand);
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B: one row per thread,
 //               read from tensor memory, weights written back as fp16 over the
-//               scores they came from, in two halves: the product with the first
-//               starts while the second is computed.
+//               scores they came from.
 // While one tile's weights are computed the tensor core works on the other's
 // products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
 // (HD each).
@@ -56,7 +55,7 @@ struct Shape {
 
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_full[2][2], o_full[2], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
 };
 
 // (sequence, row tile) of block unit u: sequences in order, each with
@@ -117,8 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int x = 0; x < 2; ++x) {
         mbar_init(smem_u32(&bars.s_full[x]), 1);
-        mbar_init(smem_u32(&bars.p_full[x][0]), 4);  // one arrival per warp
-        mbar_init(smem_u32(&bars.p_full[x][1]), 4);
+        mbar_init(smem_u32(&bars.p_full[x]), 4);  // one arrival per warp
         mbar_init(smem_u32(&bars.o_full[x]), 1);
       }
       mbar_init(smem_u32(&bars.drain), 1);
@@ -178,8 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     tc::fence_async_shared();
   }
+  // (the producer starts at once)
   tc::fence_before();
-  __syncthreads();
+  if (warp <= kMmaWarp) named_bar_sync(1, 32 * (kMmaWarp + 1));
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
@@ -270,23 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (j < n_of[x]) {
-          // the first half of the weights, then the second
+          step_wait(smem_u32(&bars.p_full[x]), j & 1, &s_failed, &g_status);
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t v = tc::desc_mn_major(slot_of(2 * j + 1), kTile * 128);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            step_wait(smem_u32(&bars.p_full[x][c]), j & 1, &s_failed, &g_status);
-            tc::fence_after();
-            if (tc::elect_one()) {
-              const uint64_t v = tc::desc_mn_major(slot_of(2 * j + 1), kTile * 128);
-#pragma unroll
-              for (int i = 0; i < kTile / 32; ++i) {
-                const int k = c * (kTile / 32) + i;
-                tc::mma_ts(tm + 2 * kTile + x * HD, tm + x * kTile + k * 8, v + (k * 2048 >> 4),
-                           Sh::kDescO, j > 0 || k > 0);
-              }
-              if (c == 1 && j == n_of[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
-            }
-            __syncwarp();
+            for (int i = 0; i < kTile / 16; ++i)
+              tc::mma_ts(tm + 2 * kTile + x * HD, tm + x * kTile + i * 8, v + (i * 2048 >> 4),
+                         Sh::kDescO, j > 0 || i > 0);
+            if (j == n_of[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
           }
+          __syncwarp();
         }
         if (x == 1 && tc::elect_one()) release(2 * j + 1);
         __syncwarp();
@@ -362,26 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float b = m == -INFINITY ? 0.f : m;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int n = 64 * half + 32 * c + 2 * k;
-            const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
-            const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
-            sum[n & 3] += x0;
-            sum[(n + 1) & 3] += x1;
-            p[k] = pack_f16(x0, x1);
-          }
-          tc::st16(st + 32 * half + 16 * c, p);
+        for (int k = 0; k < 16; ++k) {
+          const int n = 32 * c + 2 * k;
+          const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
+          const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
+          sum[n & 3] += x0;
+          sum[(n + 1) & 3] += x1;
+          p[k] = pack_f16(x0, x1);
         }
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x][half]));
+        tc::st16(st + 16 * c, p);
       }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     if (nt[x] > 0) step_wait(smem_u32(&bars.o_full[x]), 0, &s_failed, &g_status);

@@ -2,24 +2,25 @@
 // each (sequence, key/value head) and close the gaps.
 //
 // Selection: one block per (sequence, head).  Masses become 32-bit keys whose
-// order is the ranking (protected entries highest, NaN lowest); the keep-th
-// largest key T is found by radix selection, eight bits at a time, and the
-// lowest-index entries equal to T fill up what is missing.  Every warp owns a
-// run of consecutive entries, so ranks in index order are prefix sums over
-// the warps' counts.  The movers' list is written to the front of pos_out
+// order is the ranking (protected entries highest, NaN lowest), read once and
+// kept in shared memory; the keep-th largest key T is found by radix selection
+// (2048 bins: with 256 most lanes of a warp met in one, the leading bits of floats
+// of like size being the same), and the lowest-index entries equal to T fill up
+// what is missing.  Every warp owns a run of consecutive entries, so ranks in
+// index order are prefix sums over the warps' counts.  The movers' list is written to the front of pos_out
 // first (it is at most as long as what pos_out gets in the end), the holes
 // pick their mover from it, and only then the permuted masses and positions
 // are written.
 // Moving: a second kernel copies the rows of k and v whose place changed.
 // Sources lie at or beyond the new length and targets below it, so no copy
 // reads what another writes.
+#include <atomic>
+
 #include "kv_cache.cuh"
 
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // Larger key: kept first.  Equal masses (-0 and +0 too) have equal keys.
@@ -31,23 +32,29 @@ __device__ __forceinline__ unsigned rank_key(float mass, int pos, int sink, long
 }
 
 // Sums of the warps below this one, and the total over the block.
-__device__ __forceinline__ int warps_before(int mine, int* slots, int warp, int lane, int* total) {
+template <int kWarps>
+__device__ __forceinline__ int warps_before(int mine, int* slots, int warp, int lane) {
   __syncthreads();
   if (lane == 0) slots[warp] = mine;
   __syncthreads();
-  int v = slots[lane];
-  int below = lane < warp ? v : 0;
+  int below = lane < warp && lane < kWarps ? slots[lane] : 0;
 #pragma unroll
-  for (int k = 16; k > 0; k /= 2) {
-    v += __shfl_xor_sync(kAll, v, k);
-    below += __shfl_xor_sync(kAll, below, k);
-  }
-  *total = v;
+  for (int k = 16; k > 0; k /= 2) below += __shfl_xor_sync(kAll, below, k);
   return below;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
+constexpr int kBins = 2048;  // 11 bits a pass: 11, 11, 10
+
+// KEYS: the keys stay in (dynamic) shared memory; else they are made again from
+// memory at every pass.
+constexpr int kThreads = 1024;  // two blocks to a multiprocessor
+
+template <bool KEYS>
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kOwn = kBins / kThreads;  // bins of a thread in the search, highest first
+  extern __shared__ unsigned keys[];
+  __shared__ int hist[kBins];
   __shared__ int slots[kWarps];
   __shared__ unsigned s_prefix;
   __shared__ int s_left;
@@ -55,6 +62,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.x % a.c.n_kv, s = blockIdx.x / a.c.n_kv;
+  const int next = a.next_pos[s];
   const int len = seq_len(a.c, s, a.err);
   const int left = min(len, a.keep);
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
@@ -64,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   float* mass_out = a.mass_out + base;
   int* pos_out = a.pos_out + base;
   int* kept = a.kept + (static_cast<long long>(s) * a.c.n_kv + h) * a.keep;
-  const long long recent = static_cast<long long>(a.next_pos[s]) - a.n_recent;
+  const long long recent = static_cast<long long>(next) - a.n_recent;
   if (h == 0 && threadIdx.x == 0) a.len_out[s] = left;
   for (int i = left + threadIdx.x; i < a.keep; i += kThreads) kept[i] = -1;
   if (len == left) {  // nothing to choose
@@ -76,99 +84,171 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     return;
   }
 
-  // T: the left-th largest key; s_left: how many of the entries equal to it stay
-  unsigned prefix = 0;
-  int need = left;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    const unsigned above = shift == 24 ? 0u : kAll << (shift + 8);
-    for (int i0 = warp * 32; i0 < len; i0 += kThreads) {
-      const int i = i0 + lane;
-      unsigned key = 0;
-      bool in = i < len;
-      if (in) {
-        key = rank_key(mass[i], pos[i], a.n_sink, recent);
-        in = (key & above) == prefix;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+  // Four consecutive entries per thread and step (16-byte loads where the arrays
+  // allow them; the capacity is a multiple of 16).
+  const bool wide = ((reinterpret_cast<uintptr_t>(mass) | reinterpret_cast<uintptr_t>(pos)) & 15) == 0;
+  auto make4 = [&](int i, unsigned* k) {
+    float m[4];
+    int p[4];
+    if (wide) {
+      const float4 m4 = *reinterpret_cast<const float4*>(mass + i);
+      const int4 p4 = *reinterpret_cast<const int4*>(pos + i);
+      m[0] = m4.x, m[1] = m4.y, m[2] = m4.z, m[3] = m4.w;
+      p[0] = p4.x, p[1] = p4.y, p[2] = p4.z, p[3] = p4.w;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        m[c] = mass[i + c];
+        p[c] = pos[i + c];
       }
-      const unsigned bin = in ? (key >> shift) & 255u : 256u;
-      const unsigned same = __match_any_sync(kAll, bin);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) k[c] = rank_key(m[c], p[c], a.n_sink, recent);
+  };
+  auto load4 = [&](int i, unsigned* k) {
+    if constexpr (KEYS) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    } else {
+      make4(i, k);
+    }
+  };
+  if constexpr (KEYS) {
+#pragma unroll 4
+    for (int i = 4 * threadIdx.x; i < len; i += 4 * kThreads) {
+      unsigned k[4];
+      make4(i, k);
+      *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+  }
+  __syncthreads();
+
+  // T: the left-th largest key; need: how many of the entries equal to it stay
+  unsigned prefix = 0, above = 0;
+  int need = left;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const unsigned bins = pass == 2 ? 1023u : 2047u;
+    for (int i0 = warp * 128; i0 < len; i0 += 4 * kThreads) {
+      const int i = i0 + 4 * lane;
+      unsigned k[4] = {0u, 0u, 0u, 0u};
+      if (i < len) load4(i, k);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in = i + c < len && (k[c] & above) == prefix;
+        const int bin = (k[c] >> shift) & bins;
+        // lanes that all fall into the first one's bin (equal masses) count once
+        const int bin0 = __shfl_sync(kAll, bin, 0);
+        if (__all_sync(kAll, in && bin == bin0)) {
+          if (lane == 0) atomicAdd(&hist[bin], 32);
+        } else if (in) {
+          atomicAdd(&hist[bin], 1);
+        }
+      }
     }
     __syncthreads();
-    if (warp == 0) {  // the bin in which the need-th largest lies
-      int c[8], sum = 0;
+    // the bin in which the need-th largest lies
+    int c[kOwn], sum = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        c[k] = hist[255 - (lane * 8 + k)];
-        sum += c[k];
-      }
-      int incl = sum;
+    for (int k = 0; k < kOwn; ++k) {
+      c[k] = hist[kBins - 1 - (threadIdx.x * kOwn + k)];
+      sum += c[k];
+    }
+    int incl = sum;
 #pragma unroll
-      for (int k = 1; k < 32; k *= 2) {
-        const int v = __shfl_up_sync(kAll, incl, k);
-        if (lane >= k) incl += v;
-      }
-      int run = incl - sum;
+    for (int k = 1; k < 32; k *= 2) {
+      const int v = __shfl_up_sync(kAll, incl, k);
+      if (lane >= k) incl += v;
+    }
+    int run = warps_before<kWarps>(__shfl_sync(kAll, incl, 31), slots, warp, lane) + incl - sum;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (run < need && run + c[k] >= need) {
-          s_prefix = prefix | (static_cast<unsigned>(255 - (lane * 8 + k)) << shift);
-          s_left = need - run;
-        }
-        run += c[k];
+    for (int k = 0; k < kOwn; ++k) {
+      const int b = kBins - 1 - (threadIdx.x * kOwn + k);
+      if (run < need && run + c[k] >= need) {
+        s_prefix = prefix | (static_cast<unsigned>(b) << shift);
+        s_left = need - run;
       }
+      run += c[k];
+      hist[b] = 0;
     }
     __syncthreads();
     prefix = s_prefix;
     need = s_left;
+    above |= bins << shift;
   }
   const unsigned T = prefix;
 
-  // Runs of whole 32-entry groups per warp, in index order.
-  const int groups = (len + 31) / 32, per = (groups + kWarps - 1) / kWarps;
-  const int i_lo = warp * per * 32, i_hi = min(len, (warp + 1) * per * 32);
-  auto key_at = [&](int i) { return rank_key(mass[i], pos[i], a.n_sink, recent); };
-  int eq = 0;
-  for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-    const int i = i0 + lane;
-    eq += __popc(__ballot_sync(kAll, i < i_hi && key_at(i) == T));
+  // Runs of whole 128-entry groups per warp, in index order: counts of what
+  // stays for certain and of the entries equal to T, below and from `left` on.
+  const int per = ((len + 127) / 128 + kWarps - 1) / kWarps * 128;
+  const int i_lo = min(len, warp * per), i_hi = min(len, (warp + 1) * per);
+  int n_gt_low = 0, n_gt_high = 0, n_eq_low = 0, n_eq_high = 0;  // this lane's
+  for (int i = i_lo + 4 * lane; i < i_hi; i += 128) {
+    unsigned k[4];
+    load4(i, k);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bool in = i + c < i_hi, low = i + c < left;
+      n_gt_low += in && low && k[c] > T;
+      n_gt_high += in && !low && k[c] > T;
+      n_eq_low += in && low && k[c] == T;
+      n_eq_high += in && !low && k[c] == T;
+    }
   }
-  int total;
-  const int eq0 = warps_before(eq, slots, warp, lane, &total);
+  const int gt_low = __reduce_add_sync(kAll, n_gt_low), gt_high = __reduce_add_sync(kAll, n_gt_high);
+  const int eq_low = __reduce_add_sync(kAll, n_eq_low), eq_high = __reduce_add_sync(kAll, n_eq_high);
+  // Of the entries equal to T the first `need` in index order stay.
+  const int eq0 = warps_before<kWarps>(eq_low + eq_high, slots, warp, lane);
+  const int eq_stay = min(max(need - eq0, 0), eq_low + eq_high), eq_stay_low = min(eq_stay, eq_low);
+  int nh = warps_before<kWarps>(max(0, min(i_hi, left) - i_lo) - gt_low - eq_stay_low, slots, warp,
+                                lane);
+  int nm = warps_before<kWarps>(gt_high + eq_stay - eq_stay_low, slots, warp, lane);
+  int e = eq0;
   const unsigned below_lane = (1u << lane) - 1u;
-  int holes = 0, movers = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int e = eq0, nh = holes, nm = movers;  // second pass: ranks of this warp's first
-    if (pass == 0) nh = nm = 0;
-    for (int i0 = i_lo; i0 < i_hi; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned key = i < i_hi ? key_at(i) : 0u;
-      const bool is_eq = i < i_hi && key == T;
-      const unsigned eqs = __ballot_sync(kAll, is_eq);
-      const bool stays = i < i_hi && (key > T || (is_eq && e + __popc(eqs & below_lane) < need));
-      e += __popc(eqs);
-      const unsigned hb = __ballot_sync(kAll, i < i_hi && i < left && !stays);
-      const unsigned mb = __ballot_sync(kAll, i < i_hi && i >= left && stays);
-      if (pass == 1) {
-        // a hole notes its rank (negative), a mover enters the list
-        if (i < i_hi && i < left) kept[i] = stays ? i : ~(nh + __popc(hb & below_lane));
-        if ((mb >> lane) & 1u) pos_out[nm + __popc(mb & below_lane)] = i;
-      }
+  for (int i0 = i_lo; i0 < i_hi; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    unsigned k[4] = {0u, 0u, 0u, 0u};
+    if (i < i_hi) load4(i, k);
+    // ranks in index order: lanes below this one, then this lane's entries in turn
+    int e_rank = e, h_rank = nh, m_rank = nm;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const unsigned b = __ballot_sync(kAll, i + c < i_hi && k[c] == T);
+      e_rank += __popc(b & below_lane);
+      e += __popc(b);
+    }
+    bool hole[4], mover[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bool in = i + c < i_hi;
+      const bool st = in && (k[c] > T || (k[c] == T && e_rank < need));
+      e_rank += in && k[c] == T;
+      hole[c] = in && i + c < left && !st;
+      mover[c] = i + c >= left && st;
+      const unsigned hb = __ballot_sync(kAll, hole[c]), mb = __ballot_sync(kAll, mover[c]);
+      h_rank += __popc(hb & below_lane);
+      m_rank += __popc(mb & below_lane);
       nh += __popc(hb);
       nm += __popc(mb);
     }
-    if (pass == 0) {
-      holes = warps_before(nh, slots, warp, lane, &total);
-      movers = warps_before(nm, slots, warp, lane, &total);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // a hole notes its rank (negative), a mover enters the list
+      if (i + c < i_hi && i + c < left) kept[i + c] = hole[c] ? ~h_rank : i + c;
+      if (mover[c]) pos_out[m_rank] = i + c;
+      h_rank += hole[c];
+      m_rank += mover[c];
     }
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < left; i += kThreads) {
     const int k = kept[i];
     if (k < 0) kept[i] = pos_out[~k];
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < left; i += kThreads) {
     const int k = kept[i];
     mass_out[i] = mass[k];
@@ -200,36 +280,41 @@ __global__ void __launch_bounds__(128) evict_move_kernel(const EvictArgs a, int 
       dst = cache_row(a.c, q, h, i) * HD;
     }
   }
-  // two rows (k and v of one entry) at a time: half a warp each when HD = 128
-  constexpr int kPer = 32 / (2 * kVec);
+  // An entry is 2 kVec pieces of 16 bytes (its rows of k and v): kPer entries
+  // per pass of the warp, kU passes loaded before any is stored.
+  constexpr int kPer = 32 / (2 * kVec), kU = 8;
+  const int sub = lane / (2 * kVec), rest = lane % (2 * kVec);
+  __half* pool = (rest < kVec ? a.c.k : a.c.v) + (rest % kVec) * 8;
   while (moved != 0) {
-    int at[kPer];
+    uint4 x[kU];
+    long long to[kU];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      at[k] = moved != 0 ? __ffs(moved) - 1 : -1;
-      moved &= moved - 1;
-    }
-    const int sub = lane / (2 * kVec), rest = lane % (2 * kVec);
-    int mine = at[0];
+    for (int u = 0; u < kU; ++u) {
+      int mine = -1;
 #pragma unroll
-    for (int k = 1; k < kPer; ++k) mine = sub == k ? at[k] : mine;
-    const long long sr = __shfl_sync(kAll, src, mine < 0 ? 0 : mine);
-    const long long ds = __shfl_sync(kAll, dst, mine < 0 ? 0 : mine);
-    if (mine >= 0 && sr >= 0) {
-      __half* pool = rest < kVec ? a.c.k : a.c.v;
-      const int piece = (rest % kVec) * 8;
-      *reinterpret_cast<uint4*>(pool + ds + piece) =
-          *reinterpret_cast<const uint4*>(pool + sr + piece);
+      for (int k = 0; k < kPer; ++k) {
+        if (sub == k && moved != 0) mine = __ffs(moved) - 1;
+        moved &= moved - 1;
+      }
+      const long long sr = __shfl_sync(kAll, src, mine < 0 ? 0 : mine);
+      const long long ds = __shfl_sync(kAll, dst, mine < 0 ? 0 : mine);
+      to[u] = mine >= 0 && sr >= 0 ? ds : -1;
+      if (to[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(pool + sr);
     }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (to[u] >= 0) *reinterpret_cast<uint4*>(pool + to[u]) = x[u];
   }
 }
 
 template <typename F, typename... Args>
-cudaError_t launch_pdl(F* k, long long blocks, int threads, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl(F* k, long long blocks, int threads, size_t smem, cudaStream_t st,
+                       Args... args) {
   if (blocks < 1 || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -239,17 +324,36 @@ cudaError_t launch_pdl(F* k, long long blocks, int threads, cudaStream_t st, Arg
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// Keys of up to this many entries stay in shared memory.
+constexpr long long kKeysMax = 51200;
+
+cudaError_t launch_select(const EvictArgs& a, long long heads, cudaStream_t st, int device) {
+  static std::atomic<unsigned long long> done{0};
+  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
+  if (cap > kKeysMax)
+    return launch_pdl(evict_select_kernel<false>, heads, kThreads, 0, st, a);
+  const unsigned long long bit = 1ull << (device & 63);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(evict_select_kernel<true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_pdl(evict_select_kernel<true>, heads, kThreads,
+                    static_cast<size_t>(cap) * 4, st, a);
+}
+
 }  // namespace
 
-cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
+cudaError_t cache_evict_launch(const EvictArgs& a, cudaStream_t st, int device) {
   const long long heads = static_cast<long long>(a.c.n_seqs) * a.c.n_kv;
-  cudaError_t e = launch_pdl(evict_select_kernel, heads, kThreads, st, a);
+  const cudaError_t e = launch_select(a, heads, st, device);
   if (e != cudaSuccess) return e;
   const int chunks = (a.keep + 31) / 32;
   const long long blocks = (heads * chunks + 3) / 4;
-  return a.c.head_dim == 64 ? launch_pdl(evict_move_kernel<64>, blocks, 128, st, a, chunks)
-                            : launch_pdl(evict_move_kernel<128>, blocks, 128, st, a, chunks);
+  return a.c.head_dim == 64 ? launch_pdl(evict_move_kernel<64>, blocks, 128, 0, st, a, chunks)
+                            : launch_pdl(evict_move_kernel<128>, blocks, 128, 0, st, a, chunks);
 }
 
 }  // namespace qgemv

@@ -82,7 +82,7 @@ struct EvictArgs {
 
 cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device);
-cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st);
+cudaError_t cache_evict_launch(const EvictArgs& a, cudaStream_t st, int device);
 
 // How a call's cache is split: n_parts parts of `part` entries (1: not split),
 // `cluster` of them joined on chip; what is left of them is joined through
