@@ -18,7 +18,10 @@ namespace qgemv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kUnroll = 4;  // heads of a lane group loaded before the first is processed
+// Blocks to a multiprocessor that the registers are cut for (measured with four
+// groups of heads a pass, 8205 tokens of 48 heads: 5 blocks 38.1, 6 39.7, 7 36.2, 8
+// 37.9, 10 47.2 us).
+constexpr int kBlocks = 7;
 
 // 1 / (2 pi) as a sum of two floats (48 bits).
 constexpr float kTurnHi = 0.15915494f;
@@ -31,6 +34,17 @@ __device__ __forceinline__ float turns(float x, float f) {
   const float t = p * kTurnHi;
   const float te = fmaf(p, kTurnHi, -t);
   return (t - rintf(t)) + (te + fmaf(p, kTurnLo, e * kTurnHi));
+}
+
+// Eight fp16 values as floats.
+__device__ __forceinline__ void unpack8(uint2 lo, uint2 hi, float* v) {
+  const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    v[2 * j] = p.x;
+    v[2 * j + 1] = p.y;
+  }
 }
 
 // Sequence that token t belongs to (the last one that starts at or before it),
@@ -50,11 +64,72 @@ __device__ __forceinline__ int find_seq(const int* q_start, int n_seqs, int t, i
   }
 }
 
-template <int HD, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopeArgs a, int per_warp,
+// One pass of a warp: U groups of heads, kLanes lanes each, loaded
+// together.  src, dst: this lane's head of the first group; heads: how many there are from
+// the first group's first head on.
+template <int HD, bool INTER, bool NORM, bool TURN, int U>
+__device__ __forceinline__ void heads_pass(const __half* src, __half* dst, int src_step, int dst_step,
+                                           int heads, int sub, int d0, int d1, const float* cg,
+                                           bool rot, float eps) {
+  constexpr int kLanes = HD / 8, kHeads = 32 / kLanes;
+  uint2 x[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    x[u][0] = x[u][1] = make_uint2(0u, 0u);
+    if (u * kHeads + sub < heads) {
+      x[u][0] = *reinterpret_cast<const uint2*>(src + u * src_step + d0);
+      x[u][1] = *reinterpret_cast<const uint2*>(src + u * src_step + d1);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u * kHeads >= heads) break;  // the same for the whole warp
+    uint2 y0 = x[u][0], y1 = x[u][1];
+    if (TURN) {
+      float v[8], w[8], r = 1.f;
+      unpack8(y0, y1, v);
+      if (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        r = rsqrtf(fmaf(ss, 1.0f / HD, eps));
+      }
+      // cg: gamma_a cos, gamma_b sin, gamma_b cos, gamma_a sin of each pair
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // pair j: half-split (v[j], v[4 + j]), interleaved (v[2j], v[2j + 1])
+        const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : 4 + j;
+        w[ia] = v[ia] * cg[4 * j] - v[ib] * cg[4 * j + 1];
+        w[ib] = v[ib] * cg[4 * j + 2] + v[ia] * cg[4 * j + 3];
+        if (!rot) {  // (0 times an infinity would not be nothing)
+          w[ia] = v[ia] * cg[4 * j];
+          w[ib] = v[ib] * cg[4 * j + 2];
+        }
+      }
+      if (NORM)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] *= r;
+      y0 = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
+      y1 = make_uint2(pack_f16(w[4], w[5]), pack_f16(w[6], w[7]));
+    }
+    if (u * kHeads + sub < heads) {
+      *reinterpret_cast<uint2*>(dst + u * dst_step + d0) = y0;
+      *reinterpret_cast<uint2*>(dst + u * dst_step + d1) = y1;
+    }
+  }
+}
+
+// A warp's task: one token, passes p0 .. p1 of its heads.  The passes of
+// a token are those of the queries, then the keys, then the values, each of
+// per_pass heads of one kind.
+template <int HD, bool INTER, bool NORM, int U>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_append_kernel(const RopeArgs a, int per_warp,
                                                                   int groups) {
-  constexpr int kLanes = HD / 8;            // lanes per head
-  constexpr int kHeads = 32 / kLanes;       // heads a warp holds at once
+  constexpr int kLanes = HD / 8;       // lanes per head
+  constexpr int kHeads = 32 / kLanes;  // heads a warp holds at once
+  constexpr int kPerPass = kHeads * U;
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long task = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -69,19 +144,20 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopeArgs
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       f[j] = a.inv_freq[INTER ? (j < 2 ? d0 / 2 + j : d1 / 2 + j - 2) : d0 + j];
-  uint2 gq[2] = {}, gk[2] = {};
-  if (a.q_norm != nullptr) {
-    gq[0] = *reinterpret_cast<const uint2*>(a.q_norm + d0);
-    gq[1] = *reinterpret_cast<const uint2*>(a.q_norm + d1);
-    gk[0] = *reinterpret_cast<const uint2*>(a.k_norm + d0);
-    gk[1] = *reinterpret_cast<const uint2*>(a.k_norm + d1);
+  uint2 g[2][2] = {};
+  if (NORM) {
+    g[0][0] = *reinterpret_cast<const uint2*>(a.q_norm + d0);
+    g[0][1] = *reinterpret_cast<const uint2*>(a.q_norm + d1);
+    g[1][0] = *reinterpret_cast<const uint2*>(a.k_norm + d0);
+    g[1][1] = *reinterpret_cast<const uint2*>(a.k_norm + d1);
   }
   pdl_wait();
   const int t = static_cast<int>(task / groups);
   if (t >= a.n_tokens) return;
-  const int heads = a.n_q + 2 * a.c.n_kv;
-  const int h0 = static_cast<int>(task % groups) * per_warp;
-  const int h1 = min(h0 + per_warp, heads);
+  const int n_kv = a.c.n_kv;
+  const int q_passes = (a.n_q + kPerPass - 1) / kPerPass, kv_passes = (n_kv + kPerPass - 1) / kPerPass;
+  const int p0 = static_cast<int>(task % groups) * per_warp;
+  const int p1 = min(p0 + per_warp, q_passes + 2 * kv_passes);
 
   const int pos = a.positions[t];
   const int s = find_seq(a.q_start, a.c.n_seqs, t, lane);
@@ -105,100 +181,61 @@ __global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(const RopeArgs
   }
 
   const __half* row = a.qkv + static_cast<long long>(t) * a.qkv_stride;
-  for (int hb = h0; hb < h1; hb += kHeads * kUnroll) {
-    uint2 x[kUnroll][2];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = hb + u * kHeads + sub;
-      x[u][0] = x[u][1] = make_uint2(0u, 0u);
-      if (h < h1) {
-        x[u][0] = *reinterpret_cast<const uint2*>(row + h * HD + d0);
-        x[u][1] = *reinterpret_cast<const uint2*>(row + h * HD + d1);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (hb + u * kHeads >= h1) break;  // the same for the whole warp
-      const int h = hb + u * kHeads + sub;
-      const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.c.n_kv;
-      float v[8];
+  const int page_size = 1 << a.c.page_shift;
+  float cg[16];
+  for (int p = p0; p < p1; ++p) {
+    const int kind = p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;  // query, key, value
+    const int pass = kind == 0 ? p : p - q_passes - (kind == 2 ? kv_passes : 0);
+    if (kind < 2 && (p == p0 || pass == 0)) {
+      float gm[8];
+      unpack8(kind == 0 ? g[0][0] : g[1][0], kind == 0 ? g[0][1] : g[1][1], gm);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t w = j < 2 ? (j == 0 ? x[u][0].x : x[u][0].y) : (j == 2 ? x[u][1].x : x[u][1].y);
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        v[2 * j] = p.x;
-        v[2 * j + 1] = p.y;
+        const float ga = NORM ? gm[INTER ? 2 * j : j] : 1.f;
+        const float gb = NORM ? gm[INTER ? 2 * j + 1 : 4 + j] : 1.f;
+        cg[4 * j] = ga * cs[j];
+        cg[4 * j + 1] = gb * sn[j];
+        cg[4 * j + 2] = gb * cs[j];
+        cg[4 * j + 3] = ga * sn[j];
       }
-      if (a.q_norm != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float r = 1.0f / sqrtf(ss * (1.0f / HD) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t wq = j < 2 ? (j == 0 ? gq[0].x : gq[0].y) : (j == 2 ? gq[1].x : gq[1].y);
-          const uint32_t wk = j < 2 ? (j == 0 ? gk[0].x : gk[0].y) : (j == 2 ? gk[1].x : gk[1].y);
-          const uint32_t w = is_q ? wq : wk;
-          const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w));
-          v[2 * j] *= r * g.x;
-          v[2 * j + 1] *= r * g.y;
-        }
-      }
-      if (h >= h1) continue;
-      uint2 y0, y1;
-      if (is_v) {
-        y0 = x[u][0];
-        y1 = x[u][1];
+    }
+    const int h = pass * kPerPass;  // first head of the pass, among its kind
+    if (kind == 0) {
+      heads_pass<HD, INTER, NORM, true, U>(
+          row + (h + sub) * HD, a.q_out + static_cast<long long>(t) * a.q_stride + (h + sub) * HD,
+          kHeads * HD, kHeads * HD, a.n_q - h, sub, d0, d1, cg, rot, a.eps);
+    } else if (page >= 0) {
+      const long long dst = cache_row(a.c, page, h + sub, at) * HD;
+      const __half* src = row + (a.n_q + (kind == 2 ? n_kv : 0) + h + sub) * HD;
+      const int step = kHeads * page_size * HD;
+      if (kind == 2) {
+        heads_pass<HD, INTER, NORM, false, U>(src, a.c.v + dst, kHeads * HD, step, n_kv - h, sub, d0, d1,
+                                           cg, rot, a.eps);
       } else {
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // pair j: half-split (v[j], v[4 + j]), interleaved (v[2j], v[2j + 1])
-          const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : 4 + j;
-          w[ia] = v[ia] * cs[j] - v[ib] * sn[j];
-          w[ib] = v[ib] * cs[j] + v[ia] * sn[j];
-        }
-        if (!rot)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = v[j];
-        y0 = make_uint2(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]));
-        y1 = make_uint2(pack_f16(w[4], w[5]), pack_f16(w[6], w[7]));
-      }
-      __half* dst;
-      if (is_q) {
-        dst = a.q_out + static_cast<long long>(t) * a.q_stride + h * HD;
-      } else {
-        if (page < 0) continue;
-        const int kh = h - a.n_q - (is_v ? a.c.n_kv : 0);
-        dst = (is_v ? a.c.v : a.c.k) + cache_row(a.c, page, kh, at) * HD;
-        if (!is_v && l == 0) {
-          const long long e = (static_cast<long long>(s) * a.c.n_kv + kh) *
+        heads_pass<HD, INTER, NORM, true, U>(src, a.c.k + dst, kHeads * HD, step, n_kv - h, sub, d0, d1,
+                                          cg, rot, a.eps);
+        const int n = min(kPerPass, n_kv - h);
+        if (lane < n) {
+          const long long e = (static_cast<long long>(s) * n_kv + h + lane) *
                                   (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + at;
           if (a.entry_pos != nullptr) a.entry_pos[e] = pos;
           if (a.entry_mass != nullptr) a.entry_mass[e] = 0.f;
         }
       }
-      *reinterpret_cast<uint2*>(dst + d0) = y0;
-      *reinterpret_cast<uint2*>(dst + d1) = y1;
     }
   }
 }
 
-template <int HD, bool INTER>
+template <int HD, bool INTER, bool NORM, int U>
 cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t st) {
-  constexpr int kHeads = 32 * 8 / HD;
-  const int heads = a.n_q + 2 * a.c.n_kv;
-  const int batch = kHeads * kUnroll;  // heads of one pass of a warp's loop
-  const int all = (heads + batch - 1) / batch;
-  // Passes per warp: all of a token's heads once there are enough tokens to
-  // fill the machine (48 warps a multiprocessor), else the heads are spread.
-  long long passes = static_cast<long long>(a.n_tokens) * all / (static_cast<long long>(sms) * 48);
-  if (passes > all) passes = all;
-  int per_warp = static_cast<int>(passes) * batch;
-  if (passes < 1) per_warp = kHeads;  // few tokens: one head per lane group
-  const int groups = (heads + per_warp - 1) / per_warp;
+  constexpr int kPerPass = 32 * 8 / HD * U;  // heads of one pass
+  const int all = (a.n_q + kPerPass - 1) / kPerPass + 2 * ((a.c.n_kv + kPerPass - 1) / kPerPass);
+  // As many warps to a token as fill the machine (28 warps a multiprocessor),
+  // down to one, which makes the token's sines once.
+  long long split = (28LL * sms + a.n_tokens - 1) / a.n_tokens;
+  if (split > all) split = all;
+  const int per_warp = static_cast<int>((all + split - 1) / split);
+  const int groups = (all + per_warp - 1) / per_warp;
   const long long blocks = (static_cast<long long>(a.n_tokens) * groups + kWarps - 1) / kWarps;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -210,15 +247,32 @@ cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel<HD, INTER>, a, per_warp, groups);
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<HD, INTER, NORM, U>, a, per_warp, groups);
+}
+
+template <int HD, bool INTER, bool NORM>
+cudaError_t launch_u(const RopeArgs& a, int sms, cudaStream_t st) {
+  // One group of heads a pass while all of them together are a few warps to a
+  // multiprocessor: a single token of 16/8 heads of 128 takes 2.5 us, with four
+  // groups a pass 3.4; 61 tokens of 32/8 heads 3.4 and 2.7.
+  constexpr int kHeads = 32 * 8 / HD;
+  const long long warps =
+      static_cast<long long>(a.n_tokens) * ((a.n_q + 2 * a.c.n_kv + kHeads - 1) / kHeads);
+  return warps <= 4LL * sms ? launch_t<HD, INTER, NORM, 1>(a, sms, st)
+                            : launch_t<HD, INTER, NORM, 4>(a, sms, st);
+}
+
+template <int HD>
+cudaError_t launch_hd(const RopeArgs& a, int sms, cudaStream_t st) {
+  if (a.q_norm != nullptr)
+    return a.interleaved ? launch_u<HD, true, true>(a, sms, st) : launch_u<HD, false, true>(a, sms, st);
+  return a.interleaved ? launch_u<HD, true, false>(a, sms, st) : launch_u<HD, false, false>(a, sms, st);
 }
 
 }  // namespace
 
 cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st) {
-  if (a.c.head_dim == 64)
-    return a.interleaved ? launch_t<64, true>(a, sms, st) : launch_t<64, false>(a, sms, st);
-  return a.interleaved ? launch_t<128, true>(a, sms, st) : launch_t<128, false>(a, sms, st);
+  return a.c.head_dim == 64 ? launch_hd<64>(a, sms, st) : launch_hd<128>(a, sms, st);
 }
 
 }  // namespace qgemv
