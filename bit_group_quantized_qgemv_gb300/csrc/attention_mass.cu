@@ -170,19 +170,48 @@ template <int HD>
 struct Shape {
   static constexpr int kHalves = HD / 64;
   static constexpr int kBytes = kBlock * HD * 2;
-  static constexpr int kSmem = 1024 + (2 + kSlots) * kBytes;
+  static constexpr int kSmem = 1024 + (4 + kSlots) * kBytes;
+  static_assert(kSmem + 1536 <= 227 * 1024, "dynamic and static shared memory");
   static constexpr uint32_t kDesc = tc::idesc_f16(kBlock, kBlock, false);
 };
 
 struct Bars {
-  uint64_t keys, q_full[kSlots], q_empty[kSlots], s_full[2][2], s_empty[2][2], l_full[2], l_empty[2],
-      drain;
+  uint64_t keys[2], k_empty[2], q_full[kSlots], q_empty[kSlots], s_full[2][2], s_empty[2][2],
+      l_full[2], l_empty[2], drain;
 };
 
+// A block's share: 256 entries of one head of one sequence.
+struct Share {
+  int s, h, e0, len, first, tokens, off, from, steps;
+};
+
+// Share number b; false if it lies behind its sequence's end.
+__device__ __forceinline__ bool get_share(const MassArgs& a, long long b, int per_head,
+                                          int step_tokens, Share* w) {
+  w->e0 = static_cast<int>(b % per_head) * 2 * kBlock;
+  b /= per_head;
+  w->h = static_cast<int>(b % a.c.n_kv);
+  w->s = static_cast<int>(b / a.c.n_kv);
+  w->len = seq_len(a.c, w->s, a.err);
+  if (w->e0 >= w->len) return false;
+  int count;
+  seq_rows(a.q_start, w->s, a.n_tokens, a.err, &w->first, &count);
+  if (count > a.max_q) flag_error(a.err);
+  w->tokens = min(count, a.max_q);
+  w->off = w->len - count;
+  // steps of step_tokens tokens, from the one whose last token sees entry e0
+  w->from = max(0, w->e0 - w->off) / step_tokens;
+  w->steps = max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from);
+  return true;
+}
+
+// One block per multiprocessor, each taking every gridDim.x-th share.  The
+// roles walk the shares on their own, the producer ahead of the others (two
+// buffers of keys), so that a share's start hides behind the one before it.
 template <int HD>
 __global__ void __launch_bounds__(kManyThreads, 1)
     mass_many_kernel(const MassArgs a, const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap q_map, int blocks_per_head, int step_tokens) {
+                     const __grid_constant__ CUtensorMap q_map, int per_head, int step_tokens) {
   using Sh = Shape<HD>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
@@ -191,10 +220,13 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ __align__(16) float s_lse[2][kBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  uint8_t* qring = base + 2 * Sh::kBytes;
+  uint8_t* qring = base + 4 * Sh::kBytes;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bars.keys), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&bars.keys[x]), 1);
+      mbar_init(smem_u32(&bars.k_empty[x]), 1);
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&bars.q_full[i]), 1);
       mbar_init(smem_u32(&bars.q_empty[i]), 1);
@@ -211,168 +243,197 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     fence_mbar_init();
     s_failed = 0;
   }
-  pdl_wait();
-  long long b = blockIdx.x;
-  const int e0 = static_cast<int>(b % blocks_per_head) * 2 * kBlock;
-  b /= blocks_per_head;
-  const int h = static_cast<int>(b % a.c.n_kv), s = static_cast<int>(b / a.c.n_kv);
-  const int len = seq_len(a.c, s, a.err);
-  int first, count;
-  seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
-  if (count > a.max_q) flag_error(a.err);
-  if (e0 >= len) return;
-  const int tokens = min(count, a.max_q), off = len - count;
-  // steps of step_tokens tokens, from the one whose last token sees entry e0
-  const int from = max(0, e0 - off) / step_tokens;
-  const int steps = max(0, (tokens + step_tokens - 1) / step_tokens - from);
-  const int tiles = e0 + kBlock < len ? 2 : 1;
   if (warp == 8) tc::alloc(smem_u32(&s_tmem), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  pdl_wait();
   const uint32_t tmem = s_tmem;
+  const long long shares = static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs;
+  Share w;
 
   if (warp == 9) {
     // ---------------------------------------------------------- producer
-    int issued = 0;
-    if (steps > 0) {
-      const int page_rows = min(1 << a.c.page_shift, kBlock), boxes = kBlock / page_rows;
-      const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.keys), 2 * Sh::kBytes);
+    const int page_rows = min(1 << a.c.page_shift, kBlock), boxes = kBlock / page_rows;
+    const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;
+    // queries: [token][head of the group] rows of 128 bytes
+    const uint32_t bytes = static_cast<uint32_t>(step_tokens * a.group * HD * 2);
+    int kb = 0, g = 0;
+    bool ok = true;
+    for (long long b = blockIdx.x; b < shares && ok; b += gridDim.x) {
+      if (!get_share(a, b, per_head, step_tokens, &w) || w.steps == 0) continue;
+      const int kd = kb & 1;
+      if (kb > 1) ok = warp_wait(smem_u32(&bars.k_empty[kd]), (kb / 2 - 1) & 1, &g_status);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.keys[kd]), 2 * Sh::kBytes);
       __syncwarp();
       if (lane < 2 * boxes) {
-        const int x = lane / boxes, e = e0 + lane * page_rows;
-        const int p = e < len ? page_of(a.c, s, e, a.err) : -1;
-        const int row = p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
+        const int x = lane / boxes, e = w.e0 + lane * page_rows;
+        const int p = e < w.len ? page_of(a.c, w.s, e, a.err) : -1;
+        const int row = p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, w.h, e));
         const uint32_t dst =
-            smem_u32(base + x * Sh::kBytes) + (lane % boxes) * page_rows * 128;
+            smem_u32(base + (2 * kd + x) * Sh::kBytes) + (lane % boxes) * page_rows * 128;
 #pragma unroll
         for (int c = 0; c < Sh::kHalves; ++c)
-          tc::tma_2d(dst + c * (kBlock * 128), &k_map, c * 64, row, smem_u32(&bars.keys));
+          tc::tma_2d(dst + c * (kBlock * 128), &k_map, c * 64, row, smem_u32(&bars.keys[kd]));
       }
       __syncwarp();
-      // queries: [token][head of the group] rows of 128 bytes
-      const uint32_t bytes = static_cast<uint32_t>(step_tokens * a.group * HD * 2);
-      for (int j = 0; j < steps; ++j) {
-        const int slot = j % kSlots, use = j / kSlots;
-        if (use > 0 && !warp_wait(smem_u32(&bars.q_empty[slot]), (use - 1) & 1, &g_status)) break;
+      ++kb;
+      for (int j = 0; j < w.steps; ++j) {
+        const int slot = g % kSlots, use = g / kSlots;
+        if (use > 0) ok = warp_wait(smem_u32(&bars.q_empty[slot]), (use - 1) & 1, &g_status);
+        if (!ok) break;
         if (lane == 0) {
           const uint32_t full = smem_u32(&bars.q_full[slot]);
           mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
           for (int c = 0; c < Sh::kHalves; ++c)
             tc::tma_3d(smem_u32(qring + slot * Sh::kBytes) + c * (kBlock * 128), &q_map, c * 64,
-                       h * a.group, first + (from + j) * step_tokens, full);
+                       w.h * a.group, w.first + (w.from + j) * step_tokens, full);
         }
         __syncwarp();
-        issued = j + 1;
+        ++g;
       }
-      // no copy may be in flight when the block ends
-      warp_wait(smem_u32(&bars.keys), 0, &g_status);
-      for (int j = max(0, issued - kSlots); j < issued; ++j)
-        warp_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
     }
+    // no copy may be in flight when the block ends
+    for (int k = max(0, kb - 2); k < kb; ++k)
+      warp_wait(smem_u32(&bars.keys[k & 1]), (k / 2) & 1, &g_status);
+    for (int j = max(0, g - kSlots); j < g; ++j)
+      warp_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
   } else if (warp == 10) {
     // ------------------------------------------------- lse of each step's rows
     // (a row outside the sequence, or one that saw nothing: +inf, weight 0)
-    for (int j = 0; j < steps; ++j) {
-      const int d = j & 1;
-      float v[kBlock / 32];
+    int g = 0;
+    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
+      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      for (int j = 0; j < w.steps; ++j, ++g) {
+        const int d = g & 1;
+        float v[kBlock / 32];
 #pragma unroll
-      for (int k = 0; k < kBlock / 32; ++k) {
-        const int c = lane + 32 * k, t = (from + j) * step_tokens + c / a.group;
-        v[k] = INFINITY;
-        if (c < step_tokens * a.group && t < tokens) {
-          const float x =
-              a.lse[static_cast<long long>(first + t) * a.n_q + h * a.group + c % a.group];
-          if (x != -INFINITY) v[k] = x * kLog2e;
+        for (int k = 0; k < kBlock / 32; ++k) {
+          const int c = lane + 32 * k, t = (w.from + j) * step_tokens + c / a.group;
+          v[k] = INFINITY;
+          if (c < step_tokens * a.group && t < w.tokens) {
+            const float x =
+                a.lse[static_cast<long long>(w.first + t) * a.n_q + w.h * a.group + c % a.group];
+            if (x != -INFINITY) v[k] = x * kLog2e;
+          }
         }
-      }
-      if (j > 1 && !warp_wait(smem_u32(&bars.l_empty[d]), (j / 2 - 1) & 1, &g_status)) break;
+        if (g > 1) step_wait(smem_u32(&bars.l_empty[d]), (g / 2 - 1) & 1, &s_failed, &g_status);
 #pragma unroll
-      for (int k = 0; k < kBlock / 32; ++k) s_lse[d][lane + 32 * k] = v[k];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.l_full[d]));
+        for (int k = 0; k < kBlock / 32; ++k) s_lse[d][lane + 32 * k] = v[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.l_full[d]));
+      }
     }
   } else if (warp == 8) {
     // ---------------------------------------------------------- products
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
-    const int n_steps = tc::uniform(steps), n_tiles = tc::uniform(tiles);
-    if (n_steps > 0) step_wait(smem_u32(&bars.keys), 0, &s_failed, &g_status);
-    for (int j = 0; j < n_steps; ++j) {
-      const int slot = j % kSlots, d = j & 1;
-      step_wait(smem_u32(&bars.q_full[slot]), (j / kSlots) & 1, &s_failed, &g_status);
-      for (int x = 0; x < n_tiles; ++x) {
-        if (j > 1) step_wait(smem_u32(&bars.s_empty[x][d]), (j / 2 - 1) & 1, &s_failed, &g_status);
-        tc::fence_after();
-        if (tc::elect_one()) {
-          const uint64_t k = tc::desc_k_major(smem_u32(base + x * Sh::kBytes));
-          const uint64_t q = tc::desc_k_major(smem_u32(qring + slot * Sh::kBytes));
+    int kb = 0, g = 0;
+    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
+      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      const int n_steps = tc::uniform(w.steps);
+      if (n_steps == 0) continue;
+      const int kd = kb & 1;
+      step_wait(smem_u32(&bars.keys[kd]), (kb / 2) & 1, &s_failed, &g_status);
+      ++kb;
+      for (int j = 0; j < n_steps; ++j, ++g) {
+        const int slot = g % kSlots, d = g & 1;
+        step_wait(smem_u32(&bars.q_full[slot]), (g / kSlots) & 1, &s_failed, &g_status);
 #pragma unroll
-          for (int i = 0; i < HD / 16; ++i) {
-            const int step = (i / 4) * (kBlock * 128) + (i % 4) * 32;
-            tc::mma_ss(tm + (2 * x + d) * kBlock, k + (step >> 4), q + (step >> 4), Sh::kDesc,
-                       i > 0);
+        for (int x = 0; x < 2; ++x) {
+          if (g > 1)
+            step_wait(smem_u32(&bars.s_empty[x][d]), (g / 2 - 1) & 1, &s_failed, &g_status);
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t k = tc::desc_k_major(smem_u32(base + (2 * kd + x) * Sh::kBytes));
+            const uint64_t q = tc::desc_k_major(smem_u32(qring + slot * Sh::kBytes));
+#pragma unroll
+            for (int i = 0; i < HD / 16; ++i) {
+              const int step = (i / 4) * (kBlock * 128) + (i % 4) * 32;
+              tc::mma_ss(tm + (2 * x + d) * kBlock, k + (step >> 4), q + (step >> 4), Sh::kDesc,
+                         i > 0);
+            }
+            tc::commit(smem_u32(&bars.s_full[x][d]));
           }
-          tc::commit(smem_u32(&bars.s_full[x][d]));
+          __syncwarp();
+        }
+        if (tc::elect_one()) {
+          tc::commit(smem_u32(&bars.q_empty[slot]));
+          if (j == n_steps - 1) tc::commit(smem_u32(&bars.k_empty[kd]));
         }
         __syncwarp();
       }
-      if (tc::elect_one()) tc::commit(smem_u32(&bars.q_empty[slot]));
-      __syncwarp();
     }
     if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
     __syncwarp();
     warp_wait(smem_u32(&bars.drain), 0, &g_status);
   } else if (warp < 8) {
     // -------------------------------------------------------------- sums
-    const int x = warp >> 2, e = e0 + x * kBlock + (warp & 3) * 32 + lane;
-    const bool live = e < len;
-    const int page = live ? page_of(a.c, s, e, nullptr) : -1;
-    const long long at = (static_cast<long long>(s) * a.c.n_kv + h) *
-                             (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + e;
-    const float before = live && a.mass != nullptr ? a.mass[at] : 0.f;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int x = warp >> 2;
     const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
-    for (int j = 0; j < steps; ++j) {
-      const int d = j & 1;
-      step_wait(smem_u32(&bars.l_full[d]), (j / 2) & 1, &s_failed, &g_status);
-      if (x < tiles) {
-        step_wait(smem_u32(&bars.s_full[x][d]), (j / 2) & 1, &s_failed, &g_status);
+    int g = 0;
+    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
+      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      const int e = w.e0 + x * kBlock + (warp & 3) * 32 + lane;
+      const bool live = e < w.len;
+      const int page = live ? raw_page(a.c, w.s, e) : 0;
+      const long long at = (static_cast<long long>(w.s) * a.c.n_kv + w.h) *
+                               (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + e;
+      const float before = live && a.mass != nullptr ? a.mass[at] : 0.f;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < w.steps; ++j, ++g) {
+        const int d = g & 1;
+        step_wait(smem_u32(&bars.l_full[d]), (g / 2) & 1, &s_failed, &g_status);
+        step_wait(smem_u32(&bars.s_full[x][d]), (g / 2) & 1, &s_failed, &g_status);
         tc::fence_after();
         // columns before `seen` are rows that lie before this entry, those from
         // `end` on belong to no token of the sequence (and may hold anything)
-        const int t0 = (from + j) * step_tokens;
-        const int seen = (e - off - t0) * a.group;
-        const int end = min(step_tokens, tokens - t0) * a.group;
+        const int t0 = (w.from + j) * step_tokens;
+        const int seen = (e - w.off - t0) * a.group;
+        const int end = min(step_tokens, w.tokens - t0) * a.group;
         const bool all = __all_sync(0xFFFFFFFFu, seen <= 0) && end == kBlock;
+        uint32_t v[2][32];
+        tc::ld32(v[0], lanes + d * kBlock);
+        tc::wait_ld32(v[0]);
+        const float* ls = s_lse[d];
+        if (all) {
 #pragma unroll
-        for (int c = 0; c < kBlock; c += 32) {
-          uint32_t v[32];
-          tc::ld32(v, lanes + d * kBlock + c);
-          tc::wait_ld32(v);
+          for (int c = 0; c < 4; ++c) {  // the next 32 columns load while these are summed
+            if (c < 3) tc::ld32(v[(c + 1) & 1], lanes + d * kBlock + 32 * (c + 1));
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(&s_lse[d][c + k]);
-            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * c + k);
+              const float l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = ex2(fmaf(__uint_as_float(v[k + i]), a.scale_log2, -l[i]));
-              if (all)
-                sum[i] += w;
-              else
-                sum[i] += c + k + i >= seen && c + k + i < end ? w : 0.f;
+              for (int i = 0; i < 4; ++i)
+                sum[i] += ex2(fmaf(__uint_as_float(v[c & 1][k + i]), a.scale_log2, -l[i]));
             }
+            if (c < 3) tc::wait_ld32(v[(c + 1) & 1]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c < 3) tc::ld32(v[(c + 1) & 1], lanes + d * kBlock + 32 * (c + 1));
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float y = ex2(fmaf(__uint_as_float(v[c & 1][k]), a.scale_log2, -ls[32 * c + k]));
+              sum[k & 3] += 32 * c + k >= seen && 32 * c + k < end ? y : 0.f;
+            }
+            if (c < 3) tc::wait_ld32(v[(c + 1) & 1]);
           }
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.s_empty[x][d]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.s_empty[x][d]));
+          mbar_arrive(smem_u32(&bars.l_empty[d]));
+        }
       }
-      if (lane == 0) mbar_arrive(smem_u32(&bars.l_empty[d]));
+      if (live && *static_cast<volatile int*>(&s_failed) == 0)
+        a.mass_out[at] = before + (good_page(a.c, page, nullptr) >= 0
+                                       ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f);
     }
-    if (live && *static_cast<volatile int*>(&s_failed) == 0)
-      a.mass_out[at] = before + (page >= 0 ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f);
   }
   tc::fence_before();
   __syncthreads();
@@ -422,7 +483,7 @@ cudaError_t launch_few(const MassArgs& a, int sms, cudaStream_t st, int device) 
 }
 
 template <int HD>
-cudaError_t launch_many(const MassArgs& a, cudaStream_t st, int device) {
+cudaError_t launch_many(const MassArgs& a, int sms, cudaStream_t st, int device) {
   static std::atomic<unsigned long long> done{0};
   const EncodeTiledFn fn = encode_fn();
   CUtensorMap km, qm;
@@ -441,15 +502,15 @@ cudaError_t launch_many(const MassArgs& a, cudaStream_t st, int device) {
     return cudaErrorInvalidValue;
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   const int per_head = static_cast<int>((cap + 2 * kBlock - 1) / (2 * kBlock));
-  return launch(mass_many_kernel<HD>, &done, static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs,
-                kManyThreads, Shape<HD>::kSmem, st, device, a, km, qm, per_head, step_tokens);
+  const long long shares = static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs;
+  return launch(mass_many_kernel<HD>, &done, shares < sms ? shares : sms, kManyThreads, Shape<HD>::kSmem, st, device, a, km, qm, per_head, step_tokens);
 }
 
 template <int HD>
 cudaError_t launch_t(const MassArgs& a, int sms, cudaStream_t st, int device) {
   const long long rows = static_cast<long long>(a.max_q) * a.group;
   // (a group of more than 128 heads has no box of whole tokens)
-  if (rows > kRowsMax && a.group <= kBlock && a.n_tokens > 0) return launch_many<HD>(a, st, device);
+  if (rows > kRowsMax && a.group <= kBlock && a.n_tokens > 0) return launch_many<HD>(a, sms, st, device);
   if (rows <= 8) return launch_few<HD, 1>(a, sms, st, device);
   if (rows <= 16) return launch_few<HD, 2>(a, sms, st, device);
   return launch_few<HD, 4>(a, sms, st, device);
