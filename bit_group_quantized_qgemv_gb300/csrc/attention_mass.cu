@@ -303,27 +303,38 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else if (warp == 10) {
     // ------------------------------------------------- lse of each step's rows
     // (a row outside the sequence, or one that saw nothing: +inf, weight 0)
+    // The values of a step are loaded a step ahead.
+    constexpr int kOwn = kBlock / 32;
+    int row_t[kOwn], row_h[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+      const int c = lane + 32 * k;
+      row_t[k] = c < step_tokens * a.group ? c / a.group : 1 << 28;
+      row_h[k] = c % a.group;
+    }
     int g = 0;
     for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
       if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      float v[kOwn];
+      auto load = [&](int j) {
+        const int t0 = (w.from + j) * step_tokens;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+          v[k] = t0 + row_t[k] < w.tokens
+                     ? a.lse[static_cast<long long>(w.first + t0 + row_t[k]) * a.n_q +
+                             w.h * a.group + row_h[k]]
+                     : -INFINITY;
+      };
+      if (w.steps > 0) load(0);
       for (int j = 0; j < w.steps; ++j, ++g) {
         const int d = g & 1;
-        float v[kBlock / 32];
-#pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) {
-          const int c = lane + 32 * k, t = (w.from + j) * step_tokens + c / a.group;
-          v[k] = INFINITY;
-          if (c < step_tokens * a.group && t < w.tokens) {
-            const float x =
-                a.lse[static_cast<long long>(w.first + t) * a.n_q + w.h * a.group + c % a.group];
-            if (x != -INFINITY) v[k] = x * kLog2e;
-          }
-        }
         if (g > 1) step_wait(smem_u32(&bars.l_empty[d]), (g / 2 - 1) & 1, &s_failed, &g_status);
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) s_lse[d][lane + 32 * k] = v[k];
+        for (int k = 0; k < kOwn; ++k)
+          s_lse[d][lane + 32 * k] = v[k] != -INFINITY ? v[k] * kLog2e : INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.l_full[d]));
+        if (j + 1 < w.steps) load(j + 1);
       }
     }
   } else if (warp == 8) {
