@@ -129,7 +129,7 @@ def _cuda(t, dtypes, name):
 
 _CODES = (torch.int32, getattr(torch, "uint32", torch.int32))
 _F16 = (torch.float16,)
-_I32 = (torch.int32,)
+_HALF, _F32, _I32 = torch.float16, torch.float32, torch.int32
 
 
 def _weight(w, name):
@@ -510,8 +510,8 @@ class KVCache:
 
     def __init__(self, k, v, page_table, kv_len):
         self.k, self.v = _cuda(k, _F16, "k"), _cuda(v, _F16, "v")
-        self.page_table = _cuda(page_table, _I32, "page_table")
-        self.kv_len = _cuda(kv_len, _I32, "kv_len")
+        self.page_table = _cuda(page_table, (_I32,), "page_table")
+        self.kv_len = _cuda(kv_len, (_I32,), "kv_len")
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must both be [n_pages][n_kv][page_size][head_dim]")
         if page_table.dim() != 2 or kv_len.shape != page_table.shape[:1]:
@@ -541,24 +541,23 @@ def kv_cache(k, v, page_table, kv_len) -> KVCache:
     return KVCache(k, v, page_table, kv_len)
 
 
-# The current stream's handle of a device, without making a Stream object.
+# The current device, and a device's current stream, without making objects.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(cache, stream, body):
-    """body(stream handle) with the cache's device current; what it allocates
-    belongs to the stream its kernels run on."""
-    index = cache.index
+def _elsewhere(call, cache, stream, *args):
+    """A call for another stream or device than the current ones: again with
+    them current, so that its kernels run there and what it allocates belongs
+    to the stream they run on."""
     if stream is None:
-        if torch.cuda.current_device() == index:
-            return body(_raw_stream(index))
-        with torch.cuda.device(index):
-            return body(_raw_stream(index))
+        with torch.cuda.device(cache.index):
+            return call(cache, *args)
     if stream.device != cache.device:
         raise ValueError(f"stream is on {stream.device}, the cache on {cache.device}")
     with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+        return call(cache, *args)
 
 
 def _at(cache, t, dtype, name, shape=None):
@@ -612,37 +611,36 @@ def qk_norm_rope_append(cache, qkv, q_start, positions, inv_freq=None, interleav
     keys in qkv [tokens][(n_q + 2 n_kv) head_dim], keys and values into the
     cache.  inv_freq: fp32 [rotary_dim / 2], None for no rotation.  Returns
     q_out [tokens][n_q head_dim]."""
+    if stream is not None or _current_device() != cache.index:
+        return _elsewhere(qk_norm_rope_append, cache, stream, qkv, q_start, positions, inv_freq,
+                          interleaved, q_norm, k_norm, eps, q_out, entry_pos, entry_mass, err_flag)
     x, T, width, stride = _token_rows(cache, qkv, "qkv")
     hd = cache.head_dim
     n_q = _heads(cache, width, 2 * cache.n_kv, "qkv")
-
-    def body(st):
-        y = q_out
-        if y is None:
-            y = torch.empty(T, n_q * hd, dtype=torch.float16, device=cache.device)
-        yp, _, _, y_stride = _token_rows(cache, y, "q_out", T, n_q * hd)
-        _check(lib.qgemv_qk_norm_rope_append(
-            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
-            _at(cache, positions, torch.int32, "positions", (T,)),
-            _at(cache, inv_freq, torch.float32, "inv_freq"),
-            0 if inv_freq is None else 2 * inv_freq.numel(), bool(interleaved),
-            _at(cache, q_norm, torch.float16, "q_norm", (hd,)),
-            _at(cache, k_norm, torch.float16, "k_norm", (hd,)), eps, yp, y_stride,
-            _at(cache, entry_pos, torch.int32, "entry_pos", cache.entries),
-            _at(cache, entry_mass, torch.float32, "entry_mass", cache.entries),
-            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_qk_norm_rope_append")
-        return y
-
-    return _on(cache, stream, body)
+    if q_out is None:
+        q_out = torch.empty(T, n_q * hd, dtype=torch.float16, device=cache.device)
+    y, _, _, y_stride = _token_rows(cache, q_out, "q_out", T, n_q * hd)
+    rc = lib.qgemv_qk_norm_rope_append(
+        cache.ref, x, stride, T, n_q, _at(cache, q_start, _I32, "q_start", cache.starts),
+        _at(cache, positions, _I32, "positions", (T,)), _at(cache, inv_freq, _F32, "inv_freq"),
+        0 if inv_freq is None else 2 * inv_freq.numel(), interleaved,
+        _at(cache, q_norm, _HALF, "q_norm", (hd,)), _at(cache, k_norm, _HALF, "k_norm", (hd,)), eps,
+        y, y_stride, _at(cache, entry_pos, _I32, "entry_pos", cache.entries),
+        _at(cache, entry_mass, _F32, "entry_mass", cache.entries),
+        _at(cache, err_flag, _I32, "err_flag"), _raw_stream(cache.index))
+    if rc:
+        _check(rc, "qgemv_qk_norm_rope_append")
+    return q_out
 
 
 def paged_attention_workspace_bytes(cache, n_tokens, n_q, max_q) -> int:
     """Workspace with which paged_attention is fastest for these sizes."""
+    if _current_device() != cache.index:
+        return _elsewhere(paged_attention_workspace_bytes, cache, None, n_tokens, n_q, max_q)
     key = (int(n_tokens), int(n_q), int(max_q))
     n = cache.workspace_sizes.get(key)
     if n is None:
-        n = _on(cache, None, lambda st: int(
-            lib.qgemv_paged_attention_workspace_bytes(cache.ref, *key)))
+        n = int(lib.qgemv_paged_attention_workspace_bytes(cache.ref, *key))
         if len(cache.workspace_sizes) >= 1024:
             cache.workspace_sizes.clear()
         cache.workspace_sizes[key] = n
@@ -655,33 +653,33 @@ def paged_attention(cache, q, q_start, max_q=None, scale=None, out=None, want_ls
     its cache; q [tokens][n_q head_dim].  max_q: the largest number of new
     tokens in a sequence (default: all).  scale: default head_dim ** -0.5.
     Returns (out, lse fp32 [tokens][n_q] or None)."""
+    if stream is not None or _current_device() != cache.index:
+        return _elsewhere(paged_attention, cache, stream, q, q_start, max_q, scale, out, want_lse,
+                          lse, workspace, err_flag)
     x, T, width, stride = _token_rows(cache, q, "q")
     n_q = _heads(cache, width, 0, "q")
     max_q = max(T, 1) if max_q is None else int(max_q)
-
-    def body(st):
-        y, z, ws = out, lse, workspace
-        if y is None:
-            y = torch.empty(T, width, dtype=torch.float16, device=cache.device)
-        yp, _, _, y_stride = _token_rows(cache, y, "out", T, width)
-        if z is None and want_lse:
-            z = torch.empty(T, n_q, dtype=torch.float32, device=cache.device)
-        if ws is None:
-            n = paged_attention_workspace_bytes(cache, T, n_q, max_q)
-            if n:
-                ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
-        else:
-            if ws.get_device() != cache.index or not ws.is_contiguous():
-                raise ValueError("workspace must be contiguous, on the cache's device")
-            n = ws.numel() * ws.element_size()
-        _check(lib.qgemv_paged_attention(
-            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
-            max_q, cache.scale if scale is None else scale, yp, y_stride,
-            _at(cache, z, torch.float32, "lse", (T, n_q)), ws.data_ptr() if n else None, n,
-            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_paged_attention")
-        return y, z
-
-    return _on(cache, stream, body)
+    if out is None:
+        out = torch.empty(T, width, dtype=torch.float16, device=cache.device)
+    y, _, _, y_stride = _token_rows(cache, out, "out", T, width)
+    if lse is None and want_lse:
+        lse = torch.empty(T, n_q, dtype=torch.float32, device=cache.device)
+    if workspace is None:
+        n = paged_attention_workspace_bytes(cache, T, n_q, max_q)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    else:
+        if workspace.get_device() != cache.index or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the cache's device")
+        n = workspace.numel() * workspace.element_size()
+    rc = lib.qgemv_paged_attention(
+        cache.ref, x, stride, T, n_q, _at(cache, q_start, _I32, "q_start", cache.starts), max_q,
+        cache.scale if scale is None else scale, y, y_stride, _at(cache, lse, _F32, "lse", (T, n_q)),
+        workspace.data_ptr() if n else None, n, _at(cache, err_flag, _I32, "err_flag"),
+        _raw_stream(cache.index))
+    if rc:
+        _check(rc, "qgemv_paged_attention")
+    return out, lse
 
 
 def attention_mass(cache, q, q_start, lse, max_q=None, scale=None, mass=None, mass_out=None,
@@ -690,24 +688,22 @@ def attention_mass(cache, q, q_start, lse, max_q=None, scale=None, mass=None, ma
     the attention weight every cached entry receives from the new tokens; q
     and lse as paged_attention took and gave them.  Returns mass_out (a new
     array is zero behind each sequence's length; it may be mass itself)."""
+    if stream is not None or _current_device() != cache.index:
+        return _elsewhere(attention_mass, cache, stream, q, q_start, lse, max_q, scale, mass,
+                          mass_out, err_flag)
     x, T, width, stride = _token_rows(cache, q, "q")
     n_q = _heads(cache, width, 0, "q")
-    max_q = max(T, 1) if max_q is None else int(max_q)
-
-    def body(st):
-        y = mass_out
-        if y is None:
-            y = torch.zeros(cache.entries, dtype=torch.float32, device=cache.device)
-        _check(lib.qgemv_attention_mass(
-            cache.ref, x, stride, T, n_q, _at(cache, q_start, torch.int32, "q_start", cache.starts),
-            max_q, cache.scale if scale is None else scale,
-            _at(cache, lse, torch.float32, "lse", (T, n_q)),
-            _at(cache, mass, torch.float32, "mass", cache.entries),
-            _at(cache, y, torch.float32, "mass_out", cache.entries),
-            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_attention_mass")
-        return y
-
-    return _on(cache, stream, body)
+    if mass_out is None:
+        mass_out = torch.zeros(cache.entries, dtype=torch.float32, device=cache.device)
+    rc = lib.qgemv_attention_mass(
+        cache.ref, x, stride, T, n_q, _at(cache, q_start, _I32, "q_start", cache.starts),
+        max(T, 1) if max_q is None else int(max_q), cache.scale if scale is None else scale,
+        _at(cache, lse, _F32, "lse", (T, n_q)), _at(cache, mass, _F32, "mass", cache.entries),
+        _at(cache, mass_out, _F32, "mass_out", cache.entries),
+        _at(cache, err_flag, _I32, "err_flag"), _raw_stream(cache.index))
+    if rc:
+        _check(rc, "qgemv_attention_mass")
+    return mass_out
 
 
 def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, kept=None,
@@ -717,31 +713,30 @@ def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, ke
     head for itself; rows of the cache move in place.  Returns (kept int32
     [n_seqs][n_kv][keep], mass_out, pos_out, kv_len_out); kv_len_out is the new
     length, to be written into the cache's kv_len before the next call."""
-    keep = int(keep)
-    S, dev = cache.n_seqs, cache.device
-
-    def body(st):
-        k, m, p, n = kept, mass_out, pos_out, kv_len_out
-        if k is None:
-            k = torch.empty(S, cache.n_kv, max(keep, 0), dtype=torch.int32, device=dev)
-        if m is None:
-            m = torch.zeros(cache.entries, dtype=torch.float32, device=dev)
-        if p is None:
-            p = torch.zeros(cache.entries, dtype=torch.int32, device=dev)
-        if n is None:
-            n = torch.empty(S, dtype=torch.int32, device=dev)
-        _check(lib.qgemv_cache_evict(
-            cache.ref, _at(cache, mass, torch.float32, "mass", cache.entries),
-            _at(cache, entry_pos, torch.int32, "entry_pos", cache.entries),
-            _at(cache, next_pos, torch.int32, "next_pos", (S,)), keep, int(n_sink), int(n_recent),
-            _at(cache, k, torch.int32, "kept", (S, cache.n_kv, max(keep, 0))),
-            _at(cache, m, torch.float32, "mass_out", cache.entries),
-            _at(cache, p, torch.int32, "pos_out", cache.entries),
-            _at(cache, n, torch.int32, "kv_len_out", (S,)),
-            _at(cache, err_flag, torch.int32, "err_flag"), st), "qgemv_cache_evict")
-        return k, m, p, n
-
-    return _on(cache, stream, body)
+    if stream is not None or _current_device() != cache.index:
+        return _elsewhere(cache_evict, cache, stream, mass, entry_pos, next_pos, keep, n_sink,
+                          n_recent, kept, mass_out, pos_out, kv_len_out, err_flag)
+    keep, S, dev = int(keep), cache.n_seqs, cache.device
+    if kept is None:
+        kept = torch.empty(S, cache.n_kv, max(keep, 0), dtype=torch.int32, device=dev)
+    if mass_out is None:
+        mass_out = torch.zeros(cache.entries, dtype=torch.float32, device=dev)
+    if pos_out is None:
+        pos_out = torch.zeros(cache.entries, dtype=torch.int32, device=dev)
+    if kv_len_out is None:
+        kv_len_out = torch.empty(S, dtype=torch.int32, device=dev)
+    rc = lib.qgemv_cache_evict(
+        cache.ref, _at(cache, mass, _F32, "mass", cache.entries),
+        _at(cache, entry_pos, _I32, "entry_pos", cache.entries),
+        _at(cache, next_pos, _I32, "next_pos", (S,)), keep, int(n_sink), int(n_recent),
+        _at(cache, kept, _I32, "kept", (S, cache.n_kv, max(keep, 0))),
+        _at(cache, mass_out, _F32, "mass_out", cache.entries),
+        _at(cache, pos_out, _I32, "pos_out", cache.entries),
+        _at(cache, kv_len_out, _I32, "kv_len_out", (S,)), _at(cache, err_flag, _I32, "err_flag"),
+        _raw_stream(cache.index))
+    if rc:
+        _check(rc, "qgemv_cache_evict")
+    return kept, mass_out, pos_out, kv_len_out
 
 
 def device_status() -> int:

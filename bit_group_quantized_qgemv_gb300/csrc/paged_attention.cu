@@ -484,10 +484,11 @@ cudaError_t launch_few(AttnArgs a, cudaStream_t st, int device) {
 }
 
 // Warps per block: eight where the clusters leave a multiprocessor to each
-// block (at most 19 units x 8 blocks), four, two blocks to a multiprocessor,
+// block (8 units of 8 blocks; 16 do not fit next to one another: 10.4 us
+// against 6.9 for two sequences of 500), four, two blocks to a multiprocessor,
 // elsewhere.
 int few_warps(int rows, int cluster, int units) {
-  return cluster > 1 && units <= 19 && rows <= 16 ? 8 : 4;
+  return cluster > 1 && units <= 8 && rows <= 16 ? 8 : 4;
 }
 
 template <int HD>
@@ -508,11 +509,14 @@ cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
 // units and the capacity (the lengths are on the device).  Measured on GB300,
 // 32/8 heads of 128, one new token per sequence, replayed from a graph, clusters of
 // 8 blocks that join on chip against parts joined by a second kernel:
-//   1 sequence   1000 entries  5.6 us against 6.2;   4110  8.8 against 7.3
+//   1 sequence   1000 entries  5.7 us against 6.1;   4110  8.0 against 7.4;
+//                8000         10.6 against 8.3
 //   4 sequences  1000          7.4 against 7.0;      2000  9.1 against 10.2
-// so clusters serve short caches (where they also save the workspace and a
-// launch) while their blocks fill the machine at most once, two to a
-// multiprocessor.  With longer ones a cluster lasts as long as its sequence.
+// (clusters of 16: 14.7 us at 4110).  A cluster also saves the workspace and a
+// launch, 4 us of a call's time on the host, so clusters serve one sequence's
+// 8 heads up to parts of 576 entries, and more units up to 256 while their
+// blocks fill the machine at most once.  With longer caches a cluster lasts as
+// long as its sequence.
 //   Otherwise parts: for one sequence as many as fill the machine once; for
 // several, of 128 to 1024 entries, enough to fill it twice over were every
 // sequence as long as its page table allows, so that unlike lengths balance
@@ -525,7 +529,7 @@ AttnSplit attention_split(int n_seqs, int n_kv, int n_tokens, int group, int max
                                 capacity, sms);
   const long long units = static_cast<long long>(n_kv) * n_seqs;
   if (capacity <= 128) return {1, static_cast<int>(capacity), 1};
-  if (capacity <= 2048 && units <= 2 * sms / kMaxCluster) {
+  if (capacity <= kMaxCluster * (units <= 8 ? 576 : 256) && units <= 2 * sms / kMaxCluster) {
     const long long part = ((capacity + kMaxCluster - 1) / kMaxCluster + 63) / 64 * 64;
     return {kMaxCluster, static_cast<int>(part), kMaxCluster};
   }

@@ -370,7 +370,8 @@ def test_graphs_streams_and_shared_workspace():
     """Two captured graphs that share a workspace, replayed in turn on another
     stream, follow what their inputs hold at replay."""
     hd, n_q, n_kv = 128, 8, 2
-    cs = [ref.make_cache(20 + i, [(1, 3000), (1, 1)], n_kv, hd, 16) for i in range(2)]
+    # (a cache long enough for its parts to be joined through the workspace)
+    cs = [ref.make_cache(20 + i, [(1, 6000), (1, 1)], n_kv, hd, 16) for i in range(2)]
     hs = [handle(c) for c in cs]
     xs = [queries(20 + i, 2, n_q, hd).cuda() for i in range(2)]
     qs = cs[0].q_start.cuda()
