@@ -1,15 +1,20 @@
 // attention_many.cu -- qgemv_paged_attention for many query rows per
 // key/value head (prompts, chunks of prompts): tcgen05 products, TMA loads.
 //
-// A thread block takes 256 rows (two tiles of 128, A and B) of one (sequence,
-// key/value head) and walks the cache in tiles of 128 entries:
+// The work is a list of units: 256 query rows (two tiles of 128, A and B) of one
+// (sequence, key/value head) against the tiles of 128 entries that they see.
+// One thread block per multiprocessor stays for the whole call and takes
+// segments (units, or parts of units, see Scheduler):
+//   warp 10     scheduler: finds the block's segments from the lengths on the
+//               device and hands them to the others through a ring;
 //   warp 9      producer: K and V tiles by TMA, page by page, into a ring of
 //               128-byte-swizzled slots (keys and values alternate);
 //   warp 8      issues the products: S = Q K^T (operands in shared memory) and
 //               O += P V (P in tensor memory, V as the transposed operand);
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B: one row per thread,
 //               read from tensor memory, weights written back as fp16 over the
-//               scores they came from.
+//               scores they came from; the queries of the next segment are
+//               loaded before the last products of this one are awaited.
 // While one tile's weights are computed the tensor core works on the other's
 // products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
 // (HD each).
@@ -36,8 +41,8 @@ __device__ unsigned g_status = 0;
 
 constexpr int kTile = 128;           // rows of a tile, entries of a step
 // Three warpgroups; the launch gives 168 registers a thread (64,512), of which
-// the third group passes on what the two of the softmax need: 256 x 200 + 128 x
-// 104 = 64,512.
+// the third group passes on what the two of the softmax need: 256 x 192 + 128 x
+// 120 = 64,512.
 constexpr int kThreads = 384;
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
 constexpr float kSlack = 8.0f;       // log2 of the growth that makes O be rescaled
@@ -53,39 +58,170 @@ struct Shape {
   static constexpr uint32_t kDescO = tc::idesc_f16(kTile, HD, true);
 };
 
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kSegs = 4;        // segments the scheduler may be ahead
+constexpr int kMinTiles = 2;    // entries' tiles of a part of a unit, at least
+constexpr int kWholeUnits = 6;  // units per block from which no unit is split
+// What a unit costs besides its tiles, in tiles: queries, first scores, output
+// (without it a block of 31 units of one tile counted as one of a unit of 31, and
+// lasted four times as long).
+constexpr int kUnitCost = 4;
+
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
 };
 
-// (sequence, row tile) of block unit u: sequences in order, each with
-// ceil(rows / 256) units, the last (longest) first.  s = -1 behind the end.
-__device__ __forceinline__ void find_unit(const AttnArgs& a, int u, int lane, int* s_out, int* rt) {
-  *s_out = -1;
-  *rt = 0;
-  for (int s0 = 0; s0 < a.c.n_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    int first = 0, count = 0;
-    if (s < a.c.n_seqs) seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
-    if (count > a.max_q) flag_error(a.err);
-    const int mine = (min(count, a.max_q) * a.group + 2 * kTile - 1) / (2 * kTile);
-    int incl = mine;
+// A block's piece of work: tiles j0 .. j1 of a unit.
+struct Seg {
+  int s, h, r0;              // sequence (-1: no more), head, first row
+  int first, rows, off, len; // first token, rows and entries of the sequence
+  int j0, j1, slot;          // slot: where a part's result goes, -1: the output
+};
+
+// Finds a block's segments.  Units are ordered by sequence, by row tile (the
+// last, longest, first) and by head.  With a workspace and fewer than
+// kWholeUnits units per block, the tiles of all units are cut into equal runs, one
+// per block: a block's first and last unit may then be parts, whose results go to
+// the workspace for the join.  (2048 tokens over 30759 entries are 256 units of
+// 241 tiles for 152 blocks: whole units would take two rounds, 16 % of them
+// idle.)  Otherwise a block takes every gridDim.x-th unit, so that the blocks that
+// share keys stay next to one another.
+struct Scheduler {
+  const AttnArgs& a;
+  int lane;
+  int s = -1, first = 0, count = 0, len = 0, rows = 0;  // sequence at hand
+  int rt = 0, h = 0;                                     // unit at hand
+  // Sequences s0 .. s0 + 31, one per lane: what they hold, their units, and the
+  // spans of those (kUnitCost, then the tiles).
+  int s0 = -1, c_first = 0, c_count = 0, c_len = 0;
+  long long c_units = 0, c_span = 0;
+
+  __device__ Scheduler(const AttnArgs& args, int l) : a(args), lane(l) {}
+
+  __device__ static int units_of(int rows) { return (rows + kUnitRows - 1) / kUnitRows; }
+  __device__ int rows_of(int n) const { return min(n, a.max_q) * a.group; }
+  // tiles of entries that row tile r of a sequence sees, one at least
+  __device__ int tiles_of(int r, int n_rows, int n_count, int n_len) const {
+    const int last = min(n_rows, (r + 1) * kUnitRows) - 1;
+    const int see = min(n_len, n_len - n_count + div_group(last) + 1);
+    return max(1, (see + kTile - 1) / kTile);
+  }
+  // last / group: a.group_inv = floor(2^64 / group) + 1 (0 for 1)
+  __device__ int div_group(int n) const {
+    return a.group == 1 ? n : static_cast<int>(__umul64hi(static_cast<unsigned long long>(n), a.group_inv));
+  }
+  // Take up the 32 sequences from i on.
+  __device__ void look(int i, int* err) {
+    if (s0 == i) return;
+    s0 = i;
+    c_first = c_count = c_len = 0;
+    c_units = c_span = 0;
+    if (i + lane < a.c.n_seqs) {
+      seq_rows(a.q_start, i + lane, a.n_tokens, err, &c_first, &c_count);
+      c_len = seq_len(a.c, i + lane, err);
+      if (c_count > a.max_q) flag_error(err);
+    }
+    const int n_rows = rows_of(c_count), u = units_of(n_rows), n = min(32, a.c.n_seqs - i);
+    c_units = static_cast<long long>(u) * a.c.n_kv;
+    if (n <= 16) {  // few sequences: their row tiles over the lanes
+      for (int k = 0; k < n; ++k) {
+        const int k_count = __shfl_sync(0xFFFFFFFFu, c_count, k), k_rows = rows_of(k_count);
+        const int k_len = __shfl_sync(0xFFFFFFFFu, c_len, k), k_u = units_of(k_rows);
+        int t = 0;
+        for (int r = lane; r < k_u; r += 32) t += kUnitCost + tiles_of(r, k_rows, k_count, k_len);
+        t = __reduce_add_sync(0xFFFFFFFFu, t);
+        if (lane == k) c_span = t;
+      }
+    } else {
+      for (int r = 0; r < u; ++r) c_span += kUnitCost + tiles_of(r, n_rows, c_count, c_len);
+    }
+    c_span *= a.c.n_kv;
+  }
+  __device__ void total(int* err, long long* units, long long* span) {
+    long long n = 0, t = 0;
+    for (int i = 0; i < a.c.n_seqs; i += 32) {
+      look(i, err);
+      n += c_units;
+      t += c_span;
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) {
+      n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, k);
+    }
+    *units = n;
+    *span = t;
+  }
+  __device__ static long long scan(long long v, int lane) {
 #pragma unroll
     for (int k = 1; k < 32; k *= 2) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, k);
-      if (lane >= k) incl += v;
+      const long long w = __shfl_up_sync(0xFFFFFFFFu, v, k);
+      if (lane >= k) v += w;
     }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, u < incl);
-    if (hit != 0) {
-      const int l = __ffs(hit) - 1;
-      const int end = __shfl_sync(0xFFFFFFFFu, incl, l);
-      *s_out = s0 + l;
-      *rt = end - 1 - u;
-      return;
-    }
-    u -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+    return v;
   }
-}
+  // Go to the unit that holds position pos of all spans (of all units, one
+  // each); the position within it, or -1 if there is none.
+  __device__ int seek(long long pos, bool spans) {
+    for (int i = 0; i < a.c.n_seqs; i += 32) {
+      look(i, nullptr);
+      const long long mine = spans ? c_span : c_units, incl = scan(mine, lane);
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, pos < incl);
+      if (hit == 0) {
+        pos -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+        continue;
+      }
+      const int l = __ffs(hit) - 1;
+      pos -= __shfl_sync(0xFFFFFFFFu, incl - mine, l);
+      s = i + l;
+      first = __shfl_sync(0xFFFFFFFFu, c_first, l);
+      count = __shfl_sync(0xFFFFFFFFu, c_count, l);
+      len = __shfl_sync(0xFFFFFFFFu, c_len, l);
+      rows = rows_of(count);
+      for (int top = units_of(rows) - 1; top >= 0; top -= 32) {
+        const int r = top - lane;  // this lane's row tile
+        const int each = r < 0 ? 0 : spans ? kUnitCost + tiles_of(r, rows, count, len) : 1;
+        const long long here = static_cast<long long>(each) * a.c.n_kv, to = scan(here, lane);
+        const unsigned in = __ballot_sync(0xFFFFFFFFu, pos < to);
+        if (in == 0) {
+          pos -= __shfl_sync(0xFFFFFFFFu, to, 31);
+          continue;
+        }
+        const int k = __ffs(in) - 1;
+        const int rest = static_cast<int>(pos - __shfl_sync(0xFFFFFFFFu, to - here, k));
+        const int step = __shfl_sync(0xFFFFFFFFu, each, k);
+        rt = top - k;
+        h = rest / step;
+        return rest % step;
+      }
+    }
+    return -1;
+  }
+  // The unit n units on; false behind the last.
+  __device__ bool advance(int n) {
+    h += n;
+    while (h >= a.c.n_kv) {
+      h -= a.c.n_kv;
+      while (--rt < 0) {
+        if (++s >= a.c.n_seqs) return false;
+        const int l = s - s0;
+        if (l >= 0 && l < 32) {
+          first = __shfl_sync(0xFFFFFFFFu, c_first, l);
+          count = __shfl_sync(0xFFFFFFFFu, c_count, l);
+          len = __shfl_sync(0xFFFFFFFFu, c_len, l);
+        } else {
+          seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
+          len = seq_len(a.c, s, nullptr);
+        }
+        rows = rows_of(count);
+        rt = units_of(rows);
+      }
+    }
+    return true;
+  }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -102,335 +238,416 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;  // a wait ran out
-  __shared__ int s_unit[2];
+  __shared__ Seg segs[kSegs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring = base + 2 * Sh::kSlotBytes;
 
   pdl_launch_dependents();
-  if (warp == kMmaWarp) {
-    if (lane == 0) {
-      for (int i = 0; i < Sh::kSlots; ++i) {
-        mbar_init(smem_u32(&bars.full[i]), 1);
-        mbar_init(smem_u32(&bars.empty[i]), 1);
-      }
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(smem_u32(&bars.s_full[x]), 1);
-        mbar_init(smem_u32(&bars.p_full[x]), 4);  // one arrival per warp
-        mbar_init(smem_u32(&bars.o_full[x]), 1);
-      }
-      mbar_init(smem_u32(&bars.drain), 1);
-      fence_mbar_init();
-      s_failed = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::kSlots; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 1);
     }
-    __syncwarp();
-  }
-  pdl_wait();
-  if (warp == kTmaWarp) {
-    int s, rt;
-    find_unit(a, static_cast<int>(blockIdx.x / (a.n_parts * a.c.n_kv)), lane, &s, &rt);
-    if (lane == 0) {
-      s_unit[0] = s;
-      s_unit[1] = rt;
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(smem_u32(&bars.q_full[x]), 4);  // one arrival per warp
+      mbar_init(smem_u32(&bars.s_full[x]), 1);
+      mbar_init(smem_u32(&bars.p_full[x]), 4);
+      mbar_init(smem_u32(&bars.o_full[x]), 1);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(smem_u32(&bars.seg_full[i]), 1);
+      mbar_init(smem_u32(&bars.seg_empty[i]), 10);  // softmax, products and producer warps
+    }
+    mbar_init(smem_u32(&bars.drain), 1);
+    fence_mbar_init();
+    s_failed = 0;
   }
-  __syncthreads();
-  const int s = s_unit[0];
-  if (s < 0) return;
-  const int sp = blockIdx.x % a.n_parts, h = blockIdx.x / a.n_parts % a.c.n_kv;
-  int first, count;
-  seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
-  const int rows = min(count, a.max_q) * a.group;
-  const int r0 = s_unit[1] * 2 * kTile;
-  const int len = seq_len(a.c, s, a.err);
-  const int off = len - count;
-  const int k0 = sp * a.part;
-  if (sp > 0 && k0 >= len) return;
-  // tiles of entries that tile x sees (its last row sees the most)
-  int nt[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int last = min(rows, r0 + (x + 1) * kTile) - 1;
-    const int see = last >= r0 + x * kTile ? min(min(len, off + last / a.group + 1), k0 + a.part) : 0;
-    nt[x] = see > k0 ? (see - k0 + kTile - 1) / kTile : 0;
-  }
-  const int tiles = max(nt[0], nt[1]);
-  const bool has_b = r0 + kTile < rows;
-
-  if (warp == kMmaWarp) {
-    tc::alloc(smem_u32(&s_tmem), 512);
-  } else if (warp < 8 && tiles > 0) {
-    // Queries into the swizzled operand layout: [column of 128 bytes][row][128 B].
-    const int x = warp >> 2;
-    uint8_t* qs = base + x * Sh::kSlotBytes;
-    if (x == 0 || has_b)
-      for (int c = threadIdx.x & 127; c < kTile * (HD / 8); c += 128) {
-        const int r = c / (HD / 8), ch = c % (HD / 8), rr = r0 + x * kTile + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < rows)
-          v = *reinterpret_cast<const uint4*>(
-              a.q + static_cast<long long>(first + rr / a.group) * a.q_stride +
-              (h * a.group + rr % a.group) * HD + ch * 8);
-        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + r * 128 +
-                                  (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
-    tc::fence_async_shared();
-  }
-  // (the producer starts at once)
+  if (warp == kMmaWarp) tc::alloc(smem_u32(&s_tmem), 512);
   tc::fence_before();
-  if (warp <= kMmaWarp) named_bar_sync(1, 32 * (kMmaWarp + 1));
+  __syncthreads();
   tc::fence_after();
+  pdl_wait();
   const uint32_t tmem = s_tmem;
 
+  // Segment number n, as every warp but the scheduler reads it.
+  auto next_seg = [&](int n) {
+    const int i = n % kSegs;
+    step_wait(smem_u32(&bars.seg_full[i]), (n / kSegs) & 1, &s_failed, &g_status);
+    Seg g = segs[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[i]));
+    // (no segments are read after a wait ran out)
+    if (*static_cast<volatile int*>(&s_failed) != 0) g.s = -1;
+    g.s = __shfl_sync(0xFFFFFFFFu, g.s, 0);
+    return g;
+  };
+  // Tiles of tile x (0: A, 1: B) of a segment, from its j0 on.
+  auto tiles_in = [&](const Seg& g, int x) {
+    const int last = min(g.rows, g.r0 + (x + 1) * kTile) - 1;
+    if (last < g.r0 + x * kTile) return 0;
+    const int see = min(g.len, g.off + last / a.group + 1);
+    return max(0, min(g.j1, (see + kTile - 1) / kTile) - g.j0);
+  };
+
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  if (warp == kTmaWarp) {
-    // ---------------------------------------------------------- producer
-    const int page_rows = min(1 << a.c.page_shift, kTile);
-    const int boxes = kTile / page_rows;  // per tile, at most 8
-    const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;  // a row outside the tensor
-    auto page_at = [&](int j) {  // this lane's box of tile j
-      const int e = k0 + j * kTile + lane * page_rows;
-      return lane < boxes && e < len ? raw_page(a.c, s, e) : 0;
-    };
-    int next = tiles > 0 ? page_at(0) : 0, issued = 0;
-    for (int j = 0; j < tiles; ++j) {
-      const int e = k0 + j * kTile + lane * page_rows, p = good_page(a.c, next, a.err);
-      const int row = p < 0 || e >= len ? beyond : static_cast<int>(cache_row(a.c, p, h, e));
-      if (j + 1 < tiles) next = page_at(j + 1);
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int n = 2 * j + w, slot = n % Sh::kSlots, use = n / Sh::kSlots;
-        if (use > 0 && !warp_wait(smem_u32(&bars.empty[slot]), (use - 1) & 1, &g_status)) {
-          j = tiles;  // no more copies
-          break;
-        }
-        const uint32_t full = smem_u32(&bars.full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(full, Sh::kSlotBytes);
-        __syncwarp();
-        issued = n + 1;
-        if (lane < boxes) {
-          const uint32_t dst = smem_u32(ring + slot * Sh::kSlotBytes) + lane * page_rows * 128;
-#pragma unroll
-          for (int c = 0; c < Sh::kHalves; ++c)
-            tc::tma_2d(dst + c * (kTile * 128), w == 0 ? &k_map : &v_map, c * 64, row, full);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 10) {
+      // -------------------------------------------------------- scheduler
+      Scheduler sc(a, lane);
+      int n = 0;
+      auto emit = [&](bool end, int j0, int j1, int slot) {
+        const int i = n % kSegs;
+        if (n >= kSegs)
+          step_wait(smem_u32(&bars.seg_empty[i]), (n / kSegs - 1) & 1, &s_failed, &g_status);
+        if (lane == 0) {
+          segs[i] = Seg{end ? -1 : sc.s, sc.h, sc.rt * kUnitRows, sc.first, sc.rows,
+                        sc.len - sc.count, sc.len, j0, j1, slot};
+          mbar_arrive(smem_u32(&bars.seg_full[i]));
         }
         __syncwarp();
-      }
-    }
-    // no copy may be in flight when the block ends
-    for (int n = max(0, issued - Sh::kSlots); n < issued; ++n)
-      warp_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------- products
-    const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
-    const int n_tiles = tc::uniform(tiles), n_of[2] = {tc::uniform(nt[0]), tc::uniform(nt[1])};
-    const int tail = tc::uniform(len - k0);
-    auto slot_of = [&](int n) { return smem_u32(ring + (n % Sh::kSlots) * Sh::kSlotBytes); };
-    auto wait_full = [&](int n) {
-      step_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &s_failed, &g_status);
-    };
-    auto release = [&](int n) { tc::commit(smem_u32(&bars.empty[n % Sh::kSlots])); };
-    auto scores = [&](int x, int j) {
-      if (tc::elect_one()) {
-        const uint64_t q = tc::desc_k_major(smem_u32(base + x * Sh::kSlotBytes));
-        const uint64_t k = tc::desc_k_major(slot_of(2 * j));
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const int step = (i / 4) * (kTile * 128) + (i % 4) * 32;
-          tc::mma_ss(tm + x * kTile, q + (step >> 4), k + (step >> 4), Sh::kDescS, i > 0);
-        }
-        tc::commit(smem_u32(&bars.s_full[x]));
-      }
-      __syncwarp();
-    };
-    if (n_tiles > 0) {
-      wait_full(0);
-      if (n_of[0] > 0) scores(0, 0);
-      if (n_of[1] > 0) scores(1, 0);
-      if (tc::elect_one()) release(0);
-    }
-    for (int j = 0; j < n_tiles; ++j) {
-      wait_full(2 * j + 1);
-      if (tail < (j + 1) * kTile) {
-        // the rest of the last page may hold anything
-        const int ps = 1 << a.c.page_shift;
-        const int from = tail - j * kTile, to = min(kTile, (from + ps - 1) / ps * ps);
-        uint8_t* v = ring + ((2 * j + 1) % Sh::kSlots) * Sh::kSlotBytes;
-        for (int c = lane; c < (to - from) * 8 * Sh::kHalves; c += 32) {
-          const int r = from + c / (8 * Sh::kHalves), ch = c % (8 * Sh::kHalves);
-          *reinterpret_cast<uint4*>(v + (ch >> 3) * (kTile * 128) + r * 128 + (ch & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
-        tc::fence_async_shared();
-        __syncwarp();
-      }
-      if (j + 1 < n_tiles) wait_full(2 * j + 2);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (j < n_of[x]) {
-          step_wait(smem_u32(&bars.p_full[x]), j & 1, &s_failed, &g_status);
-          tc::fence_after();
-          if (tc::elect_one()) {
-            const uint64_t v = tc::desc_mn_major(slot_of(2 * j + 1), kTile * 128);
-#pragma unroll
-            for (int i = 0; i < kTile / 16; ++i)
-              tc::mma_ts(tm + 2 * kTile + x * HD, tm + x * kTile + i * 8, v + (i * 2048 >> 4),
-                         Sh::kDescO, j > 0 || i > 0);
-            if (j == n_of[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
+        ++n;
+      };
+      int* err = blockIdx.x == 0 ? a.err : nullptr;
+      long long units, all;
+      sc.total(err, &units, &all);
+      AttnUnit split{};
+      if (a.splits != nullptr && units < static_cast<long long>(kWholeUnits) * gridDim.x) {
+        const long long per = max(static_cast<long long>(kUnitCost + kMinTiles), (all + gridDim.x - 1) / gridDim.x);
+        long long left = min(per, all - blockIdx.x * per);
+        if (left > 0) {
+          int p0 = sc.seek(blockIdx.x * per, true);  // place in the unit's span
+          bool more = p0 >= 0;
+          while (more) {
+            const int t = sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len);
+            const int p1 = static_cast<int>(min(static_cast<long long>(kUnitCost + t), p0 + left));
+            const int j0 = max(0, p0 - kUnitCost), j1 = max(0, p1 - kUnitCost);
+            if (j1 > j0) {
+              if (j0 == 0 && j1 < t)
+                split = AttnUnit{1 + static_cast<int>((t - j1 + per - 1) / per), sc.s, sc.h,
+                                 sc.rt * kUnitRows, sc.first, sc.rows, sc.len - sc.count, sc.len};
+              emit(false, j0, j1,
+                   j0 > 0 || j1 < t ? 2 * static_cast<int>(blockIdx.x) + (j0 == 0) : -1);
+            }
+            left -= p1 - p0;
+            p0 = 0;
+            more = left > 0 && sc.advance(1);
           }
+        }
+      } else if (blockIdx.x < units && sc.seek(blockIdx.x, false) >= 0) {
+        do
+          emit(false, 0, sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len), -1);
+        while (sc.advance(static_cast<int>(gridDim.x)));
+      }
+      emit(true, 0, 0, -1);
+      if (a.splits != nullptr && lane == 0) a.splits[blockIdx.x] = split;
+    } else if (warp == kTmaWarp) {
+      // --------------------------------------------------------- producer
+      const int page_rows = min(1 << a.c.page_shift, kTile);
+      const int boxes = kTile / page_rows;  // per tile, at most 8
+      const int beyond = (a.c.n_pages * a.c.n_kv) << a.c.page_shift;  // a row outside the tensor
+      int issued = 0;
+      bool ok = true;
+      for (int ns = 0; ok; ++ns) {
+        const Seg g = next_seg(ns);
+        if (g.s < 0) break;
+        const int tiles = max(tiles_in(g, 0), tiles_in(g, 1));
+        auto page_at = [&](int j) {  // this lane's box of tile j
+          const int e = (g.j0 + j) * kTile + lane * page_rows;
+          return lane < boxes && e < g.len ? raw_page(a.c, g.s, e) : 0;
+        };
+        int next = tiles > 0 ? page_at(0) : 0;
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int e = (g.j0 + j) * kTile + lane * page_rows, p = good_page(a.c, next, a.err);
+          const int row = p < 0 || e >= g.len ? beyond : static_cast<int>(cache_row(a.c, p, g.h, e));
+          if (j + 1 < tiles) next = page_at(j + 1);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int slot = issued % Sh::kSlots, use = issued / Sh::kSlots;
+            if (use > 0 && ok) ok = warp_wait(smem_u32(&bars.empty[slot]), (use - 1) & 1, &g_status);
+            if (!ok) break;
+            const uint32_t full = smem_u32(&bars.full[slot]);
+            if (lane == 0) mbar_arrive_expect_tx(full, Sh::kSlotBytes);
+            __syncwarp();
+            ++issued;
+            if (lane < boxes) {
+              const uint32_t dst = smem_u32(ring + slot * Sh::kSlotBytes) + lane * page_rows * 128;
+#pragma unroll
+              for (int c = 0; c < Sh::kHalves; ++c)
+                tc::tma_2d(dst + c * (kTile * 128), w == 0 ? &k_map : &v_map, c * 64, row, full);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // no copy may be in flight when the block ends
+      for (int n = max(0, issued - Sh::kSlots); n < issued; ++n)
+        warp_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &g_status);
+    } else if (warp == kMmaWarp) {
+      // --------------------------------------------------------- products
+      const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
+      int item = 0;              // slots of the ring taken so far
+      int n_p[2] = {0, 0};       // tiles of weights awaited so far
+      int n_q[2] = {0, 0};       // queries awaited so far
+      auto slot_of = [&](int n) { return smem_u32(ring + (n % Sh::kSlots) * Sh::kSlotBytes); };
+      auto wait_full = [&](int n) {
+        step_wait(smem_u32(&bars.full[n % Sh::kSlots]), (n / Sh::kSlots) & 1, &s_failed, &g_status);
+      };
+      auto release = [&](int n) { tc::commit(smem_u32(&bars.empty[n % Sh::kSlots])); };
+      auto scores = [&](int x, int n) {  // with the keys in item n
+        if (tc::elect_one()) {
+          const uint64_t q = tc::desc_k_major(smem_u32(base + x * Sh::kSlotBytes));
+          const uint64_t k = tc::desc_k_major(slot_of(n));
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) {
+            const int step = (i / 4) * (kTile * 128) + (i % 4) * 32;
+            tc::mma_ss(tm + x * kTile, q + (step >> 4), k + (step >> 4), Sh::kDescS, i > 0);
+          }
+          tc::commit(smem_u32(&bars.s_full[x]));
+        }
+        __syncwarp();
+      };
+      for (int ns = 0;; ++ns) {
+        const Seg g = next_seg(ns);
+        if (g.s < 0) break;
+        const int n_of[2] = {tc::uniform(tiles_in(g, 0)), tc::uniform(tiles_in(g, 1))};
+        const int n_tiles = max(n_of[0], n_of[1]);
+        const int tail = tc::uniform(g.len - g.j0 * kTile);  // entries from the segment's start on
+        for (int x = 0; x < 2; ++x)
+          if (n_of[x] > 0) {
+            step_wait(smem_u32(&bars.q_full[x]), n_q[x] & 1, &s_failed, &g_status);
+            ++n_q[x];
+          }
+        tc::fence_after();
+        if (n_tiles > 0) {
+          wait_full(item);
+          if (n_of[0] > 0) scores(0, item);
+          if (n_of[1] > 0) scores(1, item);
+          if (tc::elect_one()) release(item);
           __syncwarp();
         }
-        if (x == 1 && tc::elect_one()) release(2 * j + 1);
-        __syncwarp();
-        if (j + 1 < n_of[x]) scores(x, j + 1);
+        for (int j = 0; j < n_tiles; ++j, item += 2) {
+          wait_full(item + 1);
+          if (tail < (j + 1) * kTile) {
+            // the rest of the last page may hold anything
+            const int ps = 1 << a.c.page_shift;
+            const int from = tail - j * kTile, to = min(kTile, (from + ps - 1) / ps * ps);
+            uint8_t* v = ring + ((item + 1) % Sh::kSlots) * Sh::kSlotBytes;
+            for (int c = lane; c < (to - from) * 8 * Sh::kHalves; c += 32) {
+              const int r = from + c / (8 * Sh::kHalves), ch = c % (8 * Sh::kHalves);
+              *reinterpret_cast<uint4*>(v + (ch >> 3) * (kTile * 128) + r * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_async_shared();
+            __syncwarp();
+          }
+          if (j + 1 < n_tiles) wait_full(item + 2);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j < n_of[x]) {
+              step_wait(smem_u32(&bars.p_full[x]), n_p[x] & 1, &s_failed, &g_status);
+              ++n_p[x];
+              tc::fence_after();
+              if (tc::elect_one()) {
+                const uint64_t v = tc::desc_mn_major(slot_of(item + 1), kTile * 128);
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i)
+                  tc::mma_ts(tm + 2 * kTile + x * HD, tm + x * kTile + i * 8, v + (i * 2048 >> 4),
+                             Sh::kDescO, j > 0 || i > 0);
+                if (j == n_of[x] - 1) tc::commit(smem_u32(&bars.o_full[x]));
+              }
+              __syncwarp();
+            }
+            if (x == 1 && tc::elect_one()) release(item + 1);
+            __syncwarp();
+            if (j + 1 < n_of[x]) scores(x, item + 2);
+          }
+          if (j + 1 < n_tiles && tc::elect_one()) release(item + 2);
+          __syncwarp();
+        }
       }
-      if (j + 1 < n_tiles && tc::elect_one()) release(2 * j + 2);
+      // every product is done before tensor memory goes back
+      if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
       __syncwarp();
+      warp_wait(smem_u32(&bars.drain), 0, &g_status);
     }
-    // every product is done before tensor memory goes back
-    if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
-    __syncwarp();
-    warp_wait(smem_u32(&bars.drain), 0, &g_status);
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ----------------------------------------------------------- softmax
-    const int x = warp >> 2, r = (warp & 3) * 32 + lane, rr = r0 + x * kTile + r;
-    const bool live = rr < rows;
-    const int i = live ? rr / a.group : 0;
-    const int lim = live ? off + i : -1;
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((warp & 3) << 21);  // 32 lanes per warp, lane in bits 16..
     const uint32_t st = lanes + x * kTile, ot = lanes + 2 * kTile + x * HD;
-    auto page_at = [&](int j) {  // lane b: page of entries 16b.. of tile j
-      const int e = k0 + j * kTile + lane * 16;
-      return lane < kTile / 16 && e < len ? raw_page(a.c, s, e) : 0;
+    // Queries of a segment into the swizzled operand layout: [column of 128
+    // bytes][row][128 B].  (Every product with the ones before is done: their
+    // scores have been read.)  A segment in which this tile sees nothing has none:
+    // nothing would hold its arrival back until the one before has been seen.
+    auto load_q = [&](const Seg& g) {
+      if (g.s < 0 || tiles_in(g, x) == 0) return;
+      uint8_t* qs = base + x * Sh::kSlotBytes;
+#pragma unroll 8
+      for (int c = threadIdx.x & 127; c < kTile * (HD / 8); c += 128) {
+        const int row = c / (HD / 8), ch = c % (HD / 8), rr = g.r0 + x * kTile + row;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < g.rows)
+          v = *reinterpret_cast<const uint4*>(
+              a.q + static_cast<long long>(g.first + rr / a.group) * a.q_stride +
+              (g.h * a.group + rr % a.group) * HD + ch * 8);
+        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + row * 128 +
+                                  (((ch & 7) ^ (row & 7)) << 4)) = v;
+      }
+      tc::fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
     };
-    float m = -INFINITY, l = 0.f;
-    int page_next = nt[x] > 0 ? page_at(0) : 0;
-    for (int j = 0; j < nt[x]; ++j) {
-      const unsigned bad = __ballot_sync(0xFFFFFFFFu, good_page(a.c, page_next, nullptr) < 0);
-      if (j + 1 < nt[x]) page_next = page_at(j + 1);
-      step_wait(smem_u32(&bars.s_full[x]), j & 1, &s_failed, &g_status);
-      tc::fence_after();
-      uint32_t v[128];
+    int n_s = 0, n_o = 0;  // tiles of scores, outputs awaited so far
+    Seg g = next_seg(0);
+    load_q(g);
+    for (int ns = 1; g.s >= 0; ++ns) {
+      const int rr = g.r0 + x * kTile + r;
+      const bool live = rr < g.rows;
+      const int i = live ? rr / a.group : 0;
+      const int lim = live ? g.off + i : -1;
+      const int tiles = tiles_in(g, x);
+      auto page_at = [&](int j) {  // lane b: page of entries 16b.. of tile j
+        const int e = (g.j0 + j) * kTile + lane * 16;
+        return lane < kTile / 16 && e < g.len ? raw_page(a.c, g.s, e) : 0;
+      };
+      float m = -INFINITY, l = 0.f;
+      int page_next = tiles > 0 ? page_at(0) : 0;
+      for (int j = 0; j < tiles; ++j, ++n_s) {
+        const unsigned bad = __ballot_sync(0xFFFFFFFFu, good_page(a.c, page_next, nullptr) < 0);
+        if (j + 1 < tiles) page_next = page_at(j + 1);
+        step_wait(smem_u32(&bars.s_full[x]), n_s & 1, &s_failed, &g_status);
+        tc::fence_after();
+        uint32_t v[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::ld32(v + 32 * c, st + 32 * c);
+        for (int c = 0; c < 4; ++c) tc::ld32(v + 32 * c, st + 32 * c);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc::wait_ld32(v + 32 * c);
-      const int hide = lim - (k0 + j * kTile);  // entries above this one are hidden
-      if (__any_sync(0xFFFFFFFFu, hide < kTile - 1)) {
+        for (int c = 0; c < 4; ++c) tc::wait_ld32(v + 32 * c);
+        const int hide = lim - (g.j0 + j) * kTile;  // entries above this one are hidden
+        if (__any_sync(0xFFFFFFFFu, hide < kTile - 1)) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k > hide) v[k] = 0xFF800000u;
-      }
-      if (bad != 0) {
+          for (int k = 0; k < 128; ++k)
+            if (k > hide) v[k] = 0xFF800000u;
+        }
+        if (bad != 0) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if ((bad >> (k / 16)) & 1) v[k] = 0xFF800000u;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int k = 0; k < 128; ++k)
+            if ((bad >> (k / 16)) & 1) v[k] = 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < 128; k += 2)
-        mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      // a row that grows past the slack (or from nothing) is rescaled
-      if (__any_sync(0xFFFFFFFFu, mt > m + kSlack)) {
-        const float mn = fmaxf(m, mt);
-        const float f = mn == m ? 1.f : ex2(m - mn);
-        m = mn;
-        l *= f;
-        if (j > 0) {
+        for (int k = 0; k < 128; k += 2)
+          mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        // a row that grows past the slack (or from nothing) is rescaled
+        if (__any_sync(0xFFFFFFFFu, mt > m + kSlack)) {
+          const float mn = fmaxf(m, mt);
+          const float f = mn == m ? 1.f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (j > 0) {
 #pragma unroll
-          for (int c = 0; c < HD; c += 16) {
-            uint32_t o[16];
-            tc::ld16(o, ot + c);
-            tc::wait_ld16(o);
+            for (int c = 0; c < HD; c += 16) {
+              uint32_t o[16];
+              tc::ld16(o, ot + c);
+              tc::wait_ld16(o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tc::st16(ot + c, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tc::st16(ot + c, o);
+            }
           }
         }
-      }
-      const float b = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float b = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int n = 32 * c + 2 * k;
-          const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
-          const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
-          sum[n & 3] += x0;
-          sum[(n + 1) & 3] += x1;
-          p[k] = pack_f16(x0, x1);
+          for (int k = 0; k < 16; ++k) {
+            const int n = 32 * c + 2 * k;
+            const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
+            const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
+            sum[n & 3] += x0;
+            sum[(n + 1) & 3] += x1;
+            p[k] = pack_f16(x0, x1);
+          }
+          tc::st16(st + 16 * c, p);
         }
-        tc::st16(st + 16 * c, p);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    }
-    if (nt[x] > 0) step_wait(smem_u32(&bars.o_full[x]), 0, &s_failed, &g_status);
-    const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
-    tc::fence_after();
-    const int t = first + i, head = h * a.group + (live ? rr % a.group : 0);
-    const long long at = static_cast<long long>(t) * a.n_q + head;
-    if (ok && a.n_parts > 1) {
-      float* po = a.part_o + (static_cast<long long>(sp) * a.n_tokens * a.n_q + at) * HD;
-#pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t o[32];
-        if (nt[x] > 0) {
-          tc::ld32(o, ot + c);
-          tc::wait_ld32(o);
-        }
-        if (live)
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(po + c + k) =
-                nt[x] > 0 ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
+      const Seg after = next_seg(ns);
+      load_q(after);
+
+      if (tiles > 0) {
+        step_wait(smem_u32(&bars.o_full[x]), n_o & 1, &s_failed, &g_status);
+        ++n_o;
       }
-      if (live) a.part_ml[static_cast<long long>(sp) * a.n_tokens * a.n_q + at] = make_float2(m, l);
-    } else if (ok) {
-      const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
-      bool odd = false;
-      __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD;
+      tc::fence_after();
+      const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
+      const int t = g.first + i, head = g.h * a.group + (live ? rr % a.group : 0);
+      if (ok && g.slot >= 0) {
+        const long long at = static_cast<long long>(g.slot) * kUnitRows + x * kTile + r;
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t o[32];
-        if (nt[x] > 0) {
-          tc::ld32(o, ot + c);
-          tc::wait_ld32(o);
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          float w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            w[e] = nt[x] > 0 ? __uint_as_float(o[k + e]) * inv : 0.f;
-            odd |= !(fabsf(w[e]) <= 3.0e38f);
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t o[32];
+          if (tiles > 0) {
+            tc::ld32(o, ot + c);
+            tc::wait_ld32(o);
           }
           if (live)
-            *reinterpret_cast<uint4*>(y + c + k) =
-                make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                           pack_f16(w[6], w[7]));
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<uint4*>(a.part_o + at * HD + c + k) =
+                  tiles > 0 ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
+        }
+        if (live) a.part_ml[at] = make_float2(m, l);
+      } else if (ok) {
+        const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
+        bool odd = false;
+        __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD;
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t o[32];
+          if (tiles > 0) {
+            tc::ld32(o, ot + c);
+            tc::wait_ld32(o);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              w[e] = tiles > 0 ? __uint_as_float(o[k + e]) * inv : 0.f;
+              odd |= !(fabsf(w[e]) <= 3.0e38f);
+            }
+            if (live)
+              *reinterpret_cast<uint4*>(y + c + k) =
+                  make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
+                             pack_f16(w[6], w[7]));
+          }
+        }
+        if (live && a.lse != nullptr)
+          a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
+        // rows that hide entries and came out infinite or NaN: again, without them
+        unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && lim < g.len - 1);
+        while (again != 0) {
+          const int src = __ffs(again) - 1;
+          again &= again - 1;
+          const int tt = __shfl_sync(0xFFFFFFFFu, t, src), hh = __shfl_sync(0xFFFFFFFFu, head, src);
+          const int ll = __shfl_sync(0xFFFFFFFFu, lim, src);
+          __syncwarp();
+          slow_row<HD>(a, g.s, g.h, tt, hh, ll, lane);
         }
       }
-      if (live && a.lse != nullptr) a.lse[at] = (m + log2f(l)) * kLn2;
-      // rows that hide entries and came out infinite or NaN: again, without them
-      unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && lim < len - 1);
-      while (again != 0) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int tt = __shfl_sync(0xFFFFFFFFu, t, src), hh = __shfl_sync(0xFFFFFFFFu, head, src);
-        const int ll = __shfl_sync(0xFFFFFFFFu, lim, src);
-        __syncwarp();
-        slow_row<HD>(a, s, h, tt, hh, ll, lane);
-      }
+      // (the next segment's first product into O waits for weights that these
+      // warps have yet to write)
+      tc::fence_before();
+      g = after;
     }
   }
   tc::fence_before();
@@ -441,8 +658,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Join the parts of split units: block c of the kernel above has the first part
+// of at most one (in its slot 1), the blocks behind it the others (in their
+// slots 0).  A warp per row.
+constexpr int kJoinRows = 32;
+
 template <int HD>
-cudaError_t launch_many(const AttnArgs& a, cudaStream_t st, int device) {
+__global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(const AttnArgs a) {
+  constexpr int D = HD / 32, kU = 4;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = blockIdx.x / (kUnitRows / kJoinRows), lane = threadIdx.x & 31;
+  const int r = blockIdx.x % (kUnitRows / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  const AttnUnit u = a.splits[c];
+  const int rr = u.r0 + r;
+  if (u.parts == 0 || rr >= u.rows) return;
+  float m = -INFINITY, l = 0.f, acc[D] = {};
+  for (int p0 = 0; p0 < u.parts; p0 += kU) {
+    float2 ml[kU];
+    float o[kU][D];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const int p = p0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[k][d] = 0.f;
+      if (p < u.parts) {
+        const long long at = static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * kUnitRows + r;
+        ml[k] = a.part_ml[at];
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[k][d] = a.part_o[at * HD + lane * D + d];
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) mn = fmaxf(mn, ml[k].x);
+    const float base = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - base);
+    l *= f0;
+#pragma unroll
+    for (int d = 0; d < D; ++d) acc[d] *= f0;
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+      const float f = ex2(ml[k].x - base);
+      l += ml[k].y * f;
+#pragma unroll
+      for (int d = 0; d < D; ++d) acc[d] += o[k][d] * f;
+    }
+    m = mn;
+  }
+  const int i = rr / a.group;
+  store_row<HD>(a, u.s, u.h, u.first + i, u.h * a.group + rr % a.group, min(u.off + i, u.len - 1),
+                u.len, acc, m, l, lane);
+}
+
+template <typename F, typename... Args>
+cudaError_t launch(F* k, long long blocks, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int HD>
+cudaError_t launch_many(AttnArgs a, int sms, cudaStream_t st, int device, void* workspace,
+                        size_t bytes) {
   static std::atomic<unsigned long long> done{0};
   auto* k = attention_many_kernel<HD>;
   const unsigned long long bit = 1ull << (device & 63);
@@ -454,46 +740,29 @@ cudaError_t launch_many(const AttnArgs& a, cudaStream_t st, int device) {
   }
   CUtensorMap km, vm;
   if (!encode_pool(&km, a.c, a.c.k) || !encode_pool(&vm, a.c, a.c.v)) return cudaErrorInvalidValue;
-  const long long blocks =
-      attention_many_units(a.c.n_seqs, a.n_tokens, a.group, a.max_q) * a.c.n_kv * a.n_parts;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<HD>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a, km, vm);
+  a.splits = nullptr;
+  if (bytes >= attention_many_bytes(HD, sms)) {  // outputs, {max, sum}, what the join needs
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2LL * sms * kUnitRows * HD);
+    a.splits = reinterpret_cast<AttnUnit*>(a.part_ml + 2LL * sms * kUnitRows);
+  }
+  const cudaError_t e = launch(k, sms, kThreads, Shape<HD>::kSmem, st, a, km, vm);
+  if (e != cudaSuccess || a.splits == nullptr) return e;
+  return launch(attention_join_units_kernel<HD>, static_cast<long long>(sms) * (kUnitRows / kJoinRows),
+                32 * kJoinRows, 0, st, a);
 }
 
 }  // namespace
 
-// Upper bound of the row tiles (256 rows) of all sequences: a sequence adds
-// at most one that is not full.
-long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q) {
-  const long long each = (static_cast<long long>(max_q) * group + 2 * kTile - 1) / (2 * kTile);
-  const long long full = static_cast<long long>(n_tokens) * group / (2 * kTile);
-  const long long part = n_seqs < n_tokens ? n_seqs : n_tokens;
-  const long long bound = full + part;
-  return each * n_seqs < bound ? each * n_seqs : bound;
+size_t attention_many_bytes(int head_dim, int sms) {
+  return static_cast<size_t>(sms) * (2 * kUnitRows * (static_cast<size_t>(head_dim) * 4 + 8) +
+                                     sizeof(AttnUnit));
 }
 
-// Parts of the cache: as many as fill the machine once (a block takes a whole
-// multiprocessor), each of 512 entries at least.
-AttnSplit attention_many_split(long long units, int n_kv, long long capacity, int sms) {
-  const long long want = sms / (units * n_kv);
-  if (want <= 1) return {1, static_cast<int>(capacity), 1};
-  long long part = ((capacity + want - 1) / want + kTile - 1) / kTile * kTile;
-  if (part < 512) part = 512;
-  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
-}
-
-cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device) {
-  return a.c.head_dim == 64 ? launch_many<64>(a, st, device) : launch_many<128>(a, st, device);
+cudaError_t attention_many_launch(const AttnArgs& a, int sms, cudaStream_t st, int device,
+                                  void* workspace, size_t bytes) {
+  return a.c.head_dim == 64 ? launch_many<64>(a, sms, st, device, workspace, bytes)
+                            : launch_many<128>(a, sms, st, device, workspace, bytes);
 }
 
 cudaError_t status_attention(unsigned* out) {

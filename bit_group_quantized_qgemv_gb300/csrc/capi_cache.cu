@@ -123,9 +123,10 @@ size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache* cache, int n_
     return 0;
   int dev, sms;
   if (qgemv::device_and_sms(&dev, &sms) != QGEMV_OK) return 0;
+  if (qgemv::attention_is_many(n_q / c.n_kv, max_q < n_tokens ? max_q : n_tokens))
+    return qgemv::attention_many_bytes(c.head_dim, sms);
   const qgemv::AttnSplit sp = qgemv::attention_split(
-      c.n_seqs, c.n_kv, n_tokens, n_q / c.n_kv, max_q < n_tokens ? max_q : n_tokens,
-      static_cast<long long>(c.max_pages) << c.page_shift, sms);
+      c.n_seqs, c.n_kv, static_cast<long long>(c.max_pages) << c.page_shift, sms);
   return sp.joins() > 1 ? sp.joins() * qgemv::attention_part_bytes(n_tokens, n_q, c.head_dim) : 0;
 }
 
@@ -151,6 +152,7 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
   a.n_tokens = n_tokens;
   a.n_q = n_q;
   a.group = n_q / a.c.n_kv;
+  a.group_inv = ~0ull / static_cast<unsigned>(a.group) + 1;
   a.q_start = q_start;
   a.max_q = max_q < n_tokens ? max_q : n_tokens;
   a.scale_log2 = scale * kLog2e;
@@ -158,9 +160,13 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
   a.out_stride = out_stride;
   a.lse = lse;
   a.err = err_flag;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (qgemv::attention_is_many(a.group, a.max_q))
+    return qgemv::report_launch(
+        qgemv::attention_many_launch(a, sms, st, dev, workspace, workspace_bytes));
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   const qgemv::AttnSplit sp = qgemv::attention_fit(
-      qgemv::attention_split(a.c.n_seqs, a.c.n_kv, n_tokens, a.group, a.max_q, cap, sms), cap,
+      qgemv::attention_split(a.c.n_seqs, a.c.n_kv, cap, sms), cap,
       qgemv::attention_part_bytes(n_tokens, n_q, a.c.head_dim), workspace_bytes);
   a.n_parts = sp.n_parts;
   a.part = sp.part;
@@ -170,8 +176,7 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
     a.part_ml = reinterpret_cast<float2*>(
         a.part_o + static_cast<size_t>(sp.joins()) * n_tokens * n_q * a.c.head_dim);
   }
-  return qgemv::report_launch(
-      qgemv::paged_attention_launch(a, sms, static_cast<cudaStream_t>(stream), dev));
+  return qgemv::report_launch(qgemv::attention_few_launch(a, st, dev));
 }
 
 int qgemv_attention_mass(const qgemv_kv_cache* cache, const uint16_t* q, long long q_stride,

@@ -34,6 +34,13 @@ struct RopeArgs {
   int* err;
 };
 
+// A unit of query rows whose entries several blocks share (attention_many.cu):
+// what their join has to know.
+struct AttnUnit {
+  int parts;  // 0: none
+  int s, h, r0, first, rows, off, len;
+};
+
 struct AttnArgs {
   KvView c;
   const __half* q;
@@ -51,6 +58,8 @@ struct AttnArgs {
   float* part_o;
   float2* part_ml;
   int n_parts, part, row_tiles;
+  AttnUnit* splits;  // many rows: [blocks], null: units are not split
+  unsigned long long group_inv;  // floor(2^64 / group) + 1
   int cluster;  // thread blocks that join their parts among themselves (1: none)
   int* err;
 };
@@ -84,15 +93,14 @@ cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device);
 cudaError_t cache_evict_launch(const EvictArgs& a, cudaStream_t st, int device);
 
-// How a call's cache is split: n_parts parts of `part` entries (1: not split),
+// How the cache is split for few rows: n_parts parts of `part` entries (1: not split),
 // `cluster` of them joined on chip; what is left of them is joined through
 // the workspace.
 struct AttnSplit {
   int n_parts, part, cluster;
   int joins() const { return n_parts / cluster; }
 };
-AttnSplit attention_split(int n_seqs, int n_kv, int n_tokens, int group, int max_q,
-                          long long capacity, int sms);
+AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms);
 // The split with the most parts whose workspace fits (`part` grows).
 AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes, size_t workspace_bytes);
 // Bytes of workspace per part.
@@ -102,11 +110,11 @@ size_t attention_part_bytes(int n_tokens, int n_q, int head_dim);
 inline bool attention_is_many(int group, int max_q) {
   return static_cast<long long>(group) * max_q > 32;
 }
-long long attention_many_units(int n_seqs, int n_tokens, int group, int max_q);
-AttnSplit attention_many_split(long long units, int n_kv, long long capacity, int sms);
-cudaError_t attention_many_launch(const AttnArgs& a, cudaStream_t st, int device);
+size_t attention_many_bytes(int head_dim, int sms);  // workspace it takes
+cudaError_t attention_many_launch(const AttnArgs& a, int sms, cudaStream_t st, int device,
+                                  void* workspace, size_t bytes);
 cudaError_t status_attention(unsigned* out);
 cudaError_t status_mass(unsigned* out);
-cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device);
+cudaError_t attention_few_launch(const AttnArgs& a, cudaStream_t st, int device);
 
 }  // namespace qgemv

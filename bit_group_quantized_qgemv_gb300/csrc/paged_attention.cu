@@ -522,11 +522,7 @@ cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
 // sequence as long as its page table allows, so that unlike lengths balance
 // (48 sequences of 900 to 20000 entries: 1024-entry parts 184 us, one part per
 // sequence 344 us).
-AttnSplit attention_split(int n_seqs, int n_kv, int n_tokens, int group, int max_q,
-                          long long capacity, int sms) {
-  if (attention_is_many(group, max_q))
-    return attention_many_split(attention_many_units(n_seqs, n_tokens, group, max_q), n_kv,
-                                capacity, sms);
+AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms) {
   const long long units = static_cast<long long>(n_kv) * n_seqs;
   if (capacity <= 128) return {1, static_cast<int>(capacity), 1};
   if (capacity <= kMaxCluster * (units <= 8 ? 576 : 256) && units <= 2 * sms / kMaxCluster) {
@@ -553,7 +549,6 @@ AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes,
   if (s.joins() <= 1 || fit >= static_cast<size_t>(s.joins())) return s;
   const long long n = static_cast<long long>(fit);
   if (n <= 1) return {1, static_cast<int>(capacity), 1};
-  // whole tiles of either kernel
   const long long part = ((capacity + n - 1) / n + 127) / 128 * 128;
   return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
 }
@@ -562,14 +557,9 @@ size_t attention_part_bytes(int n_tokens, int n_q, int head_dim) {
   return static_cast<size_t>(n_tokens) * n_q * (static_cast<size_t>(head_dim) * 4 + 8);
 }
 
-cudaError_t paged_attention_launch(AttnArgs a, int sms, cudaStream_t st, int device) {
-  (void)sms;
-  cudaError_t e;
-  if (attention_is_many(a.group, a.max_q))
-    e = attention_many_launch(a, st, device);
-  else
-    e = a.c.head_dim == 64 ? launch_few_rows<64>(a, st, device)
-                           : launch_few_rows<128>(a, st, device);
+cudaError_t attention_few_launch(const AttnArgs& a, cudaStream_t st, int device) {
+  const cudaError_t e = a.c.head_dim == 64 ? launch_few_rows<64>(a, st, device)
+                                           : launch_few_rows<128>(a, st, device);
   if (e != cudaSuccess || a.n_parts == a.cluster) return e;
   const long long rows = static_cast<long long>(a.c.n_seqs) * a.max_q * a.n_q;
   return a.c.head_dim == 64
