@@ -61,11 +61,12 @@ struct Shape {
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kSegs = 4;        // segments the scheduler may be ahead
 constexpr int kMinTiles = 2;    // entries' tiles of a part of a unit, at least
-constexpr int kWholeUnits = 6;  // units per block from which no unit is split
 // What a unit costs besides its tiles, in tiles: queries, first scores, output
 // (without it a block of 31 units of one tile counted as one of a unit of 31, and
 // lasted four times as long).
 constexpr int kUnitCost = 4;
+// What cutting units costs, in tiles: two outputs in fp32, and their join.
+constexpr int kSplitCost = 8;
 
 struct Bars {
   uint64_t full[10], empty[10];
@@ -80,23 +81,33 @@ struct Seg {
   int j0, j1, slot;          // slot: where a part's result goes, -1: the output
 };
 
-// Finds a block's segments.  Units are ordered by sequence, by row tile (the
-// last, longest, first) and by head.  With a workspace and fewer than
-// kWholeUnits units per block, the tiles of all units are cut into equal runs, one
-// per block: a block's first and last unit may then be parts, whose results go to
-// the workspace for the join.  (2048 tokens over 30759 entries are 256 units of
-// 241 tiles for 152 blocks: whole units would take two rounds, 16 % of them
-// idle.)  Otherwise a block takes every gridDim.x-th unit, so that the blocks that
-// share keys stay next to one another.
+// n / group by a multiplication: group_inv = floor(2^64 / group) + 1 (0 for 1).
+__device__ __forceinline__ int div_group(const AttnArgs& a, int n) {
+  return a.group == 1 ? n : static_cast<int>(__umul64hi(static_cast<unsigned long long>(n), a.group_inv));
+}
+
+// Finds a block's segments.  Units are ordered by sequence (up to 32 of them:
+// the one with the longest units first), by row tile (the last, longest, first) and
+// by head.  A block takes a unit of every
+// round, so that the blocks that share keys stay next to one another; or, with a workspace,
+// the tiles of all units are cut into equal runs, one per block: a block's
+// first and last unit may then be parts, whose results go to the workspace for the
+// join.  Whichever is expected to be done sooner: whole units last as long as
+// their rounds, or the longest of them, runs their length and kSplitCost.
+// 2048 tokens over 30759 entries (256 units of 241 tiles for 152 blocks): whole
+// 753 us, cut 677; 1200 over 8200 (152 units): whole 113, cut 129; 64 over 8064
+// (8 units): whole 109, cut 28.
 struct Scheduler {
   const AttnArgs& a;
   int lane;
-  int s = -1, first = 0, count = 0, len = 0, rows = 0;  // sequence at hand
+  int s = -1, first = 0, count = 0, len = 0, rows = 0;  // sequence at hand,
+  int place = 0;                                         // its place in the order
   int rt = 0, h = 0;                                     // unit at hand
   // Sequences s0 .. s0 + 31, one per lane: what they hold, their units, and the
   // spans of those (kUnitCost, then the tiles).
-  int s0 = -1, c_first = 0, c_count = 0, c_len = 0;
+  int s0 = -1, c_id = 0, c_first = 0, c_count = 0, c_len = 0;
   long long c_units = 0, c_span = 0;
+  int c_longest = 0;  // the longest span of one unit
 
   __device__ Scheduler(const AttnArgs& args, int l) : a(args), lane(l) {}
 
@@ -105,12 +116,8 @@ struct Scheduler {
   // tiles of entries that row tile r of a sequence sees, one at least
   __device__ int tiles_of(int r, int n_rows, int n_count, int n_len) const {
     const int last = min(n_rows, (r + 1) * kUnitRows) - 1;
-    const int see = min(n_len, n_len - n_count + div_group(last) + 1);
+    const int see = min(n_len, n_len - n_count + div_group(a, last) + 1);
     return max(1, (see + kTile - 1) / kTile);
-  }
-  // last / group: a.group_inv = floor(2^64 / group) + 1 (0 for 1)
-  __device__ int div_group(int n) const {
-    return a.group == 1 ? n : static_cast<int>(__umul64hi(static_cast<unsigned long long>(n), a.group_inv));
   }
   // Take up the 32 sequences from i on.
   __device__ void look(int i, int* err) {
@@ -118,6 +125,7 @@ struct Scheduler {
     s0 = i;
     c_first = c_count = c_len = 0;
     c_units = c_span = 0;
+    c_longest = 0;
     if (i + lane < a.c.n_seqs) {
       seq_rows(a.q_start, i + lane, a.n_tokens, err, &c_first, &c_count);
       c_len = seq_len(a.c, i + lane, err);
@@ -125,6 +133,7 @@ struct Scheduler {
     }
     const int n_rows = rows_of(c_count), u = units_of(n_rows), n = min(32, a.c.n_seqs - i);
     c_units = static_cast<long long>(u) * a.c.n_kv;
+    if (u > 0) c_longest = kUnitCost + tiles_of(u - 1, n_rows, c_count, c_len);
     if (n <= 16) {  // few sequences: their row tiles over the lanes
       for (int k = 0; k < n; ++k) {
         const int k_count = __shfl_sync(0xFFFFFFFFu, c_count, k), k_rows = rows_of(k_count);
@@ -138,13 +147,33 @@ struct Scheduler {
       for (int r = 0; r < u; ++r) c_span += kUnitCost + tiles_of(r, n_rows, c_count, c_len);
     }
     c_span *= a.c.n_kv;
+    c_id = i + lane;
+    if (a.c.n_seqs > 1 && a.c.n_seqs <= 32) {  // those with the longest units first
+      int rank = 0;
+      for (int k = 0; k < a.c.n_seqs; ++k) {
+        const int other = __shfl_sync(0xFFFFFFFFu, c_longest, k);
+        rank += other > c_longest || (other == c_longest && k < lane);
+      }
+      int from = 0;  // the lane whose rank is this lane's number
+      for (int k = 0; k < a.c.n_seqs; ++k)
+        if (__shfl_sync(0xFFFFFFFFu, rank, k) == lane) from = k;
+      c_id = __shfl_sync(0xFFFFFFFFu, c_id, from);
+      c_first = __shfl_sync(0xFFFFFFFFu, c_first, from);
+      c_count = __shfl_sync(0xFFFFFFFFu, c_count, from);
+      c_len = __shfl_sync(0xFFFFFFFFu, c_len, from);
+      c_units = __shfl_sync(0xFFFFFFFFu, c_units, from);
+      c_span = __shfl_sync(0xFFFFFFFFu, c_span, from);
+      c_longest = __shfl_sync(0xFFFFFFFFu, c_longest, from);
+    }
   }
-  __device__ void total(int* err, long long* units, long long* span) {
+  __device__ void total(int* err, long long* units, long long* span, int* longest) {
     long long n = 0, t = 0;
+    int m = 0;
     for (int i = 0; i < a.c.n_seqs; i += 32) {
       look(i, err);
       n += c_units;
       t += c_span;
+      m = max(m, c_longest);
     }
 #pragma unroll
     for (int k = 16; k > 0; k /= 2) {
@@ -153,6 +182,7 @@ struct Scheduler {
     }
     *units = n;
     *span = t;
+    *longest = __reduce_max_sync(0xFFFFFFFFu, m);
   }
   __device__ static long long scan(long long v, int lane) {
 #pragma unroll
@@ -175,7 +205,8 @@ struct Scheduler {
       }
       const int l = __ffs(hit) - 1;
       pos -= __shfl_sync(0xFFFFFFFFu, incl - mine, l);
-      s = i + l;
+      place = i + l;
+      s = __shfl_sync(0xFFFFFFFFu, c_id, l);
       first = __shfl_sync(0xFFFFFFFFu, c_first, l);
       count = __shfl_sync(0xFFFFFFFFu, c_count, l);
       len = __shfl_sync(0xFFFFFFFFu, c_len, l);
@@ -205,13 +236,15 @@ struct Scheduler {
     while (h >= a.c.n_kv) {
       h -= a.c.n_kv;
       while (--rt < 0) {
-        if (++s >= a.c.n_seqs) return false;
-        const int l = s - s0;
+        if (++place >= a.c.n_seqs) return false;
+        const int l = place - s0;
         if (l >= 0 && l < 32) {
+          s = __shfl_sync(0xFFFFFFFFu, c_id, l);
           first = __shfl_sync(0xFFFFFFFFu, c_first, l);
           count = __shfl_sync(0xFFFFFFFFu, c_count, l);
           len = __shfl_sync(0xFFFFFFFFu, c_len, l);
         } else {
+          s = place;
           seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
           len = seq_len(a.c, s, nullptr);
         }
@@ -227,6 +260,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// 32 bytes, in one store where they are aligned to it: a row per thread, every
+// store touches 32 lines of the cache.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
+  if (wide)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 template <int HD>
@@ -286,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tiles_in = [&](const Seg& g, int x) {
     const int last = min(g.rows, g.r0 + (x + 1) * kTile) - 1;
     if (last < g.r0 + x * kTile) return 0;
-    const int see = min(g.len, g.off + last / a.group + 1);
+    const int see = min(g.len, g.off + div_group(a, last) + 1);
     return max(0, min(g.j1, (see + kTile - 1) / kTile) - g.j0);
   };
 
@@ -310,10 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int* err = blockIdx.x == 0 ? a.err : nullptr;
       long long units, all;
-      sc.total(err, &units, &all);
+      int longest;
+      sc.total(err, &units, &all, &longest);
+      const long long rounds = (units + gridDim.x - 1) / gridDim.x;
+      const long long whole = max(static_cast<long long>(longest), rounds * all / max(1LL, units));
+      const long long per = max(static_cast<long long>(kUnitCost + kMinTiles),
+                                (all + gridDim.x - 1) / gridDim.x);
       AttnUnit split{};
-      if (a.splits != nullptr && units < static_cast<long long>(kWholeUnits) * gridDim.x) {
-        const long long per = max(static_cast<long long>(kUnitCost + kMinTiles), (all + gridDim.x - 1) / gridDim.x);
+      if (a.splits != nullptr && per + kSplitCost < whole) {
         long long left = min(per, all - blockIdx.x * per);
         if (left > 0) {
           int p0 = sc.seek(blockIdx.x * per, true);  // place in the unit's span
@@ -335,9 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (blockIdx.x < units && sc.seek(blockIdx.x, false) >= 0) {
+        // rounds of one unit per block, every other one backwards: units of a
+        // sequence shorten, so who had the longer one gets the shorter
+        const int step[2] = {2 * static_cast<int>(gridDim.x - blockIdx.x) - 1,
+                             2 * static_cast<int>(blockIdx.x) + 1};
+        int round = 0;
         do
           emit(false, 0, sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len), -1);
-        while (sc.advance(static_cast<int>(gridDim.x)));
+        while (sc.advance(step[round++ & 1]));
       }
       emit(true, 0, 0, -1);
       if (a.splits != nullptr && lane == 0) a.splits[blockIdx.x] = split;
@@ -483,17 +538,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing would hold its arrival back until the one before has been seen.
     auto load_q = [&](const Seg& g) {
       if (g.s < 0 || tiles_in(g, x) == 0) return;
-      uint8_t* qs = base + x * Sh::kSlotBytes;
-#pragma unroll 8
-      for (int c = threadIdx.x & 127; c < kTile * (HD / 8); c += 128) {
-        const int row = c / (HD / 8), ch = c % (HD / 8), rr = g.r0 + x * kTile + row;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < g.rows)
-          v = *reinterpret_cast<const uint4*>(
-              a.q + static_cast<long long>(g.first + rr / a.group) * a.q_stride +
-              (g.h * a.group + rr % a.group) * HD + ch * 8);
-        *reinterpret_cast<uint4*>(qs + (ch >> 3) * (kTile * 128) + row * 128 +
-                                  (((ch & 7) ^ (row & 7)) << 4)) = v;
+      // (loads first, then the stores: each chunk loaded and stored in turn took
+      // 9000 clocks)
+      const uint32_t qs = smem_u32(base + x * Sh::kSlotBytes);
+      constexpr int kLoads = kTile * (HD / 8) / 128, kBatch = 8;
+#pragma unroll
+      for (int b = 0; b < kLoads; b += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int c = (b + k) * 128 + (threadIdx.x & 127);
+          const int row = c / (HD / 8), ch = c % (HD / 8), rr = g.r0 + x * kTile + row;
+          v[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (rr < g.rows) {
+            const int i = div_group(a, rr);
+            v[k] = *reinterpret_cast<const uint4*>(
+                a.q + static_cast<long long>(g.first + i) * a.q_stride +
+                (g.h * a.group + rr - i * a.group) * HD + ch * 8);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int c = (b + k) * 128 + (threadIdx.x & 127);
+          const int row = c / (HD / 8), ch = c % (HD / 8);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           qs + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                       "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
+                       : "memory");
+        }
       }
       tc::fence_async_shared();
       __syncwarp();
@@ -505,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int ns = 1; g.s >= 0; ++ns) {
       const int rr = g.r0 + x * kTile + r;
       const bool live = rr < g.rows;
-      const int i = live ? rr / a.group : 0;
+      const int i = live ? div_group(a, rr) : 0;
       const int lim = live ? g.off + i : -1;
       const int tiles = tiles_in(g, x);
       auto page_at = [&](int j) {  // lane b: page of entries 16b.. of tile j
@@ -589,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_after();
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
-      const int t = g.first + i, head = g.h * a.group + (live ? rr % a.group : 0);
+      const int t = g.first + i, head = g.h * a.group + (live ? rr - i * a.group : 0);
       if (ok && g.slot >= 0) {
         const long long at = static_cast<long long>(g.slot) * kUnitRows + x * kTile + r;
 #pragma unroll
@@ -598,37 +670,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tiles > 0) {
             tc::ld32(o, ot + c);
             tc::wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
           if (live)
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<uint4*>(a.part_o + at * HD + c + k) =
-                  tiles > 0 ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 32; k += 8) store32(a.part_o + at * HD + c + k, o + k, true);
         }
         if (live) a.part_ml[at] = make_float2(m, l);
       } else if (ok) {
         const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
         bool odd = false;
         __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD;
+        const bool wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           uint32_t o[32];
           if (tiles > 0) {
             tc::ld32(o, ot + c);
             tc::wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              w[e] = tiles > 0 ? __uint_as_float(o[k + e]) * inv : 0.f;
-              odd |= !(fabsf(w[e]) <= 3.0e38f);
-            }
-            if (live)
-              *reinterpret_cast<uint4*>(y + c + k) =
-                  make_uint4(pack_f16(w[0], w[1]), pack_f16(w[2], w[3]), pack_f16(w[4], w[5]),
-                             pack_f16(w[6], w[7]));
+          for (int k = 0; k < 16; ++k) {
+            const float u = __uint_as_float(o[2 * k]) * inv, v = __uint_as_float(o[2 * k + 1]) * inv;
+            odd |= !(fabsf(u) <= 3.0e38f) || !(fabsf(v) <= 3.0e38f);
+            w[k] = pack_f16(u, v);
+          }
+          if (live) {
+            store32(y + c, w, wide);
+            store32(y + c + 16, w + 8, wide);
           }
         }
         if (live && a.lse != nullptr)
@@ -661,18 +736,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Join the parts of split units: block c of the kernel above has the first part
 // of at most one (in its slot 1), the blocks behind it the others (in their
 // slots 0).  A warp per row.
-constexpr int kJoinRows = 32;
+constexpr int kJoinRows = 16, kJoinBlocks = 4;  // rows at a time, blocks per unit
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(const AttnArgs a) {
   constexpr int D = HD / 32, kU = 4;
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x / (kUnitRows / kJoinRows), lane = threadIdx.x & 31;
-  const int r = blockIdx.x % (kUnitRows / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  const int c = blockIdx.x / kJoinBlocks, lane = threadIdx.x & 31;
   const AttnUnit u = a.splits[c];
+  if (u.parts == 0) return;
+  for (int r = blockIdx.x % kJoinBlocks * kJoinRows + (threadIdx.x >> 5); r < kUnitRows;
+       r += kJoinBlocks * kJoinRows) {
   const int rr = u.r0 + r;
-  if (u.parts == 0 || rr >= u.rows) return;
+  if (rr >= u.rows) return;
   float m = -INFINITY, l = 0.f, acc[D] = {};
   for (int p0 = 0; p0 < u.parts; p0 += kU) {
     float2 ml[kU];
@@ -709,6 +786,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(co
   const int i = rr / a.group;
   store_row<HD>(a, u.s, u.h, u.first + i, u.h * a.group + rr % a.group, min(u.off + i, u.len - 1),
                 u.len, acc, m, l, lane);
+  }
 }
 
 template <typename F, typename... Args>
@@ -748,7 +826,7 @@ cudaError_t launch_many(AttnArgs a, int sms, cudaStream_t st, int device, void* 
   }
   const cudaError_t e = launch(k, sms, kThreads, Shape<HD>::kSmem, st, a, km, vm);
   if (e != cudaSuccess || a.splits == nullptr) return e;
-  return launch(attention_join_units_kernel<HD>, static_cast<long long>(sms) * (kUnitRows / kJoinRows),
+  return launch(attention_join_units_kernel<HD>, static_cast<long long>(sms) * kJoinBlocks,
                 32 * kJoinRows, 0, st, a);
 }
 

@@ -32,7 +32,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ------------------------------------------------------------- few rows
 constexpr int kWarps = 4;
 constexpr int kTile = 16;
-constexpr int kStages = 4;
+// Ring depth of each warp (16 sequences of 500 to 16000 entries: two stages 30.0
+// us, three 31.4, four 33.2, six 37.1; one of 30000: 12.9, 10.8, 11.9, 13.7: more
+// blocks to a multiprocessor serve better than deeper rings).
+constexpr int kStages = 3;
 constexpr int kRowsMax = 32;  // rows of one walk over the entries
 
 template <int HD>
@@ -482,9 +485,9 @@ cudaError_t launch_few(const MassArgs& a, int sms, cudaStream_t st, int device) 
   static std::atomic<unsigned long long> done{0};
   const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   const long long units = static_cast<long long>(a.c.n_kv) * a.c.n_seqs;
-  // Parts of 128 to 1024 entries, enough to fill the machine (three blocks to
-  // a multiprocessor) twice over.
-  long long part = cap * units / (6LL * sms) / 64 * 64;
+  // Parts of 128 to 1024 entries, two to a multiprocessor were every sequence as
+  // long as its page table allows.
+  long long part = cap * units / (2LL * sms) / 64 * 64;
   if (part < 128) part = 128;
   if (part > 1024) part = 1024;
   const long long parts = (cap + part - 1) / part;

@@ -518,10 +518,10 @@ cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
 // blocks fill the machine at most once.  With longer caches a cluster lasts as
 // long as its sequence.
 //   Otherwise parts: for one sequence as many as fill the machine once; for
-// several, of 128 to 1024 entries, enough to fill it twice over were every
-// sequence as long as its page table allows, so that unlike lengths balance
-// (48 sequences of 900 to 20000 entries: 1024-entry parts 184 us, one part per
-// sequence 344 us).
+// several, of 128 to 1024 entries, one per multiprocessor were every sequence as
+// long as its page table allows, so that unlike lengths balance (48 sequences of
+// 900 to 20000 entries: 1024-entry parts 184 us, one part per sequence 344 us;
+// four of 8000: this 26 us, four parts per multiprocessor 31, sixteen 37).
 AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms) {
   const long long units = static_cast<long long>(n_kv) * n_seqs;
   if (capacity <= 128) return {1, static_cast<int>(capacity), 1};
@@ -535,7 +535,7 @@ AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms) {
     part = ((capacity + n - 1) / n + 63) / 64 * 64;
     if (part < 128) part = 128;
   } else {
-    part = capacity * units / (4LL * sms) / 64 * 64;
+    part = capacity * units / sms / 64 * 64;
     if (part < 128) part = 128;
     if (part > 1024) part = 1024;
   }
