@@ -20,6 +20,7 @@
 
 #include "kv_tensor_map.h"
 #include "mma_tile.cuh"
+#include "runs.cuh"
 #include "tcgen05.cuh"
 
 namespace qgemv {
@@ -43,24 +44,28 @@ __host__ __device__ constexpr int key_bytes() {
   return kTile * HD * 2;
 }
 
+// Blocks resident on a multiprocessor, by the registers of the rows.
+__host__ __device__ constexpr int few_resident(int nt) { return nt > 2 ? 2 : 4; }
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * kWarps) mass_few_kernel(const MassArgs a, int part,
-                                                               int parts) {
+__global__ void __launch_bounds__(32 * kWarps, few_resident(NT)) mass_few_kernel(const MassArgs a) {
   constexpr int kM = HD / 16, kChunks = HD / 8, kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  long long b = blockIdx.x;
-  const int k0 = static_cast<int>(b % parts) * part;
-  b /= parts;
-  const int h = static_cast<int>(b % a.c.n_kv), s = static_cast<int>(b / a.c.n_kv);
-  const int len = seq_len(a.c, s, a.err);
+  // blocks of 64 entries of a sequence's units
+  auto blocks_of = [&](int i) { return (seq_len(a.c, i, a.err) + 63) / 64; };
+  int s, h, j0;
+  long long per, left = run_start(a.c.n_seqs, a.c.n_kv, 2, lane, blocks_of, &per, &s, &h, &j0);
+  while (left > 0) {  // segments of this block's run
+  const int len = seq_len(a.c, s, nullptr);
   int first, count;
   seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
   if (count > a.max_q) flag_error(a.err);
-  if (k0 >= len) return;
-  const int k1 = min(len, k0 + part);
+  const int j1 = static_cast<int>(min(static_cast<long long>((len + 63) / 64), j0 + left));
+  const int k0 = j0 * 64, k1 = min(len, j1 * 64);
+  left -= j1 - j0;
   const int rows = min(count, a.max_q) * a.group, off = len - count;
   const int tiles = (k1 - k0 + kTile - 1) / kTile;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
@@ -162,6 +167,13 @@ __global__ void __launch_bounds__(32 * kWarps) mass_few_kernel(const MassArgs a,
     __syncwarp();
     r0 += kRows;
   } while (r0 < rows);
+  j0 = 0;
+  if (left > 0 && ++h == a.c.n_kv) {
+    h = 0;
+    s = run_next(s, a.c.n_seqs, lane, blocks_of);
+    if (s >= a.c.n_seqs) return;
+  }
+  }
 }
 
 // ------------------------------------------------------------ many rows
@@ -188,15 +200,17 @@ struct Share {
   int s, h, e0, len, first, tokens, off, from, steps;
 };
 
-// Share number b; false if it lies behind its sequence's end.
-__device__ __forceinline__ bool get_share(const MassArgs& a, long long b, int per_head,
-                                          int step_tokens, Share* w) {
-  w->e0 = static_cast<int>(b % per_head) * 2 * kBlock;
-  b /= per_head;
-  w->h = static_cast<int>(b % a.c.n_kv);
-  w->s = static_cast<int>(b / a.c.n_kv);
-  w->len = seq_len(a.c, w->s, a.err);
-  if (w->e0 >= w->len) return false;
+// Shares of sequence i's units, and share number b of all.  A whole warp.
+__device__ __forceinline__ int shares_of(const MassArgs& a, int i, int* err) {
+  return (seq_len(a.c, i, err) + 2 * kBlock - 1) / (2 * kBlock);
+}
+__device__ __forceinline__ void get_share(const MassArgs& a, long long b, int step_tokens, int lane,
+                                          Share* w) {
+  int j;
+  run_seek(b, a.c.n_seqs, a.c.n_kv, lane, [&](int i) { return shares_of(a, i, nullptr); }, &w->s,
+           &w->h, &j);
+  w->e0 = j * 2 * kBlock;
+  w->len = seq_len(a.c, w->s, nullptr);
   int count;
   seq_rows(a.q_start, w->s, a.n_tokens, a.err, &w->first, &count);
   if (count > a.max_q) flag_error(a.err);
@@ -205,7 +219,6 @@ __device__ __forceinline__ bool get_share(const MassArgs& a, long long b, int pe
   // steps of step_tokens tokens, from the one whose last token sees entry e0
   w->from = max(0, w->e0 - w->off) / step_tokens;
   w->steps = max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from);
-  return true;
 }
 
 // One block per multiprocessor, each taking every gridDim.x-th share.  The
@@ -214,7 +227,7 @@ __device__ __forceinline__ bool get_share(const MassArgs& a, long long b, int pe
 template <int HD>
 __global__ void __launch_bounds__(kManyThreads, 1)
     mass_many_kernel(const MassArgs a, const __grid_constant__ CUtensorMap k_map,
-                     const __grid_constant__ CUtensorMap q_map, int per_head, int step_tokens) {
+                     const __grid_constant__ CUtensorMap q_map, int step_tokens) {
   using Sh = Shape<HD>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
@@ -252,7 +265,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc::fence_after();
   pdl_wait();
   const uint32_t tmem = s_tmem;
-  const long long shares = static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs;
+  const long long shares = run_total(a.c.n_seqs, a.c.n_kv, lane, [&](int i) {
+    return shares_of(a, i, warp == 8 ? a.err : nullptr);
+  });
   Share w;
 
   if (warp == 9) {
@@ -264,7 +279,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     int kb = 0, g = 0;
     bool ok = true;
     for (long long b = blockIdx.x; b < shares && ok; b += gridDim.x) {
-      if (!get_share(a, b, per_head, step_tokens, &w) || w.steps == 0) continue;
+      get_share(a, b, step_tokens, lane, &w);
+      if (w.steps == 0) continue;
       const int kd = kb & 1;
       if (kb > 1) ok = warp_wait(smem_u32(&bars.k_empty[kd]), (kb / 2 - 1) & 1, &g_status);
       if (!ok) break;
@@ -317,7 +333,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     }
     int g = 0;
     for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      get_share(a, b, step_tokens, lane, &w);
       float v[kOwn];
       auto load = [&](int j) {
         const int t0 = (w.from + j) * step_tokens;
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
     int kb = 0, g = 0;
     for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      get_share(a, b, step_tokens, lane, &w);
       const int n_steps = tc::uniform(w.steps);
       if (n_steps == 0) continue;
       const int kd = kb & 1;
@@ -388,7 +404,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
     int g = 0;
     for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      if (!get_share(a, b, per_head, step_tokens, &w)) continue;
+      get_share(a, b, step_tokens, lane, &w);
       const int e = w.e0 + x * kBlock + (warp & 3) * 32 + lane;
       const bool live = e < w.len;
       const int page = live ? raw_page(a.c, w.s, e) : 0;
@@ -483,17 +499,8 @@ cudaError_t launch(F* k, std::atomic<unsigned long long>* done, long long blocks
 template <int HD, int NT>
 cudaError_t launch_few(const MassArgs& a, int sms, cudaStream_t st, int device) {
   static std::atomic<unsigned long long> done{0};
-  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  const long long units = static_cast<long long>(a.c.n_kv) * a.c.n_seqs;
-  // Parts of 128 to 1024 entries, two to a multiprocessor were every sequence as
-  // long as its page table allows.
-  long long part = cap * units / (2LL * sms) / 64 * 64;
-  if (part < 128) part = 128;
-  if (part > 1024) part = 1024;
-  const long long parts = (cap + part - 1) / part;
-  return launch(mass_few_kernel<HD, NT>, &done, parts * units, 32 * kWarps,
-                kWarps * kStages * key_bytes<HD>(), st, device, a, static_cast<int>(part),
-                static_cast<int>(parts));
+  return launch(mass_few_kernel<HD, NT>, &done, static_cast<long long>(sms) * few_resident(NT),
+                32 * kWarps, kWarps * kStages * key_bytes<HD>(), st, device, a);
 }
 
 template <int HD>
@@ -514,10 +521,8 @@ cudaError_t launch_many(const MassArgs& a, int sms, cudaStream_t st, int device)
          estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  const int per_head = static_cast<int>((cap + 2 * kBlock - 1) / (2 * kBlock));
-  const long long shares = static_cast<long long>(per_head) * a.c.n_kv * a.c.n_seqs;
-  return launch(mass_many_kernel<HD>, &done, shares < sms ? shares : sms, kManyThreads, Shape<HD>::kSmem, st, device, a, km, qm, per_head, step_tokens);
+  return launch(mass_many_kernel<HD>, &done, sms, kManyThreads, Shape<HD>::kSmem, st, device, a, km,
+                qm, step_tokens);
 }
 
 template <int HD>

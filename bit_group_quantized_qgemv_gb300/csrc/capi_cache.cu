@@ -28,7 +28,7 @@ int check_cache(const qgemv_kv_cache* c, KvView* v) {
       c->n_pages < 1 || c->n_kv < 1 || c->n_kv > 1024 || c->n_seqs < 1 || c->n_seqs > 65535 ||
       c->max_pages < 1)
     return QGEMV_EINVAL;
-  if (static_cast<long long>(c->max_pages) * c->page_size > 0x7FFFFFFFLL ||
+  if (static_cast<long long>(c->max_pages) * c->page_size > 1LL << 29 ||
       static_cast<long long>(c->n_pages) * c->n_kv > 0x7FFFFFFFLL / c->page_size)
     return QGEMV_EINVAL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4) ||
@@ -123,11 +123,10 @@ size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache* cache, int n_
     return 0;
   int dev, sms;
   if (qgemv::device_and_sms(&dev, &sms) != QGEMV_OK) return 0;
-  if (qgemv::attention_is_many(n_q / c.n_kv, max_q < n_tokens ? max_q : n_tokens))
-    return qgemv::attention_many_bytes(c.head_dim, sms);
-  const qgemv::AttnSplit sp = qgemv::attention_split(
-      c.n_seqs, c.n_kv, static_cast<long long>(c.max_pages) << c.page_shift, sms);
-  return sp.joins() > 1 ? sp.joins() * qgemv::attention_part_bytes(n_tokens, n_q, c.head_dim) : 0;
+  const int group = n_q / c.n_kv, most = max_q < n_tokens ? max_q : n_tokens;
+  if (qgemv::attention_is_many(group, most)) return qgemv::attention_many_bytes(c.head_dim, sms);
+  return qgemv::attention_few_bytes(c.n_seqs, c.n_kv, most * group, c.head_dim,
+                                    static_cast<long long>(c.max_pages) << c.page_shift, sms);
 }
 
 int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long long q_stride,
@@ -164,19 +163,8 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
   if (qgemv::attention_is_many(a.group, a.max_q))
     return qgemv::report_launch(
         qgemv::attention_many_launch(a, sms, st, dev, workspace, workspace_bytes));
-  const long long cap = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
-  const qgemv::AttnSplit sp = qgemv::attention_fit(
-      qgemv::attention_split(a.c.n_seqs, a.c.n_kv, cap, sms), cap,
-      qgemv::attention_part_bytes(n_tokens, n_q, a.c.head_dim), workspace_bytes);
-  a.n_parts = sp.n_parts;
-  a.part = sp.part;
-  a.cluster = sp.cluster;
-  if (sp.joins() > 1) {  // the outputs of the parts, then their maxima and sums
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(
-        a.part_o + static_cast<size_t>(sp.joins()) * n_tokens * n_q * a.c.head_dim);
-  }
-  return qgemv::report_launch(qgemv::attention_few_launch(a, st, dev));
+  return qgemv::report_launch(
+      qgemv::attention_few_launch(a, sms, st, dev, workspace, workspace_bytes));
 }
 
 int qgemv_attention_mass(const qgemv_kv_cache* cache, const uint16_t* q, long long q_stride,

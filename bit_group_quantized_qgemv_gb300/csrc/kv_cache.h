@@ -34,8 +34,8 @@ struct RopeArgs {
   int* err;
 };
 
-// A unit of query rows whose entries several blocks share (attention_many.cu):
-// what their join has to know.
+// A unit of query rows whose entries several blocks share: what their join has
+// to know.
 struct AttnUnit {
   int parts;  // 0: none
   int s, h, r0, first, rows, off, len;
@@ -52,13 +52,12 @@ struct AttnArgs {
   __half* out;
   long long out_stride;
   float* lse;
-  // Parts of a split cache, `part` entries each: part_o [part][token][n_q]
-  // [head_dim] (not yet divided by the sum), part_ml [part][token][n_q] {max,
-  // sum} in log2 units.  n_parts = 1: nothing is split.
+  // Results of parts of units, two slots per block: part_o [slot][row][head_dim]
+  // (not yet divided by the sum), part_ml [slot][row] {max, sum} in log2 units;
+  // splits [block], null: units are not cut.
   float* part_o;
   float2* part_ml;
-  int n_parts, part, row_tiles;
-  AttnUnit* splits;  // many rows: [blocks], null: units are not split
+  AttnUnit* splits;
   unsigned long long group_inv;  // floor(2^64 / group) + 1
   int cluster;  // thread blocks that join their parts among themselves (1: none)
   int* err;
@@ -93,18 +92,6 @@ cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device);
 cudaError_t cache_evict_launch(const EvictArgs& a, cudaStream_t st, int device);
 
-// How the cache is split for few rows: n_parts parts of `part` entries (1: not split),
-// `cluster` of them joined on chip; what is left of them is joined through
-// the workspace.
-struct AttnSplit {
-  int n_parts, part, cluster;
-  int joins() const { return n_parts / cluster; }
-};
-AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms);
-// The split with the most parts whose workspace fits (`part` grows).
-AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes, size_t workspace_bytes);
-// Bytes of workspace per part.
-size_t attention_part_bytes(int n_tokens, int n_q, int head_dim);
 // Whether a call has more query rows per key/value head than the mma.sync
 // kernel takes in one pass over the cache: those go to the tcgen05 kernel.
 inline bool attention_is_many(int group, int max_q) {
@@ -115,6 +102,10 @@ cudaError_t attention_many_launch(const AttnArgs& a, int sms, cudaStream_t st, i
                                   void* workspace, size_t bytes);
 cudaError_t status_attention(unsigned* out);
 cudaError_t status_mass(unsigned* out);
-cudaError_t attention_few_launch(const AttnArgs& a, cudaStream_t st, int device);
+// Workspace of the kernel for few rows (0: it needs none).
+size_t attention_few_bytes(int n_seqs, int n_kv, int rows, int head_dim, long long capacity,
+                           int sms);
+cudaError_t attention_few_launch(AttnArgs a, int sms, cudaStream_t st, int device, void* workspace,
+                                 size_t bytes);
 
 }  // namespace qgemv

@@ -15,14 +15,17 @@
 // shared memory, the parts of a split cache through the distributed shared
 // memory of a cluster or by a second kernel.
 //
-// P enters as fp16 high and low parts (two products with V), which keeps the
-// weights at 22 bits; the kernel is bound by HBM, not by the products: 48
-// sequences of 900 to 20000 entries (32/8 heads of 128, 1.23 GB) take 184 us,
-// 6.69 TB/s or 99 % of the measured copy bandwidth.
+// Up to 16 rows P enters as fp16 high and low parts (two products with V), which
+// keeps the weights at 22 bits: the kernel is bound by HBM there, not by the
+// products.  48 sequences of 900 to 20000 entries (32/8 heads of 128, 1.23 GB) take
+// 184 us, 6.69 TB/s or 99 % of the measured copy bandwidth.  With more rows the
+// products are the bound, and P is rounded once to fp16, like every weight of the
+// tcgen05 kernel.
 #include <atomic>
 
 #include "attention_common.cuh"
 #include "mma_tile.cuh"
+#include "runs.cuh"
 
 namespace qgemv {
 namespace {
@@ -30,6 +33,9 @@ namespace {
 constexpr int kTile = 16;    // entries per warp and step
 constexpr int kStages = 3;   // ring depth of each warp
 constexpr float kSlack = 8.0f;  // log2 of the growth that makes O be rescaled
+constexpr int kBlock = 64;      // entries that runs of work are counted in
+constexpr int kMinBlocks = 2;   // of a run, at least
+constexpr int kRowsMax = 32;    // rows of a unit
 
 template <int HD>
 __host__ __device__ constexpr int stage_bytes() {
@@ -65,8 +71,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
+// Blocks resident on a multiprocessor: two for heads of 128 (by shared memory;
+// one of eight warps), for heads of 64 four, by the registers of more rows three or
+// two.
+__host__ __device__ constexpr int few_resident(int head_dim, int rows, int warps) {
+  return warps == 8 ? 1 : head_dim == 128 || rows > 24 ? 2 : rows > 16 ? 3 : 4;
+}
+
 template <int HD, int NT, bool LO, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, few_resident(HD, 8 * NT, kWarps))
+    attention_few_kernel(const AttnArgs a) {
   constexpr int kM = HD / 16;      // 16-component tiles of the output, k-steps of the scores
   constexpr int kRows = 8 * NT;
   constexpr int kChunks = HD / 8;  // 16-byte chunks per row
@@ -78,40 +92,73 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
 
-  long long b = blockIdx.x;
-  const int sp = static_cast<int>(b % a.n_parts);
-  b /= a.n_parts;
-  const int h = static_cast<int>(b % a.c.n_kv);
-  b /= a.c.n_kv;
-  const int rt = static_cast<int>(b % a.row_tiles);
-  const int s = static_cast<int>(b / a.row_tiles);
+  constexpr int D = HD / 32;
+  float* so = reinterpret_cast<float*>(smem);  // [warp][row][kOut], once a segment's ring is done
 
-  // The first tile's page number is read along with the lengths.
-  const int k0 = sp * a.part;
-  const int e_first = k0 + warp * kTile;
-  int next = e_first < a.c.max_pages << a.c.page_shift ? raw_page(a.c, s, e_first) : -1;
+  // Blocks of entries of sequence i's units; its units count as one block each
+  // when there is no workspace to join parts of them.
+  const bool cut = a.splits != nullptr;
+  auto blocks_of = [&](int i) {
+    int f, n;
+    seq_rows(a.q_start, i, a.n_tokens, a.err, &f, &n);
+    if (n > a.max_q) flag_error(a.err);
+    const int l = seq_len(a.c, i, a.err);
+    return n == 0 ? 0 : cut ? max(1, (l + kBlock - 1) / kBlock) : 1;
+  };
+  int s, h, j0 = 0;
+  long long left = 1, per = 1;
+  AttnUnit split{};
+  if (a.cluster > 1) {  // a cluster per unit, a part per block of it
+    const int unit = blockIdx.x / a.cluster;
+    s = unit / a.c.n_kv;
+    h = unit % a.c.n_kv;
+  } else {
+    left = run_start(a.c.n_seqs, a.c.n_kv, cut ? kMinBlocks : 1, lane, blocks_of, &per, &s, &h, &j0);
+    if (left <= 0) {
+      if (cut && threadIdx.x == 0) a.splits[blockIdx.x] = split;
+      return;
+    }
+  }
 
+  while (true) {
   int first, count;
-  seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
-  const int len = seq_len(a.c, s, a.err);
-  if (count > a.max_q) flag_error(a.err);
-  const int rows = min(count, a.max_q) * a.group;
-  const int r0 = rt * kRows;
-  if (r0 >= rows) return;
-  const int nr = min(kRows, rows - r0);
+  int* err = a.cluster > 1 ? a.err : nullptr;  // (the others have looked at every length)
+  seq_rows(a.q_start, s, a.n_tokens, err, &first, &count);
+  const int len = seq_len(a.c, s, err);
+  if (a.cluster > 1) {
+    if (count > a.max_q) flag_error(err);
+    if (count == 0) return;
+  }
+  const int nr = min(count, a.max_q) * a.group;
   const int off = len - count;  // token i sees entries up to off + i
-  const int group = sp / a.cluster;  // parts that are joined on chip
-  // (a group behind the sequence's end is left out by the join; blocks of a
-  // group that has entries stay, for the others wait for them)
-  if (group > 0 && group * a.cluster * a.part >= len) return;
-  // entries that some row of this block sees
-  const int see = min(len, off + (r0 + nr - 1) / a.group + 1);
-  const int k1 = min(see, k0 + a.part);
+  // this segment's entries k0 .. k1, of those that some row sees
+  const int see = min(len, off + (nr - 1) / a.group + 1);
+  const int n_blocks = max(1, (len + kBlock - 1) / kBlock);
+  int k0, k1, slot = -1;
+  if (a.cluster > 1) {
+    const int part = (n_blocks + a.cluster - 1) / a.cluster * kBlock;
+    k0 = cluster_rank() * part;
+    k1 = min(see, k0 + part);
+  } else if (!cut) {
+    k0 = 0;
+    k1 = see;
+  } else {
+    const int j1 = static_cast<int>(min(static_cast<long long>(n_blocks), j0 + left));
+    k0 = j0 * kBlock;
+    k1 = min(see, j1 * kBlock);
+    if (j0 > 0 || j1 < n_blocks) slot = 2 * static_cast<int>(blockIdx.x) + (j0 == 0);
+    if (j0 == 0 && j1 < n_blocks)
+      split = AttnUnit{1 + static_cast<int>(run_div(n_blocks - j1 + per - 1, per)), s, h, 0, first, nr, off,
+                       len};
+    left -= j1 - j0;
+  }
+  if (a.cluster == 1 && !cut) --left;
 
   const uint32_t ring = smem_u32(smem) + warp * (kStages * stage_bytes<HD>());
   const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
   unsigned bad = 0;  // bit st: the tile in stage st lies on a bad page
+  int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
 
   // Queries as B fragments: column = row of the block.
   uint32_t qf[NT][kM][2];
@@ -119,7 +166,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = nt * 8 + g;
-    const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group;
+    const int i = r / a.group, head = h * a.group + r % a.group;
     const __half* q = a.q + static_cast<long long>(first + i) * a.q_stride + head * HD + 2 * tq;
 #pragma unroll
     for (int k = 0; k < kM; ++k) {
@@ -129,7 +176,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int c = nt * 8 + 2 * tq + e;
-      lim[nt][e] = c < nr ? off + (r0 + c) / a.group : -1;
+      lim[nt][e] = c < nr ? off + c / a.group : -1;
     }
   }
 
@@ -260,7 +307,6 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   }
   cp_wait<0>();
   __syncthreads();  // every warp is done with its ring: it now takes the partial outputs
-  float* so = reinterpret_cast<float*>(smem);  // [warp][row][kOut]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -283,14 +329,13 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
   }
   __syncthreads();
   // A warp per row: join the warps' parts.
-  constexpr int D = HD / 32;
   const auto finish = [&](int r, float mm, float ll, const float* acc) {
-    const int i = (r0 + r) / a.group, head = h * a.group + (r0 + r) % a.group, t = first + i;
-    if (a.n_parts == a.cluster) {
+    const int i = r / a.group, head = h * a.group + r % a.group, t = first + i;
+    if (slot < 0) {
       store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
       return;
     }
-    const long long at = (static_cast<long long>(group) * a.n_tokens + t) * a.n_q + head;
+    const long long at = static_cast<long long>(slot) * kRowsMax + r;
 #pragma unroll
     for (int d = 0; d < D; ++d) a.part_o[at * HD + lane * D + d] = acc[d];
     if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
@@ -321,9 +366,25 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
       sm_l[0][r] = ll;
     }
   }
-  if (a.cluster == 1) return;
+  if (a.cluster > 1) break;
+  if (left <= 0) break;
+  j0 = 0;
+  if (++h == a.c.n_kv) {
+    h = 0;
+    s = run_next(s, a.c.n_seqs, lane, blocks_of);
+    if (s >= a.c.n_seqs) break;
+  }
+  __syncthreads();  // the next segment's ring takes the place of these outputs
+  }
+  if (a.cluster == 1) {
+    if (cut && threadIdx.x == 0) a.splits[blockIdx.x] = split;
+    return;
+  }
   // The blocks of a cluster join theirs through distributed shared memory,
   // each for some of the rows.
+  int first, count;
+  seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
+  const int len = seq_len(a.c, s, nullptr), nr = min(count, a.max_q) * a.group;
   cluster_sync();
   for (int r = cluster_rank() * kWarps + warp; r < nr; r += a.cluster * kWarps) {
     const uint32_t m_at = smem_u32(&sm_m[0][r]), l_at = smem_u32(&sm_l[0][r]);
@@ -353,33 +414,34 @@ __global__ void __launch_bounds__(32 * kWarps) attention_few_kernel(const AttnAr
 #pragma unroll
       for (int d = 0; d < D; ++d) acc[d] += po[c][d] * f;
     }
-    finish(r, mm, ll, acc);
+    const int i = r / a.group;
+    store_row<HD>(a, s, h, first + i, h * a.group + r % a.group, min(len - count + i, len - 1), len,
+                  acc, mm, ll, lane);
   }
   cluster_sync();  // no block ends while another reads its shared memory
 }
 
-// Join the parts of a split cache: a block per (token, query head), its warps
-// take the parts in turn.
-constexpr int kJoinWarps = 4;
+// Join the parts of cut units: block c of the kernel above has the first part of
+// at most one (in its slot 1), the blocks behind it the others (in their slots
+// 0).  Four rows a block, the four warps of a row take the parts in turn.
+constexpr int kJoinWarps = 4, kJoinRows = 4;
 
 template <int HD>
-__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps * kJoinRows)
+    attention_join_kernel(const AttnArgs a, int row_blocks) {
   constexpr int D = HD / 32;
-  __shared__ float so[kJoinWarps][HD], sm[kJoinWarps], sl[kJoinWarps];
+  __shared__ float s_o[kJoinRows][kJoinWarps][HD], s_m[kJoinRows][kJoinWarps], s_l[kJoinRows][kJoinWarps];
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // (sequence, token within it, head)
-  const int head = blockIdx.x % a.n_q;
-  const int i = blockIdx.x / a.n_q % a.max_q, s = blockIdx.x / a.n_q / a.max_q;
-  int first, count;
-  seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
-  if (i >= count) return;
-  const int t = first + i;
-  const int len = seq_len(a.c, s, nullptr);
-  const int parts = max(1, (len + a.part * a.cluster - 1) / (a.part * a.cluster));
-  const long long step = static_cast<long long>(a.n_tokens) * a.n_q;
-  const long long at = static_cast<long long>(t) * a.n_q + head;
+  const int warp = (threadIdx.x >> 5) % kJoinWarps, row = threadIdx.x / (32 * kJoinWarps);
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x / row_blocks, r = blockIdx.x % row_blocks * kJoinRows + row;
+  auto& so = s_o[row];
+  auto& sm = s_m[row];
+  auto& sl = s_l[row];
+  const AttnUnit unit = a.splits[c];
+  const int parts = unit.parts;
+  if (parts == 0 || r >= unit.rows) return;  // all warps of the row
   float m = -INFINITY, l = 0.f, acc[D] = {};
   constexpr int kU = 8;  // parts in flight per warp
   for (int p0 = warp; p0 < parts; p0 += kJoinWarps * kU) {
@@ -392,8 +454,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
 #pragma unroll
       for (int d = 0; d < D; ++d) o[u][d] = 0.f;
       if (p < parts) {
-        ml[u] = a.part_ml[p * step + at];
-        const float* src = a.part_o + (p * step + at) * HD + lane * D;
+        const long long at = static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * kRowsMax + r;
+        ml[u] = a.part_ml[at];
+        const float* src = a.part_o + at * HD + lane * D;
         if constexpr (D == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
           o[u][0] = v.x, o[u][1] = v.y, o[u][2] = v.z, o[u][3] = v.w;
@@ -426,7 +489,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
     sm[warp] = m;
     sl[warp] = l;
   }
-  __syncthreads();
+  named_bar_sync(1 + row, 32 * kJoinWarps);  // the warps of this row
   if (warp != 0) return;
 #pragma unroll
   for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, sm[w]);
@@ -441,12 +504,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const A
 #pragma unroll
     for (int d = 0; d < D; ++d) acc[d] += so[w][lane * D + d] * f;
   }
-  store_row<HD>(a, s, head / a.group, t, head, min(len - count + i, len - 1), len, acc, m, l, lane);
+  const int i = r / a.group;
+  store_row<HD>(a, unit.s, unit.h, unit.first + i, unit.h * a.group + r % a.group,
+                min(unit.off + i, unit.len - 1), unit.len, acc, m, l, lane);
 }
 
-template <typename F>
+template <typename F, typename... Args>
 cudaError_t launch_pdl(F* k, long long blocks, int threads, int smem, int cluster, cudaStream_t st,
-                       const AttnArgs& a) {
+                       Args... args) {
   if (blocks < 1 || blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -462,11 +527,14 @@ cudaError_t launch_pdl(F* k, long long blocks, int threads, int smem, int cluste
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, a);
+  return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
+// Blocks of a call: as many as are resident at once.
+int few_blocks(int head_dim, int rows, int sms) { return sms * few_resident(head_dim, rows, 4); }
+
 template <int HD, int NT, bool LO, int kWarps>
-cudaError_t launch_few(AttnArgs a, cudaStream_t st, int device) {
+cudaError_t launch_few(const AttnArgs& a, int sms, cudaStream_t st, int device) {
   static std::atomic<unsigned long long> done{0};
   constexpr int smem = kWarps * kStages * stage_bytes<HD>();
   static_assert(kWarps * 8 * NT * (HD + 4) * 4 <= smem, "the warps' outputs take the ring's place");
@@ -477,9 +545,9 @@ cudaError_t launch_few(AttnArgs a, cudaStream_t st, int device) {
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  a.row_tiles = (a.max_q * a.group + 8 * NT - 1) / (8 * NT);
-  const long long blocks =
-      static_cast<long long>(a.c.n_seqs) * a.row_tiles * a.c.n_kv * a.n_parts;
+  const long long blocks = a.cluster > 1
+                               ? static_cast<long long>(a.c.n_seqs) * a.c.n_kv * a.cluster
+                               : few_blocks(HD, a.max_q * a.group, sms);
   return launch_pdl(k, blocks, 32 * kWarps, smem, a.cluster, st, a);
 }
 
@@ -492,23 +560,24 @@ int few_warps(int rows, int cluster, int units) {
 }
 
 template <int HD>
-cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
+cudaError_t launch_few_rows(const AttnArgs& a, int sms, cudaStream_t st, int device) {
   const int rows = a.max_q * a.group;
   const bool wide = few_warps(rows, a.cluster, a.c.n_seqs * a.c.n_kv) == 8;
   if (rows <= 8)
-    return wide ? launch_few<HD, 1, true, 8>(a, st, device) : launch_few<HD, 1, true, 4>(a, st, device);
+    return wide ? launch_few<HD, 1, true, 8>(a, sms, st, device)
+                : launch_few<HD, 1, true, 4>(a, sms, st, device);
   if (rows <= 16)
-    return wide ? launch_few<HD, 2, true, 8>(a, st, device) : launch_few<HD, 2, true, 4>(a, st, device);
-  if (rows <= 24) return launch_few<HD, 3, true, 4>(a, st, device);
-  return launch_few<HD, 4, true, 4>(a, st, device);
+    return wide ? launch_few<HD, 2, true, 8>(a, sms, st, device)
+                : launch_few<HD, 2, true, 4>(a, sms, st, device);
+  if (rows <= 24) return launch_few<HD, 3, false, 4>(a, sms, st, device);
+  return launch_few<HD, 4, false, 4>(a, sms, st, device);
 }
 
-}  // namespace
-
-// How the cache is split for few rows, by the number of (sequence, head)
-// units and the capacity (the lengths are on the device).  Measured on GB300,
-// 32/8 heads of 128, one new token per sequence, replayed from a graph, clusters of
-// 8 blocks that join on chip against parts joined by a second kernel:
+// Whether a cluster of blocks takes each (sequence, head) unit and joins on
+// chip, by the number of units and the capacity (the lengths are on the device);
+// otherwise the entries are cut into equal runs (runs.cuh), joined by a second
+// kernel.  Measured on GB300, 32/8 heads of 128, one new token per sequence,
+// replayed from a graph, clusters of 8 against parts joined by a second kernel:
 //   1 sequence   1000 entries  5.7 us against 6.1;   4110  8.0 against 7.4;
 //                8000         10.6 against 8.3
 //   4 sequences  1000          7.4 against 7.0;      2000  9.1 against 10.2
@@ -517,54 +586,51 @@ cudaError_t launch_few_rows(const AttnArgs& a, cudaStream_t st, int device) {
 // 8 heads up to parts of 576 entries, and more units up to 256 while their
 // blocks fill the machine at most once.  With longer caches a cluster lasts as
 // long as its sequence.
-//   Otherwise parts: for one sequence as many as fill the machine once; for
-// several, of 128 to 1024 entries, one per multiprocessor were every sequence as
-// long as its page table allows, so that unlike lengths balance (48 sequences of
-// 900 to 20000 entries: 1024-entry parts 184 us, one part per sequence 344 us;
-// four of 8000: this 26 us, four parts per multiprocessor 31, sixteen 37).
-AttnSplit attention_split(int n_seqs, int n_kv, long long capacity, int sms) {
+int few_cluster(int n_seqs, int n_kv, long long capacity, int sms) {
   const long long units = static_cast<long long>(n_kv) * n_seqs;
-  if (capacity <= 128) return {1, static_cast<int>(capacity), 1};
-  if (capacity <= kMaxCluster * (units <= 8 ? 576 : 256) && units <= 2 * sms / kMaxCluster) {
-    const long long part = ((capacity + kMaxCluster - 1) / kMaxCluster + 63) / 64 * 64;
-    return {kMaxCluster, static_cast<int>(part), kMaxCluster};
+  const bool fits = capacity > 128 && units <= 2 * sms / kMaxCluster &&
+                    capacity <= kMaxCluster * (units <= 8 ? 576 : 256);
+  return fits ? kMaxCluster : 1;
+}
+
+}  // namespace
+
+size_t attention_few_bytes(int n_seqs, int n_kv, int rows, int head_dim, long long capacity,
+                           int sms) {
+  if (few_cluster(n_seqs, n_kv, capacity, sms) > 1 || capacity <= 128) return 0;
+  return static_cast<size_t>(few_blocks(head_dim, rows, sms)) *
+         (2 * kRowsMax * (static_cast<size_t>(head_dim) * 4 + 8) + sizeof(AttnUnit));
+}
+
+cudaError_t attention_few_launch(AttnArgs a, int sms, cudaStream_t st, int device, void* workspace,
+                                 size_t bytes) {
+  const int hd = a.c.head_dim, rows = a.max_q * a.group;
+  const long long capacity = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
+  const size_t need = attention_few_bytes(a.c.n_seqs, a.c.n_kv, rows, hd, capacity, sms);
+  const int blocks = few_blocks(hd, rows, sms);
+  a.cluster = few_cluster(a.c.n_seqs, a.c.n_kv, capacity, sms);
+  a.splits = nullptr;
+  if (need > 0 && bytes >= need) {  // outputs, {max, sum}, what the join needs
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2LL * blocks * kRowsMax * hd);
+    a.splits = reinterpret_cast<AttnUnit*>(a.part_ml + 2LL * blocks * kRowsMax);
   }
-  long long part;
-  if (n_seqs == 1 && units <= 2 * sms) {
-    const long long n = 2LL * sms / units;
-    part = ((capacity + n - 1) / n + 63) / 64 * 64;
-    if (part < 128) part = 128;
-  } else {
-    part = capacity * units / sms / 64 * 64;
-    if (part < 128) part = 128;
-    if (part > 1024) part = 1024;
+  auto run = [&] {
+    return hd == 64 ? launch_few_rows<64>(a, sms, st, device)
+                    : launch_few_rows<128>(a, sms, st, device);
+  };
+  cudaError_t e = run();
+  if (e != cudaSuccess && a.cluster > 1) {  // a device that cannot host the clusters
+    cudaGetLastError();
+    a.cluster = 1;
+    e = run();
   }
-  if (capacity <= part) return {1, static_cast<int>(capacity), 1};
-  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
-}
-
-AttnSplit attention_fit(AttnSplit s, long long capacity, size_t part_bytes,
-                        size_t workspace_bytes) {
-  const size_t fit = workspace_bytes / part_bytes;
-  if (s.joins() <= 1 || fit >= static_cast<size_t>(s.joins())) return s;
-  const long long n = static_cast<long long>(fit);
-  if (n <= 1) return {1, static_cast<int>(capacity), 1};
-  const long long part = ((capacity + n - 1) / n + 127) / 128 * 128;
-  return {static_cast<int>((capacity + part - 1) / part), static_cast<int>(part), 1};
-}
-
-size_t attention_part_bytes(int n_tokens, int n_q, int head_dim) {
-  return static_cast<size_t>(n_tokens) * n_q * (static_cast<size_t>(head_dim) * 4 + 8);
-}
-
-cudaError_t attention_few_launch(const AttnArgs& a, cudaStream_t st, int device) {
-  const cudaError_t e = a.c.head_dim == 64 ? launch_few_rows<64>(a, st, device)
-                                           : launch_few_rows<128>(a, st, device);
-  if (e != cudaSuccess || a.n_parts == a.cluster) return e;
-  const long long rows = static_cast<long long>(a.c.n_seqs) * a.max_q * a.n_q;
-  return a.c.head_dim == 64
-             ? launch_pdl(attention_join_kernel<64>, rows, 32 * kJoinWarps, 0, 1, st, a)
-             : launch_pdl(attention_join_kernel<128>, rows, 32 * kJoinWarps, 0, 1, st, a);
+  if (e != cudaSuccess || a.splits == nullptr) return e;
+  const int row_blocks = (rows + kJoinRows - 1) / kJoinRows, threads = 32 * kJoinWarps * kJoinRows;
+  const long long joins = static_cast<long long>(blocks) * row_blocks;
+  return hd == 64
+             ? launch_pdl(attention_join_kernel<64>, joins, threads, 0, 1, st, a, row_blocks)
+             : launch_pdl(attention_join_kernel<128>, joins, threads, 0, 1, st, a, row_blocks);
 }
 
 }  // namespace qgemv

@@ -493,7 +493,7 @@ int qgemv_lut4(const uint32_t *codes, const uint16_t *lut, int n_luts, int rows_
  * sequence: they are neither read nor written.
  * Checks of the four calls: head_dim 64 or 128; page_size 16, 32, 64, 128 or
  * 256; n_pages, n_kv, n_seqs, max_pages >= 1; n_seqs <= 65535; n_kv <= 1024;
- * max_pages * page_size and n_pages * n_kv * page_size < 2^31 (EINVAL).
+ * max_pages * page_size <= 2^29, n_pages * n_kv * page_size < 2^31 (EINVAL).
  * What lies on the device is checked by the kernels, which set *err_flag = 1
  * (device int or NULL; never cleared by the library) and go on: a page number
  * outside [0, n_pages) is an entry that nothing sees, reads or writes; a
