@@ -594,7 +594,7 @@ def _token_rows(cache, t, name, rows=None, width=None):
         raise ValueError(f"{name} must be rows of tokens, contiguous within a row")
     if (width is not None and w != width) or (rows is not None and n != rows):
         raise ValueError(f"{name} has {n} rows of {w}, expected {rows} of {width}")
-    return t.data_ptr(), n, w, stride[0] if n > 1 else max(stride[0], w)
+    return t.data_ptr(), n, w, stride[0] if n > 1 else w
 
 
 def _heads(cache, width, extra, name):

@@ -47,8 +47,8 @@ int check_cache(const qgemv_kv_cache* c, KvView* v) {
   return QGEMV_OK;
 }
 
-// Query-side shape: n_q a multiple of n_kv, the rows of a sequence and the
-// thread blocks over them countable in 31 bits.
+// Query-side shape: n_q a multiple of n_kv, the rows of a sequence countable in
+// 30 bits.
 int check_queries(const KvView& c, long long q_stride, int n_tokens, int n_q, int max_q,
                   float scale) {
   if (n_tokens < 0 || n_q < 1 || n_q % c.n_kv != 0 || n_q > 65535 || max_q < 1 ||
@@ -57,7 +57,7 @@ int check_queries(const KvView& c, long long q_stride, int n_tokens, int n_q, in
   if (q_stride < static_cast<long long>(n_q) * c.head_dim || q_stride % 8 != 0)
     return QGEMV_EINVAL;
   const long long rows = static_cast<long long>(max_q) * (n_q / c.n_kv);
-  if (rows > 0x3FFFFFFFLL || rows / 16 * c.n_kv * c.n_seqs > 0x3FFFFFFFLL) return QGEMV_EINVAL;
+  if (rows > 0x3FFFFFFFLL) return QGEMV_EINVAL;
   return QGEMV_OK;
 }
 
@@ -204,7 +204,7 @@ int qgemv_cache_evict(const qgemv_kv_cache* cache, const float* mass, const int3
   if (int rc = check_cache(cache, &a.c)) return rc;
   if (!mass || !entry_pos || !next_pos || !kept || !mass_out || !pos_out || !kv_len_out)
     return QGEMV_ENULL;
-  if (keep < 1 || n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > keep)
+  if (keep < 1 || keep > 1 << 30 || n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > keep)
     return QGEMV_EINVAL;
   // an output that is an input would be read after it has been written
   if (mass_out == mass || pos_out == entry_pos || kv_len_out == cache->kv_len) return QGEMV_EINVAL;

@@ -138,7 +138,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_append_kernel(const
   const bool rot = l < rl;
   const int d0 = rot ? 4 * l : rd + 4 * (l - rl);
   const int d1 = rot ? rd / 2 + 4 * l : rd + (HD - rd) / 2 + 4 * (l - rl);
-  // Weights, read before the wait for the previous kernel.
+  pdl_wait();
+  const int t = static_cast<int>(task / groups);
+  if (t >= a.n_tokens) return;
+  // (frequencies and norms may be what the kernel before has just made: they are read
+  // after the wait, along with the token's position and sequence)
   float f[4] = {0.f, 0.f, 0.f, 0.f};
   if (rot)
 #pragma unroll
@@ -151,9 +155,6 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_append_kernel(const
     g[1][0] = *reinterpret_cast<const uint2*>(a.k_norm + d0);
     g[1][1] = *reinterpret_cast<const uint2*>(a.k_norm + d1);
   }
-  pdl_wait();
-  const int t = static_cast<int>(task / groups);
-  if (t >= a.n_tokens) return;
   const int n_kv = a.c.n_kv;
   const int q_passes = (a.n_q + kPerPass - 1) / kPerPass, kv_passes = (n_kv + kPerPass - 1) / kPerPass;
   const int p0 = static_cast<int>(task % groups) * per_warp;

@@ -527,8 +527,8 @@ typedef struct {
  *   positions int32 [n_tokens] (any value; the angle is reduced from the exact
  *   product), inv_freq fp32 [rotary_dim/2], both device; strides in elements,
  *   multiples of 4; qkv, q_out, norms 8-byte aligned, the rest 4-byte.
- *   Checks: n_tokens >= 0 (0: nothing is enqueued), n_q a multiple of n_kv,
- *   0 <= rotary_dim <= head_dim, a multiple of 8, qkv_stride >= (n_q + 2
+ *   Checks: n_tokens >= 0 (0: nothing is enqueued), n_q a multiple of n_kv and at
+ *   most 65535, 0 <= rotary_dim <= head_dim, a multiple of 8, qkv_stride >= (n_q + 2
  *   n_kv) * head_dim, q_stride >= n_q * head_dim, eps > 0 when normed, the
  *   norms both given or both NULL.  One launch.
  */
@@ -553,12 +553,15 @@ int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
  *   q, out: fp16 rows of n_q * head_dim, strides in elements; 16-byte aligned,
  *   strides multiples of 8.  lse: fp32 [n_tokens][n_q] or NULL.
  *   max_q: the largest q_len (tokens beyond it are left out and set
- *   *err_flag).  scale > 0.
+ *   *err_flag).  Checks: n_tokens >= 0, n_q a multiple of n_kv and at most 65535,
+ *   1 <= max_q <= 2^24, max_q * (n_q / n_kv) < 2^30, scale finite and > 0.
  *   workspace: device, 16-byte aligned, workspace_bytes long, contents on entry
  *   ignored; with fewer than qgemv_paged_attention_workspace_bytes bytes (NULL
- *   and 0 too) the cache is split over fewer thread blocks, which is slower.
- *   Calls sharing a workspace must not overlap on the GPU.
- * Up to two launches (the second joins the parts of a split cache).
+ *   and 0 too) a sequence's cache is not split over thread blocks, which can be
+ *   much slower for few long sequences.  Calls sharing a workspace must not
+ *   overlap on the GPU.
+ * Up to two launches (the second joins the parts of a split cache).  How far a
+ * page table reaches beyond the sequences costs nothing.
  */
 int qgemv_paged_attention(const qgemv_kv_cache *cache, const uint16_t *q, long long q_stride,
                           int n_tokens, int n_q, const int32_t *q_start, int max_q, float scale,
@@ -606,8 +609,8 @@ int qgemv_attention_mass(const qgemv_kv_cache *cache, const uint16_t *q, long lo
  *            as they were from there on
  *   kv_len_out int32 [n_seqs]: len'
  * The outputs may not overlap the inputs.  An entry of kept whose page, old or
- * new, is bad is listed but not copied.  Checks: keep >= 1, n_sink, n_recent
- * >= 0, n_sink + n_recent <= keep.  Two launches.
+ * new, is bad is listed but not copied.  Checks: 1 <= keep <= 2^30, n_sink and
+ * n_recent >= 0, n_sink + n_recent <= keep.  Two launches.
  */
 int qgemv_cache_evict(const qgemv_kv_cache *cache, const float *mass, const int32_t *entry_pos,
                       const int32_t *next_pos, int keep, int n_sink, int n_recent, int32_t *kept,

@@ -95,6 +95,50 @@ def test_attention_and_mass(case):
     assert int(err) == 0 and q.device_status() == 0
 
 
+def _ragged(seed, n, most, longest):
+    g = np.random.default_rng(seed)
+    new = g.integers(0, most + 1, n)
+    return [(int(m), int(m + g.integers(0, longest))) for m in new]
+
+
+WIDE = [
+    # hd, page, n_q, n_kv, sequences, page-table columns that no sequence needs
+    (128, 16, 4, 2, [(1, 500)], 4000),                          # a table for 64,000 entries
+    (64, 64, 6, 2, [(3, 700), (1, 90)], 3000),
+    (128, 16, 8, 4, [(1, 6000), (2, 5000), (0, 7000), (1, 1)], 1),  # runs over the ends of units
+    (64, 32, 24, 2, [(2, 9000)], 0),                            # 24 rows in many parts
+    (128, 64, 8, 1, [(40, 9000)], 1),                           # 320 rows in many parts
+    (64, 16, 4, 2, [(150, 3100), (20, 20)], 2000),
+    (64, 16, 160, 1, [(1, 100), (2, 37)], 1),                   # 160 query heads to a key head
+    (64, 16, 2, 1, _ragged(1, 40, 3, 200), 1),                  # more sequences than lanes
+    (64, 16, 4, 2, _ragged(2, 40, 40, 300), 1),
+    (128, 32, 4, 1, _ragged(3, 18, 60, 400), 20),
+    (64, 16, 2, 2, [(0, 9)] * 70 + [(1, 33)] + [(0, 0)] * 40 + [(2, 5)], 1),
+    (64, 16, 2, 2, [(0, 9)] * 70 + [(40, 333)] + [(0, 0)] * 40 + [(2, 5)], 1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_wide_tables_many_sequences_and_many_parts(case):
+    hd, page, n_q, n_kv, seqs, extra = WIDE[case]
+    c = ref.make_cache(50 + case, seqs, n_kv, hd, page, extra_pages=extra)
+    T, scale = sum(m for m, _ in seqs), hd ** -0.5
+    x = queries(50 + case, T, n_q, hd)
+    h, xd, qs = handle(c), x.cuda(), c.q_start.cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    max_q = max(m for m, _ in seqs)
+    want, want_lse, tol, lse_tol = ref.attention(c, x, scale)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for ws in (None, none):
+        out, lse = q.paged_attention(h, xd, qs, max_q=max_q, want_lse=True, workspace=ws, err_flag=err)
+        close(out.view(T, n_q, hd), want, tol, "out")
+        close(lse, want_lse, lse_tol, "lse")
+    got = q.attention_mass(h, xd, qs, lse, max_q=max_q, err_flag=err)
+    want_m, tol_m = ref.attention_mass(c, x, lse.cpu(), scale, torch.zeros(len(seqs), n_kv, c.cap))
+    close(got, want_m, tol_m, "mass")
+    assert int(err) == 0 and q.device_status() == 0
+
+
 def test_attention_weights_add_up():
     """Over the entries of a sequence the weights of its rows sum to one each."""
     hd, n_q, n_kv, seqs = 128, 8, 2, [(1, 5000), (40, 2100)]
@@ -305,13 +349,15 @@ EVICT = [
     (64, 128, 8, [777], 400, 300, 100, "odd"),
     (64, 16, 1, [5000, 4097], 4096, 4, 32, "ties"),
     (128, 256, 2, [600], 1000, 1, 1, "random"),
+    (64, 256, 2, [700, 90], 60, 3, 9, "wide"),   # a table for 80,000 entries: keys made anew
 ]
 
 
 @pytest.mark.parametrize("case", range(len(EVICT)))
 def test_evict(case):
     hd, page, n_kv, lens, keep, sink, recent, kind = EVICT[case]
-    c = ref.make_cache(case, [(0, n) for n in lens], n_kv, hd, page, poison=False)
+    c = ref.make_cache(case, [(0, n) for n in lens], n_kv, hd, page, poison=False,
+                       extra_pages=310 if kind == "wide" else 1)
     S, g = len(lens), torch.Generator().manual_seed(case)
     mass = torch.rand(S, n_kv, c.cap, generator=g) * 10
     if kind == "ties":

@@ -72,7 +72,7 @@ def test_cache_descriptor(call):
     for kw in (dict(page_size=8), dict(page_size=512), dict(page_size=48), dict(page_size=0),
                dict(page_size=-16), dict(head_dim=32), dict(head_dim=96), dict(head_dim=256),
                dict(n_pages=0), dict(n_kv=0), dict(n_kv=1025), dict(n_seqs=0), dict(n_seqs=65536),
-               dict(max_pages=0), dict(max_pages=-1), dict(max_pages=1 << 27),
+               dict(max_pages=0), dict(max_pages=-1), dict(max_pages=(1 << 25) + 1),
                dict(n_pages=1 << 26, n_kv=2)):
         assert call(cache(**kw)) == EINVAL, kw
     for kw in (dict(k=0x10008), dict(v=0x10002), dict(page_table=0x10002), dict(kv_len=0x10001)):
@@ -131,7 +131,7 @@ def test_mass_checks():
 def test_evict_checks():
     for n in ("mass", "pos", "nxt", "kept", "mass_out", "pos_out", "len_out"):
         assert evict(**{n: None}) == ENULL
-    for kw in (dict(keep=0), dict(keep=-1), dict(sink=-1), dict(recent=-1), dict(sink=5, recent=4),
+    for kw in (dict(keep=0), dict(keep=-1), dict(keep=(1 << 30) + 1), dict(sink=-1), dict(recent=-1), dict(sink=5, recent=4),
                dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), dict(mass_out=ptr(0x1000)),
                dict(pos_out=ptr(0x2000)), dict(len_out=ptr(0x40000))):
         assert evict(**kw) == EINVAL, kw
