@@ -226,7 +226,7 @@ int qgemv_cache_evict(const qgemv_kv_cache* cache, const float* mass, const int3
   a.len_out = kv_len_out;
   a.err = err_flag;
   return qgemv::report_launch(
-      qgemv::cache_evict_launch(a, static_cast<cudaStream_t>(stream), dev));
+      qgemv::cache_evict_launch(a, sms, static_cast<cudaStream_t>(stream), dev));
 }
 
 }  // extern "C"

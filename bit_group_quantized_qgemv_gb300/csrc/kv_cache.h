@@ -90,7 +90,7 @@ struct EvictArgs {
 
 cudaError_t rope_append_launch(const RopeArgs& a, int sms, cudaStream_t st);
 cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, int device);
-cudaError_t cache_evict_launch(const EvictArgs& a, cudaStream_t st, int device);
+cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st, int device);
 
 // Whether a call has more query rows per key/value head than the mma.sync
 // kernel takes in one pass over the cache: those go to the tcgen05 kernel.

@@ -350,6 +350,7 @@ EVICT = [
     (64, 16, 1, [5000, 4097], 4096, 4, 32, "ties"),
     (128, 256, 2, [600], 1000, 1, 1, "random"),
     (64, 256, 2, [700, 90], 60, 3, 9, "wide"),   # a table for 80,000 entries: keys made anew
+    (64, 16, 4, [(37 * i) % 120 + 20 for i in range(40)], 50, 2, 8, "ties"),  # 160 heads
 ]
 
 
