@@ -58,6 +58,7 @@ struct AttnArgs {
   float* part_o;
   float2* part_ml;
   AttnUnit* splits;
+  int* first_of;  // few rows: [unit] the block with its first part, null: not kept
   unsigned long long group_inv;  // floor(2^64 / group) + 1
   int cluster;  // thread blocks that join their parts among themselves (1: none)
   int* err;
