@@ -664,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = g.first + i, head = g.h * a.group + (live ? rr - i * a.group : 0);
       if (ok && g.slot >= 0) {
         const long long at = static_cast<long long>(g.slot) * kUnitRows + x * kTile + r;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.part_o) & 31) == 0;
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           uint32_t o[32];
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (live)
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) store32(a.part_o + at * HD + c + k, o + k, true);
+            for (int k = 0; k < 32; k += 8) store32(a.part_o + at * HD + c + k, o + k, wide);
         }
         if (live) a.part_ml[at] = make_float2(m, l);
       } else if (ok) {
@@ -748,44 +749,44 @@ __global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(co
   if (u.parts == 0) return;
   for (int r = blockIdx.x % kJoinBlocks * kJoinRows + (threadIdx.x >> 5); r < kUnitRows;
        r += kJoinBlocks * kJoinRows) {
-  const int rr = u.r0 + r;
-  if (rr >= u.rows) return;
-  float m = -INFINITY, l = 0.f, acc[D] = {};
-  for (int p0 = 0; p0 < u.parts; p0 += kU) {
-    float2 ml[kU];
-    float o[kU][D];
+    const int rr = u.r0 + r;
+    if (rr >= u.rows) return;
+    float m = -INFINITY, l = 0.f, acc[D] = {};
+    for (int p0 = 0; p0 < u.parts; p0 += kU) {
+      float2 ml[kU];
+      float o[kU][D];
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const int p = p0 + k;
-      ml[k] = make_float2(-INFINITY, 0.f);
+      for (int k = 0; k < kU; ++k) {
+        const int p = p0 + k;
+        ml[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int d = 0; d < D; ++d) o[k][d] = 0.f;
-      if (p < u.parts) {
-        const long long at = static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * kUnitRows + r;
-        ml[k] = a.part_ml[at];
+        for (int d = 0; d < D; ++d) o[k][d] = 0.f;
+        if (p < u.parts) {
+          const long long at = static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * kUnitRows + r;
+          ml[k] = a.part_ml[at];
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[k][d] = a.part_o[at * HD + lane * D + d];
+          for (int d = 0; d < D; ++d) o[k][d] = a.part_o[at * HD + lane * D + d];
+        }
       }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kU; ++k) mn = fmaxf(mn, ml[k].x);
+      const float base = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - base);
+      l *= f0;
+#pragma unroll
+      for (int d = 0; d < D; ++d) acc[d] *= f0;
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const float f = ex2(ml[k].x - base);
+        l += ml[k].y * f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) acc[d] += o[k][d] * f;
+      }
+      m = mn;
     }
-    float mn = m;
-#pragma unroll
-    for (int k = 0; k < kU; ++k) mn = fmaxf(mn, ml[k].x);
-    const float base = mn == -INFINITY ? 0.f : mn, f0 = ex2(m - base);
-    l *= f0;
-#pragma unroll
-    for (int d = 0; d < D; ++d) acc[d] *= f0;
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const float f = ex2(ml[k].x - base);
-      l += ml[k].y * f;
-#pragma unroll
-      for (int d = 0; d < D; ++d) acc[d] += o[k][d] * f;
-    }
-    m = mn;
-  }
-  const int i = rr / a.group;
-  store_row<HD>(a, u.s, u.h, u.first + i, u.h * a.group + rr % a.group, min(u.off + i, u.len - 1),
-                u.len, acc, m, l, lane);
+    const int i = rr / a.group;
+    store_row<HD>(a, u.s, u.h, u.first + i, u.h * a.group + rr % a.group, min(u.off + i, u.len - 1),
+                  u.len, acc, m, l, lane);
   }
 }
 

@@ -59,120 +59,120 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(NT)) mass_few_kernel
   int s, h, j0;
   long long per, left = run_start(a.c.n_seqs, a.c.n_kv, 2, lane, blocks_of, &per, &s, &h, &j0);
   while (left > 0) {  // segments of this block's run
-  const int len = seq_len(a.c, s, nullptr);
-  int first, count;
-  seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
-  if (count > a.max_q) flag_error(a.err);
-  const int j1 = static_cast<int>(min(static_cast<long long>((len + 63) / 64), j0 + left));
-  const int k0 = j0 * 64, k1 = min(len, j1 * 64);
-  left -= j1 - j0;
-  const int rows = min(count, a.max_q) * a.group, off = len - count;
-  const int tiles = (k1 - k0 + kTile - 1) / kTile;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  const uint32_t ring = smem_u32(smem) + warp * (kStages * key_bytes<HD>());
-  const long long entries = (static_cast<long long>(s) * a.c.n_kv + h) *
-                            (static_cast<long long>(a.c.max_pages) << a.c.page_shift);
+    const int len = seq_len(a.c, s, nullptr);
+    int first, count;
+    seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
+    if (count > a.max_q) flag_error(a.err);
+    const int j1 = static_cast<int>(min(static_cast<long long>((len + 63) / 64), j0 + left));
+    const int k0 = j0 * 64, k1 = min(len, j1 * 64);
+    left -= j1 - j0;
+    const int rows = min(count, a.max_q) * a.group, off = len - count;
+    const int tiles = (k1 - k0 + kTile - 1) / kTile;
+    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * key_bytes<HD>());
+    const long long entries = (static_cast<long long>(s) * a.c.n_kv + h) *
+                              (static_cast<long long>(a.c.max_pages) << a.c.page_shift);
 
-  int r0 = 0;
-  do {  // one walk over the entries for every kRows rows (and one if there are none)
-    const int nr = min(kRows, rows - r0);
-    uint32_t qf[NT][kM][2];
-    float ls[NT][2];
-    int lim[NT][2];
+    int r0 = 0;
+    do {  // one walk over the entries for every kRows rows (and one if there are none)
+      const int nr = min(kRows, rows - r0);
+      uint32_t qf[NT][kM][2];
+      float ls[NT][2];
+      int lim[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      const __half* q = a.q + static_cast<long long>(first + (r0 + r) / a.group) * a.q_stride +
-                        (h * a.group + (r0 + r) % a.group) * HD + 2 * tq;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+        const __half* q = a.q + static_cast<long long>(first + (r0 + r) / a.group) * a.q_stride +
+                          (h * a.group + (r0 + r) % a.group) * HD + 2 * tq;
 #pragma unroll
-      for (int k = 0; k < kM; ++k) {
-        qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
-        qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+        for (int k = 0; k < kM; ++k) {
+          qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+          qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = nt * 8 + 2 * tq + e, rr = r0 + c;
+          float v = -INFINITY;
+          if (c < nr)
+            v = a.lse[static_cast<long long>(first + rr / a.group) * a.n_q + h * a.group + rr % a.group];
+          lim[nt][e] = c < nr && v != -INFINITY ? off + rr / a.group : -1;  // a row that saw nothing
+          ls[nt][e] = v * kLog2e;
+        }
       }
+      unsigned bad = 0;
+      int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
+      auto issue = [&](int it) {
+        if (it < mine) {
+          const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
+          const uint32_t kd = ring + st * key_bytes<HD>();
+          const int page = good_page(a.c, next, a.err);
+          const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
+          const int end = page >= 0 ? len : 0;
+          bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int c = nt * 8 + 2 * tq + e, rr = r0 + c;
-        float v = -INFINITY;
-        if (c < nr)
-          v = a.lse[static_cast<long long>(first + rr / a.group) * a.n_q + h * a.group + rr % a.group];
-        lim[nt][e] = c < nr && v != -INFINITY ? off + rr / a.group : -1;  // a row that saw nothing
-        ls[nt][e] = v * kLog2e;
-      }
-    }
-    unsigned bad = 0;
-    int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
-    auto issue = [&](int it) {
-      if (it < mine) {
+          for (int c = 0; c < kTile * kChunks / 32; ++c) {
+            const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
+            cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, e0 + r < end);
+          }
+          if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
+        }
+        cp_commit();
+      };
+#pragma unroll
+      for (int p = 0; p < kStages - 1; ++p) issue(p);
+      const float* src = r0 == 0 ? a.mass : a.mass_out;
+      const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+      for (int it = 0; it < mine; ++it) {
         const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
+        // the entry this thread writes: tq 0 those of g, tq 1 those of g + 8
+        const int j_out = e0 + g + 8 * tq;
+        const bool writes = tq < 2 && j_out < len;
+        float before = 0.f;
+        if (writes && src != nullptr) before = src[entries + j_out];
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        issue(it + kStages - 1);
         const uint32_t kd = ring + st * key_bytes<HD>();
-        const int page = good_page(a.c, next, a.err);
-        const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
-        const int end = page >= 0 ? len : 0;
-        bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
+        float sc[NT][2][4];
 #pragma unroll
-        for (int c = 0; c < kTile * kChunks / 32; ++c) {
-          const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
-          cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, e0 + r < end);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kM; ++k) {
+          uint32_t kf[4];
+          ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
         }
-        if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
-      }
-      cp_commit();
-    };
+        const bool hidden = (bad >> st) & 1;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int p = 0; p < kStages - 1; ++p) issue(p);
-    const float* src = r0 == 0 ? a.mass : a.mass_out;
-    const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
-    for (int it = 0; it < mine; ++it) {
-      const int e0 = k0 + (it * kWarps + warp) * kTile, st = it % kStages;
-      // the entry this thread writes: tq 0 those of g, tq 1 those of g + 8
-      const int j_out = e0 + g + 8 * tq;
-      const bool writes = tq < 2 && j_out < len;
-      float before = 0.f;
-      if (writes && src != nullptr) before = src[entries + j_out];
-      cp_wait<kStages - 2>();
-      __syncwarp();
-      issue(it + kStages - 1);
-      const uint32_t kd = ring + st * key_bytes<HD>();
-      float sc[NT][2][4];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 4; ++e) {
+            const float w =
+                ex2(fmaf(sc[nt][0][e] + sc[nt][1][e], a.scale_log2, -ls[nt][e & 1]));
+            if (!hidden && e0 + g + 8 * (e >> 1) <= lim[nt][e & 1]) sum[e >> 1] += w;
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kM; ++k) {
-        uint32_t kf[4];
-        ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
-      }
-      const bool hidden = (bad >> st) & 1;
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w =
-              ex2(fmaf(sc[nt][0][e] + sc[nt][1][e], a.scale_log2, -ls[nt][e & 1]));
-          if (!hidden && e0 + g + 8 * (e >> 1) <= lim[nt][e & 1]) sum[e >> 1] += w;
+        for (int e = 0; e < 2; ++e) {
+          sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
+          sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
         }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 1);
-        sum[e] += __shfl_xor_sync(0xFFFFFFFFu, sum[e], 2);
+        if (writes) a.mass_out[entries + j_out] = before + (tq == 0 ? sum[0] : sum[1]);
+        __syncwarp();
       }
-      if (writes) a.mass_out[entries + j_out] = before + (tq == 0 ? sum[0] : sum[1]);
+      cp_wait<0>();
       __syncwarp();
+      r0 += kRows;
+    } while (r0 < rows);
+    j0 = 0;
+    if (left > 0 && ++h == a.c.n_kv) {
+      h = 0;
+      s = run_next(s, a.c.n_seqs, lane, blocks_of);
+      if (s >= a.c.n_seqs) return;
     }
-    cp_wait<0>();
-    __syncwarp();
-    r0 += kRows;
-  } while (r0 < rows);
-  j0 = 0;
-  if (left > 0 && ++h == a.c.n_kv) {
-    h = 0;
-    s = run_next(s, a.c.n_seqs, lane, blocks_of);
-    if (s >= a.c.n_seqs) return;
-  }
   }
 }
 

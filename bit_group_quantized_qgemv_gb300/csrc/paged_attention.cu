@@ -121,263 +121,263 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(HD, 8 * NT, kWarps))
   }
 
   while (true) {
-  int first, count;
-  int* err = a.cluster > 1 ? a.err : nullptr;  // (the others have looked at every length)
-  seq_rows(a.q_start, s, a.n_tokens, err, &first, &count);
-  const int len = seq_len(a.c, s, err);
-  if (a.cluster > 1) {
-    if (count > a.max_q) flag_error(err);
-    if (count == 0) return;
-  }
-  const int nr = min(count, a.max_q) * a.group;
-  const int off = len - count;  // token i sees entries up to off + i
-  // this segment's entries k0 .. k1, of those that some row sees
-  const int see = min(len, off + (nr - 1) / a.group + 1);
-  const int n_blocks = max(1, (len + kBlock - 1) / kBlock);
-  int k0, k1, slot = -1;
-  if (a.cluster > 1) {
-    const int part = (n_blocks + a.cluster - 1) / a.cluster * kBlock;
-    k0 = cluster_rank() * part;
-    k1 = min(see, k0 + part);
-  } else if (!cut) {
-    k0 = 0;
-    k1 = see;
-  } else {
-    const int j1 = static_cast<int>(min(static_cast<long long>(n_blocks), j0 + left));
-    k0 = j0 * kBlock;
-    k1 = min(see, j1 * kBlock);
-    if (j0 > 0 || j1 < n_blocks) slot = 2 * static_cast<int>(blockIdx.x) + (j0 == 0);
-    if (j0 == 0 && j1 < n_blocks)
-      split = AttnUnit{1 + static_cast<int>(run_div(n_blocks - j1 + per - 1, per)), s, h, 0, first, nr, off,
-                       len};
-    // who has the first part of a cut unit; -1: the unit is whole
-    if (j0 == 0 && a.first_of != nullptr && threadIdx.x == 0)
-      a.first_of[s * a.c.n_kv + h] = j1 < n_blocks ? static_cast<int>(blockIdx.x) : -1;
-    left -= j1 - j0;
-  }
-  if (a.cluster == 1 && !cut) --left;
-
-  const uint32_t ring = smem_u32(smem) + warp * (kStages * stage_bytes<HD>());
-  const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  unsigned bad = 0;  // bit st: the tile in stage st lies on a bad page
-  int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
-
-  // Queries as B fragments: column = row of the block.
-  uint32_t qf[NT][kM][2];
-  int lim[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    const int i = r / a.group, head = h * a.group + r % a.group;
-    const __half* q = a.q + static_cast<long long>(first + i) * a.q_stride + head * HD + 2 * tq;
-#pragma unroll
-    for (int k = 0; k < kM; ++k) {
-      qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
-      qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+    int first, count;
+    int* err = a.cluster > 1 ? a.err : nullptr;  // (the others have looked at every length)
+    seq_rows(a.q_start, s, a.n_tokens, err, &first, &count);
+    const int len = seq_len(a.c, s, err);
+    if (a.cluster > 1) {
+      if (count > a.max_q) flag_error(err);
+      if (count == 0) return;
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = nt * 8 + 2 * tq + e;
-      lim[nt][e] = c < nr ? off + c / a.group : -1;
+    const int nr = min(count, a.max_q) * a.group;
+    const int off = len - count;  // token i sees entries up to off + i
+    // this segment's entries k0 .. k1, of those that some row sees
+    const int see = min(len, off + (nr - 1) / a.group + 1);
+    const int n_blocks = max(1, (len + kBlock - 1) / kBlock);
+    int k0, k1, slot = -1;
+    if (a.cluster > 1) {
+      const int part = (n_blocks + a.cluster - 1) / a.cluster * kBlock;
+      k0 = cluster_rank() * part;
+      k1 = min(see, k0 + part);
+    } else if (!cut) {
+      k0 = 0;
+      k1 = see;
+    } else {
+      const int j1 = static_cast<int>(min(static_cast<long long>(n_blocks), j0 + left));
+      k0 = j0 * kBlock;
+      k1 = min(see, j1 * kBlock);
+      if (j0 > 0 || j1 < n_blocks) slot = 2 * static_cast<int>(blockIdx.x) + (j0 == 0);
+      if (j0 == 0 && j1 < n_blocks)
+        split = AttnUnit{1 + static_cast<int>(run_div(n_blocks - j1 + per - 1, per)), s, h, 0, first, nr, off,
+                         len};
+      // who has the first part of a cut unit; -1: the unit is whole
+      if (j0 == 0 && a.first_of != nullptr && threadIdx.x == 0)
+        a.first_of[s * a.c.n_kv + h] = j1 < n_blocks ? static_cast<int>(blockIdx.x) : -1;
+      left -= j1 - j0;
     }
-  }
+    if (a.cluster == 1 && !cut) --left;
 
-  float o[NT][kM][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int d = 0; d < kM; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.f;
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * stage_bytes<HD>());
+    const int tiles = k1 > k0 ? (k1 - k0 + kTile - 1) / kTile : 0;
+    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+    unsigned bad = 0;  // bit st: the tile in stage st lies on a bad page
+    int next = mine > 0 ? raw_page(a.c, s, k0 + warp * kTile) : -1;
 
-  auto issue = [&](int it) {
-    if (it < mine) {
-      const int e0 = k0 + (it * kWarps + warp) * kTile;
-      const int st = it % kStages;
-      const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
-      const int page = good_page(a.c, next, a.err);
-      const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
-      const int end = page >= 0 ? len : 0;
-      bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
-#pragma unroll
-      for (int c = 0; c < kTile * kChunks / 32; ++c) {
-        const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
-        // (rows behind the end lie on the page and are not read)
-        const bool take = e0 + r < end;
-        cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, take);
-        cp_async16(vd + tile_off<HD>(r, ch), a.c.v + base + id * 8, take);
-      }
-      // the next tile's page, a step ahead of its use
-      if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int p = 0; p < kStages - 1; ++p) issue(p);
-
-  const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
-  const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
-  for (int it = 0; it < mine; ++it) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    issue(it + kStages - 1);
-    const int st = it % kStages;
-    const int e0 = k0 + (it * kWarps + warp) * kTile;
-    const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
-    // S^T: 16 entries x 8 rows per tile of rows, even and odd k-steps apart
-    // (two shorter chains of products)
-    float sc[NT][2][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kM; ++k) {
-      uint32_t kf[4];
-      ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
-    }
-    const bool hidden = (bad >> st) & 1;
-    uint32_t ph[NT][2], pl[NT][2];
+    // Queries as B fragments: column = row of the block.
+    uint32_t qf[NT][kM][2];
+    int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float x[4];
-      bool over = false;
+      const int r = nt * 8 + g;
+      const int i = r / a.group, head = h * a.group + r % a.group;
+      const __half* q = a.q + static_cast<long long>(first + i) * a.q_stride + head * HD + 2 * tq;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = e0 + g + 8 * (e >> 1);
-        const bool seen = !hidden && j <= lim[nt][e & 1];
-        x[e] = seen ? (sc[nt][0][e] + sc[nt][1][e]) * a.scale_log2 : -INFINITY;
-        over |= x[e] > m[nt][e & 1] + kSlack;
+      for (int k = 0; k < kM; ++k) {
+        qf[nt][k][0] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+        qf[nt][k][1] = r < nr ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
       }
-      // The maximum is lazy: it moves (and O is rescaled) only where a score
-      // exceeds it by more than the slack, so most tiles cost one vote.
-      if (__any_sync(0xFFFFFFFFu, over)) {
-        float mn[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mn[e] = fmaxf(m[nt][e], fmaxf(x[e], x[e + 2]));
-          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 4));
-          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 8));
-          mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 16));
-        }
-        const float f0 = mn[0] == m[nt][0] ? 1.f : ex2(m[nt][0] - mn[0]);
-        const float f1 = mn[1] == m[nt][1] ? 1.f : ex2(m[nt][1] - mn[1]);
-        l[nt][0] *= f0;
-        l[nt][1] *= f1;
-#pragma unroll
-        for (int d = 0; d < kM; ++d) {
-          o[nt][d][0] *= f0;
-          o[nt][d][1] *= f1;
-          o[nt][d][2] *= f0;
-          o[nt][d][3] *= f1;
-        }
-        m[nt][0] = mn[0];
-        m[nt][1] = mn[1];
-      }
-      const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-      const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // entry g, then g + 8
-        const float u = ex2(x[2 * e] - b0), v = ex2(x[2 * e + 1] - b1);
-        l[nt][0] += u;
-        l[nt][1] += v;
-        const uint32_t hi = pack_f16(u, v);
-        ph[nt][e] = transpose8(hi);
-        if (LO) {
-          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          pl[nt][e] = transpose8(pack_f16(u - hf.x, v - hf.y));
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int c = nt * 8 + 2 * tq + e;
+        lim[nt][e] = c < nr ? off + c / a.group : -1;
       }
     }
-    // O^T += V^T P^T
+
+    float o[NT][kM][4], m[NT][2], l[NT][2];
 #pragma unroll
-    for (int d = 0; d < kM; ++d) {
-      uint32_t vf[4];
-      ldsm4t(vf, vd + tile_off<HD>(vr, 2 * d + vc));
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int d = 0; d < kM; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][d][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    auto issue = [&](int it) {
+      if (it < mine) {
+        const int e0 = k0 + (it * kWarps + warp) * kTile;
+        const int st = it % kStages;
+        const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
+        const int page = good_page(a.c, next, a.err);
+        const long long base = page >= 0 ? cache_row(a.c, page, h, e0) * HD : 0;
+        const int end = page >= 0 ? len : 0;
+        bad = page >= 0 ? bad & ~(1u << st) : bad | (1u << st);
+#pragma unroll
+        for (int c = 0; c < kTile * kChunks / 32; ++c) {
+          const int id = c * 32 + lane, r = id / kChunks, ch = id % kChunks;
+          // (rows behind the end lie on the page and are not read)
+          const bool take = e0 + r < end;
+          cp_async16(kd + tile_off<HD>(r, ch), a.c.k + base + id * 8, take);
+          cp_async16(vd + tile_off<HD>(r, ch), a.c.v + base + id * 8, take);
+        }
+        // the next tile's page, a step ahead of its use
+        if (it + 1 < mine) next = raw_page(a.c, s, e0 + kWarps * kTile);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int p = 0; p < kStages - 1; ++p) issue(p);
+
+    const int kr = (lane & 7) + (((lane >> 3) & 1) << 3), kc = lane >> 4;
+    const int vr = (lane & 7) + ((lane >> 4) << 3), vc = (lane >> 3) & 1;
+    for (int it = 0; it < mine; ++it) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      issue(it + kStages - 1);
+      const int st = it % kStages;
+      const int e0 = k0 + (it * kWarps + warp) * kTile;
+      const uint32_t kd = ring + st * stage_bytes<HD>(), vd = kd + stage_bytes<HD>() / 2;
+      // S^T: 16 entries x 8 rows per tile of rows, even and odd k-steps apart
+      // (two shorter chains of products)
+      float sc[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][0][e] = sc[nt][1][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kM; ++k) {
+        uint32_t kf[4];
+        ldsm4(kf, kd + tile_off<HD>(kr, 2 * k + kc));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(sc[nt][k & 1], kf, qf[nt][k][0], qf[nt][k][1]);
+      }
+      const bool hidden = (bad >> st) & 1;
+      uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma_f16(o[nt][d], vf, ph[nt][0], ph[nt][1]);
-        if (LO) mma_f16(o[nt][d], vf, pl[nt][0], pl[nt][1]);
+        float x[4];
+        bool over = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = e0 + g + 8 * (e >> 1);
+          const bool seen = !hidden && j <= lim[nt][e & 1];
+          x[e] = seen ? (sc[nt][0][e] + sc[nt][1][e]) * a.scale_log2 : -INFINITY;
+          over |= x[e] > m[nt][e & 1] + kSlack;
+        }
+        // The maximum is lazy: it moves (and O is rescaled) only where a score
+        // exceeds it by more than the slack, so most tiles cost one vote.
+        if (__any_sync(0xFFFFFFFFu, over)) {
+          float mn[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mn[e] = fmaxf(m[nt][e], fmaxf(x[e], x[e + 2]));
+            mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 4));
+            mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 8));
+            mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 16));
+          }
+          const float f0 = mn[0] == m[nt][0] ? 1.f : ex2(m[nt][0] - mn[0]);
+          const float f1 = mn[1] == m[nt][1] ? 1.f : ex2(m[nt][1] - mn[1]);
+          l[nt][0] *= f0;
+          l[nt][1] *= f1;
+#pragma unroll
+          for (int d = 0; d < kM; ++d) {
+            o[nt][d][0] *= f0;
+            o[nt][d][1] *= f1;
+            o[nt][d][2] *= f0;
+            o[nt][d][3] *= f1;
+          }
+          m[nt][0] = mn[0];
+          m[nt][1] = mn[1];
+        }
+        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // entry g, then g + 8
+          const float u = ex2(x[2 * e] - b0), v = ex2(x[2 * e + 1] - b1);
+          l[nt][0] += u;
+          l[nt][1] += v;
+          const uint32_t hi = pack_f16(u, v);
+          ph[nt][e] = transpose8(hi);
+          if (LO) {
+            const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            pl[nt][e] = transpose8(pack_f16(u - hf.x, v - hf.y));
+          }
+        }
+      }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int d = 0; d < kM; ++d) {
+        uint32_t vf[4];
+        ldsm4t(vf, vd + tile_off<HD>(vr, 2 * d + vc));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(o[nt][d], vf, ph[nt][0], ph[nt][1]);
+          if (LO) mma_f16(o[nt][d], vf, pl[nt][0], pl[nt][1]);
+        }
+      }
+      __syncwarp();
+    }
+    cp_wait<0>();
+    __syncthreads();  // every warp is done with its ring: it now takes the partial outputs
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float lsum = l[nt][e];
+        lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 4);
+        lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 8);
+        lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
+        if (g == 0) {
+          sm_m[warp][nt * 8 + 2 * tq + e] = m[nt][e];
+          sm_l[warp][nt * 8 + 2 * tq + e] = lsum;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kM; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          so[(warp * kRows + nt * 8 + 2 * tq + (e & 1)) * kOut + 16 * d + g + 8 * (e >> 1)] =
+              o[nt][d][e];
+    }
+    __syncthreads();
+    // A warp per row: join the warps' parts.
+    const auto finish = [&](int r, float mm, float ll, const float* acc) {
+      const int i = r / a.group, head = h * a.group + r % a.group, t = first + i;
+      if (slot < 0) {
+        store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
+        return;
+      }
+      const long long at = static_cast<long long>(slot) * kRowsMax + r;
+#pragma unroll
+      for (int d = 0; d < D; ++d) a.part_o[at * HD + lane * D + d] = acc[d];
+      if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
+    };
+    for (int r = warp; r < nr; r += kWarps) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f, acc[D] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(sm_m[w][r] - base);
+        ll += sm_l[w][r] * f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) acc[d] += so[(w * kRows + r) * kOut + lane * D + d] * f;
+      }
+      if (a.cluster == 1) {
+        finish(r, mm, ll, acc);
+        continue;
+      }
+      // (row r is this warp's alone: its sum may take the place of warp 0's part)
+      __syncwarp();
+#pragma unroll
+      for (int d = 0; d < D; ++d) so[r * kOut + lane * D + d] = acc[d];
+      if (lane == 0) {
+        sm_m[0][r] = mm;
+        sm_l[0][r] = ll;
       }
     }
-    __syncwarp();
-  }
-  cp_wait<0>();
-  __syncthreads();  // every warp is done with its ring: it now takes the partial outputs
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float lsum = l[nt][e];
-      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 4);
-      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 8);
-      lsum += __shfl_xor_sync(0xFFFFFFFFu, lsum, 16);
-      if (g == 0) {
-        sm_m[warp][nt * 8 + 2 * tq + e] = m[nt][e];
-        sm_l[warp][nt * 8 + 2 * tq + e] = lsum;
-      }
+    if (a.cluster > 1) break;
+    if (left <= 0) break;
+    j0 = 0;
+    if (++h == a.c.n_kv) {
+      h = 0;
+      s = run_next(s, a.c.n_seqs, lane, blocks_of);
+      if (s >= a.c.n_seqs) break;
     }
-#pragma unroll
-    for (int d = 0; d < kM; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        so[(warp * kRows + nt * 8 + 2 * tq + (e & 1)) * kOut + 16 * d + g + 8 * (e >> 1)] =
-            o[nt][d][e];
-  }
-  __syncthreads();
-  // A warp per row: join the warps' parts.
-  const auto finish = [&](int r, float mm, float ll, const float* acc) {
-    const int i = r / a.group, head = h * a.group + r % a.group, t = first + i;
-    if (slot < 0) {
-      store_row<HD>(a, s, h, t, head, min(off + i, len - 1), len, acc, mm, ll, lane);
-      return;
-    }
-    const long long at = static_cast<long long>(slot) * kRowsMax + r;
-#pragma unroll
-    for (int d = 0; d < D; ++d) a.part_o[at * HD + lane * D + d] = acc[d];
-    if (lane == 0) a.part_ml[at] = make_float2(mm, ll);
-  };
-  for (int r = warp; r < nr; r += kWarps) {
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][r]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, acc[D] = {};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(sm_m[w][r] - base);
-      ll += sm_l[w][r] * f;
-#pragma unroll
-      for (int d = 0; d < D; ++d) acc[d] += so[(w * kRows + r) * kOut + lane * D + d] * f;
-    }
-    if (a.cluster == 1) {
-      finish(r, mm, ll, acc);
-      continue;
-    }
-    // (row r is this warp's alone: its sum may take the place of warp 0's part)
-    __syncwarp();
-#pragma unroll
-    for (int d = 0; d < D; ++d) so[r * kOut + lane * D + d] = acc[d];
-    if (lane == 0) {
-      sm_m[0][r] = mm;
-      sm_l[0][r] = ll;
-    }
-  }
-  if (a.cluster > 1) break;
-  if (left <= 0) break;
-  j0 = 0;
-  if (++h == a.c.n_kv) {
-    h = 0;
-    s = run_next(s, a.c.n_seqs, lane, blocks_of);
-    if (s >= a.c.n_seqs) break;
-  }
-  __syncthreads();  // the next segment's ring takes the place of these outputs
+    __syncthreads();  // the next segment's ring takes the place of these outputs
   }
   if (a.cluster == 1) {
     if (cut && threadIdx.x == 0) a.splits[blockIdx.x] = split;

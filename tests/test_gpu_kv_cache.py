@@ -515,3 +515,16 @@ def test_decode_loop(norm):
             mass, mass2, epos, epos2 = mass2, mass, epos2, epos
             h.kv_len.copy_(left)
     assert grp == 2 and q.device_status() == 0
+
+
+@pytest.mark.parametrize("m,n_q", [(2, 4), (40, 8)])
+def test_workspace_off_a_32_byte_boundary(m, n_q):
+    """A workspace needs 16 bytes of alignment, not more."""
+    c = ref.make_cache(3, [(m, 6000)], 2, 64, 16)
+    x, h, qs = queries(3, m, n_q, 64).cuda(), handle(c), c.q_start.cuda()
+    n = q.paged_attention_workspace_bytes(h, m, n_q, m)
+    assert n > 0
+    whole = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+    out, lse = q.paged_attention(h, x, qs, max_q=m, want_lse=True)
+    out1, lse1 = q.paged_attention(h, x, qs, max_q=m, want_lse=True, workspace=whole[16:])
+    assert torch.equal(out, out1) and torch.equal(lse, lse1)
