@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         // columns before `seen` are rows that lie before this entry, those from
         // `end` on belong to no token of the sequence (and may hold anything)
         const int t0 = (w.from + j) * step_tokens;
-        const int seen = (e - w.off - t0) * a.group;
+        const int seen = max(0, e - w.off - t0) * a.group;
         const int end = min(step_tokens, w.tokens - t0) * a.group;
-        const bool all = __all_sync(0xFFFFFFFFu, seen <= 0) && end == kBlock;
+        const bool all = __all_sync(0xFFFFFFFFu, seen == 0) && end == kBlock;
         uint32_t v[2][32];
         tc::ld32(v[0], lanes + d * kBlock);
         tc::wait_ld32(v[0]);

@@ -528,3 +528,67 @@ def test_workspace_off_a_32_byte_boundary(m, n_q):
     out, lse = q.paged_attention(h, x, qs, max_q=m, want_lse=True)
     out1, lse1 = q.paged_attention(h, x, qs, max_q=m, want_lse=True, workspace=whole[16:])
     assert torch.equal(out, out1) and torch.equal(lse, lse1)
+
+
+@pytest.mark.parametrize("n_q,m", [(4, 2), (8, 8)])
+def test_longest_cache(n_q, m):
+    """2^29 entries of one head (a page table that repeats a page of zero keys,
+    and a last page of its own): the four calls in a row, at the ends of
+    every 32-bit product of entries, rows and bytes."""
+    hd, page, cap, w = 64, 256, 1 << 29, 20.0
+    g = torch.Generator().manual_seed(n_q)
+    k = torch.zeros(2, 1, page, hd, dtype=torch.float16)
+    k[1, 0, :, 0] = w                                     # weight e^w against 1
+    v = torch.randint(-4, 5, (2, 1, page, hd), generator=g).half()
+    table = torch.zeros(1, cap // page, dtype=torch.int32)
+    table[0, -1] = 1
+    h = q.kv_cache(k.cuda(), v.cuda(), table.cuda(), torch.tensor([cap], dtype=torch.int32).cuda())
+    qkv = torch.zeros(m, n_q + 2, hd, dtype=torch.float16)
+    qkv[:, :n_q, 0] = 1.0
+    qkv[:, n_q, 0] = w
+    qkv[:, n_q + 1] = torch.randint(-4, 5, (m, hd), generator=g).half()
+    v[1, 0, page - m:] = qkv[:, n_q + 1]
+    mass = torch.full(h.entries, 9.0, device="cuda")
+    pos = torch.zeros(h.entries, dtype=torch.int32, device="cuda")
+    qs = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    at = torch.arange(cap - m, cap, dtype=torch.int32)
+    x = q.qk_norm_rope_append(h, qkv.view(m, -1).cuda(), qs, at.cuda(), entry_pos=pos, entry_mass=mass)
+    assert torch.equal(x.cpu(), qkv[:, :n_q].reshape(m, -1)) and torch.equal(h.v.cpu(), v)
+    assert torch.equal(h.k.cpu(), k)
+    assert torch.equal(pos[0, 0, -m:].cpu(), at) and int(pos.count_nonzero()) == m
+    assert int(mass.count_nonzero()) == cap - m
+    out, lse = q.paged_attention(h, x, qs, max_q=m, scale=1.0, want_lse=True)
+    # exact sums: page 0 as often as the table has it, then the last page's rows
+    V0, V1, heavy = v[0, 0].double(), v[1, 0].double(), math.exp(w)
+    for i in range(m):
+        n1 = page - m + i + 1
+        total = (cap - page) + heavy * n1
+        want = ((cap // page - 1) * V0.sum(0) + heavy * V1[:n1].sum(0)) / total
+        # fp32 exponents of up to 29 (2^-20), the sums, and one rounding to fp16
+        assert torch.allclose(out[i].view(n_q, hd).cpu().double(), want.expand(n_q, hd),
+                              rtol=2.0 ** -11 + 1e-5, atol=1e-5)
+        assert torch.allclose(lse[i].cpu().double(), torch.tensor(math.log(total)).double(), atol=1e-5)
+    mass.zero_()
+    q.attention_mass(h, x, qs, lse, max_q=m, scale=1.0, mass=mass, mass_out=mass)
+    low = float(torch.exp(-lse.double()).sum())           # what every entry of weight 1 receives
+    first = mass[0, 0, :cap - page]
+    # exponents up to 42: 2^-19 relative to the weight, with those of lse
+    assert float(first.min()) >= low * (1 - 2e-5) and float(first.max()) <= low * (1 + 2e-5)
+    for j in (cap - page, cap - m - 1, cap - m, cap - 1):
+        want = float(torch.exp(w - lse[max(0, j - (cap - m)):].double()).sum())
+        assert abs(float(mass[0, 0, j]) - want) <= 2e-5 * want
+    # eviction: the lightest five go, the last five entries take their places
+    pos = torch.arange(cap, dtype=torch.int32, device="cuda").view(1, 1, -1)
+    out_of = torch.tensor([3, 1 << 20, (1 << 28) + 1, (1 << 28) + 77777, cap - 300])
+    mass[0, 0, out_of.cuda()] = 0.0
+    keep = cap - 5
+    kept, mass1, pos1, n = q.cache_evict(h, mass, pos, torch.tensor([cap], dtype=torch.int32).cuda(), keep)
+    assert n.tolist() == [keep]
+    want = torch.arange(keep, dtype=torch.int32, device="cuda")
+    want[out_of.cuda()] = torch.arange(keep, cap, dtype=torch.int32, device="cuda")
+    assert torch.equal(kept[0, 0], want) and torch.equal(pos1[0, 0, :keep], want)
+    assert torch.equal(mass1[0, 0, :keep], mass[0, 0, want.long()])
+    # the rows moved: on page 0, which every sequence of holes shares, in the last ones' order
+    moved = {int(j) % page: keep + i - (cap - page) for i, j in enumerate(out_of.tolist())}
+    for r, src in moved.items():
+        assert torch.equal(h.v[0, 0, r].cpu(), v[1, 0, src])
