@@ -7,42 +7,72 @@ namespace qgemv {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// One row computed entry by entry in fp32, by a whole warp: taken where a
-// value that the row does not see is an infinity or a NaN, which the tensor
-// cores' 0 * v would carry into it.  Writes out and returns nothing else (the
-// maximum and the sum are not affected by values).
+// One row computed again in fp32 by a whole warp, from the entries that it sees
+// alone: taken where a value that the row does not see is an infinity or a NaN,
+// which the tensor cores' 0 * v would carry into it.  Writes out only (the
+// maximum and the sum are not affected by values).  32 entries at a time: a lane
+// takes the score of one of them, then its HD / 32 components of all of them, so
+// that the loads of a step do not wait for one another.  (In the many-rows kernel
+// the block's other warps wait meanwhile: a step of 3 us puts 32 rows over 3 million
+// entries at their limit, where the call ends with a status and without these rows.)
 template <int HD>
 __device__ __noinline__ void slow_row(const AttnArgs& a, int s, int h, int t, int head, int last,
                                       int lane) {
   constexpr int D = HD / 32;
-  const __half* q = a.q + static_cast<long long>(t) * a.q_stride + head * HD + lane * D;
-  float qv[D], o[D], m = -INFINITY, l = 0.f;
-  for (int d = 0; d < D; ++d) {
-    qv[d] = __half2float(q[d]);
-    o[d] = 0.f;
-  }
-  for (int j = 0; j <= last; ++j) {
-    const int p = page_of(a.c, s, j, nullptr);
-    if (p < 0) continue;
-    const long long at = cache_row(a.c, p, h, j) * HD + lane * D;
-    float x = 0.f;
-    for (int d = 0; d < D; ++d) x = fmaf(qv[d], __half2float(a.c.k[at + d]), x);
-    for (int k = 16; k > 0; k /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x), ms = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ms), w = ex2(x - ms);
-    l = l * f + w;
-    for (int d = 0; d < D; ++d) o[d] = o[d] * f + w * __half2float(a.c.v[at + d]);
+  const uint4* q = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(t) * a.q_stride +
+                                                  head * HD);
+  float o[D] = {}, m = -INFINITY, l = 0.f;
+  for (int j0 = 0; j0 <= last; j0 += 32) {
+    const int j = j0 + lane, p = j <= last ? page_of(a.c, s, j, nullptr) : -1;
+    const long long at = p >= 0 ? cache_row(a.c, p, h, j) * HD : -1;
+    float x = -INFINITY;
+    if (at >= 0) {
+      const uint4* k = reinterpret_cast<const uint4*>(a.c.k + at);
+      x = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < HD / 8; ++i) {
+        const uint4 kv = k[i], qv = q[i];
+        const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw[e]));
+          const float2 qf = __half22float2(*reinterpret_cast<const __half2*>(&qw[e]));
+          x = fmaf(qf.x, kf.x, x);
+          x = fmaf(qf.y, kf.y, x);
+        }
+      }
+      x *= a.scale_log2;
+    }
+    float mn = x;
+    for (int k = 16; k > 0; k /= 2) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, k));
+    mn = fmaxf(m, mn);
+    const float ms = mn == -INFINITY ? 0.f : mn, f = ex2(m - ms), w = ex2(x - ms);
+    float sum = w;
+    for (int k = 16; k > 0; k /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+    l = l * f + sum;
     m = mn;
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] *= f;
+#pragma unroll 8
+    for (int e = 0; e < 32; ++e) {
+      const float we = __shfl_sync(0xFFFFFFFFu, w, e);
+      const long long ae = __shfl_sync(0xFFFFFFFFu, at, e);
+      if (ae < 0) continue;
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        o[d] = fmaf(we, __half2float(a.c.v[ae + lane * D + d]), o[d]);
+    }
   }
   __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD + lane * D;
   const float r = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
+#pragma unroll
   for (int d = 0; d < D; ++d) y[d] = __float2half_rn(o[d] * r);
 }
 
 // The output of one row, HD / 32 components per lane, divided by its sum and
 // rounded; where the row hides entries and a component came out infinite or
-// NaN, the row is computed again without the hidden values.
+// NaN, the row is computed again without the hidden values (but not where the sum
+// of the weights is a NaN, which values do not enter).
 template <int HD>
 __device__ __forceinline__ void store_row(const AttnArgs& a, int s, int h, int t, int head,
                                           int last, int len, const float* acc, float m, float l,
@@ -59,7 +89,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int s, int h, int t
   }
   if (lane == 0 && a.lse != nullptr)
     a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
-  if (__any_sync(0xFFFFFFFFu, odd) && last < len - 1) {
+  if (__any_sync(0xFFFFFFFFu, odd) && l == l && last < len - 1) {
     __syncwarp();
     slow_row<HD>(a, s, h, t, head, last, lane);
   }

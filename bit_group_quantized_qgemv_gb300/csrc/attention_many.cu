@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live && a.lse != nullptr)
           a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
         // rows that hide entries and came out infinite or NaN: again, without them
-        unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && lim < g.len - 1);
+        unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && l == l && lim < g.len - 1);
         while (again != 0) {
           const int src = __ffs(again) - 1;
           again &= again - 1;

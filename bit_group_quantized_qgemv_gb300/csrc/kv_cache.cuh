@@ -51,16 +51,20 @@ __device__ __forceinline__ long long cache_row(const KvView& c, int p, int h, in
          (i & ((1 << c.page_shift) - 1));
 }
 
+// Limit of the waits: what a warp may have to do meanwhile (slow_row) is as long
+// as a cache.
+constexpr uint64_t kWaitNs = 10000000000ull;
+
 // A bounded wait of a whole warp: every lane gets the same answer, so a wait
 // that runs out does not split the warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, status));
+  return __all_sync(0xFFFFFFFFu, mbar_wait_for(bar, parity, status, kWaitNs));
 }
 
 // A bounded wait that answers nothing, for loops whose steps are short: there
 // an answer to test at every wait, or to carry along, cost a seventh of the time
 // (measured on GB300: 448 against 387 us for 1216 tokens over 30000 entries).  A
-// wait of more than a second sets *failed (in shared memory), after which the
+// wait of more than kWaitNs sets *failed (in shared memory), after which the
 // block's waits last for a thousand tries: its loops go on over whatever they
 // find, in bounds and for as many steps as they have, and the results are
 // dropped.
@@ -74,7 +78,7 @@ __device__ __forceinline__ void step_wait(uint32_t bar, uint32_t parity, volatil
       if (*failed != 0) break;
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > 1000000000ull) {
+      if (now - t0 > kWaitNs) {
         *failed = 1;
         atomicOr(status, kStatusWaitTimeout);
         break;

@@ -592,3 +592,21 @@ def test_longest_cache(n_q, m):
     moved = {int(j) % page: keep + i - (cap - page) for i, j in enumerate(out_of.tolist())}
     for r, src in moved.items():
         assert torch.equal(h.v[0, 0, r].cpu(), v[1, 0, src])
+
+
+@pytest.mark.parametrize("m,ws", [(2, True), (40, True), (40, False)])
+def test_hidden_nan_behind_a_long_cache(m, ws):
+    """All rows but the last token's are computed again without the NaN that it
+    alone sees, over a cache long enough for that to take a while."""
+    hd, n_kv, n_q, n = 64, 1, 8, 20000
+    c = ref.make_cache(11, [(m, n)], n_kv, hd, 64)
+    x = queries(11, m, n_q, hd)
+    want, _, tol, _ = ref.attention(c, x, hd ** -0.5)
+    p, r = c.entry(0, n - 1)
+    c.v[p, :, r] = math.nan
+    w0 = None if ws else torch.empty(0, dtype=torch.uint8, device="cuda")
+    q.device_status()
+    out, _ = q.paged_attention(handle(c), x.cuda(), c.q_start.cuda(), max_q=m, workspace=w0)
+    out = out.view(m, n_q, hd)
+    close(out[:m - 1], want[:m - 1], tol[:m - 1], "rows before the NaN")
+    assert bool(torch.isnan(out[m - 1]).all()) and q.device_status() == 0
