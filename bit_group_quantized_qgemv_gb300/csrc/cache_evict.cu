@@ -364,7 +364,7 @@ cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st, int
           ? launch_select<true>(a, heads, (cap + movers) * 4, st, device)
           : launch_select<false>(a, heads, cap * 4, st, device);
   if (e != cudaSuccess) return e;
-  const int chunks = (a.keep + 31) / 32;
+  const int chunks = static_cast<int>((min(static_cast<long long>(a.keep), cap) + 31) / 32);
   const long long blocks = (heads * chunks + 3) / 4;
   return a.c.head_dim == 64 ? launch_pdl(evict_move_kernel<64>, blocks, 128, 0, st, a, chunks)
                             : launch_pdl(evict_move_kernel<128>, blocks, 128, 0, st, a, chunks);

@@ -144,6 +144,7 @@ int qgemv_paged_attention(const qgemv_kv_cache* cache, const uint16_t* q, long l
       !aligned(workspace, 16) || !aligned(err_flag, 4))
     return QGEMV_EALIGN;
   if (n_tokens == 0) return QGEMV_OK;
+  if (out == q) return QGEMV_EINVAL;  // a row may be read again after it has been written
   int dev, sms;
   if (int rc = qgemv::device_and_sms(&dev, &sms)) return rc;
   a.q = reinterpret_cast<const __half*>(q);
@@ -204,7 +205,8 @@ int qgemv_cache_evict(const qgemv_kv_cache* cache, const float* mass, const int3
   if (int rc = check_cache(cache, &a.c)) return rc;
   if (!mass || !entry_pos || !next_pos || !kept || !mass_out || !pos_out || !kv_len_out)
     return QGEMV_ENULL;
-  if (keep < 1 || keep > 1 << 30 || n_sink < 0 || n_recent < 0 || static_cast<long long>(n_sink) + n_recent > keep)
+  if (keep < 1 || keep > 1 << 30 || n_sink < 0 || n_recent < 0 ||
+      static_cast<long long>(n_sink) + n_recent > keep)
     return QGEMV_EINVAL;
   // an output that is an input would be read after it has been written
   if (mass_out == mass || pos_out == entry_pos || kv_len_out == cache->kv_len) return QGEMV_EINVAL;

@@ -499,7 +499,8 @@ int qgemv_lut4(const uint32_t *codes, const uint16_t *lut, int n_luts, int rows_
  * outside [0, n_pages) is an entry that nothing sees, reads or writes; a
  * kv_len outside [0, max_pages * page_size] and a q_start that falls or leaves
  * [0, n_tokens] are clamped.  Pages may be shared between sequences where no
- * call writes them.  With n_tokens = 0 the arrays of token rows may be NULL.
+ * call writes them (an append writes the new entries' pages, an eviction any page
+ * of the sequence).  With n_tokens = 0 the arrays of token rows may be NULL.
  */
 typedef struct {
   uint16_t *k, *v;
@@ -551,7 +552,8 @@ int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
  * and lse = -inf.  What a token does not see does not reach it, not even as an
  * infinity or a NaN.
  *   q, out: fp16 rows of n_q * head_dim, strides in elements; 16-byte aligned,
- *   strides multiples of 8.  lse: fp32 [n_tokens][n_q] or NULL.
+ *   strides multiples of 8; out may not overlap q (out == q: EINVAL).  lse: fp32
+ *   [n_tokens][n_q] or NULL.
  *   max_q: the largest q_len (tokens beyond it are left out and set
  *   *err_flag).  Checks: n_tokens >= 0, n_q a multiple of n_kv and at most 65535,
  *   1 <= max_q <= 2^24, max_q * (n_q / n_kv) < 2^30, scale finite and > 0.

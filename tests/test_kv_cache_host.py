@@ -151,3 +151,7 @@ def test_binding_refuses_cpu_tensors():
     k = torch.zeros(2, 1, 16, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
         q.kv_cache(k, k, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_attention_out_is_not_q():
+    assert attention(q=ptr(0x20000), out=ptr(0x20000)) == EINVAL
