@@ -11,14 +11,14 @@
 // sum of the softmax in fp32 registers, and O^T += V^T P^T with P^T made from
 // the accumulators by a transpose of 8 x 8 matrices.  (With the rows as the 16 of
 // the product, padded, a tile took three times the products; 48 sequences of 900 to
-// 20000 entries: 202 against 184 us.)  The warps' (max, sum, O) are joined in
+// 20000 entries: 202 against 185 us.)  The warps' (max, sum, O) are joined in
 // shared memory, the parts of a split cache through the distributed shared
 // memory of a cluster or by a second kernel.
 //
 // Up to 16 rows P enters as fp16 high and low parts (two products with V), which
 // keeps the weights at 22 bits: the kernel is bound by HBM there, not by the
 // products.  48 sequences of 900 to 20000 entries (32/8 heads of 128, 1.23 GB) take
-// 184 us, 6.69 TB/s or 99 % of the measured copy bandwidth.  With more rows the
+// 185 us, 6.65 TB/s or 98 % of the measured copy bandwidth.  With more rows the
 // products are the bound, and P is rounded once to fp16, like every weight of the
 // tcgen05 kernel.
 #include <atomic>
@@ -590,19 +590,21 @@ cudaError_t launch_few_rows(const AttnArgs& a, int sms, cudaStream_t st, int dev
 // chip, by the number of units and the capacity (the lengths are on the device);
 // otherwise the entries are cut into equal runs (runs.cuh), joined by a second
 // kernel.  Measured on GB300, 32/8 heads of 128, one new token per sequence,
-// replayed from a graph, clusters of 8 against parts joined by a second kernel:
-//   1 sequence   1000 entries  5.7 us against 6.1;   4110  8.0 against 7.4;
-//                8000         10.6 against 8.3
-//   4 sequences  1000          7.4 against 7.0;      2000  9.1 against 10.2
-// (clusters of 16: 14.7 us at 4110).  A cluster also saves the workspace and a
-// launch, 4 us of a call's time on the host, so clusters serve one sequence's
-// 8 heads up to parts of 576 entries, and more units up to 256 while their
+// replayed from a graph, clusters of 8 against runs and their join (us):
+//   1 sequence   1000 entries  6.6 against 7.9;   4110   8.9 and 10.9;
+//                8000         10.8 and 11.5;     12000  13.1 and 13.6;
+//               16000         15.2 and 14.5
+//   2 sequences  1000          7.5 and  8.7;      4000  10.7 and 12.0;   8000  15.2 and 12.1
+//   4 sequences  1000          8.3 and  8.9;      4000  11.9 and 12.7
+// (clusters of 16: 14.7 us at one of 4110).  A cluster also saves the workspace
+// and a launch, 4 us of a call's time on the host.  So clusters serve one sequence's
+// 8 heads up to parts of 1536 entries, and more units up to 512 while their
 // blocks fill the machine at most once.  With longer caches a cluster lasts as
 // long as its sequence.
 int few_cluster(int n_seqs, int n_kv, long long capacity, int sms) {
   const long long units = static_cast<long long>(n_kv) * n_seqs;
   const bool fits = capacity > 128 && units <= 2 * sms / kMaxCluster &&
-                    capacity <= kMaxCluster * (units <= 8 ? 576 : 256);
+                    capacity <= kMaxCluster * (units <= 8 ? 1536 : 512);
   return fits ? kMaxCluster : 1;
 }
 

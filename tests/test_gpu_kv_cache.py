@@ -106,7 +106,8 @@ WIDE = [
     (128, 16, 4, 2, [(1, 500)], 4000),                          # a table for 64,000 entries
     (64, 64, 6, 2, [(3, 700), (1, 90)], 3000),
     (128, 16, 8, 4, [(1, 6000), (2, 5000), (0, 7000), (1, 1)], 1),  # runs over the ends of units
-    (64, 32, 24, 2, [(2, 9000)], 0),                            # 24 rows in many parts
+    (64, 32, 24, 2, [(2, 9000)], 0),
+    (64, 32, 24, 2, [(2, 13000)], 0),                           # 24 rows in many parts
     (128, 64, 8, 1, [(40, 9000)], 1),                           # 320 rows in many parts
     (64, 16, 4, 2, [(150, 3100), (20, 20)], 2000),
     (64, 16, 160, 1, [(1, 100), (2, 37)], 1),                   # 160 query heads to a key head
@@ -418,7 +419,7 @@ def test_graphs_streams_and_shared_workspace():
     stream, follow what their inputs hold at replay."""
     hd, n_q, n_kv = 128, 8, 2
     # (a cache long enough for its parts to be joined through the workspace)
-    cs = [ref.make_cache(20 + i, [(1, 6000), (1, 1)], n_kv, hd, 16) for i in range(2)]
+    cs = [ref.make_cache(20 + i, [(1, 13000), (1, 1)], n_kv, hd, 16) for i in range(2)]
     hs = [handle(c) for c in cs]
     xs = [queries(20 + i, 2, n_q, hd).cuda() for i in range(2)]
     qs = cs[0].q_start.cuda()
@@ -520,7 +521,7 @@ def test_decode_loop(norm):
 @pytest.mark.parametrize("m,n_q", [(2, 4), (40, 8)])
 def test_workspace_off_a_32_byte_boundary(m, n_q):
     """A workspace needs 16 bytes of alignment, not more."""
-    c = ref.make_cache(3, [(m, 6000)], 2, 64, 16)
+    c = ref.make_cache(3, [(m, 13000)], 2, 64, 16)
     x, h, qs = queries(3, m, n_q, 64).cuda(), handle(c), c.q_start.cuda()
     n = q.paged_attention_workspace_bytes(h, m, n_q, m)
     assert n > 0
