@@ -80,13 +80,18 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int s, int h, int t
   constexpr int D = HD / 32;
   const float inv = l > 0.f || !(l == l) ? 1.0f / l : 0.f;
   bool odd = false;
-  __half* y = a.out + static_cast<long long>(t) * a.out_stride + head * HD + lane * D;
+  float v[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) {
-    const float v = acc[d] * inv;
-    odd |= !(fabsf(v) <= 3.0e38f);
-    y[d] = __float2half_rn(v);
+    v[d] = acc[d] * inv;
+    odd |= !(fabsf(v[d]) <= 3.0e38f);
   }
+  uint32_t* y = reinterpret_cast<uint32_t*>(a.out + static_cast<long long>(t) * a.out_stride +
+                                            head * HD + lane * D);
+  if constexpr (D == 4)
+    *reinterpret_cast<uint2*>(y) = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
+  else
+    *y = pack_f16(v[0], v[1]);
   if (lane == 0 && a.lse != nullptr)
     a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
   if (__any_sync(0xFFFFFFFFu, odd) && l == l && last < len - 1) {

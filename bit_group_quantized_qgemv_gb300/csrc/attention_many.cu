@@ -736,8 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Join the parts of split units: block c of the kernel above has the first part
 // of at most one (in its slot 1), the blocks behind it the others (in their
-// slots 0).  A warp per row.
-constexpr int kJoinRows = 16, kJoinBlocks = 4;  // rows at a time, blocks per unit
+// slots 0).  A warp per row.  Bound by the way to the parts and back: 64 tokens over
+// 30000 entries (8 units in 19 parts) take 38 us without it, 70 with 4 blocks to a
+// unit, 55 with 8 and 16-byte loads; where no unit is cut (92 us for prompts) 8 blocks
+// cost 1 us more than 4.
+constexpr int kJoinRows = 16, kJoinBlocks = 8;  // rows at a time, blocks per unit
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(const AttnArgs a) {
@@ -764,8 +767,14 @@ __global__ void __launch_bounds__(32 * kJoinRows) attention_join_units_kernel(co
         if (p < u.parts) {
           const long long at = static_cast<long long>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * kUnitRows + r;
           ml[k] = a.part_ml[at];
-#pragma unroll
-          for (int d = 0; d < D; ++d) o[k][d] = a.part_o[at * HD + lane * D + d];
+          const float* src = a.part_o + at * HD + lane * D;
+          if constexpr (D == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            o[k][0] = v.x, o[k][1] = v.y, o[k][2] = v.z, o[k][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            o[k][0] = v.x, o[k][1] = v.y;
+          }
         }
       }
       float mn = m;
