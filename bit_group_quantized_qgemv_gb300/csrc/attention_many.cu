@@ -631,18 +631,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float b = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t sum[2] = {0, 0};
+        const uint64_t scale = pair(a.scale_log2, a.scale_log2), less = pair(-b, -b);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int n = 32 * c + 2 * k;
-            const float x0 = ex2(fmaf(__uint_as_float(v[n]), a.scale_log2, -b));
-            const float x1 = ex2(fmaf(__uint_as_float(v[n + 1]), a.scale_log2, -b));
-            sum[n & 3] += x0;
-            sum[(n + 1) & 3] += x1;
-            p[k] = pack_f16(x0, x1);
+            const float2 x = unpair(fma2(pair(__uint_as_float(v[n]), __uint_as_float(v[n + 1])), scale, less));
+            const float y0 = ex2(x.x), y1 = ex2(x.y);
+            sum[k & 1] = add2(sum[k & 1], pair(y0, y1));
+            p[k] = pack_f16(y0, y1);
           }
           tc::st16(st + 16 * c, p);
         }
@@ -650,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[x]));
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 s2 = unpair(add2(sum[0], sum[1]));
+        l += s2.x + s2.y;
       }
       const Seg after = next_seg(ns);
       load_q(after);

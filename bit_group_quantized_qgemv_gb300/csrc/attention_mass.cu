@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       warp_wait(smem_u32(&bars.q_full[j % kSlots]), (j / kSlots) & 1, &g_status);
   } else if (warp == 10) {
     // ------------------------------------------------- lse of each step's rows
-    // (a row outside the sequence, or one that saw nothing: +inf, weight 0)
+    // (negated; a row outside the sequence, or one that saw nothing: -inf, weight 0)
     // The values of a step are loaded a step ahead.
     constexpr int kOwn = kBlock / 32;
     int row_t[kOwn], row_h[kOwn];
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         if (g > 1) step_wait(smem_u32(&bars.l_empty[d]), (g / 2 - 1) & 1, &s_failed, &g_status);
 #pragma unroll
         for (int k = 0; k < kOwn; ++k)
-          s_lse[d][lane + 32 * k] = v[k] != -INFINITY ? v[k] * kLog2e : INFINITY;
+          s_lse[d][lane + 32 * k] = v[k] != -INFINITY ? v[k] * -kLog2e : -INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars.l_full[d]));
         if (j + 1 < w.steps) load(j + 1);
@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const long long at = (static_cast<long long>(w.s) * a.c.n_kv + w.h) *
                                (static_cast<long long>(a.c.max_pages) << a.c.page_shift) + e;
       const float before = live && a.mass != nullptr ? a.mass[at] : 0.f;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[2] = {0, 0};
+      const uint64_t scale = pair(a.scale_log2, a.scale_log2);
       for (int j = 0; j < w.steps; ++j, ++g) {
         const int d = g & 1;
         step_wait(smem_u32(&bars.l_full[d]), (g / 2) & 1, &s_failed, &g_status);
@@ -433,11 +434,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
             if (c < 3) tc::ld32(v[(c + 1) & 1], lanes + d * kBlock + 32 * (c + 1));
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * c + k);
-              const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(ls + 32 * c + k);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                sum[i] += ex2(fmaf(__uint_as_float(v[c & 1][k + i]), a.scale_log2, -l[i]));
+              for (int i = 0; i < 2; ++i) {
+                const uint64_t s = pair(__uint_as_float(v[c & 1][k + 2 * i]),
+                                        __uint_as_float(v[c & 1][k + 2 * i + 1]));
+                const float2 x = unpair(fma2(s, scale, i == 0 ? l.x : l.y));
+                sum[i] = add2(sum[i], pair(ex2(x.x), ex2(x.y)));
+              }
             }
             if (c < 3) tc::wait_ld32(v[(c + 1) & 1]);
           }
@@ -446,9 +450,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           for (int c = 0; c < 4; ++c) {
             if (c < 3) tc::ld32(v[(c + 1) & 1], lanes + d * kBlock + 32 * (c + 1));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float y = ex2(fmaf(__uint_as_float(v[c & 1][k]), a.scale_log2, -ls[32 * c + k]));
-              sum[k & 3] += 32 * c + k >= seen && 32 * c + k < end ? y : 0.f;
+            for (int k = 0; k < 32; k += 2) {
+              float y[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int col = 32 * c + k + i;
+                y[i] = ex2(fmaf(__uint_as_float(v[c & 1][k + i]), a.scale_log2, ls[col]));
+                if (col < seen || col >= end) y[i] = 0.f;
+              }
+              sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(y[0], y[1]));
             }
             if (c < 3) tc::wait_ld32(v[(c + 1) & 1]);
           }
@@ -460,9 +470,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           mbar_arrive(smem_u32(&bars.l_empty[d]));
         }
       }
+      const float2 both = unpair(add2(sum[0], sum[1]));
       if (live && *static_cast<volatile int*>(&s_failed) == 0)
-        a.mass_out[at] = before + (good_page(a.c, page, nullptr) >= 0
-                                       ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f);
+        a.mass_out[at] = before + (good_page(a.c, page, nullptr) >= 0 ? both.x + both.y : 0.f);
     }
   }
   tc::fence_before();
