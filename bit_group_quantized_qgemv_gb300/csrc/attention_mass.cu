@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(NT)) mass_few_kernel
 constexpr int kBlock = 128;  // entries of a tile, rows of a step
 constexpr int kManyThreads = 384;
 constexpr int kSlots = 3;    // query tiles in flight
+constexpr int kAhead = 4;    // shares found ahead
 
 template <int HD>
 struct Shape {
@@ -192,10 +193,10 @@ struct Shape {
 
 struct Bars {
   uint64_t keys[2], k_empty[2], q_full[kSlots], q_empty[kSlots], s_full[2][2], s_empty[2][2],
-      l_full[2], l_empty[2], drain;
+      l_full[2], l_empty[2], share_full[kAhead], share_empty[kAhead], drain;
 };
 
-// A block's share: 256 entries of one head of one sequence.
+// A block's share: 256 entries of one head of one sequence (s -1: no more).
 struct Share {
   int s, h, e0, len, first, tokens, off, from, steps;
 };
@@ -221,9 +222,10 @@ __device__ __forceinline__ void get_share(const MassArgs& a, long long b, int st
   w->steps = max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from);
 }
 
-// One block per multiprocessor, each taking every gridDim.x-th share.  The
-// roles walk the shares on their own, the producer ahead of the others (two
-// buffers of keys), so that a share's start hides behind the one before it.
+// One block per multiprocessor, each taking every gridDim.x-th share.  Warp 11
+// finds them ahead of the others (lengths and starts are three loads in a row, 2 us of
+// a share's 18 when every warp looked for itself), the producer is ahead of the sums
+// (two buffers of keys), so that a share's start hides behind the one before it.
 template <int HD>
 __global__ void __launch_bounds__(kManyThreads, 1)
     mass_many_kernel(const MassArgs a, const __grid_constant__ CUtensorMap k_map,
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;  // a wait ran out
   __shared__ __align__(16) float s_lse[2][kBlock];
+  __shared__ Share s_share[kAhead];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* qring = base + 4 * Sh::kBytes;
@@ -255,6 +258,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       mbar_init(smem_u32(&bars.l_full[x]), 1);
       mbar_init(smem_u32(&bars.l_empty[x]), 8);
     }
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(smem_u32(&bars.share_full[i]), 1);
+      mbar_init(smem_u32(&bars.share_empty[i]), 11);  // every warp but the finder
+    }
     mbar_init(smem_u32(&bars.drain), 1);
     fence_mbar_init();
     s_failed = 0;
@@ -265,10 +272,18 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   tc::fence_after();
   pdl_wait();
   const uint32_t tmem = s_tmem;
-  const long long shares = run_total(a.c.n_seqs, a.c.n_kv, lane, [&](int i) {
-    return shares_of(a, i, warp == 8 ? a.err : nullptr);
-  });
   Share w;
+  // Share number n of this block, as every warp but the finder reads it; false
+  // behind the last.
+  auto next_share = [&](int n) {
+    const int i = n % kAhead;
+    step_wait(smem_u32(&bars.share_full[i]), (n / kAhead) & 1, &s_failed, &g_status);
+    w = s_share[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars.share_empty[i]));
+    // (no shares are taken after a wait ran out)
+    return __all_sync(0xFFFFFFFFu, w.s >= 0 && *static_cast<volatile int*>(&s_failed) == 0);
+  };
 
   if (warp == 9) {
     // ---------------------------------------------------------- producer
@@ -278,8 +293,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     const uint32_t bytes = static_cast<uint32_t>(step_tokens * a.group * HD * 2);
     int kb = 0, g = 0;
     bool ok = true;
-    for (long long b = blockIdx.x; b < shares && ok; b += gridDim.x) {
-      get_share(a, b, step_tokens, lane, &w);
+    for (int n = 0; ok && next_share(n); ++n) {
       if (w.steps == 0) continue;
       const int kd = kb & 1;
       if (kb > 1) ok = warp_wait(smem_u32(&bars.k_empty[kd]), (kb / 2 - 1) & 1, &g_status);
@@ -332,8 +346,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       row_h[k] = c % a.group;
     }
     int g = 0;
-    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      get_share(a, b, step_tokens, lane, &w);
+    for (int n = 0; next_share(n); ++n) {
       float v[kOwn];
       auto load = [&](int j) {
         const int t0 = (w.from + j) * step_tokens;
@@ -360,8 +373,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // ---------------------------------------------------------- products
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
     int kb = 0, g = 0;
-    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      get_share(a, b, step_tokens, lane, &w);
+    for (int n = 0; next_share(n); ++n) {
       const int n_steps = tc::uniform(w.steps);
       if (n_steps == 0) continue;
       const int kd = kb & 1;
@@ -398,13 +410,32 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
     __syncwarp();
     warp_wait(smem_u32(&bars.drain), 0, &g_status);
-  } else if (warp < 8) {
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ shares
+    const long long shares = run_total(a.c.n_seqs, a.c.n_kv, lane,
+                                       [&](int i) { return shares_of(a, i, a.err); });
+    int n = 0;
+    for (long long b = blockIdx.x;; b += gridDim.x, ++n) {
+      const int i = n % kAhead;
+      if (b < shares)
+        get_share(a, b, step_tokens, lane, &w);
+      else
+        w.s = -1;
+      if (n >= kAhead)
+        step_wait(smem_u32(&bars.share_empty[i]), (n / kAhead - 1) & 1, &s_failed, &g_status);
+      if (lane == 0) {
+        s_share[i] = w;
+        mbar_arrive(smem_u32(&bars.share_full[i]));
+      }
+      __syncwarp();
+      if (b >= shares || __any_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) != 0)) break;
+    }
+  } else {
     // -------------------------------------------------------------- sums
     const int x = warp >> 2;
     const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
     int g = 0;
-    for (long long b = blockIdx.x; b < shares; b += gridDim.x) {
-      get_share(a, b, step_tokens, lane, &w);
+    for (int n = 0; next_share(n); ++n) {
       const int e = w.e0 + x * kBlock + (warp & 3) * 32 + lane;
       const bool live = e < w.len;
       const int page = live ? raw_page(a.c, w.s, e) : 0;
