@@ -14,7 +14,7 @@
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B: one row per thread,
 //               read from tensor memory, weights written back as fp16 over the
 //               scores they came from; the queries of the next segment are
-//               loaded before the last products of this one are awaited.
+//               loaded while the last weights of this one are computed.
 // While one tile's weights are computed the tensor core works on the other's
 // products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
 // (HD each).
@@ -31,6 +31,7 @@
 #include <atomic>
 
 #include "attention_common.cuh"
+#include "mma_tile.cuh"
 #include "tcgen05.cuh"
 #include "kv_tensor_map.h"
 
@@ -316,16 +317,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const uint32_t tmem = s_tmem;
 
-  // Segment number n, as every warp but the scheduler reads it.
-  auto next_seg = [&](int n) {
+  // Segment number n, as every warp but the scheduler reads it; the last look
+  // (next_seg) gives its place in the ring back.
+  auto look_seg = [&](int n) {
     const int i = n % kSegs;
     step_wait(smem_u32(&bars.seg_full[i]), (n / kSegs) & 1, &s_failed, &g_status);
     Seg g = segs[i];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[i]));
     // (no segments are read after a wait ran out)
     if (*static_cast<volatile int*>(&s_failed) != 0) g.s = -1;
     g.s = __shfl_sync(0xFFFFFFFFu, g.s, 0);
+    return g;
+  };
+  auto next_seg = [&](int n) {
+    const Seg g = look_seg(n);
+    if (lane == 0) mbar_arrive(smem_u32(&bars.seg_empty[n % kSegs]));
     return g;
   };
   // Tiles of tile x (0: A, 1: B) of a segment, from its j0 on.
@@ -533,47 +538,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((warp & 3) << 21);  // 32 lanes per warp, lane in bits 16..
     const uint32_t st = lanes + x * kTile, ot = lanes + 2 * kTile + x * HD;
     // Queries of a segment into the swizzled operand layout: [column of 128
-    // bytes][row][128 B].  (Every product with the ones before is done: their
-    // scores have been read.)  A segment in which this tile sees nothing has none:
-    // nothing would hold its arrival back until the one before has been seen.
+    // bytes][row][128 B], asynchronously (once every product with the ones before is
+    // done: the last tile's scores are there).  A segment in which this tile sees
+    // nothing has none: nothing would hold its arrival back until the one before has
+    // been seen.
+    auto wants_q = [&](const Seg& g) { return g.s >= 0 && tiles_in(g, x) > 0; };
     auto load_q = [&](const Seg& g) {
-      if (g.s < 0 || tiles_in(g, x) == 0) return;
-      // (loads first, then the stores: each chunk loaded and stored in turn took
-      // 9000 clocks)
       const uint32_t qs = smem_u32(base + x * Sh::kSlotBytes);
-      constexpr int kLoads = kTile * (HD / 8) / 128, kBatch = 8;
-#pragma unroll
-      for (int b = 0; b < kLoads; b += kBatch) {
-        uint4 v[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int c = (b + k) * 128 + (threadIdx.x & 127);
-          const int row = c / (HD / 8), ch = c % (HD / 8), rr = g.r0 + x * kTile + row;
-          v[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (rr < g.rows) {
-            const int i = div_group(a, rr);
-            v[k] = *reinterpret_cast<const uint4*>(
-                a.q + static_cast<long long>(g.first + i) * a.q_stride +
-                (g.h * a.group + rr - i * a.group) * HD + ch * 8);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int c = (b + k) * 128 + (threadIdx.x & 127);
-          const int row = c / (HD / 8), ch = c % (HD / 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           qs + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
-                       "r"(v[k].x), "r"(v[k].y), "r"(v[k].z), "r"(v[k].w)
-                       : "memory");
-        }
+#pragma unroll 4
+      for (int k = 0; k < kTile * (HD / 8) / 128; ++k) {
+        const int c = k * 128 + (threadIdx.x & 127);
+        const int row = c / (HD / 8), ch = c % (HD / 8), rr = g.r0 + x * kTile + row;
+        const bool take = rr < g.rows;
+        const int i = take ? div_group(a, rr) : 0;
+        cp_async16(qs + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                   a.q + static_cast<long long>(g.first + i) * a.q_stride +
+                       (g.h * a.group + (take ? rr - i * a.group : 0)) * HD + ch * 8,
+                   take);
       }
+      cp_commit();
+    };
+    auto q_loaded = [&] {
+      cp_wait<0>();
       tc::fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
     };
     int n_s = 0, n_o = 0;  // tiles of scores, outputs awaited so far
     Seg g = next_seg(0);
-    load_q(g);
+    if (wants_q(g)) {
+      load_q(g);
+      q_loaded();
+    }
     for (int ns = 1; g.s >= 0; ++ns) {
       const int rr = g.r0 + x * kTile + r;
       const bool live = rr < g.rows;
@@ -591,6 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j + 1 < tiles) page_next = page_at(j + 1);
         step_wait(smem_u32(&bars.s_full[x]), n_s & 1, &s_failed, &g_status);
         tc::fence_after();
+        if (j == tiles - 1) {
+          const Seg after = look_seg(ns);
+          if (wants_q(after)) load_q(after);
+        }
         uint32_t v[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::ld32(v + 32 * c, st + 32 * c);
@@ -654,7 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += s2.x + s2.y;
       }
       const Seg after = next_seg(ns);
-      load_q(after);
+      if (wants_q(after)) {
+        if (tiles == 0) load_q(after);
+        q_loaded();
+      }
 
       if (tiles > 0) {
         step_wait(smem_u32(&bars.o_full[x]), n_o & 1, &s_failed, &g_status);
@@ -726,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before();
       g = after;
     }
+    cp_wait<0>();  // (nothing is in flight here unless a wait ran out)
   }
   tc::fence_before();
   __syncthreads();
