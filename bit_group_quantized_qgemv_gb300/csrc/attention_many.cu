@@ -54,12 +54,13 @@ struct Shape {
   static constexpr int kSlotBytes = kTile * HD * 2;
   static constexpr int kSlots = HD == 128 ? 5 : 10;
   static constexpr int kSmem = 1024 + (2 + kSlots) * kSlotBytes;
-  static_assert(kSmem + 1024 <= 227 * 1024, "dynamic and static shared memory");
+  static_assert(kSmem + 2048 <= 227 * 1024, "dynamic and static shared memory");
   static constexpr uint32_t kDescS = tc::idesc_f16(kTile, kTile, false);
   static constexpr uint32_t kDescO = tc::idesc_f16(kTile, HD, true);
 };
 
 constexpr int kUnitRows = 2 * kTile;
+constexpr int kMaxBlocks = 160;  // as many as multiprocessors, at most
 constexpr int kSegs = 4;        // segments the scheduler may be ahead
 constexpr int kMinTiles = 2;    // entries' tiles of a part of a unit, at least
 // What a unit costs besides its tiles, in tiles: queries, first scores, output
@@ -89,8 +90,11 @@ __device__ __forceinline__ int div_group(const AttnArgs& a, int n) {
 
 // Finds a block's segments.  Units are ordered by sequence (up to 32 of them:
 // the one with the longest units first), by row tile (the last, longest, first) and
-// by head.  A block takes a unit of every
-// round, so that the blocks that share keys stay next to one another; or, with a workspace,
+// by head.  They go out in rounds of one per block: in the first as they come, so that
+// the blocks that share keys stay next to one another, then the longest of a round
+// to the block with the least so far (every scheduler works the whole table out, while
+// the round before is computed; prompts of 1 to 4001 tokens, 384 units of 1 to 32 tiles:
+// 88 us with rounds to and fro, 85 like this).  Or, with a workspace,
 // the tiles of all units are cut into equal runs, one per block: a block's
 // first and last unit may then be parts, whose results go to the workspace for the
 // join.  Whichever is expected to be done sooner: whole units last as long as
@@ -165,6 +169,7 @@ struct Scheduler {
       c_units = __shfl_sync(0xFFFFFFFFu, c_units, from);
       c_span = __shfl_sync(0xFFFFFFFFu, c_span, from);
       c_longest = __shfl_sync(0xFFFFFFFFu, c_longest, from);
+      if (lane >= a.c.n_seqs) c_units = c_span = c_longest = 0;  // (nobody's rank)
     }
   }
   __device__ void total(int* err, long long* units, long long* span, int* longest) {
@@ -231,6 +236,15 @@ struct Scheduler {
     }
     return -1;
   }
+  // A unit to come back to.
+  struct Mark {
+    int s, first, count, len, rows, place, rt, h;
+  };
+  __device__ Mark mark() const { return {s, first, count, len, rows, place, rt, h}; }
+  __device__ void back(const Mark& m) {
+    s = m.s, first = m.first, count = m.count, len = m.len;
+    rows = m.rows, place = m.place, rt = m.rt, h = m.h;
+  }
   // The unit n units on; false behind the last.
   __device__ bool advance(int n) {
     h += n;
@@ -238,17 +252,12 @@ struct Scheduler {
       h -= a.c.n_kv;
       while (--rt < 0) {
         if (++place >= a.c.n_seqs) return false;
-        const int l = place - s0;
-        if (l >= 0 && l < 32) {
-          s = __shfl_sync(0xFFFFFFFFu, c_id, l);
-          first = __shfl_sync(0xFFFFFFFFu, c_first, l);
-          count = __shfl_sync(0xFFFFFFFFu, c_count, l);
-          len = __shfl_sync(0xFFFFFFFFu, c_len, l);
-        } else {
-          s = place;
-          seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
-          len = seq_len(a.c, s, nullptr);
-        }
+        look(place & ~31, nullptr);
+        const int l = place & 31;
+        s = __shfl_sync(0xFFFFFFFFu, c_id, l);
+        first = __shfl_sync(0xFFFFFFFFu, c_first, l);
+        count = __shfl_sync(0xFFFFFFFFu, c_count, l);
+        len = __shfl_sync(0xFFFFFFFFu, c_len, l);
         rows = rows_of(count);
         rt = units_of(rows);
       }
@@ -286,6 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;  // a wait ran out
   __shared__ Seg segs[kSegs];
+  __shared__ int s_span[kMaxBlocks], s_load[kMaxBlocks];  // the scheduler's
+  __shared__ uint8_t s_order[kMaxBlocks];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring = base + 2 * Sh::kSlotBytes;
@@ -389,15 +400,67 @@ __global__ void __launch_bounds__(kThreads, 1)
             more = left > 0 && sc.advance(1);
           }
         }
-      } else if (blockIdx.x < units && sc.seek(blockIdx.x, false) >= 0) {
-        // rounds of one unit per block, every other one backwards: units of a
-        // sequence shorten, so who had the longer one gets the shorter
-        const int step[2] = {2 * static_cast<int>(gridDim.x - blockIdx.x) - 1,
-                             2 * static_cast<int>(blockIdx.x) + 1};
-        int round = 0;
-        do
-          emit(false, 0, sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len), -1);
-        while (sc.advance(step[round++ & 1]));
+      } else if (units > 0 && sc.seek(0, false) >= 0) {
+        constexpr int kOwn = kMaxBlocks / 32;
+        const int blocks = gridDim.x, me = blockIdx.x;
+        auto emit_unit = [&](int n) {  // the n-th from here
+          if (sc.advance(n)) emit(false, 0, sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len), -1);
+        };
+        int load[kOwn] = {};  // of blocks lane, lane + 32 ..
+        bool more = true;
+        for (long long at = 0; more; at += blocks) {
+          const int n = static_cast<int>(min(static_cast<long long>(blocks), units - at));
+          const auto start = sc.mark();
+          if (at == 0) {
+            if (me < n) emit_unit(me);
+            if (units <= blocks) break;
+            sc.back(start);
+          }
+          for (int i = 0; i < n;) {  // the spans of the round's units
+            const int run = min(n - i, a.c.n_kv - sc.h);
+            const int t = kUnitCost + sc.tiles_of(sc.rt, sc.rows, sc.count, sc.len);
+            for (int k = i + lane; k < i + run; k += 32) s_span[k] = t;
+            i += run;
+            more = sc.advance(run);
+          }
+          const auto end = sc.mark();
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u) s_load[lane + 32 * u] = load[u];
+          __syncwarp();
+          int rank[kOwn] = {}, own[kOwn];  // of this lane's units, longest first
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u) own[u] = lane + 32 * u < n ? s_span[lane + 32 * u] : 0;
+          for (int k = 0; k < n; ++k) {
+            const int t = s_span[k];
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u) rank[u] += t > own[u] || (t == own[u] && k < lane + 32 * u);
+          }
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u)
+            if (lane + 32 * u < n) s_order[at == 0 ? lane + 32 * u : rank[u]] = lane + 32 * u;
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u) rank[u] = 0;  // of this lane's blocks, least first
+          for (int k = 0; k < blocks; ++k) {
+            const int t = s_load[k];
+#pragma unroll
+            for (int u = 0; u < kOwn; ++u) rank[u] += t < load[u] || (t == load[u] && k < lane + 32 * u);
+          }
+          int mine = -1;  // the round's unit that this block takes
+#pragma unroll
+          for (int u = 0; u < kOwn; ++u) {
+            const int unit = lane + 32 * u < blocks && rank[u] < n ? s_order[rank[u]] : -1;
+            if (unit >= 0) load[u] += s_span[unit];
+            const int found = __shfl_sync(0xFFFFFFFFu, unit, me % 32);
+            if (u == me / 32) mine = found;
+          }
+          __syncwarp();  // the next round's spans and loads take these ones' place
+          if (at > 0 && mine >= 0) {
+            sc.back(start);
+            emit_unit(mine);
+            sc.back(end);
+          }
+        }
       }
       emit(true, 0, 0, -1);
       if (a.splits != nullptr && lane == 0) a.splits[blockIdx.x] = split;
@@ -848,12 +911,14 @@ cudaError_t launch_many(AttnArgs a, int sms, cudaStream_t st, int device, void* 
 }  // namespace
 
 size_t attention_many_bytes(int head_dim, int sms) {
+  if (sms > kMaxBlocks) sms = kMaxBlocks;
   return static_cast<size_t>(sms) * (2 * kUnitRows * (static_cast<size_t>(head_dim) * 4 + 8) +
                                      sizeof(AttnUnit));
 }
 
 cudaError_t attention_many_launch(const AttnArgs& a, int sms, cudaStream_t st, int device,
                                   void* workspace, size_t bytes) {
+  if (sms > kMaxBlocks) sms = kMaxBlocks;
   return a.c.head_dim == 64 ? launch_many<64>(a, sms, st, device, workspace, bytes)
                             : launch_many<128>(a, sms, st, device, workspace, bytes);
 }
