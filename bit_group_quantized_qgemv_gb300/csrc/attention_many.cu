@@ -25,6 +25,12 @@
 // Weights are then at most 2^kSlack, far inside fp16; their relative rounding is
 // the same as below 1.
 //
+// 2048 tokens over 30759 entries (32/8 heads of 128) take 660 us, 1.51 PFLOP/s or
+// 79 % of a library product.  What bounds it: Q K^T reads both operands from shared
+// memory, which at 128 columns takes its 128 bytes a clock; P V (P in tensor memory)
+// does not.  The softmax, in pairs of floats, just hides behind the products: as single
+// floats it took 685 us, with an eighth of the exponentials by polynomial 2 % more.
+//
 // Entries behind the sequence or on bad pages are loaded as zeros (a TMA box
 // outside the tensor); the rows of the last page behind the sequence's end,
 // which may hold anything, are zeroed in the V tile before the product.
@@ -100,8 +106,8 @@ __device__ __forceinline__ int div_group(const AttnArgs& a, int n) {
 // join.  Whichever is expected to be done sooner: whole units last as long as
 // their rounds, or the longest of them, runs their length and kSplitCost.
 // 2048 tokens over 30759 entries (256 units of 241 tiles for 152 blocks): whole
-// 753 us, cut 677; 1200 over 8200 (152 units): whole 113, cut 129; 64 over 8064
-// (8 units): whole 109, cut 28.
+// 706 us, cut 660; 1200 over 9400 (152 units): whole 126, cut 143; 64 over 8064
+// (8 units): whole 102, cut 29; the prompts above: whole 86, cut 95.
 struct Scheduler {
   const AttnArgs& a;
   int lane;

