@@ -16,8 +16,8 @@
 // over columns in one thread.  Scores are double-buffered (4 x 128 columns).
 // 256 entries a block halve the query traffic, which 128 would put at the
 // multiprocessor's share of the L2 bandwidth (32 KB per 512 clocks of products).
-// 511 tokens over 16411 entries (32/8 heads of 128, 67.6 GFLOP) take 72 us; the
-// products alone, both operands from shared memory, 65, the sums alone 65.
+// 511 tokens over 16411 entries (32/8 heads of 128, 67.6 GFLOP) take 68 us; the
+// products alone, both operands from shared memory, and the sums alone took 65 of 74.
 #include <atomic>
 
 #include "kv_tensor_map.h"
@@ -198,22 +198,27 @@ struct Bars {
       l_full[2], l_empty[2], share_full[kAhead], share_empty[kAhead], drain;
 };
 
-// A block's share: 256 entries of one head of one sequence (s -1: no more).
+// A block's share: 256 entries of one head of one sequence (s -1: no more), in two
+// tiles, or one of them alone.
 struct Share {
-  int s, h, e0, len, first, tokens, off, from, steps;
+  int s, h, e0, len, first, tokens, off, from, steps, tiles;
 };
 
-// Shares of sequence i's units, and share number b of all.  A whole warp.
+// Pairs of tiles of sequence i's units, and share number b of all: pairs, the
+// first `whole` of them as they are, then the tiles of the rest one by one.  A whole warp.
 __device__ __forceinline__ int shares_of(const MassArgs& a, int i, int* err) {
   return (seq_len(a.c, i, err) + 2 * kBlock - 1) / (2 * kBlock);
 }
-__device__ __forceinline__ void get_share(const MassArgs& a, long long b, int step_tokens, int lane,
-                                          Share* w) {
+__device__ __forceinline__ void get_share(const MassArgs& a, long long b, long long whole,
+                                          int step_tokens, int lane, Share* w) {
   int j;
+  const int half = b < whole ? -1 : static_cast<int>((b - whole) & 1);
+  if (half >= 0) b = whole + ((b - whole) >> 1);
   run_seek(b, a.c.n_seqs, a.c.n_kv, lane, [&](int i) { return shares_of(a, i, nullptr); }, &w->s,
            &w->h, &j);
-  w->e0 = j * 2 * kBlock;
+  w->e0 = j * 2 * kBlock + max(half, 0) * kBlock;
   w->len = seq_len(a.c, w->s, nullptr);
+  w->tiles = half >= 0 || w->e0 + kBlock >= w->len ? 1 : 2;
   int count;
   seq_rows(a.q_start, w->s, a.n_tokens, a.err, &w->first, &count);
   if (count > a.max_q) flag_error(a.err);
@@ -221,7 +226,7 @@ __device__ __forceinline__ void get_share(const MassArgs& a, long long b, int st
   w->off = w->len - count;
   // steps of step_tokens tokens, from the one whose last token sees entry e0
   w->from = max(0, w->e0 - w->off) / step_tokens;
-  w->steps = max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from);
+  w->steps = w->e0 < w->len ? max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from) : 0;
 }
 
 // One block per multiprocessor, each taking every gridDim.x-th share.  Warp 11
@@ -300,9 +305,9 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const int kd = kb & 1;
       if (kb > 1) ok = warp_wait(smem_u32(&bars.k_empty[kd]), (kb / 2 - 1) & 1, &g_status);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.keys[kd]), 2 * Sh::kBytes);
+      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.keys[kd]), w.tiles * Sh::kBytes);
       __syncwarp();
-      if (lane < 2 * boxes) {
+      if (lane < w.tiles * boxes) {
         const int x = lane / boxes, e = w.e0 + lane * page_rows;
         const int p = e < w.len ? page_of(a.c, w.s, e, a.err) : -1;
         const int row = p < 0 ? beyond : static_cast<int>(cache_row(a.c, p, w.h, e));
@@ -374,20 +379,22 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else if (warp == 8) {
     // ---------------------------------------------------------- products
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
-    int kb = 0, g = 0;
+    int kb = 0, g = 0, g1 = 0;  // buffers of keys, steps, steps of two tiles so far
     for (int n = 0; next_share(n); ++n) {
-      const int n_steps = tc::uniform(w.steps);
+      const int n_steps = tc::uniform(w.steps), n_tiles = tc::uniform(w.tiles);
       if (n_steps == 0) continue;
       const int kd = kb & 1;
       step_wait(smem_u32(&bars.keys[kd]), (kb / 2) & 1, &s_failed, &g_status);
       ++kb;
       for (int j = 0; j < n_steps; ++j, ++g) {
-        const int slot = g % kSlots, d = g & 1;
+        const int slot = g % kSlots;
         step_wait(smem_u32(&bars.q_full[slot]), (g / kSlots) & 1, &s_failed, &g_status);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (g > 1)
-            step_wait(smem_u32(&bars.s_empty[x][d]), (g / 2 - 1) & 1, &s_failed, &g_status);
+          if (x >= n_tiles) break;
+          const int gx = x == 0 ? g : g1, d = gx & 1;
+          if (gx > 1)
+            step_wait(smem_u32(&bars.s_empty[x][d]), (gx / 2 - 1) & 1, &s_failed, &g_status);
           tc::fence_after();
           if (tc::elect_one()) {
             const uint64_t k = tc::desc_k_major(smem_u32(base + (2 * kd + x) * Sh::kBytes));
@@ -407,6 +414,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
           if (j == n_steps - 1) tc::commit(smem_u32(&bars.k_empty[kd]));
         }
         __syncwarp();
+        g1 += n_tiles - 1;
       }
     }
     if (tc::elect_one()) tc::commit(smem_u32(&bars.drain));
@@ -414,13 +422,17 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     warp_wait(smem_u32(&bars.drain), 0, &g_status);
   } else if (warp == 11) {
     // ------------------------------------------------------------ shares
-    const long long shares = run_total(a.c.n_seqs, a.c.n_kv, lane,
-                                       [&](int i) { return shares_of(a, i, a.err); });
+    const long long pairs = run_total(a.c.n_seqs, a.c.n_kv, lane,
+                                      [&](int i) { return shares_of(a, i, a.err); });
+    // The pairs behind the last full round go out tile by tile where every block
+    // then still gets one at most (520 pairs on 152 blocks: 68 us against 72).
+    const long long rest = pairs % gridDim.x, whole = pairs - (2 * rest <= gridDim.x ? rest : 0);
+    const long long shares = whole + 2 * (pairs - whole);
     int n = 0;
     for (long long b = blockIdx.x;; b += gridDim.x, ++n) {
       const int i = n % kAhead;
       if (b < shares)
-        get_share(a, b, step_tokens, lane, &w);
+        get_share(a, b, whole, step_tokens, lane, &w);
       else
         w.s = -1;
       if (n >= kAhead)
@@ -436,8 +448,15 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     // -------------------------------------------------------------- sums
     const int x = warp >> 2;
     const uint32_t lanes = tmem + ((warp & 3) << 21) + 2 * x * kBlock;
-    int g = 0;
+    int g = 0, gx = 0;  // steps so far, of this group's tiles
     for (int n = 0; next_share(n); ++n) {
+      if (x >= w.tiles) {  // (the other group's steps: their lse passes by)
+        for (int j = 0; j < w.steps; ++j, ++g) {
+          step_wait(smem_u32(&bars.l_full[g & 1]), (g / 2) & 1, &s_failed, &g_status);
+          if (lane == 0) mbar_arrive(smem_u32(&bars.l_empty[g & 1]));
+        }
+        continue;
+      }
       const int e = w.e0 + x * kBlock + (warp & 3) * 32 + lane;
       const bool live = e < w.len;
       const int page = live ? raw_page(a.c, w.s, e) : 0;
@@ -446,10 +465,10 @@ __global__ void __launch_bounds__(kManyThreads, 1)
       const float before = live && a.mass != nullptr ? a.mass[at] : 0.f;
       uint64_t sum[2] = {0, 0};
       const uint64_t scale = pair(a.scale_log2, a.scale_log2);
-      for (int j = 0; j < w.steps; ++j, ++g) {
-        const int d = g & 1;
-        step_wait(smem_u32(&bars.l_full[d]), (g / 2) & 1, &s_failed, &g_status);
-        step_wait(smem_u32(&bars.s_full[x][d]), (g / 2) & 1, &s_failed, &g_status);
+      for (int j = 0; j < w.steps; ++j, ++g, ++gx) {
+        const int d = gx & 1;
+        step_wait(smem_u32(&bars.l_full[g & 1]), (g / 2) & 1, &s_failed, &g_status);
+        step_wait(smem_u32(&bars.s_full[x][d]), (gx / 2) & 1, &s_failed, &g_status);
         tc::fence_after();
         // columns before `seen` are rows that lie before this entry, those from
         // `end` on belong to no token of the sequence (and may hold anything)
@@ -460,7 +479,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         uint32_t v[2][32];
         tc::ld32(v[0], lanes + d * kBlock);
         tc::wait_ld32(v[0]);
-        const float* ls = s_lse[d];
+        const float* ls = s_lse[g & 1];
         if (all) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {  // the next 32 columns load while these are summed
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&bars.s_empty[x][d]));
-          mbar_arrive(smem_u32(&bars.l_empty[d]));
+          mbar_arrive(smem_u32(&bars.l_empty[g & 1]));
         }
       }
       const float2 both = unpair(add2(sum[0], sum[1]));
