@@ -116,6 +116,8 @@ WIDE = [
     (128, 32, 4, 1, _ragged(3, 18, 60, 400), 20),
     (64, 16, 2, 2, [(0, 9)] * 70 + [(1, 33)] + [(0, 0)] * 40 + [(2, 5)], 1),
     (64, 16, 2, 2, [(0, 9)] * 70 + [(40, 333)] + [(0, 0)] * 40 + [(2, 5)], 1),
+    (64, 16, 16, 16, _ragged(6, 24, 100, 300), 1),              # units for three rounds of blocks
+    (64, 16, 8, 8, _ragged(7, 50, 60, 200), 1),
 ]
 
 
