@@ -12,7 +12,8 @@
 // written.  The list lies in shared memory while every block has a
 // multiprocessor to itself (one sequence of 4159 entries: 12.8 us against 13.7),
 // else at the front of pos_out, where it is at most as long as what comes
-// there in the end (24 sequences: 91 us against 100 with the larger blocks).
+// there in the end (24 sequences: 91 us against 100 with the larger blocks).  (Both
+// before the passes got shorter; 12.4 and 90 since.)
 // Moving: a second kernel copies the rows of k and v whose place changed.
 // Sources lie at or beyond the new length and targets below it, so no copy
 // reads what another writes.
@@ -136,17 +137,23 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       const int i = i0 + 4 * lane;
       unsigned k[4] = {0u, 0u, 0u, 0u};
       if (i < len) load4(i, k);
+      bool in[4], same = true;
+      int bin[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const bool in = i + c < len && (k[c] & above) == prefix;
-        const int bin = (k[c] >> shift) & bins;
-        // lanes that all fall into the first one's bin (equal masses) count once
-        const int bin0 = __shfl_sync(kAll, bin, 0);
-        if (__all_sync(kAll, in && bin == bin0)) {
-          if (lane == 0) atomicAdd(&hist[bin], 32);
-        } else if (in) {
-          atomicAdd(&hist[bin], 1);
-        }
+        in[c] = i + c < len && (k[c] & above) == prefix;
+        bin[c] = (k[c] >> shift) & bins;
+      }
+      // entries that all fall into the first one's bin (equal masses) count once
+      const int bin0 = __shfl_sync(kAll, bin[0], 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) same &= in[c] && bin[c] == bin0;
+      if (__all_sync(kAll, same)) {
+        if (lane == 0) atomicAdd(&hist[bin0], 128);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (in[c]) atomicAdd(&hist[bin[c]], 1);
       }
     }
     __syncthreads();
@@ -232,12 +239,22 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       e_rank += in && k[c] == T;
       hole[c] = in && i + c < left && !st;
       mover[c] = i + c >= left && st;
-      const unsigned hb = __ballot_sync(kAll, hole[c]), mb = __ballot_sync(kAll, mover[c]);
-      h_rank += __popc(hb & below_lane);
-      m_rank += __popc(mb & below_lane);
-      nh += __popc(hb);
-      nm += __popc(mb);
     }
+    // (the whole warp lies below `left`, or at and behind it, but for one time)
+    if (i0 < left)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const unsigned b = __ballot_sync(kAll, hole[c]);
+        h_rank += __popc(b & below_lane);
+        nh += __popc(b);
+      }
+    if (i0 + 128 > left)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const unsigned b = __ballot_sync(kAll, mover[c]);
+        m_rank += __popc(b & below_lane);
+        nm += __popc(b);
+      }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       // a hole notes its rank (negative), a mover enters the list
