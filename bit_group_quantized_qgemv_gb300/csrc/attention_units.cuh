@@ -5,6 +5,8 @@
 // run it on the CPU.  (Included behind kv_cache.cuh.)
 #pragma once
 
+#include "runs.cuh"
+
 namespace qgemv {
 namespace {
 
@@ -79,10 +81,12 @@ struct Scheduler {
       for (int k = 0; k < n; ++k) {
         const int k_count = __shfl_sync(0xFFFFFFFFu, c_count, k), k_rows = rows_of(k_count);
         const int k_len = __shfl_sync(0xFFFFFFFFu, c_len, k), k_u = units_of(k_rows);
-        int t = 0;
+        long long t = 0;  // (2^22 row tiles of up to 2^22 tiles)
         for (int r = lane; r < k_u; r += 32) t += kUnitCost + tiles_of(r, k_rows, k_count, k_len);
-        t = __reduce_add_sync(0xFFFFFFFFu, t);
-        if (lane == k) c_span = t;
+        // summed in two halves: a lane has less than 2^40
+        const unsigned lo = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(t & 0x3FFFFFF));
+        const unsigned hi = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(t >> 26));
+        if (lane == k) c_span = (static_cast<long long>(hi) << 26) + lo;
       }
     } else {
       for (int r = 0; r < u; ++r) c_span += kUnitCost + tiles_of(r, n_rows, c_count, c_len);
@@ -163,11 +167,11 @@ struct Scheduler {
           continue;
         }
         const int k = __ffs(in) - 1;
-        const int rest = static_cast<int>(pos - __shfl_sync(0xFFFFFFFFu, to - here, k));
+        const long long rest = pos - __shfl_sync(0xFFFFFFFFu, to - here, k);
         const int step = __shfl_sync(0xFFFFFFFFu, each, k);
         rt = top - k;
-        h = rest / step;
-        return rest % step;
+        h = static_cast<int>(run_div(rest, step));
+        return static_cast<int>(rest - static_cast<long long>(h) * step);
       }
     }
     return -1;

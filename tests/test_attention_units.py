@@ -86,3 +86,18 @@ def test_cut_and_whole(program):
 
 def test_more_tokens_than_declared(program):
     check(program, [(700, 900), (20, 20)], 2, 4, True, max_q=300)
+
+
+# Spans (tiles and kUnitCost) past 2^31: of one head, 513 units of 2^22 tiles (131,328 rows
+# over 2^29 entries) alone and among short sequences; of the heads of one row tile, 1024 x
+# 2^22 (a page table may repeat its pages, so the cache need not be that large).
+LONG = [([(131328, 1 << 29)], 1, 1), ([(5, 9), (131328, 1 << 29), (0, 4)], 2, 1),
+        ([(16500, 1 << 29)], 1, 8), ([(16500, 1 << 29)] * 3, 3, 8), ([(256, 1 << 29)], 1024, 1)]
+
+
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_more_than_2_31_tiles(program, case, cut):
+    seqs, n_kv, group = LONG[case]
+    n_cut = check(program, seqs, n_kv, group, cut)
+    assert n_cut > 0 if cut else n_cut == 0

@@ -20,7 +20,7 @@
 namespace {
 
 struct Dim {
-  int x;
+  unsigned x;
 } gridDim, blockIdx;
 
 constexpr int kLanes = 32;
@@ -90,6 +90,7 @@ unsigned __ballot_sync(unsigned, bool p) {
   for (int i = 0; i < kLanes; ++i) r |= static_cast<unsigned>(a[i] != 0) << i;
   return r;
 }
+bool __all_sync(unsigned m, bool p) { return __ballot_sync(m, p) == 0xFFFFFFFFu; }
 // (sums of 32 bits, as the GPU's)
 template <typename T>
 T __reduce_add_sync(unsigned, T v) {
@@ -155,7 +156,7 @@ int main() {
       start[s + 1] += start[s];
     }
     gridDim.x = blocks;
-    for (blockIdx.x = 0; blockIdx.x < blocks; ++blockIdx.x) {
+    for (blockIdx.x = 0; blockIdx.x < gridDim.x; ++blockIdx.x) {
       AttnUnit dummy, mine[kLanes];
       const AttnArgs a{{len.data(), n_kv, n_seqs}, start.data(), start[n_seqs], max_q, group,
                        ~0ull / static_cast<unsigned>(group) + 1, cut ? &dummy : nullptr, nullptr};
@@ -165,14 +166,14 @@ int main() {
         Scheduler sc(a, lane);
         auto emit = [&](bool, int j0, int j1, int slot) {
           if (lane == 0)
-            std::printf("g %d %d %d %d %d %d %d %d %d\n", blockIdx.x, sc.s, sc.h, sc.rt * kUnitRows,
+            std::printf("g %u %d %d %d %d %d %d %d %d\n", blockIdx.x, sc.s, sc.h, sc.rt * kUnitRows,
                         sc.rows, sc.len - sc.count, j0, j1, slot);
           __syncwarp();
         };
         mine[lane] = hand_out(a, sc, lane, span, load, order, emit);
       });
       if (mine[0].parts > 0)
-        std::printf("u %d %d %d %d %d\n", blockIdx.x, mine[0].parts, mine[0].s, mine[0].h, mine[0].r0);
+        std::printf("u %u %d %d %d %d\n", blockIdx.x, mine[0].parts, mine[0].s, mine[0].h, mine[0].r0);
     }
     std::printf("end\n");
   }
