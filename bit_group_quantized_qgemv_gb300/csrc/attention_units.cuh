@@ -5,8 +5,6 @@
 // run it on the CPU.  (Included behind kv_cache.cuh.)
 #pragma once
 
-#include "runs.cuh"
-
 namespace qgemv {
 namespace {
 
@@ -81,9 +79,16 @@ struct Scheduler {
       for (int k = 0; k < n; ++k) {
         const int k_count = __shfl_sync(0xFFFFFFFFu, c_count, k), k_rows = rows_of(k_count);
         const int k_len = __shfl_sync(0xFFFFFFFFu, c_len, k), k_u = units_of(k_rows);
-        long long t = 0;  // (2^22 row tiles of up to 2^22 tiles)
+        // 32 bits where they are enough: the start of every call waits for this
+        if (static_cast<long long>(k_u) * (kUnitCost + k_len / kTile + 1) <= 0x7FFFFFFF) {
+          int t = 0;
+          for (int r = lane; r < k_u; r += 32) t += kUnitCost + tiles_of(r, k_rows, k_count, k_len);
+          t = __reduce_add_sync(0xFFFFFFFFu, t);
+          if (lane == k) c_span = t;
+          continue;
+        }
+        long long t = 0;  // (2^22 row tiles of up to 2^22 tiles, a lane has less than 2^40)
         for (int r = lane; r < k_u; r += 32) t += kUnitCost + tiles_of(r, k_rows, k_count, k_len);
-        // summed in two halves: a lane has less than 2^40
         const unsigned lo = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(t & 0x3FFFFFF));
         const unsigned hi = __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(t >> 26));
         if (lane == k) c_span = (static_cast<long long>(hi) << 26) + lo;
@@ -167,11 +172,17 @@ struct Scheduler {
           continue;
         }
         const int k = __ffs(in) - 1;
-        const long long rest = pos - __shfl_sync(0xFFFFFFFFu, to - here, k);
+        long long rest = pos - __shfl_sync(0xFFFFFFFFu, to - here, k);
         const int step = __shfl_sync(0xFFFFFFFFu, each, k);
         rt = top - k;
-        h = static_cast<int>(run_div(rest, step));
-        return static_cast<int>(rest - static_cast<long long>(h) * step);
+        h = 0;
+        if (rest >> 31 != 0) {  // (1024 heads of 2^22 + 4 at most: below 2^32 without half of them)
+          h = a.c.n_kv / 2;
+          rest -= static_cast<long long>(h) * step;
+        }
+        const unsigned left = static_cast<unsigned>(rest);
+        h += left / step;
+        return left % step;
       }
     }
     return -1;

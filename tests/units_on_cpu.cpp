@@ -90,7 +90,6 @@ unsigned __ballot_sync(unsigned, bool p) {
   for (int i = 0; i < kLanes; ++i) r |= static_cast<unsigned>(a[i] != 0) << i;
   return r;
 }
-bool __all_sync(unsigned m, bool p) { return __ballot_sync(m, p) == 0xFFFFFFFFu; }
 // (sums of 32 bits, as the GPU's)
 template <typename T>
 T __reduce_add_sync(unsigned, T v) {
