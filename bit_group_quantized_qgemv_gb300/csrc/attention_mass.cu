@@ -229,6 +229,43 @@ __device__ __forceinline__ void get_share(const MassArgs& a, long long b, long l
   w->steps = w->e0 < w->len ? max(0, (w->tokens + step_tokens - 1) / step_tokens - w->from) : 0;
 }
 
+// What entry e of a share receives, computed again in fp32 by one thread, from the rows
+// that count alone: taken where the sum came out a NaN, which may stem from a row whose lse
+// is -inf (it adds nothing, but its score, and so its weight in the sums below, may be a NaN).
+// Here because it costs nothing elsewhere: a test of every lse took 511 tokens over 16411
+// entries from 69.5 to 75.5 us, a flag for each step and a loop of its own to 72.8.  (The
+// other warps wait meanwhile: a row takes about a microsecond, so ten million rows are at
+// their limit, where the call ends with a status and without these entries.)
+template <int HD>
+__device__ __noinline__ float slow_sum(const MassArgs& a, int h, int first, int tokens, int off, int e,
+                                       int page) {
+  const uint4* k = reinterpret_cast<const uint4*>(a.c.k + cache_row(a.c, page, h, e) * HD);
+  float sum = 0.f;
+  for (int t = max(0, e - off); t < tokens; ++t)
+    for (int i = 0; i < a.group; ++i) {
+      const int head = h * a.group + i;
+      const float lse = a.lse[static_cast<long long>(first + t) * a.n_q + head];
+      if (lse == -INFINITY) continue;
+      const uint4* q = reinterpret_cast<const uint4*>(
+          a.q + static_cast<long long>(first + t) * a.q_stride + head * HD);
+      float x = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 kv = k[c], qv = q[c];
+        const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw[j]));
+          const float2 qf = __half22float2(*reinterpret_cast<const __half2*>(&qw[j]));
+          x = fmaf(qf.x, kf.x, x);
+          x = fmaf(qf.y, kf.y, x);
+        }
+      }
+      sum += ex2(fmaf(x, a.scale_log2, lse * -kLog2e));
+    }
+  return sum;
+}
+
 // One block per multiprocessor, each taking every gridDim.x-th share.  Warp 11
 // finds them ahead of the others (lengths and starts are three loads in a row, 2 us of
 // a share's 18 when every warp looked for itself), the producer is ahead of the sums
@@ -523,8 +560,11 @@ __global__ void __launch_bounds__(kManyThreads, 1)
         }
       }
       const float2 both = unpair(add2(sum[0], sum[1]));
-      if (live && *static_cast<volatile int*>(&s_failed) == 0)
-        a.mass_out[at] = before + (good_page(a.c, page, nullptr) >= 0 ? both.x + both.y : 0.f);
+      if (live && *static_cast<volatile int*>(&s_failed) == 0) {
+        float total = good_page(a.c, page, nullptr) >= 0 ? both.x + both.y : 0.f;
+        if (!(total == total)) total = slow_sum<HD>(a, w.h, w.first, w.tokens, w.off, e, page);
+        a.mass_out[at] = before + total;
+      }
     }
   }
   tc::fence_before();
