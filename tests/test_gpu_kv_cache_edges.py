@@ -35,3 +35,52 @@ def test_rows_of_no_lse_add_nothing(n_q, n_kv, m, value):
     close(got[0, :, :n], want[0, :, :n], tol[0, :, :n], "mass")
     close(got[1, :, :40], want[1, :, :40], tol[1, :, :40], "mass of the other sequence")
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("rows", [(1, 1), (6, 4), (75, 4)])   # new tokens, query heads
+@pytest.mark.parametrize("n,at", [(3000, 0), (14000, 0), (3000, 1500)])
+@pytest.mark.parametrize("nats", [12.3, 16.7, 18.0, 19.5])
+def test_light_entries_next_to_a_heavy_one(rows, n, at, nats):
+    """One entry of weight 1 with values of zero, all others e^-nats with values of one sign:
+    the output is what the light ones add up to.
+
+    A weight is rounded to fp16 (2^-11 of it, or 2^-32 of the largest weight), the exponent
+    errs by 2^-22 (nats + 1), the output by half a step of fp16 (2^-11, or 2^-25).  The sum of
+    the weights is one of fp32 additions: equal light weights onto a heavy one are all rounded
+    the same way, each by up to half a unit of the sum, 2^-24 of it.  The fewest
+    threads that share a row's entries are 4 warps of 8, so one adds up to n / 32 of them, and
+    40 more additions join the threads, warps and blocks: (n / 32 + 40) 2^-24 of the sum, which
+    is as much of the output and, in nats, of lse.  (The many-rows kernel adds 128 entries at a
+    time: n / 128.)"""
+    m, n_q = rows
+    hd, page = 64, 64
+    c = ref.make_cache(n + m, [(m, n)], 1, hd, page)
+    g = torch.Generator().manual_seed(m)
+    value = (1000 * (0.5 + torch.rand(n, hd, generator=g))).half()
+    heavy = torch.tensor(nats).half()
+    value[at] = 0
+    for e in range(0, n, page):
+        p, _ = c.entry(0, e)
+        k = min(page, n - e)
+        c.k[p, 0, :k, 0] = 0
+        c.v[p, 0, :k] = value[e:e + k]
+    p, r = c.entry(0, at)
+    c.k[p, 0, r, 0] = heavy
+    x = torch.zeros(m, n_q, hd).half()
+    x[:, :, 0] = 1
+    light = math.exp(-float(heavy))
+    added = (n / 32 + 40) * 2.0 ** -24
+    sums = torch.cumsum(value.double(), 0)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for ws in (None, none):
+        out, lse = q.paged_attention(handle(c), x.cuda(), c.q_start.cuda(), max_q=m, scale=1.0, want_lse=True,
+                                     workspace=ws)
+        for i in range(m):
+            e = n - m + i                           # sees the heavy entry and e light ones
+            z = 1 + e * light
+            want = (light * sums[e] / z).expand(n_q, hd)
+            tol = (want * (2.0 ** -10 + 2.0 ** -21 * (nats + 1) + added) + 2.0 ** -32 * sums[e] / z + 2.0 ** -25)
+            close(out[i].view(n_q, hd), want, tol, f"row {i}")
+            close(lse[i], torch.full((n_q,), float(heavy) + math.log(z)).double(),
+                  torch.full((n_q,), 2.0 ** -21 * (nats + 1) + added).double(), f"lse {i}")
+    assert q.device_status() == 0
