@@ -84,3 +84,36 @@ def test_light_entries_next_to_a_heavy_one(rows, n, at, nats):
             close(lse[i], torch.full((n_q,), float(heavy) + math.log(z)).double(),
                   torch.full((n_q,), 2.0 ** -21 * (nats + 1) + added).double(), f"lse {i}")
     assert q.device_status() == 0
+
+
+PI_60 = 3141592653589793238462643383279502884197169399375105820974944   # pi 10^60
+TURN = (10 ** 60 << 192) // (2 * PI_60)                                 # 2^192 / (2 pi)
+
+
+def test_rotation_of_far_positions():
+    """Positions at both ends of int32 at which a sine or a cosine is close to 0: the angle has
+    to be right to 3e-6 (as kv_reference.rope allows, which takes it from a rounded product)."""
+    hd, page, T = 64, 256, 256
+    at = list(range(2 ** 31 - 300000, 2 ** 31)) + list(range(-2 ** 31, -2 ** 31 + 300000))
+    # how far position * 1 is from a whole number of quarter turns, in 2^-64 of them
+    quarter = ((p, (4 * p * TURN >> 128) + (1 << 63) & (1 << 64) - 1) for p in at)
+    near = [p for p, x in quarter if abs(x - (1 << 63)) < (1 << 64) // 4000]
+    pos = (near + at[:T])[:T]
+    assert len(near) > T // 2
+    inv = torch.ones(hd // 2)
+    inv[1::2] = torch.rand(hd // 4, generator=torch.Generator().manual_seed(1))
+    qkv = torch.zeros(T, 3, hd).half()
+    qkv[:, :, :hd // 2] = 1.0
+    k = torch.zeros(1, 1, page, hd).half().cuda()
+    h = q.kv_cache(k, k.clone(), torch.zeros(1, 1, dtype=torch.int32).cuda(),
+                   torch.tensor([T], dtype=torch.int32).cuda())
+    out = q.qk_norm_rope_append(h, qkv.view(T, -1).cuda(), torch.tensor([0, T], dtype=torch.int32).cuda(),
+                                torch.tensor(pos, dtype=torch.int32).cuda(), inv.cuda())
+    # a float is a whole number over 2^149; the turn is taken from 2^64 parts of it
+    num = [int(f.double().item() * 2 ** 149) for f in inv]
+    turn = torch.tensor([[((p * n * TURN >> 277) & (1 << 64) - 1) / 2 ** 64 for n in num] for p in pos],
+                        dtype=torch.float64)
+    want = torch.cat([torch.cos(2 * math.pi * turn), torch.sin(2 * math.pi * turn)], 1)
+    tol = 2.0 ** -11 * want.abs() + 3e-6 + 2.0 ** -25
+    close(out, want, tol, "queries")
+    close(h.k[0, 0], want, tol, "keys")
