@@ -27,6 +27,14 @@ __device__ __forceinline__ void seq_rows(const int* q_start, int s, int n_tokens
   *count = b0 - a0;
 }
 
+// Checks of sequence s that a kernel which meets only some sequences makes for all.
+__device__ __forceinline__ void check_seq(const KvView& c, const int* q_start, int s, int n_tokens,
+                                          int* err) {
+  int first, count;
+  seq_rows(q_start, s, n_tokens, err, &first, &count);
+  seq_len(c, s, err);
+}
+
 // Page-table entry for entry i of sequence s, as it stands there.  Loops load it
 // a step ahead and look at it (good_page) when they need it: a look right after
 // the load would wait for it.

@@ -139,7 +139,7 @@ __device__ __forceinline__ void heads_pass(const __half* src, __half* dst, int s
 // per_pass heads of one kind.
 template <int HD, bool INTER, bool NORM, int U>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_append_kernel(const RopeArgs a, int per_warp,
-                                                                  int groups) {
+                                                                  int groups, int work) {
   constexpr int kLanes = HD / 8;       // lanes per head
   constexpr int kHeads = 32 / kLanes;  // heads a warp holds at once
   constexpr int kPerPass = kHeads * U;
@@ -152,6 +152,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_append_kernel(const
   const int d0 = rot ? 4 * l : rd + 4 * (l - rl);
   const int d1 = rot ? rd / 2 + 4 * l : rd + (HD - rd) / 2 + 4 * (l - rl);
   pdl_wait();
+  if (blockIdx.x >= work) {  // the checks of sequences that may have no token here
+    const int i = static_cast<int>(blockIdx.x - work) * 32 * kWarps + threadIdx.x;
+    if (i < a.c.n_seqs) check_seq(a.c, a.q_start, i, a.n_tokens, a.err);
+    return;
+  }
   const int t = static_cast<int>(task / groups);
   if (t >= a.n_tokens) return;
   // (frequencies and norms may be what the kernel before has just made: they are read
@@ -259,9 +264,12 @@ cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t st) {
   const int per_warp = static_cast<int>((all + split - 1) / split);
   const int groups = (all + per_warp - 1) / per_warp;
   const long long blocks = (static_cast<long long>(a.n_tokens) * groups + kWarps - 1) / kWarps;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  // With an error flag, blocks of their own look at every sequence's start and length, so
+  // that no token's warp waits for that.
+  const int checks = a.err == nullptr ? 0 : (a.c.n_seqs + 32 * kWarps - 1) / (32 * kWarps);
+  if (blocks + checks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks + checks));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -269,7 +277,8 @@ cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_append_kernel<HD, INTER, NORM, U>, a, per_warp, groups);
+  return cudaLaunchKernelEx(&cfg, rope_append_kernel<HD, INTER, NORM, U>, a, per_warp, groups,
+                            static_cast<int>(blocks));
 }
 
 template <int HD, bool INTER, bool NORM>

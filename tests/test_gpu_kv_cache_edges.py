@@ -117,3 +117,26 @@ def test_rotation_of_far_positions():
     tol = 2.0 ** -11 * want.abs() + 3e-6 + 2.0 ** -25
     close(out, want, tol, "queries")
     close(h.k[0, 0], want, tol, "keys")
+
+
+@pytest.mark.parametrize("starts,lens", [
+    ([0, 5, 3, 8], [20, 20, 20]),                   # falls where no token looks
+    ([0, 8, 8, 6], [20, 20, 20]),
+    ([0, 0, 4, 8], [-1, 20, 20]),                   # lengths of sequences without new tokens
+    ([0, 8, 8, 8], [20, 20, 33]),
+    ([0] * 200 + [8, 8], [20] * 199 + [20, 999]),
+])
+def test_rope_append_looks_at_every_sequence(starts, lens):
+    hd, T, S = 64, 8, len(lens)
+    k = torch.zeros(2 * S, 1, 16, hd).half().cuda()
+    table = torch.arange(2 * S, dtype=torch.int32).view(S, 2).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qkv = queries(1, T, 3, hd).cuda().view(T, -1)
+    pos = torch.arange(T, dtype=torch.int32).cuda()
+    good = torch.tensor([0] * S + [T], dtype=torch.int32).cuda()
+    q.qk_norm_rope_append(q.kv_cache(k, k.clone(), table, torch.full((S,), 20, dtype=torch.int32).cuda()),
+                          qkv, good, pos, err_flag=err)
+    assert int(err) == 0
+    h = q.kv_cache(k, k.clone(), table, torch.tensor(lens, dtype=torch.int32).cuda())
+    q.qk_norm_rope_append(h, qkv, torch.tensor(starts, dtype=torch.int32).cuda(), pos, err_flag=err)
+    assert int(err) == 1
