@@ -32,6 +32,17 @@ __device__ unsigned g_status = 0;
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Entries of sequence i, whose new tokens are checked too: one without entries has no
+// share of the work, and nobody else would look at them.
+__device__ __forceinline__ int checked_len(const MassArgs& a, int i) {
+  if (a.err != nullptr) {
+    int first, count;
+    seq_rows(a.q_start, i, a.n_tokens, a.err, &first, &count);
+    if (count > a.max_q) flag_error(a.err);
+  }
+  return seq_len(a.c, i, a.err);
+}
+
 // ------------------------------------------------------------- few rows
 constexpr int kWarps = 4;
 constexpr int kTile = 16;
@@ -57,14 +68,13 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(NT)) mass_few_kernel
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
   // blocks of 64 entries of a sequence's units
-  auto blocks_of = [&](int i) { return (seq_len(a.c, i, a.err) + 63) / 64; };
+  auto blocks_of = [&](int i) { return (checked_len(a, i) + 63) / 64; };
   int s, h, j0;
   long long per, left = run_start(a.c.n_seqs, a.c.n_kv, 2, lane, blocks_of, &per, &s, &h, &j0);
   while (left > 0) {  // segments of this block's run
     const int len = seq_len(a.c, s, nullptr);
     int first, count;
-    seq_rows(a.q_start, s, a.n_tokens, a.err, &first, &count);
-    if (count > a.max_q) flag_error(a.err);
+    seq_rows(a.q_start, s, a.n_tokens, nullptr, &first, &count);
     const int j1 = static_cast<int>(min(static_cast<long long>((len + 63) / 64), j0 + left));
     const int k0 = j0 * 64, k1 = min(len, j1 * 64);
     left -= j1 - j0;
@@ -206,22 +216,19 @@ struct Share {
 
 // Pairs of tiles of sequence i's units, and share number b of all: pairs, the
 // first `whole` of them as they are, then the tiles of the rest one by one.  A whole warp.
-__device__ __forceinline__ int shares_of(const MassArgs& a, int i, int* err) {
-  return (seq_len(a.c, i, err) + 2 * kBlock - 1) / (2 * kBlock);
-}
+__device__ __forceinline__ int shares_of(int len) { return (len + 2 * kBlock - 1) / (2 * kBlock); }
 __device__ __forceinline__ void get_share(const MassArgs& a, long long b, long long whole,
                                           int step_tokens, int lane, Share* w) {
   int j;
   const int half = b < whole ? -1 : static_cast<int>((b - whole) & 1);
   if (half >= 0) b = whole + ((b - whole) >> 1);
-  run_seek(b, a.c.n_seqs, a.c.n_kv, lane, [&](int i) { return shares_of(a, i, nullptr); }, &w->s,
+  run_seek(b, a.c.n_seqs, a.c.n_kv, lane, [&](int i) { return shares_of(seq_len(a.c, i, nullptr)); }, &w->s,
            &w->h, &j);
   w->e0 = j * 2 * kBlock + max(half, 0) * kBlock;
   w->len = seq_len(a.c, w->s, nullptr);
   w->tiles = half >= 0 || w->e0 + kBlock >= w->len ? 1 : 2;
   int count;
-  seq_rows(a.q_start, w->s, a.n_tokens, a.err, &w->first, &count);
-  if (count > a.max_q) flag_error(a.err);
+  seq_rows(a.q_start, w->s, a.n_tokens, nullptr, &w->first, &count);
   w->tokens = min(count, a.max_q);
   w->off = w->len - count;
   // steps of step_tokens tokens, from the one whose last token sees entry e0
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   } else if (warp == 11) {
     // ------------------------------------------------------------ shares
     const long long pairs = run_total(a.c.n_seqs, a.c.n_kv, lane,
-                                      [&](int i) { return shares_of(a, i, a.err); });
+                                      [&](int i) { return shares_of(checked_len(a, i)); });
     // The pairs behind the last full round go out tile by tile where every block
     // then still gets one at most (520 pairs on 152 blocks: 68 us against 72).
     const long long rest = pairs % gridDim.x, whole = pairs - (2 * rest <= gridDim.x ? rest : 0);

@@ -140,3 +140,24 @@ def test_rope_append_looks_at_every_sequence(starts, lens):
     h = q.kv_cache(k, k.clone(), table, torch.tensor(lens, dtype=torch.int32).cuda())
     q.qk_norm_rope_append(h, qkv, torch.tensor(starts, dtype=torch.int32).cuda(), pos, err_flag=err)
     assert int(err) == 1
+
+
+@pytest.mark.parametrize("n_q", [2, 64])
+@pytest.mark.parametrize("starts,lens,max_q", [
+    ([0, 2, 1, 1], [20, 0, 20], 2),                 # the one that falls has no entries
+    ([0, 1, 1, 9], [20, 20, 0], 2),
+    ([0, 0, 2, 2], [20, 0, 20], 1),                 # more tokens than declared, without entries
+    ([0] * 100 + [2, 2], [20] * 99 + [0, 20], 1),
+])
+def test_mass_looks_at_every_sequence(starts, lens, max_q, n_q):
+    hd, T, S = 64, 2, len(lens)
+    k = torch.zeros(2 * S, 1, 16, hd).half().cuda()
+    table = torch.arange(2 * S, dtype=torch.int32).view(S, 2).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = queries(1, T, n_q, hd).cuda()
+    lse = torch.zeros(T, n_q).cuda()
+    h = q.kv_cache(k, k.clone(), table, torch.tensor(lens, dtype=torch.int32).cuda())
+    q.attention_mass(h, x, torch.tensor([0] * S + [1], dtype=torch.int32).cuda(), lse, max_q=max_q, err_flag=err)
+    assert int(err) == 0
+    q.attention_mass(h, x, torch.tensor(starts, dtype=torch.int32).cuda(), lse, max_q=max_q, err_flag=err)
+    assert int(err) == 1
