@@ -587,7 +587,7 @@ def _token_rows(cache, t, name, rows=None, width=None):
         inner = stride[1] == 1
     elif len(shape) == 3:
         n, w = shape[0], shape[1] * shape[2]
-        inner = stride[2] == 1 and stride[1] == shape[2]
+        inner = stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
     else:
         inner = False
     if not inner:
