@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring = base + 2 * Sh::kSlotBytes;
 
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::kSlots; ++i) {
       mbar_init(smem_u32(&bars.full[i]), 1);
@@ -134,11 +133,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     s_failed = 0;
   }
+  // Tensor memory is taken behind the kernel before and ahead of the one behind: no block
+  // holds some while it waits for a block that may need it, on the same multiprocessor, to end.
+  pdl_wait();
   if (warp == kMmaWarp) tc::alloc(smem_u32(&s_tmem), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t tmem = s_tmem;
 
   // Segment number n, as every warp but the scheduler reads it; the last look

@@ -291,7 +291,6 @@ __global__ void __launch_bounds__(kManyThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* qring = base + 4 * Sh::kBytes;
-  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&bars.keys[x]), 1);
@@ -317,11 +316,14 @@ __global__ void __launch_bounds__(kManyThreads, 1)
     fence_mbar_init();
     s_failed = 0;
   }
+  // Tensor memory is taken behind the kernel before and ahead of the one behind: no block
+  // holds some while it waits for a block that may need it, on the same multiprocessor, to end.
+  pdl_wait();
   if (warp == 8) tc::alloc(smem_u32(&s_tmem), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t tmem = s_tmem;
   Share w;
   // Share number n of this block, as every warp but the finder reads it; false
