@@ -269,6 +269,7 @@ __device__ __noinline__ float slow_sum(const MassArgs& a, int h, int first, int 
         }
       }
       sum += ex2(fmaf(x, a.scale_log2, lse * -kLog2e));
+      if (!(sum == sum)) return sum;  // a row that counts has a NaN
     }
   return sum;
 }

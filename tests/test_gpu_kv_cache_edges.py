@@ -161,3 +161,115 @@ def test_mass_looks_at_every_sequence(starts, lens, max_q, n_q):
     assert int(err) == 0
     q.attention_mass(h, x, torch.tensor(starts, dtype=torch.int32).cuda(), lse, max_q=max_q, err_flag=err)
     assert int(err) == 1
+
+
+def off(t, by=1):
+    """The same tensor on the GPU, `by` elements behind an aligned address."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+    view = buf[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("hd,n_q,n_kv,seqs", [(64, 3, 1, [(1, 500), (2, 77)]), (128, 8, 2, [(40, 300), (1, 9)])])
+def test_numbers_off_their_16_byte_boundaries(hd, n_q, n_kv, seqs):
+    """Starts, lengths, lse and mass need 4 bytes of alignment, the fused QKV rows 8 and
+    strides that are multiples of 4."""
+    c = ref.make_cache(7, seqs, n_kv, hd, 16)
+    T, max_q, scale = sum(m for m, _ in seqs), max(m for m, _ in seqs), hd ** -0.5
+    x = queries(7, T, n_q, hd)
+    h = q.kv_cache(c.k.cuda(), c.v.cuda(), off(c.table), off(c.lens, 3))
+    qs = off(c.q_start)
+    want, want_lse, tol, lse_tol = ref.attention(c, x, scale)
+    out, lse = q.paged_attention(h, x.cuda(), qs, max_q=max_q, lse=off(torch.zeros(T, n_q)))
+    close(out.view(T, n_q, hd), want, tol, "out")
+    close(lse, want_lse, lse_tol, "lse")
+    mass = torch.rand(len(seqs), n_kv, c.cap)
+    got = q.attention_mass(h, x.cuda(), qs, lse, max_q=max_q, mass=off(mass), mass_out=off(torch.zeros_like(mass), 2))
+    want_m, tol_m = ref.attention_mass(c, x, lse.cpu(), scale, mass)
+    for s, (_, n) in enumerate(seqs):
+        close(got[s, :, :n], want_m[s, :, :n], tol_m[s, :, :n], "mass")
+    # QKV rows behind four values, 4 values apart; queries into rows like that
+    w = (n_q + 2 * n_kv) * hd
+    wide = torch.zeros(T * (w + 4) + 4).half().cuda()[4:].view(T, w + 4)
+    qkv = queries(8, T, n_q + 2 * n_kv, hd).view(T, w)
+    wide[:, :w] = qkv.cuda()
+    room = torch.zeros(T * (n_q * hd + 12) + 4).half().cuda()[4:].view(T, n_q * hd + 12)
+    pos = off(torch.arange(T, dtype=torch.int32))
+    inv = off(torch.rand(hd // 2))
+    gamma = torch.rand(hd).half()
+    q.qk_norm_rope_append(h, wide[:, :w], qs, pos, inv, q_norm=off(gamma, 4), k_norm=off(gamma, 4),
+                          q_out=room[:, :n_q * hd], entry_mass=off(mass))
+    for t in range(T):
+        want, tol = ref.rope(qkv[t].view(-1, hd)[:n_q], t, inv.tolist(), gamma, 1e-6, False)
+        close(room[t, :n_q * hd].view(n_q, hd), want, tol, "query")
+    assert bool((room[:, n_q * hd:] == 0).all())
+
+
+@pytest.mark.parametrize("n_kv,lens,keep,extra", [(2, [700, 40], 300, 0), (8, [300] * 24, 200, 0),
+                                                  (2, [700, 90], 60, 3300)])
+def test_evict_off_16_byte_boundaries(n_kv, lens, keep, extra):
+    c = ref.make_cache(3, [(0, n) for n in lens], n_kv, 64, 16, poison=False, extra_pages=extra)
+    S, g = len(lens), torch.Generator().manual_seed(3)
+    mass = torch.floor(torch.rand(S, n_kv, c.cap, generator=g) * 40)
+    pos = torch.argsort(torch.rand(S, n_kv, c.cap, generator=g), -1).int()
+    nxt = torch.tensor(lens, dtype=torch.int32)
+    kept, mo, po, left = q.cache_evict(
+        handle(c), off(mass), off(pos, 2), off(nxt), keep, n_sink=3, n_recent=8,
+        kept=off(torch.zeros(S, n_kv, keep, dtype=torch.int32), 3), mass_out=off(torch.zeros_like(mass), 3),
+        pos_out=off(torch.zeros_like(pos)), kv_len_out=off(torch.zeros(S, dtype=torch.int32), 2))
+    want, want_left = ref.evict(c, mass, pos, nxt, keep, 3, 8)
+    assert left.tolist() == want_left and torch.equal(kept.cpu(), want)
+    for s, n in enumerate(want_left):
+        for hh in range(n_kv):
+            src = want[s, hh, :n].long()
+            assert torch.equal(mo[s, hh, :n].cpu(), mass[s, hh, src])
+            assert torch.equal(po[s, hh, :n].cpu(), pos[s, hh, src])
+
+
+@pytest.mark.parametrize("n_q,n_kv,seqs", [(2, 2, [(50, 0)]), (4, 1, [(60, 0), (9, 9), (300, 2), (0, 40)]),
+                                           (6, 2, [(30, 7)] * 40)])
+def test_many_new_tokens_over_empty_caches(n_q, n_kv, seqs):
+    hd = 64
+    c = ref.make_cache(1, seqs, n_kv, hd, 16)
+    T, max_q = sum(m for m, _ in seqs), max(m for m, _ in seqs)
+    x = queries(1, T, n_q, hd)
+    want, want_lse, tol, lse_tol = ref.attention(c, x, hd ** -0.5)
+    for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+        out = torch.full((T, n_q, hd), 5.0).half().cuda()
+        _, lse = q.paged_attention(handle(c), x.cuda(), c.q_start.cuda(), max_q=max_q, out=out, want_lse=True,
+                                   workspace=ws)
+        close(out, want, tol, "out")
+        close(lse, want_lse, lse_tol, "lse")
+    m = q.attention_mass(handle(c), x.cuda(), c.q_start.cuda(), lse, max_q=max_q)
+    want_m, tol_m = ref.attention_mass(c, x, lse.cpu(), hd ** -0.5, torch.zeros(len(seqs), n_kv, c.cap))
+    close(m, want_m, tol_m, "mass")
+    assert q.device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls of every kernel on two streams, workspaces of their own: as one after the other."""
+    jobs = []
+    for i, (n_q, seqs) in enumerate([(4, [(1, 9000), (1, 5000)]), (8, [(60, 3000)]), (4, [(1, 14000)]),
+                                     (2, [(200, 700)]), (4, [(7, 4000)] * 4)]):
+        c = ref.make_cache(70 + i, seqs, 2, 64, 16)
+        T, m = sum(m for m, _ in seqs), max(m for m, _ in seqs)
+        jobs.append((handle(c), queries(70 + i, T, n_q, 64).cuda(), c.q_start.cuda(), m))
+
+    def run(job):
+        h, x, qs, m = job
+        out, lse = q.paged_attention(h, x, qs, max_q=m, want_lse=True)
+        return out, lse, q.attention_mass(h, x, qs, lse, max_q=m)
+
+    want = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for turn in range(4):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k] += [(i, run(jobs[i])) for i in (range(5) if k == 0 else reversed(range(5)))]
+    torch.cuda.synchronize()
+    for i, res in got[0] + got[1]:
+        assert all(torch.equal(a, b) for a, b in zip(res, want[i]))
+    assert q.device_status() == 0
