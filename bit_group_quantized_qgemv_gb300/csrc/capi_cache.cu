@@ -47,12 +47,14 @@ int check_cache(const qgemv_kv_cache* c, KvView* v) {
   return QGEMV_OK;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 // Query-side shape: n_q a multiple of n_kv, the rows of a sequence countable in
 // 30 bits.
 int check_queries(const KvView& c, long long q_stride, int n_tokens, int n_q, int max_q,
                   float scale) {
   if (n_tokens < 0 || n_q < 1 || n_q % c.n_kv != 0 || n_q > 65535 || max_q < 1 ||
-      max_q > 1 << 24 || !(scale > 0.0f) || !std::isfinite(scale))
+      max_q > 1 << 24 || !(scale > 0.0f) || !std::isfinite(scale * kLog2e))
     return QGEMV_EINVAL;
   if (q_stride < static_cast<long long>(n_q) * c.head_dim || q_stride % 8 != 0)
     return QGEMV_EINVAL;
@@ -60,8 +62,6 @@ int check_queries(const KvView& c, long long q_stride, int n_tokens, int n_q, in
   if (rows > 0x3FFFFFFFLL) return QGEMV_EINVAL;
   return QGEMV_OK;
 }
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace
 

@@ -556,7 +556,8 @@ int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
  *   [n_tokens][n_q] or NULL.
  *   max_q: the largest q_len (tokens beyond it are left out and set
  *   *err_flag).  Checks: n_tokens >= 0, n_q a multiple of n_kv and at most 65535,
- *   1 <= max_q <= 2^24, max_q * (n_q / n_kv) < 2^30, scale finite and > 0.
+ *   1 <= max_q <= 2^24, max_q * (n_q / n_kv) < 2^30, scale > 0 and scale * log2(e)
+ *   finite.
  *   workspace: device, 16-byte aligned, workspace_bytes long, contents on entry
  *   ignored; with fewer than qgemv_paged_attention_workspace_bytes bytes (NULL
  *   and 0 too) a sequence's cache is not split over thread blocks, which can be
