@@ -25,8 +25,9 @@
 // Weights, lifted by kLift, are then at most 2^15, inside fp16, and rounded to 11 bits
 // down to 2^-21 of the maximum.
 //
-// 2048 tokens over 30759 entries (32/8 heads of 128) take 660 us, 1.51 PFLOP/s or
-// 79 % of a library product.  What bounds it: Q K^T reads both operands from shared
+// 2048 tokens over 30759 entries (32/8 heads of 128) take 660 us in a few replays of a
+// graph, 1.51 PFLOP/s or 79 % of a library product; in calls one after the other, where the
+// power limit lowers the clocks, 740 to 770 us, 1.30 to 1.35 PFLOP/s.  What bounds it: Q K^T reads both operands from shared
 // memory, which at 128 columns takes its 128 bytes a clock; P V (P in tensor memory)
 // does not.  The softmax, in pairs of floats, just hides behind the products: as single
 // floats it took 685 us, with an eighth of the exponentials by polynomial 2 % more.

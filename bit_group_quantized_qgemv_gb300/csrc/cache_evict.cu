@@ -10,10 +10,13 @@
 // index order are prefix sums over the warps' counts.  The movers are listed, the
 // holes pick theirs from the list, and only then the permuted masses and positions are
 // written.  The list lies in shared memory while every block has a
-// multiprocessor to itself (one sequence of 4159 entries: 12.8 us against 13.7),
-// else at the front of pos_out, where it is at most as long as what comes
-// there in the end (24 sequences: 91 us against 100 with the larger blocks).  (Both
-// before the passes got shorter; 12.4 and 90 since.)
+// multiprocessor to itself (one sequence of 4159 entries, 8 heads: 12.4 us a call
+// against 14.2), else at the front of pos_out, where it is at most as long as what comes
+// there in the end (24 sequences, 192 heads: 90.3 us against 98.7 with the larger
+// blocks).  What decides is the capacity, as the host knows no lengths: with
+// a table for more than kKeysMax entries the keys are made again at every pass (4159
+// entries 14.4 us for 11.4 from a graph, 24 sequences 115 for 103), and a head has one
+// block at any length (131072 entries, 8 heads: 155 us).
 // Moving: a second kernel copies the rows of k and v whose place changed.
 // Sources lie at or beyond the new length and targets below it, so no copy
 // reads what another writes.

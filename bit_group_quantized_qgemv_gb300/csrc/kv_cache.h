@@ -94,7 +94,12 @@ cudaError_t attention_mass_launch(const MassArgs& a, int sms, cudaStream_t st, i
 cudaError_t cache_evict_launch(const EvictArgs& a, int sms, cudaStream_t st, int device);
 
 // Whether a call has more query rows per key/value head than the mma.sync
-// kernel takes in one pass over the cache: those go to the tcgen05 kernel.
+// kernel takes in one pass over the cache: those go to the tcgen05 kernel.  At 24 and 32
+// rows, 8 key heads, replayed from a graph, the two kernels take (us)
+//   heads of 64,  one of 3000  8.6 and 17.7, 10.0 and 17.4;  of 21000  17.5 and 25.1, 19.9 and 24.6;
+//                 four of 3000 to 21000  24.6 and 43.4, 28.5 and 42.5
+//   heads of 128, one of 3000 13.3 and 20.0, 18.5 and 19.6;  of 21000  23.9 and 29.4, 33.2 and 28.8;
+//                 four of 3000 to 21000  44.0 and 53.0, 56.0 and 51.4
 inline bool attention_is_many(int group, int max_q) {
   return static_cast<long long>(group) * max_q > 32;
 }

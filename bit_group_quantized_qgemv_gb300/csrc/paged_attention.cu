@@ -17,11 +17,11 @@
 //
 // Up to 16 rows P enters as fp16 high and low parts (two products with V): 22 bits of
 // a weight down to 2^-9 of the running maximum, below that what lies above 2^-32 of it
-// (kLift).  The kernel is bound by HBM there, not by the
-// products.  48 sequences of 900 to 20000 entries (32/8 heads of 128, 1.23 GB) take
-// 185 us, 6.65 TB/s or 98 % of the measured copy bandwidth.  With more rows the
-// products are the bound, and P is rounded once to fp16, like every weight of the
-// tcgen05 kernel.
+// (kLift).  The kernel is bound by HBM there, not by the products.  48 sequences of 900
+// to 20000 entries (32/8 heads of 128, 1.23 GB) take 185 us, 6.65 TB/s or 98 % of the
+// measured copy bandwidth.  With more rows the products are the bound, and P is rounded
+// once to fp16, like every weight of the tcgen05 kernel.  Heads of 128 with more
+// rows than 16 take 255 registers and spill 16 bytes (24 rows) and 284 (32).
 #include <atomic>
 
 #include "attention_common.cuh"
@@ -589,18 +589,27 @@ cudaError_t launch_few_rows(const AttnArgs& a, int sms, cudaStream_t st, int dev
 // Whether a cluster of blocks takes each (sequence, head) unit and joins on
 // chip, by the number of units and the capacity (the lengths are on the device);
 // otherwise the entries are cut into equal runs (runs.cuh), joined by a second
-// kernel.  Measured on GB300, 32/8 heads of 128, one new token per sequence,
-// replayed from a graph, clusters of 8 against runs and their join (us):
-//   1 sequence   1000 entries  6.6 against 7.9;   4110   8.9 and 10.9;
-//                8000         10.8 and 11.5;     12000  13.1 and 13.6;
-//               16000         15.2 and 14.5
-//   2 sequences  1000          7.5 and  8.7;      4000  10.7 and 12.0;   8000  15.2 and 12.1
-//   4 sequences  1000          8.3 and  8.9;      4000  11.9 and 12.7
-// (clusters of 16: 14.7 us at one of 4110).  A cluster also saves the workspace
-// and a launch, 4 us of a call's time on the host.  So clusters serve one sequence's
-// 8 heads up to parts of 1536 entries, and more units up to 512 while their
-// blocks fill the machine at most once.  With longer caches a cluster lasts as
-// long as its sequence.
+// kernel.  Measured on GB300, four query heads of 128 to a key head, one new token per
+// sequence, replayed from a graph, clusters of 8 against runs and their join (us):
+//   1 sequence, key heads   1000        4110          8000          12000     entries
+//                 8    5.9 and 7.5   8.1 and 10.3  10.0 and 11.1  12.3 and 12.9
+//                 4    5.9     6.6   7.9      9.9   9.8     11.1  12.0     11.5
+//                 2    5.8     6.2   7.8      9.2   9.6     10.4  11.8     10.5
+//                 1    5.6     6.2   7.8      7.2   9.5      8.2  11.8      9.6
+//   sequences, key heads    1000        4000
+//              2, 4    5.9 and 7.7   7.7 and  9.9
+//              4, 2    5.9     7.5   7.8      9.9
+//              4, 4    7.2     8.1  10.4     11.2
+//              2, 8    7.5      8.7  10.7     12.0
+//              4, 8    8.3      8.9  11.9     12.7
+// (one sequence of 16000, 8 heads: 15.2 and 14.5; two of 8000: 15.2 and 12.1; clusters
+// of 16: 14.7 at one of 4110).  A cluster also saves the workspace and a launch, 4 us of
+// a call's time on the host.  So clusters serve one sequence's 8 heads up to parts of 1536
+// entries, and more units up to 512 while their blocks fill the machine at most once.
+// The rule was cut for 8 key heads; with a single one the runs are ahead on the GPU from
+// 4000 entries on, with two and four from 12000.  With longer caches a cluster lasts as long as
+// its sequence; a table with room for more than the rule's entries goes to the runs whatever the
+// sequence's length.
 int few_cluster(int n_seqs, int n_kv, long long capacity, int sms) {
   const long long units = static_cast<long long>(n_kv) * n_seqs;
   const bool fits = capacity > 128 && units <= 2 * sms / kMaxCluster &&

@@ -20,8 +20,9 @@ namespace {
 
 constexpr int kWarps = 4;
 // Blocks to a multiprocessor that the registers are cut for (measured with four
-// groups of heads a pass, 8205 tokens of 48 heads: 5 blocks 38.1, 6 39.7, 7 36.2, 8
-// 37.9, 10 47.2 us).
+// groups of heads a pass, 7622 tokens of 48 heads: 5 blocks 38.1, 6 39.7, 7 36.2, 8
+// 37.9, 10 47.2 us).  The normed forms spill 68 to 96 bytes at these 72 registers (with one
+// group of heads a pass 4, for heads of 64), and are fastest all the same.
 constexpr int kBlocks = 7;
 
 // 1 / (2 pi) as a sum of floats: 48 bits, and 24 more.

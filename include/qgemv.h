@@ -490,7 +490,7 @@ int qgemv_lut4(const uint32_t *codes, const uint16_t *lut, int n_luts, int rows_
  * q_start[s] .. q_start[s+1]-1 (q_start: int32 [n_seqs+1], device), 0 or more.
  * Its j-th new token is entry kv_len[s] - q_len + j and sees the entries up
  * to its own.  Rows before q_start[0] and from q_start[n_seqs] on belong to no
- * sequence: they are neither read nor written.
+ * sequence: nothing of them reaches a result, and they are not written.
  * Checks of the four calls: head_dim 64 or 128; page_size 16, 32, 64, 128 or
  * 256; n_pages, n_kv, n_seqs, max_pages >= 1; n_seqs <= 65535; n_kv <= 1024;
  * max_pages * page_size <= 2^29, n_pages * n_kv * page_size < 2^31 (EINVAL).
@@ -500,7 +500,8 @@ int qgemv_lut4(const uint32_t *codes, const uint16_t *lut, int n_luts, int rows_
  * kv_len outside [0, max_pages * page_size] and a q_start that falls or leaves
  * [0, n_tokens] are clamped.  Pages may be shared between sequences where no
  * call writes them (an append writes the new entries' pages, an eviction any page
- * of the sequence).  With n_tokens = 0 the arrays of token rows may be NULL.
+ * of the sequence), and one sequence's table may repeat a page that no call writes.
+ * With n_tokens = 0 the arrays of token rows may be NULL.
  */
 typedef struct {
   uint16_t *k, *v;
@@ -526,8 +527,9 @@ typedef struct {
  * entry would be negative (q_len > kv_len) sets *err_flag; its query is
  * written, its key and value are not.
  *   positions int32 [n_tokens] (any value; the angle is reduced from the exact
- *   product), inv_freq fp32 [rotary_dim/2], both device; strides in elements,
- *   multiples of 4; qkv, q_out, norms 8-byte aligned, the rest 4-byte.
+ *   product, to within 8.3e-7 radians), inv_freq fp32 [rotary_dim/2], both device;
+ *   strides in elements, multiples of 4; qkv, q_out, norms 8-byte aligned, the rest
+ *   4-byte.
  *   Checks: n_tokens >= 0 (0: nothing is enqueued), n_q a multiple of n_kv and at
  *   most 65535, 0 <= rotary_dim <= head_dim, a multiple of 8, qkv_stride >= (n_q + 2
  *   n_kv) * head_dim, q_stride >= n_q * head_dim, eps > 0 when normed, the
@@ -547,10 +549,13 @@ int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
  * reads key/value head h / (n_q / n_kv):
  *   p_j = exp(scale * q . k_j),  out = sum_{j <= e} p_j v_j / sum_{j <= e} p_j,
  *   lse = log(sum_{j <= e} p_j)
- * with fp32 scores, maxima and sums (the weights p_j enter the product with v
- * as fp16).  A token that sees nothing (e < 0, or only bad pages) gets out = 0
+ * with fp32 scores, maxima and sums.  The weights p_j enter the product with v
+ * as fp16: they are rounded to 11 bits (22 where max_q * (n_q / n_kv) is
+ * at most 16), and by up to 2^-32 of the row's largest weight.  A token that sees nothing (e < 0, or only bad pages) gets out = 0
  * and lse = -inf.  What a token does not see does not reach it, not even as an
- * infinity or a NaN.
+ * infinity or a NaN (a row that hides one is computed again by one warp, some 3 us
+ * for 32 entries; where that keeps a thread block waiting for more than 10 s, from 3
+ * million entries on, qgemv_device_status reports it and rows are missing).
  *   q, out: fp16 rows of n_q * head_dim, strides in elements; 16-byte aligned,
  *   strides multiples of 8; out may not overlap q (out == q: EINVAL).  lse: fp32
  *   [n_tokens][n_q] or NULL.
@@ -563,8 +568,11 @@ int qgemv_qk_norm_rope_append(const qgemv_kv_cache *cache, const uint16_t *qkv,
  *   and 0 too) a sequence's cache is not split over thread blocks, which can be
  *   much slower for few long sequences.  Calls sharing a workspace must not
  *   overlap on the GPU.
- * Up to two launches (the second joins the parts of a split cache).  How far a
- * page table reaches beyond the sequences costs nothing.
+ * Up to two launches (the second joins the parts of a split cache).  What is read
+ * does not depend on how far a page table reaches beyond the sequences; the form
+ * does: tables for up to 12288 entries (one sequence's 8 key/value heads; 4096 with up to
+ * 38 units of a head of a sequence) need no workspace and one launch, wider ones two: one
+ * token over 4111 entries takes 8.2 us, with a table for 131072 entries 10.3.
  */
 int qgemv_paged_attention(const qgemv_kv_cache *cache, const uint16_t *q, long long q_stride,
                           int n_tokens, int n_q, const int32_t *q_start, int max_q, float scale,
@@ -587,7 +595,8 @@ size_t qgemv_paged_attention_workspace_bytes(const qgemv_kv_cache *cache, int n_
  * nothing).  mass (NULL: zeros) and mass_out: fp32
  * [n_seqs][n_kv][max_pages * page_size] device, which may be the same array.
  * An entry on a bad page receives nothing.  max_q as there; the sums run in a
- * fixed order.  One launch.
+ * fixed order.  One launch.  (A sum that comes out a NaN is computed again without
+ * the rows whose lse is -inf, by one thread, a microsecond or so for a row and head.)
  */
 int qgemv_attention_mass(const qgemv_kv_cache *cache, const uint16_t *q, long long q_stride,
                          int n_tokens, int n_q, const int32_t *q_start, int max_q, float scale,
@@ -613,7 +622,11 @@ int qgemv_attention_mass(const qgemv_kv_cache *cache, const uint16_t *q, long lo
  *   kv_len_out int32 [n_seqs]: len'
  * The outputs may not overlap the inputs.  An entry of kept whose page, old or
  * new, is bad is listed but not copied.  Checks: 1 <= keep <= 2^30, n_sink and
- * n_recent >= 0, n_sink + n_recent <= keep.  Two launches.
+ * n_recent >= 0, n_sink + n_recent <= keep.  Two launches.  One thread block selects
+ * for each head of each sequence, however long it is, and up to 51200 entries that
+ * the page table has room for it keeps what it ranks on chip: 4159 entries cut to 4096
+ * (8 heads) take 11.4 us, with a table for 131072 entries 14.4; 131072 cut to 4096 take
+ * 155 us.
  */
 int qgemv_cache_evict(const qgemv_kv_cache *cache, const float *mass, const int32_t *entry_pos,
                       const int32_t *next_pos, int keep, int n_sink, int n_recent, int32_t *kept,
