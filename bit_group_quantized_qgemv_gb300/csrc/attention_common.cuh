@@ -7,14 +7,17 @@ namespace qgemv {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Weights enter the product with v as fp16, and are taken relative to the running
-// maximum less kLift (in log2): 2^kSlack above the maximum they reach 2^15, and of an entry
-// far below it 2^-32 of the maximum is the most that a rounding takes or adds (2^-25
-// without the lift: one heavy entry in front of 3000 that are 18 nats lighter left nothing of
-// them, or added half as much again).  Sums and outputs carry the same factor, which falls out
-// of their quotient and is taken out of lse.
-constexpr float kSlack = 8.0f;  // log2 of the growth that makes the maximum move
-constexpr float kLift = 7.0f;
+// Weights enter the product with v as fp16, relative to 2^base (the kernels' m): a
+// base is a row's maximum at some time less kLift, in log2 units, and moves once a
+// weight would pass 2^kTop.  Of an entry far below the maximum 2^-32 of the largest weight is the
+// most that a rounding then takes or adds (2^-25 with the maximum as the base: one heavy
+// entry in front of 3000 that are 18 nats lighter left nothing of them, or added half as much
+// again).  kTop leaves a factor of 2 below the end of fp16 for what ex2 errs.  From 2^26 on,
+// where floats are 8 apart, the maximum itself is the base.
+constexpr float kLift = 7.0f, kTop = 15.0f;
+__device__ __forceinline__ float base_of(float most) {
+  return fabsf(most) < 67108864.0f ? most - kLift : most;
+}
 
 // One row computed again in fp32 by a whole warp, from the entries that it sees
 // alone: taken where a value that the row does not see is an infinity or a NaN,
@@ -102,7 +105,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int s, int h, int t
   else
     *y = pack_f16(v[0], v[1]);
   if (lane == 0 && a.lse != nullptr)
-    a.lse[static_cast<long long>(t) * a.n_q + head] = (m - kLift + log2f(l)) * kLn2;
+    a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
   if (__any_sync(0xFFFFFFFFu, odd) && l == l && last < len - 1) {
     __syncwarp();
     slow_row<HD>(a, s, h, t, head, last, lane);

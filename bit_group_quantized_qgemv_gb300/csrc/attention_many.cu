@@ -19,11 +19,10 @@
 // products.  Tensor memory: S/P of A and B (128 columns each), O of A and B
 // (HD each).
 //
-// The running maximum is lazy: the weights are taken relative to an older
-// maximum until the new one exceeds it by 2^kSlack, so O is rescaled (a round
-// trip through tensor memory) a few times per row instead of at every tile.
-// Weights, lifted by kLift, are then at most 2^15, inside fp16, and rounded to 11 bits
-// down to 2^-21 of the maximum.
+// The base that weights are relative to is lazy: an older maximum less kLift, until a
+// weight would pass 2^kTop, so O is rescaled (a round trip through tensor memory) a few
+// times per row instead of at every tile.  Weights are then rounded to 11 bits down
+// to 2^-21 of the maximum.
 //
 // 2048 tokens over 30759 entries (32/8 heads of 128) take 660 us in a few replays of a
 // graph, 1.51 PFLOP/s or 79 % of a library product; in calls one after the other, where the
@@ -399,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 128; k += 2)
           mx[(k / 2) & 3] = max3(mx[(k / 2) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-        // a row that grows past the slack (or from nothing) is rescaled
-        if (__any_sync(0xFFFFFFFFu, mt > m + kSlack)) {
-          const float mn = fmaxf(m, mt);
+        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // a row that grows past the top (or from nothing, -inf) is rescaled
+        if (__any_sync(0xFFFFFFFFu, fmaf(most, a.scale_log2, -m) > kTop)) {
+          const float mn = fmaxf(m, base_of(most * a.scale_log2));
           const float f = mn == m ? 1.f : ex2(m - mn);
           m = mn;
           l *= f;
@@ -418,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float b = m == -INFINITY ? 0.f : m - kLift;
+        const float b = m == -INFINITY ? 0.f : m;
         uint64_t sum[2] = {0, 0};
         const uint64_t scale = pair(a.scale_log2, a.scale_log2), less = pair(-b, -b);
 #pragma unroll
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (live && a.lse != nullptr)
-          a.lse[static_cast<long long>(t) * a.n_q + head] = (m - kLift + log2f(l)) * kLn2;
+          a.lse[static_cast<long long>(t) * a.n_q + head] = (m + log2f(l)) * kLn2;
         // rows that hide entries and came out infinite or NaN: again, without them
         unsigned again = __ballot_sync(0xFFFFFFFFu, live && odd && l == l && lim < g.len - 1);
         while (again != 0) {

@@ -253,18 +253,19 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(HD, 8 * NT, kWarps))
           const int j = e0 + g + 8 * (e >> 1);
           const bool seen = !hidden && j <= lim[nt][e & 1];
           x[e] = seen ? (sc[nt][0][e] + sc[nt][1][e]) * a.scale_log2 : -INFINITY;
-          over |= x[e] > m[nt][e & 1] + kSlack;
+          over |= x[e] - m[nt][e & 1] > kTop;  // (from no base at all, -inf, on: infinite)
         }
-        // The maximum is lazy: it moves (and O is rescaled) only where a score
-        // exceeds it by more than the slack, so most tiles cost one vote.
+        // The base is lazy: it moves (and O is rescaled) only where a weight would
+        // pass the top, so most tiles cost one vote.
         if (__any_sync(0xFFFFFFFFu, over)) {
           float mn[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mn[e] = fmaxf(m[nt][e], fmaxf(x[e], x[e + 2]));
+            mn[e] = fmaxf(x[e], x[e + 2]);
             mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 4));
             mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 8));
             mn[e] = fmaxf(mn[e], __shfl_xor_sync(0xFFFFFFFFu, mn[e], 16));
+            mn[e] = fmaxf(m[nt][e], base_of(mn[e]));
           }
           const float f0 = mn[0] == m[nt][0] ? 1.f : ex2(m[nt][0] - mn[0]);
           const float f1 = mn[1] == m[nt][1] ? 1.f : ex2(m[nt][1] - mn[1]);
@@ -280,8 +281,8 @@ __global__ void __launch_bounds__(32 * kWarps, few_resident(HD, 8 * NT, kWarps))
           m[nt][0] = mn[0];
           m[nt][1] = mn[1];
         }
-        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kLift;
-        const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kLift;
+        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // entry g, then g + 8
           const float u = ex2(x[2 * e] - b0), v = ex2(x[2 * e + 1] - b1);

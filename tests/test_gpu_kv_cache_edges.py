@@ -273,3 +273,31 @@ def test_calls_on_two_streams_at_once():
     for i, res in got[0] + got[1]:
         assert all(torch.equal(a, b) for a, b in zip(res, want[i]))
     assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("rows", [(1, 1), (6, 4), (75, 4)])
+@pytest.mark.parametrize("size", [256, 2048, 4096, 5120, 7168])
+def test_large_scores_that_grow(rows, size):
+    """Scores of up to 5 10^7 whose maximum grows a little from tile to tile, at which floats
+    lie up to 4 apart: whatever the weights then are, they add up to 1 (two roundings to
+    fp16, of a weight and of the output), and no weight leaves fp16's range."""
+    m, n_q = rows
+    hd, page, n = 64, 16, 1500
+    for step in range(1, 14):
+        c = ref.make_cache(m, [(m, n)], 1, hd, page)
+        c.v[torch.isfinite(c.v)] = 1.0
+        for e in range(0, n, page):
+            p, _ = c.entry(0, e)
+            k = min(page, n - e)
+            c.k[p, 0, :k] = 0
+            c.k[p, 0, :k, 0] = size
+            c.k[p, 0, :k, 1] = (e // 128) * step / 2    # (a tile of 128, and the warps' four of 16)
+        x = torch.zeros(m, n_q, hd).half()
+        x[:, :, 0] = size
+        x[:, :, 1] = 1
+        for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+            out, lse = q.paged_attention(handle(c), x.cuda(), c.q_start.cuda(), max_q=m, scale=1.0, want_lse=True,
+                                         workspace=ws)
+            one = torch.ones(m, n_q * hd, dtype=torch.float64)
+            close(out, one, 2.0 ** -10 * one, f"step {step}")
+            assert bool(torch.isfinite(lse).all())
