@@ -57,6 +57,12 @@ _SIGS = {
     "qgemv_paged_attention_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I]),
     "qgemv_attention_mass": (_I, [_P, _P, _L, _I, _I, _P, _I, _F, _P, _P, _P, _P, _P]),
     "qgemv_cache_evict": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "qgemv_mx_quantize": (_I, [_I, _P, _I, _I, _P, _P, _P]),
+    "qgemv_mx_dequantize": (_I, [_I, _P, _P, _I, _I, _P, _P]),
+    "qgemv_residual_rmsnorm_mxfp8": (_I, [_P, _P, _P, _F, _I, _I, _P, _P, _P, _P]),
+    "qgemv_mxfp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "qgemv_mx_gemm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "qgemv_mx_swiglu": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
 }
 
 
@@ -737,6 +743,209 @@ def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, ke
     if rc:
         _check(rc, "qgemv_cache_evict")
     return kept, mass_out, pos_out, kv_len_out
+
+
+# ------------------------------------------------- microscaled (MX) operators
+
+_U8 = torch.uint8
+_E4M3 = torch.float8_e4m3fn
+
+
+def _mx_elsewhere(call, t, stream, *args):
+    """A call for another stream or device than the current ones: again with them
+    current, so that what it allocates belongs to the stream it runs on."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        with torch.cuda.device(t.get_device()):
+            return call(*args)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
+def _mx_at(index, t, dtypes, name, shape=None):
+    """Address of a contiguous tensor on GPU `index`, of the given shape; None for None."""
+    if t is None:
+        return None
+    if (t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous() or
+            (shape is not None and t.shape != shape)):
+        _cuda(t, dtypes, name)
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+_CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
+
+
+def _mx_rows(shape, name):
+    """(rows, columns, leading sizes) of a tensor whose last axis is k."""
+    if len(shape) == 0:
+        raise ValueError(f"{name} must have at least one axis")
+    return shape[:-1].numel(), shape[-1], shape[:-1]
+
+
+def _mx_weight(index, w, name):
+    """(codes address, scales address, rows, k) of an MXFP4 weight (codes, scales)."""
+    codes, scales = w
+    if codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be [rows][k / 8]")
+    n, words = codes.shape
+    return (_mx_at(index, codes, _CODES4, name + ".codes"),
+            _mx_at(index, scales, _BYTES, name + ".scales", (n, words // 4)), n, words * 8)
+
+
+def _mx_activations(index, x, k):
+    """(codes address, scales address, rows, leading sizes) of MXFP8 rows (codes, scales)."""
+    codes, scales = x
+    m, k8, lead = _mx_rows(codes.shape, "x.codes")
+    if k8 != k:
+        raise ValueError(f"x.codes has rows of {k8}, the weight of {k}")
+    return (_mx_at(index, codes, _CODES8, "x.codes"),
+            _mx_at(index, scales, _BYTES, "x.scales", (*lead, k // 32)), m, lead)
+
+
+def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
+    """qgemv_mx_quantize: fp16 rows [..., k] in microscaled form, blocks of 32 along
+    k (k a multiple of 32).  bits 4: MXFP4, codes int32 [..., k / 8]; bits 8: MXFP8,
+    codes uint8 [..., k] (e4m3; a float8_e4m3fn tensor may be given).  Returns
+    (codes, scales uint8 [..., k / 32])."""
+    index = x.get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(mx_quantize, x, stream, x, bits, codes, scales)
+    m, k, lead = _mx_rows(x.shape, "x")
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, not {bits}")
+    shape, kind = ((*lead, k // 8), torch.int32) if bits == 4 else (x.shape, _U8)
+    if codes is None:
+        codes = torch.empty(shape, dtype=kind, device=x.device)
+    if scales is None:
+        scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
+    rc = lib.qgemv_mx_quantize(bits, _mx_at(index, x, _F16, "x"), m, k,
+                               _mx_at(index, codes, _CODES4 if bits == 4 else _CODES8, "codes", shape),
+                               _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)),
+                               _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, out=None, stream=None):
+    """qgemv_mx_dequantize: the fp16 values [..., k] of MXFP4 (int32 codes) or MXFP8
+    (uint8 or float8_e4m3fn codes) rows."""
+    index = codes.get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(mx_dequantize, codes, stream, codes, scales, out)
+    m, k, lead = _mx_rows(codes.shape, "codes")
+    bits = 4 if codes.dtype in _CODES4 else 8
+    if bits == 4:
+        k *= 8
+    if out is None:
+        out = torch.empty((*lead, k), dtype=_HALF, device=codes.device)
+    rc = lib.qgemv_mx_dequantize(bits, _mx_at(index, codes, _CODES4 if bits == 4 else _CODES8, "codes"),
+                                 _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)), m, k,
+                                 _mx_at(index, out, _F16, "out", (*lead, k)), _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_mx_dequantize")
+    return out
+
+
+def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None, scales=None,
+                           stream=None):
+    """qgemv_residual_rmsnorm_mxfp8: h = x + residual (fp16 rows [..., k]; x itself
+    when residual is None), RMSNorm(h) * gamma as MXFP8.  h may be x or residual.
+    Returns (h, codes uint8 [..., k], scales uint8 [..., k / 32])."""
+    index = x.get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(residual_rmsnorm_mxfp8, x, stream, x, gamma, residual, eps, h, codes,
+                             scales)
+    m, k, lead = _mx_rows(x.shape, "x")
+    if residual is not None and h is None:
+        h = torch.empty_like(x)
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=_U8, device=x.device)
+    if scales is None:
+        scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
+    rc = lib.qgemv_residual_rmsnorm_mxfp8(
+        _mx_at(index, x, _F16, "x"), _mx_at(index, residual, _F16, "residual", x.shape),
+        _mx_at(index, gamma, _F16, "gamma", (k,)), eps, m, k,
+        None if residual is None else _mx_at(index, h, _F16, "h", x.shape),
+        _mx_at(index, codes, _CODES8, "codes", x.shape),
+        _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)), _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_residual_rmsnorm_mxfp8")
+    return (x if residual is None else h), codes, scales
+
+
+def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
+    """y = W x (+ residual) for an MXFP4 weight w = (codes int32 [n][k / 8], scales
+    uint8 [n][k / 32]) and one to eight fp16 rows x ([k] or [m][k])."""
+    index = x.get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(qgemv_mxfp4, x, stream, w, x, y, residual)
+    codes, scales, n, k = _mx_weight(index, w, "w")
+    m, kx, lead = _mx_rows(x.shape, "x")
+    if kx != k:
+        raise ValueError(f"x has rows of {kx}, the weight of {k}")
+    if y is None:
+        y = torch.empty((*lead, n), dtype=_HALF, device=x.device)
+    rc = lib.qgemv_mxfp4(codes, scales, _mx_at(index, x, _F16, "x"),
+                         _mx_at(index, y, _F16, "y", (*lead, n)), m, n, k,
+                         _mx_at(index, residual, _F16, "residual", (*lead, n)), _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_mxfp4")
+    return y
+
+
+def mx_gemm(w, x, y=None, residual=None, stream=None):
+    """qgemv_mx_gemm: y = W x (+ residual, which may be y) for an MXFP4 weight w =
+    (codes int32 [n][k / 8], scales uint8 [n][k / 32]) and any number of MXFP8 rows
+    x = (codes uint8 [..., k], scales uint8 [..., k / 32]).  Returns y fp16 [..., n]."""
+    index = x[0].get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(mx_gemm, x[0], stream, w, x, y, residual)
+    codes, scales, n, k = _mx_weight(index, w, "w")
+    xc, xs, m, lead = _mx_activations(index, x, k)
+    if y is None:
+        y = torch.empty((*lead, n), dtype=_HALF, device=x[0].device)
+    rc = lib.qgemv_mx_gemm(codes, scales, xc, xs, _mx_at(index, y, _F16, "y", (*lead, n)), m, n, k,
+                           _mx_at(index, residual, _F16, "residual", (*lead, n)),
+                           _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_mx_gemm")
+    return y
+
+
+def mx_swiglu(gate, up, x, h=None, codes=None, scales=None, stream=None):
+    """qgemv_mx_swiglu: silu(Wg x) * (Wu x) for MXFP4 weights gate, up (each (codes,
+    scales), [n][k]) and MXFP8 rows x = (codes, scales).  With h (fp16 [..., n]) alone the
+    result goes there and h is returned; else it leaves as MXFP8, what mx_gemm takes:
+    returns (codes uint8 [..., n], scales uint8 [..., n / 32]) (and fills h where given)."""
+    index = x[0].get_device()
+    if stream is not None or _current_device() != index:
+        return _mx_elsewhere(mx_swiglu, x[0], stream, gate, up, x, h, codes, scales)
+    gc, gs, n, k = _mx_weight(index, gate, "gate")
+    uc, us, n2, k2 = _mx_weight(index, up, "up")
+    if (n2, k2) != (n, k):
+        raise ValueError(f"up is {n2} x {k2}, gate {n} x {k}")
+    xc, xs, m, lead = _mx_activations(index, x, k)
+    held = h is None or codes is not None or scales is not None
+    if held:
+        if codes is None:
+            codes = torch.empty((*lead, n), dtype=_U8, device=x[0].device)
+        if scales is None:
+            scales = torch.empty((*lead, n // 32), dtype=_U8, device=x[0].device)
+    rc = lib.qgemv_mx_swiglu(gc, gs, uc, us, xc, xs, m, n, k,
+                             _mx_at(index, h, _F16, "h", (*lead, n)),
+                             _mx_at(index, codes, _CODES8, "codes", (*lead, n)),
+                             _mx_at(index, scales, _BYTES, "scales", (*lead, n // 32)),
+                             _raw_stream(index))
+    if rc:
+        _check(rc, "qgemv_mx_swiglu")
+    return (codes, scales) if held else h
 
 
 def device_status() -> int:

@@ -12,6 +12,7 @@
 #include "qgemv_args.h"
 #include "epilogue_ops.h"
 #include "kv_cache.h"
+#include "mx.h"
 
 static_assert(QGEMV_SAMPLE_MAX_K == qgemv::kMaxSampleK, "sampler candidate limit");
 static_assert(QGEMV_SAMPLE_MAX_N == qgemv::kMaxSampleN, "sampler logits limit");
@@ -466,7 +467,7 @@ int qgemv_device_status(unsigned* flags) {
   if (qgemv::status_plain(&v) != cudaSuccess || qgemv::status_norm_swiglu(&v) != cudaSuccess ||
       qgemv::status_moe(&v) != cudaSuccess || qgemv::status_generic(&v) != cudaSuccess ||
       qgemv::status_batch(&v) != cudaSuccess || qgemv::status_attention(&v) != cudaSuccess ||
-      qgemv::status_mass(&v) != cudaSuccess)
+      qgemv::status_mass(&v) != cudaSuccess || qgemv::status_mx(&v) != cudaSuccess)
     return QGEMV_EDEVICE;
   *flags = v;
   return QGEMV_OK;

@@ -634,6 +634,82 @@ int qgemv_cache_evict(const qgemv_kv_cache *cache, const float *mass, const int3
                       void *stream);
 
 /*
+ * Microscaled (MX) operators.  A third weight type beside the group-64 and the LUT
+ * weights, with activations of 8 bits for batches and prompts.  Rows of K values (K a
+ * multiple of 32) in blocks of 32 along K, each with one scale byte:
+ *   value = code * 2^(scale - 127); scale 255: every value of the block is NaN
+ *   MXFP4   codes uint32 [rows][K/8], eight 4-bit codes to a word, low bits first
+ *           (the layout of qgemv_w4g64), e2m1: sign, 0 0.5 1 1.5 2 3 4 6
+ *   MXFP8   codes uint8 [rows][K], e4m3: sign, up to 448; 0x7F and 0xFF are NaN
+ *   scales  uint8 [rows][K/32]
+ * Rows lie one behind the other, without gaps.  Checks of all: K >= 32, K % 32 == 0,
+ * rows * K <= 2^38 (EINVAL); codes and fp16 rows that are read or written in whole
+ * blocks (x, h of the norm, gamma, the values of qgemv_mx_dequantize) 16-byte aligned,
+ * y, h of qgemv_mx_swiglu and residual 2-byte (EALIGN), scales any.  M = 0 rows: nothing is enqueued
+ * and the arrays of rows may be NULL.  These kernels read nothing before the kernel
+ * enqueued ahead of them on the stream is complete (weights may come straight out of
+ * qgemv_mx_quantize); at most they fetch weights into L2.
+ */
+
+/*
+ * qgemv_mx_quantize -- fp16 rows x [M][K] as MXFP4 (bits 4) or MXFP8 (bits 8).  With a
+ * the largest magnitude of a block and emax = 2 (8 for MXFP8):
+ *   e = max(floor(log2 a) - emax, -127), scale = e + 127,
+ *   code = x / 2^e rounded to nearest even, magnitudes above 6 (448) as 6 (448).
+ * A block of zeros gets scale 0, one with an infinity or a NaN 255.  One launch.
+ */
+int qgemv_mx_quantize(int bits, const uint16_t *x, int M, int K, void *codes, uint8_t *scales,
+                      void *stream);
+
+/* qgemv_mx_dequantize -- the values of MXFP4 or MXFP8 rows as fp16 y [M][K], rounded to
+ * nearest even (exact within fp16's range and grid; beyond it infinite).  One launch. */
+int qgemv_mx_dequantize(int bits, const void *codes, const uint8_t *scales, int M, int K,
+                        uint16_t *y, void *stream);
+
+/*
+ * qgemv_residual_rmsnorm_mxfp8 -- qgemv_residual_rmsnorm for M rows with its result in
+ * MXFP8, what qgemv_mx_gemm and qgemv_mx_swiglu take:
+ *   h = x + residual, rounded once to fp16 (h = x when residual is NULL, and then h is
+ *       not written and may be NULL),
+ *   h * gamma / sqrt(mean(h^2) + eps), fp32, the mean over the fp16 h, quantised as
+ *       qgemv_mx_quantize does.
+ * x, residual, h fp16 [M][K], gamma fp16 [K]; h may be x or residual.  Checks: eps > 0
+ * and finite.  One launch.
+ */
+int qgemv_residual_rmsnorm_mxfp8(const uint16_t *x, const uint16_t *residual,
+                                 const uint16_t *gamma, float eps, int M, int K, uint16_t *h,
+                                 uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * qgemv_mxfp4 -- y[m][n] = sum_k w[n][k] x[m][k] (+ residual[m][n]) for an MXFP4 weight
+ * and fp16 activations, the decode form: 1 <= M <= QGEMV_MAX_M.  x [M][K], y, residual
+ * (NULL: none; may equal y) [M][N] fp16.  fp32 sums, one rounding.  A row of x with an
+ * infinity or a NaN gives NaN in all of its outputs.  One launch.
+ */
+int qgemv_mxfp4(const uint32_t *codes, const uint8_t *scales, const uint16_t *x, uint16_t *y,
+                int M, int N, int K, const uint16_t *residual, void *stream);
+
+/*
+ * qgemv_mx_gemm -- the same product for any number of rows in MXFP8 (x_codes [M][K],
+ * x_scales [M][K/32]): batches and prompts.  M >= 0.  Other arguments as qgemv_mxfp4.
+ */
+int qgemv_mx_gemm(const uint32_t *codes, const uint8_t *scales, const uint8_t *x_codes,
+                  const uint8_t *x_scales, uint16_t *y, int M, int N, int K,
+                  const uint16_t *residual, void *stream);
+
+/*
+ * qgemv_mx_swiglu -- h = silu(Wg x) * (Wu x), silu(z) = z / (1 + e^-z), for MXFP4
+ * weights Wg, Wu [I][K] (a caller holding one [2I][K] matrix passes base and base + I
+ * rows) and M >= 0 MXFP8 rows.  The result goes to h (fp16 [M][I], rounded once), to
+ * h_codes [M][I] and h_scales [M][I/32] (MXFP8, quantised from the fp32 result as
+ * qgemv_mx_quantize does; I % 32 == 0), or to both; NULL to skip one.  One launch.
+ */
+int qgemv_mx_swiglu(const uint32_t *gate_codes, const uint8_t *gate_scales,
+                    const uint32_t *up_codes, const uint8_t *up_scales, const uint8_t *x_codes,
+                    const uint8_t *x_scales, int M, int I, int K, uint16_t *h, uint8_t *h_codes,
+                    uint8_t *h_scales, void *stream);
+
+/*
  * qgemv_selftest_wait_timeout -- health check of the bounded device waits
  * every kernel uses: enqueues one tiny kernel on `stream` whose thread waits
  * on a shared-memory mbarrier that nothing ever arrives on, with a limit of
