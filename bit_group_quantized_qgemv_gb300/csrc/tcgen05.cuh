@@ -84,6 +84,31 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Block-scaled products of 8-, 6- and 4-bit floats (kind::mxf8f6f4; 4-bit codes lie in
+// shared memory sixteen to 16 bytes, in the first eight of them).  Instruction
+// descriptor: A e2m1, B e4m3, both K-major, ue8m0 scales, one per 32 k, M = 128, N = n.
+__host__ __device__ constexpr uint32_t idesc_mx(int n) {
+  return (5u << 7) | (static_cast<uint32_t>(n / 8) << 17) | (1u << 23) | (1u << 27);
+}
+// `byte`: which of the four scales in the words at sa, sb is that of this product's 32 k.
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int byte,
+                                       uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  const uint32_t id = idesc | (static_cast<uint32_t>(byte) << 29) | (static_cast<uint32_t>(byte) << 4);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+// Scales of 128 rows and four blocks of k, 512 bytes of shared memory (row r: the word at
+// 16 (r % 32) + 4 (r / 32)), to four columns of tensor memory, once for each warp's lanes.
+// In order with the products of the same thread.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+  const uint64_t desc =
+      static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
 // One arrival on the mbarrier once every product issued so far is done.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
