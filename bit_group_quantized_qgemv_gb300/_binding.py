@@ -765,47 +765,52 @@ def _mx_elsewhere(call, t, stream, *args):
         return call(*args)
 
 
-def _mx_at(index, t, dtypes, name, shape=None):
-    """Address of a contiguous tensor on GPU `index`, of the given shape; None for None."""
-    if t is None:
-        return None
-    if (t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous() or
-            (shape is not None and t.shape != shape)):
+def _mx_refuse(index, **tensors):
+    """Raises what is wrong with tensors (name: (tensor, dtypes, shape)) that the calls
+    below found unfit with cheaper looks; nothing where only k is (the library's to refuse)."""
+    for name, (t, dtypes, shape) in tensors.items():
+        if t is None:
+            continue
         _cuda(t, dtypes, name)
         if t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 _CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
 
 
-def _mx_rows(shape, name):
-    """(rows, columns, leading sizes) of a tensor whose last axis is k."""
-    if len(shape) == 0:
-        raise ValueError(f"{name} must have at least one axis")
-    return shape[:-1].numel(), shape[-1], shape[:-1]
+# The looks that every call takes at a tensor: its type, device, layout, number of values
+# and last axis.  Written out where they are few: on the host, where small calls spend
+# their time, a function's call costs as much as two of them.
+def _mx_fit(t, dtypes, index, count, last):
+    return (t.dtype in dtypes and t.get_device() == index and t.is_contiguous() and
+            t.numel() == count and t.size(-1) == last)
 
 
 def _mx_weight(index, w, name):
-    """(codes address, scales address, rows, k) of an MXFP4 weight (codes, scales)."""
+    """(codes, scales, rows, k) of an MXFP4 weight (codes, scales)."""
     codes, scales = w
-    if codes.dim() != 2:
-        raise ValueError(f"{name}.codes must be [rows][k / 8]")
     n, words = codes.shape
-    return (_mx_at(index, codes, _CODES4, name + ".codes"),
-            _mx_at(index, scales, _BYTES, name + ".scales", (n, words // 4)), n, words * 8)
+    if not (codes.dtype in _CODES4 and codes.get_device() == index and codes.is_contiguous() and
+            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
+            scales.numel() == n * (words // 4)):
+        _mx_refuse(index, **{name + ".codes": (codes, _CODES4, codes.shape),
+                             name + ".scales": (scales, _BYTES, (n, words // 4))})
+    return codes.data_ptr(), scales.data_ptr(), n, words * 8
 
 
 def _mx_activations(index, x, k):
-    """(codes address, scales address, rows, leading sizes) of MXFP8 rows (codes, scales)."""
+    """(codes, scales, rows) of MXFP8 rows (codes, scales) for a weight of k columns."""
     codes, scales = x
-    m, k8, lead = _mx_rows(codes.shape, "x.codes")
-    if k8 != k:
-        raise ValueError(f"x.codes has rows of {k8}, the weight of {k}")
-    return (_mx_at(index, codes, _CODES8, "x.codes"),
-            _mx_at(index, scales, _BYTES, "x.scales", (*lead, k // 32)), m, lead)
+    count = codes.numel()
+    if not (codes.dtype in _CODES8 and codes.get_device() == index and codes.is_contiguous() and
+            codes.size(-1) == k and scales.dtype is _U8 and scales.get_device() == index and
+            scales.is_contiguous() and scales.numel() * 32 == count):
+        _mx_refuse(index, **{"x.codes": (codes, _CODES8, (*codes.shape[:-1], k)),
+                             "x.scales": (scales, _BYTES, (*codes.shape[:-1], k // 32))})
+    return codes.data_ptr(), scales.data_ptr(), count // k if k else 0
 
 
 def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
@@ -816,18 +821,22 @@ def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
     index = x.get_device()
     if stream is not None or _current_device() != index:
         return _mx_elsewhere(mx_quantize, x, stream, x, bits, codes, scales)
-    m, k, lead = _mx_rows(x.shape, "x")
-    if bits not in (4, 8):
+    if bits != 8 and bits != 4:
         raise ValueError(f"bits must be 4 or 8, not {bits}")
-    shape, kind = ((*lead, k // 8), torch.int32) if bits == 4 else (x.shape, _U8)
+    count, k = x.numel(), x.size(-1)
+    per, kinds = (1, _CODES8) if bits == 8 else (8, _CODES4)
     if codes is None:
-        codes = torch.empty(shape, dtype=kind, device=x.device)
+        codes = torch.empty((*x.shape[:-1], k // per), dtype=kinds[0], device=x.device)
     if scales is None:
-        scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
-    rc = lib.qgemv_mx_quantize(bits, _mx_at(index, x, _F16, "x"), m, k,
-                               _mx_at(index, codes, _CODES4 if bits == 4 else _CODES8, "codes", shape),
-                               _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)),
-                               _raw_stream(index))
+        scales = torch.empty((*x.shape[:-1], k // 32), dtype=_U8, device=x.device)
+    if not (x.dtype is _HALF and x.is_contiguous() and
+            _mx_fit(codes, kinds, index, count // per, k // per) and
+            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
+            scales.numel() == count // 32):
+        _mx_refuse(index, x=(x, _F16, x.shape), codes=(codes, kinds, (*x.shape[:-1], k // per)),
+                   scales=(scales, _BYTES, (*x.shape[:-1], k // 32)))
+    rc = lib.qgemv_mx_quantize(bits, x.data_ptr(), count // k if count else 0, k, codes.data_ptr(),
+                               scales.data_ptr(), _raw_stream(index))
     if rc:
         _check(rc, "qgemv_mx_quantize")
     return codes, scales
@@ -839,15 +848,24 @@ def mx_dequantize(codes, scales, out=None, stream=None):
     index = codes.get_device()
     if stream is not None or _current_device() != index:
         return _mx_elsewhere(mx_dequantize, codes, stream, codes, scales, out)
-    m, k, lead = _mx_rows(codes.shape, "codes")
-    bits = 4 if codes.dtype in _CODES4 else 8
-    if bits == 4:
+    count, k, kind = codes.numel(), codes.size(-1), codes.dtype
+    bits = 8
+    if kind is not _U8 and kind is not _E4M3:
+        bits = 4
+        count *= 8
         k *= 8
     if out is None:
-        out = torch.empty((*lead, k), dtype=_HALF, device=codes.device)
-    rc = lib.qgemv_mx_dequantize(bits, _mx_at(index, codes, _CODES4 if bits == 4 else _CODES8, "codes"),
-                                 _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)), m, k,
-                                 _mx_at(index, out, _F16, "out", (*lead, k)), _raw_stream(index))
+        out = torch.empty((*codes.shape[:-1], k), dtype=_HALF, device=codes.device)
+    if not ((bits == 8 or kind in _CODES4) and codes.is_contiguous() and
+            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
+            scales.numel() == count // 32 and
+            out.dtype is _HALF and out.get_device() == index and out.is_contiguous() and
+            out.numel() == count and out.size(-1) == k):
+        _mx_refuse(index, codes=(codes, _CODES4 + _CODES8, codes.shape),
+                   scales=(scales, _BYTES, (*codes.shape[:-1], k // 32)),
+                   out=(out, _F16, (*codes.shape[:-1], k)))
+    rc = lib.qgemv_mx_dequantize(bits, codes.data_ptr(), scales.data_ptr(),
+                                 count // k if count else 0, k, out.data_ptr(), _raw_stream(index))
     if rc:
         _check(rc, "qgemv_mx_dequantize")
     return out
@@ -862,22 +880,32 @@ def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None
     if stream is not None or _current_device() != index:
         return _mx_elsewhere(residual_rmsnorm_mxfp8, x, stream, x, gamma, residual, eps, h, codes,
                              scales)
-    m, k, lead = _mx_rows(x.shape, "x")
-    if residual is not None and h is None:
-        h = torch.empty_like(x)
+    count, k = x.numel(), x.size(-1)
     if codes is None:
         codes = torch.empty(x.shape, dtype=_U8, device=x.device)
     if scales is None:
-        scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
-    rc = lib.qgemv_residual_rmsnorm_mxfp8(
-        _mx_at(index, x, _F16, "x"), _mx_at(index, residual, _F16, "residual", x.shape),
-        _mx_at(index, gamma, _F16, "gamma", (k,)), eps, m, k,
-        None if residual is None else _mx_at(index, h, _F16, "h", x.shape),
-        _mx_at(index, codes, _CODES8, "codes", x.shape),
-        _mx_at(index, scales, _BYTES, "scales", (*lead, k // 32)), _raw_stream(index))
+        scales = torch.empty((*x.shape[:-1], k // 32), dtype=_U8, device=x.device)
+    if residual is None:
+        h, r_at, h_at, fit = x, None, None, True
+    else:
+        if h is None:
+            h = torch.empty_like(x)
+        fit = _mx_fit(residual, _F16, index, count, k) and _mx_fit(h, _F16, index, count, k)
+        r_at, h_at = residual.data_ptr(), h.data_ptr()
+    if not (fit and x.dtype is _HALF and x.is_contiguous() and
+            gamma.dtype is _HALF and gamma.get_device() == index and gamma.is_contiguous() and
+            gamma.numel() == k and _mx_fit(codes, _CODES8, index, count, k) and
+            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
+            scales.numel() == count // 32):
+        _mx_refuse(index, x=(x, _F16, x.shape), gamma=(gamma, _F16, (k,)),
+                   residual=(residual, _F16, x.shape), h=(h, _F16, x.shape),
+                   codes=(codes, _CODES8, x.shape), scales=(scales, _BYTES, (*x.shape[:-1], k // 32)))
+    rc = lib.qgemv_residual_rmsnorm_mxfp8(x.data_ptr(), r_at, gamma.data_ptr(), eps,
+                                          count // k if count else 0, k, h_at, codes.data_ptr(),
+                                          scales.data_ptr(), _raw_stream(index))
     if rc:
         _check(rc, "qgemv_residual_rmsnorm_mxfp8")
-    return (x if residual is None else h), codes, scales
+    return h, codes, scales
 
 
 def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
@@ -887,14 +915,17 @@ def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
     if stream is not None or _current_device() != index:
         return _mx_elsewhere(qgemv_mxfp4, x, stream, w, x, y, residual)
     codes, scales, n, k = _mx_weight(index, w, "w")
-    m, kx, lead = _mx_rows(x.shape, "x")
-    if kx != k:
-        raise ValueError(f"x has rows of {kx}, the weight of {k}")
+    m = x.numel() // k if k else 0
     if y is None:
-        y = torch.empty((*lead, n), dtype=_HALF, device=x.device)
-    rc = lib.qgemv_mxfp4(codes, scales, _mx_at(index, x, _F16, "x"),
-                         _mx_at(index, y, _F16, "y", (*lead, n)), m, n, k,
-                         _mx_at(index, residual, _F16, "residual", (*lead, n)), _raw_stream(index))
+        y = torch.empty((*x.shape[:-1], n), dtype=_HALF, device=x.device)
+    if not (x.dtype is _HALF and x.is_contiguous() and x.size(-1) == k and
+            y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
+            y.numel() == m * n and y.size(-1) == n and
+            (residual is None or _mx_fit(residual, _F16, index, m * n, n))):
+        _mx_refuse(index, x=(x, _F16, (*x.shape[:-1], k)), y=(y, _F16, (*x.shape[:-1], n)),
+                   residual=(residual, _F16, (*x.shape[:-1], n)))
+    rc = lib.qgemv_mxfp4(codes, scales, x.data_ptr(), y.data_ptr(), m, n, k,
+                         None if residual is None else residual.data_ptr(), _raw_stream(index))
     if rc:
         _check(rc, "qgemv_mxfp4")
     return y
@@ -908,12 +939,16 @@ def mx_gemm(w, x, y=None, residual=None, stream=None):
     if stream is not None or _current_device() != index:
         return _mx_elsewhere(mx_gemm, x[0], stream, w, x, y, residual)
     codes, scales, n, k = _mx_weight(index, w, "w")
-    xc, xs, m, lead = _mx_activations(index, x, k)
+    xc, xs, m = _mx_activations(index, x, k)
     if y is None:
-        y = torch.empty((*lead, n), dtype=_HALF, device=x[0].device)
-    rc = lib.qgemv_mx_gemm(codes, scales, xc, xs, _mx_at(index, y, _F16, "y", (*lead, n)), m, n, k,
-                           _mx_at(index, residual, _F16, "residual", (*lead, n)),
-                           _raw_stream(index))
+        y = torch.empty((*x[0].shape[:-1], n), dtype=_HALF, device=x[0].device)
+    if not (y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
+            y.numel() == m * n and y.size(-1) == n and
+            (residual is None or _mx_fit(residual, _F16, index, m * n, n))):
+        shape = (*x[0].shape[:-1], n)
+        _mx_refuse(index, y=(y, _F16, shape), residual=(residual, _F16, shape))
+    rc = lib.qgemv_mx_gemm(codes, scales, xc, xs, y.data_ptr(), m, n, k,
+                           None if residual is None else residual.data_ptr(), _raw_stream(index))
     if rc:
         _check(rc, "qgemv_mx_gemm")
     return y
@@ -929,20 +964,30 @@ def mx_swiglu(gate, up, x, h=None, codes=None, scales=None, stream=None):
         return _mx_elsewhere(mx_swiglu, x[0], stream, gate, up, x, h, codes, scales)
     gc, gs, n, k = _mx_weight(index, gate, "gate")
     uc, us, n2, k2 = _mx_weight(index, up, "up")
-    if (n2, k2) != (n, k):
+    if n2 != n or k2 != k:
         raise ValueError(f"up is {n2} x {k2}, gate {n} x {k}")
-    xc, xs, m, lead = _mx_activations(index, x, k)
+    xc, xs, m = _mx_activations(index, x, k)
     held = h is None or codes is not None or scales is not None
+    c_at = s_at = h_at = None
+    fit = True
     if held:
         if codes is None:
-            codes = torch.empty((*lead, n), dtype=_U8, device=x[0].device)
+            codes = torch.empty((*x[0].shape[:-1], n), dtype=_U8, device=x[0].device)
         if scales is None:
-            scales = torch.empty((*lead, n // 32), dtype=_U8, device=x[0].device)
-    rc = lib.qgemv_mx_swiglu(gc, gs, uc, us, xc, xs, m, n, k,
-                             _mx_at(index, h, _F16, "h", (*lead, n)),
-                             _mx_at(index, codes, _CODES8, "codes", (*lead, n)),
-                             _mx_at(index, scales, _BYTES, "scales", (*lead, n // 32)),
-                             _raw_stream(index))
+            scales = torch.empty((*x[0].shape[:-1], n // 32), dtype=_U8, device=x[0].device)
+        fit = (codes.dtype in _CODES8 and codes.get_device() == index and codes.is_contiguous() and
+               codes.numel() == m * n and codes.size(-1) == n and
+               scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
+               scales.numel() == m * (n // 32))
+        c_at, s_at = codes.data_ptr(), scales.data_ptr()
+    if h is not None:
+        fit = fit and _mx_fit(h, _F16, index, m * n, n)
+        h_at = h.data_ptr()
+    if not fit:
+        lead = x[0].shape[:-1]
+        _mx_refuse(index, h=(h, _F16, (*lead, n)), codes=(codes, _CODES8, (*lead, n)),
+                   scales=(scales, _BYTES, (*lead, n // 32)))
+    rc = lib.qgemv_mx_swiglu(gc, gs, uc, us, xc, xs, m, n, k, h_at, c_at, s_at, _raw_stream(index))
     if rc:
         _check(rc, "qgemv_mx_swiglu")
     return (codes, scales) if held else h

@@ -92,7 +92,7 @@ int qgemv_residual_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual,
 int qgemv_mxfp4(const uint32_t* codes, const uint8_t* scales, const uint16_t* x, uint16_t* y,
                 int M, int N, int K, const uint16_t* residual, void* stream) {
   if (!codes || !scales || !x || !y) return QGEMV_ENULL;
-  if (M < 1 || M > QGEMV_MAX_M || N < 1 || !valid_rows(M, K) || !valid_rows(N, K)) return QGEMV_EINVAL;
+  if (M < 1 || M > QGEMV_MAX_M || K > QGEMV_MXFP4_MAX_K || N < 1 || !valid_rows(M, K) || !valid_rows(N, K)) return QGEMV_EINVAL;
   if (!aligned(codes, 16) || !aligned(x, 16) || !aligned(y, 2) || !aligned(residual, 2))
     return QGEMV_EALIGN;
   qgemv::MxProductArgs a{};

@@ -11,17 +11,23 @@
 // Each q takes four bits of what is left, so the eleven bits of an fp16 value are
 // all held, down to 2^-26 of the block's largest value; the three sums are added in fp32.
 //
-// A step is 128 k: a ring of stages (codes of A and B, 128-byte swizzled, and their
-// scales) between
-//   warp 9     TMA: codes of A (where K and the address allow it) and of MXFP8 rows;
-//   warps 4-7  scales, fp16 rows and what TMA cannot load, by cp.async, kLag steps ahead of
-//              the arrival that hands them on;
-//   warp 8     scales to tensor memory, four products (gated: eight) a step;
-//   warps 0-3  results: a weight row per lane, a column at a time; two accumulators,
-//              so that the next tile's products run meanwhile.
+// A step is 128 k: a ring of stages (codes of A and, for MXFP8 rows, of B, 128-byte
+// swizzled, and their scales) between
+//   two warps   TMA, every other step each (one wait and issue takes some 250 clocks,
+//               however large the box): codes of A (where K and the address allow it) and
+//               of MXFP8 rows;
+//   four warps  scales, four steps each: a row's bytes of them in one load where they are
+//               aligned; codes that TMA cannot load, by cp.async;
+//   two warps   scales to tensor memory and four products a step: one for each weight,
+//               or every other step into an accumulator of its own (a warp takes 550
+//               clocks a step to wait for it and issue its products, few columns only 160
+//               of the tensor core); with over 112 columns one does all;
+//   eight       results, a weight row per lane; two accumulators, so that the next tile's
+//               products run meanwhile.  Before the first result they turn the block's
+//               share of fp16 rows into columns, which stay in shared memory for the call.
 // Thread blocks stay for the whole call and take tiles one after the other.  Where
-// there are few tiles, the blocks of a cluster share K: each leaves its sums in its
-// shared memory and finishes every split-th column, adding the others' in rank order.
+// there are few tiles, the blocks of a cluster share K: each finishes every split-th
+// column, adding the others' sums, sent to its shared memory, in rank order.
 #include <atomic>
 
 #include "kv_cache.cuh"
@@ -38,10 +44,10 @@ __device__ unsigned g_status = 0;
 
 constexpr int kRowsW = 128;   // weight rows of a tile
 constexpr int kStepK = 128;   // k of a stage
-constexpr int kThreads = 320;
-constexpr int kLoadWarp = 4, kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kLag = 3;       // steps between a load's start and the wait for it
+constexpr int kLoaders = 4;   // warps
+constexpr int kTmaWarps = 2;
 constexpr int kMinStages = 4, kMaxStages = 16;
+constexpr int kMaxRowSteps = 64;  // steps of fp16 rows that a block holds, at most
 constexpr int kScaleCols = 16;                    // tensor memory of one step's scales
 constexpr int kAccCols = 512 - 2 * kScaleCols;    // and of the accumulators
 constexpr int kSplitTokens = 64;                  // most columns whose sums blocks share
@@ -53,13 +59,17 @@ struct MxPlan {
   int split;     // blocks that share K (a cluster)
   int stages;
   int row_tiles, tok_tiles;
+  int row_steps;     // steps of fp16 rows that a block holds
+  bool pair;         // every other step's products into a second accumulator
   bool rows_first;   // tiles of rows change fastest
   bool tma_w;        // weights by TMA
-  bool words_w, words_u, words_x;  // scales by aligned words
+  int bytes;         // of a row's scales in one load: 16, 4 or 1
 };
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t rows[kMaxRowSteps];  // columns of fp16 rows
+  uint64_t turn[kLoaders];      // a loader may go on to its group
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_done;
 };
@@ -77,23 +87,38 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ float load_remote(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// A value to another block's shared memory, its bytes counted on a barrier there.
+__device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool take) {
-  const int n = take ? BYTES : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
-               : "memory");
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// An arrival on the mbarrier once this thread's copies so far are done; the barrier's
+// count has it already.
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Eight bytes, or zeros.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 8 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
 // Four scale bytes of a row, from block kb on; what lies behind the row's end is 0.
@@ -108,6 +133,59 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int b
 // Place of row r's word among the scales of a step.
 __device__ __forceinline__ int scale_at(int r) { return (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4; }
 
+__device__ __forceinline__ void store_shared(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Warps by what they do.
+constexpr int kOutWarps = 8, kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders,
+              kTmaWarp = kMmaWarp + 2, kThreads = 32 * (kTmaWarp + kTmaWarps);
+
+// Eight values of a row of x (a lane; four lanes hold a block) to three columns: codes
+// to col, col + 128, col + 256 (swizzled as the columns' number wants), scales.
+__device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, uint32_t scales, int m,
+                                             int ch) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  float f[8];
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    f[2 * i] = h.x, f[2 * i + 1] = h.y;
+    most = max(most, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
+  }
+  most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+  most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+  // 2^e1 with e1 + 127 = byte; the largest value is then below 2^8
+  const int e = static_cast<int>(most >> 23), byte = max(e, 103) - 7;
+  const float inv = mx_inverse(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= inv;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const float next = q == 0 ? 16.f : 32.f;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t two = mx_codes8(f[2 * i], f[2 * i + 1]);
+      const float2 got = mx_values8(two);
+      f[2 * i] = (f[2 * i] - got.x) * next;
+      f[2 * i + 1] = (f[2 * i + 1] - got.y) * next;
+      w[i >> 1] = i & 1 ? w[i >> 1] | (two << 16) : two;
+    }
+    const int c = 3 * m + q;
+    const int sb = e == 255 ? 255 : byte - (q == 0 ? 0 : q == 1 ? 4 : 9);
+    if (live) {
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(cols + c * 128 + (((ch >> 1) ^ (c & 7)) << 4) +
+                                                           (ch & 1) * 8),
+                   "r"(w[0]), "r"(w[1])
+                   : "memory");
+      if ((ch & 3) == 0)
+        asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + scale_at(c) + (ch >> 2)), "r"(sb) : "memory");
+    }
+  }
+}
+
 // GATED: two weights.  SPLIT3: fp16 rows.
 template <bool GATED, bool SPLIT3>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -118,44 +196,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
   __shared__ int s_failed;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  // (uniform: what the products' operands and loops depend on, see tc::elect_one)
+  const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? tc::uniform(static_cast<int>(cluster_rank())) : 0;
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
   const int b_bytes = p.cols * kStepK;
-  const uint32_t a_ring = base, b_ring = a_ring + p.stages * kW * 16384;
-  const uint32_t s_ring = b_ring + p.stages * b_bytes;            // scales: A, (up,) B
-  const int s_bytes = 512 * (kW + (p.cols > 128 ? 2 : 1));
-  const uint32_t x_ring = s_ring + p.stages * s_bytes;            // fp16 rows as they are
-  const uint32_t part = x_ring + (SPLIT3 ? p.stages * p.tokens * 256 : 0);
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_u32(&bars.full[i]), 4 + (p.tma_w || !SPLIT3 ? 1 : 0));
-      mbar_init(smem_u32(&bars.empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.acc_full[i]), 1);
-      mbar_init(smem_u32(&bars.acc_empty[i]), 4);
-    }
-    mbar_init(smem_u32(&bars.part_full), 4 * p.split);
-    mbar_init(smem_u32(&bars.part_done), 4 * p.split);
-    fence_mbar_init();
-    s_failed = 0;
-  }
-  if constexpr (SPLIT3) {
-    // columns that no row of x writes
-    for (uint32_t i = threadIdx.x; i < static_cast<uint32_t>(p.stages * (b_bytes + s_bytes)) / 16; i += kThreads)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(b_ring + 16 * i), "r"(0) : "memory");
-    tc::fence_async_shared();
-  }
-  pdl_wait();
-  if (warp == kMmaWarp) tc::alloc(smem_u32(&s_tmem), 512);
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  pdl_launch_dependents();
-  if (p.split > 1) cluster_sync();  // barriers are there before a rank arrives on another's
-  const uint32_t tmem = s_tmem;
+  const int c_bytes = kW * 16384 + (SPLIT3 ? 0 : b_bytes);        // a stage: A (, up) (, B)
+  const int s_bytes = 512 * (kW + (SPLIT3 ? 0 : p.cols > 128 ? 2 : 1));  // and their scales
+  const uint32_t x_cols = base + p.stages * c_bytes;              // columns of fp16 rows
+  const uint32_t s_ring = x_cols + (SPLIT3 ? p.row_steps * b_bytes : 0);
+  const uint32_t x_scales = s_ring + p.stages * s_bytes;
+  const uint32_t part = x_scales + (SPLIT3 ? p.row_steps * 512 : 0);
 
   const int steps = (a.K + kStepK - 1) / kStepK;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * rank / p.split);
@@ -169,275 +220,353 @@ __global__ void __launch_bounds__(kThreads, 1)
     *tok = (p.rows_first ? o : i) * p.tokens;
   };
 
-  if (warp == kTmaWarp) {
-    // ------------------------------------------------------------------ TMA
-    if (p.tma_w || !SPLIT3) {
-      int stage = 0, use = 0;
-      const uint32_t bytes = (p.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
-      for (long long t = first; t < tiles; t += stride) {
-        int row, tok;
-        place(t, &row, &tok);
-        for (int k = k0; k < k1; ++k) {
-          if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
-          if (lane == 0) {
-            const uint32_t full = smem_u32(&bars.full[stage]);
-            mbar_arrive_expect_tx(full, bytes);
-            if (p.tma_w) {
-              tc::tma_2d(a_ring + stage * kW * 16384, &w_map, k * kStepK, row, full);
-              if (GATED) tc::tma_2d(a_ring + (stage * kW + 1) * 16384, &u_map, k * kStepK, row, full);
-            }
-            if (!SPLIT3) tc::tma_2d(b_ring + stage * b_bytes, &x_map, k * kStepK, tok, full);
-          }
-          __syncwarp();
-          if (++stage == p.stages) stage = 0, ++use;
+  // The first tile's weights on their way to L2 while the kernel before ends.
+  if (first < tiles) {
+    int row, tok;
+    place(first, &row, &tok);
+    if (warp == kTmaWarp && lane == 0) {
+      if (p.tma_w) {
+        for (int k = k0; k < k1 && k < k0 + p.stages; ++k) {
+          tc::prefetch_2d(&w_map, k * kStepK, row);
+          if (GATED) tc::prefetch_2d(&u_map, k * kStepK, row);
         }
       }
-      // no copy may be in flight when the block ends
-      const int turn = use > 0 ? p.stages : stage;
-      for (int i = 0; i < turn; ++i) {
-        if (--stage < 0) stage = p.stages - 1, --use;
-        warp_wait(smem_u32(&bars.full[stage]), use & 1, &g_status);
+    } else if (warp >= kLoadWarp && warp < kMmaWarp) {
+      const int n = row + threadIdx.x - kLoadWarp * 32, blocks = a.K / kMxBlock;
+      const long long at = static_cast<long long>(n) * blocks + 4 * k0;
+      if (n < a.N) {
+        prefetch_l2(a.ws + at);
+        if (GATED) prefetch_l2(a.us + at);
       }
     }
-  } else if (warp == kMmaWarp) {
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1 + (p.tma_w ? 0 : 32) + (p.tma_w || !SPLIT3 ? 1 : 0));
+      mbar_init(smem_u32(&bars.empty[i]), kW);
+    }
+    if constexpr (SPLIT3)
+      for (int i = 0; i < k1 - k0; ++i) mbar_init(smem_u32(&bars.rows[i]), 1);
+    for (int i = 0; i < kLoaders; ++i) mbar_init(smem_u32(&bars.turn[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.acc_full[i]), GATED || p.pair ? 2 : 1);
+      mbar_init(smem_u32(&bars.acc_empty[i]), kOutWarps);
+    }
+    mbar_init(smem_u32(&bars.part_full), 1);
+    mbar_init(smem_u32(&bars.part_done), kOutWarps * p.split);
+    fence_mbar_init();
+    s_failed = 0;
+  }
+  __syncthreads();
+  if (p.split > 1) cluster_arrive();
+  pdl_wait();
+  if (warp == kMmaWarp) tc::alloc(smem_u32(&s_tmem), 512);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_launch_dependents();
+  if (p.split > 1) cluster_wait();  // barriers are there before a rank arrives on another's
+  const uint32_t tmem = s_tmem;
+
+  // The steps of a warp that takes every n-th of all tiles' steps, from the me-th on, and
+  // their stages.
+  struct Steps {
+    long long t;
+    int k, stage, use;
+    bool moved;  // to another tile
+  };
+  auto start = [&](int me) { return Steps{first, k0 + me, me, 0, true}; };
+  auto find = [&](Steps& s) {  // false: there are no more
+    while (s.k >= k1 && s.t < tiles) s.k -= k1 - k0, s.t += stride, s.moved = true;
+    while (s.stage >= p.stages) s.stage -= p.stages, ++s.use;
+    return s.t < tiles;
+  };
+  if (warp >= kTmaWarp) {
+    // ------------------------------------------------------------------ TMA
+    if (p.tma_w || !SPLIT3) {
+      const uint32_t bytes = (p.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
+      Steps s = start(warp - kTmaWarp);
+      int row = 0, tok = 0;
+      for (; find(s); s.k += kTmaWarps, s.stage += kTmaWarps) {
+        if (s.moved) place(s.t, &row, &tok);
+        s.moved = false;
+        if (s.use > 0) step_wait(smem_u32(&bars.empty[s.stage]), (s.use - 1) & 1, &s_failed, &g_status);
+        if (lane == 0) {
+          const uint32_t full = smem_u32(&bars.full[s.stage]);
+          mbar_arrive_expect_tx(full, bytes);
+          const uint32_t to = base + s.stage * c_bytes;
+          if (p.tma_w) {
+            tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
+            if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
+          }
+          if (!SPLIT3) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------- products
+    const int me = warp - kMmaWarp;
+    const bool two = GATED || p.pair;
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
     const uint32_t idesc = tc::idesc_mx(p.cols);
-    int stage = 0, use = 0, n = 0;
-    for (long long t = first; t < tiles; t += stride, ++n) {
+    int stage = 0, use = 0, n = 0, odd = 0;  // odd: of all tiles' steps, the next one's number
+    uint32_t c = base, ss = s_ring;          // of the stage
+    for (long long t = first; t < tiles && (two || me == 0); t += stride, ++n) {
       const int buf = n & 1;
       if (n >= 2) step_wait(smem_u32(&bars.acc_empty[buf]), ((n >> 1) - 1) & 1, &s_failed, &g_status);
       tc::fence_after();
-      const uint32_t acc = tm + buf * (kW * p.cols);
+      const uint32_t acc = tm + (buf * (two ? 2 : 1) + me) * p.cols;
       for (int k = k0; k < k1; ++k) {
-        step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
-        tc::fence_after();
-        if (tc::elect_one()) {
-          const uint32_t st = tm + kAccCols + (k & 1) * kScaleCols;
-          const uint32_t ss = s_ring + stage * s_bytes;
-          tc::copy_scales(st, ss);
-          if (GATED) tc::copy_scales(st + 4, ss + 512);
-          tc::copy_scales(st + 8, ss + kW * 512);
-          if (p.cols > 128) tc::copy_scales(st + 12, ss + (kW + 1) * 512);
-          const uint64_t b = tc::desc_k_major(b_ring + stage * b_bytes);
-#pragma unroll
-          for (int w = 0; w < kW; ++w) {
-            const uint64_t wd = tc::desc_k_major(a_ring + (stage * kW + w) * 16384);
+        if (GATED || !p.pair || odd == me) {
+          if (SPLIT3 && n == 0) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
+          step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
+          if (!p.tma_w) tc::fence_async_shared();  // codes by cp.async, for the tensor core
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint32_t st = tm + kAccCols + (two ? me : k & 1) * kScaleCols;
+            tc::copy_scales(st, ss + (GATED ? me * 512 : 0));
+            tc::copy_scales(st + 8, SPLIT3 ? x_scales + (k - k0) * 512 : ss + kW * 512);
+            if (p.cols > 128) tc::copy_scales(st + 12, ss + (kW + 1) * 512);
+            const uint64_t b = tc::desc_k_major(SPLIT3 ? x_cols + (k - k0) * b_bytes : c + kW * 16384);
+            const uint64_t w = tc::desc_k_major(c + (GATED ? me * 16384 : 0));
+            const int more = k > k0 + (!GATED && p.pair ? 1 : 0);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc::mma_mx(acc + w * p.cols, wd + 2 * j, b + 2 * j, idesc, j, st + 4 * w, st + 8,
-                         k > k0 || j > 0);
+              tc::mma_mx(acc, w + 2 * j, b + 2 * j, idesc, j, st, st + 8, j > 0 || more);
+            tc::commit(smem_u32(&bars.empty[stage]));
           }
-          tc::commit(smem_u32(&bars.empty[stage]));
+          __syncwarp();
         }
-        __syncwarp();
-        if (++stage == p.stages) stage = 0, ++use;
+        odd ^= 1;
+        c += c_bytes, ss += s_bytes;
+        if (++stage == p.stages) stage = 0, ++use, c = base, ss = s_ring;
       }
       if (tc::elect_one()) tc::commit(smem_u32(&bars.acc_full[buf]));
       __syncwarp();
     }
   } else if (warp >= kLoadWarp) {
     // ---------------------------------------------------------------- loads
-    const int th = threadIdx.x - kLoadWarp * 32, blocks = a.K / kMxBlock;
-    int stage = 0, use = 0;      // of the step whose loads start next
-    int late = 0;                // stage of the step that is handed on next
-    int started = 0;             // steps under way, up to kLag
-    // fp16 rows: this thread's eight values of a step (row th / 16 of the tile)
-    auto convert = [&](int s) {
-      const int m = th >> 4, ch = th & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (m < p.tokens)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(x_ring + (s * p.tokens + m) * 256 + ch * 16));
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      float f[8];
-      uint32_t most = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-        f[2 * i] = h.x, f[2 * i + 1] = h.y;
-        most = max(most, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
-      }
-      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      if (m >= p.tokens) return;
-      // 2^e1 with e1 + 127 = byte; the largest value is then below 2^8
-      const int e = static_cast<int>(most >> 23), byte = max(e, 103) - 7;
-      const float inv = mx_inverse(byte);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= inv;
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        const float next = q == 0 ? 16.f : 32.f;
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = mx_codes8(f[2 * i], f[2 * i + 1]);
-          const float2 got = mx_values8(two);
-          f[2 * i] = (f[2 * i] - got.x) * next;
-          f[2 * i + 1] = (f[2 * i + 1] - got.y) * next;
-          w[i >> 1] = i & 1 ? w[i >> 1] | (two << 16) : two;
-        }
-        const int c = 3 * m + q;
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(b_ring + s * b_bytes + c * 128 +
-                                                             (((ch >> 1) ^ (c & 7)) << 4) + (ch & 1) * 8),
-                     "r"(w[0]), "r"(w[1])
-                     : "memory");
-        const int sb = e == 255 ? 255 : byte - (q == 0 ? 0 : q == 1 ? 4 : 9);
-        if ((ch & 3) == 0)
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(s_ring + s * s_bytes + kW * 512 + scale_at(c) + (ch >> 2)),
-                       "r"(sb)
-                       : "memory");
-      }
-    };
-    auto hand_on = [&] {
-      if constexpr (SPLIT3) convert(late);
-      tc::fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars.full[late]));
-      if (++late == p.stages) late = 0;
-    };
-    for (long long t = first; t < tiles; t += stride) {
+    constexpr int kRowsX = SPLIT3 ? 0 : GATED ? 4 : 8;  // rows of x a lane has scales of
+    const int me = warp - kLoadWarp, blocks = a.K / kMxBlock, my_steps = k1 - k0;
+    const int q0 = k0 >> 2, groups = ((k1 - 1) >> 2) - q0 + 1;  // of four steps, of a tile
+    const long long all = first < tiles ? ((tiles - 1 - first) / stride + 1) * groups : 0;
+    for (long long g = me; g < all; g += kLoaders) {
+      const long long turn = g / groups;
+      const int q = q0 + static_cast<int>(g % groups), from = max(k0, 4 * q), to = min(k1, 4 * q + 4);
       int row, tok;
-      place(t, &row, &tok);
-      const int n = row + th, m0 = tok + th, m1 = m0 + 128;
-      const bool has_n = n < a.N;
-      const uint8_t* wsr = a.ws + static_cast<long long>(has_n ? n : 0) * blocks;
-      const uint8_t* usr = GATED ? a.us + static_cast<long long>(has_n ? n : 0) * blocks : nullptr;
-      const bool has_0 = !SPLIT3 && th < p.tokens && m0 < a.M;
-      const bool has_1 = !SPLIT3 && th + 128 < p.tokens && m1 < a.M;
-      const uint8_t* xs0 = has_0 ? a.xs + static_cast<long long>(m0) * blocks : nullptr;
-      const uint8_t* xs1 = has_1 ? a.xs + static_cast<long long>(m1) * blocks : nullptr;
-      for (int k = k0; k < k1; ++k) {
-        // scales whose words are not aligned, before the wait
-        uint32_t sw = 0, su = 0, sx0 = 0, sx1 = 0;
-        if (!p.words_w && has_n) sw = scale_word(wsr, 4 * k, blocks);
-        if (GATED && !p.words_u && has_n) su = scale_word(usr, 4 * k, blocks);
-        if (!p.words_x && has_0) sx0 = scale_word(xs0, 4 * k, blocks);
-        if (!p.words_x && has_1) sx1 = scale_word(xs1, 4 * k, blocks);
-        if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
-        const uint32_t ss = s_ring + stage * s_bytes;
-        auto put = [&](uint32_t at, bool words, bool has, const uint8_t* from, uint32_t w) {
-          if (words)
-            cp_async_small<4>(at, has ? static_cast<const void*>(from + 4 * k) : a.w, has);
-          else
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
-        };
-        put(ss + scale_at(th), p.words_w, has_n, wsr, sw);
-        if (GATED) put(ss + 512 + scale_at(th), p.words_u, has_n, usr, su);
-        if constexpr (SPLIT3) {
-          const int m = th >> 4, at = k * kStepK + (th & 15) * 8;
-          if (m < p.tokens) {
-            const bool has = at < a.K;
-            cp_async16(x_ring + (stage * p.tokens + m) * 256 + (th & 15) * 16,
-                       a.x16 + (has ? static_cast<long long>(m) * a.K + at : 0), has);
-          }
-        } else {
-          if (th < p.tokens) put(ss + kW * 512 + scale_at(th), p.words_x, has_0, xs0, sx0);
-          if (th + 128 < p.tokens) put(ss + kW * 512 + scale_at(th + 128), p.words_x, has_1, xs1, sx1);
+      place(first + turn * stride, &row, &tok);
+      // Scales of rows lane, lane + 32, ... of an operand: of the group's four steps.
+      auto load = [&](const uint8_t* scales, int at, int end, int i) {
+        const int r = at + lane + 32 * i;
+        const uint8_t* s = scales + static_cast<long long>(r) * blocks + 16 * q;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r >= end) return v;
+        if (p.bytes == 16) return *reinterpret_cast<const uint4*>(s);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = 0;
+          if (4 * q + j < from || 4 * q + j >= to) continue;
+          w[j] = p.bytes == 4 ? *reinterpret_cast<const uint32_t*>(s + 4 * j)
+                              : scale_word(s, 4 * j, blocks - 16 * q);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      uint4 vw[4], vu[GATED ? 4 : 1], vx[kRowsX ? kRowsX : 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vw[i] = load(a.ws, row, a.N, i);
+      if constexpr (GATED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vu[i] = load(a.us, row, a.N, i);
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsX; ++i)
+        vx[i] = 32 * i < p.tokens ? load(a.xs, tok, a.M, i) : make_uint4(0, 0, 0, 0);
+      // One group after the other: a wait for a stage tells a use from the one before it,
+      // not from two before.
+      if (g > 0)
+        step_wait(smem_u32(&bars.turn[me]), ((g / kLoaders) - (me == 0 ? 1 : 0)) & 1, &s_failed, &g_status);
+      const long long done = turn * my_steps + (from - k0);  // steps before the group's
+      int stage = static_cast<int>(done % p.stages);
+      long long use = done / p.stages;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 4 * q + j;
+        if (k < from || k >= to) continue;
+        if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
         if (!p.tma_w) {
 #pragma unroll
           for (int w = 0; w < kW; ++w)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int i = th + 128 * j, r = i >> 3, c = i & 7;
+#pragma unroll 4
+            for (int i = lane; i < 8 * kRowsW; i += 32) {
+              const int r = i >> 3, c = i & 7;
               const bool has = row + r < a.N && k * kStepK + c * 16 < a.K;
-              const uint32_t* from = (w ? a.up : a.w) +
+              const uint32_t* src = (w ? a.up : a.w) +
                   (has ? static_cast<long long>(row + r) * (a.K / 8) + k * (kStepK / 8) + c * 2 : 0);
-              cp_async_small<8>(a_ring + (stage * kW + w) * 16384 + r * 128 + ((c ^ (r & 7)) << 4), from, has);
+              cp_async8(base + stage * c_bytes + w * 16384 + r * 128 + ((c ^ (r & 7)) << 4), src, has);
             }
+          arrive_copied(smem_u32(&bars.full[stage]));
         }
-        cp_commit();
-        if (started == kLag) {
-          cp_wait<kLag>();
-          hand_on();
-        } else {
-          ++started;
+        const uint32_t ss = s_ring + stage * s_bytes + lane * 16;
+        auto word = [&](const uint4& v) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
+        store_shared(ss, word(vw[0]), word(vw[1]), word(vw[2]), word(vw[3]));
+        if constexpr (GATED) store_shared(ss + 512, word(vu[0]), word(vu[1]), word(vu[2]), word(vu[3]));
+        if constexpr (kRowsX > 0) {
+          store_shared(ss + kW * 512, word(vx[0]), word(vx[1]), word(vx[2]), word(vx[3]));
+          if constexpr (kRowsX > 4)
+            if (p.cols > 128)
+              store_shared(ss + (kW + 1) * 512, word(vx[4]), word(vx[5]), word(vx[6]), word(vx[7]));
         }
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));
         if (++stage == p.stages) stage = 0, ++use;
       }
+      if (lane == 0) mbar_arrive(smem_u32(&bars.turn[(me + 1) % kLoaders]));
+      __syncwarp();
     }
-    cp_wait<0>();
-    for (; started > 0; --started) hand_on();
+    cp_wait_all();
   } else {
     // -------------------------------------------------------------- results
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
-    // The finished value of weight row n and row m of x.
-    auto finish = [&](int n, int m, float v) {
-      const long long at = static_cast<long long>(m) * a.N + n;
-      if (a.y != nullptr && n < a.N) a.y[at] = __float2half_rn(v);
-      if (GATED && a.yc != nullptr) {
-        // (N is a multiple of 32: a warp's rows are one block of the output, all there or none)
-        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-        const int byte = mx_scale_byte<8>(__uint_as_float(most));
-        if (n < a.N) {
-          a.yc[at] = static_cast<uint8_t>(mx_codes8(v * mx_inverse(byte), 0.f));
-          if (lane == 0) a.ys[at >> 5] = static_cast<uint8_t>(byte);
+    const int quarter = warp & 3, half = warp >> 2;  // lanes of tensor memory; which columns
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
+    if constexpr (SPLIT3) {
+      // the block's share of the fp16 rows, a step a warp, two rows of x at a time
+      for (int i = warp; i < k1 - k0 && first < tiles; i += kOutWarps) {
+        const int ch = lane & 15, at = (k0 + i) * kStepK + ch * 8;
+        uint4 v[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int m = 2 * h + (lane >> 4);
+          v[h] = m < p.tokens && at < a.K
+                     ? *reinterpret_cast<const uint4*>(a.x16 + static_cast<long long>(m) * a.K + at)
+                     : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (2 * h >= p.tokens) break;
+          const int m = 2 * h + (lane >> 4);
+          split_values(v[h], m < p.tokens, x_cols + i * b_bytes, x_scales + i * 512, m, ch);
+        }
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.rows[i]));
       }
+    }
+    // Finished values of weight row n and rows m, m + step, ... of x.
+    auto finish = [&](int n, int m, int step, int count, auto& v) {
+      constexpr int C = sizeof(v) / sizeof(float);
+      __half* y = a.y;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (y != nullptr && c < count && n < a.N)
+          y[static_cast<long long>(m + c * step) * a.N + n] = __float2half_rn(v[c]);
+      if constexpr (GATED) {
+        if (a.yc == nullptr) return;
+        // (N is a multiple of 32: a warp's rows are one block of the output, all there or none)
+        int byte[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          byte[c] = mx_scale_byte<8>(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[c]) & 0x7FFFFFFFu)));
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c < count && n < a.N) {
+            const long long at = static_cast<long long>(m + c * step) * a.N + n;
+            a.yc[at] = static_cast<uint8_t>(mx_codes8(v[c] * mx_inverse(byte[c]), 0.f));
+            if (lane == 0) a.ys[at >> 5] = static_cast<uint8_t>(byte[c]);
+          }
+      }
+    };
+    const int share = (p.tokens + p.split - 1) / p.split;  // rows of x that a rank finishes, at most
+    // Where rank q's sums for this rank's j-th row lie.
+    auto part_at = [&](int q, int j, int w) {
+      return part + (((q * share + j) * kW + w) * kRowsW + quarter * 32 + lane) * 4;
     };
     int n_t = 0;
     for (long long t = first; t < tiles; t += stride, ++n_t) {
       int row, tok;
       place(t, &row, &tok);
-      const int buf = n_t & 1, n = row + warp * 32 + lane, count = min(p.tokens, a.M - tok);
+      const int buf = n_t & 1, n = row + quarter * 32 + lane, count = min(p.tokens, a.M - tok);
+      const bool res = !GATED && a.res != nullptr && n < a.N;
+      auto residual = [&](int m) { return __half2float(a.res[static_cast<long long>(tok + m) * a.N + n]); };
+      const int own = (count - rank + p.split - 1) / p.split;  // rows that this rank finishes
+      if (p.split > 1 && warp == 0 && lane == 0)
+        mbar_arrive_expect_tx(smem_u32(&bars.part_full), max(own, 0) * p.split * kW * kRowsW * 4);
       step_wait(smem_u32(&bars.acc_full[buf]), (n_t >> 1) & 1, &s_failed, &g_status);
       tc::fence_after();
-      const uint32_t acc = lanes + buf * (kW * p.cols);
-      const bool res = !GATED && a.res != nullptr && n < a.N;
+      const uint32_t acc = lanes + buf * (GATED || p.pair ? 2 : 1) * p.cols;
+      // a tile of a single step has one of two accumulators: the step's
+      const bool one = !GATED && p.pair && k1 - k0 == 1;
+      const bool has0 = !one || (n_t & 1) == 0, has1 = !one || (n_t & 1) == 1;
       if (p.split > 1 && n_t > 0) {
         step_wait(smem_u32(&bars.part_done), (n_t - 1) & 1, &s_failed, &g_status);
         fence_cluster();
       }
-      auto out = [&](int m, float g, float u, float r) {  // sums of one column
-        if (p.split > 1) {
-          const uint32_t at = part + ((m * kW) * kRowsW + warp * 32 + lane) * 4;
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(g) : "memory");
-          if (GATED) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + kRowsW * 4), "f"(u) : "memory");
-        } else {
-          finish(n, tok + m, GATED ? silu_f(g) * u : g + r);
-        }
+      auto give = [&](int m, float g, float u) {  // a rank's sums of one column to who finishes it
+        const int q = m % p.split;
+        const uint32_t to = map_rank(part_at(rank, m / p.split, 0), q), bar = map_rank(smem_u32(&bars.part_full), q);
+        send(to, g, bar);
+        if (GATED) send(to + kRowsW * 4, u, bar);
       };
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
       if (ok) {
         if constexpr (SPLIT3) {
-          uint32_t v[32];
-          if (p.cols == 32) {
-            tc::ld32(v, acc);
-            tc::wait_ld32(v);
-          } else {
-            tc::ld16(v, acc);
-            tc::wait_ld16(v);
+          // four rows of x a warp: 12 columns
+          const int m0 = 4 * half, c0 = 12 * half;
+          if (m0 < count) {
+            float v[4];
+            uint32_t x0[16], x1[16];
+            tc::ld16(x0, acc + c0);
+            tc::ld16(x1, acc + p.cols + c0);
 #pragma unroll
-            for (int c = 16; c < 32; ++c) v[c] = 0u;
-          }
+            for (int m = 0; m < 4; ++m) v[m] = p.split == 1 && res && m0 + m < count ? residual(m0 + m) : 0.f;
+            tc::wait_ld16(x0);
+            tc::wait_ld16(x1);
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            if (m >= count) break;
-            const float r = p.split == 1 && res ? __half2float(a.res[static_cast<long long>(m) * a.N + n]) : 0.f;
-            out(m, (__uint_as_float(v[3 * m + 2]) + __uint_as_float(v[3 * m + 1])) + __uint_as_float(v[3 * m]), 0.f, r);
+            for (int m = 0; m < 4; ++m) {
+              float q[3];
+#pragma unroll
+              for (int c = 0; c < 3; ++c)
+                q[c] = (has0 ? __uint_as_float(x0[3 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[3 * m + c]) : 0.f);
+              v[m] += (q[2] + q[1]) + q[0];
+            }
+            if (p.split == 1) {
+              finish(n, m0, 1, count - m0, v);
+            } else {
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                if (m0 + m < count) give(m0 + m, v[m], 0.f);
+            }
           }
         } else {
-          for (int c0 = 0; c0 < count; c0 += 16) {
+          for (int c0 = half * 16; c0 < count; c0 += 32) {
             uint32_t g[16], u[16];
-            float r[16];
             tc::ld16(g, acc + c0);
-            if (GATED) tc::ld16(u, acc + p.cols + c0);
+            const bool second = GATED || p.pair;
+            if (second) tc::ld16(u, acc + p.cols + c0);
+            float v[16];
             if (!GATED) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                r[c] = p.split == 1 && res && c0 + c < count
-                           ? __half2float(a.res[static_cast<long long>(tok + c0 + c) * a.N + n])
-                           : 0.f;
+              for (int c = 0; c < 16; ++c) v[c] = p.split == 1 && res && c0 + c < count ? residual(c0 + c) : 0.f;
             }
             tc::wait_ld16(g);
-            if (GATED) tc::wait_ld16(u);
+            if (second) tc::wait_ld16(u);
+            if (!GATED && second) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c0 + c < count)
-                out(c0 + c, __uint_as_float(g[c]), GATED ? __uint_as_float(u[c]) : 0.f, GATED ? 0.f : r[c]);
+              for (int c = 0; c < 16; ++c)
+                g[c] = __float_as_uint((has0 ? __uint_as_float(g[c]) : 0.f) + (has1 ? __uint_as_float(u[c]) : 0.f));
+            }
+            if (p.split == 1) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                v[c] = GATED ? silu_f(__uint_as_float(g[c])) * __uint_as_float(u[c]) : __uint_as_float(g[c]) + v[c];
+              finish(n, tok + c0, 1, count - c0, v);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (c0 + c < count) give(c0 + c, __uint_as_float(g[c]), GATED ? __uint_as_float(u[c]) : 0.f);
+            }
           }
         }
       }
@@ -445,33 +574,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.acc_empty[buf]));
       if (p.split == 1) continue;
-      // sums of every rank, for the columns that are this one's to finish
-      fence_cluster();
-      __syncwarp();
-      if (lane < p.split) arrive_remote(map_rank(smem_u32(&bars.part_full), lane));
       step_wait(smem_u32(&bars.part_full), n_t & 1, &s_failed, &g_status);
       fence_cluster();
       const bool all = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
       if (all) {
-        for (int m = rank; m < count; m += p.split) {
-          const uint32_t at = part + ((m * kW) * kRowsW + warp * 32 + lane) * 4;
-          const float r = res ? __half2float(a.res[static_cast<long long>(tok + m) * a.N + n]) : 0.f;
-          float g = 0.f, u = 0.f;
-          for (int q = 0; q < p.split; ++q) {
-            const uint32_t there = map_rank(at, q);
-            g += load_remote(there);
-            if (GATED) u += load_remote(there + kRowsW * 4);
+        for (int j = half; j < own; j += 2) {
+          const int m = rank + j * p.split;
+          const float r = res ? residual(m) : 0.f;
+          float g[8], u[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            g[q] = u[q] = 0.f;
+            if (q < p.split) {
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g[q]) : "r"(part_at(q, j, 0)));
+              if (GATED) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[q]) : "r"(part_at(q, j, 1)));
+            }
           }
-          finish(n, tok + m, GATED ? silu_f(g) * u : g + r);
+          float v[1], w = u[0];
+          v[0] = g[0];
+#pragma unroll
+          for (int q = 1; q < 8; ++q) v[0] += g[q], w += u[q];
+          v[0] = GATED ? silu_f(v[0]) * w : v[0] + r;
+          finish(n, tok + m, 1, 1, v);
         }
       }
       __syncwarp();
       if (lane < p.split) arrive_remote(map_rank(smem_u32(&bars.part_done), lane));
     }
   }
+  // Every copy has been waited for by who uses it; after a wait that ran out, time for those
+  // in flight.
+  if (*static_cast<volatile int*>(&s_failed) != 0)
+    for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 2000000ull;) {
+    }
   tc::fence_before();
   __syncthreads();
-  if (p.split > 1) cluster_sync();  // sums are read, and barriers arrived on, by other ranks
+  if (p.split > 1) {  // other ranks send sums and arrive on barriers
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == kMmaWarp) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
@@ -482,11 +623,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kSmemMax = 227 * 1024 - 1024;  // less the kernel's static shared memory
 
-int stage_bytes(int w, int cols, int raw) {
-  return w * 16384 + cols * kStepK + 512 * (w + (cols > 128 ? 2 : 1)) + raw;
+int stage_bytes(int w, int cols, bool fp16) {
+  return w * 16384 + (fp16 ? 0 : cols * kStepK) + 512 * (w + (fp16 ? 0 : cols > 128 ? 2 : 1));
 }
 
-int part_bytes(int w, int tokens, int split) { return split > 1 ? w * tokens * kRowsW * 4 : 0; }
+int part_bytes(int w, int tokens, int split) {
+  return split > 1 ? w * ((tokens + split - 1) / split * split) * kRowsW * 4 : 0;
+}
 
 bool encode_codes(CUtensorMap* m, const void* p, bool four, long long rows, int k, int box_rows) {
   const EncodeTiledFn fn = encode_fn();
@@ -527,21 +670,28 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
     p.tokens = p.cols;
     p.tok_tiles = (a.M + p.cols - 1) / p.cols;
   }
+  p.pair = !GATED && 4 * p.cols <= kAccCols;
   p.split = 1;
   const long long tiles = static_cast<long long>(p.row_tiles) * p.tok_tiles;
   if (p.tokens <= kSplitTokens / kW)
     while (p.split < 8 && tiles * p.split * 2 <= sms && steps >= p.split * 4) p.split *= 2;
-  const int raw = SPLIT3 ? p.tokens * 256 : 0;
-  const int room = kSmemMax - 1024 - part_bytes(kW, p.tokens, p.split);
-  p.stages = room / stage_bytes(kW, p.cols, raw);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  auto row_steps = [&] { return (steps + p.split - 1) / p.split; };
+  if (SPLIT3) {
+    while (p.split < 8 && (row_steps() > kMaxRowSteps || row_steps() * (32 * kStepK + 512) > 130 * 1024)) p.split *= 2;
+    p.row_steps = row_steps();
+  }
+  const int other = 1024 + part_bytes(kW, p.tokens, p.split) + (SPLIT3 ? p.row_steps * (p.cols * kStepK + 512) : 0);
+  p.stages = (kSmemMax - other) / stage_bytes(kW, p.cols, SPLIT3);
+  // Even, so that a stage is always filled and used by the same of two warps: a wait tells
+  // a use of a stage from the one before it, not from two before.
+  p.stages = (p.stages > kMaxStages ? kMaxStages : p.stages) / 2 * 2;
   if (p.stages < kMinStages) return cudaErrorInvalidValue;
-  const int smem = 1024 + p.stages * stage_bytes(kW, p.cols, raw) + part_bytes(kW, p.tokens, p.split);
+  const int smem = other + p.stages * stage_bytes(kW, p.cols, SPLIT3);
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };
   p.tma_w = a.K % kStepK == 0 && mod(a.w, 32) && (!GATED || mod(a.up, 32));
-  p.words_w = a.K % kStepK == 0 && mod(a.ws, 4);
-  p.words_u = a.K % kStepK == 0 && mod(a.us, 4);
-  p.words_x = a.K % kStepK == 0 && mod(a.xs, 4);
+  const bool all16 = mod(a.ws, 16) && mod(a.us, 16) && mod(a.xs, 16);
+  const bool all4 = mod(a.ws, 4) && mod(a.us, 4) && mod(a.xs, 4);
+  p.bytes = a.K % 512 == 0 && all16 ? 16 : a.K % kStepK == 0 && all4 ? 4 : 1;
   p.rows_first = static_cast<long long>(a.M) * 2 > static_cast<long long>(a.N) * kW;
   CUtensorMap wm{}, um{}, xm{};
   if (p.tma_w && (!encode_codes(&wm, a.w, true, a.N, a.K, kRowsW) ||

@@ -680,9 +680,12 @@ int qgemv_residual_rmsnorm_mxfp8(const uint16_t *x, const uint16_t *residual,
                                  const uint16_t *gamma, float eps, int M, int K, uint16_t *h,
                                  uint8_t *codes, uint8_t *scales, void *stream);
 
+#define QGEMV_MXFP4_MAX_K 28672
+
 /*
  * qgemv_mxfp4 -- y[m][n] = sum_k w[n][k] x[m][k] (+ residual[m][n]) for an MXFP4 weight
- * and fp16 activations, the decode form: 1 <= M <= QGEMV_MAX_M.  x [M][K], y, residual
+ * and fp16 activations, the decode form: 1 <= M <= QGEMV_MAX_M, K <= QGEMV_MXFP4_MAX_K
+ * (the activations stay on chip).  x [M][K], y, residual
  * (NULL: none; may equal y) [M][N] fp16.  fp32 sums, one rounding.  A row of x with an
  * infinity or a NaN gives NaN in all of its outputs.  One launch.
  */
