@@ -1,0 +1,102 @@
+// mx_plan.h -- how a product with MXFP4 weights is cut into tiles (host only, no CUDA).
+#pragma once
+
+namespace qgemv {
+
+constexpr int kMxRows = 128;      // weight rows of a tile
+constexpr int kMxStep = 128;      // k of a stage
+constexpr int kMxMinStages = 4, kMxMaxStages = 16;
+constexpr int kMxRowSteps = 64;   // steps of fp16 rows that a block holds, at most
+constexpr int kMxAccCols = 480;   // tensor memory of the accumulators (512 less the scales')
+constexpr int kMxSplits[4] = {1, 2, 4, 8};
+constexpr int kMxSmem = 227 * 1024 - 1024;  // dynamic shared memory (the rest is static)
+
+struct MxShape {
+  long long M, N;
+  int K;
+  bool gated, fp16;    // two weights; fp16 rows of x
+  int clusters[4];     // clusters of 1, 2, 4, 8 blocks that run at a time
+};
+
+struct MxPlan {
+  int cols;      // columns of a tile
+  int tokens;    // rows of x of a tile
+  int split;     // blocks that share K (a cluster)
+  int stages;
+  int row_tiles, tok_tiles;
+  int row_steps; // steps of fp16 rows that a block holds
+  bool pair;     // every other step's products into a second accumulator
+  bool rows_first;  // tiles of rows change fastest
+  int smem;      // dynamic shared memory of a block
+};
+
+inline int mx_stage_bytes(int w, int cols, bool fp16) {
+  return w * kMxRows * kMxStep + (fp16 ? 0 : cols * kMxStep) + 512 * (w + (fp16 ? 0 : cols > 128 ? 2 : 1));
+}
+
+// Everything of a plan that follows from its columns and split; false where it does not
+// fit a multiprocessor.
+inline bool mx_fit(const MxShape& s, int cols, int split, MxPlan* p) {
+  const int w = s.gated ? 2 : 1, steps = (s.K + kMxStep - 1) / kMxStep;
+  p->cols = cols;
+  p->tokens = s.fp16 ? static_cast<int>(s.M) : cols;
+  p->split = split;
+  p->row_tiles = static_cast<int>((s.N + kMxRows - 1) / kMxRows);
+  p->tok_tiles = static_cast<int>((s.M + p->tokens - 1) / p->tokens);
+  p->row_steps = s.fp16 ? (steps + split - 1) / split : 0;
+  p->pair = !s.gated && 4 * cols <= kMxAccCols;
+  // the smaller operand's tiles change fastest: blocks at work at a time share the larger's
+  p->rows_first = 2 * s.M > w * s.N;
+  if (split > steps || p->row_steps > kMxRowSteps || 2 * w * cols > kMxAccCols) return false;
+  const int part = split > 1 ? w * ((p->tokens + split - 1) / split * split) * kMxRows * 4 : 0;
+  const int other = 1024 + part + p->row_steps * (cols * kMxStep + 512);
+  const int stage = mx_stage_bytes(w, cols, s.fp16);
+  if (other > kMxSmem) return false;
+  // Even, so that a stage is always filled and used by the same of two warps: a wait tells
+  // a use of a stage from the one before it, not from two before.
+  p->stages = (kMxSmem - other) / stage;
+  p->stages = (p->stages > kMxMaxStages ? kMxMaxStages : p->stages) / 2 * 2;
+  p->smem = other + p->stages * stage;
+  return p->stages >= kMxMinStages;
+}
+
+// Clocks that a plan is expected to take.
+inline double mx_cost(const MxShape& s, const MxPlan& p) {
+  const int w = s.gated ? 2 : 1, steps = (s.K + kMxStep - 1) / kMxStep;
+  int i = 0;
+  while (kMxSplits[i] != p.split) ++i;
+  const double tiles = static_cast<double>(p.row_tiles) * p.tok_tiles, clusters = s.clusters[i];
+  const double rounds = static_cast<double>(static_cast<long long>((tiles + clusters - 1) / clusters));
+  const double pipe = w * 4.0 * (p.cols / 2.0 > 32 + p.cols / 4.0 ? p.cols / 2.0 : 32 + p.cols / 4.0);
+  const double issue = s.gated || !p.pair ? 550 : 330;
+  const double bytes = (w * 8704.0 + (s.fp16 ? 0 : p.cols * 132.0)) / 32;
+  double step = pipe > issue ? pipe : issue;
+  if (bytes > step) step = bytes;
+  const double per_tile = ((steps + p.split - 1) / p.split) * step;
+  const double out = 400 + p.tokens * w * 8.0 + (p.split > 1 ? 2000 + 700 * i + p.tokens * w * 60.0 : 0);
+  return rounds * (per_tile > out ? per_tile : out) + out;
+}
+
+// The plan that is expected to be fastest.  False: none fits (K too long for fp16 rows).
+inline bool mx_plan(const MxShape& s, MxPlan* best) {
+  const int w = s.gated ? 2 : 1;
+  double least = 0;
+  bool any = false;
+  for (int i = 0; i < 4; ++i) {
+    if (s.clusters[i] < 1) continue;
+    // fp16 rows: one tile of them (the split is that of eight rows, so that a row's result
+    // does not depend on how many there are)
+    const int lo = s.fp16 ? 32 : 16, hi = s.fp16 ? 32 : kMxAccCols / (2 * w) / 16 * 16;
+    for (int cols = lo; cols <= hi; cols += 16) {
+      if (cols > lo && cols - 16 >= s.M) break;  // wider than the rows there are
+      MxPlan p;
+      if (!mx_fit(s, cols, kMxSplits[i], &p)) continue;
+      const double c = mx_cost(s, p);
+      if (!any || c < least) least = c, *best = p, any = true;
+    }
+  }
+  if (any && s.fp16 && 3 * s.M <= 16) return mx_fit(s, 16, best->split, best);
+  return any;
+}
+
+}  // namespace qgemv

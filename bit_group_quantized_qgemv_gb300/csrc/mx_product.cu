@@ -34,6 +34,7 @@
 #include "mma_tile.cuh"
 #include "mx.h"
 #include "mx_format.cuh"
+#include "mx_plan.h"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -42,33 +43,20 @@ namespace {
 
 __device__ unsigned g_status = 0;
 
-constexpr int kRowsW = 128;   // weight rows of a tile
-constexpr int kStepK = 128;   // k of a stage
+constexpr int kRowsW = kMxRows, kStepK = kMxStep;
 constexpr int kLoaders = 4;   // warps
 constexpr int kTmaWarps = 2;
-constexpr int kMinStages = 4, kMaxStages = 16;
-constexpr int kMaxRowSteps = 64;  // steps of fp16 rows that a block holds, at most
-constexpr int kScaleCols = 16;                    // tensor memory of one step's scales
-constexpr int kAccCols = 512 - 2 * kScaleCols;    // and of the accumulators
-constexpr int kSplitTokens = 64;                  // most columns whose sums blocks share
+constexpr int kScaleCols = 16;  // tensor memory of one step's scales
 
-// What a launch is made of.
-struct MxPlan {
-  int cols;      // columns of a tile
-  int tokens;    // rows of x of a tile
-  int split;     // blocks that share K (a cluster)
-  int stages;
-  int row_tiles, tok_tiles;
-  int row_steps;     // steps of fp16 rows that a block holds
-  bool pair;         // every other step's products into a second accumulator
-  bool rows_first;   // tiles of rows change fastest
-  bool tma_w;        // weights by TMA
-  int bytes;         // of a row's scales in one load: 16, 4 or 1
+// How a launch loads its operands.
+struct MxLoads {
+  bool tma_w;  // weights by TMA
+  int bytes;   // of a row's scales in one load: 16, 4 or 1
 };
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t rows[kMaxRowSteps];  // columns of fp16 rows
+  uint64_t full[kMxMaxStages], empty[kMxMaxStages];
+  uint64_t rows[kMxRowSteps];  // columns of fp16 rows
   uint64_t turn[kLoaders];      // a loader may go on to its group
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_done;
@@ -96,8 +84,9 @@ __device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
+// (relaxed: the barriers' initialisation has a fence of its own)
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -121,13 +110,30 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ta
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// Four scale bytes of a row, from block kb on; what lies behind the row's end is 0.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int kb, int blocks) {
+// The aligned word at p, of which only what lies in [from, to) is read (0 elsewhere).
+__device__ __forceinline__ uint32_t word_within(const uint8_t* p, const uint8_t* from, const uint8_t* to) {
+  if (p >= from && p + 4 <= to) return *reinterpret_cast<const uint32_t*>(p);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (kb + i < blocks) w |= static_cast<uint32_t>(row[kb + i]) << (8 * i);
+    if (p + i >= from && p + i < to) w |= static_cast<uint32_t>(p[i]) << (8 * i);
   return w;
+}
+
+// Sixteen scale bytes at s, wherever it lies; what is not in [from, to) is not read, and
+// bytes from the n-th on are 0.
+__device__ __forceinline__ uint4 scales_unaligned(const uint8_t* s, int n, const uint8_t* from, const uint8_t* to) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 3);
+  uint32_t raw[5], w[4];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) raw[i] = 4 * i < n + off ? word_within(s - off + 4 * i, from, to) : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = __funnelshift_r(raw[i], raw[i + 1], 8 * off);
+    const int left = n - 4 * i;  // bytes of this word
+    if (left < 4) w[i] &= left <= 0 ? 0u : (1u << (8 * left)) - 1;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Place of row r's word among the scales of a step.
@@ -141,40 +147,47 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint32_t x, uint32_t y
 constexpr int kOutWarps = 8, kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders,
               kTmaWarp = kMmaWarp + 2, kThreads = 32 * (kTmaWarp + kTmaWarps);
 
-// Eight values of a row of x (a lane; four lanes hold a block) to three columns: codes
-// to col, col + 128, col + 256 (swizzled as the columns' number wants), scales.
+// 2^k, -14 <= k <= 15, in both halves.
+__device__ __forceinline__ __half2 power2(int k) {
+  const uint32_t h = static_cast<uint32_t>(k + 15) << 10, w = h | (h << 16);
+  return *reinterpret_cast<const __half2*>(&w);
+}
+
+// Eight values of row m of x (a lane; four lanes hold a block) to three columns: their
+// codes at `cols` (a step's, swizzled), the blocks' scales at `scales`.  All in fp16, and
+// exact: x / 2^e1 is below 2^8, what its rounding to e4m3 leaves is a multiple of x's last
+// bit and at most half a step, and the factors are powers of two (only what is below 2^-24
+// after the division is rounded: 2^-31 of the block's largest value).
 __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, uint32_t scales, int m,
                                              int ch) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  float f[8];
-  uint32_t most = 0;
+  uint32_t most = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                           __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+  most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+  most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+  const uint32_t top = max(most & 0xFFFFu, most >> 16);  // bits of the largest magnitude
+  // e1 + 127, at least that of 2^-23
+  const int e = static_cast<int>(__float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(top)))) >> 23);
+  const int byte = max(e, 104) - 7, k = 127 - byte;      // multiplied by 2^k, -8 <= k <= 30
+  const __half2 k0 = power2(min(k, 15)), k1 = power2(max(k - 15, 0));
+  __half2 f[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-    f[2 * i] = h.x, f[2 * i + 1] = h.y;
-    most = max(most, max(__float_as_uint(h.x) & 0x7FFFFFFFu, __float_as_uint(h.y) & 0x7FFFFFFFu));
-  }
-  most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-  most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-  // 2^e1 with e1 + 127 = byte; the largest value is then below 2^8
-  const int e = static_cast<int>(most >> 23), byte = max(e, 103) - 7;
-  const float inv = mx_inverse(byte);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= inv;
+  for (int i = 0; i < 4; ++i) f[i] = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[i]), k0), k1);
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const float next = q == 0 ? 16.f : 32.f;
+    const __half2 next = power2(q == 0 ? 4 : 5);
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t two = mx_codes8(f[2 * i], f[2 * i + 1]);
-      const float2 got = mx_values8(two);
-      f[2 * i] = (f[2 * i] - got.x) * next;
-      f[2 * i + 1] = (f[2 * i + 1] - got.y) * next;
-      w[i >> 1] = i & 1 ? w[i >> 1] | (two << 16) : two;
+      uint16_t two;
+      uint32_t got;
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&f[i])));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(got) : "h"(two));
+      f[i] = __hmul2(__hsub2(f[i], *reinterpret_cast<const __half2*>(&got)), next);
+      w[i >> 1] = i & 1 ? w[i >> 1] | (static_cast<uint32_t>(two) << 16) : two;
     }
     const int c = 3 * m + q;
-    const int sb = e == 255 ? 255 : byte - (q == 0 ? 0 : q == 1 ? 4 : 9);
+    const int sb = top >= 0x7C00u ? 255 : byte - (q == 0 ? 0 : q == 1 ? 4 : 9);
     if (live) {
       asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(cols + c * 128 + (((ch >> 1) ^ (c & 7)) << 4) +
                                                            (ch & 1) * 8),
@@ -189,7 +202,7 @@ __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, 
 // GATED: two weights.  SPLIT3: fp16 rows.
 template <bool GATED, bool SPLIT3>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx_product_kernel(const MxProductArgs a, const MxPlan p, const __grid_constant__ CUtensorMap w_map,
+    mx_product_kernel(const MxProductArgs a, const MxPlan p, const MxLoads ld, const __grid_constant__ CUtensorMap w_map,
                       const __grid_constant__ CUtensorMap u_map, const __grid_constant__ CUtensorMap x_map) {
   constexpr int kW = GATED ? 2 : 1;
   extern __shared__ uint8_t raw_smem[];
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int row, tok;
     place(first, &row, &tok);
     if (warp == kTmaWarp && lane == 0) {
-      if (p.tma_w) {
+      if (ld.tma_w) {
         for (int k = k0; k < k1 && k < k0 + p.stages; ++k) {
           tc::prefetch_2d(&w_map, k * kStepK, row);
           if (GATED) tc::prefetch_2d(&u_map, k * kStepK, row);
@@ -240,22 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(smem_u32(&bars.full[i]), 1 + (p.tma_w ? 0 : 32) + (p.tma_w || !SPLIT3 ? 1 : 0));
-      mbar_init(smem_u32(&bars.empty[i]), kW);
+  if (warp == 0) {
+    if (lane < p.stages) {
+      mbar_init(smem_u32(&bars.full[lane]), 1 + (ld.tma_w ? 0 : 32) + (ld.tma_w || !SPLIT3 ? 1 : 0));
+      mbar_init(smem_u32(&bars.empty[lane]), kW);
+    }
+    if (lane < kLoaders) mbar_init(smem_u32(&bars.turn[lane]), 1);
+    if (lane < 2) {
+      mbar_init(smem_u32(&bars.acc_full[lane]), GATED || p.pair ? 2 : 1);
+      mbar_init(smem_u32(&bars.acc_empty[lane]), kOutWarps);
+    }
+    if (lane == 0) {
+      mbar_init(smem_u32(&bars.part_full), 1);
+      mbar_init(smem_u32(&bars.part_done), kOutWarps * p.split);
+      s_failed = 0;
     }
     if constexpr (SPLIT3)
-      for (int i = 0; i < k1 - k0; ++i) mbar_init(smem_u32(&bars.rows[i]), 1);
-    for (int i = 0; i < kLoaders; ++i) mbar_init(smem_u32(&bars.turn[i]), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.acc_full[i]), GATED || p.pair ? 2 : 1);
-      mbar_init(smem_u32(&bars.acc_empty[i]), kOutWarps);
-    }
-    mbar_init(smem_u32(&bars.part_full), 1);
-    mbar_init(smem_u32(&bars.part_done), kOutWarps * p.split);
+      for (int i = lane; i < k1 - k0; i += 32) mbar_init(smem_u32(&bars.rows[i]), 1);
     fence_mbar_init();
-    s_failed = 0;
   }
   __syncthreads();
   if (p.split > 1) cluster_arrive();
@@ -283,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp >= kTmaWarp) {
     // ------------------------------------------------------------------ TMA
-    if (p.tma_w || !SPLIT3) {
-      const uint32_t bytes = (p.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
+    if (ld.tma_w || !SPLIT3) {
+      const uint32_t bytes = (ld.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
       Steps s = start(warp - kTmaWarp);
       int row = 0, tok = 0;
       for (; find(s); s.k += kTmaWarps, s.stage += kTmaWarps) {
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t full = smem_u32(&bars.full[s.stage]);
           mbar_arrive_expect_tx(full, bytes);
           const uint32_t to = base + s.stage * c_bytes;
-          if (p.tma_w) {
+          if (ld.tma_w) {
             tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
             if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
           }
@@ -321,10 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (GATED || !p.pair || odd == me) {
           if (SPLIT3 && n == 0) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
           step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
-          if (!p.tma_w) tc::fence_async_shared();  // codes by cp.async, for the tensor core
+          if (!ld.tma_w) tc::fence_async_shared();  // codes by cp.async, for the tensor core
           tc::fence_after();
           if (tc::elect_one()) {
-            const uint32_t st = tm + kAccCols + (two ? me : k & 1) * kScaleCols;
+            const uint32_t st = tm + kMxAccCols + (two ? me : k & 1) * kScaleCols;
             tc::copy_scales(st, ss + (GATED ? me * 512 : 0));
             tc::copy_scales(st + 8, SPLIT3 ? x_scales + (k - k0) * 512 : ss + kW * 512);
             if (p.cols > 128) tc::copy_scales(st + 12, ss + (kW + 1) * 512);
@@ -356,33 +371,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q = q0 + static_cast<int>(g % groups), from = max(k0, 4 * q), to = min(k1, 4 * q + 4);
       int row, tok;
       place(first + turn * stride, &row, &tok);
-      // Scales of rows lane, lane + 32, ... of an operand: of the group's four steps.
-      auto load = [&](const uint8_t* scales, int at, int end, int i) {
-        const int r = at + lane + 32 * i;
-        const uint8_t* s = scales + static_cast<long long>(r) * blocks + 16 * q;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r >= end) return v;
-        if (p.bytes == 16) return *reinterpret_cast<const uint4*>(s);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = 0;
-          if (4 * q + j < from || 4 * q + j >= to) continue;
-          w[j] = p.bytes == 4 ? *reinterpret_cast<const uint32_t*>(s + 4 * j)
-                              : scale_word(s, 4 * j, blocks - 16 * q);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-      };
+      // Scales of rows lane, lane + 32, ... of each operand: of the group's four steps.  (All
+      // loads of a kind in one go, so that they are under way together.)
       uint4 vw[4], vu[GATED ? 4 : 1], vx[kRowsX ? kRowsX : 1];
+      auto load_all = [&](auto load) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vw[i] = load(a.ws, row, a.N, i);
-      if constexpr (GATED) {
+        for (int i = 0; i < 4; ++i) vw[i] = load(a.ws, row + lane + 32 * i, a.N);
+        if constexpr (GATED) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vu[i] = load(a.us, row, a.N, i);
+          for (int i = 0; i < 4; ++i) vu[i] = load(a.us, row + lane + 32 * i, a.N);
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsX; ++i)  // (rows of the next tile are loaded too, and not used)
+          vx[i] = load(a.xs, tok + lane + 32 * i, 32 * i < p.tokens ? a.M : 0);
+      };
+      auto at = [&](const uint8_t* scales, int r) { return scales + static_cast<long long>(r) * blocks + 16 * q; };
+      if (ld.bytes == 16) {
+        load_all([&](const uint8_t* scales, int r, int end) {
+          return r < end ? *reinterpret_cast<const uint4*>(at(scales, r)) : make_uint4(0, 0, 0, 0);
+        });
+      } else if (ld.bytes == 4) {
+        load_all([&](const uint8_t* scales, int r, int end) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = r < end && 4 * q + j >= from && 4 * q + j < to
+                       ? *reinterpret_cast<const uint32_t*>(at(scales, r) + 4 * j)
+                       : 0;
+          return make_uint4(w[0], w[1], w[2], w[3]);
+        });
+      } else {
+        load_all([&](const uint8_t* scales, int r, int end) {
+          return r < end ? scales_unaligned(at(scales, r), min(16, blocks - 16 * q), scales,
+                                            scales + static_cast<long long>(end) * blocks)
+                         : make_uint4(0, 0, 0, 0);
+        });
       }
-#pragma unroll
-      for (int i = 0; i < kRowsX; ++i)
-        vx[i] = 32 * i < p.tokens ? load(a.xs, tok, a.M, i) : make_uint4(0, 0, 0, 0);
       // One group after the other: a wait for a stage tells a use from the one before it,
       // not from two before.
       if (g > 0)
@@ -395,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k = 4 * q + j;
         if (k < from || k >= to) continue;
         if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
-        if (!p.tma_w) {
+        if (!ld.tma_w) {
 #pragma unroll
           for (int w = 0; w < kW; ++w)
 #pragma unroll 4
@@ -599,19 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane < p.split) arrive_remote(map_rank(smem_u32(&bars.part_done), lane));
+      // (after the last tile nobody waits for this, and who would be told may have ended)
+      if (t + stride < tiles && lane < p.split) arrive_remote(map_rank(smem_u32(&bars.part_done), lane));
     }
   }
-  // Every copy has been waited for by who uses it; after a wait that ran out, time for those
-  // in flight.
-  if (*static_cast<volatile int*>(&s_failed) != 0)
-    for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 2000000ull;) {
-    }
   tc::fence_before();
   __syncthreads();
-  if (p.split > 1) {  // other ranks send sums and arrive on barriers
-    cluster_arrive();
-    cluster_wait();
+  // Every copy and every sum of another rank has been waited for by who uses it.  After a
+  // wait that ran out: time for copies in flight, and for the ranks that may still send (the
+  // barrier waits for those that have not ended).
+  if (s_failed != 0) {
+    for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < 2000000ull;) {
+    }
+    __syncthreads();
+    if (p.split > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
   }
   if (warp == kMmaWarp) {
     tc::fence_after();
@@ -620,16 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-
-constexpr int kSmemMax = 227 * 1024 - 1024;  // less the kernel's static shared memory
-
-int stage_bytes(int w, int cols, bool fp16) {
-  return w * 16384 + (fp16 ? 0 : cols * kStepK) + 512 * (w + (fp16 ? 0 : cols > 128 ? 2 : 1));
-}
-
-int part_bytes(int w, int tokens, int split) {
-  return split > 1 ? w * ((tokens + split - 1) / split * split) * kRowsW * 4 : 0;
-}
 
 bool encode_codes(CUtensorMap* m, const void* p, bool four, long long rows, int k, int box_rows) {
   const EncodeTiledFn fn = encode_fn();
@@ -644,65 +662,69 @@ bool encode_codes(CUtensorMap* m, const void* p, bool four, long long rows, int 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of 1 << log2 blocks that the device runs at a time, asked once per kernel,
+// size and device (0 where it cannot).
+template <typename F>
+int clusters_at_a_time(F* k, int log2, int sms, int device) {
+  static std::atomic<int> known[4][64];  // one more than the answer
+  if (log2 == 0) return sms;
+  std::atomic<int>& at = known[log2][device & 63];
+  int n = at.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms >> log2 << log2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << log2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int found = 0;
+    if (cudaOccupancyMaxActiveClusters(&found, k, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      found = 0;
+    }
+    n = found + 1;
+    at.store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
 template <bool GATED, bool SPLIT3>
 cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st) {
-  constexpr int kW = GATED ? 2 : 1;
   static std::atomic<unsigned long long> done{0};
   auto* k = mx_product_kernel<GATED, SPLIT3>;
   const unsigned long long bit = 1ull << (device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int steps = (a.K + kStepK - 1) / kStepK;
+  MxShape shape{a.M, a.N, a.K, GATED, SPLIT3, {}};
+  for (int i = 0; i < 4; ++i) shape.clusters[i] = clusters_at_a_time(k, i, sms, device);
   MxPlan p{};
-  p.row_tiles = (a.N + kRowsW - 1) / kRowsW;
-  if (SPLIT3) {
-    p.tokens = a.M;
-    p.cols = 3 * a.M <= 16 ? 16 : 32;
-    p.tok_tiles = 1;
-  } else {
-    const int most = kAccCols / (2 * kW) / 16 * 16;
-    p.tok_tiles = (a.M + most - 1) / most;
-    p.cols = ((a.M + p.tok_tiles - 1) / p.tok_tiles + 15) / 16 * 16;
-    p.tokens = p.cols;
-    p.tok_tiles = (a.M + p.cols - 1) / p.cols;
-  }
-  p.pair = !GATED && 4 * p.cols <= kAccCols;
-  p.split = 1;
-  const long long tiles = static_cast<long long>(p.row_tiles) * p.tok_tiles;
-  if (p.tokens <= kSplitTokens / kW)
-    while (p.split < 8 && tiles * p.split * 2 <= sms && steps >= p.split * 4) p.split *= 2;
-  auto row_steps = [&] { return (steps + p.split - 1) / p.split; };
-  if (SPLIT3) {
-    while (p.split < 8 && (row_steps() > kMaxRowSteps || row_steps() * (32 * kStepK + 512) > 130 * 1024)) p.split *= 2;
-    p.row_steps = row_steps();
-  }
-  const int other = 1024 + part_bytes(kW, p.tokens, p.split) + (SPLIT3 ? p.row_steps * (p.cols * kStepK + 512) : 0);
-  p.stages = (kSmemMax - other) / stage_bytes(kW, p.cols, SPLIT3);
-  // Even, so that a stage is always filled and used by the same of two warps: a wait tells
-  // a use of a stage from the one before it, not from two before.
-  p.stages = (p.stages > kMaxStages ? kMaxStages : p.stages) / 2 * 2;
-  if (p.stages < kMinStages) return cudaErrorInvalidValue;
-  const int smem = other + p.stages * stage_bytes(kW, p.cols, SPLIT3);
+  if (!mx_plan(shape, &p)) return cudaErrorInvalidValue;
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };
-  p.tma_w = a.K % kStepK == 0 && mod(a.w, 32) && (!GATED || mod(a.up, 32));
+  MxLoads ld;
+  ld.tma_w = a.K % kStepK == 0 && mod(a.w, 32) && (!GATED || mod(a.up, 32));
   const bool all16 = mod(a.ws, 16) && mod(a.us, 16) && mod(a.xs, 16);
   const bool all4 = mod(a.ws, 4) && mod(a.us, 4) && mod(a.xs, 4);
-  p.bytes = a.K % 512 == 0 && all16 ? 16 : a.K % kStepK == 0 && all4 ? 4 : 1;
-  p.rows_first = static_cast<long long>(a.M) * 2 > static_cast<long long>(a.N) * kW;
+  ld.bytes = a.K % 512 == 0 && all16 ? 16 : a.K % kStepK == 0 && all4 ? 4 : 1;
   CUtensorMap wm{}, um{}, xm{};
-  if (p.tma_w && (!encode_codes(&wm, a.w, true, a.N, a.K, kRowsW) ||
+  if (ld.tma_w && (!encode_codes(&wm, a.w, true, a.N, a.K, kRowsW) ||
                   (GATED && !encode_codes(&um, a.up, true, a.N, a.K, kRowsW))))
     return cudaErrorInvalidValue;
   if (!SPLIT3 && !encode_codes(&xm, a.x, false, a.M, a.K, p.cols)) return cudaErrorInvalidValue;
-  const long long clusters = tiles < sms / p.split ? tiles : sms / p.split;
+  const long long tiles = static_cast<long long>(p.row_tiles) * p.tok_tiles;
+  const long long most = shape.clusters[__builtin_ctz(p.split)], clusters = tiles < most ? tiles : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * p.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -713,7 +735,7 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k, a, p, wm, um, xm);
+  return cudaLaunchKernelEx(&cfg, k, a, p, ld, wm, um, xm);
 }
 
 }  // namespace
