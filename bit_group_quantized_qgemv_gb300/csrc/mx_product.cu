@@ -13,11 +13,11 @@
 //
 // A step is 128 k: a ring of stages (codes of A and, for MXFP8 rows, of B, 128-byte
 // swizzled, and their scales) between
-//   two warps   TMA, every other step each (one wait and issue takes some 250 clocks,
-//               however large the box): codes of A (where K and the address allow it) and
-//               of MXFP8 rows;
+//   two warps   codes of A and of MXFP8 rows, every other step each (one wait and issue
+//               takes some 250 clocks, however large the box), by TMA or, where K or an
+//               address does not allow that for A, by cp.async;
 //   four warps  scales, four steps each: a row's bytes of them in one load where they are
-//               aligned; codes that TMA cannot load, by cp.async;
+//               aligned;
 //   two warps   scales to tensor memory and four products a step: one for each weight,
 //               or every other step into an accumulator of its own (a warp takes 550
 //               clocks a step to wait for it and issue its products, few columns only 160
@@ -297,28 +297,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     return s.t < tiles;
   };
   if (warp >= kTmaWarp) {
-    // ------------------------------------------------------------------ TMA
-    if (ld.tma_w || !SPLIT3) {
-      const uint32_t bytes = (ld.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
-      Steps s = start(warp - kTmaWarp);
-      int row = 0, tok = 0;
-      for (; find(s); s.k += kTmaWarps, s.stage += kTmaWarps) {
-        if (s.moved) place(s.t, &row, &tok);
-        s.moved = false;
-        if (s.use > 0) step_wait(smem_u32(&bars.empty[s.stage]), (s.use - 1) & 1, &s_failed, &g_status);
-        if (lane == 0) {
-          const uint32_t full = smem_u32(&bars.full[s.stage]);
-          mbar_arrive_expect_tx(full, bytes);
-          const uint32_t to = base + s.stage * c_bytes;
-          if (ld.tma_w) {
-            tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
-            if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
-          }
-          if (!SPLIT3) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
+    // ---------------------------------------------------------------- codes
+    const uint32_t bytes = (ld.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
+    Steps s = start(warp - kTmaWarp);
+    int row = 0, tok = 0;
+    for (; find(s); s.k += kTmaWarps, s.stage += kTmaWarps) {
+      if (s.moved) place(s.t, &row, &tok);
+      s.moved = false;
+      if (s.use > 0) step_wait(smem_u32(&bars.empty[s.stage]), (s.use - 1) & 1, &s_failed, &g_status);
+      const uint32_t full = smem_u32(&bars.full[s.stage]), to = base + s.stage * c_bytes;
+      if (lane == 0 && bytes > 0) {
+        mbar_arrive_expect_tx(full, bytes);
+        if (ld.tma_w) {
+          tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
+          if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
         }
-        __syncwarp();
+        if (!SPLIT3) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
+      }
+      __syncwarp();
+      if (!ld.tma_w) {
+        // sixteen codes a copy, eight lanes to a row
+        const int r0 = lane >> 3, c = lane & 7, left = a.N - row;
+        const bool inside = s.k * kStepK + c * 16 < a.K;
+        const long long at = static_cast<long long>(row + r0) * (a.K / 8) + s.k * (kStepK / 8) + c * 2;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          const uint32_t* codes = w ? a.up : a.w;
+#pragma unroll 8
+          for (int i = 0; i < kRowsW / 4; ++i) {
+            const int r = r0 + 4 * i;
+            const bool has = inside && r < left;
+            cp_async8(to + w * 16384 + r * 128 + ((c ^ (r & 7)) << 4),
+                      codes + (has ? at + static_cast<long long>(i) * (a.K / 2) : 0), has);
+          }
+        }
+        arrive_copied(full);
       }
     }
+    cp_wait_all();
   } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------- products
     const int me = warp - kMmaWarp;
@@ -414,24 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long done = turn * my_steps + (from - k0);  // steps before the group's
       int stage = static_cast<int>(done % p.stages);
       long long use = done / p.stages;
+      int written = 0;  // steps whose scales are to be handed on
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int k = 4 * q + j;
         if (k < from || k >= to) continue;
         if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
-        if (!ld.tma_w) {
-#pragma unroll
-          for (int w = 0; w < kW; ++w)
-#pragma unroll 4
-            for (int i = lane; i < 8 * kRowsW; i += 32) {
-              const int r = i >> 3, c = i & 7;
-              const bool has = row + r < a.N && k * kStepK + c * 16 < a.K;
-              const uint32_t* src = (w ? a.up : a.w) +
-                  (has ? static_cast<long long>(row + r) * (a.K / 8) + k * (kStepK / 8) + c * 2 : 0);
-              cp_async8(base + stage * c_bytes + w * 16384 + r * 128 + ((c ^ (r & 7)) << 4), src, has);
-            }
-          arrive_copied(smem_u32(&bars.full[stage]));
-        }
+        if (k == to - 1 && lane == 0) mbar_arrive(smem_u32(&bars.turn[(me + 1) % kLoaders]));
         const uint32_t ss = s_ring + stage * s_bytes + lane * 16;
         auto word = [&](const uint4& v) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
         store_shared(ss, word(vw[0]), word(vw[1]), word(vw[2]), word(vw[3]));
@@ -442,15 +447,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.cols > 128)
               store_shared(ss + (kW + 1) * 512, word(vx[4]), word(vx[5]), word(vx[6]), word(vx[7]));
         }
-        tc::fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.full[stage]));
         if (++stage == p.stages) stage = 0, ++use;
+        ++written;
+        // Handed on two or four at a time: the fence takes longer than all else.
+        if (k == to - 1 || j == 3 || (j == 1 && p.stages < 8)) {
+          tc::fence_async_shared();
+          __syncwarp();
+          const int s = stage - 1 - lane;
+          if (lane < written) mbar_arrive(smem_u32(&bars.full[s < 0 ? s + p.stages : s]));
+          written = 0;
+        }
       }
-      if (lane == 0) mbar_arrive(smem_u32(&bars.turn[(me + 1) % kLoaders]));
       __syncwarp();
     }
-    cp_wait_all();
   } else {
     // -------------------------------------------------------------- results
     const int quarter = warp & 3, half = warp >> 2;  // lanes of tensor memory; which columns
@@ -478,14 +487,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars.rows[i]));
       }
     }
-    // Finished values of weight row n and rows m, m + step, ... of x.
-    auto finish = [&](int n, int m, int step, int count, auto& v) {
+    // Finished values of weight row n and rows m, m + 1, ... of x (count of them).
+    auto finish = [&](int n, int m, int count, auto& v) {
       constexpr int C = sizeof(v) / sizeof(float);
-      __half* y = a.y;
+      const bool live = n < a.N;
+      const long long at = static_cast<long long>(m) * a.N + n;
+      if (a.y != nullptr && live) {
+        __half* y = a.y + at;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (y != nullptr && c < count && n < a.N)
-          y[static_cast<long long>(m + c * step) * a.N + n] = __float2half_rn(v[c]);
+        for (int c = 0; c < C; ++c, y += a.N)
+          if (c < count) *y = __float2half_rn(v[c]);
+      }
       if constexpr (GATED) {
         if (a.yc == nullptr) return;
         // (N is a multiple of 32: a warp's rows are one block of the output, all there or none)
@@ -493,13 +505,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c)
           byte[c] = mx_scale_byte<8>(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[c]) & 0x7FFFFFFFu)));
+        if (!live) return;
+        uint8_t* codes = a.yc + at;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (c < count && n < a.N) {
-            const long long at = static_cast<long long>(m + c * step) * a.N + n;
-            a.yc[at] = static_cast<uint8_t>(mx_codes8(v[c] * mx_inverse(byte[c]), 0.f));
-            if (lane == 0) a.ys[at >> 5] = static_cast<uint8_t>(byte[c]);
-          }
+        for (int c = 0; c < C; ++c, codes += a.N)
+          if (c < count) *codes = static_cast<uint8_t>(mx_codes8(v[c] * mx_inverse(byte[c]), 0.f));
+        // lane c has the scale of row m + c
+        int mine = byte[0];
+#pragma unroll
+        for (int c = 1; c < C; ++c) mine = lane == c ? byte[c] : mine;
+        if (lane < C && lane < count)
+          a.ys[static_cast<long long>(m + lane) * (a.N / kMxBlock) + n / kMxBlock] = static_cast<uint8_t>(mine);
       }
     };
     const int share = (p.tokens + p.split - 1) / p.split;  // rows of x that a rank finishes, at most
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[m] += (q[2] + q[1]) + q[0];
             }
             if (p.split == 1) {
-              finish(n, m0, 1, count - m0, v);
+              finish(n, m0, count - m0, v);
             } else {
 #pragma unroll
               for (int m = 0; m < 4; ++m)
@@ -585,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c)
                 v[c] = GATED ? silu_f(__uint_as_float(g[c])) * __uint_as_float(u[c]) : __uint_as_float(g[c]) + v[c];
-              finish(n, tok + c0, 1, count - c0, v);
+              finish(n, tok + c0, count - c0, v);
             } else {
 #pragma unroll
               for (int c = 0; c < 16; ++c)
@@ -619,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 1; q < 8; ++q) v[0] += g[q], w += u[q];
           v[0] = GATED ? silu_f(v[0]) * w : v[0] + r;
-          finish(n, tok + m, 1, 1, v);
+          finish(n, tok + m, 1, v);
         }
       }
       __syncwarp();

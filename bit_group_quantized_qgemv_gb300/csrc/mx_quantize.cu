@@ -233,10 +233,11 @@ cudaError_t mx_dequantize_launch(const MxDequantArgs& a, int bits, int, cudaStre
 }
 
 cudaError_t mx_norm_launch(const MxNormArgs& a, int, cudaStream_t st) {
-  // a thread a block of the row, up to 1024 of them; rows up to kThreads threads
+  // A thread a block of the row, up to 1024 of them.  Short rows share a thread block of 128
+  // (with 256 or 512, 2048 rows of 4096 take 0.6 or 1.4 us more: fewer of them at a time).
   const int warps = (a.K / kMxBlock + 31) / 32, T = 32 * (warps < 32 ? warps : 32);
   if (T > kThreads) return launch(mx_norm_kernel<false>, a.M, T, st, a, T);
-  const int rows = kThreads / T;
+  const int rows = T < 128 ? 128 / T : 1;
   return launch(mx_norm_kernel<true>, (a.M + rows - 1LL) / rows, rows * T, st, a, T);
 }
 
