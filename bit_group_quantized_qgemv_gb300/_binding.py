@@ -781,19 +781,15 @@ def _mx_refuse(index, **tensors):
 _CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
 
 
-# The looks that every call takes at a tensor: its type, device, layout, number of values
-# and last axis.  Written out where they are few: on the host, where small calls spend
-# their time, a function's call costs as much as two of them.
-def _mx_fit(t, dtypes, index, count, last):
-    return (t.dtype in dtypes and t.get_device() == index and t.is_contiguous() and
-            t.numel() == count and t.size(-1) == last)
-
-
+# The looks that every call takes at a tensor (its type, device, layout, number of values
+# and last axis) are written out in each: on the host, where small calls spend their time,
+# a function's call costs as much as two of them.
 def _mx_weight(index, w, name):
     """(codes, scales, rows, k) of an MXFP4 weight (codes, scales)."""
     codes, scales = w
     n, words = codes.shape
-    if not (codes.dtype in _CODES4 and codes.get_device() == index and codes.is_contiguous() and
+    if not ((codes.dtype is _I32 or codes.dtype in _CODES4) and
+            codes.get_device() == index and codes.is_contiguous() and
             scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
             scales.numel() == n * (words // 4)):
         _mx_refuse(index, **{name + ".codes": (codes, _CODES4, codes.shape),
@@ -805,8 +801,8 @@ def _mx_activations(index, x, k):
     """(codes, scales, rows) of MXFP8 rows (codes, scales) for a weight of k columns."""
     codes, scales = x
     count = codes.numel()
-    if not (codes.dtype in _CODES8 and codes.get_device() == index and codes.is_contiguous() and
-            codes.size(-1) == k and scales.dtype is _U8 and scales.get_device() == index and
+    if not ((codes.dtype is _U8 or codes.dtype is _E4M3) and codes.get_device() == index and
+            codes.is_contiguous() and codes.size(-1) == k and scales.dtype is _U8 and scales.get_device() == index and
             scales.is_contiguous() and scales.numel() * 32 == count):
         _mx_refuse(index, **{"x.codes": (codes, _CODES8, (*codes.shape[:-1], k)),
                              "x.scales": (scales, _BYTES, (*codes.shape[:-1], k // 32))})
@@ -830,7 +826,8 @@ def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
     if scales is None:
         scales = torch.empty((*x.shape[:-1], k // 32), dtype=_U8, device=x.device)
     if not (x.dtype is _HALF and x.is_contiguous() and
-            _mx_fit(codes, kinds, index, count // per, k // per) and
+            (codes.dtype is kinds[0] or codes.dtype in kinds) and codes.get_device() == index and
+            codes.is_contiguous() and codes.numel() == count // per and codes.size(-1) == k // per and
             scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
             scales.numel() == count // 32):
         _mx_refuse(index, x=(x, _F16, x.shape), codes=(codes, kinds, (*x.shape[:-1], k // per)),
@@ -890,11 +887,16 @@ def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None
     else:
         if h is None:
             h = torch.empty_like(x)
-        fit = _mx_fit(residual, _F16, index, count, k) and _mx_fit(h, _F16, index, count, k)
+        fit = (residual.dtype is _HALF and residual.get_device() == index and
+               residual.is_contiguous() and residual.shape == x.shape and
+               h.dtype is _HALF and h.get_device() == index and h.is_contiguous() and
+               h.shape == x.shape)
         r_at, h_at = residual.data_ptr(), h.data_ptr()
     if not (fit and x.dtype is _HALF and x.is_contiguous() and
             gamma.dtype is _HALF and gamma.get_device() == index and gamma.is_contiguous() and
-            gamma.numel() == k and _mx_fit(codes, _CODES8, index, count, k) and
+            gamma.numel() == k and (codes.dtype is _U8 or codes.dtype is _E4M3) and
+            codes.get_device() == index and codes.is_contiguous() and codes.numel() == count and
+            codes.size(-1) == k and
             scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
             scales.numel() == count // 32):
         _mx_refuse(index, x=(x, _F16, x.shape), gamma=(gamma, _F16, (k,)),
@@ -921,7 +923,9 @@ def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
     if not (x.dtype is _HALF and x.is_contiguous() and x.size(-1) == k and
             y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
             y.numel() == m * n and y.size(-1) == n and
-            (residual is None or _mx_fit(residual, _F16, index, m * n, n))):
+            (residual is None or
+             (residual.dtype is _HALF and residual.get_device() == index and
+              residual.is_contiguous() and residual.shape == y.shape))):
         _mx_refuse(index, x=(x, _F16, (*x.shape[:-1], k)), y=(y, _F16, (*x.shape[:-1], n)),
                    residual=(residual, _F16, (*x.shape[:-1], n)))
     rc = lib.qgemv_mxfp4(codes, scales, x.data_ptr(), y.data_ptr(), m, n, k,
@@ -944,7 +948,9 @@ def mx_gemm(w, x, y=None, residual=None, stream=None):
         y = torch.empty((*x[0].shape[:-1], n), dtype=_HALF, device=x[0].device)
     if not (y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
             y.numel() == m * n and y.size(-1) == n and
-            (residual is None or _mx_fit(residual, _F16, index, m * n, n))):
+            (residual is None or
+             (residual.dtype is _HALF and residual.get_device() == index and
+              residual.is_contiguous() and residual.shape == y.shape))):
         shape = (*x[0].shape[:-1], n)
         _mx_refuse(index, y=(y, _F16, shape), residual=(residual, _F16, shape))
     rc = lib.qgemv_mx_gemm(codes, scales, xc, xs, y.data_ptr(), m, n, k,
@@ -975,13 +981,14 @@ def mx_swiglu(gate, up, x, h=None, codes=None, scales=None, stream=None):
             codes = torch.empty((*x[0].shape[:-1], n), dtype=_U8, device=x[0].device)
         if scales is None:
             scales = torch.empty((*x[0].shape[:-1], n // 32), dtype=_U8, device=x[0].device)
-        fit = (codes.dtype in _CODES8 and codes.get_device() == index and codes.is_contiguous() and
-               codes.numel() == m * n and codes.size(-1) == n and
+        fit = ((codes.dtype is _U8 or codes.dtype is _E4M3) and codes.get_device() == index and
+               codes.is_contiguous() and codes.numel() == m * n and codes.size(-1) == n and
                scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
                scales.numel() == m * (n // 32))
         c_at, s_at = codes.data_ptr(), scales.data_ptr()
     if h is not None:
-        fit = fit and _mx_fit(h, _F16, index, m * n, n)
+        fit = (fit and h.dtype is _HALF and h.get_device() == index and h.is_contiguous() and
+               h.numel() == m * n and h.size(-1) == n)
         h_at = h.data_ptr()
     if not fit:
         lead = x[0].shape[:-1]

@@ -16,6 +16,12 @@ struct MxShape {
   int K;
   bool gated, fp16;    // two weights; fp16 rows of x
   int clusters[4];     // clusters of 1, 2, 4, 8 blocks that run at a time
+
+  bool operator==(const MxShape& o) const {
+    bool same = M == o.M && N == o.N && K == o.K && gated == o.gated && fp16 == o.fp16;
+    for (int i = 0; i < 4; ++i) same = same && clusters[i] == o.clusters[i];
+    return same;
+  }
 };
 
 struct MxPlan {
