@@ -9,6 +9,8 @@ no fallback: if the library cannot be loaded, importing fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -749,6 +751,26 @@ def cache_evict(cache, mass, entry_pos, next_pos, keep, n_sink=0, n_recent=0, ke
 
 _U8 = torch.uint8
 _E4M3 = torch.float8_e4m3fn
+_CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
+
+
+def _load_calls():
+    """The module that looks at a call's tensors and makes the call (csrc/mx_calls.c)."""
+    path = _build.CALLS
+    if not os.path.exists(path):
+        raise ImportError(f"_mx_calls.so not found at {path}; build it first with "
+                          "`python -m bit_group_quantized_qgemv_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_mx_calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mx_calls", loader))
+    loader.exec_module(module)
+    names = ("qgemv_mx_quantize", "qgemv_mx_dequantize", "qgemv_residual_rmsnorm_mxfp8",
+             "qgemv_mxfp4", "qgemv_mx_gemm", "qgemv_mx_swiglu")
+    module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names],
+                _HALF, _U8, _E4M3, _I32, _CODES4[1], _current_device, _raw_stream)
+    return module
+
+
+_calls = _load_calls()
 
 
 def _mx_elsewhere(call, t, stream, *args):
@@ -765,48 +787,45 @@ def _mx_elsewhere(call, t, stream, *args):
         return call(*args)
 
 
-def _mx_refuse(index, **tensors):
-    """Raises what is wrong with tensors (name: (tensor, dtypes, shape)) that the calls
-    below found unfit with cheaper looks; nothing where only k is (the library's to refuse)."""
+def _mx_unfit(call, args, what, **tensors):
+    """What to do where _calls found that something does not fit: the call on its tensors'
+    device, or the error.  tensors: name = (tensor, types, shape), the first one's device is
+    the call's."""
+    t = next(iter(tensors.values()))[0]
+    if t.is_cuda and _current_device() != t.get_device():
+        return _mx_elsewhere(call, t, None, *args)
     for name, (t, dtypes, shape) in tensors.items():
         if t is None:
             continue
         _cuda(t, dtypes, name)
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+        if t.get_device() != _current_device():
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{_current_device()}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise QgemvError(-1, what)  # sizes that the library refuses
 
 
-_CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
+def _mx_lead(t, name):
+    """All sizes of a tensor but the last, and the last."""
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one axis")
+    return t.shape[:-1], t.shape[-1]
 
 
-# The looks that every call takes at a tensor (its type, device, layout, number of values
-# and last axis) are written out in each: on the host, where small calls spend their time,
-# a function's call costs as much as two of them.
-def _mx_weight(index, w, name):
-    """(codes, scales, rows, k) of an MXFP4 weight (codes, scales)."""
+def _mx_weight(w, name):
+    """{name: (tensor, types, shape)} of an MXFP4 weight, for _mx_unfit."""
     codes, scales = w
+    if codes.dim() != 2:
+        raise ValueError(f"{name}.codes must be [rows][k / 8]")
     n, words = codes.shape
-    if not ((codes.dtype is _I32 or codes.dtype in _CODES4) and
-            codes.get_device() == index and codes.is_contiguous() and
-            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
-            scales.numel() == n * (words // 4)):
-        _mx_refuse(index, **{name + ".codes": (codes, _CODES4, codes.shape),
-                             name + ".scales": (scales, _BYTES, (n, words // 4))})
-    return codes.data_ptr(), scales.data_ptr(), n, words * 8
+    return {name + ".codes": (codes, _CODES4, codes.shape),
+            name + ".scales": (scales, _BYTES, (n, words // 4))}
 
 
-def _mx_activations(index, x, k):
-    """(codes, scales, rows) of MXFP8 rows (codes, scales) for a weight of k columns."""
-    codes, scales = x
-    count = codes.numel()
-    if not ((codes.dtype is _U8 or codes.dtype is _E4M3) and codes.get_device() == index and
-            codes.is_contiguous() and codes.size(-1) == k and scales.dtype is _U8 and scales.get_device() == index and
-            scales.is_contiguous() and scales.numel() * 32 == count):
-        _mx_refuse(index, **{"x.codes": (codes, _CODES8, (*codes.shape[:-1], k)),
-                             "x.scales": (scales, _BYTES, (*codes.shape[:-1], k // 32))})
-    return codes.data_ptr(), scales.data_ptr(), count // k if k else 0
+def _mx_rows(x, k):
+    """The same of MXFP8 rows of k columns."""
+    lead, _ = _mx_lead(x[0], "x.codes")
+    return {"x.codes": (x[0], _CODES8, (*lead, k)), "x.scales": (x[1], _BYTES, (*lead, k // 32))}
 
 
 def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
@@ -814,58 +833,48 @@ def mx_quantize(x, bits=8, codes=None, scales=None, stream=None):
     k (k a multiple of 32).  bits 4: MXFP4, codes int32 [..., k / 8]; bits 8: MXFP8,
     codes uint8 [..., k] (e4m3; a float8_e4m3fn tensor may be given).  Returns
     (codes, scales uint8 [..., k / 32])."""
-    index = x.get_device()
-    if stream is not None or _current_device() != index:
+    if stream is not None:
         return _mx_elsewhere(mx_quantize, x, stream, x, bits, codes, scales)
-    if bits != 8 and bits != 4:
-        raise ValueError(f"bits must be 4 or 8, not {bits}")
-    count, k = x.numel(), x.size(-1)
-    per, kinds = (1, _CODES8) if bits == 8 else (8, _CODES4)
-    if codes is None:
-        codes = torch.empty((*x.shape[:-1], k // per), dtype=kinds[0], device=x.device)
-    if scales is None:
-        scales = torch.empty((*x.shape[:-1], k // 32), dtype=_U8, device=x.device)
-    if not (x.dtype is _HALF and x.is_contiguous() and
-            (codes.dtype is kinds[0] or codes.dtype in kinds) and codes.get_device() == index and
-            codes.is_contiguous() and codes.numel() == count // per and codes.size(-1) == k // per and
-            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
-            scales.numel() == count // 32):
-        _mx_refuse(index, x=(x, _F16, x.shape), codes=(codes, kinds, (*x.shape[:-1], k // per)),
-                   scales=(scales, _BYTES, (*x.shape[:-1], k // 32)))
-    rc = lib.qgemv_mx_quantize(bits, x.data_ptr(), count // k if count else 0, k, codes.data_ptr(),
-                               scales.data_ptr(), _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_mx_quantize")
-    return codes, scales
+    if codes is None or scales is None:
+        lead, k = _mx_lead(x, "x")
+        if codes is None:
+            codes = torch.empty((*lead, k if bits == 8 else k // 8),
+                                dtype=_U8 if bits == 8 else _I32, device=x.device)
+        if scales is None:
+            scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
+    rc = _calls.quantize(x, bits, codes, scales)
+    if rc == 0:
+        return codes, scales
+    if rc is None:
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, not {bits}")
+        lead, k = _mx_lead(x, "x")
+        kind, per = (_CODES8, 1) if bits == 8 else (_CODES4, 8)
+        return _mx_unfit(mx_quantize, (x, bits, codes, scales), "qgemv_mx_quantize",
+                         x=(x, _F16, x.shape), codes=(codes, kind, (*lead, k // per)),
+                         scales=(scales, _BYTES, (*lead, k // 32)))
+    _check(rc, "qgemv_mx_quantize")
 
 
 def mx_dequantize(codes, scales, out=None, stream=None):
     """qgemv_mx_dequantize: the fp16 values [..., k] of MXFP4 (int32 codes) or MXFP8
     (uint8 or float8_e4m3fn codes) rows."""
-    index = codes.get_device()
-    if stream is not None or _current_device() != index:
+    if stream is not None:
         return _mx_elsewhere(mx_dequantize, codes, stream, codes, scales, out)
-    count, k, kind = codes.numel(), codes.size(-1), codes.dtype
-    bits = 8
-    if kind is not _U8 and kind is not _E4M3:
-        bits = 4
-        count *= 8
-        k *= 8
     if out is None:
-        out = torch.empty((*codes.shape[:-1], k), dtype=_HALF, device=codes.device)
-    if not ((bits == 8 or kind in _CODES4) and codes.is_contiguous() and
-            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
-            scales.numel() == count // 32 and
-            out.dtype is _HALF and out.get_device() == index and out.is_contiguous() and
-            out.numel() == count and out.size(-1) == k):
-        _mx_refuse(index, codes=(codes, _CODES4 + _CODES8, codes.shape),
-                   scales=(scales, _BYTES, (*codes.shape[:-1], k // 32)),
-                   out=(out, _F16, (*codes.shape[:-1], k)))
-    rc = lib.qgemv_mx_dequantize(bits, codes.data_ptr(), scales.data_ptr(),
-                                 count // k if count else 0, k, out.data_ptr(), _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_mx_dequantize")
-    return out
+        lead, k = _mx_lead(codes, "codes")
+        out = torch.empty((*lead, 8 * k if codes.dtype in _CODES4 else k), dtype=_HALF,
+                          device=codes.device)
+    rc = _calls.dequantize(codes, scales, out)
+    if rc == 0:
+        return out
+    if rc is None:
+        lead, k = _mx_lead(codes, "codes")
+        k = 8 * k if codes.dtype in _CODES4 else k
+        return _mx_unfit(mx_dequantize, (codes, scales, out), "qgemv_mx_dequantize",
+                         codes=(codes, _CODES4 + _CODES8, codes.shape),
+                         scales=(scales, _BYTES, (*lead, k // 32)), out=(out, _F16, (*lead, k)))
+    _check(rc, "qgemv_mx_dequantize")
 
 
 def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None, scales=None,
@@ -873,91 +882,71 @@ def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None
     """qgemv_residual_rmsnorm_mxfp8: h = x + residual (fp16 rows [..., k]; x itself
     when residual is None), RMSNorm(h) * gamma as MXFP8.  h may be x or residual.
     Returns (h, codes uint8 [..., k], scales uint8 [..., k / 32])."""
-    index = x.get_device()
-    if stream is not None or _current_device() != index:
+    if stream is not None:
         return _mx_elsewhere(residual_rmsnorm_mxfp8, x, stream, x, gamma, residual, eps, h, codes,
                              scales)
-    count, k = x.numel(), x.size(-1)
+    if residual is None:
+        h = x
+    elif h is None:
+        h = torch.empty_like(x)
     if codes is None:
         codes = torch.empty(x.shape, dtype=_U8, device=x.device)
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], k // 32), dtype=_U8, device=x.device)
-    if residual is None:
-        h, r_at, h_at, fit = x, None, None, True
-    else:
-        if h is None:
-            h = torch.empty_like(x)
-        fit = (residual.dtype is _HALF and residual.get_device() == index and
-               residual.is_contiguous() and residual.shape == x.shape and
-               h.dtype is _HALF and h.get_device() == index and h.is_contiguous() and
-               h.shape == x.shape)
-        r_at, h_at = residual.data_ptr(), h.data_ptr()
-    if not (fit and x.dtype is _HALF and x.is_contiguous() and
-            gamma.dtype is _HALF and gamma.get_device() == index and gamma.is_contiguous() and
-            gamma.numel() == k and (codes.dtype is _U8 or codes.dtype is _E4M3) and
-            codes.get_device() == index and codes.is_contiguous() and codes.numel() == count and
-            codes.size(-1) == k and
-            scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
-            scales.numel() == count // 32):
-        _mx_refuse(index, x=(x, _F16, x.shape), gamma=(gamma, _F16, (k,)),
-                   residual=(residual, _F16, x.shape), h=(h, _F16, x.shape),
-                   codes=(codes, _CODES8, x.shape), scales=(scales, _BYTES, (*x.shape[:-1], k // 32)))
-    rc = lib.qgemv_residual_rmsnorm_mxfp8(x.data_ptr(), r_at, gamma.data_ptr(), eps,
-                                          count // k if count else 0, k, h_at, codes.data_ptr(),
-                                          scales.data_ptr(), _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_residual_rmsnorm_mxfp8")
-    return h, codes, scales
+        lead, k = _mx_lead(x, "x")
+        scales = torch.empty((*lead, k // 32), dtype=_U8, device=x.device)
+    rc = _calls.norm(x, gamma, residual, eps, h, codes, scales)
+    if rc == 0:
+        return h, codes, scales
+    if rc is None:
+        lead, k = _mx_lead(x, "x")
+        return _mx_unfit(residual_rmsnorm_mxfp8, (x, gamma, residual, float(eps), h, codes, scales),
+                         "qgemv_residual_rmsnorm_mxfp8", x=(x, _F16, x.shape),
+                         gamma=(gamma, _F16, (k,)), residual=(residual, _F16, x.shape),
+                         h=(h, _F16, x.shape), codes=(codes, _CODES8, x.shape),
+                         scales=(scales, _BYTES, (*lead, k // 32)))
+    _check(rc, "qgemv_residual_rmsnorm_mxfp8")
 
 
 def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
     """y = W x (+ residual) for an MXFP4 weight w = (codes int32 [n][k / 8], scales
     uint8 [n][k / 32]) and one to eight fp16 rows x ([k] or [m][k])."""
-    index = x.get_device()
-    if stream is not None or _current_device() != index:
+    if stream is not None:
         return _mx_elsewhere(qgemv_mxfp4, x, stream, w, x, y, residual)
-    codes, scales, n, k = _mx_weight(index, w, "w")
-    m = x.numel() // k if k else 0
+    codes, scales = w
     if y is None:
-        y = torch.empty((*x.shape[:-1], n), dtype=_HALF, device=x.device)
-    if not (x.dtype is _HALF and x.is_contiguous() and x.size(-1) == k and
-            y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
-            y.numel() == m * n and y.size(-1) == n and
-            (residual is None or
-             (residual.dtype is _HALF and residual.get_device() == index and
-              residual.is_contiguous() and residual.shape == y.shape))):
-        _mx_refuse(index, x=(x, _F16, (*x.shape[:-1], k)), y=(y, _F16, (*x.shape[:-1], n)),
-                   residual=(residual, _F16, (*x.shape[:-1], n)))
-    rc = lib.qgemv_mxfp4(codes, scales, x.data_ptr(), y.data_ptr(), m, n, k,
-                         None if residual is None else residual.data_ptr(), _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_mxfp4")
-    return y
+        lead, _ = _mx_lead(x, "x")
+        y = torch.empty((*lead, codes.shape[0]), dtype=_HALF, device=x.device)
+    rc = _calls.matvec(codes, scales, x, y, residual)
+    if rc == 0:
+        return y
+    if rc is None:
+        tensors = _mx_weight(w, "w")
+        (lead, _), n, k = _mx_lead(x, "x"), codes.shape[0], 8 * codes.shape[1]
+        return _mx_unfit(qgemv_mxfp4, (w, x, y, residual), "qgemv_mxfp4", x=(x, _F16, (*lead, k)),
+                         **tensors, y=(y, _F16, (*lead, n)), residual=(residual, _F16, (*lead, n)))
+    _check(rc, "qgemv_mxfp4")
 
 
 def mx_gemm(w, x, y=None, residual=None, stream=None):
     """qgemv_mx_gemm: y = W x (+ residual, which may be y) for an MXFP4 weight w =
     (codes int32 [n][k / 8], scales uint8 [n][k / 32]) and any number of MXFP8 rows
     x = (codes uint8 [..., k], scales uint8 [..., k / 32]).  Returns y fp16 [..., n]."""
-    index = x[0].get_device()
-    if stream is not None or _current_device() != index:
-        return _mx_elsewhere(mx_gemm, x[0], stream, w, x, y, residual)
-    codes, scales, n, k = _mx_weight(index, w, "w")
-    xc, xs, m = _mx_activations(index, x, k)
+    codes, scales = w
+    xc, xs = x
+    if stream is not None:
+        return _mx_elsewhere(mx_gemm, xc, stream, w, x, y, residual)
     if y is None:
-        y = torch.empty((*x[0].shape[:-1], n), dtype=_HALF, device=x[0].device)
-    if not (y.dtype is _HALF and y.get_device() == index and y.is_contiguous() and
-            y.numel() == m * n and y.size(-1) == n and
-            (residual is None or
-             (residual.dtype is _HALF and residual.get_device() == index and
-              residual.is_contiguous() and residual.shape == y.shape))):
-        shape = (*x[0].shape[:-1], n)
-        _mx_refuse(index, y=(y, _F16, shape), residual=(residual, _F16, shape))
-    rc = lib.qgemv_mx_gemm(codes, scales, xc, xs, y.data_ptr(), m, n, k,
-                           None if residual is None else residual.data_ptr(), _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_mx_gemm")
-    return y
+        lead, _ = _mx_lead(xc, "x.codes")
+        y = torch.empty((*lead, codes.shape[0]), dtype=_HALF, device=xc.device)
+    rc = _calls.gemm(codes, scales, xc, xs, y, residual)
+    if rc == 0:
+        return y
+    if rc is None:
+        tensors = _mx_weight(w, "w")
+        (lead, _), n, k = _mx_lead(xc, "x.codes"), codes.shape[0], 8 * codes.shape[1]
+        return _mx_unfit(mx_gemm, (w, x, y, residual), "qgemv_mx_gemm", **_mx_rows(x, k), **tensors,
+                         y=(y, _F16, (*lead, n)), residual=(residual, _F16, (*lead, n)))
+    _check(rc, "qgemv_mx_gemm")
 
 
 def mx_swiglu(gate, up, x, h=None, codes=None, scales=None, stream=None):
@@ -965,39 +954,31 @@ def mx_swiglu(gate, up, x, h=None, codes=None, scales=None, stream=None):
     scales), [n][k]) and MXFP8 rows x = (codes, scales).  With h (fp16 [..., n]) alone the
     result goes there and h is returned; else it leaves as MXFP8, what mx_gemm takes:
     returns (codes uint8 [..., n], scales uint8 [..., n / 32]) (and fills h where given)."""
-    index = x[0].get_device()
-    if stream is not None or _current_device() != index:
-        return _mx_elsewhere(mx_swiglu, x[0], stream, gate, up, x, h, codes, scales)
-    gc, gs, n, k = _mx_weight(index, gate, "gate")
-    uc, us, n2, k2 = _mx_weight(index, up, "up")
-    if n2 != n or k2 != k:
-        raise ValueError(f"up is {n2} x {k2}, gate {n} x {k}")
-    xc, xs, m = _mx_activations(index, x, k)
+    gc, gs = gate
+    uc, us = up
+    xc, xs = x
+    if stream is not None:
+        return _mx_elsewhere(mx_swiglu, xc, stream, gate, up, x, h, codes, scales)
     held = h is None or codes is not None or scales is not None
-    c_at = s_at = h_at = None
-    fit = True
-    if held:
+    if held and (codes is None or scales is None):
+        lead, _ = _mx_lead(xc, "x.codes")
         if codes is None:
-            codes = torch.empty((*x[0].shape[:-1], n), dtype=_U8, device=x[0].device)
+            codes = torch.empty((*lead, gc.shape[0]), dtype=_U8, device=xc.device)
         if scales is None:
-            scales = torch.empty((*x[0].shape[:-1], n // 32), dtype=_U8, device=x[0].device)
-        fit = ((codes.dtype is _U8 or codes.dtype is _E4M3) and codes.get_device() == index and
-               codes.is_contiguous() and codes.numel() == m * n and codes.size(-1) == n and
-               scales.dtype is _U8 and scales.get_device() == index and scales.is_contiguous() and
-               scales.numel() == m * (n // 32))
-        c_at, s_at = codes.data_ptr(), scales.data_ptr()
-    if h is not None:
-        fit = (fit and h.dtype is _HALF and h.get_device() == index and h.is_contiguous() and
-               h.numel() == m * n and h.size(-1) == n)
-        h_at = h.data_ptr()
-    if not fit:
-        lead = x[0].shape[:-1]
-        _mx_refuse(index, h=(h, _F16, (*lead, n)), codes=(codes, _CODES8, (*lead, n)),
-                   scales=(scales, _BYTES, (*lead, n // 32)))
-    rc = lib.qgemv_mx_swiglu(gc, gs, uc, us, xc, xs, m, n, k, h_at, c_at, s_at, _raw_stream(index))
-    if rc:
-        _check(rc, "qgemv_mx_swiglu")
-    return (codes, scales) if held else h
+            scales = torch.empty((*lead, gc.shape[0] // 32), dtype=_U8, device=xc.device)
+    rc = _calls.gated(gc, gs, uc, us, xc, xs, h, codes, scales)
+    if rc == 0:
+        return (codes, scales) if held else h
+    if rc is None:
+        tensors = _mx_weight(gate, "gate")
+        (lead, _), n, k = _mx_lead(xc, "x.codes"), gc.shape[0], 8 * gc.shape[1]
+        if uc.shape != gc.shape:
+            raise ValueError(f"up.codes has shape {tuple(uc.shape)}, gate.codes {tuple(gc.shape)}")
+        return _mx_unfit(mx_swiglu, (gate, up, x, h, codes, scales), "qgemv_mx_swiglu",
+                         **_mx_rows(x, k), **tensors, **_mx_weight(up, "up"),
+                         h=(h, _F16, (*lead, n)), codes=(codes, _CODES8, (*lead, n)),
+                         scales=(scales, _BYTES, (*lead, n // 32)))
+    _check(rc, "qgemv_mx_swiglu")
 
 
 def device_status() -> int:

@@ -1,8 +1,9 @@
 """Build libqgemv.so in-tree with nvcc for sm_103a (GB300).
 
 Each CUDA translation unit under ``csrc/`` is compiled in parallel to an
-object file in ``_build/``, then linked into ``_build/libqgemv.so``.  The
-build is skipped when the library is newer than every source and header.
+object file in ``_build/``, then linked into ``_build/libqgemv.so``; beside it
+``csrc/mx_calls.c`` becomes the CPython module ``_build/_mx_calls.so``.  The
+build is skipped when both are newer than every source and header.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqgemv.so")
+CALLS = os.path.join(BUILD, "_mx_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I", os.path.join(ROOT, "include")]
@@ -34,15 +37,15 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
             glob.glob(os.path.join(CSRC, "*.h")) +
             glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -64,8 +67,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stderr}")
         return obj, res.stderr
 
+    def compile_calls():
+        tmp = CALLS + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "mx_calls.c"), "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"gcc failed on mx_calls.c:\n{res.stderr}")
+        return tmp
+
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        calls = ex.submit(compile_calls)
         results = list(ex.map(compile_one, srcs))
     if verbose:
         for _, log in results:
@@ -75,6 +88,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
+    os.replace(calls.result(), CALLS)
     os.replace(tmp, LIB)
     return LIB
 
