@@ -8,6 +8,7 @@ constexpr int kMxStep = 128;      // k of a stage
 constexpr int kMxMinStages = 4, kMxMaxStages = 16;
 constexpr int kMxRowSteps = 64;   // steps of fp16 rows that a block holds, at most
 constexpr int kMxAccCols = 480;   // tensor memory of the accumulators (512 less the scales')
+constexpr int kMxOut = 16;        // columns that results are written by
 constexpr int kMxSplits[4] = {1, 2, 4, 8};
 constexpr int kMxSmem = 227 * 1024 - 1024;  // dynamic shared memory (the rest is static)
 
@@ -55,7 +56,8 @@ inline bool mx_fit(const MxShape& s, int cols, int split, MxPlan* p) {
   p->rows_first = 2 * s.M > w * s.N;
   if (split > steps || p->row_steps > kMxRowSteps || 2 * w * cols > kMxAccCols) return false;
   const int part = split > 1 ? w * ((p->tokens + split - 1) / split * split) * kMxRows * 4 : 0;
-  const int other = 1024 + part + p->row_steps * (cols * kMxStep + 512);
+  const int out = s.fp16 || s.gated || split > 1 ? 0 : 2 * kMxOut * kMxRows * 4;
+  const int other = 1024 + part + out + p->row_steps * (cols * kMxStep + 512);
   const int stage = mx_stage_bytes(w, cols, s.fp16);
   if (other > kMxSmem) return false;
   // Even, so that a stage is always filled and used by the same of two warps: a wait tells

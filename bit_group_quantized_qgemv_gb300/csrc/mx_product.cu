@@ -52,6 +52,7 @@ constexpr int kScaleCols = 16;  // tensor memory of one step's scales
 struct MxLoads {
   bool tma_w;  // weights by TMA
   int bytes;   // of a row's scales in one load: 16, 4 or 1
+  bool wide;   // four values of y and the residual in one access
 };
 
 struct Bars {
@@ -505,11 +506,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < C; ++c)
           byte[c] = mx_scale_byte<8>(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[c]) & 0x7FFFFFFFu)));
-        if (!live) return;
-        uint8_t* codes = a.yc + at;
+        if constexpr (C % 4 == 0) {
+          // Four columns' codes of four lanes' rows change places: a lane then has four rows of
+          // one column, and a warp's store 32 bytes of each of four.
+          const int sub = lane & 3;
+          uint8_t* to = a.yc + static_cast<long long>(m + sub) * a.N + (n & ~3);
 #pragma unroll
-        for (int c = 0; c < C; ++c, codes += a.N)
-          if (c < count) *codes = static_cast<uint8_t>(mx_codes8(v[c] * mx_inverse(byte[c]), 0.f));
+          for (int c = 0; c < C; c += 4, to += 4LL * a.N) {
+            uint32_t w = mx_codes8(v[c] * mx_inverse(byte[c]), v[c + 1] * mx_inverse(byte[c + 1])) |
+                         (mx_codes8(v[c + 2] * mx_inverse(byte[c + 2]), v[c + 3] * mx_inverse(byte[c + 3])) << 16);
+            uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+            w = sub & 1 ? __byte_perm(o, w, 0x7351) : __byte_perm(w, o, 0x6240);
+            o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+            w = sub & 2 ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+            if (live && c + sub < count) *reinterpret_cast<uint32_t*>(to) = w;
+          }
+        } else if (live) {
+          a.yc[at] = static_cast<uint8_t>(mx_codes8(v[0] * mx_inverse(byte[0]), 0.f));
+        }
+        if (!live) return;
         // lane c has the scale of row m + c
         int mine = byte[0];
 #pragma unroll
@@ -518,6 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.ys[static_cast<long long>(m + lane) * (a.N / kMxBlock) + n / kMxBlock] = static_cast<uint8_t>(mine);
       }
     };
+    // Where results lie before they are written in rows of x (after a wait that ran out the
+    // warps still meet at the barriers around this, and write nothing).
+    const uint32_t stage_out = part + half * (kMxOut * kRowsW * 4);
     const int share = (p.tokens + p.split - 1) / p.split;  // rows of x that a rank finishes, at most
     // Where rank q's sums for this rank's j-th row lie.
     auto part_at = [&](int q, int j, int w) {
@@ -550,63 +568,112 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (GATED) send(to + kRowsW * 4, u, bar);
       };
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
-      if (ok) {
-        if constexpr (SPLIT3) {
-          // four rows of x a warp: 12 columns
-          const int m0 = 4 * half, c0 = 12 * half;
-          if (m0 < count) {
-            float v[4];
-            uint32_t x0[16], x1[16];
-            tc::ld16(x0, acc + c0);
-            tc::ld16(x1, acc + p.cols + c0);
+      if constexpr (SPLIT3) {
+        // four rows of x a warp: 12 columns
+        const int m0 = 4 * half, c0 = 12 * half;
+        if (ok && m0 < count) {
+          float v[4];
+          uint32_t x0[16], x1[16];
+          tc::ld16(x0, acc + c0);
+          tc::ld16(x1, acc + p.cols + c0);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) v[m] = p.split == 1 && res && m0 + m < count ? residual(m0 + m) : 0.f;
-            tc::wait_ld16(x0);
-            tc::wait_ld16(x1);
+          for (int m = 0; m < 4; ++m) v[m] = p.split == 1 && res && m0 + m < count ? residual(m0 + m) : 0.f;
+          tc::wait_ld16(x0);
+          tc::wait_ld16(x1);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              float q[3];
+          for (int m = 0; m < 4; ++m) {
+            float q[3];
 #pragma unroll
-              for (int c = 0; c < 3; ++c)
-                q[c] = (has0 ? __uint_as_float(x0[3 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[3 * m + c]) : 0.f);
-              v[m] += (q[2] + q[1]) + q[0];
-            }
-            if (p.split == 1) {
-              finish(n, m0, count - m0, v);
-            } else {
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-                if (m0 + m < count) give(m0 + m, v[m], 0.f);
-            }
+            for (int c = 0; c < 3; ++c)
+              q[c] = (has0 ? __uint_as_float(x0[3 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[3 * m + c]) : 0.f);
+            v[m] += (q[2] + q[1]) + q[0];
           }
-        } else {
-          for (int c0 = half * 16; c0 < count; c0 += 32) {
-            uint32_t g[16], u[16];
-            tc::ld16(g, acc + c0);
-            const bool second = GATED || p.pair;
-            if (second) tc::ld16(u, acc + p.cols + c0);
-            float v[16];
-            if (!GATED) {
+          if (p.split == 1) {
+            finish(n, m0, count - m0, v);
+          } else {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) v[c] = p.split == 1 && res && c0 + c < count ? residual(c0 + c) : 0.f;
+            for (int m = 0; m < 4; ++m)
+              if (m0 + m < count) give(m0 + m, v[m], 0.f);
+          }
+        }
+      } else {
+        // Sixteen columns at a time, four warps to them.
+        auto sums = [&](int c0, float* g, float* u) {
+          uint32_t x0[16], x1[16];
+          const bool second = GATED || p.pair;
+          tc::ld16(x0, acc + c0);
+          if (second) tc::ld16(x1, acc + p.cols + c0);
+          tc::wait_ld16(x0);
+          if (second) tc::wait_ld16(x1);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float s0 = __uint_as_float(x0[c]), s1 = second ? __uint_as_float(x1[c]) : 0.f;
+            g[c] = GATED ? s0 : (has0 ? s0 : 0.f) + (has1 ? s1 : 0.f);
+            if constexpr (GATED) u[c] = s1;
+          }
+        };
+        for (int c0 = half * kMxOut; c0 < count; c0 += 2 * kMxOut) {
+          float g[16], u[GATED ? 16 : 1];
+          if (p.split > 1) {
+            sums(c0, g, u);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (ok && c0 + c < count) give(c0 + c, g[c], GATED ? u[c] : 0.f);
+            continue;
+          }
+          if constexpr (GATED) {
+            sums(c0, g, u);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) g[c] = silu_f(g[c]) * u[c];
+            if (ok) finish(n, tok + c0, count - c0, g);
+          } else if (ld.wide) {
+            // Through shared memory: each warp writes four rows of x, a lane four weight rows
+            // of each.
+            const int m0 = c0 + 4 * quarter, n4 = row + 4 * lane;
+            const long long at = static_cast<long long>(tok + m0) * a.N + n4;
+            const bool live = ok && n4 < a.N;
+            uint2 r[4] = {};
+            if (a.res != nullptr) {
+              // (all four under way together: rows and columns that there are not are others again)
+              const __half* from = a.res + static_cast<long long>(tok) * a.N + min(n4, a.N - 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                r[i] = *reinterpret_cast<const uint2*>(from + static_cast<long long>(min(m0 + i, count - 1)) * a.N);
             }
-            tc::wait_ld16(g);
-            if (second) tc::wait_ld16(u);
-            if (!GATED && second) {
+            sums(c0, g, u);
+            named_bar_sync(1 + half, 128);  // the last columns' values have been read
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                g[c] = __float_as_uint((has0 ? __uint_as_float(g[c]) : 0.f) + (has1 ? __uint_as_float(u[c]) : 0.f));
+            for (int c = 0; c < 16; ++c)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage_out + (c * kRowsW + quarter * 32 + lane) * 4),
+                           "f"(g[c])
+                           : "memory");
+            named_bar_sync(1 + half, 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v[4];
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                           : "r"(stage_out + ((4 * quarter + i) * kRowsW + 4 * lane) * 4)
+                           : "memory");
+              const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(&r[i].x));
+              const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(&r[i].y));
+              if (live && m0 + i < count)
+                *reinterpret_cast<uint2*>(a.y + at + static_cast<long long>(i) * a.N) =
+                    make_uint2(pack_f16(v[0] + a0.x, v[1] + a0.y), pack_f16(v[2] + a1.x, v[3] + a1.y));
             }
-            if (p.split == 1) {
+          } else {
+            __half r[16];
+            if (a.res != nullptr) {
+              const __half* from = a.res + static_cast<long long>(tok) * a.N + min(n, a.N - 1);
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                v[c] = GATED ? silu_f(__uint_as_float(g[c])) * __uint_as_float(u[c]) : __uint_as_float(g[c]) + v[c];
-              finish(n, tok + c0, count - c0, v);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (c0 + c < count) give(c0 + c, __uint_as_float(g[c]), GATED ? __uint_as_float(u[c]) : 0.f);
+              for (int c = 0; c < 16; ++c) r[c] = from[static_cast<long long>(min(c0 + c, count - 1)) * a.N];
             }
+            sums(c0, g, u);
+            if (a.res != nullptr) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) g[c] += __half2float(r[c]);
+            }
+            if (ok) finish(n, tok + c0, count - c0, g);
           }
         }
       }
@@ -750,6 +817,7 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
   ld.tma_w = a.K % kStepK == 0 && mod(a.w, 32) && (!GATED || mod(a.up, 32));
   const bool all16 = mod(a.ws, 16) && mod(a.us, 16) && mod(a.xs, 16);
   const bool all4 = mod(a.ws, 4) && mod(a.us, 4) && mod(a.xs, 4);
+  ld.wide = a.N % 4 == 0 && mod(a.y, 8) && mod(a.res, 8);
   ld.bytes = a.K % 512 == 0 && all16 ? 16 : a.K % kStepK == 0 && all4 ? 4 : 1;
   CUtensorMap wm{}, um{}, xm{};
   if (ld.tma_w && (!encode_codes(&wm, a.w, true, a.N, a.K, kRowsW) ||
