@@ -18,9 +18,10 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Rows of whole blocks whose number is countable by a grid.
+// Rows of whole blocks, whose number a grid can count, with room above every index.
 bool valid_rows(int M, int K) {
-  return M >= 0 && K >= 32 && K % 32 == 0 && static_cast<long long>(M) * K <= 1LL << 38;
+  return M >= 0 && M <= 1 << 30 && K >= 32 && K <= 1 << 30 && K % 32 == 0 &&
+         static_cast<long long>(M) * K <= 1LL << 38;
 }
 
 int product(qgemv::MxProductArgs& a, void* stream) {

@@ -86,25 +86,24 @@ inline double mx_cost(const MxShape& s, const MxPlan& p) {
 }
 
 // The plan that is expected to be fastest.  False: none fits (K too long for fp16 rows).
-inline bool mx_plan(const MxShape& s, MxPlan* best) {
-  const int w = s.gated ? 2 : 1;
+inline bool mx_plan(const MxShape& shape, MxPlan* best) {
+  // fp16 rows: one tile of them, and the split that is best for eight, so that a row's
+  // result does not depend on how many there are.
+  MxShape s = shape;
+  if (s.fp16) s.M = 8;
   double least = 0;
   bool any = false;
   for (int i = 0; i < 4; ++i) {
     if (s.clusters[i] < 1) continue;
-    // fp16 rows: one tile of them (the split is that of eight rows, so that a row's result
-    // does not depend on how many there are)
-    const int lo = s.fp16 ? 32 : 16, hi = s.fp16 ? 32 : kMxAccCols / (2 * w) / 16 * 16;
-    for (int cols = lo; cols <= hi; cols += 16) {
-      if (cols > lo && cols - 16 >= s.M) break;  // wider than the rows there are
+    for (int cols = s.fp16 ? 32 : 16; cols <= (s.fp16 ? 32 : 240); cols += 16) {
+      if (!s.fp16 && cols > 16 && cols - 16 >= s.M) break;  // wider than the rows there are
       MxPlan p;
       if (!mx_fit(s, cols, kMxSplits[i], &p)) continue;
       const double c = mx_cost(s, p);
       if (!any || c < least) least = c, *best = p, any = true;
     }
   }
-  if (any && s.fp16 && 3 * s.M <= 16) return mx_fit(s, 16, best->split, best);
-  return any;
+  return any && (!s.fp16 || mx_fit(shape, 3 * shape.M <= 16 ? 16 : 32, best->split, best));
 }
 
 }  // namespace qgemv

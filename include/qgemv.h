@@ -642,8 +642,8 @@ int qgemv_cache_evict(const qgemv_kv_cache *cache, const float *mass, const int3
  *           (the layout of qgemv_w4g64), e2m1: sign, 0 0.5 1 1.5 2 3 4 6
  *   MXFP8   codes uint8 [rows][K], e4m3: sign, up to 448; 0x7F and 0xFF are NaN
  *   scales  uint8 [rows][K/32]
- * Rows lie one behind the other, without gaps.  Checks of all: K >= 32, K % 32 == 0,
- * rows * K <= 2^38 (EINVAL); codes and fp16 rows that are read or written in whole
+ * Rows lie one behind the other, without gaps.  Checks of all: K >= 32, K % 32 == 0, rows and
+ * K <= 2^30, rows * K <= 2^38 (EINVAL); codes and fp16 rows that are read or written in whole
  * blocks (x, h of the norm, gamma, the values of qgemv_mx_dequantize) 16-byte aligned,
  * y, h of qgemv_mx_swiglu and residual 2-byte (EALIGN), scales any.  M = 0 rows: nothing is enqueued
  * and the arrays of rows may be NULL.  These kernels read nothing before the kernel

@@ -447,3 +447,113 @@ def test_refusals():
             call()
     with pytest.raises(q.QgemvError):
         q.residual_rmsnorm_mxfp8(x, torch.ones(64, device="cuda").half(), eps=0.0)
+
+
+# -------------------------------------------------------- the largest, and any
+
+def test_longest_fp16_rows():
+    k = 28672
+    w, x = weight(1, 33, k), rows16(2, 8, k, 0.05)
+    y = q.qgemv_mxfp4(dev(w), x.cuda())
+    want, tol = ref.product(w, x.double())
+    wide = x.double().unflatten(-1, (-1, 32)).abs().amax(-1).repeat_interleave(32, -1)
+    ref.near(y, want, tol + 2.0 ** -26 * (wide @ ref.values(*w).abs().T), "matvec")
+    assert torch.equal(q.qgemv_mxfp4(dev(w), x[2:4].cuda()), y[2:4])
+    with pytest.raises(q.QgemvError):
+        q.qgemv_mxfp4(dev(weight(1, 4, k + 32)), torch.zeros(1, k + 32, dtype=torch.float16, device="cuda"))
+
+
+def test_long_rows():
+    k = 70016                                                    # 547 steps, no multiple of 128
+    w, x = weight(3, 20, k), acts(4, 3, k)
+    want, tol = ref.product(w, ref.values(*x))
+    ref.near(q.mx_gemm(dev(w), dev(x)), want, tol, "product")
+    want, tol = ref.gated(want, tol, want, tol)
+    h = torch.zeros(3, 20, dtype=torch.float16, device="cuda")
+    ref.near(q.mx_swiglu(dev(w), dev(w), dev(x), h=h), want, tol, "gated")
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 values quantised, outputs and weights of more than 2^31 elements: the
+    last rows against the same rows alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    m, k = 140000, 32768
+    x = torch.empty(m, k, dtype=torch.float16, device="cuda")
+    x[-300:] = torch.randn(300, k, generator=g, device="cuda").half()
+    x[:-300] = 1.0
+    for bits in (4, 8):
+        c, s = q.mx_quantize(x, bits)
+        c2, s2 = q.mx_quantize(x[-300:].contiguous(), bits)
+        assert torch.equal(c[-300:], c2) and torch.equal(s[-300:], s2) and int((s[:-300] != s[0, 0]).sum()) == 0
+        v = q.mx_dequantize(c, s)
+        assert torch.equal(v[-300:], q.mx_dequantize(c2, s2))
+        del v
+    h, nc, ns = q.residual_rmsnorm_mxfp8(x, torch.ones(k, device="cuda").half(), x)
+    _, nc2, ns2 = q.residual_rmsnorm_mxfp8(x[-300:].contiguous(), torch.ones(k, device="cuda").half(), x[-300:].contiguous())
+    assert torch.equal(nc[-300:], nc2) and torch.equal(ns[-300:], ns2)
+    del h, nc, ns, x
+    # weights of 2^32 codes, one row of x
+    w = (c[:, :4096], s) if bits == 4 else q.mx_quantize(torch.randn(300, k, generator=g, device="cuda").half(), 4)
+    big = (w[0].repeat(470, 1), w[1].repeat(470, 1))
+    xs = q.mx_quantize(torch.randn(2, k, generator=g, device="cuda").half())
+    y, y2 = q.mx_gemm(big, xs), q.mx_gemm(w, xs)
+    assert big[0].numel() * 8 > 1 << 32
+    near = (y[:, -300:].float() - y2.float()).abs().max() <= 2e-3 * y2.float().abs().max()
+    assert bool(near) and torch.equal(y[:, :300], y[:, 300:600])
+    del big, y
+    # outputs of 2^31 elements and more
+    n, m, k = 50000, 45000, 32
+    w = q.mx_quantize(torch.randn(n, k, generator=g, device="cuda").half(), 4)
+    xs = q.mx_quantize(torch.randn(m, k, generator=g, device="cuda").half())
+    y = q.mx_gemm(w, xs)
+    last = q.mx_gemm(w, (xs[0][-50:].contiguous(), xs[1][-50:].contiguous()))
+    assert y.numel() > 1 << 31 and torch.equal(y[-50:], last)
+    q.mx_gemm(w, xs, residual=y, y=y)
+    assert torch.equal(y[-50:], q.mx_gemm(w, (xs[0][-50:].contiguous(), xs[1][-50:].contiguous()), residual=last))
+    del y
+    nn = n // 32 * 32
+    w = (w[0][:nn].contiguous(), w[1][:nn].contiguous())
+    c, s = q.mx_swiglu(w, w, xs)
+    c2, s2 = q.mx_swiglu(w, w, (xs[0][-50:].contiguous(), xs[1][-50:].contiguous()))
+    assert torch.equal(c[-50:], c2) and torch.equal(s[-50:], s2)
+    assert q.device_status() == 0
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_any_size(seed):
+    import random
+    r = random.Random(seed)
+    n, k = int(2 ** r.uniform(0, 10.5)), 32 * int(2 ** r.uniform(0, 7))
+    m = int(2 ** r.uniform(0, 9.5))
+    w, x = weight(seed, n, k), acts(seed, m, k)
+    res = rows16(seed, m, n) if r.random() < 0.5 else None
+    want, tol = ref.product(w, ref.values(*x))
+    y = q.mx_gemm(dev(w), dev(x), residual=None if res is None else res.cuda())
+    extra = 0 if res is None else res.double()
+    ref.near(y, want + extra, tol + 2.0 ** -23 * (want + extra).abs(), "product")
+    u = weight(seed + 100, n, k)
+    want, tol = ref.gated(want, tol, *ref.product(u, ref.values(*x)))
+    if n % 32 == 0:
+        c, s = q.mx_swiglu(dev(w), dev(u), dev(x))
+        ref.check_mx8(c.cpu(), s.cpu(), want, tol, "gated")
+    else:
+        ref.near(q.mx_swiglu(dev(w), dev(u), dev(x), h=torch.zeros(m, n, dtype=torch.float16, device="cuda")), want, tol, "gated")
+    x16 = rows16(seed, min(m, 8), k)
+    want, tol = ref.product(w, x16.double())
+    wide = x16.double().unflatten(-1, (-1, 32)).abs().amax(-1).repeat_interleave(32, -1)
+    ref.near(q.qgemv_mxfp4(dev(w), x16.cuda()), want, tol + 2.0 ** -26 * (wide @ ref.values(*w).abs().T), "matvec")
+
+
+def test_cluster_and_ring_sizes():
+    """Few tiles and long rows: the ways K is shared, with rows of x from one to a tile's."""
+    for m, n, k in ((1, 96, 8192), (8, 224, 16384), (16, 128, 14336), (40, 160, 9216), (64, 128, 4096)):
+        w, u, x = weight(m, n, k, 1), weight(m + 1, n, k, 1), acts(m, m, k)
+        x = (x[0], (x[1].int() - 4).clamp(min=0).to(torch.uint8))
+        xv = ref.values(*x)
+        g, tg = ref.product(w, xv)
+        ref.near(q.mx_gemm(dev(w), dev(x)), g, tg, f"product {m} {n} {k}")
+        want, tol = ref.gated(g, tg, *ref.product(u, xv))
+        c, s = q.mx_swiglu(dev(w), dev(u), dev(x))
+        ref.check_mx8(c.cpu(), s.cpu(), want, tol, f"gated {m} {n} {k}")
+    assert q.device_status() == 0
