@@ -111,23 +111,33 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ta
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// The aligned word at p, of which only what lies in [from, to) is read (0 elsewhere).
-__device__ __forceinline__ uint32_t word_within(const uint8_t* p, const uint8_t* from, const uint8_t* to) {
-  if (p >= from && p + 4 <= to) return *reinterpret_cast<const uint32_t*>(p);
+// An array of bytes that starts and ends anywhere, read by aligned words: those that it only
+// shares are put together from its bytes once (Ends), and loads of the others stay inside, so
+// that they can all be under way together.
+struct Ends {
+  uint32_t head, tail;  // the words that hold its first and its last bytes, where those are not whole
+};
+
+__device__ __forceinline__ uint32_t shared_word(const uint8_t* p, const uint8_t* from, const uint8_t* to) {
   uint32_t w = 0;
-#pragma unroll
   for (int i = 0; i < 4; ++i)
     if (p + i >= from && p + i < to) w |= static_cast<uint32_t>(p[i]) << (8 * i);
   return w;
 }
+__device__ __forceinline__ const uint8_t* first_whole(const uint8_t* from) {
+  return from + (-reinterpret_cast<uintptr_t>(from) & 3);
+}
+__device__ __forceinline__ const uint8_t* behind_whole(const uint8_t* to) {
+  return to - (reinterpret_cast<uintptr_t>(to) & 3);
+}
+__device__ __forceinline__ Ends ends_of(const uint8_t* from, const uint8_t* to) {
+  return Ends{shared_word(first_whole(from) - 4, from, to), shared_word(behind_whole(to), from, to)};
+}
 
-// Sixteen scale bytes at s, wherever it lies; what is not in [from, to) is not read, and
-// bytes from the n-th on are 0.
-__device__ __forceinline__ uint4 scales_unaligned(const uint8_t* s, int n, const uint8_t* from, const uint8_t* to) {
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 3);
-  uint32_t raw[5], w[4];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) raw[i] = 4 * i < n + off ? word_within(s - off + 4 * i, from, to) : 0;
+// Sixteen bytes from five aligned words, the first of which starts `off` before them; those
+// from the n-th on are 0.
+__device__ __forceinline__ uint4 shifted(const uint32_t* raw, int off, int n) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     w[i] = __funnelshift_r(raw[i], raw[i + 1], 8 * off);
@@ -135,6 +145,30 @@ __device__ __forceinline__ uint4 scales_unaligned(const uint8_t* s, int n, const
     if (left < 4) w[i] &= left <= 0 ? 0u : (1u << (8 * left)) - 1;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sixteen bytes at s: anywhere, with three bytes of the array before them and 20 behind.
+__device__ __forceinline__ uint4 sixteen_within(const uint8_t* s, int n) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 3);
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(s - off);
+  uint32_t raw[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) raw[i] = p[i];
+  return shifted(raw, off, n);
+}
+
+// Sixteen bytes at s, a place in the array; those from the n-th on are 0.
+__device__ __forceinline__ uint4 sixteen(const uint8_t* s, int n, const uint8_t* from, const uint8_t* to, Ends ends) {
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(s) & 3);
+  const uint8_t *first = first_whole(from), *last = behind_whole(to) - 4;  // whole words, if first <= last
+  uint32_t raw[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const uint8_t *p = s - off + 4 * i, *at = p < first ? first : p > last ? last : p;
+    raw[i] = first <= last ? *reinterpret_cast<const uint32_t*>(at) : 0;
+    raw[i] = p < first ? ends.head : p > last ? (p == last + 4 ? ends.tail : 0) : raw[i];
+  }
+  return shifted(raw, off, n);
 }
 
 // Place of row r's word among the scales of a step.
@@ -383,6 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int me = warp - kLoadWarp, blocks = a.K / kMxBlock, my_steps = k1 - k0;
     const int q0 = k0 >> 2, groups = ((k1 - 1) >> 2) - q0 + 1;  // of four steps, of a tile
     const long long all = first < tiles ? ((tiles - 1 - first) / stride + 1) * groups : 0;
+    Ends w_ends = {}, u_ends = {}, x_ends = {};
+    if (ld.bytes == 1) {
+      w_ends = ends_of(a.ws, a.ws + static_cast<long long>(a.N) * blocks);
+      if (GATED) u_ends = ends_of(a.us, a.us + static_cast<long long>(a.N) * blocks);
+      if (!SPLIT3) x_ends = ends_of(a.xs, a.xs + static_cast<long long>(a.M) * blocks);
+    }
     for (long long g = me; g < all; g += kLoaders) {
       const long long turn = g / groups;
       const int q = q0 + static_cast<int>(g % groups), from = max(k0, 4 * q), to = min(k1, 4 * q + 4);
@@ -391,38 +431,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Scales of rows lane, lane + 32, ... of each operand: of the group's four steps.  (All
       // loads of a kind in one go, so that they are under way together.)
       uint4 vw[4], vu[GATED ? 4 : 1], vx[kRowsX ? kRowsX : 1];
-      auto load_all = [&](auto load) {
+      auto load_all = [&](auto load) {  // load(operand, row of the tile, 0: no row of it is there)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = load(a.ws, row + lane + 32 * i, a.N);
+        for (int i = 0; i < 4; ++i) vw[i] = load(0, row + lane + 32 * i, a.N);
         if constexpr (GATED) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vu[i] = load(a.us, row + lane + 32 * i, a.N);
+          for (int i = 0; i < 4; ++i) vu[i] = load(1, row + lane + 32 * i, a.N);
         }
 #pragma unroll
         for (int i = 0; i < kRowsX; ++i)  // (rows of the next tile are loaded too, and not used)
-          vx[i] = load(a.xs, tok + lane + 32 * i, 32 * i < p.tokens ? a.M : 0);
+          vx[i] = load(2, tok + lane + 32 * i, 32 * i < p.tokens ? a.M : 0);
       };
-      auto at = [&](const uint8_t* scales, int r) { return scales + static_cast<long long>(r) * blocks + 16 * q; };
+      auto base_of = [&](int operand) { return operand == 0 ? a.ws : operand == 1 ? a.us : a.xs; };
+      auto at = [&](int operand, int r) { return base_of(operand) + static_cast<long long>(r) * blocks + 16 * q; };
       if (ld.bytes == 16) {
-        load_all([&](const uint8_t* scales, int r, int end) {
-          return r < end ? *reinterpret_cast<const uint4*>(at(scales, r)) : make_uint4(0, 0, 0, 0);
+        load_all([&](int operand, int r, int end) {
+          return r < end ? *reinterpret_cast<const uint4*>(at(operand, r)) : make_uint4(0, 0, 0, 0);
         });
       } else if (ld.bytes == 4) {
-        load_all([&](const uint8_t* scales, int r, int end) {
+        load_all([&](int operand, int r, int end) {
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             w[j] = r < end && 4 * q + j >= from && 4 * q + j < to
-                       ? *reinterpret_cast<const uint32_t*>(at(scales, r) + 4 * j)
+                       ? *reinterpret_cast<const uint32_t*>(at(operand, r) + 4 * j)
                        : 0;
           return make_uint4(w[0], w[1], w[2], w[3]);
         });
       } else {
-        load_all([&](const uint8_t* scales, int r, int end) {
-          return r < end ? scales_unaligned(at(scales, r), min(16, blocks - 16 * q), scales,
-                                            scales + static_cast<long long>(end) * blocks)
-                         : make_uint4(0, 0, 0, 0);
-        });
+        // Tiles away from the ends of an operand's scales need no look at them.
+        const int x_rows = p.tokens > 128 ? 256 : 128, n = min(16, blocks - 16 * q);
+        auto inside = [&](int r, int rows, int end) {
+          return r > 0 && static_cast<long long>(r) * blocks >= 3 && r + rows < end &&
+                 static_cast<long long>(end - r - rows) * blocks >= 20;
+        };
+        if (inside(row, kRowsW, a.N) && (SPLIT3 || inside(tok, x_rows, a.M))) {
+          load_all([&](int operand, int r, int end) { return sixteen_within(at(operand, end > 0 ? r : tok), n); });
+        } else {
+          load_all([&](int operand, int r, int end) {
+            if (r >= end) return make_uint4(0, 0, 0, 0);
+            const uint8_t* start = base_of(operand);
+            return sixteen(at(operand, r), n, start,
+                           start + static_cast<long long>(operand == 2 ? a.M : a.N) * blocks,
+                           operand == 0 ? w_ends : operand == 1 ? u_ends : x_ends);
+          });
+        }
       }
       // One group after the other: a wait for a stage tells a use from the one before it,
       // not from two before.
@@ -597,34 +650,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        // Sixteen columns at a time, four warps to them.
+        // Some columns at a time, four warps to them (eight where there is more to do for each,
+        // so that both fours have some of a tile of sixteen).
+        constexpr int C = GATED ? 8 : kMxOut;
         auto sums = [&](int c0, float* g, float* u) {
-          uint32_t x0[16], x1[16];
+          uint32_t x0[C], x1[C];
           const bool second = GATED || p.pair;
-          tc::ld16(x0, acc + c0);
-          if (second) tc::ld16(x1, acc + p.cols + c0);
-          tc::wait_ld16(x0);
-          if (second) tc::wait_ld16(x1);
+          if constexpr (C == 8) {
+            tc::ld8(x0, acc + c0);
+            tc::ld8(x1, acc + p.cols + c0);
+            tc::wait_ld8(x0);
+            tc::wait_ld8(x1);
+          } else {
+            tc::ld16(x0, acc + c0);
+            if (second) tc::ld16(x1, acc + p.cols + c0);
+            tc::wait_ld16(x0);
+            if (second) tc::wait_ld16(x1);
+          }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < C; ++c) {
             const float s0 = __uint_as_float(x0[c]), s1 = second ? __uint_as_float(x1[c]) : 0.f;
             g[c] = GATED ? s0 : (has0 ? s0 : 0.f) + (has1 ? s1 : 0.f);
             if constexpr (GATED) u[c] = s1;
           }
         };
-        for (int c0 = half * kMxOut; c0 < count; c0 += 2 * kMxOut) {
-          float g[16], u[GATED ? 16 : 1];
+        for (int c0 = half * C; c0 < count; c0 += 2 * C) {
+          float g[C], u[GATED ? C : 1];
           if (p.split > 1) {
             sums(c0, g, u);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < C; ++c)
               if (ok && c0 + c < count) give(c0 + c, g[c], GATED ? u[c] : 0.f);
             continue;
           }
           if constexpr (GATED) {
             sums(c0, g, u);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) g[c] = silu_f(g[c]) * u[c];
+            for (int c = 0; c < C; ++c) g[c] = silu_f(g[c]) * u[c];
             if (ok) finish(n, tok + c0, count - c0, g);
           } else if (ld.wide) {
             // Through shared memory: each warp writes four rows of x, a lane four weight rows

@@ -116,7 +116,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
-// 32 (16) columns of this warp's 32 lanes, one lane per thread.  The registers of
+// 32 (16, 8) columns of this warp's 32 lanes, one lane per thread.  The registers of
 // a load are valid after the wait that names them.
 __device__ __forceinline__ void ld32(uint32_t* r, uint32_t addr) {
   asm volatile(
@@ -154,6 +154,20 @@ __device__ __forceinline__ void ld16(uint32_t* r, uint32_t addr) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void ld8(uint32_t* r, uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld8(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
