@@ -1,6 +1,8 @@
 // mx_plan.h -- how a product with MXFP4 weights is cut into tiles (host only, no CUDA).
 #pragma once
 
+#include <initializer_list>
+
 namespace qgemv {
 
 constexpr int kMxRows = 128;      // weight rows of a tile
@@ -68,21 +70,31 @@ inline bool mx_fit(const MxShape& s, int cols, int split, MxPlan* p) {
   return p->stages >= kMxMinStages;
 }
 
-// Clocks that a plan is expected to take.
+// Clocks that a plan is expected to take.  A step of a tile is bound by shared memory (what
+// the copies write, weights spread to bytes, and what the products read, x once for each
+// weight), L2, the tensor core, or the waits and the issue of products (shorter where two
+// accumulators take them in turn); a tile by its steps or by the results of the one before.
+// The rates are fitted to 33 products of 9 to 8192 rows and 16 of 1 to 8 fp16 rows, each in
+// all widths and splits: what this takes was the fastest or within 2% of it in 44 of them, 5
+// to 11% slower in five.
 inline double mx_cost(const MxShape& s, const MxPlan& p) {
   const int w = s.gated ? 2 : 1, steps = (s.K + kMxStep - 1) / kMxStep;
   int i = 0;
   while (kMxSplits[i] != p.split) ++i;
   const double tiles = static_cast<double>(p.row_tiles) * p.tok_tiles, clusters = s.clusters[i];
   const double rounds = static_cast<double>(static_cast<long long>((tiles + clusters - 1) / clusters));
-  const double pipe = w * 4.0 * (p.cols / 2.0 > 32 + p.cols / 4.0 ? p.cols / 2.0 : 32 + p.cols / 4.0);
-  const double issue = s.gated || !p.pair ? 550 : 330;
-  const double bytes = (w * 8704.0 + (s.fp16 ? 0 : p.cols * 132.0)) / 32;
-  double step = pipe > issue ? pipe : issue;
-  if (bytes > step) step = bytes;
-  const double per_tile = ((steps + p.split - 1) / p.split) * step;
-  const double out = 400 + p.tokens * w * 8.0 + (p.split > 1 ? 2000 + 700 * i + p.tokens * w * 60.0 : 0);
-  return rounds * (per_tile > out ? per_tile : out) + out;
+  const int part = (steps + p.split - 1) / p.split;  // steps of a block
+  double step, out, fill;
+  if (s.fp16) {
+    step = 420, out = 1200 + (p.split > 1 ? 1000 + 110 * i : 0), fill = 4800;
+  } else {
+    const double cols = p.cols, smem = w * kMxRows * 1.32 + (1 + w) * cols, l2 = (w * 8704 + cols * 132) / 63;
+    const double tensor = w * 4 * (cols / 2 > 32 + cols / 4 ? cols / 2 : 32 + cols / 4);
+    step = p.pair ? 360 : 560;
+    for (const double least : {smem, l2, tensor}) step = step > least ? step : least;
+    out = 2100 + w * cols * (s.gated ? 24 : 17.5) + (p.split > 1 ? 1300 + 160 * i + w * cols * 62 : 0), fill = 6300;
+  }
+  return rounds * (part * step > out ? part * step : out) + out + fill;
 }
 
 // The plan that is expected to be fastest.  False: none fits (K too long for fp16 rows).
@@ -104,6 +116,52 @@ inline bool mx_plan(const MxShape& shape, MxPlan* best) {
     }
   }
   return any && (!s.fp16 || mx_fit(shape, 3 * shape.M <= 16 ? 16 : 32, best->split, best));
+}
+
+// Tiles of two blocks that share them (mx_pair.cu): 256 rows of weights (gated: 128 of each
+// of the two), the columns half in each block.
+struct MxPairPlan {
+  int cols, stages;
+  int row_tiles, tok_tiles;
+  bool rows_first;
+  int smem;
+};
+
+inline bool mx_pair_fit(const MxShape& s, int cols, MxPairPlan* p) {
+  const int rows = s.gated ? 128 : 256;
+  p->cols = cols;
+  p->row_tiles = static_cast<int>((s.N + rows - 1) / rows);
+  p->tok_tiles = static_cast<int>((s.M + cols - 1) / cols);
+  p->rows_first = 2 * s.M > (s.gated ? 2 : 1) * s.N;
+  const int other = 1024 + 2 * kMxOut * kMxRows * 4;
+  const int stage = kMxRows * kMxStep + cols / 2 * kMxStep + 512 * (cols > 128 ? 3 : 2);
+  p->stages = (kMxSmem - other) / stage;
+  p->stages = (p->stages > kMxMaxStages ? kMxMaxStages : p->stages) / 2 * 2;
+  p->smem = other + p->stages * stage;
+  return cols % 32 == 0 && 2 * cols + 32 <= 512 && p->stages >= kMxMinStages;
+}
+
+inline double mx_pair_cost(const MxShape& s, const MxPairPlan& p) {
+  const int steps = s.K / kMxStep;
+  const double tiles = static_cast<double>(p.row_tiles) * p.tok_tiles, clusters = s.clusters[1];
+  const double rounds = static_cast<double>(static_cast<long long>((tiles + clusters - 1) / clusters));
+  const double tensor = 100 + 2.1 * p.cols, step = tensor > 330 ? tensor : 330;
+  const double per_tile = steps * step, out = 1500 + p.cols * (s.gated ? 33.5 : 15);
+  return rounds * (per_tile > out ? per_tile : out) + out + 4000;
+}
+
+// The best of them; false: none (no clusters of two, or K is no whole number of steps).
+inline bool mx_pair_plan(const MxShape& s, MxPairPlan* best, double* cost) {
+  bool any = false;
+  if (s.fp16 || s.clusters[1] < 1 || s.K % kMxStep != 0) return false;
+  for (int cols = 64; cols <= 224; cols += 32) {
+    if (cols > 64 && cols - 32 >= s.M) break;
+    MxPairPlan p;
+    if (!mx_pair_fit(s, cols, &p)) continue;
+    const double c = mx_pair_cost(s, p);
+    if (!any || c < *cost) *cost = c, *best = p, any = true;
+  }
+  return any;
 }
 
 }  // namespace qgemv

@@ -30,13 +30,7 @@
 // column, adding the others' sums, sent to its shared memory, in rank order.
 #include <atomic>
 
-#include "kv_cache.cuh"
-#include "mma_tile.cuh"
-#include "mx.h"
-#include "mx_format.cuh"
-#include "mx_plan.h"
-#include "tcgen05.cuh"
-#include "tensor_map.h"
+#include "mx_product.cuh"
 
 namespace qgemv {
 namespace {
@@ -62,40 +56,6 @@ struct Bars {
   uint64_t acc_full[2], acc_empty[2];
   uint64_t part_full, part_done;
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// A value to another block's shared memory, its bytes counted on a barrier there.
-__device__ __forceinline__ void send(uint32_t addr, float v, uint32_t bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
-               "r"(__float_as_uint(v)), "r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void fence_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-}
-// (relaxed: the barriers' initialisation has a fence of its own)
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
 
 // An arrival on the mbarrier once this thread's copies so far are done; the barrier's
 // count has it already.
@@ -173,10 +133,6 @@ __device__ __forceinline__ uint4 sixteen(const uint8_t* s, int n, const uint8_t*
 
 // Place of row r's word among the scales of a step.
 __device__ __forceinline__ int scale_at(int r) { return (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4; }
-
-__device__ __forceinline__ void store_shared(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 
 // Warps by what they do.
 constexpr int kOutWarps = 8, kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders,
@@ -541,51 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars.rows[i]));
       }
     }
-    // Finished values of weight row n and rows m, m + 1, ... of x (count of them).
-    auto finish = [&](int n, int m, int count, auto& v) {
-      constexpr int C = sizeof(v) / sizeof(float);
-      const bool live = n < a.N;
-      const long long at = static_cast<long long>(m) * a.N + n;
-      if (a.y != nullptr && live) {
-        __half* y = a.y + at;
-#pragma unroll
-        for (int c = 0; c < C; ++c, y += a.N)
-          if (c < count) *y = __float2half_rn(v[c]);
-      }
-      if constexpr (GATED) {
-        if (a.yc == nullptr) return;
-        // (N is a multiple of 32: a warp's rows are one block of the output, all there or none)
-        int byte[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          byte[c] = mx_scale_byte<8>(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v[c]) & 0x7FFFFFFFu)));
-        if constexpr (C % 4 == 0) {
-          // Four columns' codes of four lanes' rows change places: a lane then has four rows of
-          // one column, and a warp's store 32 bytes of each of four.
-          const int sub = lane & 3;
-          uint8_t* to = a.yc + static_cast<long long>(m + sub) * a.N + (n & ~3);
-#pragma unroll
-          for (int c = 0; c < C; c += 4, to += 4LL * a.N) {
-            uint32_t w = mx_codes8(v[c] * mx_inverse(byte[c]), v[c + 1] * mx_inverse(byte[c + 1])) |
-                         (mx_codes8(v[c + 2] * mx_inverse(byte[c + 2]), v[c + 3] * mx_inverse(byte[c + 3])) << 16);
-            uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-            w = sub & 1 ? __byte_perm(o, w, 0x7351) : __byte_perm(w, o, 0x6240);
-            o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
-            w = sub & 2 ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
-            if (live && c + sub < count) *reinterpret_cast<uint32_t*>(to) = w;
-          }
-        } else if (live) {
-          a.yc[at] = static_cast<uint8_t>(mx_codes8(v[0] * mx_inverse(byte[0]), 0.f));
-        }
-        if (!live) return;
-        // lane c has the scale of row m + c
-        int mine = byte[0];
-#pragma unroll
-        for (int c = 1; c < C; ++c) mine = lane == c ? byte[c] : mine;
-        if (lane < C && lane < count)
-          a.ys[static_cast<long long>(m + lane) * (a.N / kMxBlock) + n / kMxBlock] = static_cast<uint8_t>(mine);
-      }
-    };
     // Where results lie before they are written in rows of x (after a wait that ran out the
     // warps still meet at the barriers around this, and write nothing).
     const uint32_t stage_out = part + half * (kMxOut * kRowsW * 4);
@@ -642,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[m] += (q[2] + q[1]) + q[0];
           }
           if (p.split == 1) {
-            finish(n, m0, count - m0, v);
+            write_results<GATED>(a, n, m0, count - m0, v, lane);
           } else {
 #pragma unroll
             for (int m = 0; m < 4; ++m)
@@ -686,8 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (GATED) {
             sums(c0, g, u);
 #pragma unroll
-            for (int c = 0; c < C; ++c) g[c] = silu_f(g[c]) * u[c];
-            if (ok) finish(n, tok + c0, count - c0, g);
+            for (int c = 0; c < C; ++c) g[c] = mx_silu(g[c]) * u[c];
+            if (ok) write_results<GATED>(a, n, tok + c0, count - c0, g, lane);
           } else if (ld.wide) {
             // Through shared memory: each warp writes four rows of x, a lane four weight rows
             // of each.
@@ -735,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c) g[c] += __half2float(r[c]);
             }
-            if (ok) finish(n, tok + c0, count - c0, g);
+            if (ok) write_results<GATED>(a, n, tok + c0, count - c0, g, lane);
           }
         }
       }
@@ -763,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[0] = g[0];
 #pragma unroll
           for (int q = 1; q < 8; ++q) v[0] += g[q], w += u[q];
-          v[0] = GATED ? silu_f(v[0]) * w : v[0] + r;
-          finish(n, tok + m, 1, v);
+          v[0] = GATED ? mx_silu(v[0]) * w : v[0] + r;
+          write_results<GATED>(a, n, tok + m, 1, v, lane);
         }
       }
       __syncwarp();
@@ -793,19 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- host
-
-bool encode_codes(CUtensorMap* m, const void* p, bool four, long long rows, int k, int box_rows) {
-  const EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(four ? k / 2 : k)};
-  const cuuint32_t box[2] = {kStepK, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estride[2] = {1, 1};
-  return fn(m, four ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-            const_cast<void*>(p), dim, stride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // Clusters of 1 << log2 blocks that the device runs at a time, asked once per kernel,
 // size and device (0 where it cannot).
@@ -838,25 +736,29 @@ int clusters_at_a_time(F* k, int log2, int sms, int device) {
   return n - 1;
 }
 
-// The plan of a shape; a thread keeps those that it met last (a search takes a few
-// microseconds, as long as all else of a call).
-bool known_plan(const MxShape& s, MxPlan* p) {
-  struct Known {
-    MxShape shape;
-    MxPlan plan;
-  };
-  static thread_local Known known[32] = {};
+// The plans of a shape, and whether pairs of blocks are expected to be faster; a thread
+// keeps those that it met last (a search takes a few microseconds, as long as all else of a
+// call).
+struct Plans {
+  MxShape shape;
+  MxPlan plan;
+  MxPairPlan pair;
+  bool by_pairs;
+};
+
+const Plans* known_plans(const MxShape& s) {
+  static thread_local Plans known[32] = {};
   const unsigned long long h = (static_cast<unsigned long long>(s.M) * 0x9E3779B97F4A7C15ull) ^
                                (static_cast<unsigned long long>(s.N) * 0xC2B2AE3D27D4EB4Full) ^
                                (static_cast<unsigned long long>(s.K) * 0x165667B19E3779F9ull);
-  Known& at = known[(h >> 40) % 32];
-  if (at.shape == s) {
-    *p = at.plan;
-    return true;
-  }
-  if (!mx_plan(s, p)) return false;
-  at = Known{s, *p};
-  return true;
+  Plans& at = known[(h >> 40) % 32];
+  if (at.shape == s) return &at;
+  Plans p{s, {}, {}, false};
+  if (!mx_plan(s, &p.plan)) return nullptr;
+  double cost = 0;
+  p.by_pairs = mx_pair_plan(s, &p.pair, &cost) && cost < mx_cost(s, p.plan);
+  at = p;
+  return &at;
 }
 
 template <bool GATED, bool SPLIT3>
@@ -872,8 +774,10 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
   }
   MxShape shape{a.M, a.N, a.K, GATED, SPLIT3, {}};
   for (int i = 0; i < 4; ++i) shape.clusters[i] = clusters_at_a_time(k, i, sms, device);
-  MxPlan p{};
-  if (!known_plan(shape, &p)) return cudaErrorInvalidValue;
+  const Plans* plans = known_plans(shape);
+  if (plans == nullptr) return cudaErrorInvalidValue;
+  if (plans->by_pairs && mx_pair_takes(a)) return mx_pair_launch(a, plans->pair, shape.clusters[1], device, st);
+  const MxPlan p = plans->plan;
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };
   MxLoads ld;
   ld.tma_w = a.K % kStepK == 0 && mod(a.w, 32) && (!GATED || mod(a.up, 32));
@@ -918,7 +822,7 @@ cudaError_t status_mx(unsigned* out) {
   if (e != cudaSuccess) return e;
   e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
   *out |= v;
-  return e;
+  return e == cudaSuccess ? status_mx_pair(out) : e;
 }
 
 }  // namespace qgemv

@@ -86,9 +86,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 // Block-scaled products of 8-, 6- and 4-bit floats (kind::mxf8f6f4; 4-bit codes lie in
 // shared memory sixteen to 16 bytes, in the first eight of them).  Instruction
-// descriptor: A e2m1, B e4m3, both K-major, ue8m0 scales, one per 32 k, M = 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_mx(int n) {
-  return (5u << 7) | (static_cast<uint32_t>(n / 8) << 17) | (1u << 23) | (1u << 27);
+// descriptor: A e2m1, B e4m3, both K-major, ue8m0 scales, one per 32 k, M = m, N = n.
+__host__ __device__ constexpr uint32_t idesc_mx(int n, int m = 128) {
+  return (5u << 7) | (static_cast<uint32_t>(n / 8) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m / 16) << 24);
 }
 // `byte`: which of the four scales in the words at sa, sb is that of this product's 32 k.
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int byte,
@@ -108,6 +109,40 @@ __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
   const uint64_t desc =
       static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+// The same for a cluster of two blocks whose tensor cores work on one product of M = 256:
+// each block has 128 rows of A, half of the columns of B, and 128 rows of D, at the same
+// addresses; scales are copied from and to both, all columns' in each.  The block of rank 0
+// issues; a commit arrives on both blocks' mbarrier.  A whole warp of each block allocates
+// and frees.
+__device__ __forceinline__ void alloc_pair(uint32_t dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int byte,
+                                            uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  const uint32_t id = idesc | (static_cast<uint32_t>(byte) << 29) | (static_cast<uint32_t>(byte) << 4);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+      " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t smem) {
+  const uint64_t desc =
+      static_cast<uint64_t>((smem & 0x3FFFF) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 // One arrival on the mbarrier once every product issued so far is done.
 __device__ __forceinline__ void commit(uint32_t bar) {

@@ -113,6 +113,13 @@ def product(w, x):
     return y, 2.0 ** -20 * size
 
 
+# Products (rows of x, rows of weights, K, two weights) that pairs of thread blocks work on: some
+# tiles of a block, sizes that no tile divides, K of whole and of parts of the loaders' 512.
+PAIRS = [(777, 2051, 1024, 0), (1500, 5000, 256, 0), (2100, 8000, 128, 0), (333, 2500, 1152, 0), (225, 30000, 128, 0),
+         (1000, 513, 4096, 0), (1000, 2048, 2048, 1), (300, 1440, 512, 1), (100, 2816, 1024, 1), (3000, 2016, 2048, 1),
+         (640, 1001, 896, 1)]
+
+
 def gated(g, tg, u, tu):
     """silu(g) u and its error for g, u off by tg, tu: |silu'| <= 1.1, |silu(g)| <= |g|;
     expf, the division and the products take a few 2^-24 of the result, 2^-20 in all (and

@@ -212,6 +212,39 @@ def test_many_tiles(m, n, k):
         ref.near(q.qgemv_mxfp4(dev(w), x16.cuda()), want, tol + 2.0 ** -20 * want.abs().max(), "matvec")
 
 
+@pytest.mark.parametrize("m,n,k,gated", ref.PAIRS)
+def test_pairs_of_blocks(m, n, k, gated):
+    """Products that two thread blocks share, whose last tiles have rows and columns that there are not."""
+    w, x = weight(m + n, n, k), acts(k, m, k)
+    xv = ref.values(*x)
+    want, tol = ref.product(w, xv)
+    if gated:
+        up = weight(m, n, k)
+        want, tol = ref.gated(want, tol, *ref.product(up, xv))
+        h = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+        q.mx_swiglu(dev(w), dev(up), dev(x), h=h)
+        ref.near(h, want, tol, "gated")
+        if n % 32 == 0:
+            c, s = q.mx_swiglu(dev(w), dev(up), dev(x))
+            ref.check_mx8(c.cpu(), s.cpu(), want, tol, "gated, MXFP8")
+            h2, c2, s2 = torch.zeros_like(h), torch.zeros_like(c), torch.zeros_like(s)
+            q.mx_swiglu(dev(w), dev(up), dev(x), h=h2, codes=c2, scales=s2)
+            assert torch.equal(c, c2) and torch.equal(s, s2) and torch.equal(h, h2)
+    else:
+        y = q.mx_gemm(dev(w), dev(x))
+        ref.near(y, want, tol, "product")
+        r = rows16(n, m, n)
+        rd = r.cuda()
+        got = q.mx_gemm(dev(w), dev(x), residual=rd, y=rd)              # in place
+        ref.near(got, want + r.double(), tol + 2.0 ** -23 * (want + r.double()).abs(), "product and residual")
+        out = placed(torch.zeros(m, n).half(), 2)                       # (not written four at a time)
+        assert torch.equal(q.mx_gemm(dev(w), dev(x), y=out), y)
+        # scales that are not 4-byte aligned, and codes that are not 32-byte: blocks by themselves
+        wd, xd = (placed(w[0], 16), placed(w[1], 1)), (x[0].cuda(), placed(x[1], 3))
+        ref.near(q.mx_gemm(wd, xd), want, tol, "product of other alignments")
+    assert q.device_status() == 0
+
+
 def test_products_of_every_code_and_scale():
     """Each weight code times each activation code, at scales from one end to the other."""
     k = 32

@@ -6,10 +6,13 @@ import subprocess
 
 import pytest
 
+import mx_reference as ref
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "bit_group_quantized_qgemv_gb300", "csrc")
 CLUSTERS = (152, 76, 36, 15)
-NAMES = "ok cols tokens split stages row_tiles tok_tiles row_steps pair rows_first smem".split()
+NAMES = "ok cols tokens split stages row_tiles tok_tiles row_steps pair rows_first smem " \
+        "by_two faster cols2 stages2 row_tiles2 tok_tiles2 smem2".split()
 
 
 @pytest.fixture(scope="module")
@@ -25,7 +28,7 @@ def plans(program, shapes, clusters=CLUSTERS):
     return [dict(zip(NAMES, map(int, ln.split()))) for ln in r.stdout.splitlines()]
 
 
-def check(shape, p):
+def check(shape, p, two=True):
     M, N, K, gated, fp16 = shape
     w, steps = 2 if gated else 1, -(-K // 128)
     assert p["ok"], shape
@@ -42,6 +45,15 @@ def check(shape, p):
     out = 16384 if not fp16 and not gated and p["split"] == 1 else 0
     assert p["smem"] >= 1024 + p["stages"] * stage + rows + part + out
     assert p["smem"] + 1024 <= 227 * 1024                              # and what is static
+    assert p["by_two"] == (not fp16 and K % 128 == 0 and two)
+    if p["by_two"]:                                                     # two blocks that share their tiles
+        assert p["cols2"] % 32 == 0 and 2 * p["cols2"] + 32 <= 512
+        assert p["stages2"] >= 4 and p["stages2"] % 2 == 0 and p["stages2"] <= 16
+        assert p["row_tiles2"] * (128 if gated else 256) >= N and p["tok_tiles2"] * p["cols2"] >= M
+        assert (p["tok_tiles2"] - 1) * p["cols2"] < M
+        stage = 16384 + p["cols2"] * 64 + 512 * (3 if p["cols2"] > 128 else 2)
+        assert p["smem2"] >= 1024 + p["stages2"] * stage + 16384 and p["smem2"] + 1024 <= 227 * 1024
+        assert p["smem2"] > 114 * 1024                                  # one block a multiprocessor
     if fp16:
         assert p["tok_tiles"] == 1 and p["tokens"] == M and 3 * M <= p["cols"] <= 32
         assert p["pair"] and p["row_steps"] * p["split"] >= steps and p["row_steps"] <= 64
@@ -56,7 +68,7 @@ def test_random_sizes(program, clusters):
         N, M = int(2 ** rng.uniform(0, 18)), int(2 ** rng.uniform(0, 17))
         shapes.append((M, N, K, rng.random() < 0.4, 0))
     for s, p in zip(shapes, plans(program, shapes, clusters)):
-        check(s, p)
+        check(s, p, clusters[1] > 0)
 
 
 def test_fp16_rows_of_every_length(program):
@@ -78,3 +90,12 @@ def test_the_largest(program):
         assert p["ok"], s
         assert p["row_tiles"] > 0 and p["tok_tiles"] > 0
         check(s, p)
+
+
+def test_sizes_of_the_tests_of_pairs(program):
+    shapes = [(m, n, k, gated, 0) for m, n, k, gated in ref.PAIRS]
+    rounds = set()
+    for s, p in zip(shapes, plans(program, shapes)):
+        assert p["faster"], s
+        rounds.add((s[3], min(3, -(-p["row_tiles2"] * p["tok_tiles2"] // 76))))
+    assert {(0, 1), (0, 2), (0, 3), (1, 1), (1, 2), (1, 3)} <= rounds
