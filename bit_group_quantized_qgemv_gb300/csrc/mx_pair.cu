@@ -7,21 +7,25 @@
 // 16 KB of weights and 28 KB of columns into the product and 36 KB into shared memory a step,
 // which takes its 128 bytes a clock for longer than the product itself (448 clocks for 224
 // columns: 700 were measured); in a pair the columns are half of that, and 560 clocks.
-// Measured, pairs against blocks by themselves at their best widths, 2.07 GHz: 4096 rows of
-// K = 14336 to 4096 132 against 158 us (3.6 PFLOP/s; after some 25 ms of them the card's power
-// cap takes the clock to 1.5 GHz and both to 158 and 174), 1000 rows 4096 x 4096 16.5 against
-// 19.2, gated 512 rows of 4096 to 14336 45 against 51; but gated 1024 rows of 1024 to 2816 14.2
+// Measured, pairs against blocks by themselves, each at its best width: 4096 rows of K = 14336
+// to 4096 127 against 156 us, 8192 of 8192 x 8192 286 against 325 (3.8 PFLOP/s; clocks are at 1.7
+// GHz under this load, and after some 25 ms of it at 1.5 by the card's power cap: 158 against
+// 174 us for the first), 1000 rows of 4096 x 4096 16.8 against 18.8, 64 rows 8.2 against 9.3,
+// gated 512 rows of 4096 to 14336 44 against 51; but gated 1024 rows of 1024 to 2816 14.4
 // against 12.9, where results take longer than the steps (here they change places on the way).
-// Which of the two is expected to be faster mx_plan.h says.
+// Which of the two is expected to be faster mx_plan.h says.  A step of 224 columns takes 458
+// clocks, 448 of them the tensor core's; one of up to 96 some 280, about what the copy takes
+// to spread 128 x 128 codes.
 //
 // Gated: a block's 128 rows are 64 of the gate and the same 64 of the other weight, so that
 // one product has both.  Results change places between the warps of the two halves through
 // shared memory, each warp finishing half of the columns of 32 rows.
 //
 // Warps as there: two for codes (TMA alone: other K and addresses take the other kernel), four
-// for scales (each block holds its rows' and all columns'), one in the block of rank 0 that
-// issues for both (in the other it hands on, to rank 0's barrier, that a stage is full there),
-// eight for results.
+// for scales (each block holds its rows' and all columns'), two in the block of rank 0 that
+// issue for both, every other step each into an accumulator of its own (64 columns, K = 14336:
+// 284 clocks a step, 316 with one), with over 96 columns one for all; in the other block they hand on,
+// to rank 0's barrier, that a stage is full there; eight for results.
 #include <atomic>
 
 #include "mx_product.cuh"
@@ -33,7 +37,7 @@ __device__ unsigned g_status = 0;
 
 constexpr int kRowsW = kMxRows, kStepK = kMxStep;
 constexpr int kOutWarps = 8, kLoaders = 4, kTmaWarps = 2;
-constexpr int kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders, kTmaWarp = kMmaWarp + 1,
+constexpr int kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders, kTmaWarp = kMmaWarp + 2,
               kThreads = 32 * (kTmaWarp + kTmaWarps);
 
 struct Bars {
@@ -51,7 +55,8 @@ __device__ __forceinline__ void hand_on(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <bool GATED>
+// TWO: every other step's products into a second accumulator, by a warp of their own.
+template <bool GATED, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_pair_kernel(const MxProductArgs a, const MxPairPlan p, const bool wide16, const bool wide,
                    const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap u_map,
@@ -78,6 +83,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     *tok = (p.rows_first ? o : i) * p.cols;
   };
 
+  // The first tile's weights on their way to L2 while the kernel before ends.
+  if (first < tiles) {
+    int row, tok;
+    place(first, &row, &tok);
+    if (warp == kTmaWarp && lane == 0) {
+      for (int k = 0; k < steps && k < p.stages; ++k) {
+        tc::prefetch_2d(&w_map, k * kStepK, row);
+        if (GATED) tc::prefetch_2d(&u_map, k * kStepK, row);
+      }
+    } else if (warp >= kLoadWarp && warp < kMmaWarp) {
+      const int i = threadIdx.x - kLoadWarp * 32, n = row + (i & (kRows - 1));
+      if (n < a.N) prefetch_l2((GATED && i >= kRows ? a.us : a.ws) + static_cast<long long>(n) * blocks);
+    }
+  }
   if (warp == 0) {
     if (lane < p.stages) {
       // the block's scales and copies, and for the one that issues the other's as well
@@ -86,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane < kLoaders) mbar_init(smem_u32(&bars.turn[lane]), 1);
     if (lane < 2) {
-      mbar_init(smem_u32(&bars.acc_full[lane]), 1);
+      mbar_init(smem_u32(&bars.acc_full[lane]), TWO ? 2 : 1);
       mbar_init(smem_u32(&bars.acc_empty[lane]), 2 * kOutWarps);
     }
     if (lane == 0) s_failed = 0;
@@ -126,35 +145,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == kMmaWarp) {
-    int stage = 0, use = 0, n = 0;
+  } else if (warp >= kMmaWarp) {
+    const int me = warp - kMmaWarp;
+    int stage = 0, use = 0, n = 0, odd = 0;  // odd: of all tiles' steps, the next one's number
+    const bool all = rank == 0 && !TWO;    // the first warp has all steps, not every other one
+    auto next = [&] {
+      odd ^= 1;
+      if (++stage == p.stages) stage = 0, ++use;
+    };
     if (rank == 0) {
       // ----------------------------------------------------------- products
       const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
       const uint32_t idesc = tc::idesc_mx(p.cols, 256);
       uint32_t c = base, ss = s_ring;  // of the stage
-      for (long long t = first; t < tiles; t += stride, ++n) {
+      for (long long t = first; t < tiles && (TWO || me == 0); t += stride, ++n) {
         const int buf = n & 1;
         if (n >= 2) step_wait(smem_u32(&bars.acc_empty[buf]), ((n >> 1) - 1) & 1, &s_failed, &g_status);
         tc::fence_after();
-        const uint32_t acc = tm + buf * p.cols;
+        const uint32_t acc = tm + (buf * (TWO ? 2 : 1) + me) * p.cols;
         for (int k = 0; k < steps; ++k) {
-          step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
-          tc::fence_after();
-          if (tc::elect_one()) {
-            const uint32_t st = tm + 512 - 32 + (k & 1) * 16;
-            tc::copy_scales_pair(st, ss);
-            tc::copy_scales_pair(st + 8, ss + 512);
-            if (p.cols > 128) tc::copy_scales_pair(st + 12, ss + 1024);
-            const uint64_t w = tc::desc_k_major(c), b = tc::desc_k_major(c + kRowsW * kStepK);
+          if (all || odd == me) {
+            step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
+            tc::fence_after();
+            if (tc::elect_one()) {
+              const uint32_t st = tm + kMxAccCols + (TWO ? me : k & 1) * 16;
+              tc::copy_scales_pair(st, ss);
+              tc::copy_scales_pair(st + 8, ss + 512);
+              if (p.cols > 128) tc::copy_scales_pair(st + 12, ss + 1024);
+              const uint64_t w = tc::desc_k_major(c), b = tc::desc_k_major(c + kRowsW * kStepK);
+              const int more = k > (TWO ? 1 : 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc::mma_mx_pair(acc, w + 2 * j, b + 2 * j, idesc, j, st, st + 8, k > 0 || j > 0);
-            tc::commit_pair(smem_u32(&bars.empty[stage]));
+              for (int j = 0; j < 4; ++j)
+                tc::mma_mx_pair(acc, w + 2 * j, b + 2 * j, idesc, j, st, st + 8, j > 0 || more);
+              tc::commit_pair(smem_u32(&bars.empty[stage]));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          c += c_bytes, ss += s_bytes;
-          if (++stage == p.stages) stage = 0, ++use, c = base, ss = s_ring;
+          next();
+          c = stage == 0 ? base : c + c_bytes, ss = stage == 0 ? s_ring : ss + s_bytes;
         }
         if (tc::elect_one()) tc::commit_pair(smem_u32(&bars.acc_full[buf]));
         __syncwarp();
@@ -163,19 +191,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a stage that is full here, told to the block that issues
       const uint32_t there = map_rank(smem_u32(&bars.full[0]), 0);
       for (long long t = first; t < tiles; t += stride)
-        for (int k = 0; k < steps; ++k) {
-          step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
-          if (lane == 0) hand_on(there + stage * 8);
-          __syncwarp();
-          if (++stage == p.stages) stage = 0, ++use;
-        }
+        for (int k = 0; k < steps; ++k, next())
+          if (odd == me) {
+            step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
+            if (lane == 0) hand_on(there + stage * 8);
+            __syncwarp();
+          }
     }
     // A block that ends has been told of every use of its stages: no arrival is under way.
     for (int i = 0; i < p.stages; ++i) {
       if (stage == 0) stage = p.stages, --use;
-      --stage;
+      --stage, odd ^= 1;
       if (use < 0) break;
-      step_wait(smem_u32(&bars.empty[stage]), use & 1, &s_failed, &g_status);
+      if (all ? me == 0 : odd == me) step_wait(smem_u32(&bars.empty[stage]), use & 1, &s_failed, &g_status);
     }
   } else if (warp >= kLoadWarp) {
     // --------------------------------------------------------------- scales
@@ -257,13 +285,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = n_t & 1, count = min(p.cols, a.M - tok);
       step_wait(smem_u32(&bars.acc_full[buf]), (n_t >> 1) & 1, &s_failed, &g_status);
       tc::fence_after();
-      const uint32_t acc = lanes + buf * p.cols;
+      const uint32_t acc = lanes + buf * (TWO ? 2 : 1) * p.cols;
+      // (a tile of a single step has one of two accumulators: the step's)
+      const bool has0 = !TWO || steps > 1 || (n_t & 1) == 0, has1 = TWO && (steps > 1 || (n_t & 1) == 1);
+      auto sums = [&](int c0, float (&v)[16]) {
+        uint32_t x[16], x1[16];
+        tc::ld16(x, acc + c0);
+        if (TWO) tc::ld16(x1, acc + p.cols + c0);
+        tc::wait_ld16(x);
+        if (TWO) tc::wait_ld16(x1);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          v[c] = !TWO ? __uint_as_float(x[c]) : (has0 ? __uint_as_float(x[c]) : 0.f) + (has1 ? __uint_as_float(x1[c]) : 0.f);
+      };
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
       for (int c0 = half * kMxOut; c0 < count; c0 += 2 * kMxOut) {
-        uint32_t x[16];
+        float v[16];
         if constexpr (GATED) {
-          tc::ld16(x, acc + c0);
-          tc::wait_ld16(x);
+          sums(c0, v);
           // The warps with the gate's rows finish the first eight columns, those with the other
           // weight's the last: each gives its values of the others to its partner.  (Two places in
           // turn: one is written again after everyone has been past the barrier behind its reads.)
@@ -273,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++chunk;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at(part == 0 ? 8 + c : c)), "r"(part == 0 ? x[8 + c] : x[c])
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at(part == 0 ? 8 + c : c)),
+                         "r"(__float_as_uint(part == 0 ? v[8 + c] : v[c]))
                          : "memory");
           named_bar_sync(1 + half, 128);
           float h[8];
@@ -281,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 8; ++c) {
             float other;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(at(part == 0 ? c : 8 + c)) : "memory");
-            const float mine = __uint_as_float(part == 0 ? x[c] : x[8 + c]);
+            const float mine = part == 0 ? v[c] : v[8 + c];
             h[c] = mx_silu(part == 0 ? mine : other) * (part == 0 ? other : mine);
           }
           const int m = c0 + 8 * part;
@@ -301,26 +341,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 4; ++i)
                 r[i] = *reinterpret_cast<const uint2*>(from + static_cast<long long>(min(m0 + i, count - 1)) * a.N);
             }
-            tc::ld16(x, acc + c0);
-            tc::wait_ld16(x);
+            sums(c0, v);
             named_bar_sync(1 + half, 128);  // the last columns' values have been read
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_out + (c * kRowsW + quarter * 32 + lane) * 4), "r"(x[c])
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_out + (c * kRowsW + quarter * 32 + lane) * 4), "r"(__float_as_uint(v[c]))
                            : "memory");
             named_bar_sync(1 + half, 128);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float v[4];
+              float o[4];
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                           : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
                            : "r"(stage_out + ((4 * quarter + i) * kRowsW + 4 * lane) * 4)
                            : "memory");
               const float2 a0 = __half22float2(*reinterpret_cast<const __half2*>(&r[i].x));
               const float2 a1 = __half22float2(*reinterpret_cast<const __half2*>(&r[i].y));
               if (live && m0 + i < count)
                 *reinterpret_cast<uint2*>(a.y + at + static_cast<long long>(i) * a.N) =
-                    make_uint2(pack_f16(v[0] + a0.x, v[1] + a0.y), pack_f16(v[2] + a1.x, v[3] + a1.y));
+                    make_uint2(pack_f16(o[0] + a0.x, o[1] + a0.y), pack_f16(o[2] + a1.x, o[3] + a1.y));
             }
           } else {
             __half r[16];
@@ -329,11 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c) r[c] = from[static_cast<long long>(min(c0 + c, count - 1)) * a.N];
             }
-            tc::ld16(x, acc + c0);
-            tc::wait_ld16(x);
-            float v[16];
+            sums(c0, v);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(x[c]) + (a.res != nullptr ? __half2float(r[c]) : 0.f);
+            for (int c = 0; c < 16; ++c) v[c] += a.res != nullptr ? __half2float(r[c]) : 0.f;
             if (ok) write_results<GATED>(a, n, tok + c0, count - c0, v, lane);
           }
         }
@@ -359,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED>
+template <bool GATED, bool TWO>
 cudaError_t launch(const MxProductArgs& a, const MxPairPlan& p, int clusters, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  auto* k = mx_pair_kernel<GATED>;
+  auto* k = mx_pair_kernel<GATED, TWO>;
   const unsigned long long bit = 1ull << (device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
@@ -403,7 +440,9 @@ bool mx_pair_takes(const MxProductArgs& a) {
 }
 
 cudaError_t mx_pair_launch(const MxProductArgs& a, const MxPairPlan& p, int clusters, int device, cudaStream_t st) {
-  return a.up != nullptr ? launch<true>(a, p, clusters, device, st) : launch<false>(a, p, clusters, device, st);
+  if (a.up != nullptr)
+    return p.two ? launch<true, true>(a, p, clusters, device, st) : launch<true, false>(a, p, clusters, device, st);
+  return p.two ? launch<false, true>(a, p, clusters, device, st) : launch<false, false>(a, p, clusters, device, st);
 }
 
 cudaError_t status_mx_pair(unsigned* out) {

@@ -72,11 +72,10 @@ inline bool mx_fit(const MxShape& s, int cols, int split, MxPlan* p) {
 
 // Clocks that a plan is expected to take.  A step of a tile is bound by shared memory (what
 // the copies write, weights spread to bytes, and what the products read, x once for each
-// weight), L2, the tensor core, or the waits and the issue of products (shorter where two
-// accumulators take them in turn); a tile by its steps or by the results of the one before.
-// The rates are fitted to 33 products of 9 to 8192 rows and 16 of 1 to 8 fp16 rows, each in
-// all widths and splits: what this takes was the fastest or within 2% of it in 44 of them, 5
-// to 11% slower in five.
+// weight), L2, the tensor core, or the waits and the issue of products; a tile by its steps
+// or by the results of the one before.  The rates are fitted to 37 products of 9 to 8192 rows
+// and 16 of 1 to 8 fp16 rows, each in all widths and splits, by themselves and in pairs: what
+// this takes was the fastest or within 2% of it, but for three of the fp16 rows (7 to 11%).
 inline double mx_cost(const MxShape& s, const MxPlan& p) {
   const int w = s.gated ? 2 : 1, steps = (s.K + kMxStep - 1) / kMxStep;
   int i = 0;
@@ -88,11 +87,12 @@ inline double mx_cost(const MxShape& s, const MxPlan& p) {
   if (s.fp16) {
     step = 420, out = 1200 + (p.split > 1 ? 1000 + 110 * i : 0), fill = 4800;
   } else {
-    const double cols = p.cols, smem = w * kMxRows * 1.32 + (1 + w) * cols, l2 = (w * 8704 + cols * 132) / 63;
+    const double cols = p.cols;
+    const double smem = w * kMxRows * 1.58 + (1 + w) * cols * 0.85, l2 = (w * 8704 + cols * 132) / 75;
     const double tensor = w * 4 * (cols / 2 > 32 + cols / 4 ? cols / 2 : 32 + cols / 4);
-    step = p.pair ? 360 : 560;
+    step = p.pair ? 320 : 0;
     for (const double least : {smem, l2, tensor}) step = step > least ? step : least;
-    out = 2100 + w * cols * (s.gated ? 24 : 17.5) + (p.split > 1 ? 1300 + 160 * i + w * cols * 62 : 0), fill = 6300;
+    out = 1800 + w * cols * (s.gated ? 23.5 : 19) + (p.split > 1 ? 1100 + 200 * i + w * cols * 66 : 0), fill = 6500;
   }
   return rounds * (part * step > out ? part * step : out) + out + fill;
 }
@@ -124,6 +124,7 @@ struct MxPairPlan {
   int cols, stages;
   int row_tiles, tok_tiles;
   bool rows_first;
+  bool two;      // every other step's products into a second accumulator
   int smem;
 };
 
@@ -137,6 +138,7 @@ inline bool mx_pair_fit(const MxShape& s, int cols, MxPairPlan* p) {
   const int stage = kMxRows * kMxStep + cols / 2 * kMxStep + 512 * (cols > 128 ? 3 : 2);
   p->stages = (kMxSmem - other) / stage;
   p->stages = (p->stages > kMxMaxStages ? kMxMaxStages : p->stages) / 2 * 2;
+  p->two = 4 * cols <= kMxAccCols;
   p->smem = other + p->stages * stage;
   return cols % 32 == 0 && 2 * cols + 32 <= 512 && p->stages >= kMxMinStages;
 }
@@ -145,17 +147,17 @@ inline double mx_pair_cost(const MxShape& s, const MxPairPlan& p) {
   const int steps = s.K / kMxStep;
   const double tiles = static_cast<double>(p.row_tiles) * p.tok_tiles, clusters = s.clusters[1];
   const double rounds = static_cast<double>(static_cast<long long>((tiles + clusters - 1) / clusters));
-  const double tensor = 100 + 2.1 * p.cols, step = tensor > 330 ? tensor : 330;
-  const double per_tile = steps * step, out = 1500 + p.cols * (s.gated ? 33.5 : 15);
-  return rounds * (per_tile > out ? per_tile : out) + out + 4000;
+  const double tensor = 78 + 2.02 * p.cols, least = p.two ? 320 : 400, step = tensor > least ? tensor : least;
+  const double per_tile = steps * step, out = 1500 + p.cols * (s.gated ? 33 : 15) * (p.two ? 1.25 : 1);
+  return rounds * (per_tile > out ? per_tile : out) + out + 3400;
 }
 
 // The best of them; false: none (no clusters of two, or K is no whole number of steps).
 inline bool mx_pair_plan(const MxShape& s, MxPairPlan* best, double* cost) {
   bool any = false;
   if (s.fp16 || s.clusters[1] < 1 || s.K % kMxStep != 0) return false;
-  for (int cols = 64; cols <= 224; cols += 32) {
-    if (cols > 64 && cols - 32 >= s.M) break;
+  for (int cols = 32; cols <= 224; cols += 32) {
+    if (cols > 32 && cols - 32 >= s.M) break;
     MxPairPlan p;
     if (!mx_pair_fit(s, cols, &p)) continue;
     const double c = mx_pair_cost(s, p);

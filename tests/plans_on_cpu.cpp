@@ -17,7 +17,7 @@ int main() {
     const bool pairs = qgemv::mx_pair_plan(s, &two, &cost);
     std::printf("%d %d %d %d %d %d %d %d %d %d %d ", ok, p.cols, p.tokens, p.split, p.stages, p.row_tiles, p.tok_tiles,
                 p.row_steps, p.pair, p.rows_first, p.smem);
-    std::printf("%d %d %d %d %d %d %d\n", pairs, pairs && ok && cost < qgemv::mx_cost(s, p), two.cols, two.stages,
-                two.row_tiles, two.tok_tiles, two.smem);
+    std::printf("%d %d %d %d %d %d %d %d\n", pairs, pairs && ok && cost < qgemv::mx_cost(s, p), two.cols, two.stages,
+                two.row_tiles, two.tok_tiles, two.smem, two.two);
   }
 }

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "bit_group_quantized_qgemv_gb300", "csrc")
 CLUSTERS = (152, 76, 36, 15)
 NAMES = "ok cols tokens split stages row_tiles tok_tiles row_steps pair rows_first smem " \
-        "by_two faster cols2 stages2 row_tiles2 tok_tiles2 smem2".split()
+        "by_two faster cols2 stages2 row_tiles2 tok_tiles2 smem2 two2".split()
 
 
 @pytest.fixture(scope="module")
@@ -47,7 +47,7 @@ def check(shape, p, two=True):
     assert p["smem"] + 1024 <= 227 * 1024                              # and what is static
     assert p["by_two"] == (not fp16 and K % 128 == 0 and two)
     if p["by_two"]:                                                     # two blocks that share their tiles
-        assert p["cols2"] % 32 == 0 and 2 * p["cols2"] + 32 <= 512
+        assert p["cols2"] % 32 == 0 and (4 if p["two2"] else 2) * p["cols2"] + 32 <= 512
         assert p["stages2"] >= 4 and p["stages2"] % 2 == 0 and p["stages2"] <= 16
         assert p["row_tiles2"] * (128 if gated else 256) >= N and p["tok_tiles2"] * p["cols2"] >= M
         assert (p["tok_tiles2"] - 1) * p["cols2"] < M

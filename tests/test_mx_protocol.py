@@ -139,11 +139,11 @@ def run(rng, S, k0, k1, tiles, gated, pair, fp16, tma, turns=True, loaders=4, tm
     play(rng, procs, later)
 
 
-def run_pair(rng, S, steps, tiles, turns=True, loaders=4, tma_warps=2, out=8):
+def run_pair(rng, S, steps, tiles, two, turns=True, loaders=4, tma_warps=2, out=8):
     """Two blocks that share their tiles (csrc/mx_pair.cu)."""
     full = [[Barrier(3 - rank) for _ in range(S)] for rank in range(2)]
     empty = [[Barrier(1) for _ in range(S)] for _ in range(2)]
-    acc_full = [[Barrier(1) for _ in range(2)] for _ in range(2)]
+    acc_full = [[Barrier(2 if two else 1) for _ in range(2)] for _ in range(2)]
     acc_empty = [Barrier(2 * out) for _ in range(2)]              # of the one that issues
     turn = [[Barrier(1) for _ in range(loaders)] for _ in range(2)]
     later = []
@@ -187,31 +187,36 @@ def run_pair(rng, S, steps, tiles, turns=True, loaders=4, tma_warps=2, out=8):
                         yield
                     written = []
 
-    def products():
+    def products(me):
+        if me and not two:
+            return
         g = 0
         for n in range(tiles):
             if n >= 2:
                 yield from wait(acc_empty[n & 1], ((n >> 1) - 1) & 1, n >> 1)
             for _ in range(steps):
                 s, use = g % S, g // S
-                yield from wait(full[0][s], use & 1, use + 1)
-                assert full[1][s].phase == use + 1                # the other's operands are there
-                later.append(lambda s=s: both([empty[0][s], empty[1][s]]))
-                yield
+                if not two or g & 1 == me:
+                    yield from wait(full[0][s], use & 1, use + 1)
+                    assert full[1][s].phase == use + 1            # the other's operands are there
+                    later.append(lambda s=s: both([empty[0][s], empty[1][s]]))
+                    yield
                 g += 1
             later.append(lambda n=n: both([acc_full[0][n & 1], acc_full[1][n & 1]]))
             yield
 
-    def hand_on():
-        for g in range(tiles * steps):
+    def hand_on(me):
+        for g in range(me, tiles * steps, 2):
             yield from wait(full[1][g % S], (g // S) & 1, g // S + 1)
             full[0][g % S].arrive()
             yield
 
-    def last_uses(rank, before):
+    def last_uses(rank, me, before):
         yield from before
+        alone = rank == 0 and not two
         for g in range(max(0, tiles * steps - S), tiles * steps)[::-1]:
-            yield from wait(empty[rank][g % S], (g // S) & 1, g // S + 1)
+            if (me == 0 if alone else g & 1 == me):
+                yield from wait(empty[rank][g % S], (g // S) & 1, g // S + 1)
 
     def results(rank):
         for n in range(tiles):
@@ -220,7 +225,7 @@ def run_pair(rng, S, steps, tiles, turns=True, loaders=4, tma_warps=2, out=8):
                 acc_empty[n & 1].arrive()
             yield
 
-    procs = [last_uses(0, products()), last_uses(1, hand_on())]
+    procs = [last_uses(rank, me, job(me)) for rank, job in enumerate((products, hand_on)) for me in range(2)]
     for rank in range(2):
         procs += ([scales(rank, i) for i in range(loaders)] + [codes(rank, i) for i in range(tma_warps)] +
                   [results(rank) for _ in range(out)])
@@ -248,10 +253,10 @@ def test_every_wait_is_for_its_phase(seed):
 def test_pairs_of_blocks(seed):
     rng = random.Random(100 + seed)
     for _ in range(8):
-        run_pair(rng, 2 * rng.randint(2, 8), rng.randint(1, 20), rng.randint(1, 5))
+        run_pair(rng, 2 * rng.randint(2, 8), rng.randint(1, 20), rng.randint(1, 5), rng.random() < 0.5)
     with pytest.raises(AssertionError):
         for _ in range(100):
-            run_pair(rng, 2 * rng.randint(2, 8), rng.randint(8, 30), rng.randint(1, 6), turns=False)
+            run_pair(rng, 2 * rng.randint(2, 8), rng.randint(8, 30), rng.randint(1, 6), rng.random() < 0.5, turns=False)
 
 
 @pytest.mark.parametrize("wrong", ["no turns", "odd stages"])
