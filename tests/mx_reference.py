@@ -118,6 +118,8 @@ def product(w, x):
 PAIRS = [(777, 2051, 1024, 0), (1500, 5000, 256, 0), (2100, 8000, 128, 0), (333, 2500, 1152, 0), (225, 30000, 128, 0),
          (1000, 513, 4096, 0), (1000, 2048, 2048, 1), (300, 1440, 512, 1), (100, 2816, 1024, 1), (3000, 2016, 2048, 1),
          (640, 1001, 896, 1)]
+PAIRS_SMALL = [(333, 1001, 640, 0), (333, 1004, 640, 0), (333, 1004, 640, 1), (130, 1952, 896, 1)]
+PAIRS_LARGEST, PAIRS_GRAPH = (45050, 50000, 2048), (400, 1504, 1152)
 
 
 def gated(g, tg, u, tu):

@@ -245,6 +245,84 @@ def test_pairs_of_blocks(m, n, k, gated):
     assert q.device_status() == 0
 
 
+@pytest.mark.parametrize("m,n,k,gated", ref.PAIRS_SMALL)
+def test_pairs_write_nothing_else(m, n, k, gated):
+    w, x = dev(weight(1, n, k)), dev(acts(2, m, k))
+
+    def banded(shape, dtype):
+        raw = torch.full((torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size() + 4096,), 0xA5,
+                         dtype=torch.uint8, device="cuda")
+        return raw, raw[2048:-2048].view(dtype).view(shape)
+
+    bands = [banded((m, n), torch.float16)]
+    if gated and n % 32 == 0:
+        bands += [banded((m, n), torch.uint8), banded((m, n // 32), torch.uint8)]
+    kept = [t.clone() for t in (*w, *x)]
+    if gated:
+        q.mx_swiglu(w, w, x, h=bands[0][1], **({} if n % 32 else dict(codes=bands[1][1], scales=bands[2][1])))
+    else:
+        q.mx_gemm(w, x, y=bands[0][1])
+        q.mx_gemm(w, x, residual=bands[0][1], y=bands[0][1])
+    for raw, _ in bands:
+        assert bool((raw[:2048] == 0xA5).all()) and bool((raw[-2048:] == 0xA5).all())
+    assert all(torch.equal(a, b) for a, b in zip(kept, (*w, *x)))
+
+
+def test_pairs_beyond_32_bits():
+    """Outputs of more than 2^31 elements: the last rows against 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    m, n, k = ref.PAIRS_LARGEST
+    some = 70
+    w, u = (q.mx_quantize(torch.randn(n, k, generator=g, device="cuda").half(), 4) for _ in range(2))
+    x = q.mx_quantize(torch.randn(m, k, generator=g, device="cuda").half())
+    tail = (x[0][-some:].cpu(), x[1][-some:].cpu())
+    host = [(t[0].cpu(), t[1].cpu()) for t in (w, u)]
+    want, tol = ref.product(host[0], ref.values(*tail))
+    y = q.mx_gemm(w, x)
+    assert y.numel() > 1 << 31
+    ref.near(y[-some:], want, tol, "product")
+    first = y[-some:].clone()
+    q.mx_gemm(w, x, residual=y, y=y)
+    both = want + first.cpu().double()
+    ref.near(y[-some:], both, tol + 2.0 ** -23 * both.abs(), "product and residual")
+    del y
+    want, tol = ref.gated(want, tol, *ref.product(host[1], ref.values(*tail)))
+    h = torch.empty(m, n, dtype=torch.float16, device="cuda")
+    ref.near(q.mx_swiglu(w, u, x, h=h)[-some:], want, tol, "gated")
+    del h
+    n32 = n // 32 * 32
+    c, s = q.mx_swiglu(*((t[0][:n32].contiguous(), t[1][:n32].contiguous()) for t in (w, u)), x)
+    assert c.numel() > 1 << 31
+    ref.check_mx8(c[-some:].cpu(), s[-some:].cpu(), want[:, :n32], tol[:, :n32], "gated, MXFP8")
+    assert q.device_status() == 0
+    del c, s
+    torch.cuda.empty_cache()
+
+
+def test_pairs_captured_and_replayed():
+    """Of new values in the same tensors, and two of them on two streams at once."""
+    m, n, k = ref.PAIRS_GRAPH
+    w, u = dev(weight(1, n, k)), dev(weight(2, n, k))
+    x = dev(acts(3, m, k))
+    y, held = torch.zeros(m, n, dtype=torch.float16, device="cuda"), q.mx_swiglu(w, u, x)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        q.mx_gemm(w, x, y=y)
+        with torch.cuda.stream(side):
+            q.mx_swiglu(w, u, x, codes=held[0], scales=held[1])
+        torch.cuda.current_stream().wait_stream(side)
+    for seed in (7, 8):
+        for to, t in zip(x, acts(seed, m, k)):
+            to.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        c, s = q.mx_swiglu(w, u, x)
+        assert torch.equal(y, q.mx_gemm(w, x)) and torch.equal(held[0], c) and torch.equal(held[1], s)
+    assert q.device_status() == 0
+
+
 def test_products_of_every_code_and_scale():
     """Each weight code times each activation code, at scales from one end to the other."""
     k = 32
@@ -497,7 +575,7 @@ def test_longest_fp16_rows():
 
 
 def test_long_rows():
-    k = 70016                                                    # 547 steps, no multiple of 128
+    k = 70016                                                    # 547 steps, no whole groups of four
     w, x = weight(3, 20, k), acts(4, 3, k)
     want, tol = ref.product(w, ref.values(*x))
     ref.near(q.mx_gemm(dev(w), dev(x)), want, tol, "product")

@@ -98,4 +98,7 @@ def test_sizes_of_the_tests_of_pairs(program):
     for s, p in zip(shapes, plans(program, shapes)):
         assert p["faster"], s
         rounds.add((s[3], min(3, -(-p["row_tiles2"] * p["tok_tiles2"] // 76))))
+    more = [(*s[:3], s[3], 0) for s in ref.PAIRS_SMALL]
+    more += [(*s, gated, 0) for s in (ref.PAIRS_LARGEST, ref.PAIRS_GRAPH) for gated in (0, 1)]
+    assert all(p["faster"] for p in plans(program, more))
     assert {(0, 1), (0, 2), (0, 3), (1, 1), (1, 2), (1, 3)} <= rounds
