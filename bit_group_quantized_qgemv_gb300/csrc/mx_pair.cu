@@ -21,11 +21,11 @@
 // one product has both.  Results change places between the warps of the two halves through
 // shared memory, each warp finishing half of the columns of 32 rows.
 //
-// Warps as there: two for codes (TMA alone: other K and addresses take the other kernel), four
-// for scales (each block holds its rows' and all columns'), two in the block of rank 0 that
+// Warps as there: two for codes (TMA alone: other K and addresses take the other kernel); four
+// for scales (each block holds its rows' and all columns'); two in the block of rank 0 that
 // issue for both, every other step each into an accumulator of its own (64 columns, K = 14336:
-// 284 clocks a step, 316 with one), with over 96 columns one for all; in the other block they hand on,
-// to rank 0's barrier, that a stage is full there; eight for results.
+// 284 clocks a step, 316 with one), with over 96 columns one for all; in the other block they
+// hand on, to rank 0's barrier, that a stage is full there; eight for results.
 #include <atomic>
 
 #include "mx_product.cuh"
