@@ -75,13 +75,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigne
 // wait of more than kWaitNs sets *failed (in shared memory), after which the
 // block's waits last for a thousand tries: its loops go on over whatever they
 // find, in bounds and for as many steps as they have, and the results are
-// dropped.
+// dropped.  CLUSTER: other blocks of the cluster have a part in the phase.
+template <bool CLUSTER = false>
 __device__ __forceinline__ void step_wait(uint32_t bar, uint32_t parity, volatile int* failed,
                                           unsigned* status) {
-  bool done = mbar_try_wait(bar, parity);
+  auto look = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  bool done = look();
   uint64_t t0 = 0;
   for (int i = 1; !done; ++i) {
-    done = mbar_try_wait(bar, parity);
+    done = look();
     if ((i & 1023) == 0) {
       if (*failed != 0) break;
       const uint64_t now = global_timer_ns();
@@ -93,6 +95,7 @@ __device__ __forceinline__ void step_wait(uint32_t bar, uint32_t parity, volatil
       }
     }
   }
+  if (CLUSTER) mbar_acquire_cluster();
   __syncwarp();
 }
 

@@ -40,20 +40,14 @@ constexpr int kOutWarps = 8, kLoaders = 4, kTmaWarps = 2;
 constexpr int kLoadWarp = kOutWarps, kMmaWarp = kLoadWarp + kLoaders, kTmaWarp = kMmaWarp + 2,
               kThreads = 32 * (kTmaWarp + kTmaWarps);
 
+// All but `turn` are arrived on by the other block too (by its tensor core, or as a stage that is
+// full there and an accumulator that has been read): waits for them are in the cluster's scope,
+// and order shared memory alone.  Places of tensor memory have fences of their own.
 struct Bars {
   uint64_t full[kMxMaxStages], empty[kMxMaxStages];
   uint64_t turn[kLoaders];  // a loader may go on to its group
   uint64_t acc_full[2], acc_empty[2];
 };
-
-// Handed on to the other block's barrier.  What is handed on are places of shared and tensor
-// memory that the tensor core alone reads or writes next: they have no copies elsewhere, and
-// the waits and fences before this have seen them written or read.  (Released to the whole
-// cluster, as a fence of all memory, an arrival takes 1400 clocks, of a step's 500 to 600:
-// 4096 rows of K = 14336 took 427 us.)
-__device__ __forceinline__ void hand_on(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 
 // TWO: every other step's products into a second accumulator, by a warp of their own.
 template <bool GATED, bool TWO>
@@ -135,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stage >= p.stages) stage -= p.stages, ++use;
       if (moved) place(t, &row, &tok);
       moved = false;
-      if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
+      if (use > 0) step_wait<true>(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
       if (lane == 0) {
         const uint32_t full = smem_u32(&bars.full[stage]), to = base + stage * c_bytes;
         mbar_arrive_expect_tx(full, bytes);
@@ -160,12 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = base, ss = s_ring;  // of the stage
       for (long long t = first; t < tiles && (TWO || me == 0); t += stride, ++n) {
         const int buf = n & 1;
-        if (n >= 2) step_wait(smem_u32(&bars.acc_empty[buf]), ((n >> 1) - 1) & 1, &s_failed, &g_status);
+        if (n >= 2) step_wait<true>(smem_u32(&bars.acc_empty[buf]), ((n >> 1) - 1) & 1, &s_failed, &g_status);
         tc::fence_after();
         const uint32_t acc = tm + (buf * (TWO ? 2 : 1) + me) * p.cols;
         for (int k = 0; k < steps; ++k) {
           if (all || odd == me) {
-            step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
+            step_wait<true>(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
             tc::fence_after();
             if (tc::elect_one()) {
               const uint32_t st = tm + kMxAccCols + (TWO ? me : k & 1) * 16;
@@ -193,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long t = first; t < tiles; t += stride)
         for (int k = 0; k < steps; ++k, next())
           if (odd == me) {
-            step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
-            if (lane == 0) hand_on(there + stage * 8);
+            step_wait<true>(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
+            if (lane == 0) mbar_arrive_cluster(there + stage * 8);
             __syncwarp();
           }
     }
@@ -203,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stage == 0) stage = p.stages, --use;
       --stage, odd ^= 1;
       if (use < 0) break;
-      if (all ? me == 0 : odd == me) step_wait(smem_u32(&bars.empty[stage]), use & 1, &s_failed, &g_status);
+      if (all ? me == 0 : odd == me) step_wait<true>(smem_u32(&bars.empty[stage]), use & 1, &s_failed, &g_status);
     }
   } else if (warp >= kLoadWarp) {
     // --------------------------------------------------------------- scales
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) {
         const int k = 4 * q + j;
         if (k >= to) continue;
-        if (use > 0) step_wait(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
+        if (use > 0) step_wait<true>(smem_u32(&bars.empty[stage]), (use - 1) & 1, &s_failed, &g_status);
         if (k == to - 1 && lane == 0) mbar_arrive(smem_u32(&bars.turn[(me + 1) % kLoaders]));
         const uint32_t ss = s_ring + stage * s_bytes + lane * 16;
         auto word = [&](const uint4& v) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; };
@@ -283,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int row, tok;
       place(t, &row, &tok);
       const int buf = n_t & 1, count = min(p.cols, a.M - tok);
-      step_wait(smem_u32(&bars.acc_full[buf]), (n_t >> 1) & 1, &s_failed, &g_status);
+      step_wait<true>(smem_u32(&bars.acc_full[buf]), (n_t >> 1) & 1, &s_failed, &g_status);
       tc::fence_after();
       const uint32_t acc = lanes + buf * (TWO ? 2 : 1) * p.cols;
       // (a tile of a single step has one of two accumulators: the step's)
@@ -378,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before();
       __syncwarp();
       // (of the last two tiles nobody waits for this)
-      if (lane == 0 && t + 2 * stride < tiles) hand_on(map_rank(smem_u32(&bars.acc_empty[buf]), 0));
+      if (lane == 0 && t + 2 * stride < tiles) mbar_arrive_cluster(map_rank(smem_u32(&bars.acc_empty[buf]), 0));
     }
   }
   tc::fence_before();

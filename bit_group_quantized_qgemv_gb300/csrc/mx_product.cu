@@ -54,7 +54,7 @@ struct Bars {
   uint64_t rows[kMxRowSteps];  // columns of fp16 rows
   uint64_t turn[kLoaders];      // a loader may go on to its group
   uint64_t acc_full[2], acc_empty[2];
-  uint64_t part_full, part_done;
+  uint64_t part_full, part_done;  // other ranks have a part in these
 };
 
 // An arrival on the mbarrier once this thread's copies so far are done; the barrier's
@@ -522,8 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool one = !GATED && p.pair && k1 - k0 == 1;
       const bool has0 = !one || (n_t & 1) == 0, has1 = !one || (n_t & 1) == 1;
       if (p.split > 1 && n_t > 0) {
-        step_wait(smem_u32(&bars.part_done), (n_t - 1) & 1, &s_failed, &g_status);
-        fence_cluster();
+        step_wait<true>(smem_u32(&bars.part_done), (n_t - 1) & 1, &s_failed, &g_status);
       }
       auto give = [&](int m, float g, float u) {  // a rank's sums of one column to who finishes it
         const int q = m % p.split;
@@ -654,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.acc_empty[buf]));
       if (p.split == 1) continue;
-      step_wait(smem_u32(&bars.part_full), n_t & 1, &s_failed, &g_status);
-      fence_cluster();
+      step_wait<true>(smem_u32(&bars.part_full), n_t & 1, &s_failed, &g_status);
       const bool all = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
       if (all) {
         for (int j = half; j < own; j += 2) {
@@ -680,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       // (after the last tile nobody waits for this, and who would be told may have ended)
-      if (t + stride < tiles && lane < p.split) arrive_remote(map_rank(smem_u32(&bars.part_done), lane));
+      if (t + stride < tiles && lane < p.split) mbar_arrive_cluster(map_rank(smem_u32(&bars.part_done), lane));
     }
   }
   tc::fence_before();

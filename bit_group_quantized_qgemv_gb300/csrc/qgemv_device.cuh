@@ -42,6 +42,30 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same for a phase that another block of the cluster has a part in, seen in the cluster's
+// scope.  It orders nothing by itself: mbar_acquire_cluster behind it does, for shared memory.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void mbar_acquire_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
+// An arrival on another block's mbarrier, behind all that this thread has done or seen done to
+// its own block's shared memory.  (Released in full, mbarrier.arrive.release.cluster, all other
+// memory is waited for too: 1400 clocks.)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // try_wait that may suspend the thread for up to `ns` nanoseconds; it
 // resumes as soon as the phase completes, so a waiting warp does not spin
 // through issue slots that computing warps need.
