@@ -43,13 +43,18 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint32_t x, uint32_t y
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// silu by the fast exponential and division: 2^-21 of the result off, and |z| 2^-23 more where z
-// is far below 0 (there the result is small against z and its error, that of a sum of products).
+// silu(z) = z / (1 + e^-z), for z below 0 as z e^z / (1 + e^z): the divisor is between 1 and 2, and
+// small results are held for as long as fp32 holds e^z.  By the fast exponential and division:
+// 2^-20 of the result off, for z below 0 |z| 2^-22 of it more (there the result is small against z
+// and its error, that of a sum of products), and |z| 2^-149 where e^z is subnormal.
 // The exact division's branches take a thread's columns one after the other, longer than all
 // else of the results: gated 1024 rows of 1024 to 2816 19.1 us for 14.5, 2048 rows of 4096 to 14336
-// 169 for 148 in the same tiles.  Of the latter's 29.4 million MXFP8 codes 33 differ from those of a
-// 64-bit sum and silu; 30 with expf and a reciprocal to a last bit, which took 2% longer.
-__device__ __forceinline__ float mx_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// 169 for 148 in the same tiles (clocks at 1.7 GHz).  Of the latter's 29.4 million MXFP8 codes 37
+// differ from those of 64-bit sums and silu; of a plain fp32 form's 28 to 34.
+__device__ __forceinline__ float mx_silu(float z) {
+  const float e = __expf(-fabsf(z));
+  return __fdividef(z < 0.f ? z * e : z, 1.0f + e);
+}
 
 // Finished values of weight row n (a lane each) and rows m, m + 1, ... of x, count of them, to
 // y and, of the gated product, to the codes and scales.  A whole warp calls this.

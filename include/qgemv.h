@@ -711,6 +711,7 @@ int qgemv_mx_gemm(const uint32_t *codes, const uint8_t *scales, const uint8_t *x
  * rows) and M >= 0 MXFP8 rows.  The result goes to h (fp16 [M][I], rounded once), to
  * h_codes [M][I] and h_scales [M][I/32] (MXFP8, quantised from the fp32 result as
  * qgemv_mx_quantize does; I % 32 == 0), or to both; NULL to skip one.  One launch.
+ * silu is off by 2^-20 of itself, below 0 by |z| 2^-22 of itself and |z| 2^-149 more.
  * Sizes, alignments and sums as qgemv_mx_gemm; 16 rows of 4096 to 14336 take 14.4 us,
  * 2048 rows 158.
  */

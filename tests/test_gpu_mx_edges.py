@@ -1,0 +1,51 @@
+"""The microscaled products where their values are extreme, against plain 64-bit forms."""
+import pytest
+import torch
+
+import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+q = pytest.importorskip("bit_group_quantized_qgemv_gb300")
+
+
+def dev(pair):
+    return tuple(t.cuda() for t in pair)
+
+
+# (blocks by themselves, clusters that share K, pairs)
+@pytest.mark.parametrize("n,k", [(64, 96), (160, 9216), (2816, 1024)])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("up_scale", [127, 140, 250])
+def test_gates_far_from_zero(n, k, sign, up_scale):
+    """Gates of 60 to 104 on either side times 1, 2^13 and 2^123: results that fp32 holds are there,
+    however small their gate is.  Both sums are exact: three products and one."""
+    z = torch.arange(60, 104.25, 0.25, dtype=torch.float64)
+    parts = torch.stack([z - z % 8, (z % 8).floor(), z % 1], 1)
+    codes = torch.searchsorted(ref.E4M3[:127], parts)
+    assert torch.equal(ref.E4M3[codes], parts)
+    m = len(z)
+    x = torch.zeros(m, k, dtype=torch.uint8)
+    x[:, [0, 9, 31]] = (codes + (128 if sign < 0 else 0)).to(torch.uint8)
+    x[:, 32] = 0x38                                                       # 1
+    xs = torch.full((m, k // 32), 127, dtype=torch.uint8)
+    gate, up = (torch.zeros(n, k, dtype=torch.long) for _ in range(2))
+    gate[:, [0, 9, 31]] = 2
+    up[:, 32] = 2
+    gs, us = torch.full((n, k // 32), 127, dtype=torch.uint8), torch.full((n, k // 32), up_scale, dtype=torch.uint8)
+    h = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+    c, s = torch.zeros(m, n, dtype=torch.uint8, device="cuda"), torch.zeros(m, n // 32, dtype=torch.uint8, device="cuda")
+    q.mx_swiglu(dev((ref.pack4(gate), gs)), dev((ref.pack4(up), us)), dev((x, xs)), h=h, codes=c, scales=s)
+    z, u = sign * z, 2.0 ** (up_scale - 127)
+    want = z * torch.sigmoid(z) * u
+    # e^-|z|: 2 + 1.18 |z| units in the last place (2^-23), half a unit of the smallest subnormal;
+    # z e^z, 1 + e and the product with u half a unit each, the division two
+    tol = want.abs() * (2.0 ** -20 + z.abs() * 2.0 ** -22) + z.abs() * 2.0 ** -149 * u
+    want, tol = want[:, None].expand(m, n), tol[:, None].expand(m, n)
+    ref.near(h, want, tol, "fp16")
+    if sign > 0 and up_scale == 250:
+        # 60 * 2^123 = 1.9 * 2^128 and more: no fp32 value, an infinity, whose blocks are NaN
+        assert float(want.min()) > 2.0 ** 128 and bool((s == 255).all()) and bool(torch.isinf(h).all())
+        return
+    ref.check_mx8(c.cpu(), s.cpu(), want, tol, "MXFP8")
+    assert q.device_status() == 0
