@@ -29,7 +29,7 @@ static gated_fn gated_c;
 
 /* torch.float16, uint8, float8_e4m3fn, int32, uint32; the current device and a device's stream */
 static PyObject *half_, *u8_, *e4m3_, *i32_, *u32_, *get_device_, *get_stream_;
-static PyObject *s_dtype, *s_device, *s_contiguous, *s_numel, *s_size, *s_ptr, *minus_one;
+static PyObject *s_dtype, *s_device, *s_contiguous, *s_shape, *s_ptr;
 
 /* A method's whole number; -1 with *ok = 0 where there is none (the exception is dropped: the
  * caller finds out by itself). */
@@ -53,12 +53,36 @@ static long long ask(PyObject *t, PyObject *method, int *ok) {
   return number(PyObject_CallMethodNoArgs(t, method), ok);
 }
 
-static long long last_axis(PyObject *t, int *ok) {
-  return number(PyObject_CallMethodOneArg(t, s_size, minus_one), ok);
+/* A tensor's number of values, first and last axis; one without axes fits nothing. */
+typedef struct {
+  long long count, first, last;
+} Shape;
+
+static Shape shape_of(PyObject *t, int *ok) {
+  Shape s = {1, -1, -1};
+  PyObject *r = PyObject_GetAttr(t, s_shape);
+  Py_ssize_t i, n;
+  if (r == NULL || !PyTuple_Check(r) || PyTuple_GET_SIZE(r) == 0) {
+    Py_XDECREF(r);
+    PyErr_Clear();
+    *ok = 0;
+    return s;
+  }
+  n = PyTuple_GET_SIZE(r);
+  for (i = 0; i < n && *ok; ++i) {
+    s.last = PyLong_AsLongLong(PyTuple_GET_ITEM(r, i));
+    if (s.last < 0 || __builtin_mul_overflow(s.count, s.last, &s.count)) {
+      PyErr_Clear();
+      *ok = 0;
+    }
+    if (i == 0) s.first = s.last;
+  }
+  Py_DECREF(r);
+  return s;
 }
 
-/* Whether t is of type a or b, contiguous, on GPU `index`, with `count` values. */
-static int fits(PyObject *t, PyObject *a, PyObject *b, long long index, long long count) {
+/* Whether t is of type a or b, contiguous and on GPU `index`. */
+static int is_on(PyObject *t, PyObject *a, PyObject *b, long long index) {
   int ok = 1;
   PyObject *r = PyObject_GetAttr(t, s_dtype);
   if (r == NULL) {
@@ -73,8 +97,15 @@ static int fits(PyObject *t, PyObject *a, PyObject *b, long long index, long lon
     return 0;
   }
   Py_DECREF(r);
-  if (r != Py_True) return 0;
-  return ask(t, s_device, &ok) == index && ask(t, s_numel, &ok) == count && ok;
+  return r == Py_True && ask(t, s_device, &ok) == index && ok;
+}
+
+/* And has `count` values in rows of `last`.  (Rows of scales are looked at as those of values
+ * are: the scales of a transposed matrix are as many.) */
+static int fits(PyObject *t, PyObject *a, PyObject *b, long long index, long long count, long long last) {
+  int ok = 1;
+  const Shape s = shape_of(t, &ok);
+  return ok && s.count == count && s.last == last && is_on(t, a, b, index);
 }
 
 static void *address(PyObject *t, int *ok) { return (void *)(intptr_t)ask(t, s_ptr, ok); }
@@ -110,114 +141,108 @@ static int small(long long a, long long b) { return a >= 0 && b >= 0 && a <= INT
 /* x, bits, codes, scales */
 static PyObject *quantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   int ok = 1, bits, rc;
-  long long index, count, k, m;
+  long long index;
+  Shape s;
   void *x, *codes, *scales, *st;
   if (n != 4) Py_RETURN_NONE;
   index = here(a[0], &ok);
   if (index < 0) Py_RETURN_NONE;
-  count = ask(a[0], s_numel, &ok);
-  k = last_axis(a[0], &ok);
+  s = shape_of(a[0], &ok);
   bits = (int)PyLong_AsLong(a[1]);
   if (PyErr_Occurred()) PyErr_Clear();
-  if (!ok || k <= 0 || k % 32 != 0 || (bits != 4 && bits != 8)) Py_RETURN_NONE;
-  m = count / k;
-  if (!fits(a[0], half_, half_, index, count)) Py_RETURN_NONE;
-  if (bits == 8 ? !fits(a[2], u8_, e4m3_, index, count) : !fits(a[2], i32_, u32_, index, count / 8)) Py_RETURN_NONE;
-  if (!fits(a[3], u8_, u8_, index, count / 32) || last_axis(a[2], &ok) != (bits == 8 ? k : k / 8)) Py_RETURN_NONE;
+  if (!ok || s.last <= 0 || s.last % 32 != 0 || (bits != 4 && bits != 8)) Py_RETURN_NONE;
+  if (!is_on(a[0], half_, half_, index) || !fits(a[3], u8_, u8_, index, s.count / 32, s.last / 32)) Py_RETURN_NONE;
+  if (bits == 8 ? !fits(a[2], u8_, e4m3_, index, s.count, s.last) : !fits(a[2], i32_, u32_, index, s.count / 8, s.last / 8))
+    Py_RETURN_NONE;
   x = address(a[0], &ok), codes = address(a[2], &ok), scales = address(a[3], &ok), st = stream_of(index, &ok);
-  if (!ok || !small(m, k)) Py_RETURN_NONE;
-  CALL(rc, quantize_c(bits, x, (int)m, (int)k, codes, scales, st))
+  if (!ok || !small(s.count / s.last, s.last)) Py_RETURN_NONE;
+  CALL(rc, quantize_c(bits, x, (int)(s.count / s.last), (int)s.last, codes, scales, st))
   return PyLong_FromLong(rc);
 }
 
 /* codes, scales, out */
 static PyObject *dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   int ok = 1, bits = 8, rc;
-  long long index, count, k, m;
+  long long index;
+  Shape s;
   void *codes, *scales, *out, *st;
   if (n != 3) Py_RETURN_NONE;
   index = here(a[0], &ok);
   if (index < 0) Py_RETURN_NONE;
-  count = ask(a[0], s_numel, &ok);
-  k = last_axis(a[0], &ok);
+  s = shape_of(a[0], &ok);
   if (!ok) Py_RETURN_NONE;
-  if (!fits(a[0], u8_, e4m3_, index, count)) {
-    if (!fits(a[0], i32_, u32_, index, count)) Py_RETURN_NONE;
+  if (!is_on(a[0], u8_, e4m3_, index)) {
+    if (!is_on(a[0], i32_, u32_, index)) Py_RETURN_NONE;
     bits = 4;
-    count *= 8;
-    k *= 8;
+    s.count *= 8;
+    s.last *= 8;
   }
-  if (k <= 0 || k % 32 != 0) Py_RETURN_NONE;
-  m = count / k;
-  if (!fits(a[1], u8_, u8_, index, count / 32) || !fits(a[2], half_, half_, index, count) ||
-      last_axis(a[2], &ok) != k)
+  if (s.last <= 0 || s.last % 32 != 0) Py_RETURN_NONE;
+  if (!fits(a[1], u8_, u8_, index, s.count / 32, s.last / 32) || !fits(a[2], half_, half_, index, s.count, s.last))
     Py_RETURN_NONE;
   codes = address(a[0], &ok), scales = address(a[1], &ok), out = address(a[2], &ok), st = stream_of(index, &ok);
-  if (!ok || !small(m, k)) Py_RETURN_NONE;
-  CALL(rc, dequantize_c(bits, codes, scales, (int)m, (int)k, out, st))
+  if (!ok || !small(s.count / s.last, s.last)) Py_RETURN_NONE;
+  CALL(rc, dequantize_c(bits, codes, scales, (int)(s.count / s.last), (int)s.last, out, st))
   return PyLong_FromLong(rc);
 }
 
 /* x, gamma, residual or None, eps, h (anything without a residual), codes, scales */
 static PyObject *norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   int ok = 1, rc;
-  long long index, count, k, m;
+  long long index, count, k;
+  Shape s, g;
   double eps;
   void *x, *gamma, *res = NULL, *h = NULL, *codes, *scales, *st;
   if (n != 7) Py_RETURN_NONE;
   index = here(a[0], &ok);
   if (index < 0) Py_RETURN_NONE;
-  count = ask(a[0], s_numel, &ok);
-  k = last_axis(a[0], &ok);
+  s = shape_of(a[0], &ok), g = shape_of(a[1], &ok);
+  count = s.count, k = s.last;
   eps = PyFloat_AsDouble(a[3]);
   if (PyErr_Occurred()) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
-  if (!ok || k <= 0 || k % 32 != 0) Py_RETURN_NONE;
-  m = count / k;
-  if (!fits(a[0], half_, half_, index, count) || !fits(a[1], half_, half_, index, k) ||
-      !fits(a[5], u8_, e4m3_, index, count) || !fits(a[6], u8_, u8_, index, count / 32) ||
-      last_axis(a[5], &ok) != k)
+  if (!ok || k <= 0 || k % 32 != 0 || g.count != k) Py_RETURN_NONE;
+  if (!is_on(a[0], half_, half_, index) || !is_on(a[1], half_, half_, index) ||
+      !fits(a[5], u8_, e4m3_, index, count, k) || !fits(a[6], u8_, u8_, index, count / 32, k / 32))
     Py_RETURN_NONE;
   if (a[2] != Py_None) {
-    if (!fits(a[2], half_, half_, index, count) || !fits(a[4], half_, half_, index, count) ||
-        last_axis(a[2], &ok) != k || last_axis(a[4], &ok) != k)
-      Py_RETURN_NONE;
+    if (!fits(a[2], half_, half_, index, count, k) || !fits(a[4], half_, half_, index, count, k)) Py_RETURN_NONE;
     res = address(a[2], &ok), h = address(a[4], &ok);
   }
   x = address(a[0], &ok), gamma = address(a[1], &ok), codes = address(a[5], &ok), scales = address(a[6], &ok);
   st = stream_of(index, &ok);
-  if (!ok || !small(m, k)) Py_RETURN_NONE;
-  CALL(rc, norm_c(x, res, gamma, (float)eps, (int)m, (int)k, h, codes, scales, st))
+  if (!ok || !small(count / k, k)) Py_RETURN_NONE;
+  CALL(rc, norm_c(x, res, gamma, (float)eps, (int)(count / k), (int)k, h, codes, scales, st))
   return PyLong_FromLong(rc);
 }
 
-/* An MXFP4 weight, codes [n][k / 8] and scales: its rows and columns. */
+/* An MXFP4 weight, codes [n][k / 8] and scales [n][k / 32]: its rows and columns. */
 static int weight(PyObject *codes, PyObject *scales, long long index, long long *n, long long *k) {
   int ok = 1;
-  const long long count = ask(codes, s_numel, &ok), words = last_axis(codes, &ok);
-  if (!ok || words <= 0 || words % 4 != 0) return 0;
-  *n = count / words;
-  *k = 8 * words;
-  return fits(codes, i32_, u32_, index, count) && fits(scales, u8_, u8_, index, count / 4);
+  const Shape s = shape_of(codes, &ok);
+  if (!ok || s.last <= 0 || s.last % 4 != 0 || s.first != s.count / s.last) return 0;
+  *n = s.first;
+  *k = 8 * s.last;
+  return is_on(codes, i32_, u32_, index) && fits(scales, u8_, u8_, index, s.count / 4, s.last / 4);
 }
 
 /* codes, scales, x, y, residual or None */
 static PyObject *matvec(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   int ok = 1, rc;
-  long long index, rows, k, count, m;
+  long long index, rows, k, m;
+  Shape x_shape;
   void *w, *s, *x, *y, *res = NULL, *st;
   if (n != 5) Py_RETURN_NONE;
   index = here(a[2], &ok);
   if (index < 0 || !weight(a[0], a[1], index, &rows, &k)) Py_RETURN_NONE;
-  count = ask(a[2], s_numel, &ok);
-  m = count / k;
-  if (!ok || !fits(a[2], half_, half_, index, count) || last_axis(a[2], &ok) != k ||
-      !fits(a[3], half_, half_, index, m * rows) || last_axis(a[3], &ok) != rows)
+  x_shape = shape_of(a[2], &ok);
+  m = x_shape.count / k;
+  if (!ok || x_shape.last != k || !is_on(a[2], half_, half_, index) || !fits(a[3], half_, half_, index, m * rows, rows))
     Py_RETURN_NONE;
   if (a[4] != Py_None) {
-    if (!fits(a[4], half_, half_, index, m * rows) || last_axis(a[4], &ok) != rows) Py_RETURN_NONE;
+    if (!fits(a[4], half_, half_, index, m * rows, rows)) Py_RETURN_NONE;
     res = address(a[4], &ok);
   }
   w = address(a[0], &ok), s = address(a[1], &ok), x = address(a[2], &ok), y = address(a[3], &ok);
@@ -230,10 +255,9 @@ static PyObject *matvec(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 /* MXFP8 rows of k columns: how many. */
 static int activations(PyObject *codes, PyObject *scales, long long index, long long k, long long *m) {
   int ok = 1;
-  const long long count = ask(codes, s_numel, &ok);
-  *m = count / k;
-  return ok && fits(codes, u8_, e4m3_, index, count) && fits(scales, u8_, u8_, index, count / 32) &&
-         last_axis(codes, &ok) == k && ok;
+  const Shape s = shape_of(codes, &ok);
+  *m = s.count / k;
+  return ok && s.last == k && is_on(codes, u8_, e4m3_, index) && fits(scales, u8_, u8_, index, s.count / 32, k / 32);
 }
 
 /* codes, scales, x codes, x scales, y, residual or None */
@@ -244,9 +268,9 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (n != 6) Py_RETURN_NONE;
   index = here(a[2], &ok);
   if (index < 0 || !weight(a[0], a[1], index, &rows, &k) || !activations(a[2], a[3], index, k, &m)) Py_RETURN_NONE;
-  if (!fits(a[4], half_, half_, index, m * rows) || last_axis(a[4], &ok) != rows) Py_RETURN_NONE;
+  if (!fits(a[4], half_, half_, index, m * rows, rows)) Py_RETURN_NONE;
   if (a[5] != Py_None) {
-    if (!fits(a[5], half_, half_, index, m * rows) || last_axis(a[5], &ok) != rows) Py_RETURN_NONE;
+    if (!fits(a[5], half_, half_, index, m * rows, rows)) Py_RETURN_NONE;
     res = address(a[5], &ok);
   }
   w = address(a[0], &ok), s = address(a[1], &ok), x = address(a[2], &ok), xs = address(a[3], &ok);
@@ -266,10 +290,10 @@ static PyObject *gated(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (index < 0 || !weight(a[0], a[1], index, &rows, &k) || !weight(a[2], a[3], index, &rows2, &k2) || rows != rows2 ||
       k != k2 || !activations(a[4], a[5], index, k, &m))
     Py_RETURN_NONE;
-  if (a[6] != Py_None && (!fits(a[6], half_, half_, index, m * rows) || last_axis(a[6], &ok) != rows)) Py_RETURN_NONE;
+  if (a[6] != Py_None && !fits(a[6], half_, half_, index, m * rows, rows)) Py_RETURN_NONE;
   if ((a[7] == Py_None) != (a[8] == Py_None)) Py_RETURN_NONE;
-  if (a[7] != Py_None && (rows % 32 != 0 || !fits(a[7], u8_, e4m3_, index, m * rows) || last_axis(a[7], &ok) != rows ||
-                          !fits(a[8], u8_, u8_, index, m * (rows / 32))))
+  if (a[7] != Py_None && (rows % 32 != 0 || !fits(a[7], u8_, e4m3_, index, m * rows, rows) ||
+                          !fits(a[8], u8_, u8_, index, m * (rows / 32), rows / 32)))
     Py_RETURN_NONE;
   for (i = 0; i < 9; ++i)
     if (a[i] != Py_None) p[i] = address(a[i], &ok);
@@ -311,9 +335,7 @@ PyMODINIT_FUNC PyInit__mx_calls(void) {
   s_dtype = PyUnicode_InternFromString("dtype");
   s_device = PyUnicode_InternFromString("get_device");
   s_contiguous = PyUnicode_InternFromString("is_contiguous");
-  s_numel = PyUnicode_InternFromString("numel");
-  s_size = PyUnicode_InternFromString("size");
+  s_shape = PyUnicode_InternFromString("shape");
   s_ptr = PyUnicode_InternFromString("data_ptr");
-  minus_one = PyLong_FromLong(-1);
   return PyModule_Create(&module);
 }

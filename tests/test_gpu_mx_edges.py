@@ -49,3 +49,30 @@ def test_gates_far_from_zero(n, k, sign, up_scale):
         return
     ref.check_mx8(c.cpu(), s.cpu(), want, tol, "MXFP8")
     assert q.device_status() == 0
+
+
+def test_scales_of_another_shape_are_refused():
+    """As many scales as there are blocks, but in a transposed matrix or a flat array; weights in a stack."""
+    n, m, k = 96, 6, 128
+    x = torch.ones(m, k, dtype=torch.float16, device="cuda")
+    codes, scales = q.mx_quantize(torch.ones(n, k, dtype=torch.float16, device="cuda"), 4)
+    xc, xs = q.mx_quantize(x)
+    c4, s4 = q.mx_quantize(x, 4)
+    w, gamma = (codes, scales), torch.ones(k, dtype=torch.float16, device="cuda")
+    y = torch.zeros(m, n, dtype=torch.float16, device="cuda")
+    for wrong in (lambda t: t.t().contiguous(), lambda t: t.flatten(), lambda t: t.unsqueeze(-1)):
+        for call in (lambda: q.mx_quantize(x, 8, scales=wrong(xs)), lambda: q.mx_quantize(x, 4, scales=wrong(s4)),
+                     lambda: q.mx_dequantize(xc, wrong(xs)), lambda: q.mx_dequantize(c4, wrong(s4)),
+                     lambda: q.residual_rmsnorm_mxfp8(x, gamma, scales=wrong(xs)),
+                     lambda: q.qgemv_mxfp4((codes, wrong(scales)), x), lambda: q.mx_gemm((codes, wrong(scales)), (xc, xs)),
+                     lambda: q.mx_gemm(w, (xc, wrong(xs))), lambda: q.mx_swiglu((codes, wrong(scales)), w, (xc, xs)),
+                     lambda: q.mx_swiglu(w, (codes, wrong(scales)), (xc, xs)), lambda: q.mx_swiglu(w, w, (xc, wrong(xs))),
+                     lambda: q.mx_swiglu(w, w, (xc, xs), scales=wrong(torch.zeros(m, n // 32, dtype=torch.uint8, device="cuda")))):
+            with pytest.raises(ValueError):
+                call()
+    stack = (codes.view(4, 24, k // 8), scales.view(4, 24, k // 32))
+    for call in (lambda: q.qgemv_mxfp4(stack, x, y=y), lambda: q.mx_gemm(stack, (xc, xs), y=y),
+                 lambda: q.mx_swiglu(stack, w, (xc, xs), h=y), lambda: q.mx_swiglu(w, stack, (xc, xs), h=y)):
+        with pytest.raises(ValueError):
+            call()
+    assert q.mx_gemm(w, (xc, xs), y=y) is y
