@@ -6,10 +6,14 @@
 // A tile is 128 weight rows (the instruction's A operand, 4-bit codes as they are
 // stored, spread to bytes by the copy itself) by up to 240 columns (B, e4m3): nothing
 // is dequantised by arithmetic, the scales go to tensor memory and into the product.
-// Columns are the MXFP8 rows of x, or for fp16 rows three columns each: x / 2^e1 = q1 +
-// q2 / 2^4 + q3 / 2^9 with e4m3 q1, q2, q3 and e1 = floor(log2 of the block's largest) - 7.
-// Each q takes four bits of what is left, so the eleven bits of an fp16 value are
-// all held, down to 2^-26 of the block's largest value; the three sums are added in fp32.
+// Columns are the MXFP8 rows of x, or for fp16 rows four columns each: x / 2^e1 = q1 +
+// q2 / 2^5 + q3 / 2^10 + q4 / 2^28 with e4m3 q and e1 = floor(log2 of the block's largest) - 7.
+// Three columns hold the eleven bits of a value down to 2^-26 of the block's largest value; what
+// they leave of smaller ones is 2^-27 of it at most, for the fourth.  So an fp16 value is held
+// exactly where the largest of its block is below 256 (all that fp16 has is then above its grid),
+// else to 2^-32 of the largest and to a 16th of itself at least.  The four sums are added in
+// fp32.  (With three columns, 2^-9 below the first, entries beside one of 60000 were lost from
+// 2^-27 of it on; the fourth costs no tensor time: up to 32 columns take the instruction as long as 16.)
 //
 // A step is 128 k: a ring of stages (codes of A and, for MXFP8 rows, of B, 128-byte
 // swizzled, and their scales) between
@@ -41,6 +45,7 @@ constexpr int kRowsW = kMxRows, kStepK = kMxStep;
 constexpr int kLoaders = 4;   // warps
 constexpr int kTmaWarps = 2;
 constexpr int kScaleCols = 16;  // tensor memory of one step's scales
+constexpr int kSplitCols = kMxSplitCols;
 
 // How a launch loads its operands.
 struct MxLoads {
@@ -144,11 +149,11 @@ __device__ __forceinline__ __half2 power2(int k) {
   return *reinterpret_cast<const __half2*>(&w);
 }
 
-// Eight values of row m of x (a lane; four lanes hold a block) to three columns: their
-// codes at `cols` (a step's, swizzled), the blocks' scales at `scales`.  All in fp16, and
-// exact: x / 2^e1 is below 2^8, what its rounding to e4m3 leaves is a multiple of x's last
-// bit and at most half a step, and the factors are powers of two (only what is below 2^-24
-// after the division is rounded: 2^-31 of the block's largest value).
+// Eight values of row m of x (a lane; four lanes hold a block) to four columns: their codes at
+// `cols` (a step's, swizzled), the blocks' scales at `scales`.  All in fp16: x is multiplied by
+// 2^k, which puts the block's largest above 2^15 (or all of x, where that is below 2^-15, on
+// whole numbers), and what a column leaves is a multiple of x's last bit and no larger than x
+// was, so the subtractions are exact.
 __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, uint32_t scales, int m,
                                              int ch) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -157,28 +162,30 @@ __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, 
   most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
   most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
   const uint32_t top = max(most & 0xFFFFu, most >> 16);  // bits of the largest magnitude
-  // e1 + 127, at least that of 2^-23
   const int e = static_cast<int>(__float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(top)))) >> 23);
-  const int byte = max(e, 104) - 7, k = 127 - byte;      // multiplied by 2^k, -8 <= k <= 30
+  const int k = min(max(15 + 127 - e, 0), 30), byte = 127 + 8 - k;
   const __half2 k0 = power2(min(k, 15)), k1 = power2(max(k - 15, 0));
   __half2 f[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[i]), k0), k1);
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const __half2 next = power2(q == 0 ? 4 : 5);
+  for (int q = 0; q < kSplitCols; ++q) {
+    const int down = q < 3 ? 8 - 5 * q : -20;  // the column's unit is 2^down of f's
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint16_t two;
       uint32_t got;
-      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&f[i])));
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(got) : "h"(two));
-      f[i] = __hmul2(__hsub2(f[i], *reinterpret_cast<const __half2*>(&got)), next);
+      const __half2 to = q < 3 ? __hmul2(f[i], power2(-down)) : __hmul2(__hmul2(f[i], power2(15)), power2(-down - 15));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&to)));
+      if (q < 3) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(got) : "h"(two));
+        f[i] = __hfma2(*reinterpret_cast<const __half2*>(&got), __hneg2(power2(down)), f[i]);
+      }
       w[i >> 1] = i & 1 ? w[i >> 1] | (static_cast<uint32_t>(two) << 16) : two;
     }
-    const int c = 3 * m + q;
-    const int sb = top >= 0x7C00u ? 255 : byte - (q == 0 ? 0 : q == 1 ? 4 : 9);
+    const int c = kSplitCols * m + q;
+    const int sb = top >= 0x7C00u ? 255 : byte + down - 8;
     if (live) {
       asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(cols + c * 128 + (((ch >> 1) ^ (c & 7)) << 4) +
                                                            (ch & 1) * 8),
@@ -190,8 +197,8 @@ __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, 
   }
 }
 
-// GATED: two weights.  SPLIT3: fp16 rows.
-template <bool GATED, bool SPLIT3>
+// GATED: two weights.  SPLIT: fp16 rows.
+template <bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_product_kernel(const MxProductArgs a, const MxPlan p, const MxLoads ld, const __grid_constant__ CUtensorMap w_map,
                       const __grid_constant__ CUtensorMap u_map, const __grid_constant__ CUtensorMap x_map) {
@@ -205,12 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = p.split > 1 ? tc::uniform(static_cast<int>(cluster_rank())) : 0;
   const uint32_t base = (smem_u32(raw_smem) + 1023) & ~1023u;
   const int b_bytes = p.cols * kStepK;
-  const int c_bytes = kW * 16384 + (SPLIT3 ? 0 : b_bytes);        // a stage: A (, up) (, B)
-  const int s_bytes = 512 * (kW + (SPLIT3 ? 0 : p.cols > 128 ? 2 : 1));  // and their scales
+  const int c_bytes = kW * 16384 + (SPLIT ? 0 : b_bytes);        // a stage: A (, up) (, B)
+  const int s_bytes = 512 * (kW + (SPLIT ? 0 : p.cols > 128 ? 2 : 1));  // and their scales
   const uint32_t x_cols = base + p.stages * c_bytes;              // columns of fp16 rows
-  const uint32_t s_ring = x_cols + (SPLIT3 ? p.row_steps * b_bytes : 0);
+  const uint32_t s_ring = x_cols + (SPLIT ? p.row_steps * b_bytes : 0);
   const uint32_t x_scales = s_ring + p.stages * s_bytes;
-  const uint32_t part = x_scales + (SPLIT3 ? p.row_steps * 512 : 0);
+  const uint32_t part = x_scales + (SPLIT ? p.row_steps * 512 : 0);
 
   const int steps = (a.K + kStepK - 1) / kStepK;
   const int k0 = static_cast<int>(static_cast<long long>(steps) * rank / p.split);
@@ -224,13 +231,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     *tok = (p.rows_first ? o : i) * p.tokens;
   };
 
+  // Where the columns of fp16 rows leave room for few stages, a tile's weights are on their way to
+  // L2 this many steps ahead (5 rows of K = 14336 to 4096 12.4 -> 10.8 us).
+  constexpr int ahead = SPLIT ? 12 : 0;
   // The first tile's weights on their way to L2 while the kernel before ends.
   if (first < tiles) {
     int row, tok;
     place(first, &row, &tok);
     if (warp == kTmaWarp && lane == 0) {
       if (ld.tma_w) {
-        for (int k = k0; k < k1 && k < k0 + p.stages; ++k) {
+        for (int k = k0; k < k1 && k < k0 + max(p.stages, ahead); ++k) {
           tc::prefetch_2d(&w_map, k * kStepK, row);
           if (GATED) tc::prefetch_2d(&u_map, k * kStepK, row);
         }
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0) {
     if (lane < p.stages) {
-      mbar_init(smem_u32(&bars.full[lane]), 1 + (ld.tma_w ? 0 : 32) + (ld.tma_w || !SPLIT3 ? 1 : 0));
+      mbar_init(smem_u32(&bars.full[lane]), 1 + (ld.tma_w ? 0 : 32) + (ld.tma_w || !SPLIT ? 1 : 0));
       mbar_init(smem_u32(&bars.empty[lane]), kW);
     }
     if (lane < kLoaders) mbar_init(smem_u32(&bars.turn[lane]), 1);
@@ -259,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars.part_done), kOutWarps * p.split);
       s_failed = 0;
     }
-    if constexpr (SPLIT3)
+    if constexpr (SPLIT)
       for (int i = lane; i < k1 - k0; i += 32) mbar_init(smem_u32(&bars.rows[i]), 1);
     fence_mbar_init();
   }
@@ -289,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp >= kTmaWarp) {
     // ---------------------------------------------------------------- codes
-    const uint32_t bytes = (ld.tma_w ? kW * 8192 : 0) + (SPLIT3 ? 0 : b_bytes);
+    const uint32_t bytes = (ld.tma_w ? kW * 8192 : 0) + (SPLIT ? 0 : b_bytes);
     Steps s = start(warp - kTmaWarp);
     int row = 0, tok = 0;
     for (; find(s); s.k += kTmaWarps, s.stage += kTmaWarps) {
@@ -302,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ld.tma_w) {
           tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
           if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
+          if (SPLIT && p.stages < ahead && s.k + ahead < k1) tc::prefetch_2d(&w_map, (s.k + ahead) * kStepK, row);
         }
-        if (!SPLIT3) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
+        if (!SPLIT) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
       }
       __syncwarp();
       if (!ld.tma_w) {
@@ -341,16 +352,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = tm + (buf * (two ? 2 : 1) + me) * p.cols;
       for (int k = k0; k < k1; ++k) {
         if (GATED || !p.pair || odd == me) {
-          if (SPLIT3 && n == 0) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
+          if (SPLIT && n == 0) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
           step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
           if (!ld.tma_w) tc::fence_async_shared();  // codes by cp.async, for the tensor core
           tc::fence_after();
           if (tc::elect_one()) {
             const uint32_t st = tm + kMxAccCols + (two ? me : k & 1) * kScaleCols;
             tc::copy_scales(st, ss + (GATED ? me * 512 : 0));
-            tc::copy_scales(st + 8, SPLIT3 ? x_scales + (k - k0) * 512 : ss + kW * 512);
+            tc::copy_scales(st + 8, SPLIT ? x_scales + (k - k0) * 512 : ss + kW * 512);
             if (p.cols > 128) tc::copy_scales(st + 12, ss + (kW + 1) * 512);
-            const uint64_t b = tc::desc_k_major(SPLIT3 ? x_cols + (k - k0) * b_bytes : c + kW * 16384);
+            const uint64_t b = tc::desc_k_major(SPLIT ? x_cols + (k - k0) * b_bytes : c + kW * 16384);
             const uint64_t w = tc::desc_k_major(c + (GATED ? me * 16384 : 0));
             const int more = k > k0 + (!GATED && p.pair ? 1 : 0);
 #pragma unroll
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kLoadWarp) {
     // ---------------------------------------------------------------- loads
-    constexpr int kRowsX = SPLIT3 ? 0 : GATED ? 4 : 8;  // rows of x a lane has scales of
+    constexpr int kRowsX = SPLIT ? 0 : GATED ? 4 : 8;  // rows of x a lane has scales of
     const int me = warp - kLoadWarp, blocks = a.K / kMxBlock, my_steps = k1 - k0;
     const int q0 = k0 >> 2, groups = ((k1 - 1) >> 2) - q0 + 1;  // of four steps, of a tile
     const long long all = first < tiles ? ((tiles - 1 - first) / stride + 1) * groups : 0;
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ld.bytes == 1) {
       w_ends = ends_of(a.ws, a.ws + static_cast<long long>(a.N) * blocks);
       if (GATED) u_ends = ends_of(a.us, a.us + static_cast<long long>(a.N) * blocks);
-      if (!SPLIT3) x_ends = ends_of(a.xs, a.xs + static_cast<long long>(a.M) * blocks);
+      if (!SPLIT) x_ends = ends_of(a.xs, a.xs + static_cast<long long>(a.M) * blocks);
     }
     for (long long g = me; g < all; g += kLoaders) {
       const long long turn = g / groups;
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return r > 0 && static_cast<long long>(r) * blocks >= 3 && r + rows < end &&
                  static_cast<long long>(end - r - rows) * blocks >= 20;
         };
-        if (inside(row, kRowsW, a.N) && (SPLIT3 || inside(tok, x_rows, a.M))) {
+        if (inside(row, kRowsW, a.N) && (SPLIT || inside(tok, x_rows, a.M))) {
           load_all([&](int operand, int r, int end) { return sixteen_within(at(operand, end > 0 ? r : tok), n); });
         } else {
           load_all([&](int operand, int r, int end) {
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- results
     const int quarter = warp & 3, half = warp >> 2;  // lanes of tensor memory; which columns
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 21);
-    if constexpr (SPLIT3) {
+    if constexpr (SPLIT) {
       // the block's share of the fp16 rows, a step a warp, two rows of x at a time
       for (int i = warp; i < k1 - k0 && first < tiles; i += kOutWarps) {
         const int ch = lane & 15, at = (k0 + i) * kStepK + ch * 8;
@@ -531,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (GATED) send(to + kRowsW * 4, u, bar);
       };
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
-      if constexpr (SPLIT3) {
-        // four rows of x a warp: 12 columns
-        const int m0 = 4 * half, c0 = 12 * half;
+      if constexpr (SPLIT) {
+        // four rows of x a warp: 16 columns
+        const int m0 = 4 * half, c0 = 16 * half;
         if (ok && m0 < count) {
           float v[4];
           uint32_t x0[16], x1[16];
@@ -545,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_ld16(x1);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            float q[3];
+            float q[4];
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              q[c] = (has0 ? __uint_as_float(x0[3 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[3 * m + c]) : 0.f);
-            v[m] += (q[2] + q[1]) + q[0];
+            for (int c = 0; c < 4; ++c)
+              q[c] = (has0 ? __uint_as_float(x0[4 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[4 * m + c]) : 0.f);
+            v[m] += ((q[3] + q[2]) + q[1]) + q[0];
           }
           if (p.split == 1) {
             write_results<GATED>(a, n, m0, count - m0, v, lane);
@@ -759,10 +770,10 @@ const Plans* known_plans(const MxShape& s) {
   return &at;
 }
 
-template <bool GATED, bool SPLIT3>
+template <bool GATED, bool SPLIT>
 cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  auto* k = mx_product_kernel<GATED, SPLIT3>;
+  auto* k = mx_product_kernel<GATED, SPLIT>;
   const unsigned long long bit = 1ull << (device & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
@@ -770,7 +781,7 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  MxShape shape{a.M, a.N, a.K, GATED, SPLIT3, {}};
+  MxShape shape{a.M, a.N, a.K, GATED, SPLIT, {}};
   for (int i = 0; i < 4; ++i) shape.clusters[i] = clusters_at_a_time(k, i, sms, device);
   const Plans* plans = known_plans(shape);
   if (plans == nullptr) return cudaErrorInvalidValue;
@@ -787,7 +798,7 @@ cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st)
   if (ld.tma_w && (!encode_codes(&wm, a.w, true, a.N, a.K, kRowsW) ||
                   (GATED && !encode_codes(&um, a.up, true, a.N, a.K, kRowsW))))
     return cudaErrorInvalidValue;
-  if (!SPLIT3 && !encode_codes(&xm, a.x, false, a.M, a.K, p.cols)) return cudaErrorInvalidValue;
+  if (!SPLIT && !encode_codes(&xm, a.x, false, a.M, a.K, p.cols)) return cudaErrorInvalidValue;
   const long long tiles = static_cast<long long>(p.row_tiles) * p.tok_tiles;
   const long long most = shape.clusters[__builtin_ctz(p.split)], clusters = tiles < most ? tiles : most;
   cudaLaunchConfig_t cfg = {};

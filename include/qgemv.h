@@ -686,8 +686,10 @@ int qgemv_residual_rmsnorm_mxfp8(const uint16_t *x, const uint16_t *residual,
  * qgemv_mxfp4 -- y[m][n] = sum_k w[n][k] x[m][k] (+ residual[m][n]) for an MXFP4 weight
  * and fp16 activations, the decode form: 1 <= M <= QGEMV_MAX_M, K <= QGEMV_MXFP4_MAX_K
  * (the activations stay on chip).  x [M][K], y, residual
- * (NULL: none; may equal y) [M][N] fp16.  fp32 sums, one rounding.  A row of x with an
- * infinity or a NaN gives NaN in all of its outputs.  One launch.
+ * (NULL: none; may equal y) [M][N] fp16.  fp32 sums, one rounding.  x is taken apart into
+ * 8-bit pieces: a value counts exactly where the largest magnitude of its block of 32 is
+ * below 256, else to 2^-32 of that largest (and never to less than a 16th of itself).  A row
+ * of x with an infinity or a NaN gives NaN in all of its outputs.  One launch.
  */
 int qgemv_mxfp4(const uint32_t *codes, const uint8_t *scales, const uint16_t *x, uint16_t *y,
                 int M, int N, int K, const uint16_t *residual, void *stream);

@@ -76,3 +76,49 @@ def test_scales_of_another_shape_are_refused():
         with pytest.raises(ValueError):
             call()
     assert q.mx_gemm(w, (xc, xs), y=y) is y
+
+
+@pytest.mark.parametrize("top", [65504.0, 33000.0, 4000.0, 511.75, 256.0, 255.875, 16.0, 7.5, 1.0, 2.0 ** -9, 2.0 ** -16, 2.0 ** -23])
+def test_every_fp16_value_beside_a_larger_one(top):
+    """Every fp16 value up to the largest one of its block, in rows of one to eight: exact where that
+    is below 256, else to 2^-32 of it."""
+    every = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    every = every[torch.isfinite(every) & (every.abs().float() <= top)]
+    k = 1024                                                   # 32 blocks of 31 values and the largest
+    per = 31 * 32
+    rows = -(-every.numel() // per)
+    x = torch.zeros(rows * per, dtype=torch.float16)
+    x[:every.numel()] = every[torch.randperm(every.numel(), generator=torch.Generator().manual_seed(1))]
+    x = torch.cat([torch.full((rows, 32, 1), top, dtype=torch.float16), x.view(rows, 32, 31)], 2).view(rows, k)
+    one = torch.zeros(k, k, dtype=torch.long)
+    one[torch.arange(k), torch.arange(k)] = 2
+    w = dev((ref.pack4(one), torch.full((k, k // 32), 127, dtype=torch.uint8)))
+    got, at = [], 0
+    while at < rows:                                           # 8, 1, 2, ... rows a call
+        n = 8 if at < rows - 20 else 1 + at % 8
+        got.append(q.qgemv_mxfp4(w, x[at:at + n].cuda()).cpu())
+        at += n
+    off = (torch.cat(got).double() - x.double()).abs()
+    # a sum within half a step of the value rounds to it; one further off by as much again at most
+    assert float(off.max()) <= (0.0 if top < 256 else 2 * 2.0 ** -32 * top)
+
+
+@pytest.mark.parametrize("large,small", [(1000.0, 1e-2), (2000.0, 1e-3), (60000.0, 1e-3), (60000.0, 1e-4), (-60000.0, 3e-6),
+                                         (65504.0, 6e-8), (250.0, 6e-8), (1.0, 6e-8)])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 32), (5, 300, 1120), (8, 200, 8192)])
+def test_small_values_beside_one_without_weight(large, small, m, n, k):
+    """The largest value of each block times a weight of 0: nothing of it is in the sum, all of the others is."""
+    g = torch.Generator().manual_seed(m)
+    x = (small * (1 + torch.rand(m, k, generator=g))).half()
+    x.view(m, -1, 32)[:, :, 7] = large
+    numbers = torch.randint(0, 8, (n, k), generator=g)
+    numbers.view(n, -1, 32)[:, :, 7] = 0
+    w = ref.pack4(numbers), torch.full((n, k // 32), 127, dtype=torch.uint8)
+    # a value is held exactly beside less than 256, else to 2^-32 of the largest and a 16th of itself;
+    # no product of the large one is there to align others to
+    y = x.double().clone()
+    y.view(m, -1, 32)[:, :, 7] = 0
+    want, tol = ref.product(w, y)
+    held = torch.minimum(y / 16, torch.tensor(2.0 ** -32 * abs(large), dtype=torch.float64)) * (abs(large) >= 256)
+    ref.near(q.qgemv_mxfp4(dev(w), x.cuda()), want, tol + held @ ref.values(*w).T, "small values")
+    assert q.device_status() == 0
