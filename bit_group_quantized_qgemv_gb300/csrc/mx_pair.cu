@@ -26,8 +26,6 @@
 // issue for both, every other step each into an accumulator of its own (64 columns, K = 14336:
 // 284 clocks a step, 316 with one), with over 96 columns one for all; in the other block they
 // hand on, to rank 0's barrier, that a stage is full there; eight for results.
-#include <atomic>
-
 #include "mx_product.cuh"
 
 namespace qgemv {
@@ -392,14 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool GATED, bool TWO>
 cudaError_t launch(const MxProductArgs& a, const MxPairPlan& p, int clusters, int device, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  auto* k = mx_pair_kernel<GATED, TWO>;
-  const unsigned long long bit = 1ull << (device & 63);
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
+  constexpr auto* k = mx_pair_kernel<GATED, TWO>;
+  if (const cudaError_t e = allow_smem<k>(device); e != cudaSuccess) return e;
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };
   const bool wide16 = a.K % 512 == 0 && mod(a.ws, 16) && mod(a.us, 16) && mod(a.xs, 16);
   const bool wide = a.N % 4 == 0 && mod(a.y, 8) && mod(a.res, 8);
@@ -426,6 +418,15 @@ cudaError_t launch(const MxProductArgs& a, const MxPairPlan& p, int clusters, in
 }
 
 }  // namespace
+
+// (as many as each of the two kernels has: which one a plan takes follows from it)
+int mx_pair_clusters(bool gated, int sms, int device) {
+  const int one = gated ? clusters_at_a_time<mx_pair_kernel<true, false>>(1, kThreads, sms, device)
+                        : clusters_at_a_time<mx_pair_kernel<false, false>>(1, kThreads, sms, device);
+  const int two = gated ? clusters_at_a_time<mx_pair_kernel<true, true>>(1, kThreads, sms, device)
+                        : clusters_at_a_time<mx_pair_kernel<false, true>>(1, kThreads, sms, device);
+  return one < two ? one : two;
+}
 
 bool mx_pair_takes(const MxProductArgs& a) {
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };

@@ -1,6 +1,7 @@
 // mx_plan.h -- how a product with MXFP4 weights is cut into tiles (host only, no CUDA).
 #pragma once
 
+#include <atomic>
 #include <initializer_list>
 
 namespace qgemv {
@@ -14,6 +15,25 @@ constexpr int kMxAccCols = 480;   // tensor memory of the accumulators (512 less
 constexpr int kMxOut = 16;        // columns that results are written by
 constexpr int kMxSplits[4] = {1, 2, 4, 8};
 constexpr int kMxSmem = 227 * 1024 - 1024;  // dynamic shared memory (the rest is static)
+
+// How many clusters of 1 << log2 blocks a kernel has at work at a time, each kernel's own table:
+// asked once per size and device.  A question that fails is answered by 0 and asked again.
+class MxClusterTable {
+ public:
+  template <typename Ask>  // ask(&n): whether n is the answer
+  int get(int log2, int device, Ask ask) {
+    std::atomic<int>& at = known_[log2][device & 63];
+    const int known = at.load(std::memory_order_relaxed);
+    if (known > 0) return known - 1;
+    int n = 0;
+    if (!ask(&n)) return 0;
+    at.store(n + 1, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  std::atomic<int> known_[4][64] = {};  // one more than the answer
+};
 
 struct MxShape {
   long long M, N;

@@ -32,8 +32,6 @@
 // Thread blocks stay for the whole call and take tiles one after the other.  Where
 // there are few tiles, the blocks of a cluster share K: each finishes every split-th
 // column, adding the others' sums, sent to its shared memory, in rank order.
-#include <atomic>
-
 #include "mx_product.cuh"
 
 namespace qgemv {
@@ -714,78 +712,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- host
 
-// Clusters of 1 << log2 blocks that the device runs at a time, asked once per kernel,
-// size and device (0 where it cannot).
-template <typename F>
-int clusters_at_a_time(F* k, int log2, int sms, int device) {
-  static std::atomic<int> known[4][64];  // one more than the answer
-  if (log2 == 0) return sms;
-  std::atomic<int>& at = known[log2][device & 63];
-  int n = at.load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(sms >> log2 << log2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kMxSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1u << log2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int found = 0;
-    if (cudaOccupancyMaxActiveClusters(&found, k, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      found = 0;
-    }
-    n = found + 1;
-    at.store(n, std::memory_order_relaxed);
-  }
-  return n - 1;
-}
-
 // The plans of a shape, and whether pairs of blocks are expected to be faster; a thread
 // keeps those that it met last (a search takes a few microseconds, as long as all else of a
 // call).
 struct Plans {
   MxShape shape;
+  int pairs;  // of blocks that run at a time
   MxPlan plan;
   MxPairPlan pair;
   bool by_pairs;
 };
 
-const Plans* known_plans(const MxShape& s) {
+const Plans* known_plans(const MxShape& s, int pairs) {
   static thread_local Plans known[32] = {};
   const unsigned long long h = (static_cast<unsigned long long>(s.M) * 0x9E3779B97F4A7C15ull) ^
                                (static_cast<unsigned long long>(s.N) * 0xC2B2AE3D27D4EB4Full) ^
                                (static_cast<unsigned long long>(s.K) * 0x165667B19E3779F9ull);
   Plans& at = known[(h >> 40) % 32];
-  if (at.shape == s) return &at;
-  Plans p{s, {}, {}, false};
+  if (at.shape == s && at.pairs == pairs) return &at;
+  Plans p{s, pairs, {}, {}, false};
   if (!mx_plan(s, &p.plan)) return nullptr;
   double cost = 0;
-  p.by_pairs = mx_pair_plan(s, &p.pair, &cost) && cost < mx_cost(s, p.plan);
+  MxShape of_pairs = s;
+  of_pairs.clusters[1] = pairs;
+  p.by_pairs = mx_pair_plan(of_pairs, &p.pair, &cost) && cost < mx_cost(s, p.plan);
   at = p;
   return &at;
 }
 
 template <bool GATED, bool SPLIT>
 cudaError_t launch(const MxProductArgs& a, int sms, int device, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  auto* k = mx_product_kernel<GATED, SPLIT>;
-  const unsigned long long bit = 1ull << (device & 63);
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
+  constexpr auto* k = mx_product_kernel<GATED, SPLIT>;
+  if (const cudaError_t e = allow_smem<k>(device); e != cudaSuccess) return e;
   MxShape shape{a.M, a.N, a.K, GATED, SPLIT, {}};
-  for (int i = 0; i < 4; ++i) shape.clusters[i] = clusters_at_a_time(k, i, sms, device);
-  const Plans* plans = known_plans(shape);
+  for (int i = 0; i < 4; ++i) shape.clusters[i] = clusters_at_a_time<k>(i, kThreads, sms, device);
+  const int pairs = SPLIT ? 0 : mx_pair_clusters(GATED, sms, device);
+  const Plans* plans = known_plans(shape, pairs);
   if (plans == nullptr) return cudaErrorInvalidValue;
-  if (plans->by_pairs && mx_pair_takes(a)) return mx_pair_launch(a, plans->pair, shape.clusters[1], device, st);
+  if (plans->by_pairs && mx_pair_takes(a)) return mx_pair_launch(a, plans->pair, pairs, device, st);
   const MxPlan p = plans->plan;
   auto mod = [](const void* q, uintptr_t m) { return (reinterpret_cast<uintptr_t>(q) & (m - 1)) == 0; };
   MxLoads ld;

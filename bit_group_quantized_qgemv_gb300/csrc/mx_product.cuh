@@ -1,6 +1,8 @@
 // mx_product.cuh -- what the kernels of the MXFP4 products share.
 #pragma once
 
+#include <atomic>
+
 #include "kv_cache.cuh"
 #include "mma_tile.cuh"
 #include "mx.h"
@@ -104,8 +106,44 @@ __device__ __forceinline__ void write_results(const MxProductArgs& a, int n, int
   }
 }
 
-// Products by pairs of thread blocks (mx_pair.cu): whether the call's K and addresses allow
-// them, and the launch of a plan on up to `clusters` pairs.
+// All shared memory for a kernel, allowed once per device.
+template <auto* kKernel>
+cudaError_t allow_smem(int device) {
+  static std::atomic<unsigned long long> done{0};
+  const unsigned long long bit = 1ull << (device & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMxSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// Clusters of 1 << log2 blocks of a kernel that the device runs at a time (0 where it cannot).
+template <auto* kKernel>
+int clusters_at_a_time(int log2, int threads, int sms, int device) {
+  static MxClusterTable table;
+  if (log2 == 0) return sms;
+  return table.get(log2, device, [&](int* n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms >> log2 << log2));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = kMxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << log2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (allow_smem<kKernel>(device) == cudaSuccess && cudaOccupancyMaxActiveClusters(n, kKernel, &cfg) == cudaSuccess)
+      return true;
+    cudaGetLastError();
+    return false;
+  });
+}
+
+// Products by pairs of thread blocks (mx_pair.cu): how many pairs run at a time, whether the
+// call's K and addresses allow them, and the launch of a plan on up to `clusters` pairs.
+int mx_pair_clusters(bool gated, int sms, int device);
 bool mx_pair_takes(const MxProductArgs& a);
 cudaError_t mx_pair_launch(const MxProductArgs& a, const MxPairPlan& p, int clusters, int device, cudaStream_t st);
 cudaError_t status_mx_pair(unsigned* out);

@@ -2,6 +2,7 @@
 (csrc/mx_product.cu, csrc/mx_pair.cu), without a GPU."""
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -44,3 +45,22 @@ def test_arrivals_at_other_blocks_are_in_the_clusters_scope():
     assert "relaxed.cluster.shared::cta" in wait
     loop = source("kv_cache.cuh").split("void step_wait(", 1)[1].split("\n}\n", 1)[0]
     assert loop.index("mbar_try_wait_cluster") < loop.index("if (CLUSTER) mbar_acquire_cluster()") < loop.index("__syncwarp")
+
+
+# ----------------------------------------------------- how many run at a time
+
+def test_numbers_of_clusters(tmp_path):
+    exe = str(tmp_path / "clusters")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", CSRC, os.path.join(here, "clusters_on_cpu.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "done\n", r.stderr
+
+
+def test_each_kernel_is_asked():
+    """A table for each kernel (a template of the kernel, not of its type, which they share)."""
+    assert re.search(r"template <auto\* kKernel>\s+int clusters_at_a_time\(", source("mx_product.cuh"))
+    pair = source("mx_pair.cu")
+    for kernel in ("true, true", "true, false", "false, true", "false, false"):
+        assert f"clusters_at_a_time<mx_pair_kernel<{kernel}>>" in pair
+    assert "clusters_at_a_time<k>" in source("mx_product.cu")
