@@ -909,8 +909,8 @@ def residual_rmsnorm_mxfp8(x, gamma, residual=None, eps=1e-5, h=None, codes=None
 
 def qgemv_mxfp4(w, x, y=None, residual=None, stream=None):
     """y = W x (+ residual) for an MXFP4 weight w = (codes int32 [n][k / 8], scales
-    uint8 [n][k / 32]) and one to eight fp16 rows x ([k] or [m][k]).  Values of x count
-    exactly in blocks of 32 whose largest is below 256, else to 2^-32 of that largest."""
+    uint8 [n][k / 32]) and one to eight fp16 rows x ([k] or [m][k]).  x counts exactly,
+    but for the last bit of values below 2^-13 in blocks of 32 with one of 32768 or more."""
     if stream is not None:
         return _mx_elsewhere(qgemv_mxfp4, x, stream, w, x, y, residual)
     codes, scales = w

@@ -10,7 +10,6 @@ constexpr int kMxRows = 128;      // weight rows of a tile
 constexpr int kMxStep = 128;      // k of a stage
 constexpr int kMxMinStages = 4, kMxMaxStages = 16;
 constexpr int kMxRowSteps = 64;   // steps of fp16 rows that a block holds, at most
-constexpr int kMxSplitCols = 4;   // columns of an fp16 row
 constexpr int kMxAccCols = 480;   // tensor memory of the accumulators (512 less the scales')
 constexpr int kMxOut = 16;        // columns that results are written by
 constexpr int kMxSplits[4] = {1, 2, 4, 8};
@@ -136,7 +135,7 @@ inline bool mx_plan(const MxShape& shape, MxPlan* best) {
       if (!any || c < least) least = c, *best = p, any = true;
     }
   }
-  return any && (!s.fp16 || mx_fit(shape, kMxSplitCols * shape.M <= 16 ? 16 : 32, best->split, best));
+  return any && (!s.fp16 || mx_fit(shape, 3 * shape.M <= 16 ? 16 : 32, best->split, best));
 }
 
 // Tiles of two blocks that share them (mx_pair.cu): 256 rows of weights (gated: 128 of each

@@ -6,14 +6,12 @@
 // A tile is 128 weight rows (the instruction's A operand, 4-bit codes as they are
 // stored, spread to bytes by the copy itself) by up to 240 columns (B, e4m3): nothing
 // is dequantised by arithmetic, the scales go to tensor memory and into the product.
-// Columns are the MXFP8 rows of x, or for fp16 rows four columns each: x / 2^e1 = q1 +
-// q2 / 2^5 + q3 / 2^10 + q4 / 2^28 with e4m3 q and e1 = floor(log2 of the block's largest) - 7.
-// Three columns hold the eleven bits of a value down to 2^-26 of the block's largest value; what
-// they leave of smaller ones is 2^-27 of it at most, for the fourth.  So an fp16 value is held
-// exactly where the largest of its block is below 256 (all that fp16 has is then above its grid),
-// else to 2^-32 of the largest and to a 16th of itself at least.  The four sums are added in
-// fp32.  (With three columns, 2^-9 below the first, entries beside one of 60000 were lost from
-// 2^-27 of it on; the fourth costs no tensor time: up to 32 columns take the instruction as long as 16.)
+// Columns are the MXFP8 rows of x, or for fp16 rows three columns each (B then e5m2, which has
+// fp16's range): x 2^k = q1 + q2 / 2^4 + q3 / 2^8 with a k for each block.  q1 takes three
+// significant bits, q2 and q3 four of what is left and its sign: the eleven of an fp16 value, down
+// to fp16's last place.  All of x is held exactly but the last bit of values below 2^-13 in
+// blocks whose largest is 32768 or more.  The three sums are added in fp32.  (Three columns of
+// e4m3, whose range is shorter, lost entries below 2^-27 of the block's largest.)
 //
 // A step is 128 k: a ring of stages (codes of A and, for MXFP8 rows, of B, 128-byte
 // swizzled, and their scales) between
@@ -43,7 +41,6 @@ constexpr int kRowsW = kMxRows, kStepK = kMxStep;
 constexpr int kLoaders = 4;   // warps
 constexpr int kTmaWarps = 2;
 constexpr int kScaleCols = 16;  // tensor memory of one step's scales
-constexpr int kSplitCols = kMxSplitCols;
 
 // How a launch loads its operands.
 struct MxLoads {
@@ -147,11 +144,12 @@ __device__ __forceinline__ __half2 power2(int k) {
   return *reinterpret_cast<const __half2*>(&w);
 }
 
-// Eight values of row m of x (a lane; four lanes hold a block) to four columns: their codes at
-// `cols` (a step's, swizzled), the blocks' scales at `scales`.  All in fp16: x is multiplied by
-// 2^k, which puts the block's largest above 2^15 (or all of x, where that is below 2^-15, on
-// whole numbers), and what a column leaves is a multiple of x's last bit and no larger than x
-// was, so the subtractions are exact.
+// Eight values of row m of x (a lane; four lanes hold a block) to three columns: their codes at
+// `cols` (a step's, swizzled), the blocks' scales at `scales`.  All in fp16: x 2^k has its block's
+// largest in [2^14, 2^15), so what a column leaves is at most 2^11 and 2^7, and its last bits are
+// multiples of 2^-24, the last place of q3 (k = -1 halves, and rounds, fp16's last place; k = 30, for
+// blocks below 2^-16, makes all of them whole numbers).  What a column leaves is a multiple of
+// x's last bit and no larger than x was, so the subtractions are exact.
 __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, uint32_t scales, int m,
                                              int ch) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -161,29 +159,25 @@ __device__ __forceinline__ void split_values(uint4 v, bool live, uint32_t cols, 
   most = __vmaxu2(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
   const uint32_t top = max(most & 0xFFFFu, most >> 16);  // bits of the largest magnitude
   const int e = static_cast<int>(__float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(top)))) >> 23);
-  const int k = min(max(15 + 127 - e, 0), 30), byte = 127 + 8 - k;
+  const int k = min(max(14 + 127 - e, -1), 30);
   const __half2 k0 = power2(min(k, 15)), k1 = power2(max(k - 15, 0));
   __half2 f[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&u[i]), k0), k1);
 #pragma unroll
-  for (int q = 0; q < kSplitCols; ++q) {
-    const int down = q < 3 ? 8 - 5 * q : -20;  // the column's unit is 2^down of f's
+  for (int q = 0; q < 3; ++q) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint16_t two;
       uint32_t got;
-      const __half2 to = q < 3 ? __hmul2(f[i], power2(-down)) : __hmul2(__hmul2(f[i], power2(15)), power2(-down - 15));
-      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&to)));
-      if (q < 3) {
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(got) : "h"(two));
-        f[i] = __hfma2(*reinterpret_cast<const __half2*>(&got), __hneg2(power2(down)), f[i]);
-      }
+      asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&f[i])));
+      asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(got) : "h"(two));
+      f[i] = __hmul2(__hsub2(f[i], *reinterpret_cast<const __half2*>(&got)), power2(4));
       w[i >> 1] = i & 1 ? w[i >> 1] | (static_cast<uint32_t>(two) << 16) : two;
     }
-    const int c = kSplitCols * m + q;
-    const int sb = top >= 0x7C00u ? 255 : byte + down - 8;
+    const int c = 3 * m + q;
+    const int sb = top >= 0x7C00u ? 255 : 127 - k - 4 * q;
     if (live) {
       asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(cols + c * 128 + (((ch >> 1) ^ (c & 7)) << 4) +
                                                            (ch & 1) * 8),
@@ -229,16 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     *tok = (p.rows_first ? o : i) * p.tokens;
   };
 
-  // Where the columns of fp16 rows leave room for few stages, a tile's weights are on their way to
-  // L2 this many steps ahead (5 rows of K = 14336 to 4096 12.4 -> 10.8 us).
-  constexpr int ahead = SPLIT ? 12 : 0;
   // The first tile's weights on their way to L2 while the kernel before ends.
   if (first < tiles) {
     int row, tok;
     place(first, &row, &tok);
     if (warp == kTmaWarp && lane == 0) {
       if (ld.tma_w) {
-        for (int k = k0; k < k1 && k < k0 + max(p.stages, ahead); ++k) {
+        for (int k = k0; k < k1 && k < k0 + p.stages; ++k) {
           tc::prefetch_2d(&w_map, k * kStepK, row);
           if (GATED) tc::prefetch_2d(&u_map, k * kStepK, row);
         }
@@ -310,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ld.tma_w) {
           tc::tma_2d(to, &w_map, s.k * kStepK, row, full);
           if (GATED) tc::tma_2d(to + 16384, &u_map, s.k * kStepK, row, full);
-          if (SPLIT && p.stages < ahead && s.k + ahead < k1) tc::prefetch_2d(&w_map, (s.k + ahead) * kStepK, row);
         }
         if (!SPLIT) tc::tma_2d(to + kW * 16384, &x_map, s.k * kStepK, tok, full);
       }
@@ -340,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int me = warp - kMmaWarp;
     const bool two = GATED || p.pair;
     const uint32_t tm = static_cast<uint32_t>(tc::uniform(static_cast<int>(tmem)));
-    const uint32_t idesc = tc::idesc_mx(p.cols);
+    const uint32_t idesc = tc::idesc_mx(p.cols, 128, SPLIT);
     int stage = 0, use = 0, n = 0, odd = 0;  // odd: of all tiles' steps, the next one's number
     uint32_t c = base, ss = s_ring;          // of the stage
     for (long long t = first; t < tiles && (two || me == 0); t += stride, ++n) {
@@ -541,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const bool ok = __all_sync(0xFFFFFFFFu, *static_cast<volatile int*>(&s_failed) == 0);
       if constexpr (SPLIT) {
-        // four rows of x a warp: 16 columns
-        const int m0 = 4 * half, c0 = 16 * half;
+        // four rows of x a warp: 12 columns
+        const int m0 = 4 * half, c0 = 12 * half;
         if (ok && m0 < count) {
           float v[4];
           uint32_t x0[16], x1[16];
@@ -554,11 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::wait_ld16(x1);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            float q[4];
+            float q[3];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              q[c] = (has0 ? __uint_as_float(x0[4 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[4 * m + c]) : 0.f);
-            v[m] += ((q[3] + q[2]) + q[1]) + q[0];
+            for (int c = 0; c < 3; ++c)
+              q[c] = (has0 ? __uint_as_float(x0[3 * m + c]) : 0.f) + (has1 ? __uint_as_float(x1[3 * m + c]) : 0.f);
+            v[m] += (q[2] + q[1]) + q[0];
           }
           if (p.split == 1) {
             write_results<GATED>(a, n, m0, count - m0, v, lane);

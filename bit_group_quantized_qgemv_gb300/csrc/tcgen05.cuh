@@ -86,9 +86,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 // Block-scaled products of 8-, 6- and 4-bit floats (kind::mxf8f6f4; 4-bit codes lie in
 // shared memory sixteen to 16 bytes, in the first eight of them).  Instruction
-// descriptor: A e2m1, B e4m3, both K-major, ue8m0 scales, one per 32 k, M = m, N = n.
-__host__ __device__ constexpr uint32_t idesc_mx(int n, int m = 128) {
-  return (5u << 7) | (static_cast<uint32_t>(n / 8) << 17) | (1u << 23) |
+// descriptor: A e2m1, B e4m3 (or e5m2), both K-major, ue8m0 scales, one per 32 k, M = m, N = n.
+__host__ __device__ constexpr uint32_t idesc_mx(int n, int m = 128, bool e5m2 = false) {
+  return (5u << 7) | (e5m2 ? 1u << 10 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (1u << 23) |
          (static_cast<uint32_t>(m / 16) << 24);
 }
 // `byte`: which of the four scales in the words at sa, sb is that of this product's 32 k.

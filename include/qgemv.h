@@ -687,9 +687,9 @@ int qgemv_residual_rmsnorm_mxfp8(const uint16_t *x, const uint16_t *residual,
  * and fp16 activations, the decode form: 1 <= M <= QGEMV_MAX_M, K <= QGEMV_MXFP4_MAX_K
  * (the activations stay on chip).  x [M][K], y, residual
  * (NULL: none; may equal y) [M][N] fp16.  fp32 sums, one rounding.  x is taken apart into
- * 8-bit pieces: a value counts exactly where the largest magnitude of its block of 32 is
- * below 256, else to 2^-32 of that largest (and never to less than a 16th of itself).  A row
- * of x with an infinity or a NaN gives NaN in all of its outputs.  One launch.
+ * 8-bit pieces that hold it exactly, but for the last bit, 2^-24, of values below 2^-13 in
+ * blocks of 32 whose largest magnitude is 32768 or more.  A row of x with an infinity or a
+ * NaN gives NaN in all of its outputs.  One launch.
  */
 int qgemv_mxfp4(const uint32_t *codes, const uint8_t *scales, const uint16_t *x, uint16_t *y,
                 int M, int N, int K, const uint16_t *residual, void *stream);

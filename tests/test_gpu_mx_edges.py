@@ -81,7 +81,7 @@ def test_scales_of_another_shape_are_refused():
 @pytest.mark.parametrize("top", [65504.0, 33000.0, 4000.0, 511.75, 256.0, 255.875, 16.0, 7.5, 1.0, 2.0 ** -9, 2.0 ** -16, 2.0 ** -23])
 def test_every_fp16_value_beside_a_larger_one(top):
     """Every fp16 value up to the largest one of its block, in rows of one to eight: exact where that
-    is below 256, else to 2^-32 of it."""
+    is below 32768; beside larger ones fp16's last place, 2^-24, is rounded to a multiple of 2^-23."""
     every = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.float16)
     every = every[torch.isfinite(every) & (every.abs().float() <= top)]
     k = 1024                                                   # 32 blocks of 31 values and the largest
@@ -99,8 +99,7 @@ def test_every_fp16_value_beside_a_larger_one(top):
         got.append(q.qgemv_mxfp4(w, x[at:at + n].cuda()).cpu())
         at += n
     off = (torch.cat(got).double() - x.double()).abs()
-    # a sum within half a step of the value rounds to it; one further off by as much again at most
-    assert float(off.max()) <= (0.0 if top < 256 else 2 * 2.0 ** -32 * top)
+    assert float(off.max()) <= (0.0 if top < 32768 else 2.0 ** -24)
 
 
 @pytest.mark.parametrize("large,small", [(1000.0, 1e-2), (2000.0, 1e-3), (60000.0, 1e-3), (60000.0, 1e-4), (-60000.0, 3e-6),
@@ -114,11 +113,12 @@ def test_small_values_beside_one_without_weight(large, small, m, n, k):
     numbers = torch.randint(0, 8, (n, k), generator=g)
     numbers.view(n, -1, 32)[:, :, 7] = 0
     w = ref.pack4(numbers), torch.full((n, k // 32), 127, dtype=torch.uint8)
-    # a value is held exactly beside less than 256, else to 2^-32 of the largest and a 16th of itself;
-    # no product of the large one is there to align others to
+    # a value is held exactly beside less than 32768, else in multiples of 2^-23 (three columns of three
+    # significant bits and a sign, 2^-24 of the last one's smallest step of 2^-16 being the last place of
+    # values halved to below 2^15): half of that off; no product of the large one is there to align others to
     y = x.double().clone()
     y.view(m, -1, 32)[:, :, 7] = 0
     want, tol = ref.product(w, y)
-    held = torch.minimum(y / 16, torch.tensor(2.0 ** -32 * abs(large), dtype=torch.float64)) * (abs(large) >= 256)
+    held = torch.full_like(y, 2.0 ** -24 if abs(large) >= 32768 else 0.0)
     ref.near(q.qgemv_mxfp4(dev(w), x.cuda()), want, tol + held @ ref.values(*w).T, "small values")
     assert q.device_status() == 0
