@@ -512,16 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool res = !GATED && a.res != nullptr && n < a.N;
       auto residual = [&](int m) { return __half2float(a.res[static_cast<long long>(tok + m) * a.N + n]); };
       const int own = (count - rank + p.split - 1) / p.split;  // rows that this rank finishes
-      if (p.split > 1 && warp == 0 && lane == 0)
-        mbar_arrive_expect_tx(smem_u32(&bars.part_full), max(own, 0) * p.split * kW * kRowsW * 4);
       step_wait(smem_u32(&bars.acc_full[buf]), (n_t >> 1) & 1, &s_failed, &g_status);
       tc::fence_after();
       const uint32_t acc = lanes + buf * (GATED || p.pair ? 2 : 1) * p.cols;
       // a tile of a single step has one of two accumulators: the step's
       const bool one = !GATED && p.pair && k1 - k0 == 1;
       const bool has0 = !one || (n_t & 1) == 0, has1 = !one || (n_t & 1) == 1;
-      if (p.split > 1 && n_t > 0) {
-        step_wait<true>(smem_u32(&bars.part_done), (n_t - 1) & 1, &s_failed, &g_status);
+      if (p.split > 1) {
+        if (n_t > 0) step_wait<true>(smem_u32(&bars.part_done), (n_t - 1) & 1, &s_failed, &g_status);
+        // (behind that wait: a rank that finishes no row, of few, ends its phase by this alone, and its
+        // other warps must have seen the one before)
+        if (warp == 0 && lane == 0)
+          mbar_arrive_expect_tx(smem_u32(&bars.part_full), max(own, 0) * p.split * kW * kRowsW * 4);
       }
       auto give = [&](int m, float g, float u) {  // a rank's sums of one column to who finishes it
         const int q = m % p.split;
