@@ -754,12 +754,22 @@ _E4M3 = torch.float8_e4m3fn
 _CODES4, _CODES8, _BYTES = _CODES, (_U8, _E4M3), (_U8,)
 
 
+class _NoCalls:
+    """In place of a module that is not there: what needs it says so, all else works."""
+
+    def __init__(self, path):
+        self._path = path
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._path} not found: the microscaled operators need it "
+                          "(build.py makes it, with a C compiler and Python's headers)")
+
+
 def _load_calls():
     """The module that looks at a call's tensors and makes the call (csrc/mx_calls.c)."""
     path = _build.CALLS
     if not os.path.exists(path):
-        raise ImportError(f"_mx_calls.so not found at {path}; build it first with "
-                          "`python -m bit_group_quantized_qgemv_gb300.build`")
+        return _NoCalls(path)
     loader = importlib.machinery.ExtensionFileLoader("_mx_calls", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_mx_calls", loader))
     loader.exec_module(module)

@@ -2,8 +2,10 @@
 
 Each CUDA translation unit under ``csrc/`` is compiled in parallel to an
 object file in ``_build/``, then linked into ``_build/libqgemv.so``; beside it
-``csrc/mx_calls.c`` becomes the CPython module ``_build/_mx_calls.so``.  The
-build is skipped when both are newer than every source and header.
+``csrc/mx_calls.c`` becomes a CPython module, ``_build/_mx_calls`` with the suffix of
+the interpreter that it is built for (another one builds its own).  The build is
+skipped when both are newer than every source and header.  Without a C compiler or
+Python's headers the library is built all the same, and then the error raised.
 """
 from __future__ import annotations
 
@@ -19,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqgemv.so")
-CALLS = os.path.join(BUILD, "_mx_calls.so")
+CALLS = os.path.join(BUILD, "_mx_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
               "-I", os.path.join(ROOT, "include")]
@@ -71,9 +73,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         tmp = CALLS + f".tmp{os.getpid()}"
         cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
                os.path.join(CSRC, "mx_calls.c"), "-o", tmp]
-        res = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            res = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:
+            raise RuntimeError(f"gcc not found, which mx_calls.c is built with: {e}") from e
         if res.returncode != 0:
-            raise RuntimeError(f"gcc failed on mx_calls.c:\n{res.stderr}")
+            raise RuntimeError(f"gcc failed on mx_calls.c (it needs Python's headers):\n{res.stderr}")
         return tmp
 
     srcs = _sources()
@@ -88,8 +93,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
-    os.replace(calls.result(), CALLS)
     os.replace(tmp, LIB)
+    if os.path.exists(CALLS):  # of an older library
+        os.remove(CALLS)
+    os.replace(calls.result(), CALLS)
     return LIB
 
 
