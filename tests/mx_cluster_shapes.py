@@ -1,5 +1,5 @@
-"""Products (rows of x, rows of weights, K, two weights, fp16 rows) whose blocks work in clusters
-on several tiles, one after the other."""
+"""Products (rows of x, rows of weights, K, two weights, fp16 rows) whose blocks, in clusters or
+by themselves, work on several tiles, one after the other."""
 
 # clusters that share K, with K of whole steps and not: (the blocks of a cluster, product)
 SHARED = [(8, (4, 4695, 4672, 0, 1)), (8, (6, 4908, 4736, 0, 1)), (4, (7, 9798, 2656, 0, 1)), (2, (8, 19534, 1184, 0, 1)),
@@ -8,3 +8,6 @@ SHARED = [(8, (4, 4695, 4672, 0, 1)), (8, (6, 4908, 4736, 0, 1)), (4, (7, 9798, 
 # pairs with two accumulators for every other step, and an odd number of steps: the two warps that
 # issue products change places from tile to tile
 PAIRS_ODD = [(207, 4893, 384, 0, 0), (199, 4893, 896, 0, 0), (16, 39080, 384, 0, 0), (200, 4096, 384, 1, 0), (133, 4869, 1152, 1, 0)]
+# blocks by themselves with several tiles each; all but the first have a K that fits no step
+ALONE = [(3, 45000, 128, 0, 1), (5, 40000, 160, 0, 1), (700, 4000, 96, 0, 0), (2100, 1300, 160, 0, 0), (300, 8000, 160, 1, 0),
+         (130, 21001, 96, 1, 0), (16, 40000, 224, 1, 0)]

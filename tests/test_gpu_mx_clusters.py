@@ -1,10 +1,10 @@
-"""Products with MXFP4 weights by clusters of blocks with several tiles each, against plain 64-bit
+"""Products with MXFP4 weights by clusters of blocks, and by blocks, with several tiles each, against plain 64-bit
 forms, with guard bands around what they write."""
 import pytest
 import torch
 
 import mx_reference as ref
-from mx_cluster_shapes import PAIRS_ODD, SHARED
+from mx_cluster_shapes import ALONE, PAIRS_ODD, SHARED
 
 pytestmark = pytest.mark.gpu
 
@@ -49,8 +49,8 @@ class Banded:
         return bool((self.raw[:self.at] == 0xA5).all()) and bool((self.raw[end:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("m,n,k,gated,fp16", [s for _, s in SHARED] + PAIRS_ODD)
-def test_several_tiles_of_a_cluster(m, n, k, gated, fp16):
+@pytest.mark.parametrize("m,n,k,gated,fp16", [s for _, s in SHARED] + PAIRS_ODD + ALONE)
+def test_several_tiles_of_a_block(m, n, k, gated, fp16):
     w = weight(m + n, n, k)
     x = rows16(k, m, k) if fp16 else acts(k, m, k)
     want, tol = ref.product(w, x.double() if fp16 else ref.values(*x))

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 import bit_group_quantized_qgemv_gb300 as q
-from mx_cluster_shapes import PAIRS_ODD, SHARED
+from mx_cluster_shapes import ALONE, PAIRS_ODD, SHARED
 from test_mx_plan import CLUSTERS, plans, program  # noqa: F401
 from test_mx_protocol import Barrier, play, wait
 
@@ -161,3 +161,5 @@ def test_sizes_reach_several_tiles_of_a_cluster(program):  # noqa: F811
         assert p["faster"] and p["two2"] and steps % 2 == 1 and steps >= 3, shape
         rounds.add((shape[3], min(3, -(-p["row_tiles2"] * p["tok_tiles2"] // CLUSTERS[1]))))
     assert {(0, 2), (0, 3), (1, 3)} <= rounds
+    for shape, p in zip(ALONE, plans(program, ALONE)):
+        assert p["split"] == 1 and not p["faster"] and p["row_tiles"] * p["tok_tiles"] > CLUSTERS[0], shape
