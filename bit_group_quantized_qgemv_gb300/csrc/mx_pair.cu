@@ -3,19 +3,20 @@
 //
 // The same products as mx_product.cu, in tiles of 256 weight rows that the tensor cores of
 // two multiprocessors work on together: each block has 128 of the rows and half of the
-// columns, whose codes either tensor core reads from both.  A tile of one block moves
-// 16 KB of weights and 28 KB of columns into the product and 36 KB into shared memory a step,
-// which takes its 128 bytes a clock for longer than the product itself (448 clocks for 224
-// columns: 700 were measured); in a pair the columns are half of that, and 560 clocks.
-// Measured, pairs against blocks by themselves, each at its best width: 4096 rows of K = 14336
-// to 4096 127 against 156 us, 8192 of 8192 x 8192 286 against 325 (3.8 PFLOP/s; clocks are at 1.7
-// GHz under this load, and after some 25 ms of it at 1.5 by the card's power cap: 158 against
-// 174 us for the first), 1000 rows of 4096 x 4096 16.8 against 18.8, 64 rows 8.2 against 9.3,
-// gated 512 rows of 4096 to 14336 44 against 51; but gated 1024 rows of 1024 to 2816 14.4
-// against 12.9, where results take longer than the steps (here they change places on the way).
-// Which of the two is expected to be faster mx_plan.h says.  A step of 224 columns takes 458
-// clocks, 448 of them the tensor core's; one of up to 96 some 280, about what the copy takes
-// to spread 128 x 128 codes.
+// columns, whose codes either tensor core reads from both.  A step of 224 columns keeps the tensor
+// core busy for 448 clocks; in a tile of one block its 16 KB of weights and 28 KB of columns
+// move into the product and 36 KB into shared memory, at 128 bytes a clock longer than that; in a
+// pair the columns are half of it.
+// Measured (us, at 2.07 GHz; those with two figures in the first milliseconds at some 1.7 GHz and
+// then under the card's power cap at 1.4 to 1.7), pairs against blocks by themselves, each at its
+// best width: 4096 rows of K = 14336 to 4096 131 and 151 against 156 and 168, 8192 of 8192 x 8192
+// 292 and 336 against 329 and 372, 1000 rows of 4096 x 4096 16.5 against 18.6, 64 rows 7.9 against 9.3;
+// gated 512 rows of 4096 to 14336 46 and 50 against 52 and 53, 2048 rows 142 and 164 against 156 and 174; but
+// 64 rows of K = 14336 19.4 against 14.0 (which share K), and gated 1024 rows of 1024 to 2816
+// 14.4 against 12.4, where results take longer than the steps (here they change places on the
+// way).  Which of the two is expected to be faster mx_plan.h says.  By time and clock a step of 224
+// columns takes 480 to 490 clocks, results of the last tile and the start included; one of up to 96
+// some 280, about what the copy takes to spread 128 x 128 codes.
 //
 // Gated: a block's 128 rows are 64 of the gate and the same 64 of the other weight, so that
 // one product has both.  Results change places between the warps of the two halves through

@@ -1,6 +1,6 @@
-// tcgen05.cuh -- thin wrappers of the fifth-generation tensor-core
-// instructions the attention kernels use (fp16 operands, fp32 accumulators in
-// tensor memory, one CTA).
+// tcgen05.cuh -- thin wrappers of the fifth-generation tensor-core instructions:
+// fp16 operands for the attention kernels, block-scaled 4- and 8-bit ones for the
+// MXFP4 products (one block or a pair), fp32 accumulators in tensor memory.
 #pragma once
 
 #include <cuda.h>

@@ -697,8 +697,8 @@ int qgemv_mxfp4(const uint32_t *codes, const uint8_t *scales, const uint16_t *x,
 /*
  * qgemv_mx_gemm -- the same product for any number of rows in MXFP8 (x_codes [M][K],
  * x_scales [M][K/32]): batches and prompts.  M >= 0.  Other arguments as qgemv_mxfp4.
- * 4096 rows of K = 14336 to N = 4096 take 156 us (3.1 PFLOP/s, the clock held by the power
- * cap), 48 rows of 4096 to 6144 8.2.  Fastest with K a multiple of 512, or of 128, codes of
+ * 4096 rows of K = 14336 to N = 4096 take 151 to 157 us (3.1 to 3.2 PFLOP/s, the clock held
+ * by the power cap), 48 rows of 4096 to 6144 8.3.  Fastest with K a multiple of 512, or of 128, codes of
  * the weight 32-byte and scales 16- or 4-byte aligned.  Tiles, and so the order of the fp32
  * sums, follow from M, N, K and those alignments: a row's results can differ in their last
  * bit between batch sizes (not those of qgemv_mxfp4).
@@ -714,8 +714,8 @@ int qgemv_mx_gemm(const uint32_t *codes, const uint8_t *scales, const uint8_t *x
  * h_codes [M][I] and h_scales [M][I/32] (MXFP8, quantised from the fp32 result as
  * qgemv_mx_quantize does; I % 32 == 0), or to both; NULL to skip one.  One launch.
  * silu is off by 2^-20 of itself, below 0 by |z| 2^-22 of itself and |z| 2^-149 more.
- * Sizes, alignments and sums as qgemv_mx_gemm; 16 rows of 4096 to 14336 take 14.4 us,
- * 2048 rows 158.
+ * Sizes, alignments and sums as qgemv_mx_gemm; 16 rows of 4096 to 14336 take 13.9 us,
+ * 2048 rows 165 (the clock held by the power cap).
  */
 int qgemv_mx_swiglu(const uint32_t *gate_codes, const uint8_t *gate_scales,
                     const uint32_t *up_codes, const uint8_t *up_scales, const uint8_t *x_codes,
