@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = tm + (buf * (two ? 2 : 1) + me) * p.cols;
       for (int k = k0; k < k1; ++k) {
         if (GATED || !p.pair || odd == me) {
-          if (SPLIT && n == 0) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
+          // (with an odd number of steps a warp has the others of them in the second tile)
+          if (SPLIT && n < 2) step_wait(smem_u32(&bars.rows[k - k0]), 0, &s_failed, &g_status);
           step_wait(smem_u32(&bars.full[stage]), use & 1, &s_failed, &g_status);
           if (!ld.tma_w) tc::fence_async_shared();  // codes by cp.async, for the tensor core
           tc::fence_after();

@@ -11,3 +11,6 @@ PAIRS_ODD = [(207, 4893, 384, 0, 0), (199, 4893, 896, 0, 0), (16, 39080, 384, 0,
 # blocks by themselves with several tiles each; all but the first have a K that fits no step
 ALONE = [(3, 45000, 128, 0, 1), (5, 40000, 160, 0, 1), (700, 4000, 96, 0, 0), (2100, 1300, 160, 0, 0), (300, 8000, 160, 1, 0),
          (130, 21001, 96, 1, 0), (16, 40000, 224, 1, 0)]
+# fp16 rows of an odd number of steps and several tiles a block: the warps that issue products change
+# places from tile to tile, while the rows are still being taken apart
+ROWS_ODD = [(7, 29719, 128, 0, 1), (8, 60000, 128, 0, 1), (8, 40000, 96, 0, 1), (8, 30000, 384, 0, 1), (6, 25000, 640, 0, 1)]

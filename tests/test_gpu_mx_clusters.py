@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import mx_reference as ref
-from mx_cluster_shapes import ALONE, PAIRS_ODD, SHARED
+from mx_cluster_shapes import ALONE, PAIRS_ODD, ROWS_ODD, SHARED
 
 pytestmark = pytest.mark.gpu
 
@@ -49,7 +49,7 @@ class Banded:
         return bool((self.raw[:self.at] == 0xA5).all()) and bool((self.raw[end:] == 0xA5).all())
 
 
-@pytest.mark.parametrize("m,n,k,gated,fp16", [s for _, s in SHARED] + PAIRS_ODD + ALONE)
+@pytest.mark.parametrize("m,n,k,gated,fp16", [s for _, s in SHARED] + PAIRS_ODD + ALONE + ROWS_ODD)
 def test_several_tiles_of_a_block(m, n, k, gated, fp16):
     w = weight(m + n, n, k)
     x = rows16(k, m, k) if fp16 else acts(k, m, k)
@@ -112,4 +112,19 @@ def test_two_streams_of_clusters():
     torch.cuda.synchronize()
     for _, _, _, want, outs in work:
         assert all(torch.equal(o, want) for o in outs)
+    assert q.device_status() == 0
+
+
+@pytest.mark.parametrize("m,n,k", [s[:3] for s in ROWS_ODD])
+def test_rows_of_an_odd_number_of_steps(m, n, k):
+    """Many calls, each with rows of its own: those of the call before lie where these are taken apart to."""
+    w = weight(n, n, k)
+    wd, wv = dev(w), ref.values(*w).cuda()
+    for seed in range(30):
+        x = rows16(seed, m, k)
+        xv = x.double().cuda()
+        want = xv @ wv.T
+        # (a step of 32 products is off by 2^-20 of the magnitudes so far at most: there are k / 32)
+        tol = 2.0 ** -20 * (k // 32 + 1) * (xv.abs() @ wv.abs().T)
+        ref.near(q.qgemv_mxfp4(wd, x.cuda()), want.cpu(), tol.cpu(), "product")
     assert q.device_status() == 0

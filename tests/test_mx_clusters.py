@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 import bit_group_quantized_qgemv_gb300 as q
-from mx_cluster_shapes import ALONE, PAIRS_ODD, SHARED
+from mx_cluster_shapes import ALONE, PAIRS_ODD, ROWS_ODD, SHARED
 from test_mx_plan import CLUSTERS, plans, program  # noqa: F401
 from test_mx_protocol import Barrier, play, wait
 
@@ -147,6 +147,23 @@ def test_order_of_the_kernel_in_sharing():
     assert body.index("step_wait<true>(smem_u32(&bars.part_done)") < body.index("mbar_arrive_expect_tx(smem_u32(&bars.part_full)")
 
 
+# ------------------------------------------------------------- fp16 rows
+
+def test_every_use_of_fp16_rows_is_behind_a_wait_for_them():
+    """Two warps take every other step, counted over all tiles; the columns of a step are waited for in some
+    of the tiles, and each warp has to have waited for those of every step that it uses."""
+    when = re.findall(r"if \(SPLIT && ([^)]*)\) step_wait\(smem_u32\(&bars\.rows\[k - k0\]\)", source("mx_product.cu"))
+    assert len(when) == 1
+    for steps in range(1, 12):
+        seen, odd = set(), 0
+        for n in range(6):
+            for k in range(steps):
+                if eval(when[0], {"n": n}):
+                    seen.add((odd, k))
+                assert (odd, k) in seen, f"{steps} steps: step {k} of tile {n}"
+                odd ^= 1
+
+
 # --------------------------------------------------------- sizes of the tests
 
 def test_sizes_reach_several_tiles_of_a_cluster(program):  # noqa: F811
@@ -163,3 +180,5 @@ def test_sizes_reach_several_tiles_of_a_cluster(program):  # noqa: F811
     assert {(0, 2), (0, 3), (1, 3)} <= rounds
     for shape, p in zip(ALONE, plans(program, ALONE)):
         assert p["split"] == 1 and not p["faster"] and p["row_tiles"] * p["tok_tiles"] > CLUSTERS[0], shape
+    for shape, p in zip(ROWS_ODD, plans(program, ROWS_ODD)):
+        assert p["split"] == 1 and -(-shape[2] // 128) % 2 == 1 and p["row_tiles"] > CLUSTERS[0], shape
